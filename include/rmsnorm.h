@@ -83,7 +83,9 @@ typedef enum rmsnorm_status {
     RMSNORM_ERR_OPTIONS = -9,        /* malformed rmsnorm_options_t */
     RMSNORM_ERR_ALIGN = -10,         /* x, w or y not aligned to their element size, or rstd not
                                         4-byte aligned */
-    RMSNORM_ERR_WORKSPACE = -11      /* the backward's workspace is smaller than it needs */
+    RMSNORM_ERR_WORKSPACE = -11,     /* the backward's workspace is smaller than it needs */
+    RMSNORM_ERR_DEVICE_INDEX = -12   /* a kernel met a slot, page or row index out of range and
+                                        skipped it (see rmsnorm_check_device_status) */
 } rmsnorm_status_t;
 
 /* Kernel variants. RMSNORM_VARIANT_AUTO lets the planner choose. */
@@ -348,9 +350,304 @@ int rmsnorm_bwd_plan_info(int64_t M, int64_t N, int dtype, const rmsnorm_options
 int rmsnorm_bwd_workspace_size(int64_t M, int64_t N, int dtype, const rmsnorm_options_t* opts,
                                int64_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * The operators of a transformer block between its matrix products: the norms
+ * around a block (rmsnorm_block_*), the rotation of the heads of q and k with
+ * each head's norm (rmsnorm_rope_*), and the quantised cache that k and v go
+ * into (rmsnorm_cache_*). Their arguments come in structs: zero-initialise,
+ * set struct_size to the struct's size, then the fields.
+ * Common to all of them: device pointers on the current device; tensors bf16,
+ * fp16 or fp32 (one dtype per call) with elements aligned to their size; fp32
+ * arithmetic, one rounding to nearest even per output; deterministic results;
+ * work enqueued on `stream`, launched like the forward (programmatic dependent
+ * launch, stream order kept); capturable into a CUDA graph. Strides are in
+ * elements. Whole 16-byte vectors (row or head size, strides and pointers)
+ * take the vector kernels, anything else the element-wise ones. `opts` may be
+ * NULL; they read variant (AUTO, CTA: the vector kernels, GENERIC: the
+ * element-wise kernels), max_ctas and RMSNORM_FLAG_NO_PDL.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The norm after a block, the block's gate, the scaled residual and the norm
+ * before the next block, in one pass over the rows:
+ *
+ *   n    = h * rstd_post * (offset + w_post)     rstd_post = 1/sqrt(mean(h^2) + eps)
+ *   s    = beta * r + alpha * gate * n
+ *   y    = s * rstd_pre * (offset + w_pre)       rstd_pre = 1/sqrt(mean(s^2) + eps)
+ *
+ * s is the new residual stream; y is normed from s in fp32, before s is
+ * rounded for its store.
+ *   h, r   [M, N] the block's output and the residual stream (row strides ldh, ldr >= N)
+ *   w_post [N]    NULL: no norm after the block (n = h)
+ *   gate   [ceil(M / gate_rows), N] (row stride ldg >= N), row i of h takes gate row
+ *                 i / gate_rows: gate_rows >= M is one gate per channel, the tokens per
+ *                 sequence one gate per sequence, 1 a gate per element. NULL (and
+ *                 gate_rows 0): no gate
+ *   w_pre  [N]    NULL: no norm before the next block (y is then not written and NULL)
+ *   s, y   [M, N] outputs (row strides lds, ldy >= N)
+ *   rstd_post, rstd_pre  [M] fp32, kept for the backward; NULL: not stored
+ * At least one of w_post and w_pre is given. s and y may each equal h or r
+ * exactly (pointer and stride); no other overlap of an output with anything.
+ */
+typedef struct rmsnorm_block_args {
+    int32_t struct_size; /* sizeof(rmsnorm_block_args_t) */
+    int32_t dtype;       /* rmsnorm_dtype_t */
+    int64_t M;           /* rows (>= 0) */
+    int64_t N;           /* columns (> 0) */
+    int64_t gate_rows;   /* rows of h per gate row; 0 without a gate */
+    const void* h;
+    const void* r;
+    const void* w_post;
+    const void* gate;
+    const void* w_pre;
+    void* s;
+    void* y;
+    float* rstd_post;
+    float* rstd_pre;
+    int64_t ldh;
+    int64_t ldr;
+    int64_t ldg;
+    int64_t lds;
+    int64_t ldy;
+    float eps;    /* >= 0 and finite, both norms */
+    float offset; /* finite, both norms: 0 or 1 as in rmsnorm_fwd */
+    float alpha;  /* finite: scale of the block's branch */
+    float beta;   /* finite: scale of the residual */
+} rmsnorm_block_args_t;
+
+int rmsnorm_block_fwd(const rmsnorm_block_args_t* args, const rmsnorm_options_t* opts,
+                      void* stream);
+
+/*
+ * Its backward, from the gradients dy of y and ds of s, the saved s (as the
+ * forward stored it), the kept rstd and h, w_post, gate, w_pre (args.r, args.y
+ * and args.eps are not read):
+ *
+ *   t     = ds + rstd_pre * (u - s * rstd_pre^2 * sum(u s) / N)    u = dy * (offset + w_pre)
+ *   dr    = beta * t
+ *   dh    = rstd_post * (v - h * rstd_post^2 * sum(v h) / N)       v = alpha * gate * t * (offset + w_post)
+ *   dgate = sum over the gate row's rows of alpha * t * n
+ *   dw_post = sum over rows of alpha * gate * t * h * rstd_post
+ *   dw_pre  = sum over rows of dy * s * rstd_pre
+ *
+ * (without w_post: dh = alpha * gate * t; without w_pre: t = ds).
+ *   dy, ds  [M, N] dy is given exactly when w_pre is; ds may be NULL (zero) when dy is given
+ *   dh, dr  [M, N] outputs; each may equal dy, ds, h or s exactly
+ *   dgate   like gate (row stride lddg), given exactly when gate is
+ *   dw_post, dw_pre  [N] fp32, given exactly when w_post, w_pre are (zero when M == 0)
+ * Row sums are over fixed threads in a fixed order; the sums over rows are
+ * taken per CTA and then over CTAs in a fixed order by a second launch.
+ *   workspace  device scratch of rmsnorm_block_bwd_workspace_size() bytes, 16-byte
+ *              aligned; calls sharing one must not overlap on the GPU
+ */
+typedef struct rmsnorm_block_grads {
+    int32_t struct_size; /* sizeof(rmsnorm_block_grads_t) */
+    int32_t reserved;    /* 0 */
+    const void* dy;
+    const void* ds;
+    void* dh;
+    void* dr;
+    void* dgate;
+    float* dw_post;
+    float* dw_pre;
+    int64_t lddy;
+    int64_t ldds;
+    int64_t lddh;
+    int64_t lddr;
+    int64_t lddg;
+} rmsnorm_block_grads_t;
+
+int rmsnorm_block_bwd(const rmsnorm_block_args_t* args, const rmsnorm_block_grads_t* grads,
+                      void* workspace, int64_t workspace_bytes, const rmsnorm_options_t* opts,
+                      void* stream);
+
+/* Bytes of workspace rmsnorm_block_bwd needs for M rows of N columns on the
+ * current device, whatever the other arguments, alignments and options (written
+ * to *bytes; never less for a larger M). */
+int rmsnorm_block_bwd_workspace_size(int64_t M, int64_t N, int dtype, int64_t* bytes);
+
+/* Heads of a tensor: element d of head h of token s of batch b is at
+ * ptr + b * batch_stride + s * token_stride + h * head_stride + d. */
+typedef struct rmsnorm_heads {
+    void* ptr;
+    int64_t batch_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+} rmsnorm_heads_t;
+
+/*
+ * Rotary positions on the heads of q and k, after each head's RMSNorm where
+ * weights are given:
+ *
+ *   x = head * rstd * (offset + w)      rstd = 1/sqrt(mean over head_dim of head^2 + eps)
+ *                                       (x = head without weights)
+ *   out[a] = magnitude * (x[a] cos t - x[b] sin t)
+ *   out[b] = magnitude * (x[b] cos t + x[a] sin t)      t = position * frequency_i
+ *
+ * for the pairs i < rotary_dim / 2 of the first rotary_dim values: (a, b) =
+ * (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved. The values behind
+ * rotary_dim stay x. Angles are exact for every 64-bit position: frequencies
+ * are given as steps, the fraction of a turn per position times 2^64
+ * (rmsnorm_rope_steps), so position * step wraps modulo one turn.
+ *   q [batch, seq, heads_q, head_dim], k likewise with heads_k (0: no k)
+ *   out_q, out_k   outputs, may equal q and k exactly (pointer and strides)
+ *   positions      [batch, seq] int64 (row stride positions_stride; 0: one row for all
+ *                  batches); NULL: the index in the sequence
+ *   w_q, w_k       [head_dim], each may be NULL
+ *   rstd_q, rstd_k [batch, seq, heads] fp32, contiguous, kept for the backward; NULL: not
+ *                  stored (and without weights not written)
+ */
+typedef struct rmsnorm_rope_args {
+    int32_t struct_size; /* sizeof(rmsnorm_rope_args_t) */
+    int32_t dtype;       /* rmsnorm_dtype_t */
+    int64_t batch;
+    int64_t seq;
+    int32_t heads_q;     /* >= 1 */
+    int32_t heads_k;     /* >= 0 */
+    int32_t head_dim;    /* 2..65536 */
+    int32_t rotary_dim;  /* even, 2..head_dim */
+    int32_t interleaved; /* 0 or 1 */
+    int32_t reserved;    /* 0 */
+    const int64_t* positions;
+    int64_t positions_stride;
+    const uint64_t* steps; /* [rotary_dim / 2] on the device */
+    const void* w_q;
+    const void* w_k;
+    float* rstd_q;
+    float* rstd_k;
+    float eps;
+    float offset;
+    float magnitude; /* finite; 1 for plain rotation */
+    float reserved_f;
+    rmsnorm_heads_t q;
+    rmsnorm_heads_t k;
+    rmsnorm_heads_t out_q;
+    rmsnorm_heads_t out_k;
+} rmsnorm_rope_args_t;
+
+int rmsnorm_rope_fwd(const rmsnorm_rope_args_t* args, const rmsnorm_options_t* opts, void* stream);
+
+/*
+ * Its backward: gradients dout_q, dout_k of the outputs are turned back by the
+ * same angles (times magnitude) and go through the norm's backward where
+ * weights are given, which reads q, k and the kept rstd (args.out_q, args.out_k
+ * and args.eps are not read; without weights q, k and rstd are not either).
+ *   dout_q, dout_k   like the outputs; strides may be 0 (expanded)
+ *   dq, dk           outputs; may equal dout_q and dout_k exactly
+ *   dw_q, dw_k       [head_dim] fp32 sums over all tokens and heads, given exactly when the
+ *                    weights are (zero without tokens)
+ *   workspace        as in rmsnorm_block_bwd (may be NULL without weights)
+ */
+typedef struct rmsnorm_rope_grads {
+    int32_t struct_size; /* sizeof(rmsnorm_rope_grads_t) */
+    int32_t reserved;    /* 0 */
+    rmsnorm_heads_t dout_q;
+    rmsnorm_heads_t dout_k;
+    rmsnorm_heads_t dq;
+    rmsnorm_heads_t dk;
+    float* dw_q;
+    float* dw_k;
+} rmsnorm_rope_grads_t;
+
+int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* args, const rmsnorm_rope_grads_t* grads,
+                     void* workspace, int64_t workspace_bytes, const rmsnorm_options_t* opts,
+                     void* stream);
+
+/* Bytes of workspace rmsnorm_rope_bwd needs with weights on the current device
+ * for heads of head_dim values, any number of tokens and heads. */
+int rmsnorm_rope_bwd_workspace_size(int32_t head_dim, int64_t* bytes);
+
+/* Scaling of rotary frequencies to longer contexts. */
+typedef enum rmsnorm_rope_scaling_kind {
+    RMSNORM_ROPE_PLAIN = 0,
+    RMSNORM_ROPE_LINEAR = 1, /* every frequency / factor */
+    RMSNORM_ROPE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)); rotary_dim > 2 */
+    RMSNORM_ROPE_YARN = 3,   /* pairs that turn more than beta_fast times within `length` stay,
+                                those under beta_slow times are divided by factor, a ramp over
+                                the pair index between; magnitude 0.1 ln(factor) + 1 */
+    RMSNORM_ROPE_BANDS = 4   /* as YARN by the turns within `length` itself, ramp between
+                                beta_slow and beta_fast turns; magnitude 1 */
+} rmsnorm_rope_scaling_kind_t;
+
+typedef struct rmsnorm_rope_scaling {
+    int32_t struct_size; /* sizeof(rmsnorm_rope_scaling_t) */
+    int32_t kind;        /* rmsnorm_rope_scaling_kind_t */
+    double factor;       /* >= 1 */
+    double length;       /* YARN, BANDS: the original context (> 0) */
+    double beta_fast;    /* YARN, BANDS: > beta_slow > 0 */
+    double beta_slow;
+} rmsnorm_rope_scaling_t;
+
+/* The steps of the frequencies base^(-2i / rotary_dim) (scaled; NULL: plain) into
+ * the HOST array steps[rotary_dim / 2], and the magnitude that goes with them
+ * (may be NULL). No CUDA call. */
+int rmsnorm_rope_steps(int32_t rotary_dim, double base, const rmsnorm_rope_scaling_t* scaling,
+                       uint64_t* steps, float* magnitude);
+
+/* Formats of a cached value. Groups of 32 values of a head (the last group of a
+ * head may be shorter) share a scale 2^(byte - 127): the smallest such power, not
+ * below 2^-127, by which every value of the group is within the format. A group
+ * that holds an infinity or a NaN has scale byte 255 and reads back as NaN. */
+typedef enum rmsnorm_cache_format {
+    RMSNORM_CACHE_E4M3 = 0, /* 8 bits: largest 448 */
+    RMSNORM_CACHE_E2M1 = 1  /* 4 bits: 0, .5, 1, 1.5, 2, 3, 4, 6; even d in the low half of a byte */
+} rmsnorm_cache_format_t;
+
+/*
+ * A paged cache: slot page * page_size + i is token i of a page. Codes are
+ * [pages, page_size, heads, code bytes] and scales [pages, page_size, heads,
+ * ceil(head_dim / 32)] bytes, contiguous; with heads_first the heads come before
+ * the tokens of the page. Code bytes: head_dim (E4M3), ceil(head_dim / 2) (E2M1).
+ * v_codes and v_scales are both NULL in a cache of one tensor.
+ */
+typedef struct rmsnorm_cache {
+    int32_t struct_size; /* sizeof(rmsnorm_cache_t) */
+    int32_t format;      /* rmsnorm_cache_format_t */
+    int64_t pages;       /* >= 1 */
+    int32_t page_size;   /* >= 1 */
+    int32_t heads;       /* >= 1 */
+    int32_t head_dim;    /* 1..65536 */
+    int32_t heads_first; /* 0 or 1 */
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+} rmsnorm_cache_t;
+
+/*
+ * Quantises k and v (tokens [T, heads, head_dim] by their token and head
+ * strides; batch_stride is not read; v may be NULL) into the cache: token t
+ * goes to slot slots[t] (int64 on the device; negative: the token is padding
+ * and not read). A slot past the cache is skipped and reported by
+ * rmsnorm_check_device_status. Slots of a call must be distinct: a slot named
+ * twice ends with bytes of either token.
+ */
+int rmsnorm_cache_write(const rmsnorm_cache_t* cache, const rmsnorm_heads_t* k,
+                        const rmsnorm_heads_t* v, const int64_t* slots, int64_t T, int dtype,
+                        const rmsnorm_options_t* opts, void* stream);
+
+/*
+ * Reads a ragged batch back: row i of the outputs, for cu_rows[b] <= i <
+ * cu_rows[b + 1], is token p = starts[b] + i - cu_rows[b] of sequence b, from
+ * slot table[b][p / page_size] * page_size + p % page_size.
+ *   table    [sequences, table_width] int32 pages, contiguous
+ *   cu_rows  [sequences + 1] int32, not decreasing, cu_rows[0] = 0
+ *   starts   [sequences] int32 (NULL: 0)
+ *   rows     rows of the outputs; rows from cu_rows[sequences] on are left as they are
+ *   k_out, v_out  [rows, heads, head_dim] by their token and head strides; either may be
+ *            NULL (not both)
+ * A row whose page lies outside the cache or the table is set to zero and
+ * reported by rmsnorm_check_device_status.
+ */
+int rmsnorm_cache_read(const rmsnorm_cache_t* cache, const int32_t* table, int64_t table_width,
+                       const int32_t* cu_rows, const int32_t* starts, int64_t sequences,
+                       int64_t rows, const rmsnorm_heads_t* k_out, const rmsnorm_heads_t* v_out,
+                       int dtype, const rmsnorm_options_t* opts, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * word. Returns RMSNORM_OK, RMSNORM_ERR_DEVICE_TIMEOUT if any kernel since the
- * last check gave up a bounded wait, or RMSNORM_ERR_CUDA. */
+ * last check gave up a bounded wait, RMSNORM_ERR_DEVICE_INDEX if one met an
+ * index out of range, or RMSNORM_ERR_CUDA. */
 int rmsnorm_check_device_status(void* stream);
 
 /* Static text for a status code. */

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -21,12 +22,15 @@ STATUS = {
     0: "RMSNORM_OK", -1: "RMSNORM_ERR_NULL", -2: "RMSNORM_ERR_SHAPE", -3: "RMSNORM_ERR_DTYPE",
     -4: "RMSNORM_ERR_SCALAR", -5: "RMSNORM_ERR_OVERLAP", -6: "RMSNORM_ERR_CUDA",
     -7: "RMSNORM_ERR_DEVICE_TIMEOUT", -8: "RMSNORM_ERR_UNSUPPORTED", -9: "RMSNORM_ERR_OPTIONS",
-    -10: "RMSNORM_ERR_ALIGN", -11: "RMSNORM_ERR_WORKSPACE",
+    -10: "RMSNORM_ERR_ALIGN", -11: "RMSNORM_ERR_WORKSPACE", -12: "RMSNORM_ERR_DEVICE_INDEX",
 }
 # Every function include/rmsnorm.h declares.
 EXPORTS = ("rmsnorm_fwd", "rmsnorm_fwd_ex", "rmsnorm_fwd_strided", "rmsnorm_fwd_host",
            "rmsnorm_fwd_host_workspace_size", "rmsnorm_bwd", "rmsnorm_bwd_noalloc",
            "rmsnorm_bwd_workspace_size", "rmsnorm_plan_info", "rmsnorm_bwd_plan_info",
+           "rmsnorm_block_fwd", "rmsnorm_block_bwd", "rmsnorm_block_bwd_workspace_size",
+           "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_size",
+           "rmsnorm_rope_steps", "rmsnorm_cache_write", "rmsnorm_cache_read",
            "rmsnorm_check_device_status",
            "rmsnorm_strerror", "rmsnorm_last_error", "rmsnorm_version")
 
@@ -56,6 +60,56 @@ class Plan(ctypes.Structure):
         d = {n: getattr(self, n) for n, _ in self._fields_}
         d["variant"] = VARIANT_NAMES.get(d["variant"], d["variant"])
         return d
+
+
+# Argument structs of the block, rope and cache operators (field names and order
+# of include/rmsnorm.h).
+_I, _Q, _F, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class BlockArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("dtype", _I), ("M", _Q), ("N", _Q), ("gate_rows", _Q)]
+                + [(n, _P) for n in ("h", "r", "w_post", "gate", "w_pre", "s", "y", "rstd_post",
+                                     "rstd_pre")]
+                + [(n, _Q) for n in ("ldh", "ldr", "ldg", "lds", "ldy")]
+                + [(n, _F) for n in ("eps", "offset", "alpha", "beta")])
+
+
+class BlockGrads(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("reserved", _I)]
+                + [(n, _P) for n in ("dy", "ds", "dh", "dr", "dgate", "dw_post", "dw_pre")]
+                + [(n, _Q) for n in ("lddy", "ldds", "lddh", "lddr", "lddg")])
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", _P), ("batch_stride", _Q), ("token_stride", _Q), ("head_stride", _Q)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("dtype", _I), ("batch", _Q), ("seq", _Q)]
+                + [(n, _I) for n in ("heads_q", "heads_k", "head_dim", "rotary_dim", "interleaved",
+                                     "reserved")]
+                + [("positions", _P), ("positions_stride", _Q)]
+                + [(n, _P) for n in ("steps", "w_q", "w_k", "rstd_q", "rstd_k")]
+                + [(n, _F) for n in ("eps", "offset", "magnitude", "reserved_f")]
+                + [(n, Heads) for n in ("q", "k", "out_q", "out_k")])
+
+
+class RopeGrads(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("reserved", _I)]
+                + [(n, Heads) for n in ("dout_q", "dout_k", "dq", "dk")]
+                + [("dw_q", _P), ("dw_k", _P)])
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("kind", _I)]
+                + [(n, ctypes.c_double) for n in ("factor", "length", "beta_fast", "beta_slow")])
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("format", _I), ("pages", _Q)]
+                + [(n, _I) for n in ("page_size", "heads", "head_dim", "heads_first")]
+                + [(n, _P) for n in ("k_codes", "k_scales", "v_codes", "v_scales")])
 
 
 _lock = threading.Lock()
@@ -107,6 +161,21 @@ def lib() -> ctypes.CDLL:
             L.rmsnorm_bwd_plan_info.argtypes = [i64, i64, i32, ctypes.POINTER(Options),
                                                 ctypes.POINTER(Plan)]
             L.rmsnorm_bwd_plan_info.restype = i32
+            # Argument structs: a ctypes structure by reference, or its packed bytes.
+            L.rmsnorm_block_fwd.argtypes = [vp, ctypes.POINTER(Options), vp]
+            L.rmsnorm_block_bwd.argtypes = [vp, vp, vp, i64, ctypes.POINTER(Options), vp]
+            L.rmsnorm_block_bwd_workspace_size.argtypes = [i64, i64, i32,
+                                                           ctypes.POINTER(ctypes.c_int64)]
+            L.rmsnorm_rope_fwd.argtypes = [vp, ctypes.POINTER(Options), vp]
+            L.rmsnorm_rope_bwd.argtypes = [vp, vp, vp, i64, ctypes.POINTER(Options), vp]
+            L.rmsnorm_rope_bwd_workspace_size.argtypes = [i32, ctypes.POINTER(ctypes.c_int64)]
+            L.rmsnorm_rope_steps.argtypes = [i32, ctypes.c_double, vp, vp, vp]
+            L.rmsnorm_cache_write.argtypes = [vp, vp, vp, vp, i64, i32, ctypes.POINTER(Options), vp]
+            L.rmsnorm_cache_read.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, vp, i32,
+                                             ctypes.POINTER(Options), vp]
+            for name in EXPORTS:
+                if name.startswith(("rmsnorm_block", "rmsnorm_rope", "rmsnorm_cache")):
+                    getattr(L, name).restype = i32
             L.rmsnorm_check_device_status.argtypes = [vp]
             L.rmsnorm_check_device_status.restype = i32
             L.rmsnorm_strerror.argtypes = [i32]
@@ -221,6 +290,68 @@ def rmsnorm_bwd_plan_info(M: int, N: int, dtype: int, opts: Options | None = Non
     _check(lib().rmsnorm_bwd_plan_info(M, N, dtype, ctypes.byref(opts) if opts is not None else None,
                                        ctypes.byref(out)))
     return out.as_dict()
+
+
+def _arg(s):
+    """An argument struct as the library takes it: packed bytes as they are."""
+    return s if s is None or isinstance(s, bytes) else ctypes.byref(s)
+
+
+def _opt(opts: Options | None):
+    return ctypes.byref(opts) if opts is not None else None
+
+
+def rmsnorm_block_fwd(args: BlockArgs | bytes, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_block_fwd(_arg(args), _opt(opts), stream)
+
+
+def rmsnorm_block_bwd(args: BlockArgs | bytes, grads: BlockGrads | bytes, workspace: int,
+                      workspace_bytes: int, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_block_bwd(_arg(args), _arg(grads), workspace, workspace_bytes, _opt(opts),
+                                   stream)
+
+
+def rmsnorm_block_bwd_workspace_size(M: int, N: int, dtype: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().rmsnorm_block_bwd_workspace_size(M, N, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def rmsnorm_rope_fwd(args: RopeArgs | bytes, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_rope_fwd(_arg(args), _opt(opts), stream)
+
+
+def rmsnorm_rope_bwd(args: RopeArgs | bytes, grads: RopeGrads | bytes, workspace: int,
+                     workspace_bytes: int, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_rope_bwd(_arg(args), _arg(grads), workspace, workspace_bytes, _opt(opts),
+                                  stream)
+
+
+def rmsnorm_rope_bwd_workspace_size(head_dim: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().rmsnorm_rope_bwd_workspace_size(head_dim, ctypes.byref(out)))
+    return out.value
+
+
+def rmsnorm_rope_steps(rotary_dim: int, base: float, scaling: RopeScaling | None, steps: int,
+                       magnitude: int = 0) -> int:
+    """Steps into host memory at the address `steps` (rotary_dim / 2 64-bit
+    values) and the magnitude into the float at `magnitude` (0: not wanted)."""
+    return lib().rmsnorm_rope_steps(rotary_dim, base, _arg(scaling), steps, magnitude or None)
+
+
+def rmsnorm_cache_write(cache: CacheArgs | bytes, k: Heads | bytes | None, v: Heads | bytes | None,
+                        slots: int, T: int, dtype: int, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_cache_write(_arg(cache), _arg(k), _arg(v), slots, T, dtype, _opt(opts),
+                                     stream)
+
+
+def rmsnorm_cache_read(cache: CacheArgs | bytes, table: int, table_width: int, cu_rows: int,
+                       starts: int, sequences: int, rows: int, k_out: Heads | bytes | None,
+                       v_out: Heads | bytes | None, dtype: int, opts: Options | None,
+                       stream: int) -> int:
+    return lib().rmsnorm_cache_read(_arg(cache), table, table_width, cu_rows, starts, sequences,
+                                    rows, _arg(k_out), _arg(v_out), dtype, _opt(opts), stream)
 
 
 def rmsnorm_check_device_status(stream: int = 0) -> int:
@@ -358,3 +489,465 @@ def bwd(x, w, rstd, dy, offset: float = 0.0, dx=None, stream=None, **options):
         # reused before the work on `s` is done.
         ws.record_stream(s)
     return dx, dw
+
+
+# ---- the operators between a block's matrix products -----------------------
+#
+# Calls of a decoding step are host-bound, so these pack their argument structs
+# with struct.Struct (a microsecond) and make no context managers unless the
+# tensors' device or the stream is not the current one.
+
+_BLOCK = struct.Struct("=2i3q9Q5q4f")
+_BLOCK_GRADS = struct.Struct("=2i7Q5q")
+_ROPE = struct.Struct("=2i2q6iQq5Q4f" + "Q3q" * 4)
+_ROPE_GRADS = struct.Struct("=2i" + "Q3q" * 4 + "2Q")
+_CACHE = struct.Struct("=2iq4i4Q")
+_HEADS = struct.Struct("=Q3q")
+CACHE_FORMATS = {"e4m3": 0, "e2m1": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+_CODES = None
+
+
+def _code(dtype):
+    global _CODES
+    if _CODES is None:
+        import torch
+        _CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"RMSNorm takes bf16, fp16 or fp32 activations, got {dtype}")
+    return code
+
+
+def _elsewhere(t, stream):
+    """None where `t` is on the current device and no stream is given; else a
+    context in which both are current (outputs and workspaces made there belong
+    to that stream)."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        return None if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _stream_ptr():
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _same(t, like, name, dtype=None):
+    if t is not None and (t.dtype != (dtype or like.dtype) or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must be {dtype or like.dtype} on {like.device}, "
+                         f"got {t.dtype} on {t.device}")
+
+
+def _rows(t, name, like, M, N):
+    """(address, row stride) of a matrix of M rows given as [..., N]."""
+    if t is None:
+        return 0, 0
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    _same(t, like, name)
+    if t.is_contiguous():
+        return t.data_ptr(), N
+    if t.dim() == 2 and (t.stride(1) == 1 or N == 1):
+        return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{name} must be contiguous, or 2-D with unit column stride")
+
+
+def _vector(t, name, like, N, dtype=None):
+    if t is None:
+        return 0
+    _same(t, like, name, dtype)
+    if t.numel() != N or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {N} elements")
+    return t.data_ptr()
+
+
+def _gate(gate, gate_rows, like, M, N):
+    """(address, row stride, rows of h per gate row) of a gate [N] or [..., N]."""
+    if gate is None:
+        if gate_rows:
+            raise ValueError("gate_rows without a gate")
+        return 0, 0, 0
+    _same(gate, like, "gate")
+    if gate.shape[-1] != N:
+        raise ValueError(f"gate must have {N} columns, got {tuple(gate.shape)}")
+    G = gate.numel() // N
+    if not gate_rows:
+        gate_rows = max(M, 1) if gate.dim() == 1 or G == 1 else M // G if G and M % G == 0 else 0
+    if gate_rows < 1 or -(-M // gate_rows) != G and M > 0:
+        raise ValueError(f"{G} gate rows do not divide {M} rows: give gate_rows, the rows per gate row")
+    if gate.is_contiguous() or G <= 1 and gate.stride(-1) == 1:
+        return gate.data_ptr(), N, gate_rows
+    if gate.dim() == 3 and gate.shape[1] == 1:
+        gate = gate[:, 0]
+    if gate.dim() == 2 and (gate.stride(1) == 1 or N == 1):
+        return gate.data_ptr(), gate.stride(0), gate_rows
+    raise ValueError("gate must be contiguous, or 2-D with unit column stride")
+
+
+def block_fwd(h, r, w_post=None, w_pre=None, gate=None, gate_rows=None, eps: float = 1e-6,
+              offset: float = 0.0, alpha: float = 1.0, beta: float = 1.0, s=None, y=None,
+              rstd: bool = True, stream=None, **options):
+    """s, y, rstd_post, rstd_pre = block_fwd(h, r, w_post, w_pre): the norm after a
+    block, its gate, the scaled residual and the norm before the next block.
+
+        n = h * rstd_post * (offset + w_post);  s = beta * r + alpha * gate * n
+        y = s * rstd_pre * (offset + w_pre)
+
+    h, r: CUDA tensors [..., N] (contiguous, or 2-D with unit column stride).
+    Without w_post there is no norm of h, without w_pre no y (None). ``gate`` is
+    [N] (a gate per channel), h's shape (per element), or [G, N] or [G, 1, N]
+    with ``gate_rows`` consecutive rows of h per gate row (default M / G). ``s`` and
+    ``y`` may be passed to write into (each may be h or r); ``rstd=False`` keeps no
+    rstd. Options as for :func:`make_options` (variant, max_ctas, pdl).
+    """
+    import torch
+    ctx = _elsewhere(h, stream)
+    if ctx is not None:
+        with ctx:
+            return block_fwd(h, r, w_post, w_pre, gate, gate_rows, eps, offset, alpha, beta, s, y,
+                             rstd, **options)
+    N = h.shape[-1]
+    M = h.numel() // N if N else 0
+    hp, ldh = _rows(h, "h", h, M, N)
+    rp, ldr = _rows(r, "r", h, M, N)
+    gp, ldg, gate_rows = _gate(gate, gate_rows, h, M, N)
+    wpost, wpre = _vector(w_post, "w_post", h, N), _vector(w_pre, "w_pre", h, N)
+    if s is None:
+        s = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if y is None:
+        y = torch.empty(h.shape, dtype=h.dtype, device=h.device) if wpre else None
+    elif not wpre:
+        raise ValueError("y without w_pre")
+    sp, lds = _rows(s, "s", h, M, N)
+    yp, ldy = _rows(y, "y", h, M, N)
+    a = b = None
+    if rstd:
+        if wpost:
+            a = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
+        if wpre:
+            b = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
+    args = _BLOCK.pack(160, _code(h.dtype), M, N, gate_rows, hp, rp, wpost, gp, wpre, sp, yp,
+                       0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(),
+                       ldh, ldr, ldg, lds, ldy, eps, offset, alpha, beta)
+    _check(rmsnorm_block_fwd(args, make_options(**options) if options else None, _stream_ptr()))
+    return s, y, a, b
+
+
+def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=None, gate=None,
+              gate_rows=None, offset: float = 0.0, alpha: float = 1.0, beta: float = 1.0, dh=None,
+              dr=None, workspace=None, stream=None, **options):
+    """dh, dr, dgate, dw_post, dw_pre = block_bwd(h, s, rstd_post, rstd_pre, dy, ds, ...):
+    backward of :func:`block_fwd` from the gradients dy of y and ds of s (None:
+    zero), the s and rstd that the forward returned and its other arguments.
+
+    dgate is in the gate's shape and dtype, dw_post and dw_pre in fp32 (None
+    without gate, w_post, w_pre). ``workspace`` is a CUDA tensor of at least
+    rmsnorm_block_bwd_workspace_size() bytes; allocated here when not given.
+    """
+    import torch
+    ctx = _elsewhere(h, stream)
+    if ctx is not None:
+        with ctx:
+            return block_bwd(h, s, rstd_post, rstd_pre, dy, ds, w_post, w_pre, gate, gate_rows,
+                             offset, alpha, beta, dh, dr, workspace, **options)
+    N = h.shape[-1]
+    M = h.numel() // N if N else 0
+    code = _code(h.dtype)
+    hp, ldh = _rows(h, "h", h, M, N)
+    sp, lds = _rows(s, "s", h, M, N)
+    dyp, lddy = _rows(dy, "dy", h, M, N)
+    dsp, ldds = _rows(ds, "ds", h, M, N)
+    gp, ldg, gate_rows = _gate(gate, gate_rows, h, M, N)
+    wpost, wpre = _vector(w_post, "w_post", h, N), _vector(w_pre, "w_pre", h, N)
+    ap = _vector(rstd_post, "rstd_post", h, M, torch.float32) if wpost else 0
+    bp = _vector(rstd_pre, "rstd_pre", h, M, torch.float32) if wpre else 0
+    if dh is None:
+        dh = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if dr is None:
+        dr = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    dhp, lddh = _rows(dh, "dh", h, M, N)
+    drp, lddr = _rows(dr, "dr", h, M, N)
+    dgate = torch.empty(gate.shape, dtype=h.dtype, device=h.device) if gp else None
+    dwa = torch.empty(N, dtype=torch.float32, device=h.device) if wpost else None
+    dwb = torch.empty(N, dtype=torch.float32, device=h.device) if wpre else None
+    if workspace is None:
+        workspace = torch.empty(rmsnorm_block_bwd_workspace_size(M, N, code), dtype=torch.uint8,
+                                device=h.device)
+    args = _BLOCK.pack(160, code, M, N, gate_rows, hp, 0, wpost, gp, wpre, sp, 0, ap, bp,
+                       ldh, 0, ldg, lds, 0, 0.0, offset, alpha, beta)
+    grads = _BLOCK_GRADS.pack(104, 0, dyp, dsp, dhp, drp, 0 if dgate is None else dgate.data_ptr(),
+                              0 if dwa is None else dwa.data_ptr(),
+                              0 if dwb is None else dwb.data_ptr(),
+                              lddy, ldds, lddh, lddr, N if dgate is not None else 0)
+    _check(rmsnorm_block_bwd(args, grads, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(),
+                             make_options(**options) if options else None, _stream_ptr()))
+    return dh, dr, dgate, dwa, dwb
+
+
+def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda"):
+    """steps, magnitude = rope_steps(rotary_dim): the frequencies of rotary positions
+    as rope_fwd and rope_bwd take them (int64 [rotary_dim / 2] on the device: turns
+    per position times 2^64), and the factor on cos and sin that belongs to them.
+
+    ``scaling``: None or a dict with "kind" ("linear", "ntk", "yarn" or "bands"),
+    "factor", and for "yarn" and "bands" the original "length" and optionally
+    "beta_fast" (32 for yarn, 4 for bands) and "beta_slow" (1).
+    """
+    import torch
+    steps = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
+    sc = None
+    if scaling:
+        extra = set(scaling) - {"kind", "factor", "length", "beta_fast", "beta_slow"}
+        if extra or scaling.get("kind") not in ROPE_SCALINGS:
+            raise ValueError(f"not a scaling of rotary positions: {scaling}")
+        kind = scaling["kind"]
+        sc = RopeScaling(ctypes.sizeof(RopeScaling), ROPE_SCALINGS[kind], scaling.get("factor", 1.0),
+                         scaling.get("length", 0.0),
+                         scaling.get("beta_fast", 32.0 if kind == "yarn" else 4.0),
+                         scaling.get("beta_slow", 1.0))
+    mag = ctypes.c_float(1.0)
+    _check(rmsnorm_rope_steps(rotary_dim, base, sc, steps.data_ptr(), ctypes.addressof(mag)))
+    return steps.to(device), mag.value
+
+
+def _heads(t, name, like, shape):
+    """A heads tensor [T, H, D] or [B, S, H, D] as the struct's four values."""
+    if t is None:
+        return 0, 0, 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same(t, like, name)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name} must have unit stride within a head")
+    return (t.data_ptr(), 0, st[0], st[1]) if len(st) == 3 else (t.data_ptr(), st[0], st[1], st[2])
+
+
+def _rope_common(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude):
+    """The fields of the rope structs up to the weights, and k's shape."""
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [tokens, heads, head_dim] or [batch, seq, heads, head_dim]")
+    shape = q.shape
+    B, S = (1, shape[0]) if len(shape) == 3 else (shape[0], shape[1])
+    D, hk = shape[-1], 0
+    if k is not None:
+        if k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != D:
+            raise ValueError(f"k must be like q but for its heads, got {tuple(k.shape)}")
+        hk = k.shape[-2]
+    _same(steps, q, "steps", torch.int64)
+    if not steps.is_contiguous():
+        raise ValueError("steps must be contiguous")
+    pp = ps = 0
+    if positions is not None:
+        _same(positions, q, "positions", torch.int64)
+        ok = positions.shape == shape[:-2] or positions.dim() == 1 and positions.shape[0] == S
+        if not ok or positions.stride(-1) != 1 and S > 1:
+            raise ValueError("positions must be [seq] or [batch, seq], the last contiguous")
+        pp, ps = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    return (248, _code(q.dtype), B, S, shape[-2], hk, D, 2 * steps.numel(), 1 if interleaved else 0,
+            0, pp, ps, steps.data_ptr(), _vector(w_q, "w_q", q, D), _vector(w_k, "w_k", q, D)), \
+        (eps, offset, magnitude, 0.0)
+
+
+def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool = False,
+             eps: float = 1e-6, offset: float = 0.0, magnitude: float = 1.0, q_out=None, k_out=None,
+             rstd: bool = True, stream=None, **options):
+    """q_out, k_out, rstd_q, rstd_k = rope_fwd(q, k, steps, positions): rotary positions
+    on the first 2 * len(steps) values of every head, after the head's RMSNorm where
+    w_q or w_k is given.
+
+    q, k (k may be None): CUDA tensors [T, heads, head_dim] or [batch, seq, heads,
+    head_dim] with unit stride within a head, any other strides (slices of a
+    projection, transposed [batch, heads, seq, head_dim]). ``steps`` and ``magnitude``
+    come from :func:`rope_steps`; ``positions`` is int64 [T], [seq] or [batch, seq]
+    (default: the index). Pairs are (i, i + half), or (2i, 2i + 1) when
+    ``interleaved``. ``q_out`` and ``k_out`` may be passed (q and k themselves to work in
+    place). rstd_q and rstd_k are None without weights or with ``rstd=False``.
+    """
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return rope_fwd(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude,
+                            q_out, k_out, rstd, **options)
+    head, scalars = _rope_common(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    elif k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    a = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if rstd and w_q is not None else None
+    b = torch.empty(k.shape[:-1], dtype=torch.float32, device=dev) \
+        if rstd and w_k is not None and k is not None else None
+    ks = None if k is None else k.shape
+    args = _ROPE.pack(*head, 0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(),
+                      *scalars, *_heads(q, "q", q, q.shape), *_heads(k, "k", q, ks),
+                      *_heads(q_out, "q_out", q, q.shape), *_heads(k_out, "k_out", q, ks))
+    _check(rmsnorm_rope_fwd(args, make_options(**options) if options else None, _stream_ptr()))
+    return q_out, k_out, a, b
+
+
+def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None, rstd_k=None,
+             w_q=None, w_k=None, interleaved: bool = False, offset: float = 0.0,
+             magnitude: float = 1.0, dq=None, dk=None, workspace=None, stream=None, **options):
+    """dq, dk, dw_q, dw_k = rope_bwd(dq_out, dk_out, steps, positions, ...): backward of
+    :func:`rope_fwd` from the gradients of its outputs. With w_q (w_k) it needs the
+    forward's q (k) and the rstd_q (rstd_k) it returned. dw_q and dw_k are fp32
+    (None without weights). ``dq`` and ``dk`` may be passed (dq_out and dk_out
+    themselves to work in place); ``workspace`` as in :func:`block_bwd`
+    (rmsnorm_rope_bwd_workspace_size() bytes, needed with weights only).
+    """
+    import torch
+    ctx = _elsewhere(dq_out, stream)
+    if ctx is not None:
+        with ctx:
+            return rope_bwd(dq_out, dk_out, steps, positions, q, k, rstd_q, rstd_k, w_q, w_k,
+                            interleaved, offset, magnitude, dq, dk, workspace, **options)
+    head, scalars = _rope_common(dq_out, dk_out, steps, positions, w_q, w_k, interleaved, 0.0, offset,
+                                 magnitude)
+    dev, D = dq_out.device, dq_out.shape[-1]
+    qs, ks = dq_out.shape, None if dk_out is None else dk_out.shape
+    if dq is None:
+        dq = torch.empty(qs, dtype=dq_out.dtype, device=dev)
+    if dk_out is None:
+        if dk is not None:
+            raise ValueError("dk without dk_out")
+    elif dk is None:
+        dk = torch.empty(ks, dtype=dq_out.dtype, device=dev)
+    ap = bp = 0
+    dwq = dwk = None
+    if w_q is not None:
+        ap = _vector(rstd_q, "rstd_q", dq_out, qs[:-1].numel(), torch.float32)
+        dwq = torch.empty(D, dtype=torch.float32, device=dev)
+    if w_k is not None and ks is not None:
+        bp = _vector(rstd_k, "rstd_k", dq_out, ks[:-1].numel(), torch.float32)
+        dwk = torch.empty(D, dtype=torch.float32, device=dev)
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(rmsnorm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
+    none = (0, 0, 0, 0)
+    args = _ROPE.pack(*head, ap, bp, *scalars,
+                      *(_heads(q, "q", dq_out, qs) if w_q is not None else none),
+                      *(_heads(k, "k", dq_out, ks) if w_k is not None else none), *none, *none)
+    grads = _ROPE_GRADS.pack(152, 0, *_heads(dq_out, "dq_out", dq_out, qs),
+                             *_heads(dk_out, "dk_out", dq_out, ks), *_heads(dq, "dq", dq_out, qs),
+                             *_heads(dk, "dk", dq_out, ks), 0 if dwq is None else dwq.data_ptr(),
+                             0 if dwk is None else dwk.data_ptr())
+    ws_ptr = 0 if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
+                            make_options(**options) if options else None, _stream_ptr()))
+    return dq, dk, dwq, dwk
+
+
+class Cache:
+    """A paged cache of k and v in 8 ("e4m3") or 4 ("e2m1") bits per value, one
+    power-of-two scale byte for 32 values of a head: ``k_codes`` and ``v_codes``
+    [pages, page_size, heads, code bytes], ``k_scales`` and ``v_scales`` [pages,
+    page_size, heads, ceil(head_dim / 32)] (heads before page_size with
+    ``heads_first``), zero at the start. ``values=False`` holds k alone;
+    ``tensors`` = (k_codes, k_scales, v_codes, v_scales) takes existing memory.
+    """
+
+    def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, fmt: str = "e4m3",
+                 device="cuda", heads_first: bool = False, values: bool = True, tensors=None):
+        import torch
+        if fmt not in CACHE_FORMATS:
+            raise ValueError(f"cache format must be one of {sorted(CACHE_FORMATS)}, got {fmt!r}")
+        self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, head_dim
+        self.fmt, self.heads_first = fmt, bool(heads_first)
+        lead = (pages, heads, page_size) if heads_first else (pages, page_size, heads)
+        shapes = [(*lead, head_dim if fmt == "e4m3" else (head_dim + 1) // 2),
+                  (*lead, (head_dim + 31) // 32)]
+        shapes = shapes * 2 if values else shapes
+        if tensors is None:
+            tensors = [torch.zeros(s, dtype=torch.uint8, device=device) for s in shapes]
+        if len(tensors) != len(shapes):
+            raise ValueError(f"the cache is made of {len(shapes)} tensors, got {len(tensors)}")
+        for t, s in zip(tensors, shapes):
+            if tuple(t.shape) != s or t.dtype != torch.uint8 or not t.is_contiguous() or \
+                    t.device != tensors[0].device or not t.is_cuda:
+                raise ValueError(f"cache tensors must be contiguous uint8 CUDA tensors {s} on one "
+                                 f"device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        self.k_codes, self.k_scales = tensors[:2]
+        self.v_codes, self.v_scales = tensors[2:] if values else (None, None)
+        self._args = _CACHE.pack(64, CACHE_FORMATS[fmt], pages, page_size, heads, head_dim,
+                                 int(self.heads_first), *(t.data_ptr() for t in tensors),
+                                 *(() if values else (0, 0)))
+
+
+def _tokens(t, name, like, shape, dtype):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same(t, like, name, dtype)
+    st = t.stride()
+    if st[2] != 1 and shape[2] != 1:
+        raise ValueError(f"{name} must have unit stride within a head")
+    return _HEADS.pack(t.data_ptr(), 0, st[0], st[1])
+
+
+def cache_write(cache: Cache, k, v, slots, stream=None, **options) -> None:
+    """Quantises k and v ([T, heads, head_dim], unit stride within a head; v None: k
+    alone) into ``cache``: token t into slot slots[t] (int64: page * page_size +
+    index; negative: padding, skipped). Slots must be distinct."""
+    import torch
+    ctx = _elsewhere(cache.k_codes, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_write(cache, k, v, slots, **options)
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, head_dim]")
+    T = k.shape[0]
+    shape = (T, cache.heads, cache.head_dim)
+    kh = _tokens(k, "k", cache.k_codes, shape, k.dtype)
+    vh = None if v is None else _tokens(v, "v", cache.k_codes, shape, k.dtype)
+    sp = _vector(slots, "slots", cache.k_codes, T, torch.int64)
+    _check(rmsnorm_cache_write(cache._args, kh, vh, sp, T, _code(k.dtype),
+                               make_options(**options) if options else None, _stream_ptr()))
+
+
+def cache_read(cache: Cache, table, cu_rows, rows: int, starts=None, dtype=None, k_out=None,
+               v_out=None, stream=None, **options):
+    """k, v = cache_read(cache, table, cu_rows, rows): a ragged batch read back. Rows
+    cu_rows[b] to cu_rows[b + 1] of the outputs [rows, heads, head_dim] are the
+    tokens of sequence b from starts[b] (default 0) on, by its row of ``table``.
+
+    ``table`` int32 [sequences, pages per sequence], ``cu_rows`` int32 [sequences + 1],
+    ``starts`` int32 [sequences]. Outputs are ``dtype`` (default bf16) and are
+    allocated here, or passed as ``k_out`` and ``v_out`` (unit stride within a head);
+    rows behind cu_rows[-1] are not written. v is None in a cache without v.
+    """
+    import torch
+    ctx = _elsewhere(cache.k_codes, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_read(cache, table, cu_rows, rows, starts, dtype, k_out, v_out, **options)
+    like = cache.k_codes
+    dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+    shape = (rows, cache.heads, cache.head_dim)
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be contiguous [sequences, pages per sequence]")
+    _same(table, like, "table", torch.int32)
+    n, width = table.shape
+    cp = _vector(cu_rows, "cu_rows", like, n + 1, torch.int32)
+    sp = _vector(starts, "starts", like, n, torch.int32)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=like.device)
+    if v_out is None and cache.v_codes is not None:
+        v_out = torch.empty(shape, dtype=dtype, device=like.device)
+    kh = _tokens(k_out, "k_out", like, shape, dtype)
+    vh = None if v_out is None else _tokens(v_out, "v_out", like, shape, dtype)
+    _check(rmsnorm_cache_read(cache._args, table.data_ptr(), width, cp, sp, n, rows, kh, vh,
+                              _code(dtype), make_options(**options) if options else None,
+                              _stream_ptr()))
+    return k_out, v_out

@@ -4,6 +4,7 @@
 #include "rmsnorm.h"
 
 #include "launch.h"
+#include "ops.h"
 
 #include <cmath>
 #include <cstdarg>
@@ -33,6 +34,8 @@ std::once_flag g_dev_once[kMaxDevices];
 DeviceInfo g_dev[kMaxDevices];
 cudaError_t g_dev_err[kMaxDevices];
 
+}  // namespace
+
 cudaError_t device_info(DeviceInfo* out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -51,8 +54,6 @@ cudaError_t device_info(DeviceInfo* out) {
     *out = g_dev[dev];
     return cudaSuccess;
 }
-
-}  // namespace
 
 bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -541,13 +542,16 @@ extern "C" int rmsnorm_bwd_plan_info(int64_t M, int64_t N, int dtype, const rmsn
 extern "C" int rmsnorm_check_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "synchronize: %s", cudaGetErrorString(e));
-    unsigned int v = 0, vc = 0, vb = 0;
+    unsigned int v = 0, vc = 0, vb = 0, vi = 0;
     e = status_read_and_clear(&v);
     if (e == cudaSuccess) e = cluster_status_read_and_clear(&vc);
     if (e == cudaSuccess) e = bwd_status_read_and_clear(&vb);
+    if (e == cudaSuccess) e = cache_status_read_and_clear(&vi);
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
     if (v != 0 || vc != 0 || vb != 0)
         return fail(RMSNORM_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait");
+    if (vi != 0)
+        return fail(RMSNORM_ERR_DEVICE_INDEX, "a kernel skipped a slot, page or row index out of range");
     return RMSNORM_OK;
 }
 
@@ -565,6 +569,7 @@ extern "C" const char* rmsnorm_strerror(int status) {
         case RMSNORM_ERR_OPTIONS: return "bad options";
         case RMSNORM_ERR_ALIGN: return "misaligned pointer";
         case RMSNORM_ERR_WORKSPACE: return "workspace too small";
+        case RMSNORM_ERR_DEVICE_INDEX: return "index out of range in device memory";
         default: return "unknown status";
     }
 }
