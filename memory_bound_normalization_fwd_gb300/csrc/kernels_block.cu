@@ -8,9 +8,242 @@
 
 #include "ops.h"
 #include "ops_common.cuh"
+#include "row_ring.cuh"
+#include "row_ring_host.h"
+
+#include <algorithm>
 
 namespace rmsn {
+
+// Bit 0: a bounded wait ran out since the last read. One word per device.
+__device__ unsigned int g_block_status;
+
 namespace {
+
+// Vector kernel: row teams with a ring of h and r rows (and gate rows, where
+// each row has its own) in shared memory. A thread keeps its columns of the row
+// in registers between the reductions: h is read once, s once made.
+// GATE: 0 none, 1 one gate row for several rows (kept in registers, read again
+// where the gate row changes), 2 a gate row per row (staged like h and r).
+template <int DT, int V, int GATE, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, const RingShape g) {
+    constexpr int E = VecElems<DT>::value;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ RingShared sh;
+    __shared__ __align__(16) float parts[kMaxTeams][2][kMaxTeamWarps];
+
+    const int team = threadIdx.x / g.T, t = threadIdx.x - team * g.T;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * g.teams + team;
+    const int64_t r0 = me * g.q + (me < g.rem ? me : g.rem);
+    const int rows = static_cast<int>(g.q) + (me < g.rem ? 1 : 0);
+    Ring ring;
+    ring.row_bytes = static_cast<uint32_t>(g.nvec) * 16u;
+    ring.stage_bytes = ring.row_bytes * g.arrays;
+    ring.stages = g.stages;
+    ring.mem = smem + static_cast<size_t>(team) * g.stages * ring.stage_bytes;
+    ring.base = smem_u32(ring.mem);
+    ring.bars = smem_u32(&sh.bars[team][0]);
+    if (t == 0) {
+        for (int st = 0; st < g.stages; ++st) mbar_init(ring.bar(st), 1);
+        fence_mbar_init();
+        sh.dead[team] = 0;
+    }
+    for (int i = t; i < 2 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
+
+    const uint4* h = static_cast<const uint4*>(p.h) + r0 * p.ldh;
+    const uint4* r = static_cast<const uint4*>(p.r) + r0 * p.ldr;
+    const uint4* gate = static_cast<const uint4*>(p.gate);
+    uint4* s = static_cast<uint4*>(p.s) + r0 * p.lds;
+    uint4* y = static_cast<uint4*>(p.y) + r0 * p.ldy;
+    auto issue = [&](int row, int st) {
+        ring.expect(st);
+        ring.copy(st, 0, h + row * p.ldh);
+        ring.copy(st, 1, r + row * p.ldr);
+        if (GATE == 2) ring.copy(st, 2, gate + (r0 + row) * p.ldg);
+    };
+    pdl_wait();
+    if (t == 0) {
+        for (int k = 0; k < g.stages && k < rows; ++k) issue(k, k);
+    }
+    uint4 wpost[V], wpre[V], gv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = v * g.T + t;
+        wpost[v] = wpre[v] = gv[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < g.nvec) {
+            if (p.w_post) wpost[v] = __ldg(static_cast<const uint4*>(p.w_post) + c);
+            if (p.w_pre) wpre[v] = __ldg(static_cast<const uint4*>(p.w_pre) + c);
+        }
+    }
+    int64_t grow = 0;
+    int64_t left = 0;  // rows until the gate row changes
+    if (GATE == 1) {
+        grow = r0 / p.gate_rows;
+        left = (grow + 1) * p.gate_rows - r0;
+    }
+    auto load_gate = [&]() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            if (c < g.nvec) gv[v] = __ldg(gate + grow * p.ldg + c);
+        }
+    };
+    if (GATE == 1) load_gate();
+    __syncthreads();  // barriers and flags are set up
+    pdl_launch_dependents();
+
+    int st = 0, parity = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    int row = 0;
+    for (; row < rows; ++row) {
+        if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
+        uint4 hv[V], rv[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            hv[v] = rv[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < g.nvec) {
+                hv[v] = ring.row(st, 0)[c];
+                rv[v] = ring.row(st, 1)[c];
+                if (GATE == 2) gv[v] = ring.row(st, 2)[c];
+            }
+        }
+        // Behind a row's first barrier every thread has read the stage: the
+        // leader refills it.
+        auto behind_first_barrier = [&]() {
+            dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+            if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
+        };
+        float a = 1.f;
+        if (p.w_post) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int v = 0; v < V; ++v) ss[0] = sumsq_vec<DT>(hv[v], ss[0]);
+            team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+            parity ^= 1;
+            behind_first_barrier();
+            if (dead) break;
+            a = row_rstd(ss[0], p.n, p.eps);
+            if (t == 0 && p.rstd_post) p.rstd_post[r0 + row] = a;
+        }
+        if (GATE == 1) {
+            if (left == 0) {
+                ++grow;
+                left = p.gate_rows;
+                load_gate();
+            }
+            --left;
+        }
+        float f[V][E];
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float w[E], x[E];
+            unpack_vec<DT>(hv[v], f[v]);
+            if (p.w_post) {
+                weights_vec<DT>(wpost[v], p.offset, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[v][e] = f[v][e] * a * w[e];
+            }
+            if (GATE != 0) {
+                unpack_vec<DT>(gv[v], x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[v][e] *= x[e];
+            }
+            unpack_vec<DT>(rv[v], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                f[v][e] = fmaf(p.beta, x[e], p.alpha * f[v][e]);
+                ss[0] = fmaf(f[v][e], f[v][e], ss[0]);
+            }
+        }
+        float b = 0.f;
+        if (!p.w_post) {  // then w_pre is given
+            team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+            parity ^= 1;
+            behind_first_barrier();
+            if (dead) break;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            if (c < g.nvec) st_stream(s + row * p.lds + c, pack_vec<DT>(f[v]));
+        }
+        if (p.w_pre) {
+            if (p.w_post) {
+                team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+                parity ^= 1;
+            }
+            b = row_rstd(ss[0], p.n, p.eps);
+            if (t == 0 && p.rstd_pre) p.rstd_pre[r0 + row] = b;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = v * g.T + t;
+                float w[E];
+                weights_vec<DT>(wpre[v], p.offset, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[v][e] = f[v][e] * b * w[e];
+                if (c < g.nvec) st_stream(y + row * p.ldy + c, pack_vec<DT>(f[v]));
+            }
+        }
+        if (++st == g.stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    if (dead && t == 0) {
+        atomicOr(&g_block_status, 1u);
+        // Rows below row + stages were issued and may still be landing.
+        for (int k = row; k < row + g.stages && k < rows; ++k) {
+            mbar_wait_bounded(ring.bar(st), phase, g.limit);
+            if (++st == g.stages) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+    }
+}
+
+template <int DT, int GATE>
+cudaError_t launch_ring(BlockP p, const OpCfg& c, bool* taken) {
+    constexpr int E = VecElems<DT>::value;
+    using Fn = void (*)(const BlockP, const RingShape);
+    const int64_t nvec = p.N / E;
+    RingPlan plan;
+    *taken = false;
+    // One vector per thread up to 256 threads, then two, then four.
+    const int V = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 0;
+    if (V == 0) return cudaSuccess;
+    const int T = static_cast<int>((nvec + V * 32 - 1) / (V * 32)) * 32;
+    const bool wide = T > 256;
+    const Fn fn = V == 1   ? block_fwd_ring_kernel<DT, 1, GATE, 256>
+                  : V == 2 ? (wide ? block_fwd_ring_kernel<DT, 2, GATE, 512>
+                                   : block_fwd_ring_kernel<DT, 2, GATE, 256>)
+                           : block_fwd_ring_kernel<DT, 4, GATE, 512>;
+    if (!ring_plan(reinterpret_cast<const void*>(fn), c, p.M, static_cast<int>(nvec), T, wide ? 512 : 256,
+                   GATE == 2 ? 3 : 2, 0, &plan))
+        return cudaSuccess;
+    p.ldh /= E;
+    p.ldr /= E;
+    p.ldg /= E;
+    p.lds /= E;
+    p.ldy /= E;
+    *taken = true;
+    return op_launch(c, fn, plan.grid, plan.threads, plan.smem, p, plan.shape);
+}
+
+// Whole vectors everywhere: rows, strides and addresses.
+bool vectors(const BlockP& p) {
+    const int64_t e = vec_elems(p.dtype);
+    const void* ptrs[] = {p.h, p.r, p.w_post, p.gate, p.w_pre, p.s, p.y};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return false;
+    const int64_t sizes[] = {p.N, p.ldh, p.ldr, p.lds, p.gate ? p.ldg : 0, p.y ? p.ldy : 0};
+    for (int64_t n : sizes)
+        if (n % e != 0) return false;
+    return true;
+}
 
 // Element-wise kernel: any N, alignment and stride. One CTA per row, three
 // passes over the row's columns (sum of h^2; sum of s^2 over s recomputed from
@@ -66,6 +299,14 @@ __global__ void __launch_bounds__(512) block_fwd_generic_kernel(const BlockP p) 
 
 template <int DT>
 cudaError_t run(const BlockP& p, const OpCfg& c) {
+    if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(p)) {
+        bool taken = false;
+        const cudaError_t e = !p.gate              ? launch_ring<DT, 0>(p, c, &taken)
+                              : p.gate_rows == 1 ? launch_ring<DT, 2>(p, c, &taken)
+                                                   : launch_ring<DT, 1>(p, c, &taken);
+        if (taken) return e;
+    }
+    if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_fwd_generic_kernel<DT>;
@@ -81,6 +322,10 @@ cudaError_t block_fwd_run(const BlockP& p, const OpCfg& c) {
         case kFP16: return run<kFP16>(p, c);
         default: return run<kFP32>(p, c);
     }
+}
+
+cudaError_t block_status_read_and_clear(unsigned int* value) {
+    return symbol_read_and_clear(g_block_status, value);
 }
 
 }  // namespace rmsn

@@ -20,10 +20,16 @@
 
 #include "ops.h"
 #include "ops_common.cuh"
+#include "row_ring.cuh"
+#include "row_ring_host.h"
 
 #include <algorithm>
 
 namespace rmsn {
+
+// Bit 0: a bounded wait ran out since the last read. One word per device.
+__device__ unsigned int g_block_bwd_status;
+
 namespace {
 
 __host__ __device__ inline int64_t range_begin(int64_t b, int64_t grid, int64_t M) {
@@ -35,24 +41,356 @@ __host__ __device__ inline int64_t range_owner(int64_t row, int64_t grid, int64_
     return row < big * (q + 1) ? row / (q + 1) : big + (row - big * (q + 1)) / q;
 }
 
-// Workspace: four areas of `grid` partial rows of `pitch` floats: dw_post,
-// dw_pre, gate sums that begin with the CTA's range, gate sums that begin
-// inside it.
-__device__ inline float* partial(float* ws, int area, int64_t cta, int64_t grid, int64_t pitch) {
-    return ws + (area * grid + cta) * pitch;
+// Workspace: four areas of `slots` partial rows of `pitch` floats: dw_post and
+// dw_pre (a row per CTA), gate sums that begin with a range, gate sums that
+// begin inside it (a row per range: of a CTA, or of a team).
+__device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, int64_t pitch) {
+    return ws + (area * slots + i) * pitch;
+}
+
+// Vector kernel: row teams (row_ring.cuh) with the rows of h, s, dy, ds, and of
+// the gate where each row has its own, staged in shared memory.
+// GATE: 0 none, 1 one gate row for several rows, 2 a gate row per row.
+// A thread owns V vectors of columns. In registers per column: the sums over
+// rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the current row
+// t without its -e s, s and h between the two passes. With a gate row for
+// several rows dw_post changes only where the gate row ends: its sums are in
+// shared memory, a thread's own. fp32 with four vectors has no registers for
+// s, h and the weights: it reads them again (HOLD false), and a stage is then
+// free one row later, behind the next row's barrier.
+template <int DT, int V, int GATE, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
+    constexpr int E = VecElems<DT>::value;
+    constexpr bool HOLD = V * E * (DT == kFP32 ? 2 : 1) <= 16;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ RingShared sh;
+    __shared__ __align__(16) float parts[kMaxTeams][2][3 * kMaxTeamWarps];
+
+    const int team = threadIdx.x / g.T, t = threadIdx.x - team * g.T;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * g.teams + team;
+    const int64_t r0 = me * g.q + (me < g.rem ? me : g.rem);
+    const int rows = static_cast<int>(g.q) + (me < g.rem ? 1 : 0);
+    Ring ring;
+    ring.row_bytes = static_cast<uint32_t>(g.nvec) * 16u;
+    ring.stage_bytes = ring.row_bytes * g.arrays;
+    ring.stages = g.stages;
+    ring.mem = smem + static_cast<size_t>(team) * g.stages * ring.stage_bytes;
+    ring.base = smem_u32(ring.mem);
+    ring.bars = smem_u32(&sh.bars[team][0]);
+    // dw_post sums of GATE 1, [V * E / 4][threads] float4 behind the rings.
+    float4* post_sums = reinterpret_cast<float4*>(smem + g.sums_at);
+    if (t == 0) {
+        for (int st = 0; st < g.stages; ++st) mbar_init(ring.bar(st), 1);
+        fence_mbar_init();
+        sh.dead[team] = 0;
+    }
+    for (int i = t; i < 2 * 3 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
+    const bool need_h = p.w_post || GATE != 0;
+    // Which array of a stage each tensor is.
+    int n_arrays = 0;
+    const int ih = need_h ? n_arrays++ : 0;
+    const int is = p.w_pre ? n_arrays++ : 0;
+    const int idy = p.w_pre ? n_arrays++ : 0;
+    const int ids = p.ds ? n_arrays++ : 0;
+    const int ig = n_arrays;
+    auto issue = [&](int row, int st) {
+        const int64_t i = r0 + row;
+        ring.expect(st);
+        if (need_h) ring.copy(st, ih, static_cast<const uint4*>(p.h) + i * p.ldh);
+        if (p.w_pre) {
+            ring.copy(st, is, static_cast<const uint4*>(p.s) + i * p.lds);
+            ring.copy(st, idy, static_cast<const uint4*>(p.dy) + i * p.lddy);
+        }
+        if (p.ds) ring.copy(st, ids, static_cast<const uint4*>(p.ds) + i * p.ldds);
+        if (GATE == 2) ring.copy(st, ig, static_cast<const uint4*>(p.gate) + i * p.ldg);
+    };
+    pdl_wait();
+    if (t == 0) {
+        for (int k = 0; k < g.stages && k < rows; ++k) issue(k, k);
+    }
+    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+    const uint4* w_post = static_cast<const uint4*>(p.w_post);
+    const uint4* w_pre = static_cast<const uint4*>(p.w_pre);
+    const uint4* gate = static_cast<const uint4*>(p.gate);
+    uint4 wpost[V], wpre[V], gv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = v * g.T + t;
+        wpost[v] = wpre[v] = gv[v] = zero4;
+        if (HOLD && c < g.nvec) {
+            if (w_post) wpost[v] = __ldg(w_post + c);
+            if (w_pre) wpre[v] = __ldg(w_pre + c);
+        }
+    }
+    int64_t grow = 0, left = 0;
+    if (GATE == 1) {
+        grow = r0 / p.gate_rows;
+        left = (grow + 1) * p.gate_rows - r0;
+    }
+    auto load_gate = [&]() {
+        if (!HOLD) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            if (c < g.nvec) gv[v] = __ldg(gate + grow * p.ldg + c);
+        }
+    };
+    if (GATE == 1) {
+        load_gate();
+#pragma unroll
+        for (int i = 0; i < V * E / 4; ++i)
+            post_sums[i * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float P[V][E], pre[V][E];  // GATE 2: P is dw_post
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < E; ++e) P[v][e] = pre[v][e] = 0.f;
+    __syncthreads();
+
+    int st = 0, parity = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    int row = 0;
+    for (; row < rows; ++row) {
+        if (GATE == 1 && left == 0) {
+            ++grow;
+            left = p.gate_rows;
+            load_gate();
+        }
+        if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
+        const float k1 = p.w_post ? __ldg(p.rstd_post + r0 + row) : 1.f;
+        const float k2 = p.w_pre ? __ldg(p.rstd_pre + r0 + row) : 0.f;
+        // The columns' alpha * gate * (offset + w_post), offset + w_pre.
+        auto gate_vec = [&](int v, int c) {
+            return GATE == 2 ? (HOLD ? gv[v] : c < g.nvec ? ring.row(st, ig)[c] : zero4)
+                   : HOLD      ? gv[v] : c < g.nvec ? __ldg(gate + grow * p.ldg + c) : zero4;
+        };
+        auto scales = [&](int v, int c, float* a) {
+            if (GATE != 0) {
+                unpack_vec<DT>(gate_vec(v, c), a);
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] *= p.alpha;
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] = p.alpha;
+            }
+            if (w_post) {
+                float w[E];
+                weights_vec<DT>(HOLD ? wpost[v] : c < g.nvec ? __ldg(w_post + c) : zero4, p.offset, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] *= w[e];
+            }
+        };
+        uint4 hv[V], sv[V];
+        float t0[V][E];
+        float sums[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            const bool in = c < g.nvec;
+            uint4 dyv = zero4, dsv = zero4;
+            hv[v] = sv[v] = zero4;
+            if (in) {
+                if (need_h) hv[v] = ring.row(st, ih)[c];
+                if (p.w_pre) {
+                    sv[v] = ring.row(st, is)[c];
+                    dyv = ring.row(st, idy)[c];
+                }
+                if (p.ds) dsv = ring.row(st, ids)[c];
+                if (GATE == 2 && HOLD) gv[v] = ring.row(st, ig)[c];
+            }
+            unpack_vec<DT>(dsv, t0[v]);
+            float s[E];
+            unpack_vec<DT>(sv[v], s);
+            if (p.w_pre) {
+                float dy[E], w[E];
+                unpack_vec<DT>(dyv, dy);
+                weights_vec<DT>(HOLD ? wpre[v] : in ? __ldg(w_pre + c) : zero4, p.offset, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float u = dy[e] * w[e];
+                    t0[v][e] = fmaf(k2, u, t0[v][e]);
+                    sums[0] = fmaf(u, s[e], sums[0]);
+                    pre[v][e] = fmaf(dy[e], s[e] * k2, pre[v][e]);
+                }
+            }
+            if (w_post) {
+                float a[E], h[E];
+                scales(v, c, a);
+                unpack_vec<DT>(hv[v], h);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float ah = a[e] * h[e];
+                    sums[1] = fmaf(ah, t0[v][e], sums[1]);
+                    sums[2] = fmaf(ah, s[e], sums[2]);
+                }
+            }
+        }
+        team_sums<3>(sums, &parts[team][parity][0], team, t, g.T);
+        parity ^= 1;
+        dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+        if (dead) break;
+        if (t == 0) {
+            if (HOLD) {
+                if (row + g.stages < rows) issue(row + g.stages, st);
+            } else if (row > 0 && row - 1 + g.stages < rows) {
+                // every thread is past its second reading of the row before
+                issue(row - 1 + g.stages, st == 0 ? g.stages - 1 : st - 1);
+            }
+        }
+        const float e2 = k2 * k2 * k2 * (sums[0] / p.n);
+        const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) / p.n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = v * g.T + t;
+            const bool in = c < g.nvec;
+            float s[E], h[E], a[E], o[E];
+            unpack_vec<DT>(HOLD ? sv[v] : in && p.w_pre ? ring.row(st, is)[c] : zero4, s);
+            unpack_vec<DT>(HOLD ? hv[v] : in && need_h ? ring.row(st, ih)[c] : zero4, h);
+            scales(v, c, a);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float tt = fmaf(-e2, s[e], t0[v][e]);
+                t0[v][e] = tt;
+                o[e] = p.beta * tt;
+            }
+            if (in) st_stream(static_cast<uint4*>(p.dr) + (r0 + row) * p.lddr + c, pack_vec<DT>(o));
+            if (GATE == 2) {
+                float w[E], q[E];
+                unpack_vec<DT>(gate_vec(v, c), q);
+                if (w_post)
+                    weights_vec<DT>(HOLD ? wpost[v] : in ? __ldg(w_post + c) : zero4, p.offset, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float gw = p.alpha * (t0[v][e] * (h[e] * k1));
+                    P[v][e] = fmaf(gw, q[e], P[v][e]);
+                    o[e] = w_post ? gw * w[e] : gw;
+                }
+                if (in) st_stream(static_cast<uint4*>(p.dgate) + (r0 + row) * p.lddg + c, pack_vec<DT>(o));
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) P[v][e] = fmaf(t0[v][e], h[e] * k1, P[v][e]);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] = w_post ? fmaf(k1 * a[e], t0[v][e], -(k1 * f) * h[e]) : a[e] * t0[v][e];
+            if (in) st_stream(static_cast<uint4*>(p.dh) + (r0 + row) * p.lddh + c, pack_vec<DT>(o));
+        }
+        if (GATE == 1 && (--left == 0 || row + 1 == rows)) {
+            // The end of a gate row's rows here: their P into dw_post's sums, and
+            // out as dgate where they are all of the gate row's rows.
+            const int64_t first = grow * p.gate_rows;
+            const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
+            const bool whole = first >= r0 && last <= r0 + rows;
+            float* out = partial(p.ws, first > r0 ? 3 : 2, me, g.slots, block_bwd_pitch(p.N));
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = v * g.T + t;
+                const bool in = c < g.nvec;
+                float q[E], w[E], o[E];
+                unpack_vec<DT>(gate_vec(v, c), q);
+                if (w_post)
+                    weights_vec<DT>(HOLD ? wpost[v] : in ? __ldg(w_post + c) : zero4, p.offset, w);
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    float4& acc = post_sums[(v * (E / 4) + i) * blockDim.x + threadIdx.x];
+                    float4 x = acc;
+                    x.x = fmaf(p.alpha * P[v][4 * i], q[4 * i], x.x);
+                    x.y = fmaf(p.alpha * P[v][4 * i + 1], q[4 * i + 1], x.y);
+                    x.z = fmaf(p.alpha * P[v][4 * i + 2], q[4 * i + 2], x.z);
+                    x.w = fmaf(p.alpha * P[v][4 * i + 3], q[4 * i + 3], x.w);
+                    acc = x;
+                    if (in && !whole)
+                        reinterpret_cast<float4*>(out)[c * (E / 4) + i] =
+                            make_float4(P[v][4 * i], P[v][4 * i + 1], P[v][4 * i + 2], P[v][4 * i + 3]);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    o[e] = p.alpha * P[v][e];
+                    if (w_post) o[e] *= w[e];
+                    P[v][e] = 0.f;
+                }
+                if (in && whole)
+                    static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack_vec<DT>(o);
+            }
+        }
+        if (++st == g.stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    if (dead && t == 0) {
+        atomicOr(&g_block_bwd_status, 1u);
+        // Rows below row + stages (HOLD false: row + stages - 1) were issued and
+        // may still be landing.
+        for (int k = row; k < row + g.stages - (HOLD || row == 0 ? 0 : 1) && k < rows; ++k) {
+            mbar_wait_bounded(ring.bar(st), phase, g.limit);
+            if (++st == g.stages) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    pdl_launch_dependents();
+    // The teams' column sums, added in team order through the rings' memory,
+    // into the CTA's partial rows.
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which == 0 ? !w_post : !w_pre) continue;
+        float4* all = reinterpret_cast<float4*>(smem);
+        __syncthreads();  // the rings, or the sums of the round before, are done with
+#pragma unroll
+        for (int i = 0; i < V * E / 4; ++i) {
+            float4 x;
+            if (which == 0 && GATE == 1) {
+                x = post_sums[i * blockDim.x + threadIdx.x];
+            } else {
+                const float* q = (which == 0 ? &P[0][0] : &pre[0][0]) + 4 * i;
+                const float k = which == 0 && GATE == 0 ? p.alpha : 1.f;
+                x = make_float4(k * q[0], k * q[1], k * q[2], k * q[3]);
+            }
+            if (g.teams > 1) all[i * blockDim.x + threadIdx.x] = x;
+            else {
+                const int c = (i / (E / 4)) * g.T + t;
+                if (c < g.nvec)
+                    reinterpret_cast<float4*>(partial(p.ws, which, blockIdx.x, g.slots, block_bwd_pitch(p.N)))
+                        [c * (E / 4) + i % (E / 4)] = x;
+            }
+        }
+        if (g.teams == 1) continue;
+        __syncthreads();
+        if (team == 0) {
+#pragma unroll
+            for (int i = 0; i < V * E / 4; ++i) {
+                const int c = (i / (E / 4)) * g.T + t;
+                float4 x = all[i * blockDim.x + t];
+                for (int k = 1; k < g.teams; ++k) {
+                    const float4 z = all[i * blockDim.x + k * g.T + t];
+                    x.x += z.x;
+                    x.y += z.y;
+                    x.z += z.z;
+                    x.w += z.w;
+                }
+                if (c < g.nvec)
+                    reinterpret_cast<float4*>(partial(p.ws, which, blockIdx.x, g.slots, block_bwd_pitch(p.N)))
+                        [c * (E / 4) + i % (E / 4)] = x;
+            }
+        }
+    }
 }
 
 // Element-wise kernel: any N, alignment and stride; a thread owns the columns
 // tid, tid + T, ... and keeps their sums in the CTA's partial rows.
 template <int DT>
-__global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP p) {
+__global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP p, int64_t slots) {
     __shared__ float part[2 * 3 * 32];
     int parity = 0;
     const int tid = threadIdx.x, T = blockDim.x;
     const int64_t G = gridDim.x, b = blockIdx.x, pitch = block_bwd_pitch(p.N);
     const int64_t r0 = range_begin(b, G, p.M), r1 = range_begin(b + 1, G, p.M);
-    float* acc_post = partial(p.ws, 0, b, G, pitch);
-    float* acc_pre = partial(p.ws, 1, b, G, pitch);
+    float* acc_post = partial(p.ws, 0, b, slots, pitch);
+    float* acc_pre = partial(p.ws, 1, b, slots, pitch);
     const bool per_element = p.gate && p.gate_rows == 1;
     const bool grouped = p.gate && !per_element;
     pdl_wait();
@@ -66,7 +404,7 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
         const int64_t grow = p.gate ? row / p.gate_rows : 0;
         const int64_t g0 = grow * p.ldg;
         if (grouped && (row == r0 || row % p.gate_rows == 0)) {
-            acc_gate = partial(p.ws, row == r0 ? 2 : 3, b, G, pitch);
+            acc_gate = partial(p.ws, row == r0 ? 2 : 3, b, slots, pitch);
             for (int64_t j = tid; j < p.N; j += T) acc_gate[j] = 0.f;
         }
         const float k1 = p.w_post ? p.rstd_post[row] : 1.f;
@@ -132,60 +470,161 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
     pdl_launch_dependents();
 }
 
-// Sums of the partial rows in CTA order: dw_post, dw_pre, and the gate rows
-// that more than one CTA worked on. blockIdx.y is the row summed: 0 dw_post,
-// 1 dw_pre, then one per gate row.
+// Sums of the partial rows in order: dw_post and dw_pre over the G CTAs, and
+// the gate rows that more than one of the R ranges worked on. A CTA sums 32
+// vectors of 4 columns: its 8 warps take every eighth partial row, four loads
+// in flight each, and meet in shared memory in warp order. blockIdx.y: 0
+// dw_post, 1 dw_pre, then gate rows.
 template <int DT>
-__global__ void __launch_bounds__(256) block_bwd_finish_kernel(const BlockBwdP p, int64_t G) {
+__global__ void __launch_bounds__(256) block_bwd_finish_kernel(const BlockBwdP p, int64_t slots, int64_t G,
+                                                               int64_t R) {
+    __shared__ float4 red[8][32];
     const int64_t pitch = block_bwd_pitch(p.N);
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t j4 = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     pdl_wait();
-    if (j >= p.N) return;
     for (int64_t item = blockIdx.y;; item += gridDim.y) {
-        if (item < 2) {
-            float* out = item == 0 ? p.dw_post : p.dw_pre;
-            if (!out) continue;
-            float t = 0.f;
-            for (int64_t b = 0; b < G; ++b)
-                t += partial(p.ws, static_cast<int>(item), b, G, pitch)[j];
-            out[j] = t;
-            continue;
-        }
         const int64_t grow = item - 2;
-        if (!p.gate || p.gate_rows == 1 || grow * p.gate_rows >= p.M) return;
-        const int64_t first = grow * p.gate_rows;
-        const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
-        const int64_t b0 = range_owner(first, G, p.M), b1 = range_owner(last - 1, G, p.M);
-        if (b0 == b1) continue;
-        float t = 0.f;
-        for (int64_t b = b0; b <= b1; ++b) {
-            const int area = b == b0 && range_begin(b, G, p.M) < first ? 3 : 2;
-            t += partial(p.ws, area, b, G, pitch)[j];
+        if (item >= 2 && (!p.gate || p.gate_rows == 1 || grow * p.gate_rows >= p.M)) return;
+        int64_t b0 = 0, b1 = G;
+        int area = static_cast<int>(item), area0 = area;
+        if (item < 2) {
+            if (!(item == 0 ? p.dw_post : p.dw_pre)) continue;
+        } else {
+            const int64_t first = grow * p.gate_rows;
+            const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
+            b0 = range_owner(first, R, p.M);
+            b1 = range_owner(last - 1, R, p.M) + 1;
+            if (b1 - b0 == 1) continue;  // finished by the range itself
+            area = 2;
+            area0 = range_begin(b0, R, p.M) < first ? 3 : 2;
         }
-        t *= p.alpha;
-        if (p.w_post) t *= p.offset + load1<DT>(p.w_post, j);
-        store1<DT>(p.dgate, grow * p.lddg + j, t);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j4 * 4 < p.N) {
+            auto at = [&](int64_t b) {
+                return reinterpret_cast<const float4*>(
+                    partial(p.ws, b == b0 ? area0 : area, b, slots, pitch))[j4];
+            };
+            auto add = [&](const float4& z) {
+                x.x += z.x;
+                x.y += z.y;
+                x.z += z.z;
+                x.w += z.w;
+            };
+            int64_t b = b0 + w;
+            for (; b + 24 < b1; b += 32) {
+                const float4 z0 = at(b), z1 = at(b + 8), z2 = at(b + 16), z3 = at(b + 24);
+                add(z0);
+                add(z1);
+                add(z2);
+                add(z3);
+            }
+            for (; b < b1; b += 8) add(at(b));
+        }
+        __syncthreads();
+        red[w][lane] = x;
+        __syncthreads();
+        if (w < 4) {  // warp w: column w of each vector
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += reinterpret_cast<const float*>(&red[k][lane])[w];
+            const int64_t j = j4 * 4 + w;
+            if (j < p.N) {
+                if (item < 2) {
+                    (item == 0 ? p.dw_post : p.dw_pre)[j] = s;
+                } else {
+                    s *= p.alpha;
+                    if (p.w_post) s *= p.offset + load1<DT>(p.w_post, j);
+                    store1<DT>(p.dgate, grow * p.lddg + j, s);
+                }
+            }
+        }
     }
 }
 
 template <int DT>
+cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G, int64_t R) {
+    const int64_t grows = p.gate && p.gate_rows > 1 ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
+    if (!p.dw_post && !p.dw_pre && grows == 0) return cudaSuccess;
+    Launch l;
+    l.grid = static_cast<int>((p.N + 127) / 128);
+    l.threads = 256;
+    LaunchCfg cfg(l, c.stream, c.pdl);
+    cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + grows, 1024));
+    return cudaLaunchKernelEx(&cfg.cfg, block_bwd_finish_kernel<DT>, p, slots, G, R);
+}
+
+template <int DT, int GATE>
+cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
+    constexpr int E = VecElems<DT>::value;
+    using Fn = void (*)(const BlockBwdP, const RingShape);
+    const int64_t nvec = in.N / E;
+    *taken = false;
+    // Eight columns per thread up to 512 threads, sixteen above.
+    constexpr int V1 = 8 / E;
+    const int V = nvec <= 512 * V1 ? V1 : nvec <= 1024 * V1 ? 2 * V1 : 0;
+    if (V == 0) return cudaSuccess;
+    const int T = static_cast<int>((nvec + V * 32 - 1) / (V * 32)) * 32;
+    const Fn fn = V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512> : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512>;
+    const int arrays = (in.w_post || GATE ? 1 : 0) + (in.w_pre ? 2 : 0) + (in.ds ? 1 : 0) + (GATE == 2 ? 1 : 0);
+    OpCfg cc = c;
+    const int64_t slots = block_bwd_max_grid(in.M, in.N, c.dev.sm_count);
+    RingPlan plan;
+    const int extra = GATE == 1 ? V * E * 4 : 0;
+    if (!ring_plan(reinterpret_cast<const void*>(fn), cc, in.M, static_cast<int>(nvec), T, 512, arrays, extra, &plan))
+        return cudaSuccess;
+    // The teams' sums meet in the rings' memory: with a row per team it may be
+    // smaller than they are.
+    plan.shape.sums_at = std::max(plan.smem - extra * plan.threads, plan.threads * V * E * 4);
+    plan.smem = plan.shape.sums_at + extra * plan.threads;
+    plan.shape.slots = slots;
+    const int64_t teams = plan.grid * plan.shape.teams;
+    if (teams > slots) return cudaSuccess;
+    BlockBwdP p = in;
+    p.ldh /= E;
+    p.lds /= E;
+    p.ldg /= E;
+    p.lddy /= E;
+    p.ldds /= E;
+    p.lddh /= E;
+    p.lddr /= E;
+    p.lddg /= E;
+    *taken = true;
+    const cudaError_t e = op_launch(c, fn, plan.grid, plan.threads, plan.smem, p, plan.shape);
+    return e != cudaSuccess ? e : finish<DT>(in, c, slots, plan.grid, teams);
+}
+
+bool vectors(const BlockBwdP& p) {
+    const int64_t e = vec_elems(p.dtype);
+    const void* ptrs[] = {p.h, p.s, p.w_post, p.gate, p.w_pre, p.dy, p.ds, p.dh, p.dr, p.dgate};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return false;
+    const int64_t sizes[] = {p.N, p.ldh, p.w_pre ? p.lds : 0, p.gate ? p.ldg : 0, p.dy ? p.lddy : 0,
+                             p.ds ? p.ldds : 0, p.lddh, p.lddr, p.gate ? p.lddg : 0};
+    for (int64_t n : sizes)
+        if (n % e != 0) return false;
+    return true;
+}
+
+template <int DT>
 cudaError_t run(const BlockBwdP& p, const OpCfg& c) {
+    if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(p)) {
+        bool taken = false;
+        const cudaError_t e = !p.gate              ? launch_ring<DT, 0>(p, c, &taken)
+                              : p.gate_rows == 1 ? launch_ring<DT, 2>(p, c, &taken)
+                                                   : launch_ring<DT, 1>(p, c, &taken);
+        if (taken) return e;
+    }
+    if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_bwd_generic_kernel<DT>;
     const int occ = occupancy(reinterpret_cast<const void*>(fn), T, 0);
-    const int64_t cap = block_bwd_max_grid(p.M, p.N, c.dev.sm_count);
+    const int64_t slots = block_bwd_max_grid(p.M, p.N, c.dev.sm_count);
     const int64_t G = std::min<int64_t>(
-        cap, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas));
-    cudaError_t e = op_launch(c, fn, G, T, 0, p);
-    const int64_t grows = p.gate && p.gate_rows > 1 ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
-    if (e != cudaSuccess || (!p.dw_post && !p.dw_pre && grows == 0)) return e;
-    Launch l;
-    l.grid = static_cast<int>((p.N + 255) / 256);
-    l.threads = 256;
-    LaunchCfg cfg(l, c.stream, c.pdl);
-    cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + grows, 1024));
-    return cudaLaunchKernelEx(&cfg.cfg, block_bwd_finish_kernel<DT>, p, G);
+        slots, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas));
+    const cudaError_t e = op_launch(c, fn, G, T, 0, p, slots);
+    return e != cudaSuccess ? e : finish<DT>(p, c, slots, G, G);
 }
 
 }  // namespace
@@ -204,6 +643,10 @@ cudaError_t block_bwd_run(const BlockBwdP& p, const OpCfg& c) {
         case kFP16: return run<kFP16>(p, c);
         default: return run<kFP32>(p, c);
     }
+}
+
+cudaError_t block_bwd_status_read_and_clear(unsigned int* value) {
+    return symbol_read_and_clear(g_block_bwd_status, value);
 }
 
 }  // namespace rmsn

@@ -10,6 +10,7 @@
 
 #include "ops.h"
 #include "ops_common.cuh"
+#include "row_ring_host.h"
 
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -207,12 +208,7 @@ cudaError_t cache_read_run(const CacheP& p, const OpCfg& c) {
 }
 
 cudaError_t cache_status_read_and_clear(unsigned int* value) {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_cache_status, sizeof(*value));
-    if (e == cudaSuccess && *value != 0) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_cache_status, &zero, sizeof(zero));
-    }
-    return e;
+    return symbol_read_and_clear(g_cache_status, value);
 }
 
 }  // namespace rmsn

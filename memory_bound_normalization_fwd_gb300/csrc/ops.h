@@ -72,6 +72,8 @@ struct BlockBwdP {
 
 cudaError_t block_fwd_run(const BlockP& p, const OpCfg& c);
 cudaError_t block_bwd_run(const BlockBwdP& p, const OpCfg& c);
+cudaError_t block_status_read_and_clear(unsigned int* value);
+cudaError_t block_bwd_status_read_and_clear(unsigned int* value);
 
 // The backward's grid never exceeds this (partial rows are counted by it).
 int block_bwd_max_grid(int64_t M, int64_t N, int sm_count);

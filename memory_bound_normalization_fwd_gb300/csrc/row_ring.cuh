@@ -1,0 +1,96 @@
+// Row teams with a ring of rows in shared memory, for the block operator's
+// vector kernels.
+//
+// A team of T threads (whole warps) walks a contiguous range of rows. Its
+// leader brings each row's arrays into the team's ring of S stages by bulk
+// asynchronous copies, counted on the stage's mbarrier, S rows ahead, so the
+// bytes in flight do not depend on registers. A CTA holds up to kMaxTeams
+// teams; they share nothing but the SM.
+//
+// Waits are bounded: a thread whose stage does not land in time marks its team,
+// which all of its threads see behind the row's reduction barrier; the team
+// then writes nothing more, waits (bounded) for its copies in flight and ends.
+#pragma once
+
+#include "async_copy.cuh"
+#include "ops_common.cuh"
+
+namespace rmsn {
+
+constexpr int kMaxTeams = 8;
+constexpr int kMaxRing = 8;      // stages
+constexpr int kMaxTeamWarps = 16;
+
+// How rows, teams and stages are laid out; filled by the host.
+struct RingShape {
+    int T;            // threads of a team, a multiple of 32
+    int teams;        // of a CTA
+    int stages;
+    int nvec;         // 16-byte vectors of a row
+    int arrays;       // rows per stage
+    int rem;          // the first `rem` teams walk q + 1 rows, the others q
+    int64_t q;
+    int64_t slots;    // partial rows per workspace area (backward)
+    int sums_at;      // byte offset behind the rings (backward)
+    long long limit;  // bound of a wait in SM cycles
+};
+
+struct RingShared {
+    uint64_t bars[kMaxTeams][kMaxRing];
+    unsigned int dead[kMaxTeams];
+};
+
+__device__ __forceinline__ void ring_barrier(int team, int T) {
+    if (T == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(T) : "memory");
+}
+
+// Sums over a team in a fixed order; `part` is [K][kMaxTeamWarps] floats of this
+// call's parity, zero behind the team's warps. One team barrier.
+template <int K>
+__device__ __forceinline__ void team_sums(float (&v)[K], float* part, int team, int t, int T) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    }
+    if (T > 32 && (t & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) part[k * kMaxTeamWarps + (t >> 5)] = v[k];
+    }
+    ring_barrier(team, T);
+    if (T > 32) {
+        const int n4 = (T + 127) >> 7;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float4* q = reinterpret_cast<const float4*>(part + k * kMaxTeamWarps);
+            float s = 0.f;
+            for (int i = 0; i < n4; ++i) {
+                const float4 x = q[i];
+                s += (x.x + x.y) + (x.z + x.w);
+            }
+            v[k] = s;
+        }
+    }
+}
+
+// A team's ring: the leader's issue side and everybody's wait side.
+struct Ring {
+    uint32_t bars;       // shared address of the team's barriers
+    uint32_t base;       // shared address of the team's stages
+    const unsigned char* mem;
+    uint32_t row_bytes;  // of one array
+    uint32_t stage_bytes;
+    int stages;
+
+    __device__ __forceinline__ const uint4* row(int st, int array) const {
+        return reinterpret_cast<const uint4*>(mem + st * stage_bytes + array * row_bytes);
+    }
+    __device__ __forceinline__ uint32_t bar(int st) const { return bars + 8 * st; }
+    __device__ __forceinline__ void expect(int st) const { mbar_arrive_expect_tx(bar(st), stage_bytes); }
+    __device__ __forceinline__ void copy(int st, int array, const void* src) const {
+        bulk_g2s(base + st * stage_bytes + array * row_bytes, src, row_bytes, bar(st));
+    }
+};
+
+}  // namespace rmsn

@@ -1,0 +1,33 @@
+// Host side of the row-team kernels: how many teams, stages and CTAs.
+#pragma once
+
+#include "ops.h"
+#include "row_ring.cuh"
+
+namespace rmsn {
+
+struct RingPlan {
+    RingShape shape;
+    int64_t grid;
+    int threads;
+    int smem;
+};
+
+// Lays out `arrays` rows of `nvec` vectors per stage for teams of T threads in
+// CTAs of up to `max_threads`, with `extra` more bytes of shared memory per
+// CTA thread. False where a row does not fit two stages of shared memory.
+bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
+               int extra, RingPlan* out);
+
+// Reads a status word of the current device and clears it.
+template <typename S>
+cudaError_t symbol_read_and_clear(const S& symbol, unsigned int* value) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, symbol, sizeof(*value));
+    if (e == cudaSuccess && *value != 0) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace rmsn
