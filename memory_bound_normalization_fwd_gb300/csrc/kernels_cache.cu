@@ -12,6 +12,8 @@
 #include "ops_common.cuh"
 #include "row_ring_host.h"
 
+#include <algorithm>
+
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -178,8 +180,190 @@ __global__ void __launch_bounds__(256) cache_read_generic_kernel(const CacheP p)
     }
 }
 
+// Vector kernels: groups of 32 values as 16-byte vectors. A thread takes 16
+// values: half a group, whose other half is the neighbouring lane's, and one
+// 16-byte (E4M3) or 8-byte (E2M1) piece of codes. Consecutive threads take
+// consecutive halves of k's token, then of v's. Bound by HBM: each value read
+// and each code written once, or the other way round.
+
+// The largest magnitude of 16 values, as fp32 bits.
+__device__ __forceinline__ uint32_t amax16(const float* f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
+        m = b > m ? b : m;
+    }
+    return m;
+}
+
+// `halves`: 16-value pieces of a token's heads of one tensor; units = T * tensors * halves.
+template <int DT, int F>
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheP p, int tensors, int halves, int head_halves) {
+    constexpr int E = VecElems<DT>::value, NV = 16 / E;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t units = p.T * tensors * halves;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    // whole warps stay together: the two halves of a group are neighbouring lanes
+    for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; u0 < units; u0 += step) {
+        const int64_t u = u0 + threadIdx.x;
+        const int64_t tk = u / halves;
+        const int i = static_cast<int>(u - tk * halves);
+        const int64_t t = tensors == 2 ? tk >> 1 : tk;
+        const int k = tensors == 2 ? static_cast<int>(tk & 1) : 0;
+        const int h = i / head_halves, part = i - h * head_halves;
+        const int64_t slot = u < units ? __ldg(p.slot + t) : -1;
+        const bool in = slot >= 0 && slot < p.slots;
+        if (slot >= p.slots && i == 0 && k == 0) atomicOr(&g_cache_status, 1u);
+        float f[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) f[q] = 0.f;
+        if (in) {
+            const uint4* x = static_cast<const uint4*>(p.t[k].p) + t * p.t[k].st + h * p.t[k].sh + part * NV;
+            uint4 v[NV];
+#pragma unroll
+            for (int q = 0; q < NV; ++q) v[q] = ld_stream(x + q);
+#pragma unroll
+            for (int q = 0; q < NV; ++q) unpack_vec<DT>(v[q], f + q * E);
+        }
+        uint32_t amax = amax16(f);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, amax, 1);
+        amax = other > amax ? other : amax;
+        const uint32_t byte = scale_byte<F>(amax);
+        const float inv = inverse_scale(byte);
+        if (!in) continue;
+        const int64_t head = cache_head(p, slot, h);
+        if ((part & 1) == 0) p.scales[k][head * p.groups + (part >> 1)] = static_cast<uint8_t>(byte);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) f[q] = byte == 255u ? 0.f : f[q] * inv;
+        if (F == RMSNORM_CACHE_E4M3) {
+            uint32_t c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                c[q] = to_e4m3x2(f[4 * q], f[4 * q + 1]) | to_e4m3x2(f[4 * q + 2], f[4 * q + 3]) << 16;
+            *reinterpret_cast<uint4*>(p.codes[k] + head * p.code_bytes + part * 16) =
+                make_uint4(c[0], c[1], c[2], c[3]);
+        } else {
+            uint32_t c[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                c[q] = to_e2m1x2(f[8 * q], f[8 * q + 1]) | to_e2m1x2(f[8 * q + 2], f[8 * q + 3]) << 8 |
+                       to_e2m1x2(f[8 * q + 4], f[8 * q + 5]) << 16 | to_e2m1x2(f[8 * q + 6], f[8 * q + 7]) << 24;
+            *reinterpret_cast<uint2*>(p.codes[k] + head * p.code_bytes + part * 8) = make_uint2(c[0], c[1]);
+        }
+    }
+}
+
+// A CTA takes rows of the outputs in tiles: a row's slot is looked up once, by one
+// thread, and shared; then the threads take the tile's 16-value pieces.
+constexpr int kReadRows = 64;  // most rows of a tile
+
+template <int DT, int F>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheP p, int tensors, int first, int halves,
+                                                         int head_halves, int tile_rows) {
+    constexpr int E = VecElems<DT>::value, NV = 16 / E;
+    __shared__ int64_t slots[kReadRows];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t tiles = (p.rows + tile_rows - 1) / tile_rows;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t row0 = tile * tile_rows;
+        const int n = static_cast<int>(min(static_cast<int64_t>(tile_rows), p.rows - row0));
+        __syncthreads();  // the slots of the tile before are read
+        if (threadIdx.x < n) {
+            const int64_t slot = read_slot(p, row0 + threadIdx.x);
+            if (slot == -2) atomicOr(&g_cache_status, 1u);
+            slots[threadIdx.x] = slot;
+        }
+        __syncthreads();
+        const int units = n * tensors * halves;
+#pragma unroll 2
+        for (int u = threadIdx.x; u < units; u += 256) {
+            const int rk = u / halves, i = u - rk * halves;
+            const int row = tensors == 2 ? rk >> 1 : rk;
+            const int k = tensors == 2 ? rk & 1 : first;
+            const int64_t slot = slots[row];
+            if (slot == -1) continue;
+            const int h = i / head_halves, part = i - h * head_halves;
+            uint4* y = static_cast<uint4*>(p.t[k].p) + (row0 + row) * p.t[k].st + h * p.t[k].sh + part * NV;
+            float f[16];
+            if (slot < 0) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) f[q] = 0.f;
+            } else {
+                const int64_t head = cache_head(p, slot, h);
+                const float scale = scale_of(__ldg(p.scales[k] + head * p.groups + (part >> 1)));
+                if (F == RMSNORM_CACHE_E4M3) {
+                    const uint4 c = ld_stream(
+                        reinterpret_cast<const uint4*>(p.codes[k] + head * p.code_bytes + part * 16));
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 a = from_e4m3x2(w[q] & 0xffffu), b = from_e4m3x2(w[q] >> 16);
+                        f[4 * q] = a.x * scale;
+                        f[4 * q + 1] = a.y * scale;
+                        f[4 * q + 2] = b.x * scale;
+                        f[4 * q + 3] = b.y * scale;
+                    }
+                } else {
+                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(p.codes[k] + head * p.code_bytes + part * 8));
+                    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float2 a = from_e2m1x2((w[q >> 2] >> (8 * (q & 3))) & 0xffu);
+                        f[2 * q] = a.x * scale;
+                        f[2 * q + 1] = a.y * scale;
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NV; ++q) st_stream(y + q, pack_vec<DT>(f + q * E));
+        }
+    }
+}
+
+// Whole groups, vectors and pieces everywhere.
+bool vectors(bool write, const CacheP& p) {
+    const int E = vec_elems(p.dtype);
+    if (p.D % kGroup != 0) return false;
+    const int64_t rows = write ? p.T : p.rows;
+    const uintptr_t to = p.format == RMSNORM_CACHE_E4M3 ? 15 : 7;
+    for (int k = 0; k < 2; ++k) {
+        if (!p.t[k].p) continue;
+        if (!aligned16(p.t[k].p) || (rows > 1 && p.t[k].st % E) || (p.heads > 1 && p.t[k].sh % E) ||
+            (reinterpret_cast<uintptr_t>(p.codes[k]) & to))
+            return false;
+    }
+    return static_cast<int64_t>(p.heads) * p.D / 16 * 2 * kReadRows < (int64_t(1) << 31);
+}
+
+template <int DT, int F>
+cudaError_t run_vector(bool write, CacheP p, const OpCfg& c) {
+    const int E = VecElems<DT>::value;
+    const int head_halves = p.D / 16, halves = p.heads * head_halves;
+    for (int k = 0; k < 2; ++k) {
+        p.t[k].st /= E;
+        p.t[k].sh /= E;
+    }
+    const int tensors = (p.t[0].p ? 1 : 0) + (p.t[1].p ? 1 : 0);
+    if (write) {
+        const int64_t G = persistent_grid(p.T * tensors * halves, 256, c.dev.sm_count, 8, c.max_ctas);
+        return op_launch(c, cache_write_kernel<DT, F>, G, 256, 0, p, tensors, halves, head_halves);
+    }
+    // About eight pieces per thread and tile, fewer where rows are few.
+    int64_t tile = std::max<int64_t>(1, 8 * 256 / (tensors * halves));
+    tile = std::min<int64_t>(tile, std::max<int64_t>(1, p.rows / (2 * c.dev.sm_count)));
+    tile = std::min<int64_t>(tile, kReadRows);
+    const int64_t G = persistent_grid((p.rows + tile - 1) / tile, 1, c.dev.sm_count, 8, c.max_ctas);
+    return op_launch(c, cache_read_kernel<DT, F>, G, 256, 0, p, tensors, p.t[0].p ? 0 : 1, halves, head_halves,
+                     static_cast<int>(tile));
+}
+
 template <int DT, int F>
 cudaError_t run(bool write, const CacheP& p, const OpCfg& c) {
+    if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(write, p)) return run_vector<DT, F>(write, p, c);
+    if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     const int64_t units = (write ? p.T : p.rows) * p.heads * p.groups;
     const int64_t G = persistent_grid(units, 256, c.dev.sm_count, 8, c.max_ctas);
     return op_launch(c, write ? cache_write_generic_kernel<DT, F> : cache_read_generic_kernel<DT, F>,
