@@ -494,8 +494,8 @@ def bwd(x, w, rstd, dy, offset: float = 0.0, dx=None, stream=None, **options):
 # ---- the operators between a block's matrix products -----------------------
 #
 # Calls of a decoding step are host-bound, so these pack their argument structs
-# with struct.Struct (a microsecond) and make no context managers unless the
-# tensors' device or the stream is not the current one.
+# with struct.Struct, check a tensor in one expression and make no context managers
+# unless the tensors' device or the stream is not the current one.
 
 _BLOCK = struct.Struct("=2i3q9Q5q4f")
 _BLOCK_GRADS = struct.Struct("=2i7Q5q")
@@ -505,17 +505,18 @@ _CACHE = struct.Struct("=2iq4i4Q")
 _HEADS = struct.Struct("=Q3q")
 CACHE_FORMATS = {"e4m3": 0, "e2m1": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
-_CODES = None
+_CODES: dict = {}
+_sizes: dict = {}  # workspace bytes by device and sizes
 
 
 def _code(dtype):
-    global _CODES
-    if _CODES is None:
-        import torch
-        _CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
     code = _CODES.get(dtype)
     if code is None:
-        raise TypeError(f"RMSNorm takes bf16, fp16 or fp32 activations, got {dtype}")
+        import torch
+        _CODES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        if dtype not in _CODES:
+            raise TypeError(f"RMSNorm takes bf16, fp16 or fp32 activations, got {dtype}")
+        code = _CODES[dtype]
     return code
 
 
@@ -533,47 +534,62 @@ def _elsewhere(t, stream):
     return torch.cuda.stream(stream)
 
 
-def _stream_ptr():
+def _stream_ptr(device: int) -> int:
+    """The current stream of a device (torch's own accessor of the address where it
+    has one: 0.1 us against 2.9 for a Stream object)."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _same(t, like, name, dtype=None):
-    if t is not None and (t.dtype != (dtype or like.dtype) or t.get_device() != like.get_device()):
-        raise ValueError(f"{name} must be {dtype or like.dtype} on {like.device}, "
-                         f"got {t.dtype} on {t.device}")
+def _workspace(t, size, *key):
+    """A workspace of size(*key) bytes on t's device, the current one."""
+    import torch
+    n = _sizes.get((size, t.get_device(), key))
+    if n is None:
+        if len(_sizes) >= 4096:  # ragged batches: as many sizes as lengths
+            _sizes.clear()
+        n = _sizes[(size, t.get_device(), key)] = size(*key)
+    return t.new_empty(n, dtype=torch.uint8)
 
 
-def _rows(t, name, like, M, N):
-    """(address, row stride) of a matrix of M rows given as [..., N]."""
+def _refuse(t, name, shape, dtype, device):
+    if t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name, shape, dtype, device, N):
+    """(address, row stride) of a matrix of rows given as [..., N]."""
     if t is None:
         return 0, 0
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    _same(t, like, name)
-    if t.is_contiguous():
-        return t.data_ptr(), N
-    if t.dim() == 2 and (t.stride(1) == 1 or N == 1):
-        return t.data_ptr(), t.stride(0)
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), N
+        if t.dim() == 2 and (t.stride(1) == 1 or N == 1):
+            return t.data_ptr(), t.stride(0)
+    _refuse(t, name, shape, dtype, device)
     raise ValueError(f"{name} must be contiguous, or 2-D with unit column stride")
 
 
-def _vector(t, name, like, N, dtype=None):
+def _vector(t, name, n, dtype, device):
+    """The address of n contiguous elements (0 for None)."""
     if t is None:
         return 0
-    _same(t, like, name, dtype)
-    if t.numel() != N or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {N} elements")
-    return t.data_ptr()
+    if t.numel() == n and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, None, dtype, device)
+    raise ValueError(f"{name} must be contiguous with {n} elements")
 
 
-def _gate(gate, gate_rows, like, M, N):
+def _gate(gate, gate_rows, dtype, device, M, N):
     """(address, row stride, rows of h per gate row) of a gate [N] or [..., N]."""
     if gate is None:
         if gate_rows:
             raise ValueError("gate_rows without a gate")
         return 0, 0, 0
-    _same(gate, like, "gate")
+    _refuse(gate, "gate", None, dtype, device)
     if gate.shape[-1] != N:
         raise ValueError(f"gate must have {N} columns, got {tuple(gate.shape)}")
     G = gate.numel() // N
@@ -612,30 +628,44 @@ def block_fwd(h, r, w_post=None, w_pre=None, gate=None, gate_rows=None, eps: flo
         with ctx:
             return block_fwd(h, r, w_post, w_pre, gate, gate_rows, eps, offset, alpha, beta, s, y,
                              rstd, **options)
-    N = h.shape[-1]
+    shape, dtype, dev = h.shape, h.dtype, h.get_device()
+    N = shape[-1]
     M = h.numel() // N if N else 0
-    hp, ldh = _rows(h, "h", h, M, N)
-    rp, ldr = _rows(r, "r", h, M, N)
-    gp, ldg, gate_rows = _gate(gate, gate_rows, h, M, N)
-    wpost, wpre = _vector(w_post, "w_post", h, N), _vector(w_pre, "w_pre", h, N)
+    code = _code(dtype)
+    hp, ldh = _rows(h, "h", shape, dtype, dev, N)
+    rp, ldr = _rows(r, "r", shape, dtype, dev, N)
+    gp, ldg, gate_rows = _gate(gate, gate_rows, dtype, dev, M, N)
+    wpost = _vector(w_post, "w_post", N, dtype, dev)
+    wpre = _vector(w_pre, "w_pre", N, dtype, dev)
+    lds = ldy = N
     if s is None:
-        s = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    if y is None:
-        y = torch.empty(h.shape, dtype=h.dtype, device=h.device) if wpre else None
-    elif not wpre:
-        raise ValueError("y without w_pre")
-    sp, lds = _rows(s, "s", h, M, N)
-    yp, ldy = _rows(y, "y", h, M, N)
+        s = h.new_empty(shape)
+        sp = s.data_ptr()
+    else:
+        sp, lds = _rows(s, "s", shape, dtype, dev, N)
+    yp = 0
+    if y is not None:
+        if not wpre:
+            raise ValueError("y without w_pre")
+        yp, ldy = _rows(y, "y", shape, dtype, dev, N)
+    elif wpre:
+        y = h.new_empty(shape)
+        yp = y.data_ptr()
     a = b = None
+    ap = bp = 0
     if rstd:
         if wpost:
-            a = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
+            a = h.new_empty(shape[:-1], dtype=torch.float32)
+            ap = a.data_ptr()
         if wpre:
-            b = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
-    args = _BLOCK.pack(160, _code(h.dtype), M, N, gate_rows, hp, rp, wpost, gp, wpre, sp, yp,
-                       0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(),
+            b = h.new_empty(shape[:-1], dtype=torch.float32)
+            bp = b.data_ptr()
+    args = _BLOCK.pack(160, code, M, N, gate_rows, hp, rp, wpost, gp, wpre, sp, yp, ap, bp,
                        ldh, ldr, ldg, lds, ldy, eps, offset, alpha, beta)
-    _check(rmsnorm_block_fwd(args, make_options(**options) if options else None, _stream_ptr()))
+    rc = (_lib or lib()).rmsnorm_block_fwd(args, _opt(make_options(**options)) if options else None,
+                                           _stream_ptr(dev))
+    if rc:
+        _check(rc)
     return s, y, a, b
 
 
@@ -656,38 +686,53 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
         with ctx:
             return block_bwd(h, s, rstd_post, rstd_pre, dy, ds, w_post, w_pre, gate, gate_rows,
                              offset, alpha, beta, dh, dr, workspace, **options)
-    N = h.shape[-1]
+    shape, dtype, dev = h.shape, h.dtype, h.get_device()
+    N = shape[-1]
     M = h.numel() // N if N else 0
-    code = _code(h.dtype)
-    hp, ldh = _rows(h, "h", h, M, N)
-    sp, lds = _rows(s, "s", h, M, N)
-    dyp, lddy = _rows(dy, "dy", h, M, N)
-    dsp, ldds = _rows(ds, "ds", h, M, N)
-    gp, ldg, gate_rows = _gate(gate, gate_rows, h, M, N)
-    wpost, wpre = _vector(w_post, "w_post", h, N), _vector(w_pre, "w_pre", h, N)
-    ap = _vector(rstd_post, "rstd_post", h, M, torch.float32) if wpost else 0
-    bp = _vector(rstd_pre, "rstd_pre", h, M, torch.float32) if wpre else 0
+    code, f32 = _code(dtype), torch.float32
+    hp, ldh = _rows(h, "h", shape, dtype, dev, N)
+    sp, lds = _rows(s, "s", shape, dtype, dev, N)
+    dyp, lddy = _rows(dy, "dy", shape, dtype, dev, N)
+    dsp, ldds = _rows(ds, "ds", shape, dtype, dev, N)
+    gp, ldg, gate_rows = _gate(gate, gate_rows, dtype, dev, M, N)
+    wpost = _vector(w_post, "w_post", N, dtype, dev)
+    wpre = _vector(w_pre, "w_pre", N, dtype, dev)
+    ap = _vector(rstd_post, "rstd_post", M, f32, dev) if wpost else 0
+    bp = _vector(rstd_pre, "rstd_pre", M, f32, dev) if wpre else 0
+    lddh = lddr = N
     if dh is None:
-        dh = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        dh = h.new_empty(shape)
+        dhp = dh.data_ptr()
+    else:
+        dhp, lddh = _rows(dh, "dh", shape, dtype, dev, N)
     if dr is None:
-        dr = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    dhp, lddh = _rows(dh, "dh", h, M, N)
-    drp, lddr = _rows(dr, "dr", h, M, N)
-    dgate = torch.empty(gate.shape, dtype=h.dtype, device=h.device) if gp else None
-    dwa = torch.empty(N, dtype=torch.float32, device=h.device) if wpost else None
-    dwb = torch.empty(N, dtype=torch.float32, device=h.device) if wpre else None
+        dr = h.new_empty(shape)
+        drp = dr.data_ptr()
+    else:
+        drp, lddr = _rows(dr, "dr", shape, dtype, dev, N)
+    dgate = dwa = dwb = None
+    dgp = dwap = dwbp = lddg = 0
+    if gp:
+        dgate = h.new_empty(gate.shape)
+        dgp, lddg = dgate.data_ptr(), N
+    if wpost:
+        dwa = h.new_empty(N, dtype=f32)
+        dwap = dwa.data_ptr()
+    if wpre:
+        dwb = h.new_empty(N, dtype=f32)
+        dwbp = dwb.data_ptr()
     if workspace is None:
-        workspace = torch.empty(rmsnorm_block_bwd_workspace_size(M, N, code), dtype=torch.uint8,
-                                device=h.device)
+        workspace = _workspace(h, rmsnorm_block_bwd_workspace_size, M, N, code)
     args = _BLOCK.pack(160, code, M, N, gate_rows, hp, 0, wpost, gp, wpre, sp, 0, ap, bp,
                        ldh, 0, ldg, lds, 0, 0.0, offset, alpha, beta)
-    grads = _BLOCK_GRADS.pack(104, 0, dyp, dsp, dhp, drp, 0 if dgate is None else dgate.data_ptr(),
-                              0 if dwa is None else dwa.data_ptr(),
-                              0 if dwb is None else dwb.data_ptr(),
-                              lddy, ldds, lddh, lddr, N if dgate is not None else 0)
-    _check(rmsnorm_block_bwd(args, grads, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(),
-                             make_options(**options) if options else None, _stream_ptr()))
+    grads = _BLOCK_GRADS.pack(104, 0, dyp, dsp, dhp, drp, dgp, dwap, dwbp, lddy, ldds, lddh, lddr,
+                              lddg)
+    rc = (_lib or lib()).rmsnorm_block_bwd(args, grads, workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           _opt(make_options(**options)) if options else None,
+                                           _stream_ptr(dev))
+    if rc:
+        _check(rc)
     return dh, dr, dgate, dwa, dwb
 
 
@@ -717,44 +762,49 @@ def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: dict | None = No
     return steps.to(device), mag.value
 
 
-def _heads(t, name, like, shape):
+def _heads(t, name, shape, dtype, device):
     """A heads tensor [T, H, D] or [B, S, H, D] as the struct's four values."""
     if t is None:
-        return 0, 0, 0, 0
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same(t, like, name)
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name} must have unit stride within a head")
-    return (t.data_ptr(), 0, st[0], st[1]) if len(st) == 3 else (t.data_ptr(), st[0], st[1], st[2])
+        return _NO_HEADS
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+        st = t.stride()
+        if st[-1] == 1 or shape[-1] == 1:
+            return (t.data_ptr(), 0, st[0], st[1]) if len(st) == 3 else (t.data_ptr(), *st[:3])
+    _refuse(t, name, shape, dtype, device)
+    raise ValueError(f"{name} must have unit stride within a head")
 
 
-def _rope_common(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude):
-    """The fields of the rope structs up to the weights, and k's shape."""
+_NO_HEADS = (0, 0, 0, 0)
+
+
+def _rope_common(q, k, steps, positions, w_q, w_k, interleaved):
+    """The fields of the rope struct up to the weights."""
     import torch
-    if q.dim() not in (3, 4):
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    if len(shape) == 3:
+        B, (S, hq, D) = 1, shape
+    elif len(shape) == 4:
+        B, S, hq, D = shape
+    else:
         raise ValueError("q must be [tokens, heads, head_dim] or [batch, seq, heads, head_dim]")
-    shape = q.shape
-    B, S = (1, shape[0]) if len(shape) == 3 else (shape[0], shape[1])
-    D, hk = shape[-1], 0
+    hk = 0
     if k is not None:
-        if k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != D:
-            raise ValueError(f"k must be like q but for its heads, got {tuple(k.shape)}")
-        hk = k.shape[-2]
-    _same(steps, q, "steps", torch.int64)
-    if not steps.is_contiguous():
-        raise ValueError("steps must be contiguous")
+        ks = k.shape
+        if len(ks) != len(shape) or ks[:-2] != shape[:-2] or ks[-1] != D:
+            raise ValueError(f"k must be like q but for its heads, got {tuple(ks)}")
+        hk = ks[-2]
+    half = steps.numel()
+    sp = _vector(steps, "steps", half, torch.int64, dev)
     pp = ps = 0
     if positions is not None:
-        _same(positions, q, "positions", torch.int64)
-        ok = positions.shape == shape[:-2] or positions.dim() == 1 and positions.shape[0] == S
-        if not ok or positions.stride(-1) != 1 and S > 1:
+        if positions.dtype is not torch.int64 or positions.get_device() != dev:
+            _refuse(positions, "positions", None, torch.int64, dev)
+        ps = positions.shape
+        if (ps != shape[:-2] and ps != (S,)) or (S > 1 and positions.stride(-1) != 1):
             raise ValueError("positions must be [seq] or [batch, seq], the last contiguous")
-        pp, ps = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    return (248, _code(q.dtype), B, S, shape[-2], hk, D, 2 * steps.numel(), 1 if interleaved else 0,
-            0, pp, ps, steps.data_ptr(), _vector(w_q, "w_q", q, D), _vector(w_k, "w_k", q, D)), \
-        (eps, offset, magnitude, 0.0)
+        pp, ps = positions.data_ptr(), positions.stride(0) if len(ps) == 2 and B > 1 else 0
+    return (248, _code(dtype), B, S, hq, hk, D, 2 * half, 1 if interleaved else 0, 0, pp, ps, sp,
+            _vector(w_q, "w_q", D, dtype, dev), _vector(w_k, "w_k", D, dtype, dev))
 
 
 def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool = False,
@@ -778,23 +828,34 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
         with ctx:
             return rope_fwd(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude,
                             q_out, k_out, rstd, **options)
-    head, scalars = _rope_common(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude)
-    dev = q.device
+    head = _rope_common(q, k, steps, positions, w_q, w_k, interleaved)
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    qh = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-    elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    a = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if rstd and w_q is not None else None
-    b = torch.empty(k.shape[:-1], dtype=torch.float32, device=dev) \
-        if rstd and w_k is not None and k is not None else None
-    ks = None if k is None else k.shape
-    args = _ROPE.pack(*head, 0 if a is None else a.data_ptr(), 0 if b is None else b.data_ptr(),
-                      *scalars, *_heads(q, "q", q, q.shape), *_heads(k, "k", q, ks),
-                      *_heads(q_out, "q_out", q, q.shape), *_heads(k_out, "k_out", q, ks))
-    _check(rmsnorm_rope_fwd(args, make_options(**options) if options else None, _stream_ptr()))
+        q_out = q.new_empty(shape)
+    qo = _heads(q_out, "q_out", shape, dtype, dev)
+    kh = ko = _NO_HEADS
+    a = b = None
+    ap = bp = 0
+    if k is not None:
+        kshape = k.shape
+        kh = _heads(k, "k", kshape, dtype, dev)
+        if k_out is None:
+            k_out = k.new_empty(kshape)
+        ko = _heads(k_out, "k_out", kshape, dtype, dev)
+        if rstd and w_k is not None:
+            b = k.new_empty(kshape[:-1], dtype=torch.float32)
+            bp = b.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if rstd and w_q is not None:
+        a = q.new_empty(shape[:-1], dtype=torch.float32)
+        ap = a.data_ptr()
+    args = _ROPE.pack(*head, ap, bp, eps, offset, magnitude, 0.0, *qh, *kh, *qo, *ko)
+    rc = (_lib or lib()).rmsnorm_rope_fwd(args, _opt(make_options(**options)) if options else None,
+                                          _stream_ptr(dev))
+    if rc:
+        _check(rc)
     return q_out, k_out, a, b
 
 
@@ -814,39 +875,46 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
         with ctx:
             return rope_bwd(dq_out, dk_out, steps, positions, q, k, rstd_q, rstd_k, w_q, w_k,
                             interleaved, offset, magnitude, dq, dk, workspace, **options)
-    head, scalars = _rope_common(dq_out, dk_out, steps, positions, w_q, w_k, interleaved, 0.0, offset,
-                                 magnitude)
-    dev, D = dq_out.device, dq_out.shape[-1]
-    qs, ks = dq_out.shape, None if dk_out is None else dk_out.shape
+    head = _rope_common(dq_out, dk_out, steps, positions, w_q, w_k, interleaved)
+    shape, dtype, dev, f32 = dq_out.shape, dq_out.dtype, dq_out.get_device(), torch.float32
+    D = shape[-1]
+    gq = _heads(dq_out, "dq_out", shape, dtype, dev)
     if dq is None:
-        dq = torch.empty(qs, dtype=dq_out.dtype, device=dev)
-    if dk_out is None:
-        if dk is not None:
-            raise ValueError("dk without dk_out")
-    elif dk is None:
-        dk = torch.empty(ks, dtype=dq_out.dtype, device=dev)
-    ap = bp = 0
+        dq = dq_out.new_empty(shape)
+    oq = _heads(dq, "dq", shape, dtype, dev)
+    qh = kh = gk = ok = _NO_HEADS
     dwq = dwk = None
+    ap = bp = wqp = wkp = 0
     if w_q is not None:
-        ap = _vector(rstd_q, "rstd_q", dq_out, qs[:-1].numel(), torch.float32)
-        dwq = torch.empty(D, dtype=torch.float32, device=dev)
-    if w_k is not None and ks is not None:
-        bp = _vector(rstd_k, "rstd_k", dq_out, ks[:-1].numel(), torch.float32)
-        dwk = torch.empty(D, dtype=torch.float32, device=dev)
-    if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(rmsnorm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
-    none = (0, 0, 0, 0)
-    args = _ROPE.pack(*head, ap, bp, *scalars,
-                      *(_heads(q, "q", dq_out, qs) if w_q is not None else none),
-                      *(_heads(k, "k", dq_out, ks) if w_k is not None else none), *none, *none)
-    grads = _ROPE_GRADS.pack(152, 0, *_heads(dq_out, "dq_out", dq_out, qs),
-                             *_heads(dk_out, "dk_out", dq_out, ks), *_heads(dq, "dq", dq_out, qs),
-                             *_heads(dk, "dk", dq_out, ks), 0 if dwq is None else dwq.data_ptr(),
-                             0 if dwk is None else dwk.data_ptr())
-    ws_ptr = 0 if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
-                            make_options(**options) if options else None, _stream_ptr()))
+        ap = _vector(rstd_q, "rstd_q", shape[:-1].numel(), f32, dev)
+        qh = _heads(q, "q", shape, dtype, dev)
+        dwq = dq_out.new_empty(D, dtype=f32)
+        wqp = dwq.data_ptr()
+    if dk_out is not None:
+        kshape = dk_out.shape
+        gk = _heads(dk_out, "dk_out", kshape, dtype, dev)
+        if dk is None:
+            dk = dk_out.new_empty(kshape)
+        ok = _heads(dk, "dk", kshape, dtype, dev)
+        if w_k is not None:
+            bp = _vector(rstd_k, "rstd_k", kshape[:-1].numel(), f32, dev)
+            kh = _heads(k, "k", kshape, dtype, dev)
+            dwk = dq_out.new_empty(D, dtype=f32)
+            wkp = dwk.data_ptr()
+    elif dk is not None:
+        raise ValueError("dk without dk_out")
+    if workspace is None and (wqp or wkp):
+        workspace = _workspace(dq_out, rmsnorm_rope_bwd_workspace_size, D)
+    args = _ROPE.pack(*head, ap, bp, 0.0, offset, magnitude, 0.0, *qh, *kh, *_NO_HEADS, *_NO_HEADS)
+    grads = _ROPE_GRADS.pack(152, 0, *gq, *gk, *oq, *ok, wqp, wkp)
+    ws_ptr = ws_bytes = 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = (_lib or lib()).rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
+                                          _opt(make_options(**options)) if options else None,
+                                          _stream_ptr(dev))
+    if rc:
+        _check(rc)
     return dq, dk, dwq, dwk
 
 
@@ -886,14 +954,13 @@ class Cache:
                                  *(() if values else (0, 0)))
 
 
-def _tokens(t, name, like, shape, dtype):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same(t, like, name, dtype)
-    st = t.stride()
-    if st[2] != 1 and shape[2] != 1:
-        raise ValueError(f"{name} must have unit stride within a head")
-    return _HEADS.pack(t.data_ptr(), 0, st[0], st[1])
+def _tokens(t, name, shape, dtype, device):
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+        st = t.stride()
+        if st[2] == 1 or shape[2] == 1:
+            return _HEADS.pack(t.data_ptr(), 0, st[0], st[1])
+    _refuse(t, name, shape, dtype, device)
+    raise ValueError(f"{name} must have unit stride within a head")
 
 
 def cache_write(cache: Cache, k, v, slots, stream=None, **options) -> None:
@@ -905,15 +972,18 @@ def cache_write(cache: Cache, k, v, slots, stream=None, **options) -> None:
     if ctx is not None:
         with ctx:
             return cache_write(cache, k, v, slots, **options)
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, head_dim]")
-    T = k.shape[0]
+    dev, dtype = cache.k_codes.get_device(), k.dtype
+    T = k.shape[0] if k.dim() == 3 else -1
     shape = (T, cache.heads, cache.head_dim)
-    kh = _tokens(k, "k", cache.k_codes, shape, k.dtype)
-    vh = None if v is None else _tokens(v, "v", cache.k_codes, shape, k.dtype)
-    sp = _vector(slots, "slots", cache.k_codes, T, torch.int64)
-    _check(rmsnorm_cache_write(cache._args, kh, vh, sp, T, _code(k.dtype),
-                               make_options(**options) if options else None, _stream_ptr()))
+    code = _code(dtype)
+    kh = _tokens(k, "k", shape, dtype, dev)
+    vh = None if v is None else _tokens(v, "v", shape, dtype, dev)
+    sp = _vector(slots, "slots", T, torch.int64, dev)
+    rc = (_lib or lib()).rmsnorm_cache_write(cache._args, kh, vh, sp, T, code,
+                                             _opt(make_options(**options)) if options else None,
+                                             _stream_ptr(dev))
+    if rc:
+        _check(rc)
 
 
 def cache_read(cache: Cache, table, cu_rows, rows: int, starts=None, dtype=None, k_out=None,
@@ -928,26 +998,33 @@ def cache_read(cache: Cache, table, cu_rows, rows: int, starts=None, dtype=None,
     rows behind cu_rows[-1] are not written. v is None in a cache without v.
     """
     import torch
-    ctx = _elsewhere(cache.k_codes, stream)
+    like = cache.k_codes
+    ctx = _elsewhere(like, stream)
     if ctx is not None:
         with ctx:
             return cache_read(cache, table, cu_rows, rows, starts, dtype, k_out, v_out, **options)
-    like = cache.k_codes
-    dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+    dev, i32 = like.get_device(), torch.int32
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else torch.bfloat16
+    code = _code(dtype)
     shape = (rows, cache.heads, cache.head_dim)
-    if table.dim() != 2 or not table.is_contiguous():
-        raise ValueError("table must be contiguous [sequences, pages per sequence]")
-    _same(table, like, "table", torch.int32)
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages per sequence]")
     n, width = table.shape
-    cp = _vector(cu_rows, "cu_rows", like, n + 1, torch.int32)
-    sp = _vector(starts, "starts", like, n, torch.int32)
+    tp = _vector(table, "table", n * width, i32, dev)
+    cp = _vector(cu_rows, "cu_rows", n + 1, i32, dev)
+    sp = _vector(starts, "starts", n, i32, dev)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=like.device)
-    if v_out is None and cache.v_codes is not None:
-        v_out = torch.empty(shape, dtype=dtype, device=like.device)
-    kh = _tokens(k_out, "k_out", like, shape, dtype)
-    vh = None if v_out is None else _tokens(v_out, "v_out", like, shape, dtype)
-    _check(rmsnorm_cache_read(cache._args, table.data_ptr(), width, cp, sp, n, rows, kh, vh,
-                              _code(dtype), make_options(**options) if options else None,
-                              _stream_ptr()))
+        k_out = like.new_empty(shape, dtype=dtype)
+    kh, vh = _tokens(k_out, "k_out", shape, dtype, dev), None
+    if cache.v_codes is not None:
+        if v_out is None:
+            v_out = like.new_empty(shape, dtype=dtype)
+    if v_out is not None:
+        vh = _tokens(v_out, "v_out", shape, dtype, dev)
+    rc = (_lib or lib()).rmsnorm_cache_read(cache._args, tp, width, cp, sp, n, rows, kh, vh, code,
+                                            _opt(make_options(**options)) if options else None,
+                                            _stream_ptr(dev))
+    if rc:
+        _check(rc)
     return k_out, v_out
