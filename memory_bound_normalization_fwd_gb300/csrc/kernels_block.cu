@@ -65,30 +65,45 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     if (t == 0) {
         for (int k = 0; k < g.stages && k < rows; ++k) issue(k, k);
     }
-    uint4 wpost[V], wpre[V], gv[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = v * g.T + t;
-        wpost[v] = wpre[v] = gv[v] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < g.nvec) {
-            if (p.w_post) wpost[v] = __ldg(static_cast<const uint4*>(p.w_post) + c);
-            if (p.w_pre) wpre[v] = __ldg(static_cast<const uint4*>(p.w_pre) + c);
-        }
-    }
+    // Per column, as pairs: alpha (offset + w_post), times the gate where it stands
+    // for several rows, and offset + w_pre.
+    constexpr int H = E / 2;
+    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+    f2 scale[V][H], wpre[V][H];
     int64_t grow = 0;
     int64_t left = 0;  // rows until the gate row changes
     if (GATE == 1) {
         grow = r0 / p.gate_rows;
         left = (grow + 1) * p.gate_rows - r0;
     }
-    auto load_gate = [&]() {
+    auto load_scale = [&]() {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * g.T + t;
-            if (c < g.nvec) gv[v] = __ldg(gate + grow * p.ldg + c);
+            const bool in = c < g.nvec;
+            if (p.w_post) {
+                weights2<DT>(in ? __ldg(static_cast<const uint4*>(p.w_post) + c) : zero4, p.offset, scale[v]);
+#pragma unroll
+                for (int e = 0; e < H; ++e) scale[v][e] = f2_mul(scale[v][e], f2_dup(p.alpha));
+            } else {
+#pragma unroll
+                for (int e = 0; e < H; ++e) scale[v][e] = f2_dup(p.alpha);
+            }
+            if (GATE == 1) {
+                f2 x[H];
+                unpack2<DT>(in ? __ldg(gate + grow * p.ldg + c) : zero4, x);
+#pragma unroll
+                for (int e = 0; e < H; ++e) scale[v][e] = f2_mul(scale[v][e], x[e]);
+            }
         }
     };
-    if (GATE == 1) load_gate();
+    load_scale();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = v * g.T + t;
+        weights2<DT>(p.w_pre && c < g.nvec ? __ldg(static_cast<const uint4*>(p.w_pre) + c) : zero4, p.offset,
+                     wpre[v]);
+    }
     __syncthreads();  // barriers and flags are set up
     pdl_launch_dependents();
 
@@ -96,17 +111,34 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     uint32_t phase = 0;
     bool dead = false;
     int row = 0;
+    const f2 beta = f2_dup(p.beta);
     for (; row < rows; ++row) {
+        if (GATE == 1) {
+            if (left == 0) {
+                ++grow;
+                left = p.gate_rows;
+                load_scale();
+            }
+            --left;
+        }
         if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
-        uint4 hv[V], rv[V];
+        f2 f[V][H];
+        uint4 rv[V], gv[V];
+        f2 sq = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * g.T + t;
-            hv[v] = rv[v] = make_uint4(0u, 0u, 0u, 0u);
+            uint4 hv = zero4;
+            rv[v] = gv[v] = zero4;
             if (c < g.nvec) {
-                hv[v] = ring.row(st, 0)[c];
+                hv = ring.row(st, 0)[c];
                 rv[v] = ring.row(st, 1)[c];
                 if (GATE == 2) gv[v] = ring.row(st, 2)[c];
+            }
+            unpack2<DT>(hv, f[v]);
+            if (p.w_post) {
+#pragma unroll
+                for (int e = 0; e < H; ++e) sq = f2_fma(f[v][e], f[v][e], sq);
             }
         }
         // Behind a row's first barrier every thread has read the stage: the
@@ -117,50 +149,31 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
         };
         float a = 1.f;
         if (p.w_post) {
-            float ss[1] = {0.f};
-#pragma unroll
-            for (int v = 0; v < V; ++v) ss[0] = sumsq_vec<DT>(hv[v], ss[0]);
-            team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+            const float ss = team_sum(f2_sum(sq), &parts[team][parity][0], team, t, g.T);
             parity ^= 1;
             behind_first_barrier();
             if (dead) break;
-            a = row_rstd(ss[0], p.n, p.eps);
+            a = row_rstd(ss, p.n, p.eps);
             if (t == 0 && p.rstd_post) p.rstd_post[r0 + row] = a;
         }
-        if (GATE == 1) {
-            if (left == 0) {
-                ++grow;
-                left = p.gate_rows;
-                load_gate();
-            }
-            --left;
-        }
-        float f[V][E];
-        float ss[1] = {0.f};
+        sq = 0;
+        const f2 a2 = f2_dup(a);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float w[E], x[E];
-            unpack_vec<DT>(hv[v], f[v]);
-            if (p.w_post) {
-                weights_vec<DT>(wpost[v], p.offset, w);
+            f2 x[H], q[H];
+            if (GATE == 2) unpack2<DT>(gv[v], q);
+            unpack2<DT>(rv[v], x);
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[v][e] = f[v][e] * a * w[e];
-            }
-            if (GATE != 0) {
-                unpack_vec<DT>(gv[v], x);
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[v][e] *= x[e];
-            }
-            unpack_vec<DT>(rv[v], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                f[v][e] = fmaf(p.beta, x[e], p.alpha * f[v][e]);
-                ss[0] = fmaf(f[v][e], f[v][e], ss[0]);
+            for (int e = 0; e < H; ++e) {
+                // the same bits whether the gate is a row's own or stands for several
+                const f2 k = GATE == 2 ? f2_mul(scale[v][e], q[e]) : scale[v][e];
+                f[v][e] = f2_fma(f2_mul(f[v][e], a2), k, f2_mul(beta, x[e]));
+                sq = f2_fma(f[v][e], f[v][e], sq);
             }
         }
-        float b = 0.f;
+        float ss = f2_sum(sq);
         if (!p.w_post) {  // then w_pre is given
-            team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+            ss = team_sum(ss, &parts[team][parity][0], team, t, g.T);
             parity ^= 1;
             behind_first_barrier();
             if (dead) break;
@@ -168,23 +181,22 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * g.T + t;
-            if (c < g.nvec) st_stream(s + row * p.lds + c, pack_vec<DT>(f[v]));
+            if (c < g.nvec) st_stream(s + row * p.lds + c, pack2<DT>(f[v]));
         }
         if (p.w_pre) {
             if (p.w_post) {
-                team_sums<1>(ss, &parts[team][parity][0], team, t, g.T);
+                ss = team_sum(ss, &parts[team][parity][0], team, t, g.T);
                 parity ^= 1;
             }
-            b = row_rstd(ss[0], p.n, p.eps);
+            const float b = row_rstd(ss, p.n, p.eps);
             if (t == 0 && p.rstd_pre) p.rstd_pre[r0 + row] = b;
+            const f2 b2 = f2_dup(b);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * g.T + t;
-                float w[E];
-                weights_vec<DT>(wpre[v], p.offset, w);
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[v][e] = f[v][e] * b * w[e];
-                if (c < g.nvec) st_stream(y + row * p.ldy + c, pack_vec<DT>(f[v]));
+                for (int e = 0; e < H; ++e) f[v][e] = f2_mul(f2_mul(f[v][e], b2), wpre[v][e]);
+                if (c < g.nvec) st_stream(y + row * p.ldy + c, pack2<DT>(f[v]));
             }
         }
         if (++st == g.stages) {

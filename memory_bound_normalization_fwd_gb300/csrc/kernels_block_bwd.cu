@@ -51,20 +51,22 @@ __device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, 
 // Vector kernel: row teams (row_ring.cuh) with the rows of h, s, dy, ds, and of
 // the gate where each row has its own, staged in shared memory.
 // GATE: 0 none, 1 one gate row for several rows, 2 a gate row per row.
-// A thread owns V vectors of columns. In registers per column: the sums over
-// rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the current row
-// t without its -e s, s and h between the two passes. With a gate row for
+// A thread owns V vectors of columns. In registers per column: the scales, the
+// sums over rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the current
+// row t without its -e s, s and h between the two passes. With a gate row for
 // several rows dw_post changes only where the gate row ends: its sums are in
 // shared memory, a thread's own. fp32 with four vectors has no registers for
-// s, h and the weights: it reads them again (HOLD false), and a stage is then
-// free one row later, behind the next row's barrier.
+// s and h: it reads them again (HOLD false), and a stage is then free one row
+// later, behind the next row's barrier. The arithmetic is on pairs (f32x2):
+// scalar code took three times the instructions and was bound by them (16384 x
+// 4096 bf16: 564 warp instructions per 8 columns of 32 lanes).
 template <int DT, int V, int GATE, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
     constexpr int E = VecElems<DT>::value;
     constexpr bool HOLD = V * E * (DT == kFP32 ? 2 : 1) <= 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RingShared sh;
-    __shared__ __align__(16) float parts[kMaxTeams][2][3 * kMaxTeamWarps];
+    __shared__ __align__(16) float parts[kMaxTeams][2][4 * kMaxTeamWarps];
 
     const int team = threadIdx.x / g.T, t = threadIdx.x - team * g.T;
     const int64_t me = static_cast<int64_t>(blockIdx.x) * g.teams + team;
@@ -84,7 +86,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
         fence_mbar_init();
         sh.dead[team] = 0;
     }
-    for (int i = t; i < 2 * 3 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
+    for (int i = t; i < 2 * 4 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
     const bool need_h = p.w_post || GATE != 0;
     // Which array of a stage each tensor is.
     int n_arrays = 0;
@@ -108,126 +110,125 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     if (t == 0) {
         for (int k = 0; k < g.stages && k < rows; ++k) issue(k, k);
     }
+    constexpr int H = E / 2;
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const uint4* w_post = static_cast<const uint4*>(p.w_post);
     const uint4* w_pre = static_cast<const uint4*>(p.w_pre);
     const uint4* gate = static_cast<const uint4*>(p.gate);
-    uint4 wpost[V], wpre[V], gv[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = v * g.T + t;
-        wpost[v] = wpre[v] = gv[v] = zero4;
-        if (HOLD && c < g.nvec) {
-            if (w_post) wpost[v] = __ldg(w_post + c);
-            if (w_pre) wpre[v] = __ldg(w_pre + c);
-        }
-    }
+    // Per column, as pairs: a = alpha gate (offset + w_post) (GATE 2: without the
+    // gate) and offset + w_pre.
+    f2 a[V][H], wpre[V][H];
     int64_t grow = 0, left = 0;
     if (GATE == 1) {
         grow = r0 / p.gate_rows;
         left = (grow + 1) * p.gate_rows - r0;
     }
-    auto load_gate = [&]() {
-        if (!HOLD) return;
+    auto column = [&](int v) { return v * g.T + t; };
+    // alpha (offset + w_post) of a vector of columns.
+    auto post_scale = [&](int v, f2* o) {
+        const int c = column(v);
+        if (w_post) {
+            weights2<DT>(c < g.nvec ? __ldg(w_post + c) : zero4, p.offset, o);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * g.T + t;
-            if (c < g.nvec) gv[v] = __ldg(gate + grow * p.ldg + c);
+            for (int e = 0; e < H; ++e) o[e] = f2_mul(o[e], f2_dup(p.alpha));
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) o[e] = f2_dup(p.alpha);
         }
     };
+    auto gate_row = [&](int v, f2* o) {
+        const int c = column(v);
+        unpack2<DT>(c < g.nvec ? __ldg(gate + grow * p.ldg + c) : zero4, o);
+    };
+    auto load_scale = [&]() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            post_scale(v, a[v]);
+            if (GATE == 1) {
+                f2 x[H];
+                gate_row(v, x);
+#pragma unroll
+                for (int e = 0; e < H; ++e) a[v][e] = f2_mul(a[v][e], x[e]);
+            }
+        }
+    };
+    load_scale();
+    f2 P[V][H], pre[V][H];  // GATE 2: P is dw_post without its alpha
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = column(v);
+        weights2<DT>(w_pre && c < g.nvec ? __ldg(w_pre + c) : zero4, p.offset, wpre[v]);
+#pragma unroll
+        for (int e = 0; e < H; ++e) P[v][e] = pre[v][e] = 0;
+    }
     if (GATE == 1) {
-        load_gate();
 #pragma unroll
         for (int i = 0; i < V * E / 4; ++i)
             post_sums[i * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float P[V][E], pre[V][E];  // GATE 2: P is dw_post
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < E; ++e) P[v][e] = pre[v][e] = 0.f;
     __syncthreads();
 
     int st = 0, parity = 0;
     uint32_t phase = 0;
     bool dead = false;
     int row = 0;
+    const f2 beta = f2_dup(p.beta);
     for (; row < rows; ++row) {
         if (GATE == 1 && left == 0) {
             ++grow;
             left = p.gate_rows;
-            load_gate();
+            load_scale();
         }
         if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
-        const float k1 = p.w_post ? __ldg(p.rstd_post + r0 + row) : 1.f;
-        const float k2 = p.w_pre ? __ldg(p.rstd_pre + r0 + row) : 0.f;
-        // The columns' alpha * gate * (offset + w_post), offset + w_pre.
-        auto gate_vec = [&](int v, int c) {
-            return GATE == 2 ? (HOLD ? gv[v] : c < g.nvec ? ring.row(st, ig)[c] : zero4)
-                   : HOLD      ? gv[v] : c < g.nvec ? __ldg(gate + grow * p.ldg + c) : zero4;
-        };
-        auto scales = [&](int v, int c, float* a) {
-            if (GATE != 0) {
-                unpack_vec<DT>(gate_vec(v, c), a);
-#pragma unroll
-                for (int e = 0; e < E; ++e) a[e] *= p.alpha;
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) a[e] = p.alpha;
-            }
-            if (w_post) {
-                float w[E];
-                weights_vec<DT>(HOLD ? wpost[v] : c < g.nvec ? __ldg(w_post + c) : zero4, p.offset, w);
-#pragma unroll
-                for (int e = 0; e < E; ++e) a[e] *= w[e];
-            }
-        };
-        uint4 hv[V], sv[V];
-        float t0[V][E];
-        float sums[3] = {0.f, 0.f, 0.f};
+        const float k1 = w_post ? __ldg(p.rstd_post + r0 + row) : 1.f;
+        const float k2 = w_pre ? __ldg(p.rstd_pre + r0 + row) : 0.f;
+        uint4 hv[V], sv[V], gv[V];
+        f2 t0[V][H];
+        f2 c0 = 0, c1 = 0, c2 = 0;
+        const f2 k22 = f2_dup(k2);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * g.T + t;
-            const bool in = c < g.nvec;
+            const int c = column(v);
             uint4 dyv = zero4, dsv = zero4;
-            hv[v] = sv[v] = zero4;
-            if (in) {
+            hv[v] = sv[v] = gv[v] = zero4;
+            if (c < g.nvec) {
                 if (need_h) hv[v] = ring.row(st, ih)[c];
-                if (p.w_pre) {
+                if (w_pre) {
                     sv[v] = ring.row(st, is)[c];
                     dyv = ring.row(st, idy)[c];
                 }
                 if (p.ds) dsv = ring.row(st, ids)[c];
-                if (GATE == 2 && HOLD) gv[v] = ring.row(st, ig)[c];
+                if (GATE == 2) gv[v] = ring.row(st, ig)[c];
             }
-            unpack_vec<DT>(dsv, t0[v]);
-            float s[E];
-            unpack_vec<DT>(sv[v], s);
-            if (p.w_pre) {
-                float dy[E], w[E];
-                unpack_vec<DT>(dyv, dy);
-                weights_vec<DT>(HOLD ? wpre[v] : in ? __ldg(w_pre + c) : zero4, p.offset, w);
+            unpack2<DT>(dsv, t0[v]);
+            f2 s[H];
+            unpack2<DT>(sv[v], s);
+            if (w_pre) {
+                f2 dy[H];
+                unpack2<DT>(dyv, dy);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float u = dy[e] * w[e];
-                    t0[v][e] = fmaf(k2, u, t0[v][e]);
-                    sums[0] = fmaf(u, s[e], sums[0]);
-                    pre[v][e] = fmaf(dy[e], s[e] * k2, pre[v][e]);
+                for (int e = 0; e < H; ++e) {
+                    const f2 u = f2_mul(dy[e], wpre[v][e]);
+                    t0[v][e] = f2_fma(k22, u, t0[v][e]);
+                    c0 = f2_fma(u, s[e], c0);
+                    pre[v][e] = f2_fma(dy[e], f2_mul(s[e], k22), pre[v][e]);
                 }
             }
             if (w_post) {
-                float a[E], h[E];
-                scales(v, c, a);
-                unpack_vec<DT>(hv[v], h);
+                f2 h[H], x[H];
+                unpack2<DT>(hv[v], h);
+                if (GATE == 2) unpack2<DT>(gv[v], x);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float ah = a[e] * h[e];
-                    sums[1] = fmaf(ah, t0[v][e], sums[1]);
-                    sums[2] = fmaf(ah, s[e], sums[2]);
+                for (int e = 0; e < H; ++e) {
+                    f2 ah = f2_mul(a[v][e], h[e]);
+                    if (GATE == 2) ah = f2_mul(ah, x[e]);
+                    c1 = f2_fma(ah, t0[v][e], c1);
+                    c2 = f2_fma(ah, s[e], c2);
                 }
             }
         }
-        team_sums<3>(sums, &parts[team][parity][0], team, t, g.T);
+        float sums[3] = {f2_sum(c0), f2_sum(c1), f2_sum(c2)};
+        team_sums3(sums, &parts[team][parity][0], team, t, g.T);
         parity ^= 1;
         dead = *(volatile unsigned int*)&sh.dead[team] != 0;
         if (dead) break;
@@ -241,41 +242,41 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
         }
         const float e2 = k2 * k2 * k2 * (sums[0] / p.n);
         const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) / p.n);
+        const f2 me2 = f2_dup(-e2), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * g.T + t;
+            const int c = column(v);
             const bool in = c < g.nvec;
-            float s[E], h[E], a[E], o[E];
-            unpack_vec<DT>(HOLD ? sv[v] : in && p.w_pre ? ring.row(st, is)[c] : zero4, s);
-            unpack_vec<DT>(HOLD ? hv[v] : in && need_h ? ring.row(st, ih)[c] : zero4, h);
-            scales(v, c, a);
+            f2 s[H], h[H], x[H], o[H];
+            unpack2<DT>(HOLD ? sv[v] : in && w_pre ? ring.row(st, is)[c] : zero4, s);
+            unpack2<DT>(HOLD ? hv[v] : in && need_h ? ring.row(st, ih)[c] : zero4, h);
+            if (GATE == 2) unpack2<DT>(HOLD ? gv[v] : in ? ring.row(st, ig)[c] : zero4, x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float tt = fmaf(-e2, s[e], t0[v][e]);
-                t0[v][e] = tt;
-                o[e] = p.beta * tt;
+            for (int e = 0; e < H; ++e) {
+                t0[v][e] = f2_fma(me2, s[e], t0[v][e]);
+                o[e] = f2_mul(beta, t0[v][e]);
             }
-            if (in) st_stream(static_cast<uint4*>(p.dr) + (r0 + row) * p.lddr + c, pack_vec<DT>(o));
+            if (in) st_stream(static_cast<uint4*>(p.dr) + (r0 + row) * p.lddr + c, pack2<DT>(o));
             if (GATE == 2) {
-                float w[E], q[E];
-                unpack_vec<DT>(gate_vec(v, c), q);
-                if (w_post)
-                    weights_vec<DT>(HOLD ? wpost[v] : in ? __ldg(w_post + c) : zero4, p.offset, w);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float gw = p.alpha * (t0[v][e] * (h[e] * k1));
-                    P[v][e] = fmaf(gw, q[e], P[v][e]);
-                    o[e] = w_post ? gw * w[e] : gw;
+                for (int e = 0; e < H; ++e) {
+                    const f2 th = f2_mul(t0[v][e], f2_mul(h[e], k12));
+                    P[v][e] = f2_fma(th, x[e], P[v][e]);
+                    o[e] = f2_mul(a[v][e], th);
                 }
-                if (in) st_stream(static_cast<uint4*>(p.dgate) + (r0 + row) * p.lddg + c, pack_vec<DT>(o));
-            } else {
+                if (in) st_stream(static_cast<uint4*>(p.dgate) + (r0 + row) * p.lddg + c, pack2<DT>(o));
+            } else if (need_h) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) P[v][e] = fmaf(t0[v][e], h[e] * k1, P[v][e]);
+                for (int e = 0; e < H; ++e) P[v][e] = f2_fma(t0[v][e], f2_mul(h[e], k12), P[v][e]);
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[e] = w_post ? fmaf(k1 * a[e], t0[v][e], -(k1 * f) * h[e]) : a[e] * t0[v][e];
-            if (in) st_stream(static_cast<uint4*>(p.dh) + (r0 + row) * p.lddh + c, pack_vec<DT>(o));
+            for (int e = 0; e < H; ++e) {
+                f2 q = f2_mul(a[v][e], k12);
+                if (GATE == 2) q = f2_mul(q, x[e]);
+                o[e] = f2_mul(q, t0[v][e]);
+                if (w_post) o[e] = f2_fma(mf, h[e], o[e]);
+            }
+            if (in) st_stream(static_cast<uint4*>(p.dh) + (r0 + row) * p.lddh + c, pack2<DT>(o));
         }
         if (GATE == 1 && (--left == 0 || row + 1 == rows)) {
             // The end of a gate row's rows here: their P into dw_post's sums, and
@@ -286,33 +287,29 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
             float* out = partial(p.ws, first > r0 ? 3 : 2, me, g.slots, block_bwd_pitch(p.N));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int c = v * g.T + t;
+                const int c = column(v);
                 const bool in = c < g.nvec;
-                float q[E], w[E], o[E];
-                unpack_vec<DT>(gate_vec(v, c), q);
-                if (w_post)
-                    weights_vec<DT>(HOLD ? wpost[v] : in ? __ldg(w_post + c) : zero4, p.offset, w);
+                f2 q[H], o[H];
+                gate_row(v, q);
+                post_scale(v, o);
 #pragma unroll
                 for (int i = 0; i < E / 4; ++i) {
+                    const f2 p0 = P[v][2 * i], p1 = P[v][2 * i + 1];
                     float4& acc = post_sums[(v * (E / 4) + i) * blockDim.x + threadIdx.x];
-                    float4 x = acc;
-                    x.x = fmaf(p.alpha * P[v][4 * i], q[4 * i], x.x);
-                    x.y = fmaf(p.alpha * P[v][4 * i + 1], q[4 * i + 1], x.y);
-                    x.z = fmaf(p.alpha * P[v][4 * i + 2], q[4 * i + 2], x.z);
-                    x.w = fmaf(p.alpha * P[v][4 * i + 3], q[4 * i + 3], x.w);
-                    acc = x;
+                    const float4 x = acc;
+                    const float2 lo = f2_get(f2_fma(p0, q[2 * i], f2_make(x.x, x.y)));
+                    const float2 hi = f2_get(f2_fma(p1, q[2 * i + 1], f2_make(x.z, x.w)));
+                    acc = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    const float2 u = f2_get(p0), w = f2_get(p1);
                     if (in && !whole)
-                        reinterpret_cast<float4*>(out)[c * (E / 4) + i] =
-                            make_float4(P[v][4 * i], P[v][4 * i + 1], P[v][4 * i + 2], P[v][4 * i + 3]);
+                        reinterpret_cast<float4*>(out)[c * (E / 4) + i] = make_float4(u.x, u.y, w.x, w.y);
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    o[e] = p.alpha * P[v][e];
-                    if (w_post) o[e] *= w[e];
-                    P[v][e] = 0.f;
+                for (int e = 0; e < H; ++e) {
+                    o[e] = f2_mul(o[e], P[v][e]);
+                    P[v][e] = 0;
                 }
-                if (in && whole)
-                    static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack_vec<DT>(o);
+                if (in && whole) static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack2<DT>(o);
             }
         }
         if (++st == g.stages) {
@@ -342,14 +339,12 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
         __syncthreads();  // the rings, or the sums of the round before, are done with
 #pragma unroll
         for (int i = 0; i < V * E / 4; ++i) {
-            float4 x;
-            if (which == 0 && GATE == 1) {
-                x = post_sums[i * blockDim.x + threadIdx.x];
-            } else {
-                const float* q = (which == 0 ? &P[0][0] : &pre[0][0]) + 4 * i;
-                const float k = which == 0 && GATE == 0 ? p.alpha : 1.f;
-                x = make_float4(k * q[0], k * q[1], k * q[2], k * q[3]);
-            }
+            const int v = i / (E / 4), e = 2 * (i % (E / 4));
+            const float2 lo = f2_get(which == 0 ? P[v][e] : pre[v][e]);
+            const float2 hi = f2_get(which == 0 ? P[v][e + 1] : pre[v][e + 1]);
+            float4 x = make_float4(lo.x, lo.y, hi.x, hi.y);
+            if (which == 0 && GATE == 1) x = post_sums[i * blockDim.x + threadIdx.x];
+            if (which == 0) x = make_float4(p.alpha * x.x, p.alpha * x.y, p.alpha * x.z, p.alpha * x.w);
             if (g.teams > 1) all[i * blockDim.x + threadIdx.x] = x;
             else {
                 const int c = (i / (E / 4)) * g.T + t;

@@ -45,33 +45,49 @@ __device__ __forceinline__ void ring_barrier(int team, int T) {
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(T) : "memory");
 }
 
-// Sums over a team in a fixed order; `part` is [K][kMaxTeamWarps] floats of this
-// call's parity, zero behind the team's warps. One team barrier.
-template <int K>
-__device__ __forceinline__ void team_sums(float (&v)[K], float* part, int team, int t, int T) {
+// Sums over a team in a fixed order, one team barrier. `part` is [4][kMaxTeamWarps]
+// floats of this call's parity ([1][..] for one sum), zero behind the team's warps.
+// One sum: a butterfly over the warp, then over the warps' sums, which every warp
+// reads with one load.
+__device__ __forceinline__ float team_sum(float v, float* part, int team, int t, int T) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-    }
-    if (T > 32 && (t & 31) == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) part[k * kMaxTeamWarps + (t >> 5)] = v[k];
-    }
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (T > 32 && (t & 31) == 0) part[t >> 5] = v;
     ring_barrier(team, T);
     if (T > 32) {
-        const int n4 = (T + 127) >> 7;
+        v = part[t & 15];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float4* q = reinterpret_cast<const float4*>(part + k * kMaxTeamWarps);
-            float s = 0.f;
-            for (int i = 0; i < n4; ++i) {
-                const float4 x = q[i];
-                s += (x.x + x.y) + (x.z + x.w);
-            }
-            v[k] = s;
-        }
+        for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     }
+    return v;
+}
+
+// Three sums at once: the first two steps of the butterfly also hand out which
+// sum a lane goes on with (lanes 0-7 the first, 8-15 the second, 16-23 the
+// third), so six shuffles do what fifteen would; the same across the warps.
+__device__ __forceinline__ void team_sums3(float (&v)[3], float* part, int team, int t, int T) {
+    const int lane = t & 31;
+    const bool up = lane & 16, up8 = lane & 8;
+    float a = up ? v[2] : v[0], b = up ? 0.f : v[1];
+    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xffffffffu, up ? v[1] : 0.f, 16);
+    float k = up8 ? b : a;
+    k += __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
+    k += __shfl_xor_sync(0xffffffffu, k, 4);
+    k += __shfl_xor_sync(0xffffffffu, k, 2);
+    k += __shfl_xor_sync(0xffffffffu, k, 1);
+    if (T > 32 && (lane & 7) == 0) part[(lane >> 3) * kMaxTeamWarps + (t >> 5)] = k;
+    ring_barrier(team, T);
+    if (T > 32) {
+        const float* q = part + (lane >> 3) * kMaxTeamWarps + (lane & 7);
+        k = q[0] + q[8];
+        k += __shfl_xor_sync(0xffffffffu, k, 4);
+        k += __shfl_xor_sync(0xffffffffu, k, 2);
+        k += __shfl_xor_sync(0xffffffffu, k, 1);
+    }
+    v[0] = __shfl_sync(0xffffffffu, k, 0);
+    v[1] = __shfl_sync(0xffffffffu, k, 8);
+    v[2] = __shfl_sync(0xffffffffu, k, 16);
 }
 
 // A team's ring: the leader's issue side and everybody's wait side.
