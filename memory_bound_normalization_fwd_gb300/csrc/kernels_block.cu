@@ -25,9 +25,12 @@ namespace {
 // in registers between the reductions: h is read once, s once made.
 // GATE: 0 none, 1 one gate row for several rows (kept in registers, read again
 // where the gate row changes), 2 a gate row per row (staged like h and r).
-template <int DT, int V, int GATE, int MAXT>
+// FULL: both norms are there and a row is exactly V vectors of every thread, which
+// the compiler then knows: no test of either is left in the loop.
+template <int DT, int V, int GATE, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, const RingShape g) {
     constexpr int E = VecElems<DT>::value;
+    const bool post = FULL || p.w_post, pre = FULL || p.w_pre;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RingShared sh;
     __shared__ __align__(16) float parts[kMaxTeams][2][kMaxTeamWarps];
@@ -39,9 +42,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     Ring ring;
     ring.row_bytes = static_cast<uint32_t>(g.nvec) * 16u;
     ring.stage_bytes = ring.row_bytes * g.arrays;
-    ring.stages = g.stages;
-    ring.mem = smem + static_cast<size_t>(team) * g.stages * ring.stage_bytes;
-    ring.base = smem_u32(ring.mem);
+    ring.base = smem_u32(smem) + static_cast<uint32_t>(team * g.stages) * ring.stage_bytes;
     ring.bars = smem_u32(&sh.bars[team][0]);
     if (t == 0) {
         for (int st = 0; st < g.stages; ++st) mbar_init(ring.bar(st), 1);
@@ -53,8 +54,8 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     const uint4* h = static_cast<const uint4*>(p.h) + r0 * p.ldh;
     const uint4* r = static_cast<const uint4*>(p.r) + r0 * p.ldr;
     const uint4* gate = static_cast<const uint4*>(p.gate);
-    uint4* s = static_cast<uint4*>(p.s) + r0 * p.lds;
-    uint4* y = static_cast<uint4*>(p.y) + r0 * p.ldy;
+    uint4* s = static_cast<uint4*>(p.s) + r0 * p.lds + t;
+    uint4* y = static_cast<uint4*>(p.y) + r0 * p.ldy + t;
     auto issue = [&](int row, int st) {
         ring.expect(st);
         ring.copy(st, 0, h + row * p.ldh);
@@ -112,7 +113,11 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     bool dead = false;
     int row = 0;
     const f2 beta = f2_dup(p.beta);
-    for (; row < rows; ++row) {
+    // Vectors of the row; those past its end stay zero.
+    uint4 hv[V], rv[V], gv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) hv[v] = rv[v] = gv[v] = zero4;
+    for (; row < rows; ++row, s += p.lds, y += p.ldy) {
         if (GATE == 1) {
             if (left == 0) {
                 ++grow;
@@ -123,20 +128,18 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
         }
         if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
         f2 f[V][H];
-        uint4 rv[V], gv[V];
         f2 sq = 0;
+        const uint32_t at = ring.stage(st) + 16u * t;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * g.T + t;
-            uint4 hv = zero4;
-            rv[v] = gv[v] = zero4;
-            if (c < g.nvec) {
-                hv = ring.row(st, 0)[c];
-                rv[v] = ring.row(st, 1)[c];
-                if (GATE == 2) gv[v] = ring.row(st, 2)[c];
+            if (FULL || v * g.T + t < g.nvec) {
+                const uint32_t q = at + 16u * (v * g.T);
+                hv[v] = lds16(q);
+                rv[v] = lds16(q + ring.row_bytes);
+                if (GATE == 2) gv[v] = lds16(q + 2 * ring.row_bytes);
             }
-            unpack2<DT>(hv, f[v]);
-            if (p.w_post) {
+            unpack2<DT>(hv[v], f[v]);
+            if (post) {
 #pragma unroll
                 for (int e = 0; e < H; ++e) sq = f2_fma(f[v][e], f[v][e], sq);
             }
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
             if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
         };
         float a = 1.f;
-        if (p.w_post) {
+        if (post) {
             const float ss = team_sum(f2_sum(sq), &parts[team][parity][0], team, t, g.T);
             parity ^= 1;
             behind_first_barrier();
@@ -172,19 +175,17 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
             }
         }
         float ss = f2_sum(sq);
-        if (!p.w_post) {  // then w_pre is given
+        if (!post) {  // then w_pre is given
             ss = team_sum(ss, &parts[team][parity][0], team, t, g.T);
             parity ^= 1;
             behind_first_barrier();
             if (dead) break;
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * g.T + t;
-            if (c < g.nvec) st_stream(s + row * p.lds + c, pack2<DT>(f[v]));
-        }
-        if (p.w_pre) {
-            if (p.w_post) {
+        for (int v = 0; v < V; ++v)
+            if (FULL || v * g.T + t < g.nvec) st_stream(s + v * g.T, pack2<DT>(f[v]));
+        if (pre) {
+            if (post) {
                 ss = team_sum(ss, &parts[team][parity][0], team, t, g.T);
                 parity ^= 1;
             }
@@ -193,10 +194,9 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
             const f2 b2 = f2_dup(b);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int c = v * g.T + t;
 #pragma unroll
                 for (int e = 0; e < H; ++e) f[v][e] = f2_mul(f2_mul(f[v][e], b2), wpre[v][e]);
-                if (c < g.nvec) st_stream(y + row * p.ldy + c, pack2<DT>(f[v]));
+                if (FULL || v * g.T + t < g.nvec) st_stream(y + v * g.T, pack2<DT>(f[v]));
             }
         }
         if (++st == g.stages) {
@@ -229,10 +229,18 @@ cudaError_t launch_ring(BlockP p, const OpCfg& c, bool* taken) {
     if (V == 0) return cudaSuccess;
     const int T = static_cast<int>((nvec + V * 32 - 1) / (V * 32)) * 32;
     const bool wide = T > 256;
-    const Fn fn = V == 1   ? block_fwd_ring_kernel<DT, 1, GATE, 256>
-                  : V == 2 ? (wide ? block_fwd_ring_kernel<DT, 2, GATE, 512>
-                                   : block_fwd_ring_kernel<DT, 2, GATE, 256>)
-                           : block_fwd_ring_kernel<DT, 4, GATE, 512>;
+    const bool full = p.w_post && p.w_pre && nvec == static_cast<int64_t>(V) * T;
+    Fn fn = nullptr;
+    if (full)
+        fn = V == 1   ? block_fwd_ring_kernel<DT, 1, GATE, 256, true>
+             : V == 2 ? (wide ? block_fwd_ring_kernel<DT, 2, GATE, 512, true>
+                              : block_fwd_ring_kernel<DT, 2, GATE, 256, true>)
+                      : block_fwd_ring_kernel<DT, 4, GATE, 512, true>;
+    else
+        fn = V == 1   ? block_fwd_ring_kernel<DT, 1, GATE, 256, false>
+             : V == 2 ? (wide ? block_fwd_ring_kernel<DT, 2, GATE, 512, false>
+                              : block_fwd_ring_kernel<DT, 2, GATE, 256, false>)
+                      : block_fwd_ring_kernel<DT, 4, GATE, 512, false>;
     if (!ring_plan(reinterpret_cast<const void*>(fn), c, p.M, static_cast<int>(nvec), T, wide ? 512 : 256,
                    GATE == 2 ? 3 : 2, 0, &plan))
         return cudaSuccess;

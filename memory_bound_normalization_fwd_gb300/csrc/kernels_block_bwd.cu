@@ -60,9 +60,12 @@ __device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, 
 // later, behind the next row's barrier. The arithmetic is on pairs (f32x2):
 // scalar code took three times the instructions and was bound by them (16384 x
 // 4096 bf16: 564 warp instructions per 8 columns of 32 lanes).
-template <int DT, int V, int GATE, int MAXT>
+// FULL: both norms and ds are there and a row is exactly V vectors of every
+// thread, which the compiler then knows: no test of them is left in the loop.
+template <int DT, int V, int GATE, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
     constexpr int E = VecElems<DT>::value;
+    const bool post = FULL || p.w_post, prenorm = FULL || p.w_pre, has_ds = FULL || p.ds;
     constexpr bool HOLD = V * E * (DT == kFP32 ? 2 : 1) <= 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RingShared sh;
@@ -75,9 +78,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     Ring ring;
     ring.row_bytes = static_cast<uint32_t>(g.nvec) * 16u;
     ring.stage_bytes = ring.row_bytes * g.arrays;
-    ring.stages = g.stages;
-    ring.mem = smem + static_cast<size_t>(team) * g.stages * ring.stage_bytes;
-    ring.base = smem_u32(ring.mem);
+    ring.base = smem_u32(smem) + static_cast<uint32_t>(team * g.stages) * ring.stage_bytes;
     ring.bars = smem_u32(&sh.bars[team][0]);
     // dw_post sums of GATE 1, [V * E / 4][threads] float4 behind the rings.
     float4* post_sums = reinterpret_cast<float4*>(smem + g.sums_at);
@@ -87,23 +88,23 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
         sh.dead[team] = 0;
     }
     for (int i = t; i < 2 * 4 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
-    const bool need_h = p.w_post || GATE != 0;
+    const bool need_h = post || GATE != 0;
     // Which array of a stage each tensor is.
     int n_arrays = 0;
     const int ih = need_h ? n_arrays++ : 0;
-    const int is = p.w_pre ? n_arrays++ : 0;
-    const int idy = p.w_pre ? n_arrays++ : 0;
-    const int ids = p.ds ? n_arrays++ : 0;
+    const int is = prenorm ? n_arrays++ : 0;
+    const int idy = prenorm ? n_arrays++ : 0;
+    const int ids = has_ds ? n_arrays++ : 0;
     const int ig = n_arrays;
     auto issue = [&](int row, int st) {
         const int64_t i = r0 + row;
         ring.expect(st);
         if (need_h) ring.copy(st, ih, static_cast<const uint4*>(p.h) + i * p.ldh);
-        if (p.w_pre) {
+        if (prenorm) {
             ring.copy(st, is, static_cast<const uint4*>(p.s) + i * p.lds);
             ring.copy(st, idy, static_cast<const uint4*>(p.dy) + i * p.lddy);
         }
-        if (p.ds) ring.copy(st, ids, static_cast<const uint4*>(p.ds) + i * p.ldds);
+        if (has_ds) ring.copy(st, ids, static_cast<const uint4*>(p.ds) + i * p.ldds);
         if (GATE == 2) ring.copy(st, ig, static_cast<const uint4*>(p.gate) + i * p.ldg);
     };
     pdl_wait();
@@ -173,39 +174,55 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     bool dead = false;
     int row = 0;
     const f2 beta = f2_dup(p.beta);
-    for (; row < rows; ++row) {
+    const float inv_n = 1.f / p.n;
+    const float* rstd_post = p.rstd_post + r0;
+    const float* rstd_pre = p.rstd_pre + r0;
+    float k1_next = post ? __ldg(rstd_post) : 1.f;
+    float k2_next = prenorm ? __ldg(rstd_pre) : 0.f;
+    uint4* dr = static_cast<uint4*>(p.dr) + r0 * p.lddr + t;
+    uint4* dh = static_cast<uint4*>(p.dh) + r0 * p.lddh + t;
+    uint4* dgate = static_cast<uint4*>(p.dgate) + (GATE == 2 ? r0 * p.lddg + t : 0);
+    // Vectors of the row; those past its end stay zero.
+    uint4 hv[V], sv[V], gv[V], dyv[V], dsv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) hv[v] = sv[v] = gv[v] = dyv[v] = dsv[v] = zero4;
+    const uint32_t oh = 16u * t + ih * ring.row_bytes, os = 16u * t + is * ring.row_bytes;
+    const uint32_t ody = 16u * t + idy * ring.row_bytes, ods = 16u * t + ids * ring.row_bytes;
+    const uint32_t og = 16u * t + ig * ring.row_bytes;
+    for (; row < rows; ++row, dr += p.lddr, dh += p.lddh) {
         if (GATE == 1 && left == 0) {
             ++grow;
             left = p.gate_rows;
             load_scale();
         }
         if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
-        const float k1 = w_post ? __ldg(p.rstd_post + r0 + row) : 1.f;
-        const float k2 = w_pre ? __ldg(p.rstd_pre + r0 + row) : 0.f;
-        uint4 hv[V], sv[V], gv[V];
+        const float k1 = k1_next, k2 = k2_next;
+        if (row + 1 < rows) {  // the next row's, a global load ahead of its use
+            if (post) k1_next = __ldg(rstd_post + row + 1);
+            if (prenorm) k2_next = __ldg(rstd_pre + row + 1);
+        }
         f2 t0[V][H];
         f2 c0 = 0, c1 = 0, c2 = 0;
         const f2 k22 = f2_dup(k2);
+        const uint32_t at = ring.stage(st);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = column(v);
-            uint4 dyv = zero4, dsv = zero4;
-            hv[v] = sv[v] = gv[v] = zero4;
-            if (c < g.nvec) {
-                if (need_h) hv[v] = ring.row(st, ih)[c];
-                if (w_pre) {
-                    sv[v] = ring.row(st, is)[c];
-                    dyv = ring.row(st, idy)[c];
+            if (FULL || column(v) < g.nvec) {
+                const uint32_t q = at + 16u * (v * g.T);
+                if (need_h) hv[v] = lds16(q + oh);
+                if (prenorm) {
+                    sv[v] = lds16(q + os);
+                    dyv[v] = lds16(q + ody);
                 }
-                if (p.ds) dsv = ring.row(st, ids)[c];
-                if (GATE == 2) gv[v] = ring.row(st, ig)[c];
+                if (has_ds) dsv[v] = lds16(q + ods);
+                if (GATE == 2) gv[v] = lds16(q + og);
             }
-            unpack2<DT>(dsv, t0[v]);
+            unpack2<DT>(dsv[v], t0[v]);
             f2 s[H];
             unpack2<DT>(sv[v], s);
-            if (w_pre) {
+            if (prenorm) {
                 f2 dy[H];
-                unpack2<DT>(dyv, dy);
+                unpack2<DT>(dyv[v], dy);
 #pragma unroll
                 for (int e = 0; e < H; ++e) {
                     const f2 u = f2_mul(dy[e], wpre[v][e]);
@@ -214,7 +231,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                     pre[v][e] = f2_fma(dy[e], f2_mul(s[e], k22), pre[v][e]);
                 }
             }
-            if (w_post) {
+            if (post) {
                 f2 h[H], x[H];
                 unpack2<DT>(hv[v], h);
                 if (GATE == 2) unpack2<DT>(gv[v], x);
@@ -240,23 +257,28 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 issue(row - 1 + g.stages, st == 0 ? g.stages - 1 : st - 1);
             }
         }
-        const float e2 = k2 * k2 * k2 * (sums[0] / p.n);
-        const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) / p.n);
+        const float e2 = k2 * k2 * k2 * (sums[0] * inv_n);
+        const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) * inv_n);
         const f2 me2 = f2_dup(-e2), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = column(v);
-            const bool in = c < g.nvec;
+            const bool in = FULL || column(v) < g.nvec;
             f2 s[H], h[H], x[H], o[H];
-            unpack2<DT>(HOLD ? sv[v] : in && w_pre ? ring.row(st, is)[c] : zero4, s);
-            unpack2<DT>(HOLD ? hv[v] : in && need_h ? ring.row(st, ih)[c] : zero4, h);
-            if (GATE == 2) unpack2<DT>(HOLD ? gv[v] : in ? ring.row(st, ig)[c] : zero4, x);
+            if (!HOLD && in) {
+                const uint32_t q = at + 16u * (v * g.T);
+                if (need_h) hv[v] = lds16(q + oh);
+                if (prenorm) sv[v] = lds16(q + os);
+                if (GATE == 2) gv[v] = lds16(q + og);
+            }
+            unpack2<DT>(sv[v], s);
+            unpack2<DT>(hv[v], h);
+            if (GATE == 2) unpack2<DT>(gv[v], x);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
                 t0[v][e] = f2_fma(me2, s[e], t0[v][e]);
                 o[e] = f2_mul(beta, t0[v][e]);
             }
-            if (in) st_stream(static_cast<uint4*>(p.dr) + (r0 + row) * p.lddr + c, pack2<DT>(o));
+            if (in) st_stream(dr + v * g.T, pack2<DT>(o));
             if (GATE == 2) {
 #pragma unroll
                 for (int e = 0; e < H; ++e) {
@@ -264,7 +286,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                     P[v][e] = f2_fma(th, x[e], P[v][e]);
                     o[e] = f2_mul(a[v][e], th);
                 }
-                if (in) st_stream(static_cast<uint4*>(p.dgate) + (r0 + row) * p.lddg + c, pack2<DT>(o));
+                if (in) st_stream(dgate + v * g.T, pack2<DT>(o));
             } else if (need_h) {
 #pragma unroll
                 for (int e = 0; e < H; ++e) P[v][e] = f2_fma(t0[v][e], f2_mul(h[e], k12), P[v][e]);
@@ -274,10 +296,11 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 f2 q = f2_mul(a[v][e], k12);
                 if (GATE == 2) q = f2_mul(q, x[e]);
                 o[e] = f2_mul(q, t0[v][e]);
-                if (w_post) o[e] = f2_fma(mf, h[e], o[e]);
+                if (post) o[e] = f2_fma(mf, h[e], o[e]);
             }
-            if (in) st_stream(static_cast<uint4*>(p.dh) + (r0 + row) * p.lddh + c, pack2<DT>(o));
+            if (in) st_stream(dh + v * g.T, pack2<DT>(o));
         }
+        if (GATE == 2) dgate += p.lddg;
         if (GATE == 1 && (--left == 0 || row + 1 == rows)) {
             // The end of a gate row's rows here: their P into dw_post's sums, and
             // out as dgate where they are all of the gate row's rows.
@@ -309,7 +332,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                     o[e] = f2_mul(o[e], P[v][e]);
                     P[v][e] = 0;
                 }
-                if (in && whole) static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack2<DT>(o);
+                if (in && whole)
+                    static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack2<DT>(o);
             }
         }
         if (++st == g.stages) {
@@ -560,7 +584,11 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
     const int V = nvec <= 512 * V1 ? V1 : nvec <= 1024 * V1 ? 2 * V1 : 0;
     if (V == 0) return cudaSuccess;
     const int T = static_cast<int>((nvec + V * 32 - 1) / (V * 32)) * 32;
-    const Fn fn = V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512> : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512>;
+    const bool full = in.w_post && in.w_pre && in.ds && nvec == static_cast<int64_t>(V) * T;
+    const Fn fn = full ? (V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512, true>
+                                  : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512, true>)
+                       : (V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512, false>
+                                  : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512, false>);
     const int arrays = (in.w_post || GATE ? 1 : 0) + (in.w_pre ? 2 : 0) + (in.ds ? 1 : 0) + (GATE == 2 ? 1 : 0);
     OpCfg cc = c;
     const int64_t slots = block_bwd_max_grid(in.M, in.N, c.dev.sm_count);
