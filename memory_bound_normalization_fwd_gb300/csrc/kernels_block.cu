@@ -129,14 +129,14 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
         if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
         f2 f[V][H];
         f2 sq = 0;
-        const uint32_t at = ring.stage(st) + 16u * t;
+        const unsigned char* at = smem + (ring.stage(st) - smem_u32(smem)) + 16u * t;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (FULL || v * g.T + t < g.nvec) {
-                const uint32_t q = at + 16u * (v * g.T);
-                hv[v] = lds16(q);
-                rv[v] = lds16(q + ring.row_bytes);
-                if (GATE == 2) gv[v] = lds16(q + 2 * ring.row_bytes);
+                const unsigned char* q = at + 16u * (v * g.T);
+                hv[v] = *reinterpret_cast<const uint4*>(q);
+                rv[v] = *reinterpret_cast<const uint4*>(q + ring.row_bytes);
+                if (GATE == 2) gv[v] = *reinterpret_cast<const uint4*>(q + 2 * ring.row_bytes);
             }
             unpack2<DT>(hv[v], f[v]);
             if (post) {
@@ -241,8 +241,11 @@ cudaError_t launch_ring(BlockP p, const OpCfg& c, bool* taken) {
              : V == 2 ? (wide ? block_fwd_ring_kernel<DT, 2, GATE, 512, false>
                               : block_fwd_ring_kernel<DT, 2, GATE, 256, false>)
                       : block_fwd_ring_kernel<DT, 4, GATE, 512, false>;
+    // 64 KB of stages per SM carry the reads; more make reads and writes fight
+    // (GB300, us: 16384x4096 bf16 at 64 / 96 / 128 / 192 KB 86 / 97 / 97 / 97,
+    // 16384x8192 164 / 178 / 184 / 184, 65536x512 at 48 / 72 / 96 KB 52 / 46 / 46).
     if (!ring_plan(reinterpret_cast<const void*>(fn), c, p.M, static_cast<int>(nvec), T, wide ? 512 : 256,
-                   GATE == 2 ? 3 : 2, 0, &plan))
+                   GATE == 2 ? 3 : 2, 0, 64 << 10, &plan))
         return cudaSuccess;
     p.ldh /= E;
     p.ldr /= E;

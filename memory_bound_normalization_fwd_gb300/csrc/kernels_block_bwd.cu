@@ -590,11 +590,13 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
                        : (V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512, false>
                                   : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512, false>);
     const int arrays = (in.w_post || GATE ? 1 : 0) + (in.w_pre ? 2 : 0) + (in.ds ? 1 : 0) + (GATE == 2 ? 1 : 0);
-    OpCfg cc = c;
     const int64_t slots = block_bwd_max_grid(in.M, in.N, c.dev.sm_count);
     RingPlan plan;
     const int extra = GATE == 1 ? V * E * 4 : 0;
-    if (!ring_plan(reinterpret_cast<const void*>(fn), cc, in.M, static_cast<int>(nvec), T, 512, arrays, extra, &plan))
+    // 128 KB of stages per SM (GB300, us: 16384x4096 bf16 at 64 / 96 / 128 / 192
+    // KB 147 / 130 / 129 / 132, 65536x512 91 / 87 / 88 / 88).
+    if (!ring_plan(reinterpret_cast<const void*>(fn), c, in.M, static_cast<int>(nvec), T, 512, arrays, extra,
+                   128 << 10, &plan))
         return cudaSuccess;
     // The teams' sums meet in the rings' memory: with a row per team it may be
     // smaller than they are.

@@ -12,6 +12,9 @@
 #include "ops_common.cuh"
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace rmsn {
 namespace {
@@ -43,9 +46,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 //
 // The cos and sin of a token serve all of its heads, so a CTA takes whole tokens
 // of one tensor (a tile), makes their tables in shared memory once, and walks the
-// tile's heads. The first heads' loads are issued before the tables are made.
+// tile's heads, whose vectors it copies into shared memory a few steps ahead.
 // Bound by HBM: one read and one write of every head (backward with the norm:
 // two reads).
+//
+// Tables: cos and sin of pair i of a tile's token at [token][0][i] and [token][1][i].
+// The arithmetic is on pairs of values (f32x2).
 struct RopeTile {
     int L;           // lanes per head
     int log2L;
@@ -54,6 +60,7 @@ struct RopeTile {
     int tokens[2];   // tokens per tile, q and k
     int64_t tiles[2];
     int64_t ctas[2]; // CTAs of q, of k
+    float inv_d;     // 1 / head_dim
 };
 
 // The two vectors of lane l: a in [0, nv), b in [0, nv) or past it (none).
@@ -67,41 +74,48 @@ __device__ __forceinline__ void lane_vectors(const RopeTile& g, bool interleaved
     }
 }
 
-// Turns the values of a lane by sign * angle. tab: cos and sin of the token's
-// pairs (float2 per pair).
-template <int DT, bool INTER>
-__device__ __forceinline__ void turn_lane(const RopeTile& g, const float2* tab, int l, float sign, float* x,
-                                          float* z, int R) {
-    constexpr int E = VecElems<DT>::value;
+// Turns a lane's values by SIGN * angle, on tables `cs` (cos) and `sn` (sin) of the
+// token. Half layout: x and z hold the first and the second values of the same
+// pairs. Interleaved: a pair is one f2 of x or z.
+template <int DT, bool INTER, int SIGN>
+__device__ __forceinline__ void turn_lane(const RopeTile& g, const float* cs, const float* sn, int l, f2* x, f2* z,
+                                          int R) {
+    constexpr int E = VecElems<DT>::value, H = E / 2;
     if (!INTER) {
         if (l < g.pairs) {
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float4 c = *reinterpret_cast<const float4*>(tab + l * E + e);
-                const float s0 = sign * c.y, s1 = sign * c.w;
-                const float a0 = x[e], a1 = x[e + 1], b0 = z[e], b1 = z[e + 1];
-                x[e] = fmaf(a0, c.x, -b0 * s0);
-                z[e] = fmaf(b0, c.x, a0 * s0);
-                x[e + 1] = fmaf(a1, c.z, -b1 * s1);
-                z[e + 1] = fmaf(b1, c.z, a1 * s1);
+            for (int i = 0; i < H; i += 2) {
+                const float4 c4 = *reinterpret_cast<const float4*>(cs + l * E + 2 * i);
+                const float4 s4 = *reinterpret_cast<const float4*>(sn + l * E + 2 * i);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f2 c = k == 0 ? f2_make(c4.x, c4.y) : f2_make(c4.z, c4.w);
+                    const float s0 = k == 0 ? s4.x : s4.z, s1 = k == 0 ? s4.y : s4.w;
+                    const f2 ps = f2_make(s0, s1), ns = f2_make(-s0, -s1);
+                    const f2 a = x[i + k], b = z[i + k];
+                    x[i + k] = f2_fma(b, SIGN > 0 ? ns : ps, f2_mul(a, c));
+                    z[i + k] = f2_fma(a, SIGN > 0 ? ps : ns, f2_mul(b, c));
+                }
             }
         }
     } else {
-        // pairs of vector 2l: (2l E / 2) + i; of vector 2l + 1: E / 2 further
+        // pairs of vector 2l: l E + i; of vector 2l + 1: E / 2 further
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float* y = k == 0 ? x : z;
-            if ((2 * l + k) * E < R) {
-                const float2* q = tab + (2 * l + k) * (E / 2);
+            f2* y = k == 0 ? x : z;
+            const int first = (2 * l + k) * H;
+            if (first < R / 2) {  // the rotated part may end inside the vector
 #pragma unroll
-                for (int i = 0; i < E / 2; i += 2) {
-                    const float4 c = *reinterpret_cast<const float4*>(q + i);
-                    const float s0 = sign * c.y, s1 = sign * c.w;
-                    const float a0 = y[2 * i], b0 = y[2 * i + 1], a1 = y[2 * i + 2], b1 = y[2 * i + 3];
-                    y[2 * i] = fmaf(a0, c.x, -b0 * s0);
-                    y[2 * i + 1] = fmaf(b0, c.x, a0 * s0);
-                    y[2 * i + 2] = fmaf(a1, c.z, -b1 * s1);
-                    y[2 * i + 3] = fmaf(b1, c.z, a1 * s1);
+                for (int i = 0; i < H; i += 2) {
+                    const float2 c2 = *reinterpret_cast<const float2*>(cs + first + i);
+                    const float2 s2 = *reinterpret_cast<const float2*>(sn + first + i);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (first + i + q >= R / 2) continue;
+                        const float c = q == 0 ? c2.x : c2.y, s = SIGN * (q == 0 ? s2.x : s2.y);
+                        const float2 v = f2_get(y[i + q]);
+                        y[i + q] = f2_make(fmaf(v.x, c, -v.y * s), fmaf(v.y, c, v.x * s));
+                    }
                 }
             }
         }
@@ -113,103 +127,96 @@ __device__ __forceinline__ float lanes_sum(float v, int L) {
     return v;
 }
 
-// Forward over tiles. UNROLL heads of a thread are in flight at once.
-template <int DT, bool INTER, bool NORM, int UNROLL>
-__global__ void __launch_bounds__(256) rope_fwd_tile_kernel(const RopeP p, const RopeTile g) {
-    constexpr int E = VecElems<DT>::value;
-    extern __shared__ __align__(16) float2 table[];
-    const int which = blockIdx.x >= g.ctas[0];
-    const RopeSeg& sg = p.seg[which];
+// cos and sin of the tile's tokens into shared memory, `pad` entries of each per
+// token (those past the rotated part are read with whole vectors, not used).
+__device__ __forceinline__ void make_tables(const RopeP& p, int64_t tok0, int n, int pad, float* table) {
     const int half = p.R / 2;
-    const int l = threadIdx.x & (g.L - 1);
-    const int team = threadIdx.x >> g.log2L, teams = 256 >> g.log2L;
-    int va, vb;
-    lane_vectors(g, INTER, l, va, vb);
-    const bool has_a = va < g.nv, has_b = vb < g.nv;
-    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-    pdl_wait();
-    pdl_launch_dependents();
-    float wa[E], wb[E];
-    if (NORM && sg.w) {
-        const uint4* w = static_cast<const uint4*>(sg.w);
-        weights_vec<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
-        weights_vec<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
-    }
-    const int64_t tokens = p.batch * p.seq;
-    const int64_t cta = blockIdx.x - (which ? g.ctas[0] : 0);
-    for (int64_t tile = cta; tile < g.tiles[which]; tile += g.ctas[which]) {
-        const int64_t tok0 = tile * g.tokens[which];
-        const int n = static_cast<int>(min(static_cast<int64_t>(g.tokens[which]), tokens - tok0));
-        const int units = n * sg.heads;
-        uint4 xa[UNROLL], xb[UNROLL];
-        int64_t out_at[UNROLL], head_at[UNROLL];
-        int tok[UNROLL];
-        auto fetch = [&](int u0) {
-#pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                const int u = u0 + k * teams;
-                xa[k] = xb[k] = zero4;
-                if (u < units) {
-                    const int tk = u / sg.heads, h = u - tk * sg.heads;
-                    const int64_t tkn = tok0 + tk;
-                    const int64_t b = p.batch == 1 ? 0 : tkn / p.seq, s = tkn - b * p.seq;
-                    const uint4* x = static_cast<const uint4*>(sg.in.p) + b * sg.in.sb + s * sg.in.st + h * sg.in.sh;
-                    if (has_a) xa[k] = ld_stream(x + va);
-                    if (has_b) xb[k] = ld_stream(x + vb);
-                    out_at[k] = b * sg.out.sb + s * sg.out.st + h * sg.out.sh;
-                    head_at[k] = tkn * sg.heads + h;
-                    tok[k] = tk;
-                }
-            }
-        };
-        fetch(team);
-        for (int i = threadIdx.x; i < n * half; i += 256) {
-            const int tk = i / half, j = i - tk * half;
+    for (int i = threadIdx.x; i < n * pad; i += 256) {
+        const int tk = i / pad, j = i - tk * pad;
+        float2 cs = make_float2(0.f, 0.f);
+        if (j < half) {
             const int64_t tkn = tok0 + tk;
             const int64_t b = p.batch == 1 ? 0 : tkn / p.seq;
-            table[i] = turn(position_of(p, b, tkn - b * p.seq), __ldg(p.steps + j), p.magnitude);
+            cs = turn(position_of(p, b, tkn - b * p.seq), __ldg(p.steps + j), p.magnitude);
         }
-        __syncthreads();
-        for (int u0 = team; u0 - team < units; u0 += UNROLL * teams) {
-            if (u0 != team) fetch(u0);
-#pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                float x[E], z[E];
-                unpack_vec<DT>(xa[k], x);
-                unpack_vec<DT>(xb[k], z);
-                if (NORM && sg.w) {
-                    float ss = sumsq_vec<DT>(xb[k], sumsq_vec<DT>(xa[k], 0.f));
-                    ss = lanes_sum(ss, g.L);
-                    const float r = row_rstd(ss, static_cast<float>(p.D), p.eps);
-                    if (l == 0 && sg.rstd && u0 + k * teams < units) sg.rstd[head_at[k]] = r;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        x[e] = x[e] * r * wa[e];
-                        z[e] = z[e] * r * wb[e];
-                    }
-                }
-                if (u0 + k * teams < units) {
-                    turn_lane<DT, INTER>(g, table + tok[k] * half, l, 1.f, x, z, p.R);
-                    uint4* y = static_cast<uint4*>(sg.out.p) + out_at[k];
-                    if (has_a) st_stream(y + va, pack_vec<DT>(x));
-                    if (has_b) st_stream(y + vb, pack_vec<DT>(z));
-                }
-            }
-        }
-        __syncthreads();  // the tables are read before the next tile's are made
+        table[2 * tk * pad + j] = cs.x;
+        table[(2 * tk + 1) * pad + j] = cs.y;
     }
 }
 
-// Backward over tiles: turned back, then the norm's backward, with the weights'
-// gradients of a lane's columns summed in registers over all the heads it sees,
-// and over the CTA's teams (in order) into one partial row.
-template <int DT, bool INTER, bool NORM, int UNROLL>
-__global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const RopeTile g) {
-    constexpr int E = VecElems<DT>::value;
-    extern __shared__ __align__(16) float2 table[];
+// Asynchronous copies into shared memory that the copying thread alone reads
+// back (cp.async: any stride, no registers, no barrier).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A team's way through the CTA's tiles: in step s of a tile it takes unit
+// s * teams + team (unit = token of the tile * heads + head), without divisions.
+struct Walk {
+    int64_t tile, tok0;
+    int n;          // tokens of the tile; 0: past the last tile
+    int step, steps;
+    int tok, h;     // this step's token of the tile and head; none where tok >= n
+
+    __device__ __forceinline__ void enter(const RopeTile& g, int which, int64_t tokens, int team, int teams,
+                                          int heads) {
+        tok0 = tile * g.tokens[which];
+        n = tile < g.tiles[which] ? static_cast<int>(min(static_cast<int64_t>(g.tokens[which]), tokens - tok0)) : 0;
+        steps = (n * heads + teams - 1) / teams;
+        step = 0;
+        tok = 0;
+        h = team;
+        while (h >= heads) {
+            h -= heads;
+            ++tok;
+        }
+    }
+    __device__ __forceinline__ void advance(const RopeTile& g, int which, int64_t tokens, int team, int teams,
+                                            int heads) {
+        if (++step == steps) {
+            tile += g.ctas[which];
+            enter(g, which, tokens, team, teams, heads);
+            return;
+        }
+        h += teams;
+        while (h >= heads) {
+            h -= heads;
+            ++tok;
+        }
+    }
+    __device__ __forceinline__ bool live() const { return tok < n; }
+    // Offset of the step's head.
+    __device__ __forceinline__ int64_t at(const RopeP& p, const HeadsP& x) const {
+        const int64_t tkn = tok0 + tok;
+        if (p.batch == 1) return tkn * x.st + h * x.sh;
+        const int64_t b = tkn / p.seq;
+        return b * x.sb + (tkn - b * p.seq) * x.st + h * x.sh;
+    }
+};
+
+constexpr int kSteps = 3;  // steps of a thread's copies in flight
+
+// Shared memory of a CTA: the tables, then [kSteps][vectors][256] 16-byte slots and
+// (backward with the norm) [kSteps][256] floats.
+__host__ __device__ constexpr int tile_slots(int vectors) { return kSteps * vectors * 256 * 16; }
+
+// Forward over tiles.
+template <int DT, bool INTER, bool NORM>
+__global__ void __launch_bounds__(256) rope_fwd_tile_kernel(const RopeP p, const RopeTile g, int pad, int table_bytes) {
+    constexpr int E = VecElems<DT>::value, H = E / 2;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* table = reinterpret_cast<float*>(smem);
     const int which = blockIdx.x >= g.ctas[0];
     const RopeSeg& sg = p.seg[which];
-    const int half = p.R / 2;
+    const int heads = sg.heads;
     const int l = threadIdx.x & (g.L - 1);
     const int team = threadIdx.x >> g.log2L, teams = 256 >> g.log2L;
     int va, vb;
@@ -217,122 +224,223 @@ __global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const
     const bool has_a = va < g.nv, has_b = vb < g.nv;
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const bool norm = NORM && sg.w;
+    const int64_t tokens = p.batch * p.seq;
+    const uint4* in = static_cast<const uint4*>(sg.in.p) + va;
+    uint4* out = static_cast<uint4*>(sg.out.p) + va;
+    const int vd = vb - va;
+    unsigned char* slots = smem + table_bytes + threadIdx.x * 16;
+    for (int k = 0; k < 2 * kSteps; ++k) *reinterpret_cast<uint4*>(slots + k * 4096) = zero4;
+    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+    Walk ahead;
+    ahead.tile = blockIdx.x - (which ? g.ctas[0] : 0);
+    ahead.enter(g, which, tokens, team, teams, heads);
+    Walk at = ahead;
+    int put = 0, take = 0;
+    auto fetch = [&]() {
+        if (ahead.n > 0) {
+            if (ahead.live()) {
+                const uint4* x = in + ahead.at(p, sg.in);
+                if (has_a) copy16(slot0 + (2 * put) * 4096, x);
+                if (has_b) copy16(slot0 + (2 * put + 1) * 4096, x + vd);
+            }
+            ahead.advance(g, which, tokens, team, teams, heads);
+        }
+        copies_commit();
+        put = put + 1 == kSteps ? 0 : put + 1;
+    };
     pdl_wait();
-    float wa[E], wb[E], da[E], db[E];
+    pdl_launch_dependents();
 #pragma unroll
-    for (int e = 0; e < E; ++e) da[e] = db[e] = 0.f;
+    for (int k = 0; k < kSteps; ++k) fetch();
+    f2 wa[H], wb[H];
     if (norm) {
         const uint4* w = static_cast<const uint4*>(sg.w);
-        weights_vec<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
-        weights_vec<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
+        weights2<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
+        weights2<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
     }
-    const float inv_d = 1.f / static_cast<float>(p.D);
+    while (at.n > 0) {
+        if (at.step == 0) {  // a new tile
+            __syncthreads();  // the tables of the tile before are read
+            make_tables(p, at.tok0, at.n, pad, table);
+            __syncthreads();
+        }
+        copies_wait<kSteps - 1>();
+        f2 x[H], z[H];
+        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (2 * take) * 4096), x);
+        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (2 * take + 1) * 4096), z);
+        take = take + 1 == kSteps ? 0 : take + 1;
+        fetch();
+        const bool live = at.live();
+        if (norm) {
+            f2 sq = 0;
+#pragma unroll
+            for (int e = 0; e < H; ++e) sq = f2_fma(x[e], x[e], sq);
+#pragma unroll
+            for (int e = 0; e < H; ++e) sq = f2_fma(z[e], z[e], sq);
+            const float ss = lanes_sum(f2_sum(sq), g.L);
+            const float r = rsqrtf(fmaf(ss, g.inv_d, p.eps));
+            if (l == 0 && sg.rstd && live) sg.rstd[(at.tok0 + at.tok) * heads + at.h] = r;
+            const f2 r2 = f2_dup(r);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                x[e] = f2_mul(f2_mul(x[e], r2), wa[e]);
+                z[e] = f2_mul(f2_mul(z[e], r2), wb[e]);
+            }
+        }
+        if (live) {
+            const float* cs = table + 2 * at.tok * pad;
+            turn_lane<DT, INTER, 1>(g, cs, cs + pad, l, x, z, p.R);
+            uint4* y = out + at.at(p, sg.out);
+            if (has_a) st_stream(y, pack2<DT>(x));
+            if (has_b) st_stream(y + vd, pack2<DT>(z));
+        }
+        at.advance(g, which, tokens, team, teams, heads);
+    }
+    copies_wait<0>();
+}
+
+// Backward over tiles: turned back, then the norm's backward, with the weights'
+// gradients of a lane's columns summed in registers over all the heads it sees,
+// and over the CTA's teams (in order) into one partial row.
+template <int DT, bool INTER, bool NORM>
+__global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const RopeTile g, int pad, int table_bytes) {
+    constexpr int E = VecElems<DT>::value, H = E / 2, NV = NORM ? 4 : 2;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* table = reinterpret_cast<float*>(smem);
+    const int which = blockIdx.x >= g.ctas[0];
+    const RopeSeg& sg = p.seg[which];
+    const int heads = sg.heads;
+    const int l = threadIdx.x & (g.L - 1);
+    const int team = threadIdx.x >> g.log2L, teams = 256 >> g.log2L;
+    int va, vb;
+    lane_vectors(g, INTER, l, va, vb);
+    const bool has_a = va < g.nv, has_b = vb < g.nv;
+    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+    const bool norm = NORM && sg.w;
     const int64_t tokens = p.batch * p.seq;
+    const uint4* in = static_cast<const uint4*>(sg.in.p) + va;
+    const uint4* xin = static_cast<const uint4*>(sg.x.p) + va;
+    uint4* out = static_cast<uint4*>(sg.out.p) + va;
+    const int vd = vb - va;
+    unsigned char* slots = smem + table_bytes + threadIdx.x * 16;
+    for (int k = 0; k < NV * kSteps; ++k) *reinterpret_cast<uint4*>(slots + k * 4096) = zero4;
+    float* rs = reinterpret_cast<float*>(smem + table_bytes + tile_slots(NV)) + threadIdx.x;
+    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+    const uint32_t rs0 = static_cast<uint32_t>(__cvta_generic_to_shared(rs));
     const int64_t cta = blockIdx.x - (which ? g.ctas[0] : 0);
-    for (int64_t tile = cta; tile < g.tiles[which]; tile += g.ctas[which]) {
-        const int64_t tok0 = tile * g.tokens[which];
-        const int n = static_cast<int>(min(static_cast<int64_t>(g.tokens[which]), tokens - tok0));
-        const int units = n * sg.heads;
-        uint4 ga[UNROLL], gb[UNROLL], xa[UNROLL], xb[UNROLL];
-        float rs[UNROLL];
-        int64_t out_at[UNROLL];
-        int tok[UNROLL];
-        auto fetch = [&](int u0) {
-#pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                const int u = u0 + k * teams;
-                ga[k] = gb[k] = xa[k] = xb[k] = zero4;
-                rs[k] = 0.f;
-                tok[k] = 0;
-                if (u < units) {
-                    const int tk = u / sg.heads, h = u - tk * sg.heads;
-                    const int64_t tkn = tok0 + tk;
-                    const int64_t b = p.batch == 1 ? 0 : tkn / p.seq, s = tkn - b * p.seq;
-                    const uint4* d = static_cast<const uint4*>(sg.in.p) + b * sg.in.sb + s * sg.in.st + h * sg.in.sh;
-                    if (has_a) ga[k] = ld_stream(d + va);
-                    if (has_b) gb[k] = ld_stream(d + vb);
-                    if (norm) {
-                        const uint4* x = static_cast<const uint4*>(sg.x.p) + b * sg.x.sb + s * sg.x.st + h * sg.x.sh;
-                        if (has_a) xa[k] = ld_stream(x + va);
-                        if (has_b) xb[k] = ld_stream(x + vb);
-                        rs[k] = __ldg(sg.rstd + tkn * sg.heads + h);
-                    }
-                    out_at[k] = b * sg.out.sb + s * sg.out.st + h * sg.out.sh;
-                    tok[k] = tk;
-                }
-            }
-        };
-        fetch(team);
-        for (int i = threadIdx.x; i < n * half; i += 256) {
-            const int tk = i / half, j = i - tk * half;
-            const int64_t tkn = tok0 + tk;
-            const int64_t b = p.batch == 1 ? 0 : tkn / p.seq;
-            table[i] = turn(position_of(p, b, tkn - b * p.seq), __ldg(p.steps + j), p.magnitude);
-        }
-        __syncthreads();
-        for (int u0 = team; u0 - team < units; u0 += UNROLL * teams) {
-            if (u0 != team) fetch(u0);
-#pragma unroll
-            for (int k = 0; k < UNROLL; ++k) {
-                float ta[E], tb[E];
-                unpack_vec<DT>(ga[k], ta);
-                unpack_vec<DT>(gb[k], tb);
-                turn_lane<DT, INTER>(g, table + tok[k] * half, l, -1.f, ta, tb, p.R);
+    Walk ahead;
+    ahead.tile = cta;
+    ahead.enter(g, which, tokens, team, teams, heads);
+    Walk at = ahead;
+    int put = 0, take = 0;
+    auto fetch = [&]() {
+        if (ahead.n > 0) {
+            if (ahead.live()) {
+                const uint4* d = in + ahead.at(p, sg.in);
+                if (has_a) copy16(slot0 + (NV * put) * 4096, d);
+                if (has_b) copy16(slot0 + (NV * put + 1) * 4096, d + vd);
                 if (norm) {
-                    float x[E], z[E], c = 0.f;
-                    unpack_vec<DT>(xa[k], x);
-                    unpack_vec<DT>(xb[k], z);
-                    const float r = rs[k];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float gx = ta[e] * x[e], gz = tb[e] * z[e];
-                        da[e] = fmaf(gx, r, da[e]);
-                        db[e] = fmaf(gz, r, db[e]);
-                        c = fmaf(gx, wa[e], c);
-                        c = fmaf(gz, wb[e], c);
-                    }
-                    c = lanes_sum(c, g.L);
-                    const float f = r * r * r * (c * inv_d);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        ta[e] = fmaf(r * ta[e], wa[e], -f * x[e]);
-                        tb[e] = fmaf(r * tb[e], wb[e], -f * z[e]);
-                    }
-                }
-                if (u0 + k * teams < units) {
-                    uint4* y = static_cast<uint4*>(sg.out.p) + out_at[k];
-                    if (has_a) st_stream(y + va, pack_vec<DT>(ta));
-                    if (has_b) st_stream(y + vb, pack_vec<DT>(tb));
+                    const uint4* x = xin + ahead.at(p, sg.x);
+                    if (has_a) copy16(slot0 + (NV * put + 2) * 4096, x);
+                    if (has_b) copy16(slot0 + (NV * put + 3) * 4096, x + vd);
+                    copy4(rs0 + put * 1024, sg.rstd + (ahead.tok0 + ahead.tok) * heads + ahead.h);
                 }
             }
+            ahead.advance(g, which, tokens, team, teams, heads);
         }
-        __syncthreads();  // the tables are read before the next tile's are made
+        copies_commit();
+        put = put + 1 == kSteps ? 0 : put + 1;
+    };
+    pdl_wait();
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) fetch();
+    f2 wa[H], wb[H], da[H], db[H];
+#pragma unroll
+    for (int e = 0; e < H; ++e) da[e] = db[e] = 0;
+    if (norm) {
+        const uint4* w = static_cast<const uint4*>(sg.w);
+        weights2<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
+        weights2<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
     }
+    while (at.n > 0) {
+        if (at.step == 0) {  // a new tile
+            __syncthreads();  // the tables of the tile before are read
+            make_tables(p, at.tok0, at.n, pad, table);
+            __syncthreads();
+        }
+        copies_wait<kSteps - 1>();
+        f2 ta[H], tb[H];
+        uint4 xa = zero4, xb = zero4;
+        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (NV * take) * 4096), ta);
+        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (NV * take + 1) * 4096), tb);
+        float r = 0.f;
+        if (norm) {
+            xa = *reinterpret_cast<const uint4*>(slots + (NV * take + 2) * 4096);
+            xb = *reinterpret_cast<const uint4*>(slots + (NV * take + 3) * 4096);
+            r = rs[take * 256];
+        }
+        take = take + 1 == kSteps ? 0 : take + 1;
+        fetch();
+        const bool live = at.live();
+        const float* cs = table + 2 * (live ? at.tok : 0) * pad;
+        turn_lane<DT, INTER, -1>(g, cs, cs + pad, l, ta, tb, p.R);
+        if (norm) {
+            f2 x[H], z[H], c2 = 0;
+            unpack2<DT>(xa, x);
+            unpack2<DT>(xb, z);
+            const f2 r2 = f2_dup(r);
+            if (live) {  // past the tile's last unit a slot holds an older one's values
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const f2 gx = f2_mul(ta[e], x[e]), gz = f2_mul(tb[e], z[e]);
+                    da[e] = f2_fma(gx, r2, da[e]);
+                    db[e] = f2_fma(gz, r2, db[e]);
+                    c2 = f2_fma(gx, wa[e], c2);
+                    c2 = f2_fma(gz, wb[e], c2);
+                }
+            }
+            const float c = lanes_sum(f2_sum(c2), g.L);
+            const f2 mf = f2_dup(-(r * r * r * (c * g.inv_d)));
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
+                tb[e] = f2_fma(f2_mul(tb[e], r2), wb[e], f2_mul(z[e], mf));
+            }
+        }
+        if (live) {
+            uint4* y = out + at.at(p, sg.out);
+            if (has_a) st_stream(y, pack2<DT>(ta));
+            if (has_b) st_stream(y + vd, pack2<DT>(tb));
+        }
+        at.advance(g, which, tokens, team, teams, heads);
+    }
+    copies_wait<0>();
     pdl_launch_dependents();
     if (!norm) return;
     // A warp's teams meet by shuffles, the warps in order in shared memory:
     // [8 warps][L lanes][2E].
-    float* part = reinterpret_cast<float*>(table);
-    for (int off = g.L; off < 32; off <<= 1) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            da[e] += __shfl_xor_sync(0xffffffffu, da[e], off);
-            db[e] += __shfl_xor_sync(0xffffffffu, db[e], off);
-        }
-    }
+    __syncthreads();  // the tables are read
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane < g.L) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            part[(w * g.L + lane) * 2 * E + e] = da[e];
-            part[(w * g.L + lane) * 2 * E + E + e] = db[e];
+    for (int e = 0; e < H; ++e) {
+        float2 a = f2_get(da[e]), b = f2_get(db[e]);
+        for (int off = g.L; off < 32; off <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, off);
+            a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
+            b.x += __shfl_xor_sync(0xffffffffu, b.x, off);
+            b.y += __shfl_xor_sync(0xffffffffu, b.y, off);
+        }
+        if (lane < g.L) {
+            float2* part = reinterpret_cast<float2*>(table) + (w * g.L + lane) * E;
+            part[e] = a;
+            part[H + e] = b;
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < g.L * 2 * E; i += 256) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t += part[k * g.L * 2 * E + i];
+        for (int k = 0; k < 8; ++k) t += table[k * g.L * 2 * E + i];
         int a, b;
         lane_vectors(g, INTER, i / (2 * E), a, b);
         const int e = i % (2 * E);
@@ -515,13 +623,16 @@ int64_t generic_grid(const RopeP& p, const OpCfg& c) {
     return persistent_grid(units, 8, c.dev.sm_count, kGenericCtasPerSM, c.max_ctas);
 }
 
+// Table entries per token: the rotated pairs, up to whole vectors.
+int table_pad(const RopeP& p) { return (p.R / 2 + 3) / 4 * 4; }
+
 // Whether every head is whole 16-byte vectors that the tile kernels can pair up,
 // and how: lanes per head, tokens per tile, CTAs.
 bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* g) {
     const int E = vec_elems(p.dtype);
     if (p.D % E != 0 || p.D > 64 * E) return false;
-    // Half layout: both halves whole vectors; interleaved: the rotated part is.
-    if (p.R % (p.interleaved ? E : 2 * E) != 0) return false;
+    // Half layout: both halves whole vectors. Interleaved: any even rotary_dim.
+    if (!p.interleaved && p.R % (2 * E) != 0) return false;
     for (int k = 0; k < 2; ++k) {
         const RopeSeg& s = p.seg[k];
         if (s.heads == 0) continue;
@@ -535,6 +646,7 @@ bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* 
         if (!aligned16(s.w)) return false;
     }
     g->nv = p.D / E;
+    g->inv_d = 1.f / static_cast<float>(p.D);
     g->pairs = p.interleaved ? 0 : p.R / (2 * E);
     g->L = 1;
     g->log2L = 0;
@@ -550,11 +662,11 @@ bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* 
         g->tokens[k] = 1;
         g->tiles[k] = 0;
         if (heads == 0) continue;
-        // A tile fills the CTA's teams about twice, as far as the tokens reach
+        // A tile is about four steps of the CTA's teams, as far as the tokens reach
         // every SM and their tables 16 KB.
-        int64_t n = std::max<int64_t>(1, 2 * teams / heads);
-        n = std::min<int64_t>(n, std::max<int64_t>(1, tokens * 2 / c.dev.sm_count));
-        n = std::min<int64_t>(n, std::max<int64_t>(1, 2048 / (p.R / 2)));
+        int64_t n = std::max<int64_t>(1, 4 * teams / heads);
+        n = std::min<int64_t>(n, std::max<int64_t>(1, tokens / (2 * c.dev.sm_count)));
+        n = std::min<int64_t>(n, std::max<int64_t>(1, 2048 / table_pad(p)));
         g->tokens[k] = static_cast<int>(n);
         g->tiles[k] = (tokens + n - 1) / n;
         work[k] = heads;
@@ -567,18 +679,39 @@ bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* 
     return true;
 }
 
+// Shared memory a tile kernel is given for its tables: 16 KB, one token's where
+// that is more.
+int table_bytes(const RopeP& p) { return std::max(16384, table_pad(p) * 8); }
+
+// Opts a kernel into `smem` bytes on the current device, once; the CTAs per SM.
+int tile_occupancy(const void* fn, int smem) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, int> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    {
+        std::lock_guard<std::mutex> guard(mu);
+        int& have = done[{dev, fn}];
+        if (have < smem) {
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+            have = smem;
+        }
+    }
+    return occupancy(fn, 256, smem);
+}
+
 template <int DT, bool INTER, bool NORM>
 cudaError_t fwd_tiles(RopeP p, const OpCfg& c, bool* taken) {
-    auto fn = rope_fwd_tile_kernel<DT, INTER, NORM, 2>;
+    auto fn = rope_fwd_tile_kernel<DT, INTER, NORM>;
     RopeTile g;
-    const int occ = std::max(1, occupancy(reinterpret_cast<const void*>(fn), 256, 16384));
-    *taken = tiles(p, c, false, occ, &g);
+    const int tb = table_bytes(p), smem = tb + tile_slots(2);
+    const int occ = tile_occupancy(reinterpret_cast<const void*>(fn), smem);
+    *taken = occ > 0 && tiles(p, c, false, occ, &g);
     if (!*taken) return cudaSuccess;
     constexpr int E = VecElems<DT>::value;
     for (RopeSeg& s : p.seg)
         for (HeadsP* h : {&s.in, &s.out}) h->sb /= E, h->st /= E, h->sh /= E;
-    const int smem = std::max(g.tokens[0], g.tokens[1]) * (p.R / 2) * 8;
-    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g);
+    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g, table_pad(p), tb);
 }
 
 cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t rows_k, int paired) {
@@ -592,17 +725,17 @@ cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t ro
 
 template <int DT, bool INTER, bool NORM>
 cudaError_t bwd_tiles(RopeP p, const OpCfg& c, bool* taken) {
-    auto fn = rope_bwd_tile_kernel<DT, INTER, NORM, 2>;
+    auto fn = rope_bwd_tile_kernel<DT, INTER, NORM>;
     RopeTile g;
-    const int occ = std::min(8, std::max(1, occupancy(reinterpret_cast<const void*>(fn), 256, 16384)));
-    *taken = tiles(p, c, true, occ, &g);
-    if (!*taken) return cudaSuccess;
     constexpr int E = VecElems<DT>::value;
+    // The sums of the weights' gradients meet where the tables were (16 KB at most).
+    const int tb = table_bytes(p), smem = tb + tile_slots(NORM ? 4 : 2) + (NORM ? kSteps * 1024 : 0);
+    const int occ = tile_occupancy(reinterpret_cast<const void*>(fn), smem);
+    *taken = occ > 0 && tiles(p, c, true, std::min(8, occ), &g);
+    if (!*taken) return cudaSuccess;
     for (RopeSeg& s : p.seg)
         for (HeadsP* h : {&s.in, &s.out, &s.x}) h->sb /= E, h->st /= E, h->sh /= E;
-    const int smem = std::max(std::max(g.tokens[0], g.tokens[1]) * (p.R / 2) * 8,
-                              NORM ? 8 * g.L * 2 * E * 4 : 0);
-    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g);
+    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g, table_pad(p), tb);
     return e != cudaSuccess || !NORM ? e : launch_dw(p, c, g.ctas[0], g.ctas[1], 0);
 }
 

@@ -40,7 +40,7 @@ Facts facts(const void* fn, int threads, int max_optin) {
 }  // namespace
 
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, RingPlan* out) {
+               int extra, int in_flight, RingPlan* out) {
     if (T > max_threads) return false;
     int teams = std::min(max_threads / T, kMaxTeams);
     // Few rows: one team per CTA spreads them over more SMs.
@@ -54,9 +54,12 @@ bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int m
     for (; ctas >= 1; --ctas) {
         const int64_t room = per_sm / ctas - 1024 - f.static_smem - static_cast<int64_t>(extra) * teams * T;
         stages = static_cast<int>(std::min<int64_t>(room / stage, kMaxRing));
-        if (stages >= 3 || (ctas == 1 && stages >= 2)) break;
+        if (stages >= 2) break;
     }
     if (ctas < 1) return false;
+    // More stages than carry the bandwidth cost it (see the callers' figures).
+    const int64_t enough = (in_flight + ctas * stage / 2) / (ctas * stage);
+    stages = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(stages, enough)));
     const int64_t want = (M + teams - 1) / teams;
     int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas;
     if (c.max_ctas > 0) cap = std::min<int64_t>(cap, c.max_ctas);

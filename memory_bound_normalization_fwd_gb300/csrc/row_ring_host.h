@@ -15,9 +15,10 @@ struct RingPlan {
 
 // Lays out `arrays` rows of `nvec` vectors per stage for teams of T threads in
 // CTAs of up to `max_threads`, with `extra` more bytes of shared memory per
-// CTA thread. False where a row does not fit two stages of shared memory.
+// CTA thread and about `in_flight` bytes of stages per SM. False where a row
+// does not fit two stages of shared memory.
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, RingPlan* out);
+               int extra, int in_flight, RingPlan* out);
 
 // Reads a status word of the current device and clears it.
 template <typename S>

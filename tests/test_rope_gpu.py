@@ -201,6 +201,19 @@ def test_heads_before_tokens_and_shifted_addresses():
         _check_bwd(d, got[2:], res, D, False, 0.0, 1.0, where=f"heads first {shift}")
 
 
+@pytest.mark.parametrize("D,R,inter", [(128, 64, False), (80, 20, True), (80, 20, False), (64, 6, True), (33, 2, True)])
+def test_values_behind_the_rotated_part_stay_whatever_they_are(D, R, inter):
+    d = _make((11,), 3, 1, D, R, "bf16", 22, norm=False)
+    d["q"][..., R::2] = float("inf")
+    d["q"][..., R + 1::4] = float("nan")
+    for variant in ("auto", "generic"):
+        out = B.rope_fwd(d["q"], d["k"], d["steps"], d["positions"], interleaved=inter, variant=variant)
+        assert torch.equal(torch.nan_to_num(out[0][..., R:], nan=7.0), torch.nan_to_num(d["q"][..., R:], nan=7.0))
+        assert bool(torch.isfinite(out[0][..., :R].float()).all())
+        back = B.rope_bwd(d["q"], d["k"], d["steps"], d["positions"], interleaved=inter, variant=variant)
+        assert torch.equal(torch.nan_to_num(back[0][..., R:], nan=7.0), torch.nan_to_num(d["q"][..., R:], nan=7.0))
+
+
 def test_turning_back_undoes_the_turn():
     d = _make((33,), 4, 4, 64, 64, "fp32", 16, norm=False)
     out = B.rope_fwd(d["q"], d["k"], d["steps"], d["positions"])
