@@ -12,19 +12,24 @@
 #include "ops_common.cuh"
 
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <utility>
 
 namespace rmsn {
 namespace {
 
-// cos and sin (times magnitude) of pair i at a position.
+// cos and sin (times magnitude) of pair i at a position. Outputs of 16 bits take
+// the hardware's approximations, whose error of 2^-21 is 2^-10 of those types'
+// half steps; fp32 takes sincospif.
+template <int DT>
 __device__ __forceinline__ float2 turn(int64_t position, uint64_t step, float magnitude) {
     const uint64_t phase = static_cast<uint64_t>(position) * step;
     const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
     float s, c;
-    sincospif(x, &s, &c);
+    if constexpr (DT == kFP32) {
+        sincospif(x, &s, &c);
+    } else {
+        s = __sinf(x * 3.14159265358979f);
+        c = __cosf(x * 3.14159265358979f);
+    }
     return make_float2(c * magnitude, s * magnitude);
 }
 
@@ -38,388 +43,359 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Vector kernels. A head is nv = head_dim / E vectors of 16 bytes; a lane takes two
-// of them, so that both values of every pair are in one thread: vectors i and
-// i + R/(2E) of the rotated part in the half layout, 2i and 2i + 1 when interleaved
-// and behind R. L lanes (a power of two, 1..32) make a head; the row sum of a
-// head's norm is a butterfly over them.
+// Vector kernels. A head is nv = head_dim / E vectors of 16 bytes; L lanes (a power
+// of two, 1..32: a team) make a head, two vectors each, and a row sum of the head's
+// norm is a butterfly over them. LAYOUT says which two vectors a lane takes:
+//   kHalves      i and i + R/(2E) of the rotated part, so that both values of a pair
+//                are in one thread; 2i and 2i + 1 behind it
+//   kInterleaved 2i and 2i + 1: a pair lies inside a vector
+//   kExchange    2i and 2i + 1, halves that are not whole vectors: the other value of
+//                a pair is read from a copy of the head in shared memory
 //
-// The cos and sin of a token serve all of its heads, so a CTA takes whole tokens
-// of one tensor (a tile), makes their tables in shared memory once, and walks the
-// tile's heads, whose vectors it copies into shared memory a few steps ahead.
-// Bound by HBM: one read and one write of every head (backward with the norm:
-// two reads).
-//
-// Tables: cos and sin of pair i of a tile's token at [token][0][i] and [token][1][i].
-// The arithmetic is on pairs of values (f32x2).
-struct RopeTile {
+// A unit is a token with some of its heads, and a team takes one unit after
+// another: the cos and sin of a lane's pairs depend on the token alone, so a lane
+// makes its own once per unit and keeps them in registers over the unit's heads;
+// no table, no barrier. What is left per head is two loads, the arithmetic on pairs
+// of values (f32x2) and two stores. Bound by HBM: one read and one write of every
+// head (backward with the norm: two reads).
+// (Tables of a CTA's tokens in shared memory, made once for all heads, took twice
+// the instructions per head: 16384 tokens of 40 heads of 128 bf16 with norms 90 to
+// 114 us in several forms.)
+constexpr int kHalves = 0, kInterleaved = 1, kExchange = 2;
+constexpr int kAhead = 2;  // heads of a team loaded ahead
+
+struct RopeUnits {
     int L;           // lanes per head
     int log2L;
     int nv;          // vectors per head
-    int pairs;       // vectors per half of the rotated part (half layout: R / (2E))
-    int tokens[2];   // tokens per tile, q and k
-    int64_t tiles[2];
+    int pairs;       // kHalves: vectors per half of the rotated part
+    int per[2];      // heads of a unit, q and k
+    int chunks[2];   // units of a token
+    int64_t units[2];
     int64_t ctas[2]; // CTAs of q, of k
     float inv_d;     // 1 / head_dim
 };
 
-// The two vectors of lane l: a in [0, nv), b in [0, nv) or past it (none).
-__device__ __forceinline__ void lane_vectors(const RopeTile& g, bool interleaved, int l, int& a, int& b) {
-    if (interleaved || l >= g.pairs) {
-        a = 2 * l;  // behind the rotated part 2 pairs is even, so 2l starts there
-        b = a + 1;
-    } else {
-        a = l;
-        b = l + g.pairs;
-    }
-}
+// A lane's place: its two vectors and its cos and sin.
+template <int DT, int LAYOUT>
+struct Lane {
+    static constexpr int E = VecElems<DT>::value, H = E / 2;
+    static constexpr int N = LAYOUT == kExchange ? 2 * E : E;  // cos and sin of a lane
+    int l, va, vb;
+    bool has_a, has_b;
+    f2 c[N / 2], s[N / 2];
 
-// Turns a lane's values by SIGN * angle, on tables `cs` (cos) and `sn` (sin) of the
-// token. Half layout: x and z hold the first and the second values of the same
-// pairs. Interleaved: a pair is one f2 of x or z.
-template <int DT, bool INTER, int SIGN>
-__device__ __forceinline__ void turn_lane(const RopeTile& g, const float* cs, const float* sn, int l, f2* x, f2* z,
-                                          int R) {
-    constexpr int E = VecElems<DT>::value, H = E / 2;
-    if (!INTER) {
-        if (l < g.pairs) {
+    __device__ __forceinline__ Lane(const RopeUnits& g) {
+        l = threadIdx.x & (g.L - 1);
+        if (LAYOUT != kHalves || l >= g.pairs) {
+            va = 2 * l;  // behind the rotated part 2 pairs is even, so 2l starts there
+            vb = va + 1;
+        } else {
+            va = l;
+            vb = l + g.pairs;
+        }
+        has_a = va < g.nv;
+        has_b = vb < g.nv;
 #pragma unroll
-            for (int i = 0; i < H; i += 2) {
-                const float4 c4 = *reinterpret_cast<const float4*>(cs + l * E + 2 * i);
-                const float4 s4 = *reinterpret_cast<const float4*>(sn + l * E + 2 * i);
+        for (int i = 0; i < N / 2; ++i) c[i] = s[i] = 0;  // a team without a unit turns zeros
+    }
+    // kHalves: pairs l E + i. kInterleaved: pairs of vector 2l, then of 2l + 1.
+    // kExchange: the pair of each of the lane's values.
+    __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t position) {
+        if (LAYOUT == kHalves ? l >= g.pairs : va * E >= p.R) return;
+        const int half = p.R / 2;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f2 c = k == 0 ? f2_make(c4.x, c4.y) : f2_make(c4.z, c4.w);
-                    const float s0 = k == 0 ? s4.x : s4.z, s1 = k == 0 ? s4.y : s4.w;
-                    const f2 ps = f2_make(s0, s1), ns = f2_make(-s0, -s1);
-                    const f2 a = x[i + k], b = z[i + k];
-                    x[i + k] = f2_fma(b, SIGN > 0 ? ns : ps, f2_mul(a, c));
-                    z[i + k] = f2_fma(a, SIGN > 0 ? ps : ns, f2_mul(b, c));
+        for (int i = 0; i < N; i += 2) {
+            float2 t[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                int j = l * E + i + k;
+                if (LAYOUT == kExchange) {
+                    j = 2 * l * E + i + k;
+                    if (j >= half) j -= half;
+                }
+                t[k] = make_float2(0.f, 0.f);
+                if (LAYOUT == kHalves || j < half) t[k] = turn<DT>(position, __ldg(p.steps + j), p.magnitude);
+            }
+            c[i / 2] = f2_make(t[0].x, t[1].x);
+            s[i / 2] = f2_make(t[0].y, t[1].y);
+        }
+    }
+    // The lane's values turned by SIGN times the angle; `row`: the team's room for a
+    // head in shared memory (kExchange).
+    template <int SIGN>
+    __device__ __forceinline__ void turned(const RopeP& p, const RopeUnits& g, f2* x, f2* z, float* row) const {
+        const int half = p.R / 2;
+        if (LAYOUT == kHalves) {
+            if (l >= g.pairs) return;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 sv = f2_get(s[i]), a = f2_get(x[i]), b = f2_get(z[i]);
+                const float2 ca = f2_get(f2_mul(x[i], c[i])), cb = f2_get(f2_mul(z[i], c[i]));
+                if (SIGN > 0) {
+                    x[i] = f2_make(fmaf(-b.x, sv.x, ca.x), fmaf(-b.y, sv.y, ca.y));
+                    z[i] = f2_make(fmaf(a.x, sv.x, cb.x), fmaf(a.y, sv.y, cb.y));
+                } else {
+                    x[i] = f2_make(fmaf(b.x, sv.x, ca.x), fmaf(b.y, sv.y, ca.y));
+                    z[i] = f2_make(fmaf(-a.x, sv.x, cb.x), fmaf(-a.y, sv.y, cb.y));
                 }
             }
-        }
-    } else {
-        // pairs of vector 2l: l E + i; of vector 2l + 1: E / 2 further
+        } else if (LAYOUT == kInterleaved) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            f2* y = k == 0 ? x : z;
-            const int first = (2 * l + k) * H;
-            if (first < R / 2) {  // the rotated part may end inside the vector
+            for (int k = 0; k < 2; ++k) {
+                f2* y = k == 0 ? x : z;
 #pragma unroll
-                for (int i = 0; i < H; i += 2) {
-                    const float2 c2 = *reinterpret_cast<const float2*>(cs + first + i);
-                    const float2 s2 = *reinterpret_cast<const float2*>(sn + first + i);
+                for (int i = 0; i < H; ++i) {
+                    if (2 * l * H + k * H + i >= half) continue;  // the rotated part may end in a vector
+                    const int n = k * H + i;
+                    const float2 cp = f2_get(c[n / 2]), sp = f2_get(s[n / 2]), v = f2_get(y[i]);
+                    const float cv = n & 1 ? cp.y : cp.x, sv = SIGN * (n & 1 ? sp.y : sp.x);
+                    y[i] = f2_make(fmaf(-v.y, sv, v.x * cv), fmaf(v.x, sv, v.y * cv));
+                }
+            }
+        } else {
+            __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (first + i + q >= R / 2) continue;
-                        const float c = q == 0 ? c2.x : c2.y, s = SIGN * (q == 0 ? s2.x : s2.y);
-                        const float2 v = f2_get(y[i + q]);
-                        y[i + q] = f2_make(fmaf(v.x, c, -v.y * s), fmaf(v.y, c, v.x * s));
+            for (int k = 0; k < 2; ++k) {
+                f2* y = k == 0 ? x : z;
+                if ((va + k) * E < p.R) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 v = f2_get(y[i]);
+                        *reinterpret_cast<float2*>(row + (va + k) * E + 2 * i) = v;
                     }
                 }
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                f2* y = k == 0 ? x : z;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const float2 cp = f2_get(c[k * H + i]), sp = f2_get(s[k * H + i]);
+                    float2 v = f2_get(y[i]);
+                    const int j = (va + k) * E + 2 * i;
+                    if (j < p.R) v.x = other(row, j, half, v.x, cp.x, SIGN * sp.x);
+                    if (j + 1 < p.R) v.y = other(row, j + 1, half, v.y, cp.y, SIGN * sp.y);
+                    y[i] = f2_make(v.x, v.y);
+                }
+            }
         }
     }
-}
-
-__device__ __forceinline__ float lanes_sum(float v, int L) {
-    for (int off = L >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-
-// cos and sin of the tile's tokens into shared memory, `pad` entries of each per
-// token (those past the rotated part are read with whole vectors, not used).
-__device__ __forceinline__ void make_tables(const RopeP& p, int64_t tok0, int n, int pad, float* table) {
-    const int half = p.R / 2;
-    for (int i = threadIdx.x; i < n * pad; i += 256) {
-        const int tk = i / pad, j = i - tk * pad;
-        float2 cs = make_float2(0.f, 0.f);
-        if (j < half) {
-            const int64_t tkn = tok0 + tk;
-            const int64_t b = p.batch == 1 ? 0 : tkn / p.seq;
-            cs = turn(position_of(p, b, tkn - b * p.seq), __ldg(p.steps + j), p.magnitude);
-        }
-        table[2 * tk * pad + j] = cs.x;
-        table[(2 * tk + 1) * pad + j] = cs.y;
-    }
-}
-
-// Asynchronous copies into shared memory that the copying thread alone reads
-// back (cp.async: any stride, no registers, no barrier).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// A team's way through the CTA's tiles: in step s of a tile it takes unit
-// s * teams + team (unit = token of the tile * heads + head), without divisions.
-struct Walk {
-    int64_t tile, tok0;
-    int n;          // tokens of the tile; 0: past the last tile
-    int step, steps;
-    int tok, h;     // this step's token of the tile and head; none where tok >= n
-
-    __device__ __forceinline__ void enter(const RopeTile& g, int which, int64_t tokens, int team, int teams,
-                                          int heads) {
-        tok0 = tile * g.tokens[which];
-        n = tile < g.tiles[which] ? static_cast<int>(min(static_cast<int64_t>(g.tokens[which]), tokens - tok0)) : 0;
-        steps = (n * heads + teams - 1) / teams;
-        step = 0;
-        tok = 0;
-        h = team;
-        while (h >= heads) {
-            h -= heads;
-            ++tok;
-        }
-    }
-    __device__ __forceinline__ void advance(const RopeTile& g, int which, int64_t tokens, int team, int teams,
-                                            int heads) {
-        if (++step == steps) {
-            tile += g.ctas[which];
-            enter(g, which, tokens, team, teams, heads);
-            return;
-        }
-        h += teams;
-        while (h >= heads) {
-            h -= heads;
-            ++tok;
-        }
-    }
-    __device__ __forceinline__ bool live() const { return tok < n; }
-    // Offset of the step's head.
-    __device__ __forceinline__ int64_t at(const RopeP& p, const HeadsP& x) const {
-        const int64_t tkn = tok0 + tok;
-        if (p.batch == 1) return tkn * x.st + h * x.sh;
-        const int64_t b = tkn / p.seq;
-        return b * x.sb + (tkn - b * p.seq) * x.st + h * x.sh;
+    __device__ __forceinline__ static float other(const float* row, int j, int half, float v, float c, float s) {
+        return j < half ? fmaf(-row[j + half], s, v * c) : fmaf(row[j - half], s, v * c);
     }
 };
 
-constexpr int kSteps = 3;  // steps of a thread's copies in flight
+__device__ __forceinline__ float lanes_sum(float v, int L) {
+    if (L > 8) {
+        if (L > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+    }
+    if (L > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+    if (L > 2) v += __shfl_xor_sync(0xffffffffu, v, 2);
+    if (L > 1) v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v;
+}
 
-// Shared memory of a CTA: the tables, then [kSteps][vectors][256] 16-byte slots and
-// (backward with the norm) [kSteps][256] floats.
-__host__ __device__ constexpr int tile_slots(int vectors) { return kSteps * vectors * 256 * 16; }
+// A unit: its token and heads.
+struct Unit {
+    int64_t b, s, token;
+    int h, n;  // first head, heads (0: no unit)
+    __device__ __forceinline__ Unit(const RopeP& p, const RopeUnits& g, int which, int heads, int64_t u) {
+        const int chunks = g.chunks[which];
+        int chunk;
+        if (g.units[which] < (int64_t(1) << 31)) {  // 32-bit division
+            const int t = static_cast<int>(u) / chunks;
+            chunk = static_cast<int>(u) - t * chunks;
+            token = t;
+        } else {
+            token = u / chunks;
+            chunk = static_cast<int>(u - token * chunks);
+        }
+        b = p.batch == 1 ? 0 : token / p.seq;
+        s = token - b * p.seq;
+        h = chunk * g.per[which];
+        n = u < g.units[which] ? min(g.per[which], heads - h) : 0;
+    }
+    __device__ __forceinline__ int64_t at(const HeadsP& x) const { return b * x.sb + s * x.st + h * x.sh; }
+};
 
-// Forward over tiles.
-template <int DT, bool INTER, bool NORM>
-__global__ void __launch_bounds__(256) rope_fwd_tile_kernel(const RopeP p, const RopeTile g, int pad, int table_bytes) {
-    constexpr int E = VecElems<DT>::value, H = E / 2;
-    extern __shared__ __align__(16) unsigned char smem[];
-    float* table = reinterpret_cast<float*>(smem);
+// Forward.
+template <int DT, int LAYOUT, bool NORM>
+__global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const RopeUnits g) {
+    using Ln = Lane<DT, LAYOUT>;
+    constexpr int H = Ln::H;
+    extern __shared__ __align__(16) float rows[];
     const int which = blockIdx.x >= g.ctas[0];
-    const RopeSeg& sg = p.seg[which];
-    const int heads = sg.heads;
-    const int l = threadIdx.x & (g.L - 1);
+    const RopeSeg sg = p.seg[which];
+    Ln ln(g);
     const int team = threadIdx.x >> g.log2L, teams = 256 >> g.log2L;
-    int va, vb;
-    lane_vectors(g, INTER, l, va, vb);
-    const bool has_a = va < g.nv, has_b = vb < g.nv;
+    float* row = rows + team * p.D;
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const bool norm = NORM && sg.w;
-    const int64_t tokens = p.batch * p.seq;
-    const uint4* in = static_cast<const uint4*>(sg.in.p) + va;
-    uint4* out = static_cast<uint4*>(sg.out.p) + va;
-    const int vd = vb - va;
-    unsigned char* slots = smem + table_bytes + threadIdx.x * 16;
-    for (int k = 0; k < 2 * kSteps; ++k) *reinterpret_cast<uint4*>(slots + k * 4096) = zero4;
-    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
-    Walk ahead;
-    ahead.tile = blockIdx.x - (which ? g.ctas[0] : 0);
-    ahead.enter(g, which, tokens, team, teams, heads);
-    Walk at = ahead;
-    int put = 0, take = 0;
-    auto fetch = [&]() {
-        if (ahead.n > 0) {
-            if (ahead.live()) {
-                const uint4* x = in + ahead.at(p, sg.in);
-                if (has_a) copy16(slot0 + (2 * put) * 4096, x);
-                if (has_b) copy16(slot0 + (2 * put + 1) * 4096, x + vd);
-            }
-            ahead.advance(g, which, tokens, team, teams, heads);
-        }
-        copies_commit();
-        put = put + 1 == kSteps ? 0 : put + 1;
-    };
+    const int vd = ln.vb - ln.va, per = g.per[which];
     pdl_wait();
     pdl_launch_dependents();
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) fetch();
     f2 wa[H], wb[H];
     if (norm) {
         const uint4* w = static_cast<const uint4*>(sg.w);
-        weights2<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
-        weights2<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
+        weights2<DT>(ln.has_a ? __ldg(w + ln.va) : zero4, p.offset, wa);
+        weights2<DT>(ln.has_b ? __ldg(w + ln.vb) : zero4, p.offset, wb);
     }
-    while (at.n > 0) {
-        if (at.step == 0) {  // a new tile
-            __syncthreads();  // the tables of the tile before are read
-            make_tables(p, at.tok0, at.n, pad, table);
-            __syncthreads();
-        }
-        copies_wait<kSteps - 1>();
-        f2 x[H], z[H];
-        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (2 * take) * 4096), x);
-        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (2 * take + 1) * 4096), z);
-        take = take + 1 == kSteps ? 0 : take + 1;
-        fetch();
-        const bool live = at.live();
-        if (norm) {
-            f2 sq = 0;
+    const int64_t first = (blockIdx.x - (which ? g.ctas[0] : 0)) * teams;
+    for (int64_t u0 = first; u0 < g.units[which]; u0 += g.ctas[which] * teams) {
+        const Unit u(p, g, which, sg.heads, u0 + team);
+        const uint4* in = static_cast<const uint4*>(sg.in.p) + u.at(sg.in) + ln.va;
+        uint4* out = static_cast<uint4*>(sg.out.p) + u.at(sg.out) + ln.va;
+        uint4 na[kAhead], nb[kAhead];
+        auto fetch = [&](int h) {
 #pragma unroll
-            for (int e = 0; e < H; ++e) sq = f2_fma(x[e], x[e], sq);
+            for (int k = 0; k < kAhead; ++k) {
+                na[k] = nb[k] = zero4;
+                if (h + k < u.n) {
+                    if (ln.has_a) na[k] = ld_stream(in);
+                    if (ln.has_b) nb[k] = ld_stream(in + vd);
+                }
+                in += sg.in.sh;
+            }
+        };
+        fetch(0);
+        if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
+        for (int h = 0; h < per; h += kAhead) {
+            uint4 xa[kAhead], xb[kAhead];
 #pragma unroll
-            for (int e = 0; e < H; ++e) sq = f2_fma(z[e], z[e], sq);
-            const float ss = lanes_sum(f2_sum(sq), g.L);
-            const float r = rsqrtf(fmaf(ss, g.inv_d, p.eps));
-            if (l == 0 && sg.rstd && live) sg.rstd[(at.tok0 + at.tok) * heads + at.h] = r;
-            const f2 r2 = f2_dup(r);
+            for (int k = 0; k < kAhead; ++k) xa[k] = na[k], xb[k] = nb[k];
+            if (h + kAhead < per) fetch(h + kAhead);
 #pragma unroll
-            for (int e = 0; e < H; ++e) {
-                x[e] = f2_mul(f2_mul(x[e], r2), wa[e]);
-                z[e] = f2_mul(f2_mul(z[e], r2), wb[e]);
+            for (int k = 0; k < kAhead; ++k) {
+                const bool live = h + k < u.n;
+                f2 x[H], z[H];
+                unpack2<DT>(xa[k], x);
+                unpack2<DT>(xb[k], z);
+                if (norm) {
+                    f2 sq = 0;
+#pragma unroll
+                    for (int e = 0; e < H; ++e) sq = f2_fma(z[e], z[e], f2_fma(x[e], x[e], sq));
+                    const float r = rsqrtf(fmaf(lanes_sum(f2_sum(sq), g.L), g.inv_d, p.eps));
+                    if (ln.l == 0 && live && sg.rstd) sg.rstd[u.token * sg.heads + u.h + h + k] = r;
+                    const f2 r2 = f2_dup(r);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        x[e] = f2_mul(f2_mul(x[e], r2), wa[e]);
+                        z[e] = f2_mul(f2_mul(z[e], r2), wb[e]);
+                    }
+                }
+                ln.template turned<1>(p, g, x, z, row);
+                if (live) {
+                    if (ln.has_a) st_stream(out, pack2<DT>(x));
+                    if (ln.has_b) st_stream(out + vd, pack2<DT>(z));
+                }
+                out += sg.out.sh;
             }
         }
-        if (live) {
-            const float* cs = table + 2 * at.tok * pad;
-            turn_lane<DT, INTER, 1>(g, cs, cs + pad, l, x, z, p.R);
-            uint4* y = out + at.at(p, sg.out);
-            if (has_a) st_stream(y, pack2<DT>(x));
-            if (has_b) st_stream(y + vd, pack2<DT>(z));
-        }
-        at.advance(g, which, tokens, team, teams, heads);
     }
-    copies_wait<0>();
 }
 
-// Backward over tiles: turned back, then the norm's backward, with the weights'
-// gradients of a lane's columns summed in registers over all the heads it sees,
-// and over the CTA's teams (in order) into one partial row.
-template <int DT, bool INTER, bool NORM>
-__global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const RopeTile g, int pad, int table_bytes) {
-    constexpr int E = VecElems<DT>::value, H = E / 2, NV = NORM ? 4 : 2;
-    extern __shared__ __align__(16) unsigned char smem[];
-    float* table = reinterpret_cast<float*>(smem);
+// Backward: turned back, then the norm's backward, with the weights' gradients of
+// a lane's columns summed in registers over all the heads it sees, and over the
+// CTA's teams (in order) into one partial row.
+template <int DT, int LAYOUT, bool NORM>
+__global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const RopeUnits g) {
+    using Ln = Lane<DT, LAYOUT>;
+    constexpr int E = Ln::E, H = Ln::H, A = NORM ? 1 : kAhead;
+    extern __shared__ __align__(16) float rows[];
     const int which = blockIdx.x >= g.ctas[0];
-    const RopeSeg& sg = p.seg[which];
-    const int heads = sg.heads;
-    const int l = threadIdx.x & (g.L - 1);
+    const RopeSeg sg = p.seg[which];
+    Ln ln(g);
     const int team = threadIdx.x >> g.log2L, teams = 256 >> g.log2L;
-    int va, vb;
-    lane_vectors(g, INTER, l, va, vb);
-    const bool has_a = va < g.nv, has_b = vb < g.nv;
+    float* row = rows + team * p.D;
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const bool norm = NORM && sg.w;
-    const int64_t tokens = p.batch * p.seq;
-    const uint4* in = static_cast<const uint4*>(sg.in.p) + va;
-    const uint4* xin = static_cast<const uint4*>(sg.x.p) + va;
-    uint4* out = static_cast<uint4*>(sg.out.p) + va;
-    const int vd = vb - va;
-    unsigned char* slots = smem + table_bytes + threadIdx.x * 16;
-    for (int k = 0; k < NV * kSteps; ++k) *reinterpret_cast<uint4*>(slots + k * 4096) = zero4;
-    float* rs = reinterpret_cast<float*>(smem + table_bytes + tile_slots(NV)) + threadIdx.x;
-    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
-    const uint32_t rs0 = static_cast<uint32_t>(__cvta_generic_to_shared(rs));
-    const int64_t cta = blockIdx.x - (which ? g.ctas[0] : 0);
-    Walk ahead;
-    ahead.tile = cta;
-    ahead.enter(g, which, tokens, team, teams, heads);
-    Walk at = ahead;
-    int put = 0, take = 0;
-    auto fetch = [&]() {
-        if (ahead.n > 0) {
-            if (ahead.live()) {
-                const uint4* d = in + ahead.at(p, sg.in);
-                if (has_a) copy16(slot0 + (NV * put) * 4096, d);
-                if (has_b) copy16(slot0 + (NV * put + 1) * 4096, d + vd);
-                if (norm) {
-                    const uint4* x = xin + ahead.at(p, sg.x);
-                    if (has_a) copy16(slot0 + (NV * put + 2) * 4096, x);
-                    if (has_b) copy16(slot0 + (NV * put + 3) * 4096, x + vd);
-                    copy4(rs0 + put * 1024, sg.rstd + (ahead.tok0 + ahead.tok) * heads + ahead.h);
-                }
-            }
-            ahead.advance(g, which, tokens, team, teams, heads);
-        }
-        copies_commit();
-        put = put + 1 == kSteps ? 0 : put + 1;
-    };
+    const int vd = ln.vb - ln.va, per = g.per[which];
     pdl_wait();
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) fetch();
     f2 wa[H], wb[H], da[H], db[H];
 #pragma unroll
     for (int e = 0; e < H; ++e) da[e] = db[e] = 0;
     if (norm) {
         const uint4* w = static_cast<const uint4*>(sg.w);
-        weights2<DT>(has_a ? __ldg(w + va) : zero4, p.offset, wa);
-        weights2<DT>(has_b ? __ldg(w + vb) : zero4, p.offset, wb);
+        weights2<DT>(ln.has_a ? __ldg(w + ln.va) : zero4, p.offset, wa);
+        weights2<DT>(ln.has_b ? __ldg(w + ln.vb) : zero4, p.offset, wb);
     }
-    while (at.n > 0) {
-        if (at.step == 0) {  // a new tile
-            __syncthreads();  // the tables of the tile before are read
-            make_tables(p, at.tok0, at.n, pad, table);
-            __syncthreads();
-        }
-        copies_wait<kSteps - 1>();
-        f2 ta[H], tb[H];
-        uint4 xa = zero4, xb = zero4;
-        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (NV * take) * 4096), ta);
-        unpack2<DT>(*reinterpret_cast<const uint4*>(slots + (NV * take + 1) * 4096), tb);
-        float r = 0.f;
-        if (norm) {
-            xa = *reinterpret_cast<const uint4*>(slots + (NV * take + 2) * 4096);
-            xb = *reinterpret_cast<const uint4*>(slots + (NV * take + 3) * 4096);
-            r = rs[take * 256];
-        }
-        take = take + 1 == kSteps ? 0 : take + 1;
-        fetch();
-        const bool live = at.live();
-        const float* cs = table + 2 * (live ? at.tok : 0) * pad;
-        turn_lane<DT, INTER, -1>(g, cs, cs + pad, l, ta, tb, p.R);
-        if (norm) {
-            f2 x[H], z[H], c2 = 0;
-            unpack2<DT>(xa, x);
-            unpack2<DT>(xb, z);
-            const f2 r2 = f2_dup(r);
-            if (live) {  // past the tile's last unit a slot holds an older one's values
+    const int64_t cta = blockIdx.x - (which ? g.ctas[0] : 0);
+    for (int64_t u0 = cta * teams; u0 < g.units[which]; u0 += g.ctas[which] * teams) {
+        const Unit u(p, g, which, sg.heads, u0 + team);
+        const uint4* in = static_cast<const uint4*>(sg.in.p) + u.at(sg.in) + ln.va;
+        const uint4* xin = static_cast<const uint4*>(sg.x.p) + (norm ? u.at(sg.x) + ln.va : 0);
+        uint4* out = static_cast<uint4*>(sg.out.p) + u.at(sg.out) + ln.va;
+        const float* rstd = norm ? sg.rstd + (u.token * sg.heads + u.h) : nullptr;
+        uint4 na[A], nb[A], ma[A], mb[A];
+        float nr[A];
+        auto fetch = [&](int h) {
 #pragma unroll
-                for (int e = 0; e < H; ++e) {
-                    const f2 gx = f2_mul(ta[e], x[e]), gz = f2_mul(tb[e], z[e]);
-                    da[e] = f2_fma(gx, r2, da[e]);
-                    db[e] = f2_fma(gz, r2, db[e]);
-                    c2 = f2_fma(gx, wa[e], c2);
-                    c2 = f2_fma(gz, wb[e], c2);
+            for (int k = 0; k < A; ++k) {
+                na[k] = nb[k] = ma[k] = mb[k] = zero4;
+                nr[k] = 0.f;
+                if (h + k < u.n) {
+                    if (ln.has_a) na[k] = ld_stream(in);
+                    if (ln.has_b) nb[k] = ld_stream(in + vd);
+                    if (norm) {
+                        if (ln.has_a) ma[k] = ld_stream(xin);
+                        if (ln.has_b) mb[k] = ld_stream(xin + vd);
+                        nr[k] = __ldg(rstd + h + k);
+                    }
                 }
+                in += sg.in.sh;
+                xin += sg.x.sh;
             }
-            const float c = lanes_sum(f2_sum(c2), g.L);
-            const f2 mf = f2_dup(-(r * r * r * (c * g.inv_d)));
+        };
+        fetch(0);
+        if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
+        for (int h = 0; h < per; h += A) {
+            uint4 ga[A], gb[A], xa[A], xb[A];
+            float rs[A];
 #pragma unroll
-            for (int e = 0; e < H; ++e) {
-                ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
-                tb[e] = f2_fma(f2_mul(tb[e], r2), wb[e], f2_mul(z[e], mf));
+            for (int k = 0; k < A; ++k) ga[k] = na[k], gb[k] = nb[k], xa[k] = ma[k], xb[k] = mb[k], rs[k] = nr[k];
+            if (h + A < per) fetch(h + A);
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+                f2 ta[H], tb[H];
+                unpack2<DT>(ga[k], ta);
+                unpack2<DT>(gb[k], tb);
+                ln.template turned<-1>(p, g, ta, tb, row);
+                if (norm) {
+                    f2 x[H], z[H], c2 = 0;
+                    unpack2<DT>(xa[k], x);
+                    unpack2<DT>(xb[k], z);
+                    const f2 r2 = f2_dup(rs[k]);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        const f2 gx = f2_mul(ta[e], x[e]), gz = f2_mul(tb[e], z[e]);
+                        da[e] = f2_fma(gx, r2, da[e]);
+                        db[e] = f2_fma(gz, r2, db[e]);
+                        c2 = f2_fma(gz, wb[e], f2_fma(gx, wa[e], c2));
+                    }
+                    const float c = lanes_sum(f2_sum(c2), g.L);
+                    const f2 mf = f2_dup(-(rs[k] * rs[k] * rs[k] * (c * g.inv_d)));
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
+                        tb[e] = f2_fma(f2_mul(tb[e], r2), wb[e], f2_mul(z[e], mf));
+                    }
+                }
+                if (h + k < u.n) {
+                    if (ln.has_a) st_stream(out, pack2<DT>(ta));
+                    if (ln.has_b) st_stream(out + vd, pack2<DT>(tb));
+                }
+                out += sg.out.sh;
             }
         }
-        if (live) {
-            uint4* y = out + at.at(p, sg.out);
-            if (has_a) st_stream(y, pack2<DT>(ta));
-            if (has_b) st_stream(y + vd, pack2<DT>(tb));
-        }
-        at.advance(g, which, tokens, team, teams, heads);
     }
-    copies_wait<0>();
     pdl_launch_dependents();
     if (!norm) return;
     // A warp's teams meet by shuffles, the warps in order in shared memory:
     // [8 warps][L lanes][2E].
-    __syncthreads();  // the tables are read
+    __syncthreads();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int e = 0; e < H; ++e) {
@@ -431,7 +407,7 @@ __global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const
             b.y += __shfl_xor_sync(0xffffffffu, b.y, off);
         }
         if (lane < g.L) {
-            float2* part = reinterpret_cast<float2*>(table) + (w * g.L + lane) * E;
+            float2* part = reinterpret_cast<float2*>(rows) + (w * g.L + lane) * E;
             part[e] = a;
             part[H + e] = b;
         }
@@ -440,10 +416,10 @@ __global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const
     for (int i = threadIdx.x; i < g.L * 2 * E; i += 256) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t += table[k * g.L * 2 * E + i];
-        int a, b;
-        lane_vectors(g, INTER, i / (2 * E), a, b);
-        const int e = i % (2 * E);
+        for (int k = 0; k < 8; ++k) t += rows[k * g.L * 2 * E + i];
+        const int li = i / (2 * E), e = i % (2 * E);
+        int a = 2 * li, b = a + 1;
+        if (LAYOUT == kHalves && li < g.pairs) a = li, b = li + g.pairs;
         const int j = e < E ? a * E + e : b * E + e - E;
         if (j < p.D) p.ws[(which ? g.ctas[0] + cta : cta) * p.D + j] = t;
     }
@@ -454,14 +430,14 @@ __global__ void __launch_bounds__(256) rope_bwd_tile_kernel(const RopeP p, const
 // lane, lane + 32, ... and the values behind rotary_dim in the same way, reads
 // both values of a pair before it writes them, and no lane reads another's, so
 // the outputs may lie on the inputs.
-struct Unit {
+struct Place {
     int seg;
     int64_t b, s, h, token;
 };
 
-__device__ __forceinline__ Unit unit_of(const RopeP& p, int64_t u) {
+__device__ __forceinline__ Place unit_of(const RopeP& p, int64_t u) {
     const int H = p.seg[0].heads + p.seg[1].heads;
-    Unit o;
+    Place o;
     o.token = u / H;
     o.h = u - o.token * H;
     o.seg = o.h >= p.seg[0].heads;
@@ -471,7 +447,7 @@ __device__ __forceinline__ Unit unit_of(const RopeP& p, int64_t u) {
     return o;
 }
 
-__device__ __forceinline__ int64_t at(const HeadsP& h, const Unit& u) {
+__device__ __forceinline__ int64_t at(const HeadsP& h, const Place& u) {
     return u.b * h.sb + u.s * h.st + u.h * h.sh;
 }
 
@@ -484,7 +460,7 @@ __global__ void __launch_bounds__(256) rope_fwd_generic_kernel(const RopeP p) {
     pdl_wait();
     pdl_launch_dependents();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < units; i += warps) {
-        const Unit u = unit_of(p, i);
+        const Place u = unit_of(p, i);
         const RopeSeg& g = p.seg[u.seg];
         const int64_t x0 = at(g.in, u), y0 = at(g.out, u);
         float r = 1.f;
@@ -504,7 +480,7 @@ __global__ void __launch_bounds__(256) rope_fwd_generic_kernel(const RopeP p) {
         const int64_t pos = position_of(p, u.b, u.s);
         __syncwarp();  // every lane's reads for the sum before the first write
         for (int j = lane; j < half; j += 32) {
-            const float2 cs = turn(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn<kFP32>(pos, p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float xa = x(a), xb = x(b);
             store1<DT>(g.out.p, y0 + a, fmaf(xa, cs.x, -xb * cs.y));
@@ -531,14 +507,14 @@ __global__ void __launch_bounds__(256) rope_bwd_generic_kernel(const RopeP p) {
         for (int j = p.R + lane; j < p.D; j += 32) acc[j] = 0.f;
     }
     for (int64_t i = me; i < units; i += warps) {
-        const Unit u = unit_of(p, i);
+        const Place u = unit_of(p, i);
         const RopeSeg& g = p.seg[u.seg];
         const int64_t d0 = at(g.in, u), o0 = at(g.out, u), x0 = at(g.x, u);
         const int64_t pos = position_of(p, u.b, u.s);
         // The gradient of the normed head at pair j (as its two values) and
         // behind rotary_dim.
         auto back = [&](int j) {
-            const float2 cs = turn(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn<kFP32>(pos, p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float da = load1<DT>(g.in.p, d0 + a), db = load1<DT>(g.in.p, d0 + b);
             return make_float2(fmaf(da, cs.x, db * cs.y), fmaf(db, cs.x, -da * cs.y));
@@ -623,18 +599,11 @@ int64_t generic_grid(const RopeP& p, const OpCfg& c) {
     return persistent_grid(units, 8, c.dev.sm_count, kGenericCtasPerSM, c.max_ctas);
 }
 
-// Table entries per token: the rotated pairs, up to whole vectors.
-int table_pad(const RopeP& p) { return (p.R / 2 + 3) / 4 * 4; }
-
-// Whether every head is whole 16-byte vectors that the tile kernels can pair up,
-// and how: lanes per head, tokens per tile, CTAs.
-bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* g) {
+// Whether every head is whole 16-byte vectors, of at most 64.
+bool vectors(const RopeP& p, bool bwd) {
     const int E = vec_elems(p.dtype);
     if (p.D % E != 0 || p.D > 64 * E) return false;
-    // Half layout: both halves whole vectors. Interleaved: any even rotary_dim.
-    if (!p.interleaved && p.R % (2 * E) != 0) return false;
-    for (int k = 0; k < 2; ++k) {
-        const RopeSeg& s = p.seg[k];
+    for (const RopeSeg& s : p.seg) {
         if (s.heads == 0) continue;
         const HeadsP* hs[] = {&s.in, &s.out, bwd && s.w ? &s.x : nullptr};
         for (const HeadsP* h : hs) {
@@ -645,73 +614,66 @@ bool tiles(const RopeP& p, const OpCfg& c, bool bwd, int ctas_per_sm, RopeTile* 
         }
         if (!aligned16(s.w)) return false;
     }
-    g->nv = p.D / E;
-    g->inv_d = 1.f / static_cast<float>(p.D);
-    g->pairs = p.interleaved ? 0 : p.R / (2 * E);
-    g->L = 1;
-    g->log2L = 0;
-    while (g->L * 2 < g->nv) {
-        g->L <<= 1;
-        ++g->log2L;
-    }
-    const int teams = 256 / g->L;
-    const int64_t tokens = p.batch * p.seq;
-    int64_t work[2] = {0, 0};
-    for (int k = 0; k < 2; ++k) {
-        const int64_t heads = p.seg[k].heads;
-        g->tokens[k] = 1;
-        g->tiles[k] = 0;
-        if (heads == 0) continue;
-        // A tile is about four steps of the CTA's teams, as far as the tokens reach
-        // every SM and their tables 16 KB.
-        int64_t n = std::max<int64_t>(1, 4 * teams / heads);
-        n = std::min<int64_t>(n, std::max<int64_t>(1, tokens / (2 * c.dev.sm_count)));
-        n = std::min<int64_t>(n, std::max<int64_t>(1, 2048 / table_pad(p)));
-        g->tokens[k] = static_cast<int>(n);
-        g->tiles[k] = (tokens + n - 1) / n;
-        work[k] = heads;
-    }
-    // CTAs in proportion to the heads.
-    int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas_per_sm;
-    if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(c.max_ctas, 2));
-    g->ctas[0] = std::min(g->tiles[0], std::max<int64_t>(1, cap * work[0] / (work[0] + work[1])));
-    g->ctas[1] = work[1] ? std::min(g->tiles[1], std::max<int64_t>(1, cap - g->ctas[0])) : 0;
     return true;
 }
 
-// Shared memory a tile kernel is given for its tables: 16 KB, one token's where
-// that is more.
-int table_bytes(const RopeP& p) { return std::max(16384, table_pad(p) * 8); }
-
-// Opts a kernel into `smem` bytes on the current device, once; the CTAs per SM.
-int tile_occupancy(const void* fn, int smem) {
-    static std::mutex mu;
-    static std::map<std::pair<int, const void*>, int> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    {
-        std::lock_guard<std::mutex> guard(mu);
-        int& have = done[{dev, fn}];
-        if (have < smem) {
-            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
-            have = smem;
-        }
-    }
-    return occupancy(fn, 256, smem);
+int layout_of(const RopeP& p) {
+    return p.interleaved ? kInterleaved : p.R % (2 * vec_elems(p.dtype)) == 0 ? kHalves : kExchange;
 }
 
-template <int DT, bool INTER, bool NORM>
-cudaError_t fwd_tiles(RopeP p, const OpCfg& c, bool* taken) {
-    auto fn = rope_fwd_tile_kernel<DT, INTER, NORM>;
-    RopeTile g;
-    const int tb = table_bytes(p), smem = tb + tile_slots(2);
-    const int occ = tile_occupancy(reinterpret_cast<const void*>(fn), smem);
-    *taken = occ > 0 && tiles(p, c, false, occ, &g);
-    if (!*taken) return cudaSuccess;
-    constexpr int E = VecElems<DT>::value;
-    for (RopeSeg& s : p.seg)
-        for (HeadsP* h : {&s.in, &s.out}) h->sb /= E, h->st /= E, h->sh /= E;
-    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g, table_pad(p), tb);
+// Lays out the units: lanes per head, heads per unit, CTAs; strides in vectors.
+RopeUnits units_of(RopeP* p, const OpCfg& c, int ctas_per_sm) {
+    const int E = vec_elems(p->dtype);
+    for (RopeSeg& s : p->seg)
+        for (HeadsP* h : {&s.in, &s.out, &s.x}) h->sb /= E, h->st /= E, h->sh /= E;
+    RopeUnits g;
+    g.nv = p->D / E;
+    g.inv_d = 1.f / static_cast<float>(p->D);
+    g.pairs = layout_of(*p) == kHalves ? p->R / (2 * E) : 0;
+    g.L = 1;
+    g.log2L = 0;
+    while (g.L * 2 < g.nv) {
+        g.L <<= 1;
+        ++g.log2L;
+    }
+    const int64_t teams = 256 / g.L, tokens = p->batch * p->seq;
+    int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas_per_sm;
+    if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(c.max_ctas, 2));
+    // Units of as many heads as leave every team about eight units, so that the
+    // teams end together; a unit of many heads costs fewer angles.
+    const int64_t heads = p->seg[0].heads + p->seg[1].heads;
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(16, tokens * heads / (8 * cap * teams)));
+    int64_t work[2] = {0, 0};
+    for (int k = 0; k < 2; ++k) {
+        const int64_t n = p->seg[k].heads;
+        g.per[k] = g.chunks[k] = 0;
+        g.units[k] = 0;
+        if (n == 0) continue;
+        g.chunks[k] = static_cast<int>((n + share - 1) / share);
+        g.per[k] = static_cast<int>((n + g.chunks[k] - 1) / g.chunks[k]);
+        g.chunks[k] = static_cast<int>((n + g.per[k] - 1) / g.per[k]);
+        g.units[k] = tokens * g.chunks[k];
+        work[k] = n;
+    }
+    // CTAs in proportion to the heads.
+    int64_t need[2] = {(g.units[0] + teams - 1) / teams, (g.units[1] + teams - 1) / teams};
+    if (need[0] + need[1] <= cap) {
+        g.ctas[0] = need[0];
+        g.ctas[1] = need[1];
+    } else {
+        g.ctas[0] = std::min(need[0], std::max<int64_t>(1, (cap * work[0] + heads / 2) / heads));
+        g.ctas[1] = work[1] ? std::min(need[1], std::max<int64_t>(1, cap - g.ctas[0])) : 0;
+    }
+    return g;
+}
+
+template <int DT, int LAYOUT, bool NORM>
+cudaError_t fwd_units(RopeP p, const OpCfg& c) {
+    auto fn = rope_fwd_kernel<DT, LAYOUT, NORM>;
+    const int smem = LAYOUT == kExchange ? 256 * 2 * VecElems<DT>::value * 4 : 0;  // at most
+    const int occ = std::max(1, occupancy(reinterpret_cast<const void*>(fn), 256, smem));
+    const RopeUnits g = units_of(&p, c, occ);
+    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, LAYOUT == kExchange ? (256 >> g.log2L) * p.D * 4 : 0, p, g);
 }
 
 cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t rows_k, int paired) {
@@ -723,50 +685,46 @@ cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t ro
     return cudaLaunchKernelEx(&cfg.cfg, rope_dw_kernel, p, RopeRows{{rows_q, rows_k}}, paired);
 }
 
-template <int DT, bool INTER, bool NORM>
-cudaError_t bwd_tiles(RopeP p, const OpCfg& c, bool* taken) {
-    auto fn = rope_bwd_tile_kernel<DT, INTER, NORM>;
-    RopeTile g;
+template <int DT, int LAYOUT, bool NORM>
+cudaError_t bwd_units(RopeP p, const OpCfg& c) {
     constexpr int E = VecElems<DT>::value;
-    // The sums of the weights' gradients meet where the tables were (16 KB at most).
-    const int tb = table_bytes(p), smem = tb + tile_slots(NORM ? 4 : 2) + (NORM ? kSteps * 1024 : 0);
-    const int occ = tile_occupancy(reinterpret_cast<const void*>(fn), smem);
-    *taken = occ > 0 && tiles(p, c, true, std::min(8, occ), &g);
-    if (!*taken) return cudaSuccess;
-    for (RopeSeg& s : p.seg)
-        for (HeadsP* h : {&s.in, &s.out, &s.x}) h->sb /= E, h->st /= E, h->sh /= E;
-    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g, table_pad(p), tb);
+    auto fn = rope_bwd_kernel<DT, LAYOUT, NORM>;
+    const int smem = LAYOUT == kExchange ? 256 * 2 * E * 4 : 0;  // at most
+    const int occ = std::max(1, std::min(8, occupancy(reinterpret_cast<const void*>(fn), 256, smem)));
+    const RopeUnits g = units_of(&p, c, occ);
+    const int bytes = std::max(LAYOUT == kExchange ? (256 >> g.log2L) * p.D * 4 : 0, NORM ? 8 * g.L * 2 * E * 4 : 0);
+    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, bytes, p, g);
     return e != cudaSuccess || !NORM ? e : launch_dw(p, c, g.ctas[0], g.ctas[1], 0);
 }
 
-template <int DT>
-cudaError_t fwd(const RopeP& p, const OpCfg& c) {
-    if (c.variant != RMSNORM_VARIANT_GENERIC) {
-        bool taken = false;
-        const bool norm = p.seg[0].w || p.seg[1].w;
-        const cudaError_t e =
-            p.interleaved ? (norm ? fwd_tiles<DT, true, true>(p, c, &taken) : fwd_tiles<DT, true, false>(p, c, &taken))
-                          : (norm ? fwd_tiles<DT, false, true>(p, c, &taken) : fwd_tiles<DT, false, false>(p, c, &taken));
-        if (taken) return e;
-    }
-    if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
-    return op_launch(c, rope_fwd_generic_kernel<DT>, generic_grid(p, c), 256, 0, p);
+template <int DT, int LAYOUT>
+cudaError_t run_units(const RopeP& p, const OpCfg& c, bool bwd) {
+    if (p.seg[0].w || p.seg[1].w) return bwd ? bwd_units<DT, LAYOUT, true>(p, c) : fwd_units<DT, LAYOUT, true>(p, c);
+    return bwd ? bwd_units<DT, LAYOUT, false>(p, c) : fwd_units<DT, LAYOUT, false>(p, c);
 }
 
 template <int DT>
-cudaError_t bwd(const RopeP& p, const OpCfg& c) {
-    const bool norm = p.seg[0].w || p.seg[1].w;
-    if (c.variant != RMSNORM_VARIANT_GENERIC) {
-        bool taken = false;
-        const cudaError_t e =
-            p.interleaved ? (norm ? bwd_tiles<DT, true, true>(p, c, &taken) : bwd_tiles<DT, true, false>(p, c, &taken))
-                          : (norm ? bwd_tiles<DT, false, true>(p, c, &taken) : bwd_tiles<DT, false, false>(p, c, &taken));
-        if (taken) return e;
+cudaError_t run(const RopeP& p, const OpCfg& c, bool bwd) {
+    if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(p, bwd)) {
+        switch (layout_of(p)) {
+            case kHalves: return run_units<DT, kHalves>(p, c, bwd);
+            case kInterleaved: return run_units<DT, kInterleaved>(p, c, bwd);
+            default: return run_units<DT, kExchange>(p, c, bwd);
+        }
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     const int64_t G = generic_grid(p, c);
+    if (!bwd) return op_launch(c, rope_fwd_generic_kernel<DT>, G, 256, 0, p);
     const cudaError_t e = op_launch(c, rope_bwd_generic_kernel<DT>, G, 256, 0, p);
-    return e != cudaSuccess || !norm ? e : launch_dw(p, c, G * 8, G * 8, 1);
+    return e != cudaSuccess || !(p.seg[0].w || p.seg[1].w) ? e : launch_dw(p, c, G * 8, G * 8, 1);
+}
+
+cudaError_t run(const RopeP& p, const OpCfg& c, bool bwd) {
+    switch (p.dtype) {
+        case kBF16: return run<kBF16>(p, c, bwd);
+        case kFP16: return run<kFP16>(p, c, bwd);
+        default: return run<kFP32>(p, c, bwd);
+    }
 }
 
 }  // namespace
@@ -775,20 +733,8 @@ int64_t rope_bwd_partial_rows(int sm_count) {
     return 2LL * sm_count * kGenericCtasPerSM * 8;
 }
 
-cudaError_t rope_fwd_run(const RopeP& p, const OpCfg& c) {
-    switch (p.dtype) {
-        case kBF16: return fwd<kBF16>(p, c);
-        case kFP16: return fwd<kFP16>(p, c);
-        default: return fwd<kFP32>(p, c);
-    }
-}
+cudaError_t rope_fwd_run(const RopeP& p, const OpCfg& c) { return run(p, c, false); }
 
-cudaError_t rope_bwd_run(const RopeP& p, const OpCfg& c) {
-    switch (p.dtype) {
-        case kBF16: return bwd<kBF16>(p, c);
-        case kFP16: return bwd<kFP16>(p, c);
-        default: return bwd<kFP32>(p, c);
-    }
-}
+cudaError_t rope_bwd_run(const RopeP& p, const OpCfg& c) { return run(p, c, true); }
 
 }  // namespace rmsn
