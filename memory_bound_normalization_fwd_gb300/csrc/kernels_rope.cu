@@ -12,6 +12,9 @@
 #include "ops_common.cuh"
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace rmsn {
 namespace {
@@ -47,9 +50,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // of two, 1..32: a team) make a head, two vectors each, and a row sum of the head's
 // norm is a butterfly over them. LAYOUT says which two vectors a lane takes:
 //   kHalves      i and i + R/(2E) of the rotated part, so that both values of a pair
-//                are in one thread; 2i and 2i + 1 behind it
-//   kInterleaved 2i and 2i + 1: a pair lies inside a vector
-//   kExchange    2i and 2i + 1, halves that are not whole vectors: the other value of
+//                are in one thread
+//   kInterleaved i and i + L: a pair lies inside a vector
+//   kExchange    i and i + L, halves that are not whole vectors: the other value of
 //                a pair is read from a copy of the head in shared memory
 //
 // A unit is a token with some of its heads, and a team takes one unit after
@@ -62,7 +65,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // the instructions per head: 16384 tokens of 40 heads of 128 bf16 with norms 90 to
 // 114 us in several forms.)
 constexpr int kHalves = 0, kInterleaved = 1, kExchange = 2;
-constexpr int kAhead = 2;  // heads of a team loaded ahead
+// Heads of a team on their way into shared memory at a time. (Held in registers
+// instead, they cost the backward with norms its occupancy: 100 against 83 us at
+// 16384x40x128 bf16; three ahead 84, four 86.)
+constexpr int kAhead = 2;
 
 struct RopeUnits {
     int L;           // lanes per head
@@ -74,7 +80,24 @@ struct RopeUnits {
     int64_t units[2];
     int64_t ctas[2]; // CTAs of q, of k
     float inv_d;     // 1 / head_dim
+    int slots_at;    // byte offset of the copies in shared memory (backward)
 };
+
+// The two vectors of lane l (past nv: none). Lanes of a team take neighbouring
+// vectors: the copies go past L1, and would fetch a sector twice for two lanes.
+template <int LAYOUT>
+__device__ __forceinline__ void lane_vectors(const RopeUnits& g, int l, int& a, int& b) {
+    if (LAYOUT != kHalves) {
+        a = l;
+        b = l + g.L;
+    } else if (l < g.pairs) {
+        a = l;
+        b = l + g.pairs;
+    } else {  // behind the rotated part
+        a = l + g.pairs;
+        b = l + g.L;
+    }
+}
 
 // A lane's place: its two vectors and its cos and sin.
 template <int DT, int LAYOUT>
@@ -87,38 +110,31 @@ struct Lane {
 
     __device__ __forceinline__ Lane(const RopeUnits& g) {
         l = threadIdx.x & (g.L - 1);
-        if (LAYOUT != kHalves || l >= g.pairs) {
-            va = 2 * l;  // behind the rotated part 2 pairs is even, so 2l starts there
-            vb = va + 1;
-        } else {
-            va = l;
-            vb = l + g.pairs;
-        }
+        lane_vectors<LAYOUT>(g, l, va, vb);
         has_a = va < g.nv;
         has_b = vb < g.nv;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) c[i] = s[i] = 0;  // a team without a unit turns zeros
     }
-    // kHalves: pairs l E + i. kInterleaved: pairs of vector 2l, then of 2l + 1.
-    // kExchange: the pair of each of the lane's values.
+    // The value (kExchange) or pair that the lane's n-th cos and sin are for.
+    __device__ __forceinline__ int index(int n) const {
+        return LAYOUT == kHalves ? l * E + n : n < N / 2 ? va * (N / 2) + n : vb * (N / 2) + n - N / 2;
+    }
     __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t position) {
         if (LAYOUT == kHalves ? l >= g.pairs : va * E >= p.R) return;
         const int half = p.R / 2;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
+        for (int n = 0; n < N; n += 2) {
             float2 t[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                int j = l * E + i + k;
-                if (LAYOUT == kExchange) {
-                    j = 2 * l * E + i + k;
-                    if (j >= half) j -= half;
-                }
+                int j = index(n + k);
+                if (LAYOUT == kExchange && j >= half) j -= half;
                 t[k] = make_float2(0.f, 0.f);
                 if (LAYOUT == kHalves || j < half) t[k] = turn<DT>(position, __ldg(p.steps + j), p.magnitude);
             }
-            c[i / 2] = f2_make(t[0].x, t[1].x);
-            s[i / 2] = f2_make(t[0].y, t[1].y);
+            c[n / 2] = f2_make(t[0].x, t[1].x);
+            s[n / 2] = f2_make(t[0].y, t[1].y);
         }
     }
     // The lane's values turned by SIGN times the angle; `row`: the team's room for a
@@ -146,8 +162,8 @@ struct Lane {
                 f2* y = k == 0 ? x : z;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    if (2 * l * H + k * H + i >= half) continue;  // the rotated part may end in a vector
                     const int n = k * H + i;
+                    if (index(n) >= half) continue;  // the rotated part may end in a vector
                     const float2 cp = f2_get(c[n / 2]), sp = f2_get(s[n / 2]), v = f2_get(y[i]);
                     const float cv = n & 1 ? cp.y : cp.x, sv = SIGN * (n & 1 ? sp.y : sp.x);
                     y[i] = f2_make(fmaf(-v.y, sv, v.x * cv), fmaf(v.x, sv, v.y * cv));
@@ -158,12 +174,10 @@ struct Lane {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 f2* y = k == 0 ? x : z;
-                if ((va + k) * E < p.R) {
+                const int first = (k == 0 ? va : vb) * E;
+                if (first < p.R) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float2 v = f2_get(y[i]);
-                        *reinterpret_cast<float2*>(row + (va + k) * E + 2 * i) = v;
-                    }
+                    for (int i = 0; i < H; ++i) *reinterpret_cast<float2*>(row + first + 2 * i) = f2_get(y[i]);
                 }
             }
             __syncwarp();
@@ -174,7 +188,7 @@ struct Lane {
                 for (int i = 0; i < H; ++i) {
                     const float2 cp = f2_get(c[k * H + i]), sp = f2_get(s[k * H + i]);
                     float2 v = f2_get(y[i]);
-                    const int j = (va + k) * E + 2 * i;
+                    const int j = (k == 0 ? va : vb) * E + 2 * i;
                     if (j < p.R) v.x = other(row, j, half, v.x, cp.x, SIGN * sp.x);
                     if (j + 1 < p.R) v.y = other(row, j + 1, half, v.y, cp.y, SIGN * sp.y);
                     y[i] = f2_make(v.x, v.y);
@@ -221,11 +235,22 @@ struct Unit {
     __device__ __forceinline__ int64_t at(const HeadsP& x) const { return b * x.sb + s * x.st + h * x.sh; }
 };
 
+// Asynchronous copies into shared memory that the copying thread alone reads
+// back (cp.async: any stride, no registers, no barrier).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Forward.
 template <int DT, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const RopeUnits g) {
     using Ln = Lane<DT, LAYOUT>;
-    constexpr int H = Ln::H;
+    constexpr int H = Ln::H, S = kAhead;
     extern __shared__ __align__(16) float rows[];
     const int which = blockIdx.x >= g.ctas[0];
     const RopeSeg sg = p.seg[which];
@@ -235,6 +260,10 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const bool norm = NORM && sg.w;
     const int vd = ln.vb - ln.va, per = g.per[which];
+    const unsigned char* slots = reinterpret_cast<const unsigned char*>(rows) + g.slots_at + threadIdx.x * 16;
+    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+    for (int k = 0; k < S * 2; ++k)  // lanes past the head's end read zeros
+        *reinterpret_cast<uint4*>(const_cast<unsigned char*>(slots) + k * 4096) = zero4;
     pdl_wait();
     pdl_launch_dependents();
     f2 wa[H], wb[H];
@@ -248,53 +277,52 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
         const Unit u(p, g, which, sg.heads, u0 + team);
         const uint4* in = static_cast<const uint4*>(sg.in.p) + u.at(sg.in) + ln.va;
         uint4* out = static_cast<uint4*>(sg.out.p) + u.at(sg.out) + ln.va;
-        uint4 na[kAhead], nb[kAhead];
-        auto fetch = [&](int h) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                na[k] = nb[k] = zero4;
-                if (h + k < u.n) {
-                    if (ln.has_a) na[k] = ld_stream(in);
-                    if (ln.has_b) nb[k] = ld_stream(in + vd);
-                }
+        float* rstd = norm && sg.rstd && ln.l == 0 ? sg.rstd + (u.token * sg.heads + u.h) : nullptr;
+        uint32_t put = 0, take = 0;
+        int ahead = 0;
+        auto fetch = [&]() {
+            if (ahead < u.n) {
+                if (ln.has_a) copy16(slot0 + put, in);
+                if (ln.has_b) copy16(slot0 + put + 4096, in + vd);
                 in += sg.in.sh;
             }
+            ++ahead;
+            copies_commit();
+            put = put == (S - 1) * 8192 ? 0 : put + 8192;
         };
-        fetch(0);
+#pragma unroll
+        for (int k = 0; k < S; ++k) fetch();
         if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
-        for (int h = 0; h < per; h += kAhead) {
-            uint4 xa[kAhead], xb[kAhead];
+        for (int h = 0; h < per; ++h) {
+            const bool live = h < u.n;
+            copies_wait<S - 1>();
+            f2 x[H], z[H];
+            unpack2<DT>(*reinterpret_cast<const uint4*>(slots + take), x);
+            unpack2<DT>(*reinterpret_cast<const uint4*>(slots + take + 4096), z);
+            take = take == (S - 1) * 8192 ? 0 : take + 8192;
+            fetch();
+            if (norm) {
+                f2 sq = 0;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) xa[k] = na[k], xb[k] = nb[k];
-            if (h + kAhead < per) fetch(h + kAhead);
+                for (int e = 0; e < H; ++e) sq = f2_fma(z[e], z[e], f2_fma(x[e], x[e], sq));
+                const float r = rsqrtf(fmaf(lanes_sum(f2_sum(sq), g.L), g.inv_d, p.eps));
+                if (live && rstd) rstd[h] = r;
+                const f2 r2 = f2_dup(r);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const bool live = h + k < u.n;
-                f2 x[H], z[H];
-                unpack2<DT>(xa[k], x);
-                unpack2<DT>(xb[k], z);
-                if (norm) {
-                    f2 sq = 0;
-#pragma unroll
-                    for (int e = 0; e < H; ++e) sq = f2_fma(z[e], z[e], f2_fma(x[e], x[e], sq));
-                    const float r = rsqrtf(fmaf(lanes_sum(f2_sum(sq), g.L), g.inv_d, p.eps));
-                    if (ln.l == 0 && live && sg.rstd) sg.rstd[u.token * sg.heads + u.h + h + k] = r;
-                    const f2 r2 = f2_dup(r);
-#pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        x[e] = f2_mul(f2_mul(x[e], r2), wa[e]);
-                        z[e] = f2_mul(f2_mul(z[e], r2), wb[e]);
-                    }
+                for (int e = 0; e < H; ++e) {
+                    x[e] = f2_mul(f2_mul(x[e], r2), wa[e]);
+                    z[e] = f2_mul(f2_mul(z[e], r2), wb[e]);
                 }
-                ln.template turned<1>(p, g, x, z, row);
-                if (live) {
-                    if (ln.has_a) st_stream(out, pack2<DT>(x));
-                    if (ln.has_b) st_stream(out + vd, pack2<DT>(z));
-                }
-                out += sg.out.sh;
             }
+            ln.template turned<1>(p, g, x, z, row);
+            if (live) {
+                if (ln.has_a) st_stream(out, pack2<DT>(x));
+                if (ln.has_b) st_stream(out + vd, pack2<DT>(z));
+            }
+            out += sg.out.sh;
         }
     }
+    copies_wait<0>();
 }
 
 // Backward: turned back, then the norm's backward, with the weights' gradients of
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
 template <int DT, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const RopeUnits g) {
     using Ln = Lane<DT, LAYOUT>;
-    constexpr int E = Ln::E, H = Ln::H, A = NORM ? 1 : kAhead;
+    constexpr int E = Ln::E, H = Ln::H, NV = NORM ? 4 : 2, S = kAhead;
     extern __shared__ __align__(16) float rows[];
     const int which = blockIdx.x >= g.ctas[0];
     const RopeSeg sg = p.seg[which];
@@ -313,6 +341,10 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
     const bool norm = NORM && sg.w;
     const int vd = ln.vb - ln.va, per = g.per[which];
+    const unsigned char* slots = reinterpret_cast<const unsigned char*>(rows) + g.slots_at + threadIdx.x * 16;
+    const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots));
+    for (int k = 0; k < S * NV; ++k)  // lanes past the head's end read zeros
+        *reinterpret_cast<uint4*>(const_cast<unsigned char*>(slots) + k * 4096) = zero4;
     pdl_wait();
     f2 wa[H], wb[H], da[H], db[H];
 #pragma unroll
@@ -329,68 +361,75 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
         const uint4* xin = static_cast<const uint4*>(sg.x.p) + (norm ? u.at(sg.x) + ln.va : 0);
         uint4* out = static_cast<uint4*>(sg.out.p) + u.at(sg.out) + ln.va;
         const float* rstd = norm ? sg.rstd + (u.token * sg.heads + u.h) : nullptr;
-        uint4 na[A], nb[A], ma[A], mb[A];
-        float nr[A];
-        auto fetch = [&](int h) {
-#pragma unroll
-            for (int k = 0; k < A; ++k) {
-                na[k] = nb[k] = ma[k] = mb[k] = zero4;
-                nr[k] = 0.f;
-                if (h + k < u.n) {
-                    if (ln.has_a) na[k] = ld_stream(in);
-                    if (ln.has_b) nb[k] = ld_stream(in + vd);
-                    if (norm) {
-                        if (ln.has_a) ma[k] = ld_stream(xin);
-                        if (ln.has_b) mb[k] = ld_stream(xin + vd);
-                        nr[k] = __ldg(rstd + h + k);
-                    }
+        uint32_t put = 0, take = 0;
+        int ahead = 0;
+        auto fetch = [&]() {
+            if (ahead < u.n) {
+                if (ln.has_a) copy16(slot0 + put, in);
+                if (ln.has_b) copy16(slot0 + put + 4096, in + vd);
+                if (norm) {
+                    if (ln.has_a) copy16(slot0 + put + 8192, xin);
+                    if (ln.has_b) copy16(slot0 + put + 12288, xin + vd);
                 }
                 in += sg.in.sh;
                 xin += sg.x.sh;
             }
+            ++ahead;
+            copies_commit();
+            put = put == (S - 1) * NV * 4096 ? 0 : put + NV * 4096;
         };
-        fetch(0);
+#pragma unroll
+        for (int k = 0; k < S; ++k) fetch();
+        float r_next = norm && u.n > 0 ? __ldg(rstd) : 0.f;
         if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
-        for (int h = 0; h < per; h += A) {
-            uint4 ga[A], gb[A], xa[A], xb[A];
-            float rs[A];
-#pragma unroll
-            for (int k = 0; k < A; ++k) ga[k] = na[k], gb[k] = nb[k], xa[k] = ma[k], xb[k] = mb[k], rs[k] = nr[k];
-            if (h + A < per) fetch(h + A);
-#pragma unroll
-            for (int k = 0; k < A; ++k) {
-                f2 ta[H], tb[H];
-                unpack2<DT>(ga[k], ta);
-                unpack2<DT>(gb[k], tb);
-                ln.template turned<-1>(p, g, ta, tb, row);
+        for (int h = 0; h < per; ++h) {
+            const bool live = h < u.n;
+            const float r = r_next;
+            r_next = norm && h + 1 < u.n ? __ldg(rstd + h + 1) : 0.f;
+            copies_wait<S - 1>();
+            uint4 ga = zero4, gb = zero4, xa = zero4, xb = zero4;
+            if (live) {
+                ga = *reinterpret_cast<const uint4*>(slots + take);
+                gb = *reinterpret_cast<const uint4*>(slots + take + 4096);
                 if (norm) {
-                    f2 x[H], z[H], c2 = 0;
-                    unpack2<DT>(xa[k], x);
-                    unpack2<DT>(xb[k], z);
-                    const f2 r2 = f2_dup(rs[k]);
-#pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        const f2 gx = f2_mul(ta[e], x[e]), gz = f2_mul(tb[e], z[e]);
-                        da[e] = f2_fma(gx, r2, da[e]);
-                        db[e] = f2_fma(gz, r2, db[e]);
-                        c2 = f2_fma(gz, wb[e], f2_fma(gx, wa[e], c2));
-                    }
-                    const float c = lanes_sum(f2_sum(c2), g.L);
-                    const f2 mf = f2_dup(-(rs[k] * rs[k] * rs[k] * (c * g.inv_d)));
-#pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
-                        tb[e] = f2_fma(f2_mul(tb[e], r2), wb[e], f2_mul(z[e], mf));
-                    }
+                    xa = *reinterpret_cast<const uint4*>(slots + take + 8192);
+                    xb = *reinterpret_cast<const uint4*>(slots + take + 12288);
                 }
-                if (h + k < u.n) {
-                    if (ln.has_a) st_stream(out, pack2<DT>(ta));
-                    if (ln.has_b) st_stream(out + vd, pack2<DT>(tb));
-                }
-                out += sg.out.sh;
             }
+            take = take == (S - 1) * NV * 4096 ? 0 : take + NV * 4096;
+            fetch();
+            f2 ta[H], tb[H];
+            unpack2<DT>(ga, ta);
+            unpack2<DT>(gb, tb);
+            ln.template turned<-1>(p, g, ta, tb, row);
+            if (norm) {
+                f2 x[H], z[H], c2 = 0;
+                unpack2<DT>(xa, x);
+                unpack2<DT>(xb, z);
+                const f2 r2 = f2_dup(r);
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const f2 gx = f2_mul(ta[e], x[e]), gz = f2_mul(tb[e], z[e]);
+                    da[e] = f2_fma(gx, r2, da[e]);
+                    db[e] = f2_fma(gz, r2, db[e]);
+                    c2 = f2_fma(gz, wb[e], f2_fma(gx, wa[e], c2));
+                }
+                const float c = lanes_sum(f2_sum(c2), g.L);
+                const f2 mf = f2_dup(-(r * r * r * (c * g.inv_d)));
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
+                    tb[e] = f2_fma(f2_mul(tb[e], r2), wb[e], f2_mul(z[e], mf));
+                }
+            }
+            if (live) {
+                if (ln.has_a) st_stream(out, pack2<DT>(ta));
+                if (ln.has_b) st_stream(out + vd, pack2<DT>(tb));
+            }
+            out += sg.out.sh;
         }
     }
+    copies_wait<0>();
     pdl_launch_dependents();
     if (!norm) return;
     // A warp's teams meet by shuffles, the warps in order in shared memory:
@@ -418,8 +457,8 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
 #pragma unroll
         for (int k = 0; k < 8; ++k) t += rows[k * g.L * 2 * E + i];
         const int li = i / (2 * E), e = i % (2 * E);
-        int a = 2 * li, b = a + 1;
-        if (LAYOUT == kHalves && li < g.pairs) a = li, b = li + g.pairs;
+        int a, b;
+        lane_vectors<LAYOUT>(g, li, a, b);
         const int j = e < E ? a * E + e : b * E + e - E;
         if (j < p.D) p.ws[(which ? g.ctas[0] + cta : cta) * p.D + j] = t;
     }
@@ -560,8 +599,8 @@ __global__ void __launch_bounds__(256) rope_bwd_generic_kernel(const RopeP p) {
 struct RopeRows {
     int64_t n[2];
 };
-__global__ void __launch_bounds__(256) rope_dw_kernel(const RopeP p, RopeRows rows, int paired) {
-    __shared__ float part[8][33];
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const RopeP p, RopeRows rows, int paired) {
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = p.R / 2;
     const int slot = static_cast<int>(blockIdx.x) * 32 + lane;
     pdl_wait();
@@ -571,21 +610,21 @@ __global__ void __launch_bounds__(256) rope_dw_kernel(const RopeP p, RopeRows ro
         const float* q = p.ws + (blockIdx.y ? rows.n[0] : 0) * p.D + slot;
         const int64_t n = rows.n[blockIdx.y];
         int64_t i = w;
-        for (; i + 24 < n; i += 32) {
-            const float a = q[i * p.D], b = q[(i + 8) * p.D], c = q[(i + 16) * p.D], d = q[(i + 24) * p.D];
-            t += a;
-            t += b;
-            t += c;
-            t += d;
+        for (; i + 7 * 32 < n; i += 8 * 32) {  // eight loads, then the additions in order
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = q[(i + 32 * k) * p.D];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t += v[k];
         }
-        for (; i < n; i += 8) t += q[i * p.D];
+        for (; i < n; i += 32) t += q[i * p.D];
     }
     part[w][lane] = t;
     __syncthreads();
     if (w == 0 && slot < p.D) {
         t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t += part[k][lane];
+        for (int k = 0; k < 32; ++k) t += part[k][lane];
         const int j = !paired || !p.interleaved || slot >= p.R ? slot
                       : slot < half ? 2 * slot : 2 * (slot - half) + 1;
         p.seg[blockIdx.y].dw[j] = t;
@@ -621,12 +660,30 @@ int layout_of(const RopeP& p) {
     return p.interleaved ? kInterleaved : p.R % (2 * vec_elems(p.dtype)) == 0 ? kHalves : kExchange;
 }
 
+// Opts a kernel into `smem` bytes on the current device, once; the CTAs per SM.
+int opt_in_occupancy(const void* fn, int threads, int smem) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, int> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    {
+        std::lock_guard<std::mutex> guard(mu);
+        int& have = done[{dev, fn}];
+        if (have < smem) {
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+            have = smem;
+        }
+    }
+    return occupancy(fn, threads, smem);
+}
+
 // Lays out the units: lanes per head, heads per unit, CTAs; strides in vectors.
-RopeUnits units_of(RopeP* p, const OpCfg& c, int ctas_per_sm) {
+RopeUnits units_of(RopeP* p, const OpCfg& c, int threads, int ctas_per_sm) {
     const int E = vec_elems(p->dtype);
     for (RopeSeg& s : p->seg)
         for (HeadsP* h : {&s.in, &s.out, &s.x}) h->sb /= E, h->st /= E, h->sh /= E;
     RopeUnits g;
+    g.slots_at = 0;
     g.nv = p->D / E;
     g.inv_d = 1.f / static_cast<float>(p->D);
     g.pairs = layout_of(*p) == kHalves ? p->R / (2 * E) : 0;
@@ -636,7 +693,7 @@ RopeUnits units_of(RopeP* p, const OpCfg& c, int ctas_per_sm) {
         g.L <<= 1;
         ++g.log2L;
     }
-    const int64_t teams = 256 / g.L, tokens = p->batch * p->seq;
+    const int64_t teams = threads / g.L, tokens = p->batch * p->seq;
     int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas_per_sm;
     if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(c.max_ctas, 2));
     // Units of as many heads as leave every team about eight units, so that the
@@ -670,16 +727,20 @@ RopeUnits units_of(RopeP* p, const OpCfg& c, int ctas_per_sm) {
 template <int DT, int LAYOUT, bool NORM>
 cudaError_t fwd_units(RopeP p, const OpCfg& c) {
     auto fn = rope_fwd_kernel<DT, LAYOUT, NORM>;
-    const int smem = LAYOUT == kExchange ? 256 * 2 * VecElems<DT>::value * 4 : 0;  // at most
-    const int occ = std::max(1, occupancy(reinterpret_cast<const void*>(fn), 256, smem));
-    const RopeUnits g = units_of(&p, c, occ);
-    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, LAYOUT == kExchange ? (256 >> g.log2L) * p.D * 4 : 0, p, g);
+    // Heads to exchange, behind them the copies.
+    const int at = LAYOUT == kExchange ? 256 * 2 * VecElems<DT>::value * 4 : 0;
+    const int smem = at + 2 * kAhead * 4096;
+    const int occ = opt_in_occupancy(reinterpret_cast<const void*>(fn), 256, smem);
+    if (occ < 1) return cudaErrorInvalidConfiguration;
+    RopeUnits g = units_of(&p, c, 256, occ);
+    g.slots_at = at;
+    return op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g);
 }
 
 cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t rows_k, int paired) {
     Launch l;
     l.grid = (p.D + 31) / 32;
-    l.threads = 256;
+    l.threads = 1024;
     LaunchCfg cfg(l, c.stream, c.pdl);
     cfg.cfg.gridDim.y = 2;
     return cudaLaunchKernelEx(&cfg.cfg, rope_dw_kernel, p, RopeRows{{rows_q, rows_k}}, paired);
@@ -689,11 +750,14 @@ template <int DT, int LAYOUT, bool NORM>
 cudaError_t bwd_units(RopeP p, const OpCfg& c) {
     constexpr int E = VecElems<DT>::value;
     auto fn = rope_bwd_kernel<DT, LAYOUT, NORM>;
-    const int smem = LAYOUT == kExchange ? 256 * 2 * E * 4 : 0;  // at most
-    const int occ = std::max(1, std::min(8, occupancy(reinterpret_cast<const void*>(fn), 256, smem)));
-    const RopeUnits g = units_of(&p, c, occ);
-    const int bytes = std::max(LAYOUT == kExchange ? (256 >> g.log2L) * p.D * 4 : 0, NORM ? 8 * g.L * 2 * E * 4 : 0);
-    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, bytes, p, g);
+    // Heads to exchange, then the sums over the warps; behind them the copies.
+    const int at = LAYOUT == kExchange || NORM ? 256 * 2 * E * 4 : 0;
+    const int smem = at + (NORM ? 4 : 2) * kAhead * 4096;
+    const int occ = std::min(8, opt_in_occupancy(reinterpret_cast<const void*>(fn), 256, smem));
+    if (occ < 1) return cudaErrorInvalidConfiguration;
+    RopeUnits g = units_of(&p, c, 256, occ);
+    g.slots_at = at;
+    const cudaError_t e = op_launch(c, fn, g.ctas[0] + g.ctas[1], 256, smem, p, g);
     return e != cudaSuccess || !NORM ? e : launch_dw(p, c, g.ctas[0], g.ctas[1], 0);
 }
 
