@@ -72,12 +72,13 @@ __device__ __forceinline__ int64_t cache_head(const CacheP& p, int64_t slot, int
     return (page * p.heads + h) * p.page_size + (slot - page * p.page_size);
 }
 
-// The sequence whose rows hold row i: the last b with cu_rows[b] <= i.
-__device__ __forceinline__ int64_t sequence_of(const CacheP& p, int64_t i) {
+// The sequence whose rows hold row i: the last b with cu[b] <= i. cu is cu_rows
+// or a copy of it.
+__device__ __forceinline__ int64_t sequence_of(const CacheP& p, const int32_t* cu, int64_t i) {
     int64_t lo = 0, hi = p.sequences - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) >> 1;
-        if (p.cu_rows[mid] <= i) lo = mid;
+        if (cu[mid] <= i) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -85,10 +86,10 @@ __device__ __forceinline__ int64_t sequence_of(const CacheP& p, int64_t i) {
 
 // The slot of row i: -1 for a row behind the last sequence, -2 for one whose
 // page is not there.
-__device__ __forceinline__ int64_t read_slot(const CacheP& p, int64_t i) {
-    if (p.sequences <= 0 || i >= p.cu_rows[p.sequences]) return -1;
-    const int64_t b = sequence_of(p, i);
-    const int64_t pos = i - p.cu_rows[b] + (p.starts ? p.starts[b] : 0);
+__device__ __forceinline__ int64_t read_slot(const CacheP& p, const int32_t* cu, int64_t i) {
+    if (p.sequences <= 0 || i >= cu[p.sequences]) return -1;
+    const int64_t b = sequence_of(p, cu, i);
+    const int64_t pos = i - cu[b] + (p.starts ? p.starts[b] : 0);
     if (pos < 0) return -2;
     const int64_t col = pos / p.page_size;
     if (col >= p.table_width) return -2;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(256) cache_read_generic_kernel(const CacheP p)
         const int64_t i = u / (p.heads * p.groups);
         const int rest = static_cast<int>(u - i * (p.heads * p.groups));
         const int h = rest / p.groups, g = rest - h * p.groups;
-        const int64_t slot = read_slot(p, i);
+        const int64_t slot = read_slot(p, p.cu_rows, i);
         if (slot == -1) continue;
         if (slot < 0 && rest == 0) atomicOr(&g_cache_status, 1u);
         const int64_t head = slot < 0 ? 0 : cache_head(p, slot, h);
@@ -180,145 +181,251 @@ __global__ void __launch_bounds__(256) cache_read_generic_kernel(const CacheP p)
     }
 }
 
-// Vector kernels: groups of 32 values as 16-byte vectors. A thread takes 16
-// values: half a group, whose other half is the neighbouring lane's, and one
-// 16-byte (E4M3) or 8-byte (E2M1) piece of codes. Consecutive threads take
-// consecutive halves of k's token, then of v's. Bound by HBM: each value read
-// and each code written once, or the other way round.
+// Vector kernels. A piece is 16 values: half a group, whose other half is the
+// neighbouring lane's, and one 16-byte (E4M3) or 8-byte (E2M1) run of codes. A CTA
+// takes tokens in tiles; a token's slot is looked up once, by one thread, a tile
+// ahead, and shared; then consecutive threads take consecutive pieces of k's and
+// v's heads. Where a token's pieces divide the CTA's
+// threads, a thread's head and place in it never change. Bound by HBM: each value
+// read and each code written once, or the other way round; so the arithmetic is on
+// pairs (f32x2), 16-bit magnitudes are compared two at a time, and there is no
+// division in the loops (with those it was bound by instructions: a write of 32768
+// tokens 45 us, a read of 134k rows 200 us; now 34 and 146). Pieces in flight per
+// thread, GB300, us: write of 32768 tokens at 1 / 2 / 4: 34.3 / 33.8 / 35.7; read of
+// 134k rows 146 / 159 / 161.
+constexpr int kTileTokens = 64;   // most tokens of a tile
+constexpr int kWriteBatch = 2;    // pieces of a thread in flight
+constexpr int kSharedRows = 2048; // sequences whose first rows fit into shared memory
 
-// The largest magnitude of 16 values, as fp32 bits.
-__device__ __forceinline__ uint32_t amax16(const float* f) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
-        m = b > m ? b : m;
+// How a tile's pieces go round the CTA's threads.
+struct Pieces {
+    int tensors, first;       // 1 or 2, and which one where it is one
+    int halves, head_halves;  // pieces of a token's heads of one tensor, of a head
+    int tile;                 // tokens per tile
+    int64_t tiles;
+};
+
+// A thread's way through a tile: token, tensor, head and part, going up by the CTA's
+// 256 threads.
+struct PieceWay {
+    int per, dt, dp;   // pieces of a token; 256 over that, and the remainder
+    int t0, p0;
+    int t, p;          // token of the tile, piece of the token
+    int k, h, part;
+    __device__ __forceinline__ void set(const Pieces& g) {
+        const int q = p / g.halves, i = p - q * g.halves;
+        k = g.tensors == 2 ? q : g.first;
+        h = i / g.head_halves;
+        part = i - h * g.head_halves;
     }
-    return m;
-}
-
-// `halves`: 16-value pieces of a token's heads of one tensor; units = T * tensors * halves.
-template <int DT, int F>
-__global__ void __launch_bounds__(256) cache_write_kernel(const CacheP p, int tensors, int halves, int head_halves) {
-    constexpr int E = VecElems<DT>::value, NV = 16 / E;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t units = p.T * tensors * halves;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    // whole warps stay together: the two halves of a group are neighbouring lanes
-    for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; u0 < units; u0 += step) {
-        const int64_t u = u0 + threadIdx.x;
-        const int64_t tk = u / halves;
-        const int i = static_cast<int>(u - tk * halves);
-        const int64_t t = tensors == 2 ? tk >> 1 : tk;
-        const int k = tensors == 2 ? static_cast<int>(tk & 1) : 0;
-        const int h = i / head_halves, part = i - h * head_halves;
-        const int64_t slot = u < units ? __ldg(p.slot + t) : -1;
-        const bool in = slot >= 0 && slot < p.slots;
-        if (slot >= p.slots && i == 0 && k == 0) atomicOr(&g_cache_status, 1u);
-        float f[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) f[q] = 0.f;
-        if (in) {
-            const uint4* x = static_cast<const uint4*>(p.t[k].p) + t * p.t[k].st + h * p.t[k].sh + part * NV;
-            uint4 v[NV];
-#pragma unroll
-            for (int q = 0; q < NV; ++q) v[q] = ld_stream(x + q);
-#pragma unroll
-            for (int q = 0; q < NV; ++q) unpack_vec<DT>(v[q], f + q * E);
-        }
-        uint32_t amax = amax16(f);
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, amax, 1);
-        amax = other > amax ? other : amax;
-        const uint32_t byte = scale_byte<F>(amax);
-        const float inv = inverse_scale(byte);
-        if (!in) continue;
-        const int64_t head = cache_head(p, slot, h);
-        if ((part & 1) == 0) p.scales[k][head * p.groups + (part >> 1)] = static_cast<uint8_t>(byte);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) f[q] = byte == 255u ? 0.f : f[q] * inv;
-        if (F == RMSNORM_CACHE_E4M3) {
-            uint32_t c[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                c[q] = to_e4m3x2(f[4 * q], f[4 * q + 1]) | to_e4m3x2(f[4 * q + 2], f[4 * q + 3]) << 16;
-            *reinterpret_cast<uint4*>(p.codes[k] + head * p.code_bytes + part * 16) =
-                make_uint4(c[0], c[1], c[2], c[3]);
-        } else {
-            uint32_t c[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                c[q] = to_e2m1x2(f[8 * q], f[8 * q + 1]) | to_e2m1x2(f[8 * q + 2], f[8 * q + 3]) << 8 |
-                       to_e2m1x2(f[8 * q + 4], f[8 * q + 5]) << 16 | to_e2m1x2(f[8 * q + 6], f[8 * q + 7]) << 24;
-            *reinterpret_cast<uint2*>(p.codes[k] + head * p.code_bytes + part * 8) = make_uint2(c[0], c[1]);
+    __device__ __forceinline__ explicit PieceWay(const Pieces& g) {
+        per = g.tensors * g.halves;
+        dt = 256 / per;
+        dp = 256 - dt * per;
+        t0 = threadIdx.x / per;
+        p0 = threadIdx.x - t0 * per;
+        t = t0;
+        p = p0;
+        set(g);
+    }
+    __device__ __forceinline__ void restart(const Pieces& g) {
+        t = t0;
+        if (dp != 0) {
+            p = p0;
+            set(g);
         }
     }
+    __device__ __forceinline__ void go(const Pieces& g) {
+        t += dt;
+        if (dp != 0) {
+            p += dp;
+            if (p >= per) {
+                p -= per;
+                ++t;
+            }
+            set(g);
+        }
+    }
+};
+
+// Index of a slot's head 0 among the cache's heads; head h is h * stride further.
+__device__ __forceinline__ int64_t first_head(const CacheP& p, int64_t slot) {
+    if (!p.heads_first) return slot * p.heads;
+    const int64_t page = slot / p.page_size;
+    return page * p.heads * p.page_size + (slot - page * p.page_size);
 }
 
-// A CTA takes rows of the outputs in tiles: a row's slot is looked up once, by one
-// thread, and shared; then the threads take the tile's 16-value pieces.
-constexpr int kReadRows = 64;  // most rows of a tile
+// The largest magnitude of a lane's 16 values as fp32 bits. 16-bit values are
+// compared by their bits, two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t amax16(const uint4* v) {
+    if constexpr (DT == kFP32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            m = max(m, max(v[q].x & 0x7fffffffu, v[q].y & 0x7fffffffu));
+            m = max(m, max(v[q].z & 0x7fffffffu, v[q].w & 0x7fffffffu));
+        }
+        return m;
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            m = __vmaxu2(m, __vmaxu2(v[q].x & 0x7fff7fffu, v[q].y & 0x7fff7fffu));
+            m = __vmaxu2(m, __vmaxu2(v[q].z & 0x7fff7fffu, v[q].w & 0x7fff7fffu));
+        }
+        const uint32_t top = max(m & 0xffffu, m >> 16);
+        return __float_as_uint(Codec<DT>::unpack1(static_cast<uint16_t>(top)));
+    }
+}
 
 template <int DT, int F>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheP p, int tensors, int first, int halves,
-                                                         int head_halves, int tile_rows) {
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheP p, const Pieces g) {
     constexpr int E = VecElems<DT>::value, NV = 16 / E;
-    __shared__ int64_t slots[kReadRows];
+    __shared__ int64_t heads_of[2][kTileTokens];  // -1: no slot
+    const int64_t head_stride = p.heads_first ? p.page_size : 1;
+    PieceWay way(g);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t tiles = (p.rows + tile_rows - 1) / tile_rows;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t row0 = tile * tile_rows;
-        const int n = static_cast<int>(min(static_cast<int64_t>(tile_rows), p.rows - row0));
-        __syncthreads();  // the slots of the tile before are read
-        if (threadIdx.x < n) {
-            const int64_t slot = read_slot(p, row0 + threadIdx.x);
-            if (slot == -2) atomicOr(&g_cache_status, 1u);
-            slots[threadIdx.x] = slot;
+    auto lookup = [&](int64_t tile) -> int64_t {
+        const int64_t t = tile * g.tile + threadIdx.x;
+        if (threadIdx.x >= g.tile || t >= p.T) return -1;
+        const int64_t slot = __ldg(p.slot + t);
+        if (slot < 0) return -1;
+        if (slot >= p.slots) {
+            atomicOr(&g_cache_status, 1u);
+            return -1;
         }
-        __syncthreads();
-        const int units = n * tensors * halves;
-#pragma unroll 2
-        for (int u = threadIdx.x; u < units; u += 256) {
-            const int rk = u / halves, i = u - rk * halves;
-            const int row = tensors == 2 ? rk >> 1 : rk;
-            const int k = tensors == 2 ? rk & 1 : first;
-            const int64_t slot = slots[row];
-            if (slot == -1) continue;
-            const int h = i / head_halves, part = i - h * head_halves;
-            uint4* y = static_cast<uint4*>(p.t[k].p) + (row0 + row) * p.t[k].st + h * p.t[k].sh + part * NV;
-            float f[16];
-            if (slot < 0) {
+        return first_head(p, slot);
+    };
+    int64_t found = lookup(blockIdx.x);
+    int buffer = 0;
+    for (int64_t tile = blockIdx.x; tile < g.tiles; tile += gridDim.x, buffer ^= 1) {
+        if (threadIdx.x < g.tile) heads_of[buffer][threadIdx.x] = found;
+        __syncthreads();  // the other buffer is free behind the next tile's barrier
+        found = lookup(tile + gridDim.x);
+        const int64_t t0 = tile * g.tile;
+        const int n = static_cast<int>(min(static_cast<int64_t>(g.tile), p.T - t0));
+        const int units = n * way.per;
+        way.restart(g);
+        for (int u = 0; u < units; u += 256 * kWriteBatch) {
+            uint4 v[kWriteBatch][NV];
+            int64_t head[kWriteBatch];
+            int k[kWriteBatch], part[kWriteBatch];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) f[q] = 0.f;
-            } else {
-                const int64_t head = cache_head(p, slot, h);
-                const float scale = scale_of(__ldg(p.scales[k] + head * p.groups + (part >> 1)));
-                if (F == RMSNORM_CACHE_E4M3) {
-                    const uint4 c = ld_stream(
-                        reinterpret_cast<const uint4*>(p.codes[k] + head * p.code_bytes + part * 16));
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            for (int b = 0; b < kWriteBatch; ++b) {
+                head[b] = way.t < n ? heads_of[buffer][way.t] : -1;
+                k[b] = way.k;
+                part[b] = way.part;
+                if (head[b] >= 0) {
+                    head[b] += way.h * head_stride;
+                    const uint4* x = static_cast<const uint4*>(p.t[way.k].p) + (t0 + way.t) * p.t[way.k].st +
+                                     way.h * p.t[way.k].sh + way.part * NV;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 a = from_e4m3x2(w[q] & 0xffffu), b = from_e4m3x2(w[q] >> 16);
-                        f[4 * q] = a.x * scale;
-                        f[4 * q + 1] = a.y * scale;
-                        f[4 * q + 2] = b.x * scale;
-                        f[4 * q + 3] = b.y * scale;
-                    }
+                    for (int q = 0; q < NV; ++q) v[b][q] = ld_stream(x + q);
                 } else {
-                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(p.codes[k] + head * p.code_bytes + part * 8));
-                    const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float2 a = from_e2m1x2((w[q >> 2] >> (8 * (q & 3))) & 0xffu);
-                        f[2 * q] = a.x * scale;
-                        f[2 * q + 1] = a.y * scale;
-                    }
+                    for (int q = 0; q < NV; ++q) v[b][q] = make_uint4(0u, 0u, 0u, 0u);
                 }
+                way.go(g);
             }
 #pragma unroll
-            for (int q = 0; q < NV; ++q) st_stream(y + q, pack_vec<DT>(f + q * E));
+            for (int b = 0; b < kWriteBatch; ++b) {
+                uint32_t amax = amax16<DT>(v[b]);
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                if (head[b] < 0) continue;
+                const uint32_t byte = scale_byte<F>(amax);
+                const f2 inv = f2_dup(inverse_scale(byte));
+                f2 f[8];
+#pragma unroll
+                for (int q = 0; q < NV; ++q) unpack2<DT>(v[b][q], f + q * (E / 2));
+                uint32_t c[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float2 y = f2_get(f2_mul(f[q], inv));
+                    c[q] = F == RMSNORM_CACHE_E4M3 ? to_e4m3x2(y.x, y.y) : to_e2m1x2(y.x, y.y);
+                }
+                uint8_t* codes = p.codes[k[b]] + head[b] * p.code_bytes;
+                const bool bad = byte == 255u;
+                if (F == RMSNORM_CACHE_E4M3) {
+                    const uint32_t w0 = c[0] | c[1] << 16, w1 = c[2] | c[3] << 16;
+                    const uint32_t w2 = c[4] | c[5] << 16, w3 = c[6] | c[7] << 16;
+                    *reinterpret_cast<uint4*>(codes + part[b] * 16) =
+                        make_uint4(bad ? 0u : w0, bad ? 0u : w1, bad ? 0u : w2, bad ? 0u : w3);
+                } else {
+                    const uint32_t w0 = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+                    const uint32_t w1 = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+                    *reinterpret_cast<uint2*>(codes + part[b] * 8) = make_uint2(bad ? 0u : w0, bad ? 0u : w1);
+                }
+                if ((part[b] & 1) == 0)
+                    p.scales[k[b]][head[b] * p.groups + (part[b] >> 1)] = static_cast<uint8_t>(byte);
+            }
+        }
+    }
+}
+
+template <int DT, int F>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheP p, const Pieces g) {
+    constexpr int E = VecElems<DT>::value, NV = 16 / E;
+    __shared__ int64_t heads_of[2][kTileTokens];  // -1: not a row, -2: zeros
+    __shared__ int32_t first_rows[kSharedRows + 1];
+    const int64_t head_stride = p.heads_first ? p.page_size : 1;
+    PieceWay way(g);
+    pdl_wait();
+    pdl_launch_dependents();
+    const bool shared_rows = p.sequences <= kSharedRows;
+    if (shared_rows) {
+        for (int i = threadIdx.x; i <= p.sequences; i += 256) first_rows[i] = p.cu_rows[i];
+        __syncthreads();
+    }
+    const int32_t* cu = shared_rows ? first_rows : p.cu_rows;
+    auto lookup = [&](int64_t tile) -> int64_t {
+        const int64_t i = tile * g.tile + threadIdx.x;
+        if (threadIdx.x >= g.tile || i >= p.rows) return -1;
+        const int64_t slot = read_slot(p, cu, i);
+        if (slot == -2) atomicOr(&g_cache_status, 1u);
+        return slot < 0 ? slot : first_head(p, slot);
+    };
+    int64_t found = lookup(blockIdx.x);
+    int buffer = 0;
+    for (int64_t tile = blockIdx.x; tile < g.tiles; tile += gridDim.x, buffer ^= 1) {
+        if (threadIdx.x < g.tile) heads_of[buffer][threadIdx.x] = found;
+        __syncthreads();  // the other buffer is free behind the next tile's barrier
+        found = tile + gridDim.x < g.tiles ? lookup(tile + gridDim.x) : -1;
+        const int64_t row0 = tile * g.tile;
+        const int n = static_cast<int>(min(static_cast<int64_t>(g.tile), p.rows - row0));
+        const int units = n * way.per;
+        way.restart(g);
+        for (int u = 0; u < units; u += 256, way.go(g)) {
+            const int64_t base = way.t < n ? heads_of[buffer][way.t] : -1;
+            if (base == -1) continue;
+            uint4 c = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t byte = 0;
+            if (base >= 0) {
+                const int64_t head = base + way.h * head_stride;
+                const uint8_t* codes = p.codes[way.k] + head * p.code_bytes;
+                if (F == RMSNORM_CACHE_E4M3) {
+                    c = ld_stream(reinterpret_cast<const uint4*>(codes + way.part * 16));
+                } else {
+                    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(codes + way.part * 8));
+                    c.x = w.x;
+                    c.y = w.y;
+                }
+                byte = __ldg(p.scales[way.k] + head * p.groups + (way.part >> 1));
+            }
+            const f2 scale = f2_dup(scale_of(byte));
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            f2 f[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float2 a = F == RMSNORM_CACHE_E4M3 ? from_e4m3x2((w[q >> 1] >> (16 * (q & 1))) & 0xffffu)
+                                                         : from_e2m1x2((w[q >> 2] >> (8 * (q & 3))) & 0xffu);
+                f[q] = f2_mul(f2_make(a.x, a.y), scale);
+            }
+            uint4* y = static_cast<uint4*>(p.t[way.k].p) + (row0 + way.t) * p.t[way.k].st + way.h * p.t[way.k].sh +
+                       way.part * NV;
+#pragma unroll
+            for (int q = 0; q < NV; ++q) st_stream(y + q, pack2<DT>(f + q * (E / 2)));
         }
     }
 }
@@ -335,29 +442,32 @@ bool vectors(bool write, const CacheP& p) {
             (reinterpret_cast<uintptr_t>(p.codes[k]) & to))
             return false;
     }
-    return static_cast<int64_t>(p.heads) * p.D / 16 * 2 * kReadRows < (int64_t(1) << 31);
+    return static_cast<int64_t>(p.heads) * p.D / 16 * 2 * kTileTokens < (int64_t(1) << 30);
 }
 
 template <int DT, int F>
 cudaError_t run_vector(bool write, CacheP p, const OpCfg& c) {
     const int E = VecElems<DT>::value;
-    const int head_halves = p.D / 16, halves = p.heads * head_halves;
     for (int k = 0; k < 2; ++k) {
         p.t[k].st /= E;
         p.t[k].sh /= E;
     }
-    const int tensors = (p.t[0].p ? 1 : 0) + (p.t[1].p ? 1 : 0);
-    if (write) {
-        const int64_t G = persistent_grid(p.T * tensors * halves, 256, c.dev.sm_count, 8, c.max_ctas);
-        return op_launch(c, cache_write_kernel<DT, F>, G, 256, 0, p, tensors, halves, head_halves);
-    }
-    // About eight pieces per thread and tile, fewer where rows are few.
-    int64_t tile = std::max<int64_t>(1, 8 * 256 / (tensors * halves));
-    tile = std::min<int64_t>(tile, std::max<int64_t>(1, p.rows / (2 * c.dev.sm_count)));
-    tile = std::min<int64_t>(tile, kReadRows);
-    const int64_t G = persistent_grid((p.rows + tile - 1) / tile, 1, c.dev.sm_count, 8, c.max_ctas);
-    return op_launch(c, cache_read_kernel<DT, F>, G, 256, 0, p, tensors, p.t[0].p ? 0 : 1, halves, head_halves,
-                     static_cast<int>(tile));
+    Pieces g;
+    g.tensors = (p.t[0].p ? 1 : 0) + (p.t[1].p ? 1 : 0);
+    g.first = p.t[0].p ? 0 : 1;
+    g.head_halves = p.D / 16;
+    g.halves = p.heads * g.head_halves;
+    auto fn = write ? cache_write_kernel<DT, F> : cache_read_kernel<DT, F>;
+    const int occ = std::max(1, occupancy(reinterpret_cast<const void*>(fn), 256, 0));
+    const int64_t rows = write ? p.T : p.rows;
+    const int per = g.tensors * g.halves;
+    // Four pieces per thread and tile, fewer where tokens are few.
+    int64_t tile = std::max<int64_t>(1, 4 * 256 / per);
+    tile = std::min<int64_t>(tile, std::max<int64_t>(1, rows / c.dev.sm_count));
+    g.tile = static_cast<int>(std::min<int64_t>(tile, kTileTokens));
+    g.tiles = (rows + g.tile - 1) / g.tile;
+    const int64_t G = persistent_grid(g.tiles, 1, c.dev.sm_count, occ, c.max_ctas);
+    return op_launch(c, fn, G, 256, 0, p, g);
 }
 
 template <int DT, int F>
