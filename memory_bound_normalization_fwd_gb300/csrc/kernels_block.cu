@@ -268,7 +268,7 @@ bool vectors(const BlockP& p) {
     return true;
 }
 
-// Element-wise kernel: any N, alignment and stride. One CTA per row, three
+// Element-wise kernel for rows that no other takes: one CTA per row, three
 // passes over the row's columns (sum of h^2; sum of s^2 over s recomputed from
 // h and r; s again, stored, and y), the later ones from L1/L2. A thread reads
 // a column of h and r and then writes it, and no other pass follows, so s and
@@ -320,6 +320,71 @@ __global__ void __launch_bounds__(512) block_fwd_generic_kernel(const BlockP p) 
     }
 }
 
+// Rows that are not whole vectors (any N, stride and alignment), of up to 1024 V
+// columns: a CTA per row, element loads, a thread's columns t, t + T, ... kept in
+// registers between the reductions, so that h and r are read once.
+template <int DT, int V>
+__global__ void __launch_bounds__(1024) block_fwd_columns_kernel(const BlockP p) {
+    __shared__ float part[2 * 32];
+    int parity = 0;
+    const int t = threadIdx.x, T = blockDim.x, N = static_cast<int>(p.N);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+        float f[V], r[V], w[V], ss[1] = {0.f};
+        load_columns<DT, V>(p.h, row * p.ldh, t, T, N, f);
+        load_columns<DT, V>(p.r, row * p.ldr, t, T, N, r);
+        float a = 1.f;
+        if (p.w_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) ss[0] = fmaf(f[v], f[v], ss[0]);
+            block_sums<1>(ss, part, parity);
+            a = row_rstd(ss[0], p.n, p.eps);
+            if (t == 0 && p.rstd_post) p.rstd_post[row] = a;
+            ss[0] = 0.f;
+            load_columns<DT, V>(p.w_post, 0, t, T, N, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = f[v] * a * (p.alpha * (p.offset + w[v]));
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] *= p.alpha;
+        }
+        if (p.gate) {
+            load_columns<DT, V>(p.gate, row / p.gate_rows * p.ldg, t, T, N, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] *= w[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int j = v * T + t;
+            f[v] = fmaf(p.beta, r[v], f[v]);
+            if (j < N) {
+                store1<DT>(p.s, row * p.lds + j, f[v]);
+                ss[0] = fmaf(f[v], f[v], ss[0]);
+            }
+        }
+        if (p.w_pre) {
+            load_columns<DT, V>(p.w_pre, 0, t, T, N, w);
+            block_sums<1>(ss, part, parity);
+            const float b = row_rstd(ss[0], p.n, p.eps);
+            if (t == 0 && p.rstd_pre) p.rstd_pre[row] = b;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = v * T + t;
+                if (j < N) store1<DT>(p.y, row * p.ldy + j, f[v] * b * (p.offset + w[v]));
+            }
+        }
+    }
+}
+
+template <int DT, int V>
+cudaError_t launch_columns(const BlockP& p, const OpCfg& c) {
+    auto fn = block_fwd_columns_kernel<DT, V>;
+    const int T = static_cast<int>((p.N + V * 32 - 1) / (V * 32)) * 32;
+    const int occ = occupancy(reinterpret_cast<const void*>(fn), T, 0);
+    return op_launch(c, fn, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas), T, 0, p);
+}
+
 template <int DT>
 cudaError_t run(const BlockP& p, const OpCfg& c) {
     if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(p)) {
@@ -330,6 +395,8 @@ cudaError_t run(const BlockP& p, const OpCfg& c) {
         if (taken) return e;
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
+    if (p.N <= 1024 * 4) return launch_columns<DT, 4>(p, c);
+    if (p.N <= 1024 * 8) return launch_columns<DT, 8>(p, c);
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_fwd_generic_kernel<DT>;

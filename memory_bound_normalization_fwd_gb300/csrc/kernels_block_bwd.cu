@@ -216,6 +216,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 }
                 if (has_ds) dsv[v] = lds16(q + ods);
                 if (GATE == 2) gv[v] = lds16(q + og);
+            } else if (V * E > 8) {  // no registers to carry the zeros round the loop
+                hv[v] = sv[v] = gv[v] = dyv[v] = dsv[v] = zero4;
             }
             unpack2<DT>(dsv[v], t0[v]);
             f2 s[H];
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     }
 }
 
-// Element-wise kernel: any N, alignment and stride; a thread owns the columns
+// Element-wise kernel for rows that no other takes; a thread owns the columns
 // tid, tid + T, ... and keeps their sums in the CTA's partial rows.
 template <int DT>
 __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP p, int64_t slots) {
@@ -487,6 +489,165 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
         }
     }
     pdl_launch_dependents();
+}
+
+// Rows that are not whole vectors (any N, stride and alignment), of up to 1024 V
+// columns: a CTA per range of rows, element loads, a thread's columns t, t + T, ...
+// of the row and of the sums in registers (dw_post's with a gate row for several
+// rows in shared memory).
+template <int DT, int V>
+__global__ void __launch_bounds__(1024) block_bwd_columns_kernel(const BlockBwdP p, int64_t slots) {
+    extern __shared__ __align__(16) float post[];  // [V][T]
+    __shared__ float part[2 * 3 * 32];
+    int parity = 0;
+    const int t = threadIdx.x, T = blockDim.x, N = static_cast<int>(p.N);
+    const int64_t G = gridDim.x, b = blockIdx.x, pitch = block_bwd_pitch(p.N);
+    const int64_t r0 = range_begin(b, G, p.M), r1 = range_begin(b + 1, G, p.M);
+    const bool per_element = p.gate && p.gate_rows == 1;
+    const bool grouped = p.gate && !per_element;
+    const float inv_n = 1.f / p.n;
+    pdl_wait();
+    float P[V], pre[V];  // P: sums of t h rstd_post (times the gate where a row has its own)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        P[v] = pre[v] = 0.f;
+        if (grouped) post[v * T + t] = 0.f;
+    }
+    int64_t grow = grouped ? r0 / p.gate_rows : 0;
+    int64_t left = grouped ? (grow + 1) * p.gate_rows - r0 : 0;
+    float k1_next = p.w_post ? __ldg(p.rstd_post + r0) : 1.f;
+    float k2_next = p.w_pre ? __ldg(p.rstd_pre + r0) : 0.f;
+    // alpha gate (offset + w_post) of the thread's columns; `wp` without the gate.
+    auto scales = [&](int64_t row, float (&a)[V], bool with_gate) {
+        if (p.w_post) {
+            load_columns<DT, V>(p.w_post, 0, t, T, N, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] = p.alpha * (p.offset + a[v]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] = p.alpha;
+        }
+        if (with_gate && p.gate) {
+            float q[V];
+            load_columns<DT, V>(p.gate, (per_element ? row : grow) * p.ldg, t, T, N, q);
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] *= q[v];
+        }
+    };
+    for (int64_t row = r0; row < r1; ++row) {
+        const float k1 = k1_next, k2 = k2_next;
+        if (row + 1 < r1) {
+            if (p.w_post) k1_next = __ldg(p.rstd_post + row + 1);
+            if (p.w_pre) k2_next = __ldg(p.rstd_pre + row + 1);
+        }
+        float t0[V], h[V], s[V], a[V], sums[3] = {0.f, 0.f, 0.f};
+        load_columns<DT, V>(p.h, row * p.ldh, t, T, N, h);
+        if (p.ds) {
+            load_columns<DT, V>(p.ds, row * p.ldds, t, T, N, t0);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) t0[v] = 0.f;
+        }
+        if (p.w_pre) {
+            float dy[V];
+            load_columns<DT, V>(p.s, row * p.lds, t, T, N, s);
+            load_columns<DT, V>(p.dy, row * p.lddy, t, T, N, dy);
+            load_columns<DT, V>(p.w_pre, 0, t, T, N, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float u = dy[v] * (p.offset + a[v]);
+                t0[v] = fmaf(k2, u, t0[v]);
+                sums[0] = fmaf(u, s[v], sums[0]);
+                pre[v] = fmaf(dy[v], s[v] * k2, pre[v]);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = 0.f;
+        }
+        scales(row, a, true);
+        if (p.w_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float ah = a[v] * h[v];
+                sums[1] = fmaf(ah, t0[v], sums[1]);
+                sums[2] = fmaf(ah, s[v], sums[2]);
+            }
+        }
+        block_sums<3>(sums, part, parity);
+        const float e = k2 * k2 * k2 * (sums[0] * inv_n);
+        const float f = k1 * k1 * (fmaf(-e, sums[2], sums[1]) * inv_n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int j = v * T + t;
+            t0[v] = fmaf(-e, s[v], t0[v]);
+            s[v] = t0[v] * (h[v] * k1);  // what P sums
+            if (j < N) {
+                store1<DT>(p.dr, row * p.lddr + j, p.beta * t0[v]);
+                store1<DT>(p.dh, row * p.lddh + j, p.w_post ? k1 * fmaf(a[v], t0[v], -h[v] * f) : a[v] * t0[v]);
+            }
+        }
+        if (per_element) {
+            load_columns<DT, V>(p.gate, row * p.ldg, t, T, N, h);
+            scales(row, a, false);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = v * T + t;
+                if (j < N) {
+                    store1<DT>(p.dgate, row * p.lddg + j, a[v] * s[v]);
+                    P[v] = fmaf(s[v], h[v], P[v]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v * T + t < N) P[v] += s[v];
+        }
+        if (grouped && (--left == 0 || row + 1 == r1)) {
+            const int64_t first = grow * p.gate_rows;
+            const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
+            const bool whole = first >= r0 && last <= r1;
+            float* out = partial(p.ws, first > r0 ? 3 : 2, b, slots, pitch);
+            load_columns<DT, V>(p.gate, grow * p.ldg, t, T, N, h);
+            scales(row, a, false);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = v * T + t;
+                if (j < N) {
+                    post[j] = fmaf(P[v], h[v], post[j]);
+                    if (whole) store1<DT>(p.dgate, grow * p.lddg + j, a[v] * P[v]);
+                    else out[j] = P[v];
+                }
+                P[v] = 0.f;
+            }
+            ++grow;
+            left = p.gate_rows;
+        }
+    }
+    pdl_launch_dependents();
+    float* acc_post = partial(p.ws, 0, b, slots, pitch);
+    float* acc_pre = partial(p.ws, 1, b, slots, pitch);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int j = v * T + t;
+        if (j >= N) continue;
+        if (p.w_post) acc_post[j] = p.alpha * (grouped ? post[j] : P[v]);
+        if (p.w_pre) acc_pre[j] = pre[v];
+    }
+}
+
+template <int DT>
+cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G, int64_t R);
+
+template <int DT, int V>
+cudaError_t launch_columns(const BlockBwdP& p, const OpCfg& c) {
+    auto fn = block_bwd_columns_kernel<DT, V>;
+    const int T = static_cast<int>((p.N + V * 32 - 1) / (V * 32)) * 32;
+    const int smem = p.gate && p.gate_rows > 1 ? V * T * 4 : 0;  // at most 32 KB
+    const int occ = occupancy(reinterpret_cast<const void*>(fn), T, smem);
+    const int64_t slots = block_bwd_max_grid(p.M, p.N, c.dev.sm_count);
+    const int64_t G = std::min<int64_t>(slots, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas));
+    const cudaError_t e = op_launch(c, fn, G, T, smem, p, slots);
+    return e != cudaSuccess ? e : finish<DT>(p, c, slots, G, G);
 }
 
 // Sums of the partial rows in order: dw_post and dw_pre over the G CTAs, and
@@ -641,6 +802,8 @@ cudaError_t run(const BlockBwdP& p, const OpCfg& c) {
         if (taken) return e;
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
+    if (p.N <= 1024 * 4) return launch_columns<DT, 4>(p, c);
+    if (p.N <= 1024 * 8) return launch_columns<DT, 8>(p, c);
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_bwd_generic_kernel<DT>;

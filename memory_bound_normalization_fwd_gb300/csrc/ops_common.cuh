@@ -42,6 +42,19 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float f) {
     static_cast<typename Elem<DT>::T*>(p)[i] = Elem<DT>::store(f);
 }
 
+// Columns t, t + T, ... of a row of N elements starting at element `base`, zero past
+// the row's end. Every load is made (the last column again past the end), so that
+// none waits for another.
+template <int DT, int V>
+__device__ __forceinline__ void load_columns(const void* p, int64_t base, int t, int T, int N, float (&out)[V]) {
+    const typename Elem<DT>::T* q = static_cast<const typename Elem<DT>::T*>(p) + base;
+    typename Elem<DT>::T raw[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) raw[v] = q[min(v * T + t, N - 1)];
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = v * T + t < N ? Elem<DT>::load(raw[v]) : 0.f;
+}
+
 // Pairs of fp32 values for the packed instructions of sm_100 and later
 // (mul/add/fma.rn.f32x2: each half rounded as the scalar instruction would be),
 // half the instructions of scalar code.
