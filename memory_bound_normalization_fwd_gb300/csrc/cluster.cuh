@@ -39,4 +39,19 @@ static __device__ __forceinline__ uint32_t ld_peer_u32(uint32_t local_addr, uint
     return v;
 }
 
+// Writes four floats to the same shared-memory offset (16-byte aligned) in CTA `rank`
+// of the cluster and counts the 16 bytes on the mbarrier at `bar`'s offset there.
+// (A cluster barrier instead would also wait for this thread's stores to global
+// memory, by its release.)
+static __device__ __forceinline__ void st_async_peer_f4(uint32_t local_addr, uint32_t bar, uint32_t rank, float a,
+                                                        float b, float c, float d) {
+    uint32_t remote, remote_bar;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote_bar) : "r"(bar), "r"(rank));
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
+        "f"(a), "f"(b), "f"(c), "f"(d), "r"(remote_bar)
+        : "memory");
+}
+
 }  // namespace rmsn

@@ -18,6 +18,7 @@
 // A second launch sums the partial rows in CTA order.
 #include "rmsnorm.h"
 
+#include "cluster.cuh"
 #include "ops.h"
 #include "ops_common.cuh"
 #include "row_ring.cuh"
@@ -51,32 +52,40 @@ __device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, 
 // Vector kernel: row teams (row_ring.cuh) with the rows of h, s, dy, ds, and of
 // the gate where each row has its own, staged in shared memory.
 // GATE: 0 none, 1 one gate row for several rows, 2 a gate row per row.
-// A thread owns V vectors of columns. In registers per column: the scales, the
-// sums over rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the current
-// row t without its -e s, s and h between the two passes. With a gate row for
-// several rows dw_post changes only where the gate row ends: its sums are in
-// shared memory, a thread's own. fp32 with four vectors has no registers for
-// s and h: it reads them again (HOLD false), and a stage is then free one row
-// later, behind the next row's barrier. The arithmetic is on pairs (f32x2):
-// scalar code took three times the instructions and was bound by them (16384 x
-// 4096 bf16: 564 warp instructions per 8 columns of 32 lanes).
+// A thread owns V vectors of columns, eight columns. In registers per column: the
+// scales, the sums over rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the
+// current row t without its -e s, s and h between the two passes. With a gate row
+// for several rows dw_post changes only where the gate row ends: its sums are in
+// shared memory, a thread's own. The arithmetic is on pairs (f32x2): scalar code
+// took three times the instructions and was bound by them (16384 x 4096 bf16: 564
+// warp instructions per 8 columns of 32 lanes).
+// WIDE: a row's columns are more than 512 threads of eight; the CTAs of a cluster
+// take a slice each, and send their row sums into each other's shared memory. (Sixteen columns per thread in one CTA spilled: 8192 x
+// 8192 bf16 192 us, 8192 x 5000 241 us.)
 // FULL: both norms and ds are there and a row is exactly V vectors of every
 // thread, which the compiler then knows: no test of them is left in the loop.
-template <int DT, int V, int GATE, int MAXT, bool FULL>
-__global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
+template <int DT, int GATE, bool FULL, bool WIDE>
+__global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
     constexpr int E = VecElems<DT>::value;
     const bool post = FULL || p.w_post, prenorm = FULL || p.w_pre, has_ds = FULL || p.ds;
-    constexpr bool HOLD = V * E * (DT == kFP32 ? 2 : 1) <= 16;
+    constexpr int V = 8 / E;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RingShared sh;
     __shared__ __align__(16) float parts[kMaxTeams][2][4 * kMaxTeamWarps];
+    __shared__ float4 peers[2][8];  // WIDE: the sums of the cluster's CTAs, and their arrival
+    __shared__ uint64_t peer_bars[2];
 
     const int team = threadIdx.x / g.T, t = threadIdx.x - team * g.T;
-    const int64_t me = static_cast<int64_t>(blockIdx.x) * g.teams + team;
+    // WIDE: this CTA's slice of the row begins at vector first_vec.
+    const int rank = WIDE ? static_cast<int>(cluster_rank()) : 0;
+    const int first_vec = WIDE ? rank * g.slice : 0;
+    const int nvec = WIDE ? min(g.slice, g.nvec - first_vec) : g.nvec;
+    const int64_t group = WIDE ? blockIdx.x / g.cluster : blockIdx.x;
+    const int64_t me = group * g.teams + team;
     const int64_t r0 = me * g.q + (me < g.rem ? me : g.rem);
     const int rows = static_cast<int>(g.q) + (me < g.rem ? 1 : 0);
     Ring ring;
-    ring.row_bytes = static_cast<uint32_t>(g.nvec) * 16u;
+    ring.row_bytes = static_cast<uint32_t>(nvec) * 16u;
     ring.stage_bytes = ring.row_bytes * g.arrays;
     ring.base = smem_u32(smem) + static_cast<uint32_t>(team * g.stages) * ring.stage_bytes;
     ring.bars = smem_u32(&sh.bars[team][0]);
@@ -84,6 +93,10 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     float4* post_sums = reinterpret_cast<float4*>(smem + g.sums_at);
     if (t == 0) {
         for (int st = 0; st < g.stages; ++st) mbar_init(ring.bar(st), 1);
+        if (WIDE) {
+            mbar_init(smem_u32(&peer_bars[0]), 1);
+            mbar_init(smem_u32(&peer_bars[1]), 1);
+        }
         fence_mbar_init();
         sh.dead[team] = 0;
     }
@@ -99,13 +112,13 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     auto issue = [&](int row, int st) {
         const int64_t i = r0 + row;
         ring.expect(st);
-        if (need_h) ring.copy(st, ih, static_cast<const uint4*>(p.h) + i * p.ldh);
+        if (need_h) ring.copy(st, ih, static_cast<const uint4*>(p.h) + first_vec + i * p.ldh);
         if (prenorm) {
-            ring.copy(st, is, static_cast<const uint4*>(p.s) + i * p.lds);
-            ring.copy(st, idy, static_cast<const uint4*>(p.dy) + i * p.lddy);
+            ring.copy(st, is, static_cast<const uint4*>(p.s) + first_vec + i * p.lds);
+            ring.copy(st, idy, static_cast<const uint4*>(p.dy) + first_vec + i * p.lddy);
         }
-        if (has_ds) ring.copy(st, ids, static_cast<const uint4*>(p.ds) + i * p.ldds);
-        if (GATE == 2) ring.copy(st, ig, static_cast<const uint4*>(p.gate) + i * p.ldg);
+        if (has_ds) ring.copy(st, ids, static_cast<const uint4*>(p.ds) + first_vec + i * p.ldds);
+        if (GATE == 2) ring.copy(st, ig, static_cast<const uint4*>(p.gate) + first_vec + i * p.ldg);
     };
     pdl_wait();
     if (t == 0) {
@@ -113,9 +126,9 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     }
     constexpr int H = E / 2;
     const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-    const uint4* w_post = static_cast<const uint4*>(p.w_post);
-    const uint4* w_pre = static_cast<const uint4*>(p.w_pre);
-    const uint4* gate = static_cast<const uint4*>(p.gate);
+    const uint4* w_post = p.w_post ? static_cast<const uint4*>(p.w_post) + first_vec : nullptr;
+    const uint4* w_pre = p.w_pre ? static_cast<const uint4*>(p.w_pre) + first_vec : nullptr;
+    const uint4* gate = static_cast<const uint4*>(p.gate) + first_vec;
     // Per column, as pairs: a = alpha gate (offset + w_post) (GATE 2: without the
     // gate) and offset + w_pre.
     f2 a[V][H], wpre[V][H];
@@ -129,7 +142,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     auto post_scale = [&](int v, f2* o) {
         const int c = column(v);
         if (w_post) {
-            weights2<DT>(c < g.nvec ? __ldg(w_post + c) : zero4, p.offset, o);
+            weights2<DT>(c < nvec ? __ldg(w_post + c) : zero4, p.offset, o);
 #pragma unroll
             for (int e = 0; e < H; ++e) o[e] = f2_mul(o[e], f2_dup(p.alpha));
         } else {
@@ -139,7 +152,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     };
     auto gate_row = [&](int v, f2* o) {
         const int c = column(v);
-        unpack2<DT>(c < g.nvec ? __ldg(gate + grow * p.ldg + c) : zero4, o);
+        unpack2<DT>(c < nvec ? __ldg(gate + grow * p.ldg + c) : zero4, o);
     };
     auto load_scale = [&]() {
 #pragma unroll
@@ -158,7 +171,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = column(v);
-        weights2<DT>(w_pre && c < g.nvec ? __ldg(w_pre + c) : zero4, p.offset, wpre[v]);
+        weights2<DT>(w_pre && c < nvec ? __ldg(w_pre + c) : zero4, p.offset, wpre[v]);
 #pragma unroll
         for (int e = 0; e < H; ++e) P[v][e] = pre[v][e] = 0;
     }
@@ -167,7 +180,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
         for (int i = 0; i < V * E / 4; ++i)
             post_sums[i * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __syncthreads();
+    if (WIDE) cluster_sync();  // the others run before anything is written to them
+    else __syncthreads();
 
     int st = 0, parity = 0;
     uint32_t phase = 0;
@@ -179,9 +193,9 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     const float* rstd_pre = p.rstd_pre + r0;
     float k1_next = post ? __ldg(rstd_post) : 1.f;
     float k2_next = prenorm ? __ldg(rstd_pre) : 0.f;
-    uint4* dr = static_cast<uint4*>(p.dr) + r0 * p.lddr + t;
-    uint4* dh = static_cast<uint4*>(p.dh) + r0 * p.lddh + t;
-    uint4* dgate = static_cast<uint4*>(p.dgate) + (GATE == 2 ? r0 * p.lddg + t : 0);
+    uint4* dr = static_cast<uint4*>(p.dr) + r0 * p.lddr + first_vec + t;
+    uint4* dh = static_cast<uint4*>(p.dh) + r0 * p.lddh + first_vec + t;
+    uint4* dgate = static_cast<uint4*>(p.dgate) + (GATE == 2 ? r0 * p.lddg + first_vec + t : 0);
     // Vectors of the row; those past its end stay zero.
     uint4 hv[V], sv[V], gv[V], dyv[V], dsv[V];
 #pragma unroll
@@ -202,12 +216,12 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
             if (prenorm) k2_next = __ldg(rstd_pre + row + 1);
         }
         f2 t0[V][H];
-        f2 c0 = 0, c1 = 0, c2 = 0;
+        f2 us = 0, aht = 0, ahs = 0;
         const f2 k22 = f2_dup(k2);
         const uint32_t at = ring.stage(st);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (FULL || column(v) < g.nvec) {
+            if (FULL || column(v) < nvec) {
                 const uint32_t q = at + 16u * (v * g.T);
                 if (need_h) hv[v] = lds16(q + oh);
                 if (prenorm) {
@@ -216,8 +230,6 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 }
                 if (has_ds) dsv[v] = lds16(q + ods);
                 if (GATE == 2) gv[v] = lds16(q + og);
-            } else if (V * E > 8) {  // no registers to carry the zeros round the loop
-                hv[v] = sv[v] = gv[v] = dyv[v] = dsv[v] = zero4;
             }
             unpack2<DT>(dsv[v], t0[v]);
             f2 s[H];
@@ -229,7 +241,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 for (int e = 0; e < H; ++e) {
                     const f2 u = f2_mul(dy[e], wpre[v][e]);
                     t0[v][e] = f2_fma(k22, u, t0[v][e]);
-                    c0 = f2_fma(u, s[e], c0);
+                    us = f2_fma(u, s[e], us);
                     pre[v][e] = f2_fma(dy[e], f2_mul(s[e], k22), pre[v][e]);
                 }
             }
@@ -241,37 +253,52 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                 for (int e = 0; e < H; ++e) {
                     f2 ah = f2_mul(a[v][e], h[e]);
                     if (GATE == 2) ah = f2_mul(ah, x[e]);
-                    c1 = f2_fma(ah, t0[v][e], c1);
-                    c2 = f2_fma(ah, s[e], c2);
+                    aht = f2_fma(ah, t0[v][e], aht);
+                    ahs = f2_fma(ah, s[e], ahs);
                 }
             }
         }
-        float sums[3] = {f2_sum(c0), f2_sum(c1), f2_sum(c2)};
+        float sums[3] = {f2_sum(us), f2_sum(aht), f2_sum(ahs)};
         team_sums3(sums, &parts[team][parity][0], team, t, g.T);
         parity ^= 1;
         dead = *(volatile unsigned int*)&sh.dead[team] != 0;
-        if (dead) break;
-        if (t == 0) {
-            if (HOLD) {
-                if (row + g.stages < rows) issue(row + g.stages, st);
-            } else if (row > 0 && row - 1 + g.stages < rows) {
-                // every thread is past its second reading of the row before
-                issue(row - 1 + g.stages, st == 0 ? g.stages - 1 : st - 1);
+        if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
+        if (WIDE) {
+            // Slot and barrier of this row, used again two rows on: a CTA sends a row's
+            // sums when all its threads have read those of the row before.
+            const int slot = row & 1;
+            const uint32_t bar = smem_u32(&peer_bars[slot]);
+            if (t == 0) mbar_arrive_expect_tx(bar, 16u * g.cluster);
+            if (t < g.cluster)
+                st_async_peer_f4(smem_u32(&peers[slot][rank]), bar, t, sums[0], sums[1], sums[2], dead ? 1.f : 0.f);
+            if (dead) break;
+            if (!mbar_wait_bounded(bar, (row >> 1) & 1, g.limit)) {
+                *(volatile unsigned int*)&sh.dead[team] = 1;
+                atomicOr(&g_block_bwd_status, 1u);
             }
+            // Added in rank order, so that all get the same. That another CTA has given
+            // up is acted on behind the next row's barrier, by all threads alike.
+            float4 x = peers[slot][0];
+            for (int i = 1; i < g.cluster; ++i) {
+                const float4 z = peers[slot][i];
+                x.x += z.x;
+                x.y += z.y;
+                x.z += z.z;
+                x.w += z.w;
+            }
+            sums[0] = x.x;
+            sums[1] = x.y;
+            sums[2] = x.z;
+            if (x.w != 0.f) *(volatile unsigned int*)&sh.dead[team] = 1;
         }
+        if (dead) break;
         const float e2 = k2 * k2 * k2 * (sums[0] * inv_n);
         const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) * inv_n);
         const f2 me2 = f2_dup(-e2), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const bool in = FULL || column(v) < g.nvec;
+            const bool in = FULL || column(v) < nvec;
             f2 s[H], h[H], x[H], o[H];
-            if (!HOLD && in) {
-                const uint32_t q = at + 16u * (v * g.T);
-                if (need_h) hv[v] = lds16(q + oh);
-                if (prenorm) sv[v] = lds16(q + os);
-                if (GATE == 2) gv[v] = lds16(q + og);
-            }
             unpack2<DT>(sv[v], s);
             unpack2<DT>(hv[v], h);
             if (GATE == 2) unpack2<DT>(gv[v], x);
@@ -309,11 +336,11 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
             const int64_t first = grow * p.gate_rows;
             const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
             const bool whole = first >= r0 && last <= r0 + rows;
-            float* out = partial(p.ws, first > r0 ? 3 : 2, me, g.slots, block_bwd_pitch(p.N));
+            float* out = partial(p.ws, first > r0 ? 3 : 2, me, g.slots, block_bwd_pitch(p.N)) + first_vec * E;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = column(v);
-                const bool in = c < g.nvec;
+                const bool in = c < nvec;
                 f2 q[H], o[H];
                 gate_row(v, q);
                 post_scale(v, o);
@@ -335,7 +362,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                     P[v][e] = 0;
                 }
                 if (in && whole)
-                    static_cast<uint4*>(p.dgate)[grow * p.lddg + c] = pack2<DT>(o);
+                    static_cast<uint4*>(p.dgate)[grow * p.lddg + first_vec + c] = pack2<DT>(o);
             }
         }
         if (++st == g.stages) {
@@ -345,9 +372,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
     }
     if (dead && t == 0) {
         atomicOr(&g_block_bwd_status, 1u);
-        // Rows below row + stages (HOLD false: row + stages - 1) were issued and
-        // may still be landing.
-        for (int k = row; k < row + g.stages - (HOLD || row == 0 ? 0 : 1) && k < rows; ++k) {
+        // Rows below row + stages were issued and may still be landing.
+        for (int k = row; k < row + g.stages && k < rows; ++k) {
             mbar_wait_bounded(ring.bar(st), phase, g.limit);
             if (++st == g.stages) {
                 st = 0;
@@ -355,6 +381,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
             }
         }
     }
+    if (WIDE) cluster_sync();  // nobody writes to a CTA that has ended
     pdl_launch_dependents();
     // The teams' column sums, added in team order through the rings' memory,
     // into the CTA's partial rows.
@@ -374,8 +401,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
             if (g.teams > 1) all[i * blockDim.x + threadIdx.x] = x;
             else {
                 const int c = (i / (E / 4)) * g.T + t;
-                if (c < g.nvec)
-                    reinterpret_cast<float4*>(partial(p.ws, which, blockIdx.x, g.slots, block_bwd_pitch(p.N)))
+                if (c < nvec)
+                    reinterpret_cast<float4*>(partial(p.ws, which, group, g.slots, block_bwd_pitch(p.N)) + first_vec * E)
                         [c * (E / 4) + i % (E / 4)] = x;
             }
         }
@@ -393,8 +420,8 @@ __global__ void __launch_bounds__(MAXT) block_bwd_ring_kernel(const BlockBwdP p,
                     x.z += z.z;
                     x.w += z.w;
                 }
-                if (c < g.nvec)
-                    reinterpret_cast<float4*>(partial(p.ws, which, blockIdx.x, g.slots, block_bwd_pitch(p.N)))
+                if (c < nvec)
+                    reinterpret_cast<float4*>(partial(p.ws, which, group, g.slots, block_bwd_pitch(p.N)) + first_vec * E)
                         [c * (E / 4) + i % (E / 4)] = x;
             }
         }
@@ -736,36 +763,37 @@ cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G,
 
 template <int DT, int GATE>
 cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
-    constexpr int E = VecElems<DT>::value;
+    constexpr int E = VecElems<DT>::value, V = 8 / E;  // eight columns per thread
     using Fn = void (*)(const BlockBwdP, const RingShape);
     const int64_t nvec = in.N / E;
     *taken = false;
-    // Eight columns per thread up to 512 threads, sixteen above.
-    constexpr int V1 = 8 / E;
-    const int V = nvec <= 512 * V1 ? V1 : nvec <= 1024 * V1 ? 2 * V1 : 0;
-    if (V == 0) return cudaSuccess;
-    const int T = static_cast<int>((nvec + V * 32 - 1) / (V * 32)) * 32;
-    const bool full = in.w_post && in.w_pre && in.ds && nvec == static_cast<int64_t>(V) * T;
-    const Fn fn = full ? (V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512, true>
-                                  : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512, true>)
-                       : (V == V1 ? block_bwd_ring_kernel<DT, V1, GATE, 512, false>
-                                  : block_bwd_ring_kernel<DT, 2 * V1, GATE, 512, false>);
+    int cluster = 1;
+    while (cluster <= 8 && nvec > 512 * V * cluster) cluster *= 2;
+    if (cluster > 8) return cudaSuccess;
+    const int slice = static_cast<int>((nvec + cluster - 1) / cluster);
+    const int T = (slice + V * 32 - 1) / (V * 32) * 32;
+    const bool full = in.w_post && in.w_pre && in.ds && nvec == static_cast<int64_t>(V) * T * cluster;
+    const Fn fn = cluster > 1 ? (full ? block_bwd_ring_kernel<DT, GATE, true, true>
+                                      : block_bwd_ring_kernel<DT, GATE, false, true>)
+                              : (full ? block_bwd_ring_kernel<DT, GATE, true, false>
+                                      : block_bwd_ring_kernel<DT, GATE, false, false>);
     const int arrays = (in.w_post || GATE ? 1 : 0) + (in.w_pre ? 2 : 0) + (in.ds ? 1 : 0) + (GATE == 2 ? 1 : 0);
     const int64_t slots = block_bwd_max_grid(in.M, in.N, c.dev.sm_count);
     RingPlan plan;
     const int extra = GATE == 1 ? V * E * 4 : 0;
     // 128 KB of stages per SM (GB300, us: 16384x4096 bf16 at 64 / 96 / 128 / 192
     // KB 147 / 130 / 129 / 132, 65536x512 91 / 87 / 88 / 88).
-    if (!ring_plan(reinterpret_cast<const void*>(fn), c, in.M, static_cast<int>(nvec), T, 512, arrays, extra,
-                   128 << 10, &plan))
+    if (!ring_plan(reinterpret_cast<const void*>(fn), c, in.M, slice, T, 512, arrays, extra, 128 << 10, cluster,
+                   &plan))
         return cudaSuccess;
     // The teams' sums meet in the rings' memory: with a row per team it may be
     // smaller than they are.
     plan.shape.sums_at = std::max(plan.smem - extra * plan.threads, plan.threads * V * E * 4);
     plan.smem = plan.shape.sums_at + extra * plan.threads;
     plan.shape.slots = slots;
-    const int64_t teams = plan.grid * plan.shape.teams;
-    if (teams > slots) return cudaSuccess;
+    plan.shape.nvec = static_cast<int>(nvec);
+    const int64_t groups = plan.grid / cluster, ranges = groups * plan.shape.teams;
+    if (ranges > slots) return cudaSuccess;
     BlockBwdP p = in;
     p.ldh /= E;
     p.lds /= E;
@@ -776,8 +804,27 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
     p.lddr /= E;
     p.lddg /= E;
     *taken = true;
-    const cudaError_t e = op_launch(c, fn, plan.grid, plan.threads, plan.smem, p, plan.shape);
-    return e != cudaSuccess ? e : finish<DT>(in, c, slots, plan.grid, teams);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (c.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(plan.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, plan.shape);
+    return e != cudaSuccess ? e : finish<DT>(in, c, slots, groups, ranges);
 }
 
 bool vectors(const BlockBwdP& p) {

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 namespace rmsn {
@@ -37,12 +38,38 @@ Facts facts(const void* fn, int threads, int max_optin) {
     return cache[key] = f;
 }
 
+// Clusters of CTAs that the device holds at once, looked up once.
+int max_clusters(const void* fn, int cluster, int threads, int smem) {
+    static std::mutex mu;
+    static std::map<std::tuple<int, const void*, int, int, int>, int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> guard(mu);
+    const auto key = std::make_tuple(dev, fn, cluster, threads, smem);
+    auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+    return cache[key] = n;
+}
+
 }  // namespace
 
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, int in_flight, RingPlan* out) {
+               int extra, int in_flight, int cluster, RingPlan* out) {
     if (T > max_threads) return false;
-    int teams = std::min(max_threads / T, kMaxTeams);
+    int teams = cluster > 1 ? 1 : std::min(max_threads / T, kMaxTeams);
     // Few rows: one team per CTA spreads them over more SMs.
     while (teams > 1 && static_cast<int64_t>(teams) * c.dev.sm_count > M) --teams;
     const Facts f = facts(fn, teams * T, c.dev.max_smem_optin);
@@ -62,13 +89,19 @@ bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int m
     stages = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(stages, enough)));
     const int64_t want = (M + teams - 1) / teams;
     int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas;
-    if (c.max_ctas > 0) cap = std::min<int64_t>(cap, c.max_ctas);
-    out->grid = std::min(want, cap);
+    if (cluster > 1)
+        cap = max_clusters(fn, cluster, teams * T,
+                           static_cast<int>(stage * stages + static_cast<int64_t>(extra) * teams * T));
+    if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(1, c.max_ctas / cluster));
+    int64_t groups = std::min(want, cap);  // CTAs, or clusters
     // Every team walks at least one row.
-    while (out->grid * teams > M) --out->grid;
-    if (out->grid < 1) return false;
-    const int64_t n = out->grid * teams;
+    while (groups * teams > M) --groups;
+    if (groups < 1) return false;
+    const int64_t n = groups * teams;
+    out->grid = groups * cluster;
     RingShape& s = out->shape;
+    s.cluster = cluster;
+    s.slice = nvec;
     s.T = T;
     s.teams = teams;
     s.q = M / n;

@@ -27,6 +27,8 @@ struct RingShape {
     int teams;        // of a CTA
     int stages;
     int nvec;         // 16-byte vectors of a row
+    int cluster;      // CTAs of a cluster that share a row (1: none)
+    int slice;        // vectors of a row in each of them but the last
     int arrays;       // rows per stage
     int rem;          // the first `rem` teams walk q + 1 rows, the others q
     int64_t q;

@@ -8,7 +8,7 @@ namespace rmsn {
 
 struct RingPlan {
     RingShape shape;
-    int64_t grid;
+    int64_t grid;  // CTAs
     int threads;
     int smem;
 };
@@ -16,9 +16,10 @@ struct RingPlan {
 // Lays out `arrays` rows of `nvec` vectors per stage for teams of T threads in
 // CTAs of up to `max_threads`, with `extra` more bytes of shared memory per
 // CTA thread and about `in_flight` bytes of stages per SM. False where a row
-// does not fit two stages of shared memory.
+// does not fit two stages of shared memory. cluster > 1: the CTAs of a cluster
+// take a row's slices, `nvec` vectors each (one team per CTA).
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, int in_flight, RingPlan* out);
+               int extra, int in_flight, int cluster, RingPlan* out);
 
 // Reads a status word of the current device and clears it.
 template <typename S>

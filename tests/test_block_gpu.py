@@ -108,6 +108,16 @@ def test_gate_rows_that_cross_the_ranges_of_ctas(dtype, max_ctas, gate_rows):
         _both(100, 264, dtype, 5, True, True, gate_rows, 0.0, 1.0, 1.0, opts)
 
 
+@pytest.mark.parametrize("dtype,N", [("bf16", 4104), ("bf16", 5000), ("bf16", 8192), ("fp16", 16384), ("bf16", 32768),
+                                     ("fp32", 4100), ("fp32", 8192), ("fp32", 16384)])
+@pytest.mark.parametrize("gate_rows", [0, 1, 5, 1000])
+def test_wide_rows(dtype, N, gate_rows):
+    for kw in (dict(), dict(max_ctas=3), dict(max_ctas=40)):
+        _both(41, N, dtype, gate_rows + N, True, True, gate_rows, 1.0, 0.5, 1.5, kw)
+    _both(300, N, dtype, gate_rows + N, True, False, gate_rows, 1.0, 0.5, 1.5, {})
+    _both(7, N, dtype, gate_rows + N, False, True, gate_rows, 1.0, 0.5, 1.5, {})
+
+
 def test_backward_without_the_residuals_gradient():
     for opts in _variants():
         _both(40, 512, "bf16", 3, True, True, 8, 0.0, 1.0, 1.0, opts, ds=False)
@@ -160,7 +170,7 @@ def test_in_place_gives_the_same_bits(N, s_on, y_on):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("N", [512, 777, 20001])
+@pytest.mark.parametrize("N", [512, 777, 8192, 20001])
 @pytest.mark.parametrize("dh_on,dr_on", [("dy", "ds"), ("h", "s"), ("ds", "dy"), (None, "ds")])
 def test_backward_in_place_gives_the_same_bits(N, dh_on, dr_on):
     d = _make(33, N, "fp16", 4, gate_rows=11)
@@ -241,7 +251,7 @@ def test_batched_shapes_and_gates():
         B.block_fwd(h, r, d["w_post"], d["w_pre"], d["gate"][:2])
 
 
-@pytest.mark.parametrize("N", [512, 4096, 777])
+@pytest.mark.parametrize("N", [512, 4096, 8192, 777])
 def test_results_do_not_depend_on_the_run(N):
     d = _make(700, N, "bf16", 21, gate_rows=90)
     runs = []
@@ -255,7 +265,7 @@ def test_results_do_not_depend_on_the_run(N):
 
 
 @pytest.mark.parametrize("pdl", [True, False])
-@pytest.mark.parametrize("N", [512, 4096])
+@pytest.mark.parametrize("N", [512, 4096, 5000])
 def test_a_chain_of_layers_keeps_stream_order(N, pdl):
     # Each layer's r is the layer's before s, its h that layer's y; then all the
     # backward calls in turn through one workspace. The same calls with the
