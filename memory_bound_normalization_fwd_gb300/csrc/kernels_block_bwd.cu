@@ -62,12 +62,16 @@ __device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, 
 // WIDE: a row's columns are more than 512 threads of eight; the CTAs of a cluster
 // take a slice each, and send their row sums into each other's shared memory. (Sixteen columns per thread in one CTA spilled: 8192 x
 // 8192 bf16 192 us, 8192 x 5000 241 us.)
-// FULL: both norms and ds are there and a row is exactly V vectors of every
-// thread, which the compiler then knows: no test of them is left in the loop.
-template <int DT, int GATE, bool FULL, bool WIDE>
+// PARTS: kAll, kPreOnly: both norms (the one before alone) and ds are there and a
+// row is exactly V vectors of every thread, which the compiler then knows: no test of
+// them is left in the loop. kAny: tests.
+constexpr int kAny = 0, kAll = 1, kPreOnly = 2;
+template <int DT, int GATE, int PARTS, bool WIDE>
 __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, const RingShape g) {
     constexpr int E = VecElems<DT>::value;
-    const bool post = FULL || p.w_post, prenorm = FULL || p.w_pre, has_ds = FULL || p.ds;
+    constexpr bool FULL = PARTS != kAny;
+    const bool post = PARTS == kAll || (PARTS == kAny && p.w_post);
+    const bool prenorm = FULL || p.w_pre, has_ds = FULL || p.ds;
     constexpr int V = 8 / E;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RingShared sh;
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
     // alpha (offset + w_post) of a vector of columns.
     auto post_scale = [&](int v, f2* o) {
         const int c = column(v);
-        if (w_post) {
+        if (post) {
             weights2<DT>(c < nvec ? __ldg(w_post + c) : zero4, p.offset, o);
 #pragma unroll
             for (int e = 0; e < H; ++e) o[e] = f2_mul(o[e], f2_dup(p.alpha));
@@ -679,13 +683,13 @@ cudaError_t launch_columns(const BlockBwdP& p, const OpCfg& c) {
 
 // Sums of the partial rows in order: dw_post and dw_pre over the G CTAs, and
 // the gate rows that more than one of the R ranges worked on. A CTA sums 32
-// vectors of 4 columns: its 8 warps take every eighth partial row, four loads
-// in flight each, and meet in shared memory in warp order. blockIdx.y: 0
+// vectors of 4 columns: its 16 warps take every sixteenth partial row, eight
+// loads in flight each, and meet in shared memory in warp order. blockIdx.y: 0
 // dw_post, 1 dw_pre, then gate rows.
 template <int DT>
-__global__ void __launch_bounds__(256) block_bwd_finish_kernel(const BlockBwdP p, int64_t slots, int64_t G,
+__global__ void __launch_bounds__(512) block_bwd_finish_kernel(const BlockBwdP p, int64_t slots, int64_t G,
                                                                int64_t R) {
-    __shared__ float4 red[8][32];
+    __shared__ float4 red[16][32];
     const int64_t pitch = block_bwd_pitch(p.N);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t j4 = static_cast<int64_t>(blockIdx.x) * 32 + lane;
@@ -719,14 +723,15 @@ __global__ void __launch_bounds__(256) block_bwd_finish_kernel(const BlockBwdP p
                 x.w += z.w;
             };
             int64_t b = b0 + w;
-            for (; b + 24 < b1; b += 32) {
-                const float4 z0 = at(b), z1 = at(b + 8), z2 = at(b + 16), z3 = at(b + 24);
-                add(z0);
-                add(z1);
-                add(z2);
-                add(z3);
+            while (b < b1) {
+                float4 z[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    z[k] = b + 16 * k < b1 ? at(b + 16 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) add(z[k]);
+                b += 128;
             }
-            for (; b < b1; b += 8) add(at(b));
         }
         __syncthreads();
         red[w][lane] = x;
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(256) block_bwd_finish_kernel(const BlockBwdP p
         if (w < 4) {  // warp w: column w of each vector
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s += reinterpret_cast<const float*>(&red[k][lane])[w];
+            for (int k = 0; k < 16; ++k) s += reinterpret_cast<const float*>(&red[k][lane])[w];
             const int64_t j = j4 * 4 + w;
             if (j < p.N) {
                 if (item < 2) {
@@ -755,7 +760,7 @@ cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G,
     if (!p.dw_post && !p.dw_pre && grows == 0) return cudaSuccess;
     Launch l;
     l.grid = static_cast<int>((p.N + 127) / 128);
-    l.threads = 256;
+    l.threads = 512;
     LaunchCfg cfg(l, c.stream, c.pdl);
     cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + grows, 1024));
     return cudaLaunchKernelEx(&cfg.cfg, block_bwd_finish_kernel<DT>, p, slots, G, R);
@@ -772,11 +777,15 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
     if (cluster > 8) return cudaSuccess;
     const int slice = static_cast<int>((nvec + cluster - 1) / cluster);
     const int T = (slice + V * 32 - 1) / (V * 32) * 32;
-    const bool full = in.w_post && in.w_pre && in.ds && nvec == static_cast<int64_t>(V) * T * cluster;
-    const Fn fn = cluster > 1 ? (full ? block_bwd_ring_kernel<DT, GATE, true, true>
-                                      : block_bwd_ring_kernel<DT, GATE, false, true>)
-                              : (full ? block_bwd_ring_kernel<DT, GATE, true, false>
-                                      : block_bwd_ring_kernel<DT, GATE, false, false>);
+    const bool full = in.w_pre && in.ds && nvec == static_cast<int64_t>(V) * T * cluster;
+    const int parts = full && in.w_post ? kAll : full && GATE == 0 ? kPreOnly : kAny;
+    constexpr int PRE = GATE == 0 ? kPreOnly : kAny;
+    const Fn fn = cluster > 1 ? (parts == kAll   ? block_bwd_ring_kernel<DT, GATE, kAll, true>
+                                 : parts == kAny ? block_bwd_ring_kernel<DT, GATE, kAny, true>
+                                                 : block_bwd_ring_kernel<DT, GATE, PRE, true>)
+                              : (parts == kAll   ? block_bwd_ring_kernel<DT, GATE, kAll, false>
+                                 : parts == kAny ? block_bwd_ring_kernel<DT, GATE, kAny, false>
+                                                 : block_bwd_ring_kernel<DT, GATE, PRE, false>);
     const int arrays = (in.w_post || GATE ? 1 : 0) + (in.w_pre ? 2 : 0) + (in.ds ? 1 : 0) + (GATE == 2 ? 1 : 0);
     const int64_t slots = block_bwd_max_grid(in.M, in.N, c.dev.sm_count);
     RingPlan plan;
