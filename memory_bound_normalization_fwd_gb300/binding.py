@@ -777,6 +777,16 @@ def _heads(t, name, shape, dtype, device):
 _NO_HEADS = (0, 0, 0, 0)
 
 
+def _new_heads(like, shape):
+    """A new contiguous heads tensor and its struct values."""
+    t = like.new_empty(shape)
+    if len(shape) == 3:
+        H, D = shape[1], shape[2]
+        return t, (t.data_ptr(), 0, H * D, D)
+    S, H, D = shape[1], shape[2], shape[3]
+    return t, (t.data_ptr(), S * H * D, H * D, D)
+
+
 def _rope_common(q, k, steps, positions, w_q, w_k, interleaved):
     """The fields of the rope struct up to the weights."""
     import torch
@@ -832,8 +842,9 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     qh = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
-        q_out = q.new_empty(shape)
-    qo = _heads(q_out, "q_out", shape, dtype, dev)
+        q_out, qo = _new_heads(q, shape)
+    else:
+        qo = _heads(q_out, "q_out", shape, dtype, dev)
     kh = ko = _NO_HEADS
     a = b = None
     ap = bp = 0
@@ -841,8 +852,9 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
         kshape = k.shape
         kh = _heads(k, "k", kshape, dtype, dev)
         if k_out is None:
-            k_out = k.new_empty(kshape)
-        ko = _heads(k_out, "k_out", kshape, dtype, dev)
+            k_out, ko = _new_heads(k, kshape)
+        else:
+            ko = _heads(k_out, "k_out", kshape, dtype, dev)
         if rstd and w_k is not None:
             b = k.new_empty(kshape[:-1], dtype=torch.float32)
             bp = b.data_ptr()
@@ -880,8 +892,9 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
     D = shape[-1]
     gq = _heads(dq_out, "dq_out", shape, dtype, dev)
     if dq is None:
-        dq = dq_out.new_empty(shape)
-    oq = _heads(dq, "dq", shape, dtype, dev)
+        dq, oq = _new_heads(dq_out, shape)
+    else:
+        oq = _heads(dq, "dq", shape, dtype, dev)
     qh = kh = gk = ok = _NO_HEADS
     dwq = dwk = None
     ap = bp = wqp = wkp = 0
@@ -894,8 +907,9 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
         kshape = dk_out.shape
         gk = _heads(dk_out, "dk_out", kshape, dtype, dev)
         if dk is None:
-            dk = dk_out.new_empty(kshape)
-        ok = _heads(dk, "dk", kshape, dtype, dev)
+            dk, ok = _new_heads(dk_out, kshape)
+        else:
+            ok = _heads(dk, "dk", kshape, dtype, dev)
         if w_k is not None:
             bp = _vector(rstd_k, "rstd_k", kshape[:-1].numel(), f32, dev)
             kh = _heads(k, "k", kshape, dtype, dev)

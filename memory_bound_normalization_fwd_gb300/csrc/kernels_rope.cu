@@ -52,8 +52,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 //   kHalves      i and i + R/(2E) of the rotated part, so that both values of a pair
 //                are in one thread
 //   kInterleaved i and i + L: a pair lies inside a vector
-//   kExchange    i and i + L, halves that are not whole vectors: the other value of
-//                a pair is read from a copy of the head in shared memory
+//   kExchange    i and i + L, halves that are not whole vectors but even: the other
+//                values of pairs are read from a copy of the head in shared memory
 //
 // A unit is a token with some of its heads, and a team takes one unit after
 // another: the cos and sin of a lane's pairs depend on the token alone, so a lane
@@ -120,6 +120,8 @@ struct Lane {
     __device__ __forceinline__ int index(int n) const {
         return LAYOUT == kHalves ? l * E + n : n < N / 2 ? va * (N / 2) + n : vb * (N / 2) + n - N / 2;
     }
+    // kExchange: the sines come with the sign that the other value of the pair takes.
+    template <int SIGN>
     __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t position) {
         if (LAYOUT == kHalves ? l >= g.pairs : va * E >= p.R) return;
         const int half = p.R / 2;
@@ -129,9 +131,11 @@ struct Lane {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 int j = index(n + k);
-                if (LAYOUT == kExchange && j >= half) j -= half;
+                const bool second = LAYOUT == kExchange && j >= half;
+                if (second) j -= half;
                 t[k] = make_float2(0.f, 0.f);
                 if (LAYOUT == kHalves || j < half) t[k] = turn<DT>(position, __ldg(p.steps + j), p.magnitude);
+                if (LAYOUT == kExchange && second == (SIGN < 0)) t[k].y = -t[k].y;
             }
             c[n / 2] = f2_make(t[0].x, t[1].x);
             s[n / 2] = f2_make(t[0].y, t[1].y);
@@ -181,23 +185,19 @@ struct Lane {
                 }
             }
             __syncwarp();
+            // half is even, so two values and their two others lie side by side
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 f2* y = k == 0 ? x : z;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    const float2 cp = f2_get(c[k * H + i]), sp = f2_get(s[k * H + i]);
-                    float2 v = f2_get(y[i]);
                     const int j = (k == 0 ? va : vb) * E + 2 * i;
-                    if (j < p.R) v.x = other(row, j, half, v.x, cp.x, SIGN * sp.x);
-                    if (j + 1 < p.R) v.y = other(row, j + 1, half, v.y, cp.y, SIGN * sp.y);
-                    y[i] = f2_make(v.x, v.y);
+                    if (j >= p.R) continue;
+                    const float2 o = *reinterpret_cast<const float2*>(row + (j < half ? j + half : j - half));
+                    y[i] = f2_fma(f2_make(o.x, o.y), s[k * H + i], f2_mul(y[i], c[k * H + i]));
                 }
             }
         }
-    }
-    __device__ __forceinline__ static float other(const float* row, int j, int half, float v, float c, float s) {
-        return j < half ? fmaf(-row[j + half], s, v * c) : fmaf(row[j - half], s, v * c);
     }
 };
 
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
         };
 #pragma unroll
         for (int k = 0; k < S; ++k) fetch();
-        if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
+        if (u.n) ln.template angles<1>(p, g, position_of(p, u.b, u.s));
         for (int h = 0; h < per; ++h) {
             const bool live = h < u.n;
             copies_wait<S - 1>();
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
 #pragma unroll
         for (int k = 0; k < S; ++k) fetch();
         float r_next = norm && u.n > 0 ? __ldg(rstd) : 0.f;
-        if (u.n) ln.angles(p, g, position_of(p, u.b, u.s));
+        if (u.n) ln.template angles<-1>(p, g, position_of(p, u.b, u.s));
         for (int h = 0; h < per; ++h) {
             const bool live = h < u.n;
             const float r = r_next;
@@ -642,6 +642,7 @@ int64_t generic_grid(const RopeP& p, const OpCfg& c) {
 bool vectors(const RopeP& p, bool bwd) {
     const int E = vec_elems(p.dtype);
     if (p.D % E != 0 || p.D > 64 * E) return false;
+    if (!p.interleaved && p.R % 4 != 0) return false;  // kExchange takes values in twos
     for (const RopeSeg& s : p.seg) {
         if (s.heads == 0) continue;
         const HeadsP* hs[] = {&s.in, &s.out, bwd && s.w ? &s.x : nullptr};
