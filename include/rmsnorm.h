@@ -364,7 +364,8 @@ int rmsnorm_bwd_workspace_size(int64_t M, int64_t N, int dtype, const rmsnorm_op
  * elements. Whole 16-byte vectors (row or head size, strides and pointers)
  * take the vector kernels, anything else the element-wise ones. `opts` may be
  * NULL; they read variant (AUTO, CTA: the vector kernels, GENERIC: the
- * element-wise kernels), max_ctas and RMSNORM_FLAG_NO_PDL.
+ * element-wise kernels), max_ctas, RMSNORM_FLAG_NO_PDL and, for the block
+ * operator's kernels that stage rows, wait_limit_ns.
  * ------------------------------------------------------------------------- */
 
 /*

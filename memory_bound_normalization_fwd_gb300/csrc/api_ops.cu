@@ -100,6 +100,7 @@ int read_op_options(const rmsnorm_options_t* opts, OpCfg* c) {
     c->variant = variant;
     c->max_ctas = k.max_ctas;
     c->pdl = (k.flags & RMSNORM_FLAG_NO_PDL) == 0;
+    c->wait_limit_ns = k.wait_limit_ns < 60000000000LL ? k.wait_limit_ns : 60000000000LL;
     return RMSNORM_OK;
 }
 
@@ -110,7 +111,16 @@ int finish_cfg(OpCfg* c, void* stream) {
     return RMSNORM_OK;
 }
 
-int launched(cudaError_t e) {
+// Plans and launches, and reports. The plans' caches allocate host memory: no
+// exception leaves the C entry points.
+template <typename F>
+int launched(F run) {
+    cudaError_t e;
+    try {
+        e = run();
+    } catch (...) {
+        e = cudaErrorMemoryAllocation;
+    }
     if (e == cudaErrorNotSupported)
         return fail(RMSNORM_ERR_UNSUPPORTED, "the vector kernels cannot take these sizes, strides or alignments");
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
@@ -234,7 +244,7 @@ extern "C" int rmsnorm_block_fwd(const rmsnorm_block_args_t* a, const rmsnorm_op
     const BlockP p{a->h, a->r, a->w_post, a->gate, a->w_pre, a->s, a->y, a->rstd_post, a->rstd_pre,
                    M, N, a->gate_rows, a->ldh, a->ldr, a->ldg, a->lds, a->ldy,
                    static_cast<float>(N), a->eps, a->offset, a->alpha, a->beta, a->dtype};
-    return launched(block_fwd_run(p, c));
+    return launched([&] { return block_fwd_run(p, c); });
 }
 
 extern "C" int rmsnorm_block_bwd_workspace_size(int64_t M, int64_t N, int dtype, int64_t* bytes) {
@@ -340,7 +350,7 @@ extern "C" int rmsnorm_block_bwd(const rmsnorm_block_args_t* a, const rmsnorm_bl
                       a->ldh, a->lds, a->ldg, g->lddy, g->ldds, g->lddh, g->lddr, g->lddg,
                       static_cast<float>(N), a->offset, a->alpha, a->beta, a->dtype,
                       static_cast<float*>(workspace)};
-    return launched(block_bwd_run(p, c));
+    return launched([&] { return block_bwd_run(p, c); });
 }
 
 // ---- rope ---------------------------------------------------------------------
@@ -471,7 +481,7 @@ extern "C" int rmsnorm_rope_fwd(const rmsnorm_rope_args_t* a, const rmsnorm_opti
     p.seg[0].out = heads_p(a->out_q);
     p.seg[1].in = heads_p(a->k);
     p.seg[1].out = heads_p(a->out_k);
-    return launched(rope_fwd_run(p, c));
+    return launched([&] { return rope_fwd_run(p, c); });
 }
 
 extern "C" int rmsnorm_rope_bwd_workspace_size(int32_t head_dim, int64_t* bytes) {
@@ -559,7 +569,7 @@ extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope
     p.seg[1].out = heads_p(g->dk);
     p.seg[1].x = heads_p(a->k);
     p.seg[1].dw = g->dw_k;
-    return launched(rope_bwd_run(p, c));
+    return launched([&] { return rope_bwd_run(p, c); });
 }
 
 extern "C" int rmsnorm_rope_steps(int32_t rotary_dim, double base, const rmsnorm_rope_scaling_t* sc,
@@ -712,7 +722,7 @@ extern "C" int rmsnorm_cache_write(const rmsnorm_cache_t* cache, const rmsnorm_h
     p.scales[1] = v ? cache->v_scales : nullptr;
     p.slot = slots;
     p.T = T;
-    return launched(cache_write_run(p, c));
+    return launched([&] { return cache_write_run(p, c); });
 }
 
 extern "C" int rmsnorm_cache_read(const rmsnorm_cache_t* cache, const int32_t* table, int64_t table_width,
@@ -760,5 +770,5 @@ extern "C" int rmsnorm_cache_read(const rmsnorm_cache_t* cache, const int32_t* t
     p.starts = starts;
     p.sequences = sequences;
     p.rows = rows;
-    return launched(cache_read_run(p, c));
+    return launched([&] { return cache_read_run(p, c); });
 }

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
         atomicOr(&g_block_status, 1u);
         // Rows below row + stages were issued and may still be landing.
         for (int k = row; k < row + g.stages && k < rows; ++k) {
-            mbar_wait_bounded(ring.bar(st), phase, g.limit);
+            mbar_wait_bounded(ring.bar(st), phase, g.drain);
             if (++st == g.stages) {
                 st = 0;
                 phase ^= 1;

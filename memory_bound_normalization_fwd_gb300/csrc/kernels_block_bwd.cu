@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
 
     int st = 0, parity = 0;
     uint32_t phase = 0;
-    bool dead = false;
-    int row = 0;
+    bool dead = false, lost = false;
+    int row = 0, dead_row = 0, dead_st = 0;
+    uint32_t dead_phase = 0;
     const f2 beta = f2_dup(p.beta);
     const float inv_n = 1.f / p.n;
     const float* rstd_post = p.rstd_post + r0;
@@ -213,7 +214,8 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             left = p.gate_rows;
             load_scale();
         }
-        if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
+        if (!(WIDE && dead) && !mbar_wait_bounded(ring.bar(st), phase, g.limit))
+            *(volatile unsigned int*)&sh.dead[team] = 1;
         const float k1 = k1_next, k2 = k2_next;
         if (row + 1 < rows) {  // the next row's, a global load ahead of its use
             if (post) k1_next = __ldg(rstd_post + row + 1);
@@ -265,24 +267,29 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
         float sums[3] = {f2_sum(us), f2_sum(aht), f2_sum(ahs)};
         team_sums3(sums, &parts[team][parity][0], team, t, g.T);
         parity ^= 1;
-        dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+        if (!dead && *(volatile unsigned int*)&sh.dead[team] != 0) {
+            dead = true;
+            dead_row = row;
+            dead_st = st;
+            dead_phase = phase;
+        }
         if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
         if (WIDE) {
             // Slot and barrier of this row, used again two rows on: a CTA sends a row's
-            // sums when all its threads have read those of the row before.
+            // sums when all its threads have read those of the row before. A CTA that
+            // gave up says so, stores nothing more, and so do the others from the next
+            // row on; but all of them send and receive to the last row, so that nothing
+            // is on its way to a CTA that has ended.
             const int slot = row & 1;
             const uint32_t bar = smem_u32(&peer_bars[slot]);
             if (t == 0) mbar_arrive_expect_tx(bar, 16u * g.cluster);
             if (t < g.cluster)
                 st_async_peer_f4(smem_u32(&peers[slot][rank]), bar, t, sums[0], sums[1], sums[2], dead ? 1.f : 0.f);
-            if (dead) break;
-            if (!mbar_wait_bounded(bar, (row >> 1) & 1, g.limit)) {
+            if (!lost && !mbar_wait_bounded(bar, (row >> 1) & 1, g.drain)) {
+                lost = true;
                 *(volatile unsigned int*)&sh.dead[team] = 1;
-                atomicOr(&g_block_bwd_status, 1u);
             }
-            // Added in rank order, so that all get the same. That another CTA has given
-            // up is acted on behind the next row's barrier, by all threads alike.
-            float4 x = peers[slot][0];
+            float4 x = peers[slot][0];  // added in rank order, so that all get the same
             for (int i = 1; i < g.cluster; ++i) {
                 const float4 z = peers[slot][i];
                 x.x += z.x;
@@ -294,8 +301,10 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             sums[1] = x.y;
             sums[2] = x.z;
             if (x.w != 0.f) *(volatile unsigned int*)&sh.dead[team] = 1;
+            if (dead) continue;
+        } else if (dead) {
+            break;
         }
-        if (dead) break;
         const float e2 = k2 * k2 * k2 * (sums[0] * inv_n);
         const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) * inv_n);
         const f2 me2 = f2_dup(-e2), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));
@@ -374,14 +383,14 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             phase ^= 1;
         }
     }
-    if (dead && t == 0) {
+    if ((dead || lost) && t == 0) {
         atomicOr(&g_block_bwd_status, 1u);
-        // Rows below row + stages were issued and may still be landing.
-        for (int k = row; k < row + g.stages && k < rows; ++k) {
-            mbar_wait_bounded(ring.bar(st), phase, g.limit);
-            if (++st == g.stages) {
-                st = 0;
-                phase ^= 1;
+        // Rows below dead_row + stages were issued and may still be landing.
+        for (int i = dead_row; dead && i < dead_row + g.stages && i < rows; ++i) {
+            mbar_wait_bounded(ring.bar(dead_st), dead_phase, g.drain);
+            if (++dead_st == g.stages) {
+                dead_st = 0;
+                dead_phase ^= 1;
             }
         }
     }

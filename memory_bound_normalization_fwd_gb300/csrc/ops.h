@@ -14,6 +14,7 @@ struct OpCfg {
     int variant = 0;  // RMSNORM_VARIANT_AUTO, _CTA (vector kernels) or _GENERIC (element-wise)
     int max_ctas = 0;
     bool pdl = true;
+    int64_t wait_limit_ns = 0;  // bound of a wait in the kernels that stage rows; 0: one second
     DeviceInfo dev;
     cudaStream_t stream = nullptr;
 };

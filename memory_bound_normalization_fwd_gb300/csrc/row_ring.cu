@@ -111,7 +111,8 @@ bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int m
     s.arrays = arrays;
     s.slots = 0;
     s.sums_at = 0;
-    s.limit = 2100000000LL;  // one second at the top SM clock
+    s.drain = 2100000000LL;  // one second at the top SM clock
+    s.limit = c.wait_limit_ns > 0 ? std::max<long long>(1, c.wait_limit_ns * 21 / 10) : s.drain;
     out->threads = teams * T;
     out->smem = static_cast<int>(stage * s.stages + static_cast<int64_t>(extra) * teams * T);
     return s.q < (int64_t(1) << 31);

@@ -35,6 +35,7 @@ struct RingShape {
     int64_t slots;    // partial rows per workspace area (backward)
     int sums_at;      // byte offset behind the rings (backward)
     long long limit;  // bound of a wait in SM cycles
+    long long drain;  // of the wait for copies in flight before a team that gave up ends
 };
 
 // A 16-byte vector of shared memory by its 32-bit shared address. (The address

@@ -355,6 +355,52 @@ def test_the_workspace_is_as_large_as_it_says(M, N):
     assert e.value.status in (-5, -11)
 
 
+def test_the_vector_kernels_can_be_asked_for():
+    d = _make(20, 512, "bf16", 81)
+    for N in (512, 8192):
+        d = _make(20, N, "bf16", 81)
+        want = B.block_fwd(d["h"], d["r"], d["w_post"], d["w_pre"])
+        got = B.block_fwd(d["h"], d["r"], d["w_post"], d["w_pre"], variant="cta")
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    d = _make(20, 511, "bf16", 81)
+    with pytest.raises(B.RMSNormError) as e:
+        B.block_fwd(d["h"], d["r"], d["w_post"], d["w_pre"], variant="cta")
+    assert e.value.status == -8
+
+
+@pytest.mark.parametrize("M,N,dtype", [(500, 512, "bf16"), (500, 4096, "bf16"), (500, 8192, "bf16"),
+                                       (20000, 512, "bf16"), (8192, 4096, "bf16"), (4096, 8192, "bf16"),
+                                       (4096, 8192, "fp32")])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(M, N, dtype):
+    # With a limit of a few cycles a wait for a staged row that has not landed ends
+    # at once: the kernel gives up, in bounds, and says so. Where every row happens to
+    # land before it is waited for, the call is right instead. Which of the two is a
+    # matter of timing; that it is one of them is not.
+    d = _make(M, N, dtype, 91, gate_rows=100)
+    args = (d["w_post"], d["w_pre"], d["gate"], 100)
+    s, y, a, b = B.block_fwd(d["h"], d["r"], *args)
+    want = B.block_bwd(d["h"], s, a, b, d["dy"], d["ds"], *args)
+    assert B.rmsnorm_check_device_status(0) == 0
+
+    def short(call, right):
+        got = call()
+        status = B.rmsnorm_check_device_status(0)
+        assert status in (0, -7)
+        if status == 0:
+            for p, q in zip(got, right):
+                assert torch.equal(p, q)
+        assert B.rmsnorm_check_device_status(0) == 0
+
+    short(lambda: B.block_fwd(d["h"], d["r"], *args, wait_limit_ns=1), (s, y, a, b))
+    short(lambda: B.block_bwd(d["h"], s, a, b, d["dy"], d["ds"], *args, wait_limit_ns=1), want)
+    for p, q in zip((s, y, a, b), B.block_fwd(d["h"], d["r"], *args)):
+        assert torch.equal(p, q)
+    for p, q in zip(want, B.block_bwd(d["h"], s, a, b, d["dy"], d["ds"], *args)):
+        assert torch.equal(p, q)
+    assert B.rmsnorm_check_device_status(0) == 0
+
+
 def test_refused_tensors():
     d = _make(4, 64, "bf16", 71)
     ok = dict(h=d["h"], r=d["r"], w_post=d["w_post"], w_pre=d["w_pre"])
