@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
     int st = 0, parity = 0;
     uint32_t phase = 0;
     bool dead = false, lost = false;
-    int row = 0, dead_row = 0, dead_st = 0;
-    uint32_t dead_phase = 0;
+    int row = 0, dead_row = 0;
     const f2 beta = f2_dup(p.beta);
     const float inv_n = 1.f / p.n;
     const float* rstd_post = p.rstd_post + r0;
@@ -267,11 +266,9 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
         float sums[3] = {f2_sum(us), f2_sum(aht), f2_sum(ahs)};
         team_sums3(sums, &parts[team][parity][0], team, t, g.T);
         parity ^= 1;
-        if (!dead && *(volatile unsigned int*)&sh.dead[team] != 0) {
-            dead = true;
-            dead_row = row;
-            dead_st = st;
-            dead_phase = phase;
+        if (!(WIDE && dead)) {
+            dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+            if (WIDE) dead_row = row;
         }
         if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
         if (WIDE) {
@@ -385,12 +382,14 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
     }
     if ((dead || lost) && t == 0) {
         atomicOr(&g_block_bwd_status, 1u);
-        // Rows below dead_row + stages were issued and may still be landing.
+        // Rows below the one given up at + stages were issued and may still be landing
+        // (its stage and phase are still the current ones).
+        if (!WIDE) dead_row = row;
         for (int i = dead_row; dead && i < dead_row + g.stages && i < rows; ++i) {
-            mbar_wait_bounded(ring.bar(dead_st), dead_phase, g.drain);
-            if (++dead_st == g.stages) {
-                dead_st = 0;
-                dead_phase ^= 1;
+            mbar_wait_bounded(ring.bar(st), phase, g.drain);
+            if (++st == g.stages) {
+                st = 0;
+                phase ^= 1;
             }
         }
     }
