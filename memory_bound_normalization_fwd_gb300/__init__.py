@@ -1,5 +1,8 @@
 """GB300 (sm_103a) RMSNorm forward: y = x * rsqrt(mean(x^2) + eps) * (offset + w),
-with the per-row fp32 rstd kept for backward.
+with the per-row fp32 rstd kept for backward, and the operators a transformer block
+runs next to it: block_fwd / block_bwd (norms around a block, gate, residual),
+rope_fwd / rope_bwd (rotary positions with head norms), Cache, cache_write and
+cache_read (k and v in 8 or 4 bits).
 
 The computation runs in hand-written CUDA kernels behind the C ABI of
 ``include/rmsnorm.h`` (``librmsnorm_gb300.so``); this package is the ctypes
