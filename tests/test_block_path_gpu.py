@@ -113,3 +113,81 @@ def test_decoding_from_the_cache_one_token_at_a_time(fmt):
     whole = B.rope_fwd(qkv[:, :HQ], qkv[:, HQ:HQ + HK], steps, pos, w["w_q"], w["w_k"], offset=1.0)[1]
     assert torch.equal(torch.cat(keys), whole)
     assert B.rmsnorm_check_device_status(0) == 0
+
+
+def test_calls_from_several_threads_on_their_own_streams():
+    # Four host threads, each with its stream, tensors and cache, all three operators
+    # in turn: the results of the same calls one after another.
+    import threading
+    w = [_weights(10 + i, torch.bfloat16) for i in range(4)]
+    steps, _ = B.rope_steps(D, device=DEV)
+    pos = torch.arange(S, device=DEV)
+    table = torch.arange(3, dtype=torch.int32, device=DEV).view(1, 3)
+    cu = torch.tensor([0, S], dtype=torch.int32, device=DEV)
+
+    def calls(x, stream):
+        out = []
+        cache = B.Cache(3, 16, HK, D)
+        for _ in range(5):
+            s, y, a, b = B.block_fwd(x["x"], x["ds"], x["w_post"], x["w_pre"], x["gate"], stream=stream)
+            out += [s, y, a, b]
+            out += B.block_bwd(x["x"], s, a, b, x["dy"], x["ds"], x["w_post"], x["w_pre"], x["gate"], stream=stream)
+            qk = x["x"].view(S, 4, D)
+            q, k, rq, rk = B.rope_fwd(qk[:, :2], qk[:, 2:], steps, pos, x["w_q"], x["w_k"], stream=stream)
+            out += [q, k, rq, rk]
+            out += B.rope_bwd(q, k, steps, pos, qk[:, :2], qk[:, 2:], rq, rk, x["w_q"], x["w_k"], stream=stream)
+            B.cache_write(cache, k, q, pos, stream=stream)
+            out += B.cache_read(cache, table, cu, S, stream=stream)
+        stream.synchronize()
+        return out
+
+    streams = [torch.cuda.Stream() for _ in w]
+    torch.cuda.synchronize()
+    want = [calls(x, streams[0]) for x in w]
+    got = [None] * len(w)
+
+    def work(i):
+        got[i] = calls(w[i], streams[i])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(w))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert b is not None and len(a) == len(b)
+        for p, q in zip(a, b):
+            assert torch.equal(p, q)
+
+
+def test_two_captured_graphs_with_workspaces_of_their_own():
+    # Two training steps captured with their own workspaces, replayed at once on two
+    # streams: the results of each replayed alone.
+    w = [_weights(20 + i, torch.bfloat16) for i in range(2)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in w]
+    for x in w:
+        s, _, a, b = B.block_fwd(x["x"], x["ds"], x["w_post"], x["w_pre"], x["gate"])
+        ws = torch.empty(B.rmsnorm_block_bwd_workspace_size(S, N, B.BF16), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = B.block_bwd(x["x"], s, a, b, x["dy"], x["ds"], x["w_post"], x["w_pre"], x["gate"], workspace=ws)
+        graphs.append((g, ws, s, a, b))
+        outs.append(o)
+    alone = []
+    for (g, *_), o in zip(graphs, outs):
+        g.replay()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in o])
+        for t in o:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, *_), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, a in zip(outs, alone):
+        for p, q in zip(o, a):
+            assert torch.equal(p, q)
