@@ -723,6 +723,8 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
         dwbp = dwb.data_ptr()
     if workspace is None:
         workspace = _workspace(h, rmsnorm_block_bwd_workspace_size, M, N, code)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
     args = _BLOCK.pack(160, code, M, N, gate_rows, hp, 0, wpost, gp, wpre, sp, 0, ap, bp,
                        ldh, 0, ldg, lds, 0, 0.0, offset, alpha, beta)
     grads = _BLOCK_GRADS.pack(104, 0, dyp, dsp, dhp, drp, dgp, dwap, dwbp, lddy, ldds, lddh, lddr,
@@ -923,6 +925,8 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
     grads = _ROPE_GRADS.pack(152, 0, *gq, *gk, *oq, *ok, wqp, wkp)
     ws_ptr = ws_bytes = 0
     if workspace is not None:
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     rc = (_lib or lib()).rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
                                           _opt(make_options(**options)) if options else None,

@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(256) cache_write_generic_kernel(const CacheP p
     const int64_t units = p.T * p.heads * p.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < units; u += step) {
-        const int64_t t = u / (p.heads * p.groups);
-        const int rest = static_cast<int>(u - t * (p.heads * p.groups));
-        const int h = rest / p.groups, g = rest - h * p.groups;
+        const int64_t per = static_cast<int64_t>(p.heads) * p.groups;
+        const int64_t t = u / per, rest = u - t * per;
+        const int h = static_cast<int>(rest / p.groups), g = static_cast<int>(rest - static_cast<int64_t>(h) * p.groups);
         const int64_t slot = p.slot[t];
         if (slot < 0) continue;
         if (slot >= p.slots) {
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(256) cache_read_generic_kernel(const CacheP p)
     const int64_t units = p.rows * p.heads * p.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < units; u += step) {
-        const int64_t i = u / (p.heads * p.groups);
-        const int rest = static_cast<int>(u - i * (p.heads * p.groups));
-        const int h = rest / p.groups, g = rest - h * p.groups;
+        const int64_t per = static_cast<int64_t>(p.heads) * p.groups;
+        const int64_t i = u / per, rest = u - i * per;
+        const int h = static_cast<int>(rest / p.groups), g = static_cast<int>(rest - static_cast<int64_t>(h) * p.groups);
         const int64_t slot = read_slot(p, p.cu_rows, i);
         if (slot == -1) continue;
         if (slot < 0 && rest == 0) atomicOr(&g_cache_status, 1u);

@@ -401,6 +401,38 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(M, N, dtype
     assert B.rmsnorm_check_device_status(0) == 0
 
 
+@pytest.mark.slow
+@pytest.mark.parametrize("M,N", [(530000, 4096), (2800000, 777)])
+def test_offsets_past_32_bits(M, N):
+    # Tensors of more than 2^31 elements made of 1000 rows again and again: every
+    # thousand rows of the outputs are alike, and the sums over rows are theirs.
+    base = _make(1000, N, "bf16", 101)
+    want = B.block_fwd(base["h"], base["r"], base["w_post"], base["w_pre"])
+
+    def tall(t):
+        return t.expand(M // 1000, *t.shape).reshape(M, N)
+
+    h, r = tall(base["h"]), tall(base["r"])
+    s, y, a, b = B.block_fwd(h, r, base["w_post"], base["w_pre"], s=r, y=None)
+    for got, w in ((s, want[0]), (y, want[1]), (a, want[2]), (b, want[3])):
+        got = got.view(M // 1000, *w.shape)
+        assert torch.equal(got[0], w) and torch.equal(got[-1], w) and torch.equal(got[M // 2000], w)
+    dy, ds = tall(base["dy"]), tall(base["ds"])
+    one = B.block_bwd(base["h"], want[0], want[2], want[3], base["dy"], base["ds"], base["w_post"], base["w_pre"])
+    dh, dr, _, dwa, dwb = B.block_bwd(h, s, a, b, dy, ds, base["w_post"], base["w_pre"], dh=dy, dr=ds)
+    for got, w in ((dh, one[0]), (dr, one[1])):
+        got = got.view(M // 1000, *w.shape)
+        assert torch.equal(got[0], w) and torch.equal(got[-1], w) and torch.equal(got[M // 2000], w)
+    # The sums: the thousand rows' times M / 1000, each within TAU of its magnitudes
+    # (the magnitudes of the sum over rows are M / 1000 times the thousand rows').
+    _, mag = U.block_bwd(base["h"], want[0], want[2], want[3], base["dy"], base["ds"], base["w_post"],
+                         base["w_pre"], None, 0, 0.0, 1.0, 1.0)
+    for got, w, name in ((dwa, one[3], "dw_post"), (dwb, one[4], "dw_pre")):
+        err = (got.double() / (M // 1000) - w.double()).abs()
+        # a chain of M / 152 additions in fp32 per CTA: at most that many half steps of the sum
+        assert bool((err <= (2 * U.TAU + M / 152 * 2.0 ** -24) * mag[name]).all())
+
+
 def test_refused_tensors():
     d = _make(4, 64, "bf16", 71)
     ok = dict(h=d["h"], r=d["r"], w_post=d["w_post"], w_pre=d["w_pre"])

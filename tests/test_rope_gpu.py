@@ -278,6 +278,26 @@ def test_workspace_of_the_backward():
     assert e.value.status == -11
 
 
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    T, hq, D = 530000, 32, 128
+    d = _make((1000,), hq, 0, D, D, "bf16", 31)
+    want = B.rope_fwd(d["q"], None, d["steps"], d["positions"], d["w_q"])
+    n = T // 1000
+    q = d["q"].expand(n, *d["q"].shape).reshape(T, hq, D)
+    pos = d["positions"].expand(n, 1000).reshape(T)
+    keep = q.clone()
+    out, _, rstd, _ = B.rope_fwd(q, None, d["steps"], pos, d["w_q"], q_out=q)
+    for got, w in ((out, want[0]), (rstd, want[2])):
+        got = got.view(n, *w.shape)
+        assert torch.equal(got[0], w) and torch.equal(got[-1], w) and torch.equal(got[n // 2], w)
+    one = B.rope_bwd(d["dq"], None, d["steps"], d["positions"], d["q"], None, want[2], None, d["w_q"])
+    dq = d["dq"].expand(n, *d["dq"].shape).reshape(T, hq, D)
+    got, _, _, _ = B.rope_bwd(dq, None, d["steps"], pos, keep, None, rstd, None, d["w_q"], dq=dq)
+    got = got.view(n, *one[0].shape)
+    assert torch.equal(got[0], one[0]) and torch.equal(got[-1], one[0]) and torch.equal(got[n // 2], one[0])
+
+
 def test_refused_tensors():
     d = _make((4,), 2, 1, 64, 64, "bf16", 21)
     ok = dict(q=d["q"], k=d["k"], steps=d["steps"], positions=d["positions"], w_q=d["w_q"], w_k=d["w_k"])
