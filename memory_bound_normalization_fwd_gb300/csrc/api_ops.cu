@@ -607,9 +607,18 @@ extern "C" int rmsnorm_rope_steps(int32_t rotary_dim, double base, const rmsnorm
         auto index = [&](double turns) {
             return R * std::log(sc->length / (turns * two_pi)) / (2.0 * std::log(base));
         };
-        lo = std::fmax(std::floor(index(sc->beta_fast)), 0.0);
-        hi = std::fmin(std::ceil(index(sc->beta_slow)), R - 1.0);
-        if (hi == lo) hi += 0.001;
+        lo = std::floor(index(sc->beta_fast));
+        hi = std::ceil(index(sc->beta_slow));
+        if (hi <= 0.0) {  // every pair is under beta_slow turns
+            lo = -2.0;
+            hi = -1.0;
+        } else if (lo > R - 1.0) {  // every pair is above beta_fast turns
+            hi = lo + 1.0;
+        } else {
+            lo = std::fmax(lo, 0.0);
+            hi = std::fmin(hi, R - 1.0);
+            if (hi == lo) hi += 0.001;
+        }
     }
     for (int i = 0; i < half; ++i) {
         double f = std::pow(base, -2.0 * i / R);  // radians per position

@@ -151,6 +151,18 @@ def test_scaled_steps():
         assert f == pytest.approx(want, rel=1e-12)
 
 
+@pytest.mark.parametrize("R,base,length,divided", [
+    (64, 1e4, 1.0, True), (64, 1e4, 6.0, True), (128, 1e4, 0.01, True),   # under one turn, all
+    (64, 100.0, 1e9, False), (128, 2.0, 1e5, False), (2, 1e4, 1e9, False),  # above 32 turns, all
+])
+def test_yarn_where_all_pairs_are_on_one_side_of_the_ramp(R, base, length, divided):
+    steps, _ = B.rope_steps(R, base, dict(kind="yarn", factor=4.0, length=length), device="cpu")
+    for i, f in enumerate(_freq(steps)):
+        turns = length * base ** (-2.0 * i / R) / (2 * math.pi)
+        assert turns <= 1 if divided else turns >= 32
+        assert f == pytest.approx(base ** (-2.0 * i / R) / (4 if divided else 1), rel=1e-13)
+
+
 @pytest.mark.parametrize("R,base,scaling,code", [
     (0, 1e4, None, -2), (3, 1e4, None, -2), (-2, 1e4, None, -2), (1 << 17, 1e4, None, -2),
     (64, 1.0, None, -4), (64, float("nan"), None, -4), (64, float("inf"), None, -4),
