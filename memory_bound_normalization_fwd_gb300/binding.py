@@ -592,7 +592,7 @@ def _gate(gate, gate_rows, dtype, device, M, N):
     _refuse(gate, "gate", None, dtype, device)
     if gate.shape[-1] != N:
         raise ValueError(f"gate must have {N} columns, got {tuple(gate.shape)}")
-    G = gate.numel() // N
+    G = gate.numel() // N if N else 0
     if not gate_rows:
         gate_rows = max(M, 1) if gate.dim() == 1 or G == 1 else M // G if G and M % G == 0 else 0
     if gate_rows < 1 or -(-M // gate_rows) != G and M > 0:

@@ -5,6 +5,7 @@
 
 #include "ops.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace rmsn {
@@ -16,7 +17,7 @@ bool dtype_ok(int dtype) {
     return dtype == RMSNORM_DTYPE_BF16 || dtype == RMSNORM_DTYPE_FP16 || dtype == RMSNORM_DTYPE_FP32;
 }
 
-// A strided array: up to four dimensions of (count, stride in bytes) around
+// A strided array: up to three dimensions of (count, stride in bytes) around
 // `inner` contiguous bytes. For overlap checks.
 struct View {
     uintptr_t base = 0;
@@ -186,6 +187,12 @@ int block_shapes(const rmsnorm_block_args_t* a, bool need_r) {
     return RMSNORM_OK;
 }
 
+// Rows of h per gate row as the kernels take them: what lies past the last row
+// is left out, so that a product with it stays small (more than one stays so).
+int64_t gate_rows_of(const rmsnorm_block_args_t* a) {
+    return a->gate ? std::min(a->gate_rows, std::max<int64_t>(a->M, 2)) : 0;
+}
+
 int check_ld(const char* name, int64_t ld, int64_t rows, int64_t N, int64_t eb) {
     if (ld < N)
         return fail(RMSNORM_ERR_SHAPE, "the row stride of %s is %lld, below N", name,
@@ -214,7 +221,8 @@ extern "C" int rmsnorm_block_fwd(const rmsnorm_block_args_t* a, const rmsnorm_op
     if (a->M == 0) return RMSNORM_OK;
     if (!a->h || !a->r || !a->s) return fail(RMSNORM_ERR_NULL, "h, r and s must be non-NULL");
     const int64_t eb = elem_bytes(a->dtype), N = a->N, M = a->M;
-    const int64_t grows = a->gate ? (M + a->gate_rows - 1) / a->gate_rows : 0;
+    const int64_t gate_rows = gate_rows_of(a);
+    const int64_t grows = a->gate ? (M + gate_rows - 1) / gate_rows : 0;
     if ((rc = check_ld("h", a->ldh, M, N, eb)) || (rc = check_ld("r", a->ldr, M, N, eb)) ||
         (rc = check_ld("s", a->lds, M, N, eb)) ||
         (a->y && (rc = check_ld("y", a->ldy, M, N, eb))) ||
@@ -242,7 +250,7 @@ extern "C" int rmsnorm_block_fwd(const rmsnorm_block_args_t* a, const rmsnorm_op
     rc = finish_cfg(&c, stream);
     if (rc != RMSNORM_OK) return rc;
     const BlockP p{a->h, a->r, a->w_post, a->gate, a->w_pre, a->s, a->y, a->rstd_post, a->rstd_pre,
-                   M, N, a->gate_rows, a->ldh, a->ldr, a->ldg, a->lds, a->ldy,
+                   M, N, gate_rows, a->ldh, a->ldr, a->ldg, a->lds, a->ldy,
                    static_cast<float>(N), a->eps, a->offset, a->alpha, a->beta, a->dtype};
     return launched([&] { return block_fwd_run(p, c); });
 }
@@ -299,7 +307,8 @@ extern "C" int rmsnorm_block_bwd(const rmsnorm_block_args_t* a, const rmsnorm_bl
         return fail(RMSNORM_ERR_NULL, "s and rstd_pre must be given with w_pre");
     if (a->w_post && !a->rstd_post) return fail(RMSNORM_ERR_NULL, "rstd_post must be given with w_post");
     const void* s = a->w_pre ? a->s : nullptr;
-    const int64_t grows = a->gate ? (M + a->gate_rows - 1) / a->gate_rows : 0;
+    const int64_t gate_rows = gate_rows_of(a);
+    const int64_t grows = a->gate ? (M + gate_rows - 1) / gate_rows : 0;
     if ((rc = check_ld("h", a->ldh, M, N, eb)) || (s && (rc = check_ld("s", a->lds, M, N, eb))) ||
         (g->dy && (rc = check_ld("dy", g->lddy, M, N, eb))) ||
         (g->ds && (rc = check_ld("ds", g->ldds, M, N, eb))) ||
@@ -346,7 +355,7 @@ extern "C" int rmsnorm_block_bwd(const rmsnorm_block_args_t* a, const rmsnorm_bl
     for (const Named& i : ins)
         if (meet(ws, i.v)) return fail(RMSNORM_ERR_OVERLAP, "the workspace overlaps %s", i.name);
     const BlockBwdP p{a->h, s, a->w_post, a->gate, a->w_pre, a->rstd_post, a->rstd_pre, g->dy, g->ds,
-                      g->dh, g->dr, g->dgate, g->dw_post, g->dw_pre, M, N, a->gate_rows,
+                      g->dh, g->dr, g->dgate, g->dw_post, g->dw_pre, M, N, gate_rows,
                       a->ldh, a->lds, a->ldg, g->lddy, g->ldds, g->lddh, g->lddr, g->lddg,
                       static_cast<float>(N), a->offset, a->alpha, a->beta, a->dtype,
                       static_cast<float*>(workspace)};

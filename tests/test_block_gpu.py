@@ -100,6 +100,28 @@ def test_parity_over_parts(N, post, pre, gate_rows):
         _both(67, N, "bf16", gate_rows + N, post, pre, gate_rows, 1.0, -0.75, 1.25, opts)
 
 
+@pytest.mark.parametrize("N", [264, 777, 8208 + 3])
+@pytest.mark.parametrize("M", [1, 67])
+def test_gate_rows_far_past_the_last_row(M, N):
+    d = _make(M, N, "bf16", 3, gate_rows=1000)
+    for opts in _variants():
+        want = None
+        for gate_rows in (1000, 1 << 40, 1 << 62, (1 << 63) - 1):
+            s, y, a, b = B.block_fwd(d["h"], d["r"], d["w_post"], d["w_pre"], d["gate"], gate_rows, **opts)
+            got = (s, y, *B.block_bwd(d["h"], s, a, b, d["dy"], d["ds"], d["w_post"], d["w_pre"], d["gate"],
+                                      gate_rows, **opts))
+            want = want or got
+            assert all(torch.equal(g, w) for g, w in zip(got, want)), (gate_rows, opts)
+
+
+def test_no_columns():
+    x, w = torch.empty(2, 0, device=DEV), torch.empty(0, device=DEV)
+    with pytest.raises(B.RMSNormError):
+        B.block_fwd(x, x, w, w, gate=w)
+    with pytest.raises(B.RMSNormError):
+        B.block_fwd(x, x, w, w)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("max_ctas", [1, 3, 7, 50])
 @pytest.mark.parametrize("gate_rows", [1, 2, 3, 16, 25, 100])
