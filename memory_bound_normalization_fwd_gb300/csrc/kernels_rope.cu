@@ -697,10 +697,14 @@ RopeUnits units_of(RopeP* p, const OpCfg& c, int threads, int ctas_per_sm) {
     const int64_t teams = threads / g.L, tokens = p->batch * p->seq;
     int64_t cap = static_cast<int64_t>(c.dev.sm_count) * ctas_per_sm;
     if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(c.max_ctas, 2));
-    // Units of as many heads as leave every team about eight units, so that the
-    // teams end together; a unit of many heads costs fewer angles.
+    // Units of as many heads as leave every team one, and of eight at most, so that the
+    // teams of long calls end together; a unit of many heads costs fewer angles (GB300,
+    // us, at eight units per team and up to 16 heads / one and up to 16 / one and up to
+    // 8: 8169 tokens of 25 heads of 128 bf16 with norms 31.6 / 22.8 / 23.6, 7391 of 24 of
+    // 80 29.9 / 18.0 / 17.9, 16384 of 40 of 128 59.0 / 59.0 / 56.7, its backward 82.8 /
+    // 84.2 / 82.9).
     const int64_t heads = p->seg[0].heads + p->seg[1].heads;
-    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(16, tokens * heads / (8 * cap * teams)));
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(8, tokens * heads / (cap * teams)));
     int64_t work[2] = {0, 0};
     for (int k = 0; k < 2; ++k) {
         const int64_t n = p->seg[k].heads;
