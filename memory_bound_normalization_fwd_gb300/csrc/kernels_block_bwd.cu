@@ -530,12 +530,187 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
     pdl_launch_dependents();
 }
 
-// Rows that are not whole vectors (any N, stride and alignment), of up to 1024 V
+// Rows that are not whole vectors (any N, stride and alignment), of up to 512 V
 // columns: a CTA per range of rows, element loads, a thread's columns t, t + T, ...
+// of the row, its scales and the sums in registers (dw_post's sums with a gate row
+// for several rows in shared memory). The next row is loaded into registers while
+// this one is reduced, and a load is one instruction (GB300, us, against the kernel
+// below: 18503x708 bf16 105 -> 72, 23493x987 fp32 161 -> 112, 16384x777 bf16 117 ->
+// 76).
+template <int DT, int V>
+__global__ void __launch_bounds__(512) block_bwd_columns_kernel(const BlockBwdP p, int64_t slots) {
+    using Raw = typename Elem<DT>::T;
+    extern __shared__ __align__(16) float post[];  // [V][T]
+    __shared__ __align__(16) float part[2][4 * kMaxTeamWarps];
+    int parity = 0;
+    const int t = threadIdx.x, T = blockDim.x, N = static_cast<int>(p.N);
+    const int64_t G = gridDim.x, b = blockIdx.x, pitch = block_bwd_pitch(p.N);
+    const int64_t r0 = range_begin(b, G, p.M), r1 = range_begin(b + 1, G, p.M);
+    const bool per_element = p.gate && p.gate_rows == 1;
+    const bool grouped = p.gate && !per_element;
+    const float inv_n = 1.f / p.n;
+    Raw rh[V], rs[V], rdy[V], rds[V];
+    // Byte offsets of the thread's columns (past the row's end: of the last one): a
+    // row's base is the same for all threads, and a load is one instruction.
+    uint32_t off[V];
+    bool in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        in[v] = v * T + t < N;
+        off[v] = static_cast<uint32_t>(min(v * T + t, N - 1)) * static_cast<uint32_t>(sizeof(Raw));
+    }
+    auto load_raw = [&](const void* x, int64_t base, Raw (&out)[V]) {
+        const char* q = static_cast<const char*>(x) + base * static_cast<int64_t>(sizeof(Raw));
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = *reinterpret_cast<const Raw*>(q + off[v]);
+    };
+    auto store = [&](void* x, int64_t base, int v, float f) {
+        char* q = static_cast<char*>(x) + base * static_cast<int64_t>(sizeof(Raw));
+        *reinterpret_cast<Raw*>(q + off[v]) = Elem<DT>::store(f);
+    };
+    auto fetch = [&](int64_t row) {
+        load_raw(p.h, row * p.ldh, rh);
+        if (p.ds) load_raw(p.ds, row * p.ldds, rds);
+        if (p.w_pre) {
+            load_raw(p.s, row * p.lds, rs);
+            load_raw(p.dy, row * p.lddy, rdy);
+        }
+    };
+    auto unpacked = [&](const Raw (&x)[V], float (&out)[V]) {  // zero past the row's end
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = in[v] ? Elem<DT>::load(x[v]) : 0.f;
+    };
+    for (int i = t; i < 2 * 4 * kMaxTeamWarps; i += T) part[0][i] = 0.f;
+    __syncthreads();
+    pdl_wait();
+    fetch(r0);
+    float P[V], pre[V];  // P: sums of t h rstd_post (times the gate where a row has its own)
+    float a[V], wpre[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        P[v] = pre[v] = wpre[v] = 0.f;
+        if (grouped) post[v * T + t] = 0.f;
+    }
+    if (p.w_pre) {
+        load_columns<DT, V>(p.w_pre, 0, t, T, N, wpre);
+#pragma unroll
+        for (int v = 0; v < V; ++v) wpre[v] += p.offset;
+    }
+    int64_t grow = grouped ? r0 / p.gate_rows : 0;
+    int64_t left = grouped ? (grow + 1) * p.gate_rows - r0 : 0;
+    float k1_next = p.w_post ? __ldg(p.rstd_post + r0) : 1.f;
+    float k2_next = p.w_pre ? __ldg(p.rstd_pre + r0) : 0.f;
+    // alpha (offset + w_post) of the thread's columns.
+    auto post_scale = [&](float (&o)[V]) {
+        if (p.w_post) load_columns<DT, V>(p.w_post, 0, t, T, N, o);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = p.w_post ? p.alpha * (p.offset + o[v]) : p.alpha;
+    };
+    // a: times the gate row, but where each row has its own.
+    auto load_scale = [&]() {
+        post_scale(a);
+        if (!grouped) return;
+        float q[V];
+        load_columns<DT, V>(p.gate, grow * p.ldg, t, T, N, q);
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] *= q[v];
+    };
+    load_scale();
+    for (int64_t row = r0; row < r1; ++row) {
+        const float k1 = k1_next, k2 = k2_next;
+        if (row + 1 < r1) {
+            if (p.w_post) k1_next = __ldg(p.rstd_post + row + 1);
+            if (p.w_pre) k2_next = __ldg(p.rstd_pre + row + 1);
+        }
+        float t0[V], h[V], s[V], q[V], sums[3] = {0.f, 0.f, 0.f};
+        unpacked(rh, h);
+        if (per_element) {
+            Raw x[V];
+            load_raw(p.gate, row * p.ldg, x);
+            unpacked(x, q);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            t0[v] = s[v] = 0.f;
+            if (!per_element) q[v] = 1.f;
+        }
+        if (p.ds) unpacked(rds, t0);
+        if (p.w_pre) {
+            float dy[V];
+            unpacked(rs, s);
+            unpacked(rdy, dy);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float u = dy[v] * wpre[v];
+                t0[v] = fmaf(k2, u, t0[v]);
+                sums[0] = fmaf(u, s[v], sums[0]);
+                pre[v] = fmaf(dy[v], s[v] * k2, pre[v]);
+            }
+        }
+        if (row + 1 < r1) fetch(row + 1);
+        if (p.w_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float ah = a[v] * q[v] * h[v];
+                sums[1] = fmaf(ah, t0[v], sums[1]);
+                sums[2] = fmaf(ah, s[v], sums[2]);
+            }
+        }
+        team_sums3(sums, &part[parity][0], 0, t, T);
+        parity ^= 1;
+        const float e = k2 * k2 * k2 * (sums[0] * inv_n);
+        const float f = k1 * k1 * (fmaf(-e, sums[2], sums[1]) * inv_n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            t0[v] = fmaf(-e, s[v], t0[v]);
+            const float th = t0[v] * (h[v] * k1);
+            if (!in[v]) continue;
+            const float aq = a[v] * q[v];
+            store(p.dr, row * p.lddr, v, p.beta * t0[v]);
+            store(p.dh, row * p.lddh, v, p.w_post ? k1 * fmaf(aq, t0[v], -h[v] * f) : aq * t0[v]);
+            if (per_element) store(p.dgate, row * p.lddg, v, a[v] * th);
+            P[v] = fmaf(th, q[v], P[v]);
+        }
+        if (grouped && (--left == 0 || row + 1 == r1)) {
+            const int64_t first = grow * p.gate_rows;
+            const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
+            const bool whole = first >= r0 && last <= r1;
+            float* out = partial(p.ws, first > r0 ? 3 : 2, b, slots, pitch);
+            load_columns<DT, V>(p.gate, grow * p.ldg, t, T, N, q);
+            post_scale(t0);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = v * T + t;
+                if (j < N) {
+                    post[j] = fmaf(P[v], q[v], post[j]);
+                    if (whole) store1<DT>(p.dgate, grow * p.lddg + j, t0[v] * P[v]);
+                    else out[j] = P[v];
+                }
+                P[v] = 0.f;
+            }
+            ++grow;
+            left = p.gate_rows;
+            if (row + 1 < r1) load_scale();
+        }
+    }
+    pdl_launch_dependents();
+    float* acc_post = partial(p.ws, 0, b, slots, pitch);
+    float* acc_pre = partial(p.ws, 1, b, slots, pitch);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int j = v * T + t;
+        if (j >= N) continue;
+        if (p.w_post) acc_post[j] = p.alpha * (grouped ? post[j] : P[v]);
+        if (p.w_pre) acc_pre[j] = pre[v];
+    }
+}
+
+// The same for longer rows of up to 1024 V columns, whose next row and scales would
+// not fit into registers (4096x3001 bf16 106 us, with them 152): a CTA per range of rows, element loads, a thread's columns t, t + T, ...
 // of the row and of the sums in registers (dw_post's with a gate row for several
 // rows in shared memory).
 template <int DT, int V>
-__global__ void __launch_bounds__(1024) block_bwd_columns_kernel(const BlockBwdP p, int64_t slots) {
+__global__ void __launch_bounds__(1024) block_bwd_wide_columns_kernel(const BlockBwdP p, int64_t slots) {
     extern __shared__ __align__(16) float post[];  // [V][T]
     __shared__ float part[2 * 3 * 32];
     int parity = 0;
@@ -677,9 +852,9 @@ __global__ void __launch_bounds__(1024) block_bwd_columns_kernel(const BlockBwdP
 template <int DT>
 cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G, int64_t R);
 
-template <int DT, int V>
+template <int DT, int V, bool WIDE>
 cudaError_t launch_columns(const BlockBwdP& p, const OpCfg& c) {
-    auto fn = block_bwd_columns_kernel<DT, V>;
+    auto fn = WIDE ? block_bwd_wide_columns_kernel<DT, V> : block_bwd_columns_kernel<DT, WIDE ? 4 : V>;
     const int T = static_cast<int>((p.N + V * 32 - 1) / (V * 32)) * 32;
     const int smem = p.gate && p.gate_rows > 1 ? V * T * 4 : 0;  // at most 32 KB
     const int occ = occupancy(reinterpret_cast<const void*>(fn), T, smem);
@@ -690,21 +865,56 @@ cudaError_t launch_columns(const BlockBwdP& p, const OpCfg& c) {
 }
 
 // Sums of the partial rows in order: dw_post and dw_pre over the G CTAs, and
-// the gate rows that more than one of the R ranges worked on. A CTA sums 32
-// vectors of 4 columns: its 16 warps take every sixteenth partial row, eight
-// loads in flight each, and meet in shared memory in warp order. blockIdx.y: 0
-// dw_post, 1 dw_pre, then gate rows.
+// the gate rows that more than one of the R ranges worked on. Latency is what this
+// launch costs, so a CTA sums 32 columns only: groups of eight threads, as many as
+// there are eights of partial rows (16 to 64), take every so many-th partial row,
+// eight loads in flight each, and meet by shuffles and then in shared memory in a
+// fixed order. blockIdx.y: 0 dw_post, 1 dw_pre, then gate rows.
+// `flat`: gate rows are short and many, each in few ranges. Then the CTAs behind
+// the first two rows of the grid go over the borders between ranges instead, a thread
+// per border and four columns: a gate row is summed at the first border inside it.
 template <int DT>
 __global__ void __launch_bounds__(512) block_bwd_finish_kernel(const BlockBwdP p, int64_t slots, int64_t G,
-                                                               int64_t R) {
-    __shared__ float4 red[16][32];
+                                                               int64_t R, bool flat) {
+    __shared__ float4 red[16][8];
     const int64_t pitch = block_bwd_pitch(p.N);
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t j4 = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    auto put_gate = [&](int64_t grow, int64_t j, float s) {
+        s *= p.alpha;
+        if (p.w_post) s *= p.offset + load1<DT>(p.w_post, j);
+        store1<DT>(p.dgate, grow * p.lddg + j, s);
+    };
+    if (flat && blockIdx.y >= 2) {
+        const int64_t nv = (p.N + 3) / 4, all = (R - 1) * nv;
+        const int64_t me = (static_cast<int64_t>(blockIdx.y - 2) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
+        pdl_wait();
+        for (int64_t i = me; i < all; i += static_cast<int64_t>(gridDim.y - 2) * gridDim.x * blockDim.x) {
+            const int64_t b = 1 + i / nv, j4 = i - (b - 1) * nv;
+            const int64_t begin = range_begin(b, R, p.M), before = range_begin(b - 1, R, p.M);
+            const int64_t grow = begin / p.gate_rows, first = grow * p.gate_rows;
+            if (first == begin || before > first) continue;  // no gate row is split, or not first here
+            const int64_t last = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
+            float4 x = reinterpret_cast<const float4*>(
+                partial(p.ws, before < first ? 3 : 2, b - 1, slots, pitch))[j4];
+            for (int64_t k = b, at = begin; at < last; at = range_begin(++k, R, p.M)) {
+                const float4 z = reinterpret_cast<const float4*>(partial(p.ws, 2, k, slots, pitch))[j4];
+                x.x += z.x;
+                x.y += z.y;
+                x.z += z.z;
+                x.w += z.w;
+            }
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j4 * 4 + e < p.N) put_gate(grow, j4 * 4 + e, v[e]);
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 7, w = threadIdx.x >> 3, groups = blockDim.x >> 3;
+    const int64_t j4 = static_cast<int64_t>(blockIdx.x) * 8 + lane;
     pdl_wait();
     for (int64_t item = blockIdx.y;; item += gridDim.y) {
         const int64_t grow = item - 2;
-        if (item >= 2 && (!p.gate || p.gate_rows == 1 || grow * p.gate_rows >= p.M)) return;
+        if (item >= 2 && (flat || !p.gate || p.gate_rows == 1 || grow * p.gate_rows >= p.M)) return;
         int64_t b0 = 0, b1 = G;
         int area = static_cast<int>(item), area0 = area;
         if (item < 2) {
@@ -735,27 +945,32 @@ __global__ void __launch_bounds__(512) block_bwd_finish_kernel(const BlockBwdP p
                 float4 z[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    z[k] = b + 16 * k < b1 ? at(b + 16 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    z[k] = b + groups * k < b1 ? at(b + groups * k) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) add(z[k]);
-                b += 128;
+                b += groups * 8;
             }
         }
-        __syncthreads();
-        red[w][lane] = x;
-        __syncthreads();
-        if (w < 4) {  // warp w: column w of each vector
-            float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) s += reinterpret_cast<const float*>(&red[k][lane])[w];
-            const int64_t j = j4 * 4 + w;
+        for (int off = 8; off < 32; off <<= 1) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, off);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, off);
+            x.z += __shfl_xor_sync(0xffffffffu, x.z, off);
+            x.w += __shfl_xor_sync(0xffffffffu, x.w, off);
+        }
+        __syncthreads();
+        if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][lane] = x;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            float s = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < groups / 4; ++k) s += reinterpret_cast<const float*>(&red[k][0])[threadIdx.x];
+            const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
             if (j < p.N) {
                 if (item < 2) {
                     (item == 0 ? p.dw_post : p.dw_pre)[j] = s;
                 } else {
-                    s *= p.alpha;
-                    if (p.w_post) s *= p.offset + load1<DT>(p.w_post, j);
-                    store1<DT>(p.dgate, grow * p.lddg + j, s);
+                    put_gate(grow, j, s);
                 }
             }
         }
@@ -767,11 +982,17 @@ cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G,
     const int64_t grows = p.gate && p.gate_rows > 1 ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
     if (!p.dw_post && !p.dw_pre && grows == 0) return cudaSuccess;
     Launch l;
-    l.grid = static_cast<int>((p.N + 127) / 128);
-    l.threads = 512;
+    l.grid = static_cast<int>((p.N + 31) / 32);
+    l.threads = G <= 128 ? 128 : G <= 256 ? 256 : 512;
     LaunchCfg cfg(l, c.stream, c.pdl);
-    cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + grows, 1024));
-    return cudaLaunchKernelEx(&cfg.cfg, block_bwd_finish_kernel<DT>, p, slots, G, R);
+    // Gate rows in eight ranges or fewer each go with the borders (GB300, us, the whole
+    // backward: 4096x4096 bf16 with a gate row per 3 rows 157 -> 51, 8231x272 fp32 with
+    // one per 2 rows 56 -> 24).
+    const bool flat = grows * 8 >= R;
+    const int64_t borders = ((R - 1) * ((p.N + 3) / 4) + l.threads - 1) / l.threads;  // CTAs of them
+    const int64_t gates = flat && grows ? (borders + l.grid - 1) / l.grid : grows;
+    cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + gates, 1024));
+    return cudaLaunchKernelEx(&cfg.cfg, block_bwd_finish_kernel<DT>, p, slots, G, R, flat && grows > 0);
 }
 
 template <int DT, int GATE>
@@ -866,8 +1087,9 @@ cudaError_t run(const BlockBwdP& p, const OpCfg& c) {
         if (taken) return e;
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
-    if (p.N <= 1024 * 4) return launch_columns<DT, 4>(p, c);
-    if (p.N <= 1024 * 8) return launch_columns<DT, 8>(p, c);
+    if (p.N <= 512 * 4) return launch_columns<DT, 4, false>(p, c);
+    if (p.N <= 1024 * 4) return launch_columns<DT, 4, true>(p, c);
+    if (p.N <= 1024 * 8) return launch_columns<DT, 8, true>(p, c);
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_bwd_generic_kernel<DT>;
