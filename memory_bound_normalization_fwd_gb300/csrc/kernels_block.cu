@@ -320,11 +320,110 @@ __global__ void __launch_bounds__(512) block_fwd_generic_kernel(const BlockP p) 
     }
 }
 
-// Rows that are not whole vectors (any N, stride and alignment), of up to 1024 V
+// Rows that are not whole vectors (any N, stride and alignment), of up to 512 V
 // columns: a CTA per row, element loads, a thread's columns t, t + T, ... kept in
-// registers between the reductions, so that h and r are read once.
+// registers between the reductions, so that h and r are read once. The scales stay in
+// registers, the next row (and its gate row, where one gate does not stand for all
+// rows) is loaded while this one is reduced, and a load is one instruction (GB300,
+// us, against the kernel below: 18503x708 bf16 60 -> 44, 23493x987 fp32 92 -> 72,
+// 16384x777 bf16 with a gate row per 100 rows 74 -> 57).
 template <int DT, int V>
-__global__ void __launch_bounds__(1024) block_fwd_columns_kernel(const BlockP p) {
+__global__ void __launch_bounds__(512) block_fwd_columns_kernel(const BlockP p) {
+    using Raw = typename Elem<DT>::T;
+    __shared__ __align__(16) float part[2][kMaxTeamWarps];
+    int parity = 0;
+    const int t = threadIdx.x, T = blockDim.x, N = static_cast<int>(p.N);
+    const bool row_gate = p.gate && p.gate_rows < p.M;
+    Raw rh[V], rr[V], rg[V];
+    // Byte offsets of the thread's columns (past the row's end: of the last one): a
+    // row's base is the same for all threads.
+    uint32_t off[V];
+    bool in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        in[v] = v * T + t < N;
+        off[v] = static_cast<uint32_t>(min(v * T + t, N - 1)) * static_cast<uint32_t>(sizeof(Raw));
+    }
+    auto load_raw = [&](const void* x, int64_t base, Raw (&out)[V]) {
+        const char* q = static_cast<const char*>(x) + base * static_cast<int64_t>(sizeof(Raw));
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = *reinterpret_cast<const Raw*>(q + off[v]);
+    };
+    auto store = [&](void* x, int64_t base, int v, float f) {
+        char* q = static_cast<char*>(x) + base * static_cast<int64_t>(sizeof(Raw));
+        *reinterpret_cast<Raw*>(q + off[v]) = Elem<DT>::store(f);
+    };
+    auto fetch = [&](int64_t row) {
+        load_raw(p.h, row * p.ldh, rh);
+        load_raw(p.r, row * p.ldr, rr);
+        if (row_gate) load_raw(p.gate, row / p.gate_rows * p.ldg, rg);
+    };
+    for (int i = t; i < 2 * kMaxTeamWarps; i += T) (&part[0][0])[i] = 0.f;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    fetch(blockIdx.x);
+    float scale[V], wpre[V];  // alpha (offset + w_post), times a gate for all rows
+    if (p.w_post) load_columns<DT, V>(p.w_post, 0, t, T, N, scale);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        scale[v] = p.w_post ? p.alpha * (p.offset + scale[v]) : p.alpha;
+        wpre[v] = 0.f;
+    }
+    if (p.gate && !row_gate) {
+        float q[V];
+        load_columns<DT, V>(p.gate, 0, t, T, N, q);
+#pragma unroll
+        for (int v = 0; v < V; ++v) scale[v] *= q[v];
+    }
+    if (p.w_pre) {
+        load_columns<DT, V>(p.w_pre, 0, t, T, N, wpre);
+#pragma unroll
+        for (int v = 0; v < V; ++v) wpre[v] += p.offset;
+    }
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+        float f[V], r[V], k[V], ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            f[v] = in[v] ? Elem<DT>::load(rh[v]) : 0.f;
+            r[v] = in[v] ? Elem<DT>::load(rr[v]) : 0.f;
+            // the same bits whether the gate is a row's own or stands for all
+            k[v] = row_gate ? scale[v] * Elem<DT>::load(rg[v]) : scale[v];
+        }
+        if (row + gridDim.x < p.M) fetch(row + gridDim.x);
+        float a = 1.f;
+        if (p.w_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) ss = fmaf(f[v], f[v], ss);
+            ss = team_sum(ss, &part[parity][0], 0, t, T);
+            parity ^= 1;
+            a = row_rstd(ss, p.n, p.eps);
+            if (t == 0 && p.rstd_post) p.rstd_post[row] = a;
+            ss = 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            f[v] = fmaf(f[v] * a, k[v], p.beta * r[v]);
+            if (in[v]) {
+                store(p.s, row * p.lds, v, f[v]);
+                ss = fmaf(f[v], f[v], ss);
+            }
+        }
+        if (p.w_pre) {
+            ss = team_sum(ss, &part[parity][0], 0, t, T);
+            parity ^= 1;
+            const float b = row_rstd(ss, p.n, p.eps);
+            if (t == 0 && p.rstd_pre) p.rstd_pre[row] = b;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (in[v]) store(p.y, row * p.ldy, v, f[v] * b * wpre[v]);
+        }
+    }
+}
+
+// The same for longer rows of up to 1024 V columns, a row at a time.
+template <int DT, int V>
+__global__ void __launch_bounds__(1024) block_fwd_wide_columns_kernel(const BlockP p) {
     __shared__ float part[2 * 32];
     int parity = 0;
     const int t = threadIdx.x, T = blockDim.x, N = static_cast<int>(p.N);
@@ -377,9 +476,9 @@ __global__ void __launch_bounds__(1024) block_fwd_columns_kernel(const BlockP p)
     }
 }
 
-template <int DT, int V>
+template <int DT, int V, bool WIDE>
 cudaError_t launch_columns(const BlockP& p, const OpCfg& c) {
-    auto fn = block_fwd_columns_kernel<DT, V>;
+    auto fn = WIDE ? block_fwd_wide_columns_kernel<DT, V> : block_fwd_columns_kernel<DT, WIDE ? 4 : V>;
     const int T = static_cast<int>((p.N + V * 32 - 1) / (V * 32)) * 32;
     const int occ = occupancy(reinterpret_cast<const void*>(fn), T, 0);
     return op_launch(c, fn, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas), T, 0, p);
@@ -395,8 +494,9 @@ cudaError_t run(const BlockP& p, const OpCfg& c) {
         if (taken) return e;
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
-    if (p.N <= 1024 * 4) return launch_columns<DT, 4>(p, c);
-    if (p.N <= 1024 * 8) return launch_columns<DT, 8>(p, c);
+    if (p.N <= 512 * 4) return launch_columns<DT, 4, false>(p, c);
+    if (p.N <= 1024 * 4) return launch_columns<DT, 4, true>(p, c);
+    if (p.N <= 1024 * 8) return launch_columns<DT, 8, true>(p, c);
     int T = 32;
     while (T < 512 && static_cast<int64_t>(T) * 4 < p.N) T <<= 1;
     auto fn = block_fwd_generic_kernel<DT>;
