@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
     if (t == 0) {
         for (int st = 0; st < g.stages; ++st) mbar_init(ring.bar(st), 1);
         fence_mbar_init();
-        sh.dead[team] = 0;
+        sh.give_up[team].clear();
     }
     for (int i = t; i < 2 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
 
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
             }
             --left;
         }
-        if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) *(volatile unsigned int*)&sh.dead[team] = 1;
+        if (!mbar_wait_bounded(ring.bar(st), phase, g.limit)) sh.give_up[team].mark(row);
         f2 f[V][H];
         f2 sq = 0;
         const unsigned char* at = smem + (ring.stage(st) - smem_u32(smem)) + 16u * t;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(MAXT) block_fwd_ring_kernel(const BlockP p, co
         // Behind a row's first barrier every thread has read the stage: the
         // leader refills it.
         auto behind_first_barrier = [&]() {
-            dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+            dead = sh.give_up[team].at(row);
             if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
         };
         float a = 1.f;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             mbar_init(smem_u32(&peer_bars[1]), 1);
         }
         fence_mbar_init();
-        sh.dead[team] = 0;
+        sh.give_up[team].clear();
     }
     for (int i = t; i < 2 * 4 * kMaxTeamWarps; i += g.T) parts[team][0][i] = 0.f;
     const bool need_h = post || GATE != 0;
@@ -213,8 +213,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             left = p.gate_rows;
             load_scale();
         }
-        if (!(WIDE && dead) && !mbar_wait_bounded(ring.bar(st), phase, g.limit))
-            *(volatile unsigned int*)&sh.dead[team] = 1;
+        if (!(WIDE && dead) && !mbar_wait_bounded(ring.bar(st), phase, g.limit)) sh.give_up[team].mark(row);
         const float k1 = k1_next, k2 = k2_next;
         if (row + 1 < rows) {  // the next row's, a global load ahead of its use
             if (post) k1_next = __ldg(rstd_post + row + 1);
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
         team_sums3(sums, &parts[team][parity][0], team, t, g.T);
         parity ^= 1;
         if (!(WIDE && dead)) {
-            dead = *(volatile unsigned int*)&sh.dead[team] != 0;
+            dead = sh.give_up[team].at(row);
             if (WIDE) dead_row = row;
         }
         if (!dead && t == 0 && row + g.stages < rows) issue(row + g.stages, st);
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
                 st_async_peer_f4(smem_u32(&peers[slot][rank]), bar, t, sums[0], sums[1], sums[2], dead ? 1.f : 0.f);
             if (!lost && !mbar_wait_bounded(bar, (row >> 1) & 1, g.drain)) {
                 lost = true;
-                *(volatile unsigned int*)&sh.dead[team] = 1;
+                sh.give_up[team].mark(row + 1);
             }
             float4 x = peers[slot][0];  // added in rank order, so that all get the same
             for (int i = 1; i < g.cluster; ++i) {
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
             sums[0] = x.x;
             sums[1] = x.y;
             sums[2] = x.z;
-            if (x.w != 0.f) *(volatile unsigned int*)&sh.dead[team] = 1;
+            if (x.w != 0.f) sh.give_up[team].mark(row + 1);
             if (dead) continue;
         } else if (dead) {
             break;

@@ -7,12 +7,13 @@
 // bytes in flight do not depend on registers. A CTA holds up to kMaxTeams
 // teams; they share nothing but the SM.
 //
-// Waits are bounded: a thread whose stage does not land in time marks its team,
-// which all of its threads see behind the row's reduction barrier; the team
-// then writes nothing more, waits (bounded) for its copies in flight and ends.
+// Waits are bounded: a thread whose stage does not land in time marks the row,
+// which all threads of the team see behind the row's reduction barrier (give_up.h);
+// the team then writes nothing more, waits (bounded) for its copies in flight and ends.
 #pragma once
 
 #include "async_copy.cuh"
+#include "give_up.h"
 #include "ops_common.cuh"
 
 namespace rmsn {
@@ -49,7 +50,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 
 struct RingShared {
     uint64_t bars[kMaxTeams][kMaxRing];
-    unsigned int dead[kMaxTeams];
+    GiveUp give_up[kMaxTeams];
 };
 
 __device__ __forceinline__ void ring_barrier(int team, int T) {
