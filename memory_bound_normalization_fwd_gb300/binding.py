@@ -553,6 +553,15 @@ def _workspace(t, size, *key):
     return t.new_empty(n, dtype=torch.uint8)
 
 
+def _given(workspace, device):
+    """(address, bytes) of a caller's workspace: all of its bytes and no others."""
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
+    if not workspace.is_contiguous():  # a view's bytes are not numel * element size from its start
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _refuse(t, name, shape, dtype, device):
     if t.dtype != dtype or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
@@ -677,8 +686,8 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
     zero), the s and rstd that the forward returned and its other arguments.
 
     dgate is in the gate's shape and dtype, dw_post and dw_pre in fp32 (None
-    without gate, w_post, w_pre). ``workspace`` is a CUDA tensor of at least
-    rmsnorm_block_bwd_workspace_size() bytes; allocated here when not given.
+    without gate, w_post, w_pre). ``workspace`` is a contiguous CUDA tensor of at
+    least rmsnorm_block_bwd_workspace_size() bytes; allocated here when not given.
     """
     import torch
     ctx = _elsewhere(h, stream)
@@ -723,14 +732,12 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
         dwbp = dwb.data_ptr()
     if workspace is None:
         workspace = _workspace(h, rmsnorm_block_bwd_workspace_size, M, N, code)
-    elif workspace.get_device() != dev:
-        raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
+    ws_ptr, ws_bytes = _given(workspace, dev)
     args = _BLOCK.pack(160, code, M, N, gate_rows, hp, 0, wpost, gp, wpre, sp, 0, ap, bp,
                        ldh, 0, ldg, lds, 0, 0.0, offset, alpha, beta)
     grads = _BLOCK_GRADS.pack(104, 0, dyp, dsp, dhp, drp, dgp, dwap, dwbp, lddy, ldds, lddh, lddr,
                               lddg)
-    rc = (_lib or lib()).rmsnorm_block_bwd(args, grads, workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(),
+    rc = (_lib or lib()).rmsnorm_block_bwd(args, grads, ws_ptr, ws_bytes,
                                            _opt(make_options(**options)) if options else None,
                                            _stream_ptr(dev))
     if rc:
@@ -925,9 +932,7 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
     grads = _ROPE_GRADS.pack(152, 0, *gq, *gk, *oq, *ok, wqp, wkp)
     ws_ptr = ws_bytes = 0
     if workspace is not None:
-        if workspace.get_device() != dev:
-            raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = _given(workspace, dev)
     rc = (_lib or lib()).rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
                                           _opt(make_options(**options)) if options else None,
                                           _stream_ptr(dev))
