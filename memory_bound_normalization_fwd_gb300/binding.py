@@ -686,7 +686,7 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
     zero), the s and rstd that the forward returned and its other arguments.
 
     dgate is in the gate's shape and dtype, dw_post and dw_pre in fp32 (None
-    without gate, w_post, w_pre). ``workspace`` is a contiguous CUDA tensor of at
+    without gate, w_post, w_pre; zeros where there are no rows). ``workspace`` is a contiguous CUDA tensor of at
     least rmsnorm_block_bwd_workspace_size() bytes; allocated here when not given.
     """
     import torch
@@ -722,7 +722,8 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
     dgate = dwa = dwb = None
     dgp = dwap = dwbp = lddg = 0
     if gp:
-        dgate = h.new_empty(gate.shape)
+        # no row: the sum of nothing, which no kernel writes
+        dgate = h.new_empty(gate.shape) if M else h.new_zeros(gate.shape)
         dgp, lddg = dgate.data_ptr(), N
     if wpost:
         dwa = h.new_empty(N, dtype=f32)
