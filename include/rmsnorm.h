@@ -383,7 +383,7 @@ int rmsnorm_bwd_workspace_size(int64_t M, int64_t N, int dtype, const rmsnorm_op
  *   gate   [ceil(M / gate_rows), N] (row stride ldg >= N), row i of h takes gate row
  *                 i / gate_rows: gate_rows >= M is one gate per channel, the tokens per
  *                 sequence one gate per sequence, 1 a gate per element. NULL (and
- *                 gate_rows 0): no gate
+ *                 gate_rows 0, which without rows is not looked at): no gate
  *   w_pre  [N]    NULL: no norm before the next block (y is then not written and NULL)
  *   s, y   [M, N] outputs (row strides lds, ldy >= N)
  *   rstd_post, rstd_pre  [M] fp32, kept for the backward; NULL: not stored

@@ -603,7 +603,10 @@ def _gate(gate, gate_rows, dtype, device, M, N):
         raise ValueError(f"gate must have {N} columns, got {tuple(gate.shape)}")
     G = gate.numel() // N if N else 0
     if not gate_rows:
-        gate_rows = max(M, 1) if gate.dim() == 1 or G == 1 else M // G if G and M % G == 0 else 0
+        if gate.dim() == 1 or G == 1 or M == 0:
+            gate_rows = max(M, 1)
+        else:
+            gate_rows = M // G if G and M % G == 0 else 0
     if gate_rows < 1 or -(-M // gate_rows) != G and M > 0:
         raise ValueError(f"{G} gate rows do not divide {M} rows: give gate_rows, the rows per gate row")
     if gate.is_contiguous() or G <= 1 and gate.stride(-1) == 1:
@@ -721,7 +724,7 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
         drp, lddr = _rows(dr, "dr", shape, dtype, dev, N)
     dgate = dwa = dwb = None
     dgp = dwap = dwbp = lddg = 0
-    if gp:
+    if gate is not None:
         # no row: the sum of nothing, which no kernel writes
         dgate = h.new_empty(gate.shape) if M else h.new_zeros(gate.shape)
         dgp, lddg = dgate.data_ptr(), N

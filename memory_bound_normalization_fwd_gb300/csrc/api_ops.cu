@@ -177,7 +177,8 @@ int block_shapes(const rmsnorm_block_args_t* a, bool need_r) {
     if (a->M < 0 || a->N <= 0 || a->N > (int64_t(1) << 31))
         return fail(RMSNORM_ERR_SHAPE, "need M >= 0 and 0 < N <= 2^31 (got M=%lld N=%lld)",
                     static_cast<long long>(a->M), static_cast<long long>(a->N));
-    if (a->gate ? a->gate_rows < 1 : a->gate_rows != 0)
+    // A gate of no rows may have no address.
+    if (a->gate ? a->gate_rows < 1 : a->M == 0 ? a->gate_rows < 0 : a->gate_rows != 0)
         return fail(RMSNORM_ERR_SHAPE, "gate_rows is %lld: rows per gate row (>= 1), 0 without a gate",
                     static_cast<long long>(a->gate_rows));
     if (!std::isfinite(a->offset) || !std::isfinite(a->alpha) || !std::isfinite(a->beta))

@@ -20,7 +20,7 @@ def _dirty():
 
 
 @pytest.mark.parametrize("shape", [(0, N), (2, 0, N), (0, 5, N)])
-@pytest.mark.parametrize("gate_shape,gate_rows", [((N,), None), ((N,), 7), ((1, N), None), ((3, N), 4)])
+@pytest.mark.parametrize("gate_shape,gate_rows", [((N,), None), ((N,), 7), ((1, N), None), ((3, N), 4), ((0, N), 1), ((3, N), None)])
 @pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
 def test_gradients_of_no_rows_are_zero(shape, gate_shape, gate_rows, post, pre):
     h = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
@@ -37,3 +37,16 @@ def test_gradients_of_no_rows_are_zero(shape, gate_shape, gate_rows, post, pre):
         assert (got is not None) == given
         if given:
             assert bool((got == 0).all())
+
+
+@pytest.mark.parametrize("shape", [(0, N), (2, 0, N), (0, 5, N)])
+def test_a_gate_per_element_of_no_rows(shape):
+    # the gate in h's shape, without gate_rows and with them
+    h = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(N, dtype=torch.bfloat16, device=DEV)
+    for gate_rows in (None, 1, 5):
+        gate = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+        s, y, a, b = B.block_fwd(h, h.clone(), w, w, gate, gate_rows)
+        assert s.shape == y.shape == shape and a.shape == b.shape == shape[:-1]
+        dgate = B.block_bwd(h, s, a, b, h.clone(), h.clone(), w, w, gate, gate_rows)[2]
+        assert dgate.shape == shape and dgate.dtype == gate.dtype
