@@ -245,7 +245,7 @@ cudaError_t launch_ring(BlockP p, const OpCfg& c, bool* taken) {
     // (GB300, us: 16384x4096 bf16 at 64 / 96 / 128 / 192 KB 86 / 97 / 97 / 97,
     // 16384x8192 164 / 178 / 184 / 184, 65536x512 at 48 / 72 / 96 KB 52 / 46 / 46).
     if (!ring_plan(reinterpret_cast<const void*>(fn), c, p.M, static_cast<int>(nvec), T, wide ? 512 : 256,
-                   GATE == 2 ? 3 : 2, 0, 64 << 10, 1, &plan))
+                   GATE == 2 ? 3 : 2, 0, 64 << 10, 1, INT64_MAX, &plan))
         return cudaSuccess;
     p.ldh /= E;
     p.ldr /= E;

@@ -42,6 +42,9 @@ __host__ __device__ inline int64_t range_owner(int64_t row, int64_t grid, int64_
     return row < big * (q + 1) ? row / (q + 1) : big + (row - big * (q + 1)) / q;
 }
 
+constexpr int kCtasPerSM = 8;   // most CTAs of the kernels without teams
+constexpr int kShortRow = 256;  // columns of a team of one warp
+
 // Workspace: four areas of `slots` partial rows of `pitch` floats: dw_post and
 // dw_pre (a row per CTA), gate sums that begin with a range, gate sums that
 // begin inside it (a row per range: of a CTA, or of a team).
@@ -858,7 +861,8 @@ cudaError_t launch_columns(const BlockBwdP& p, const OpCfg& c) {
     const int smem = p.gate && p.gate_rows > 1 ? V * T * 4 : 0;  // at most 32 KB
     const int occ = occupancy(reinterpret_cast<const void*>(fn), T, smem);
     const int64_t slots = block_bwd_max_grid(p.M, p.N, c.dev.sm_count);
-    const int64_t G = std::min<int64_t>(slots, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas));
+    const int64_t G = std::min<int64_t>(
+        slots, persistent_grid(p.M, 1, c.dev.sm_count, std::min(occ, kCtasPerSM), c.max_ctas));
     const cudaError_t e = op_launch(c, fn, G, T, smem, p, slots);
     return e != cudaSuccess ? e : finish<DT>(p, c, slots, G, G);
 }
@@ -982,12 +986,13 @@ cudaError_t finish(const BlockBwdP& p, const OpCfg& c, int64_t slots, int64_t G,
     if (!p.dw_post && !p.dw_pre && grows == 0) return cudaSuccess;
     Launch l;
     l.grid = static_cast<int>((p.N + 31) / 32);
-    l.threads = G <= 128 ? 128 : G <= 256 ? 256 : 512;
-    LaunchCfg cfg(l, c.stream, c.pdl);
     // Gate rows in eight ranges or fewer each go with the borders (GB300, us, the whole
     // backward: 4096x4096 bf16 with a gate row per 3 rows 157 -> 51, 8231x272 fp32 with
     // one per 2 rows 56 -> 24).
     const bool flat = grows * 8 >= R;
+    const int64_t most = grows && !flat ? std::max(G, R) : G;  // partial rows of a sum
+    l.threads = most <= 128 ? 128 : most <= 256 ? 256 : 512;
+    LaunchCfg cfg(l, c.stream, c.pdl);
     const int64_t borders = ((R - 1) * ((p.N + 3) / 4) + l.threads - 1) / l.threads;  // CTAs of them
     const int64_t gates = flat && grows ? (borders + l.grid - 1) / l.grid : grows;
     cfg.cfg.gridDim.y = static_cast<unsigned>(std::min<int64_t>(2 + gates, 1024));
@@ -1021,7 +1026,7 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
     // 128 KB of stages per SM (GB300, us: 16384x4096 bf16 at 64 / 96 / 128 / 192
     // KB 147 / 130 / 129 / 132, 65536x512 91 / 87 / 88 / 88).
     if (!ring_plan(reinterpret_cast<const void*>(fn), c, in.M, slice, T, 512, arrays, extra, 128 << 10, cluster,
-                   &plan))
+                   slots, &plan))
         return cudaSuccess;
     // The teams' sums meet in the rings' memory: with a row per team it may be
     // smaller than they are.
@@ -1030,7 +1035,14 @@ cudaError_t launch_ring(const BlockBwdP& in, const OpCfg& c, bool* taken) {
     plan.shape.slots = slots;
     plan.shape.nvec = static_cast<int>(nvec);
     const int64_t groups = plan.grid / cluster, ranges = groups * plan.shape.teams;
-    if (ranges > slots) return cudaSuccess;
+    // A gate row in more than a thousand ranges costs the second launch more than short
+    // rows of few gain here: a range is a warp's, in the kernel below a CTA's (GB300, us,
+    // here / there, bf16, one gate row for all: 4096x64 14.6 / 11.0, 8231x128 17.1 / 14.3,
+    // 32768x16 28.5 / 26.1; 65536x64 44.6 / 49.8, 8231x256 15.9 / 18.4; 8231x128 with one
+    // per 100 rows 12.6 / 14.5, without 10.3 / 12.8).
+    if (GATE == 1 && c.variant == RMSNORM_VARIANT_AUTO && in.N <= 128 && in.M < 12 * ranges &&
+        ranges > 1024 * ((in.M + in.gate_rows - 1) / in.gate_rows))
+        return cudaSuccess;
     BlockBwdP p = in;
     p.ldh /= E;
     p.lds /= E;
@@ -1095,7 +1107,7 @@ cudaError_t run(const BlockBwdP& p, const OpCfg& c) {
     const int occ = occupancy(reinterpret_cast<const void*>(fn), T, 0);
     const int64_t slots = block_bwd_max_grid(p.M, p.N, c.dev.sm_count);
     const int64_t G = std::min<int64_t>(
-        slots, persistent_grid(p.M, 1, c.dev.sm_count, occ, c.max_ctas));
+        slots, persistent_grid(p.M, 1, c.dev.sm_count, std::min(occ, kCtasPerSM), c.max_ctas));
     const cudaError_t e = op_launch(c, fn, G, T, 0, p, slots);
     return e != cudaSuccess ? e : finish<DT>(p, c, slots, G, G);
 }
@@ -1103,10 +1115,11 @@ cudaError_t run(const BlockBwdP& p, const OpCfg& c) {
 }  // namespace
 
 int block_bwd_max_grid(int64_t M, int64_t N, int sm_count) {
-    // Up to eight CTAs per SM; for very long rows fewer, so that the partial
-    // rows stay within about 256 MB.
+    // Up to eight ranges per SM, or 24 of short rows, where a team is a warp; for very
+    // long rows fewer, so that the partial rows stay within about 256 MB.
     const int64_t rows = (int64_t(1) << 28) / (kBlockBwdRows * 4 * block_bwd_pitch(N));
-    const int64_t g = std::min<int64_t>(M, std::min<int64_t>(8LL * sm_count, std::max<int64_t>(rows, 1)));
+    const int64_t per_sm = N <= kShortRow ? 24 : kCtasPerSM;
+    const int64_t g = std::min<int64_t>(M, std::min<int64_t>(per_sm * sm_count, std::max<int64_t>(rows, 1)));
     return static_cast<int>(std::max<int64_t>(g, 1));
 }
 

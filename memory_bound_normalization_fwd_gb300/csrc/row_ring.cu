@@ -67,7 +67,7 @@ int max_clusters(const void* fn, int cluster, int threads, int smem) {
 }  // namespace
 
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, int in_flight, int cluster, RingPlan* out) {
+               int extra, int in_flight, int cluster, int64_t max_teams, RingPlan* out) {
     if (T > max_threads) return false;
     int teams = cluster > 1 ? 1 : std::min(max_threads / T, kMaxTeams);
     // Few rows: one team per CTA spreads them over more SMs.
@@ -93,6 +93,7 @@ bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int m
         cap = max_clusters(fn, cluster, teams * T,
                            static_cast<int>(stage * stages + static_cast<int64_t>(extra) * teams * T));
     if (c.max_ctas > 0) cap = std::min<int64_t>(cap, std::max(1, c.max_ctas / cluster));
+    cap = std::min(cap, max_teams / teams);
     int64_t groups = std::min(want, cap);  // CTAs, or clusters
     // Every team walks at least one row.
     while (groups * teams > M) --groups;

@@ -17,9 +17,10 @@ struct RingPlan {
 // CTAs of up to `max_threads`, with `extra` more bytes of shared memory per
 // CTA thread and about `in_flight` bytes of stages per SM. False where a row
 // does not fit two stages of shared memory. cluster > 1: the CTAs of a cluster
-// take a row's slices, `nvec` vectors each (one team per CTA).
+// take a row's slices, `nvec` vectors each (one team per CTA). At most `max_teams`
+// teams (clusters) in all.
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
-               int extra, int in_flight, int cluster, RingPlan* out);
+               int extra, int in_flight, int cluster, int64_t max_teams, RingPlan* out);
 
 // Reads a status word of the current device and clears it.
 template <typename S>
