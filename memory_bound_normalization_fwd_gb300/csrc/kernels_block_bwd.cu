@@ -1,13 +1,15 @@
 // Backward of the block operator (the formulas are in include/rmsnorm.h).
 //
-// One reduction per row: with u = dy (offset + w_pre), k2 = rstd_pre,
+// One reduction per row: with u = dy (offset + w_pre), k2 = rstd_pre, n2 = k2 s,
 // a = alpha gate (offset + w_post),
 //
-//   c2 = sum u s,   A = sum a h (ds + k2 u),   B = sum a h s
-//   t  = ds + k2 u - e s            e = k2^3 c2 / N
+//   c2 = sum u n2,   A = sum a h (ds + k2 u),   B = sum a h n2
+//   t  = ds + k2 u - e n2           e = k2 c2 / N
 //   sum a h t = A - e B             (what the norm after the block subtracts)
 //
-// so both norms' row sums come from one pass. Sums over rows: P = sum of
+// so both norms' row sums come from one pass. (n2 is of the size of 1 whatever s is;
+// with s itself, rows of an RMS below 1e-13 would need k2^3 and sums of products that
+// are past fp32's range where the gradients are not.) Sums over rows: P = sum of
 // t h rstd_post over the rows of one gate row gives that row's dgate
 // (alpha (offset + w_post) P) and its part of dw_post (alpha gate P), so one
 // column sum serves both.
@@ -57,7 +59,7 @@ __device__ inline float* partial(float* ws, int area, int64_t i, int64_t slots, 
 // GATE: 0 none, 1 one gate row for several rows, 2 a gate row per row.
 // A thread owns V vectors of columns, eight columns. In registers per column: the
 // scales, the sums over rows (P and dw_pre; GATE 2: dw_post and dw_pre), and of the
-// current row t without its -e s, s and h between the two passes. With a gate row
+// current row t without its -e n2, s and h between the two passes. With a gate row
 // for several rows dw_post changes only where the gate row ends: its sums are in
 // shared memory, a thread's own. The arithmetic is on pairs (f32x2): scalar code
 // took three times the instructions and was bound by them (16384 x 4096 bf16: 564
@@ -248,8 +250,9 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
                 for (int e = 0; e < H; ++e) {
                     const f2 u = f2_mul(dy[e], wpre[v][e]);
                     t0[v][e] = f2_fma(k22, u, t0[v][e]);
+                    s[e] = f2_mul(s[e], k22);  // n2
                     us = f2_fma(u, s[e], us);
-                    pre[v][e] = f2_fma(dy[e], f2_mul(s[e], k22), pre[v][e]);
+                    pre[v][e] = f2_fma(dy[e], s[e], pre[v][e]);
                 }
             }
             if (post) {
@@ -304,9 +307,9 @@ __global__ void __launch_bounds__(512) block_bwd_ring_kernel(const BlockBwdP p, 
         } else if (dead) {
             break;
         }
-        const float e2 = k2 * k2 * k2 * (sums[0] * inv_n);
-        const float f = k1 * k1 * (fmaf(-e2, sums[2], sums[1]) * inv_n);
-        const f2 me2 = f2_dup(-e2), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));
+        const float e2 = k2 * (sums[0] * inv_n);
+        const float f = k1 * (k1 * (fmaf(-e2, sums[2], sums[1]) * inv_n));
+        const f2 me2 = f2_dup(-(e2 * k2)), k12 = f2_dup(k1), mf = f2_dup(-(k1 * f));  // me2: of s
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool in = FULL || column(v) < nvec;
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
         };
         float v[3] = {0.f, 0.f, 0.f};
         for (int64_t j = tid; j < p.N; j += T) {
-            const float s = p.w_pre ? load1<DT>(p.s, s0 + j) : 0.f;
+            const float s = p.w_pre ? load1<DT>(p.s, s0 + j) * k2 : 0.f;  // n2
             const float u = p.w_pre ? load1<DT>(p.dy, dy0 + j) * (p.offset + load1<DT>(p.w_pre, j)) : 0.f;
             const float d = p.ds ? load1<DT>(p.ds, ds0 + j) : 0.f;
             v[0] = fmaf(u, s, v[0]);
@@ -490,17 +493,17 @@ __global__ void __launch_bounds__(512) block_bwd_generic_kernel(const BlockBwdP 
             }
         }
         block_sums<3>(v, part, parity);
-        const float e = k2 * k2 * k2 * (v[0] / p.n);
-        const float f = k1 * k1 * (fmaf(-e, v[2], v[1]) / p.n);
+        const float e = k2 * (v[0] / p.n);
+        const float f = k1 * (k1 * (fmaf(-e, v[2], v[1]) / p.n));
         for (int64_t j = tid; j < p.N; j += T) {
             float t = p.ds ? load1<DT>(p.ds, ds0 + j) : 0.f;
             const float a = scale(j);
             const float h = load1<DT>(p.h, h0 + j);
             if (p.w_pre) {
-                const float s = load1<DT>(p.s, s0 + j), dy = load1<DT>(p.dy, dy0 + j);
+                const float s = load1<DT>(p.s, s0 + j) * k2, dy = load1<DT>(p.dy, dy0 + j);
                 t = fmaf(k2, dy * (p.offset + load1<DT>(p.w_pre, j)), t);
                 t = fmaf(-e, s, t);
-                acc_pre[j] = fmaf(dy, s * k2, acc_pre[j]);
+                acc_pre[j] = fmaf(dy, s, acc_pre[j]);
             }
             const float th = t * (h * k1);
             store1<DT>(p.dr, row * p.lddr + j, p.beta * t);
@@ -645,8 +648,9 @@ __global__ void __launch_bounds__(512) block_bwd_columns_kernel(const BlockBwdP 
             for (int v = 0; v < V; ++v) {
                 const float u = dy[v] * wpre[v];
                 t0[v] = fmaf(k2, u, t0[v]);
+                s[v] *= k2;  // n2
                 sums[0] = fmaf(u, s[v], sums[0]);
-                pre[v] = fmaf(dy[v], s[v] * k2, pre[v]);
+                pre[v] = fmaf(dy[v], s[v], pre[v]);
             }
         }
         if (row + 1 < r1) fetch(row + 1);
@@ -660,8 +664,8 @@ __global__ void __launch_bounds__(512) block_bwd_columns_kernel(const BlockBwdP 
         }
         team_sums3(sums, &part[parity][0], 0, t, T);
         parity ^= 1;
-        const float e = k2 * k2 * k2 * (sums[0] * inv_n);
-        const float f = k1 * k1 * (fmaf(-e, sums[2], sums[1]) * inv_n);
+        const float e = k2 * (sums[0] * inv_n);
+        const float f = k1 * (k1 * (fmaf(-e, sums[2], sums[1]) * inv_n));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             t0[v] = fmaf(-e, s[v], t0[v]);
@@ -773,8 +777,9 @@ __global__ void __launch_bounds__(1024) block_bwd_wide_columns_kernel(const Bloc
             for (int v = 0; v < V; ++v) {
                 const float u = dy[v] * (p.offset + a[v]);
                 t0[v] = fmaf(k2, u, t0[v]);
+                s[v] *= k2;  // n2
                 sums[0] = fmaf(u, s[v], sums[0]);
-                pre[v] = fmaf(dy[v], s[v] * k2, pre[v]);
+                pre[v] = fmaf(dy[v], s[v], pre[v]);
             }
         } else {
 #pragma unroll
@@ -790,8 +795,8 @@ __global__ void __launch_bounds__(1024) block_bwd_wide_columns_kernel(const Bloc
             }
         }
         block_sums<3>(sums, part, parity);
-        const float e = k2 * k2 * k2 * (sums[0] * inv_n);
-        const float f = k1 * k1 * (fmaf(-e, sums[2], sums[1]) * inv_n);
+        const float e = k2 * (sums[0] * inv_n);
+        const float f = k1 * (k1 * (fmaf(-e, sums[2], sums[1]) * inv_n));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int j = v * T + t;
