@@ -415,7 +415,9 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
                     c2 = f2_fma(gz, wb[e], f2_fma(gx, wa[e], c2));
                 }
                 const float c = lanes_sum(f2_sum(c2), g.L);
-                const f2 mf = f2_dup(-(r * r * r * (c * g.inv_d)));
+                // r^3 c / D, the small factor first: r^3 alone leaves fp32's range for
+                // heads of an RMS below 1e-13
+                const f2 mf = f2_dup(-(r * (r * (r * (c * g.inv_d)))));
 #pragma unroll
                 for (int e = 0; e < H; ++e) {
                     ta[e] = f2_fma(f2_mul(ta[e], r2), wa[e], f2_mul(x[e], mf));
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(256) rope_bwd_generic_kernel(const RopeP p) {
             for (int j = p.R + lane; j < p.D; j += 32)
                 c = fmaf(load1<DT>(g.in.p, d0 + j) * (p.offset + load1<DT>(g.w, j)),
                          load1<DT>(g.x.p, x0 + j), c);
-            f = r * r * (warp_sum(c) / static_cast<float>(p.D));
+            f = r * (r * (warp_sum(c) / static_cast<float>(p.D)));
         }
         float* acc = p.ws + (u.seg * warps + me) * p.D;
         auto put = [&](int j, int slot, float d) {
