@@ -2,10 +2,10 @@
 // backward of the two (the operation is stated in include/rmsnorm.h).
 //
 // Angles. A frequency is held as the fraction of a turn per position times
-// 2^64, so position * step modulo 2^64 is the phase, exact for any position:
-// its top 32 bits as a signed number are the angle in half turns times 2^31,
-// and sincospif of that needs no range reduction. The phase is off by 2^-32
-// turns and its fp32 value by 2^-25 half turns.
+// 2^64, so position * step modulo 2^64 is the phase, exact for any position.
+// The nearest quarter turn is taken off it in integers, so what becomes an fp32
+// value (off by 2^-23 of itself) is at most an eighth of a turn, and cos and sin
+// keep all their bits however near to zero they are.
 #include "rmsnorm.h"
 
 #include "ops.h"
@@ -19,21 +19,60 @@
 namespace rmsn {
 namespace {
 
-// cos and sin (times magnitude) of pair i at a position. Outputs of 16 bits take
-// the hardware's approximations, whose error of 2^-21 is 2^-10 of those types'
-// half steps; fp32 takes sincospif.
-template <int DT>
-__device__ __forceinline__ float2 turn(int64_t position, uint64_t step, float magnitude) {
-    const uint64_t phase = static_cast<uint64_t>(position) * step;
-    const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-    float s, c;
-    if constexpr (DT == kFP32) {
-        sincospif(x, &s, &c);
-    } else {
-        s = __sinf(x * 3.14159265358979f);
-        c = __cosf(x * 3.14159265358979f);
+// cos and sin (times magnitude) of two pairs at a position: the Taylor series of sin and
+// cos of y quarter turns, |y| <= 1/2, to y^9 and y^10 (what is left out is below 2^-28),
+// then turned by the quarters. The large term comes last, in one rounding. The same bits
+// for every type and kernel. (The hardware's approximations, whose error does not shrink
+// with sin, put fp16 outputs off by up to 16 half steps. GB300, us, those / this, bf16
+// with norms: 64 tokens of 40 heads of 128 2.68 / 2.69, 16384 tokens 56.5 / 56.6, backward
+// 83.1 / 84.2, 16384 of 20 heads of 80 with 20 turned 45.4 / 46.3. sincospif of the same
+// rest: 3.05, 58.9, 86.1, 51.2; one angle at a time from a 64-bit conversion: 3.0, 57.9,
+// 84.9, 48.2.)
+__device__ __forceinline__ void turn2(int64_t position, uint64_t step0, uint64_t step1, float magnitude, f2& c,
+                                      f2& s) {
+    constexpr double q = 1.57079632679489661923;  // a quarter turn
+    constexpr double q2 = q * q;
+    constexpr float s1 = static_cast<float>(q), s1_rest = static_cast<float>(q - s1);
+    constexpr float s3 = static_cast<float>(-q * q2 / 6), s5 = static_cast<float>(q * q2 * q2 / 120);
+    constexpr float s7 = static_cast<float>(-q * q2 * q2 * q2 / 5040);
+    constexpr float s9 = static_cast<float>(q * q2 * q2 * q2 * q2 / 362880);
+    constexpr float c2 = static_cast<float>(-q2 / 2), c4 = static_cast<float>(q2 * q2 / 24);
+    constexpr float c6 = static_cast<float>(-q2 * q2 * q2 / 720), c8 = static_cast<float>(q2 * q2 * q2 * q2 / 40320);
+    constexpr float c10 = static_cast<float>(-q2 * q2 * q2 * q2 * q2 / 3628800);
+    uint32_t quarter[2];  // the nearest quarter in the top two bits
+    float hi[2], lo[2];   // what is left, in quarter turns times 2^32 and 2^64
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint64_t phase = static_cast<uint64_t>(position) * (k == 0 ? step0 : step1);
+        const uint64_t near = phase + (uint64_t(1) << 29);  // so that lo is signed
+        quarter[k] = static_cast<uint32_t>(near >> 32) + 0x20000000u;
+        hi[k] = static_cast<float>(static_cast<int32_t>(near >> 30));
+        lo[k] = static_cast<float>(static_cast<int32_t>(phase << 2));
     }
-    return make_float2(c * magnitude, s * magnitude);
+    const f2 y = f2_fma(f2_make(lo[0], lo[1]), f2_dup(0x1p-64f), f2_mul(f2_make(hi[0], hi[1]), f2_dup(0x1p-32f)));
+    const f2 z = f2_mul(y, y);
+    auto series = [&](f2 x, float a) { return f2_fma(z, x, f2_dup(a)); };
+    const f2 sn = f2_fma(y, f2_dup(s1), f2_mul(y, series(series(series(series(f2_dup(s9), s7), s5), s3), s1_rest)));
+    const f2 cn = series(series(series(series(series(f2_dup(c10), c8), c6), c4), c2), 1.f);
+    const float2 sv = f2_get(f2_mul(sn, f2_dup(magnitude))), cv = f2_get(f2_mul(cn, f2_dup(magnitude)));
+    float cs[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t sb = __float_as_uint(k == 0 ? sv.x : sv.y), cb = __float_as_uint(k == 0 ? cv.x : cv.y);
+        const uint32_t h = quarter[k];
+        const bool odd = h & 0x40000000u;
+        // cos is negated in the quarters 1 and 2, sin in 2 and 3
+        cs[0][k] = __uint_as_float((odd ? sb : cb) ^ ((h ^ (h << 1)) & 0x80000000u));
+        cs[1][k] = __uint_as_float((odd ? cb : sb) ^ (h & 0x80000000u));
+    }
+    c = f2_make(cs[0][0], cs[0][1]);
+    s = f2_make(cs[1][0], cs[1][1]);
+}
+
+__device__ __forceinline__ float2 turn(int64_t position, uint64_t step, float magnitude) {
+    f2 c, s;
+    turn2(position, step, step, magnitude, c, s);
+    return make_float2(f2_get(c).x, f2_get(s).x);
 }
 
 __device__ __forceinline__ int64_t position_of(const RopeP& p, int64_t b, int64_t s) {
@@ -127,18 +166,22 @@ struct Lane {
         const int half = p.R / 2;
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
-            float2 t[2];
+            uint64_t step[2];  // 0: an angle that is not used
+            uint32_t flip[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 int j = index(n + k);
                 const bool second = LAYOUT == kExchange && j >= half;
                 if (second) j -= half;
-                t[k] = make_float2(0.f, 0.f);
-                if (LAYOUT == kHalves || j < half) t[k] = turn<DT>(position, __ldg(p.steps + j), p.magnitude);
-                if (LAYOUT == kExchange && second == (SIGN < 0)) t[k].y = -t[k].y;
+                step[k] = LAYOUT == kHalves || j < half ? __ldg(p.steps + j) : 0;
+                flip[k] = LAYOUT == kExchange && second == (SIGN < 0) ? 0x80000000u : 0u;
             }
-            c[n / 2] = f2_make(t[0].x, t[1].x);
-            s[n / 2] = f2_make(t[0].y, t[1].y);
+            turn2(position, step[0], step[1], p.magnitude, c[n / 2], s[n / 2]);
+            if (LAYOUT == kExchange) {
+                const float2 v = f2_get(s[n / 2]);
+                s[n / 2] = f2_make(__uint_as_float(__float_as_uint(v.x) ^ flip[0]),
+                                   __uint_as_float(__float_as_uint(v.y) ^ flip[1]));
+            }
         }
     }
     // The lane's values turned by SIGN times the angle; `row`: the team's room for a
@@ -521,7 +564,7 @@ __global__ void __launch_bounds__(256) rope_fwd_generic_kernel(const RopeP p) {
         const int64_t pos = position_of(p, u.b, u.s);
         __syncwarp();  // every lane's reads for the sum before the first write
         for (int j = lane; j < half; j += 32) {
-            const float2 cs = turn<kFP32>(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn(pos, p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float xa = x(a), xb = x(b);
             store1<DT>(g.out.p, y0 + a, fmaf(xa, cs.x, -xb * cs.y));
@@ -555,7 +598,7 @@ __global__ void __launch_bounds__(256) rope_bwd_generic_kernel(const RopeP p) {
         // The gradient of the normed head at pair j (as its two values) and
         // behind rotary_dim.
         auto back = [&](int j) {
-            const float2 cs = turn<kFP32>(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn(pos, p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float da = load1<DT>(g.in.p, d0 + a), db = load1<DT>(g.in.p, d0 + b);
             return make_float2(fmaf(da, cs.x, db * cs.y), fmaf(db, cs.x, -da * cs.y));
