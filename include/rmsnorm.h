@@ -648,7 +648,8 @@ int rmsnorm_cache_read(const rmsnorm_cache_t* cache, const int32_t* table, int64
 /* Synchronises `stream`, then reads and clears the current device's status
  * word. Returns RMSNORM_OK, RMSNORM_ERR_DEVICE_TIMEOUT if any kernel since the
  * last check gave up a bounded wait, RMSNORM_ERR_DEVICE_INDEX if one met an
- * index out of range, or RMSNORM_ERR_CUDA. */
+ * index out of range (where both happened, the next check reports the index), or
+ * RMSNORM_ERR_CUDA. */
 int rmsnorm_check_device_status(void* stream);
 
 /* Static text for a status code. */

@@ -546,12 +546,14 @@ extern "C" int rmsnorm_check_device_status(void* stream) {
     e = status_read_and_clear(&v);
     if (e == cudaSuccess) e = cluster_status_read_and_clear(&vc);
     if (e == cudaSuccess) e = bwd_status_read_and_clear(&vb);
-    if (e == cudaSuccess) e = cache_status_read_and_clear(&vi);
     if (e == cudaSuccess) e = block_status_read_and_clear(&vo);
     if (e == cudaSuccess) e = block_bwd_status_read_and_clear(&vw);
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
     if (v != 0 || vc != 0 || vb != 0 || vo != 0 || vw != 0)
         return fail(RMSNORM_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait");
+    // Read behind the waits' words: an index stays for the next check where one is reported.
+    e = cache_status_read_and_clear(&vi);
+    if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
     if (vi != 0)
         return fail(RMSNORM_ERR_DEVICE_INDEX, "a kernel skipped a slot, page or row index out of range");
     return RMSNORM_OK;
