@@ -17,6 +17,7 @@ namespace rmsn {
 
 // Bit 0: a bounded wait ran out since the last read. One word per device.
 __device__ unsigned int g_block_status;
+static std::atomic<bool> g_launched{false};  // a kernel that writes it
 
 namespace {
 
@@ -507,6 +508,7 @@ cudaError_t run(const BlockP& p, const OpCfg& c) {
 }  // namespace
 
 cudaError_t block_fwd_run(const BlockP& p, const OpCfg& c) {
+    g_launched.store(true);
     switch (p.dtype) {
         case kBF16: return run<kBF16>(p, c);
         case kFP16: return run<kFP16>(p, c);
@@ -515,7 +517,7 @@ cudaError_t block_fwd_run(const BlockP& p, const OpCfg& c) {
 }
 
 cudaError_t block_status_read_and_clear(unsigned int* value) {
-    return symbol_read_and_clear(g_block_status, value);
+    return symbol_read_and_clear(g_block_status, g_launched, value);
 }
 
 }  // namespace rmsn

@@ -32,6 +32,7 @@ namespace rmsn {
 
 // Bit 0: a bounded wait ran out since the last read. One word per device.
 __device__ unsigned int g_block_bwd_status;
+static std::atomic<bool> g_launched{false};  // a kernel that writes it
 
 namespace {
 
@@ -1129,6 +1130,7 @@ int block_bwd_max_grid(int64_t M, int64_t N, int sm_count) {
 }
 
 cudaError_t block_bwd_run(const BlockBwdP& p, const OpCfg& c) {
+    g_launched.store(true);
     switch (p.dtype) {
         case kBF16: return run<kBF16>(p, c);
         case kFP16: return run<kFP16>(p, c);
@@ -1137,7 +1139,7 @@ cudaError_t block_bwd_run(const BlockBwdP& p, const OpCfg& c) {
 }
 
 cudaError_t block_bwd_status_read_and_clear(unsigned int* value) {
-    return symbol_read_and_clear(g_block_bwd_status, value);
+    return symbol_read_and_clear(g_block_bwd_status, g_launched, value);
 }
 
 }  // namespace rmsn

@@ -21,6 +21,7 @@ namespace rmsn {
 
 // Bit 0: an index was out of range since the last read. One word per device.
 __device__ unsigned int g_cache_status;
+static std::atomic<bool> g_launched{false};  // a kernel that writes it
 
 namespace {
 
@@ -495,17 +496,19 @@ cudaError_t pick(bool write, const CacheP& p, const OpCfg& c) {
 }  // namespace
 
 cudaError_t cache_write_run(const CacheP& p, const OpCfg& c) {
+    g_launched.store(true);
     return p.format == RMSNORM_CACHE_E4M3 ? pick<RMSNORM_CACHE_E4M3>(true, p, c)
                                           : pick<RMSNORM_CACHE_E2M1>(true, p, c);
 }
 
 cudaError_t cache_read_run(const CacheP& p, const OpCfg& c) {
+    g_launched.store(true);
     return p.format == RMSNORM_CACHE_E4M3 ? pick<RMSNORM_CACHE_E4M3>(false, p, c)
                                           : pick<RMSNORM_CACHE_E2M1>(false, p, c);
 }
 
 cudaError_t cache_status_read_and_clear(unsigned int* value) {
-    return symbol_read_and_clear(g_cache_status, value);
+    return symbol_read_and_clear(g_cache_status, g_launched, value);
 }
 
 }  // namespace rmsn

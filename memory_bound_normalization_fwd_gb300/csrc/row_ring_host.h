@@ -4,6 +4,8 @@
 #include "ops.h"
 #include "row_ring.cuh"
 
+#include <atomic>
+
 namespace rmsn {
 
 struct RingPlan {
@@ -22,9 +24,12 @@ struct RingPlan {
 bool ring_plan(const void* fn, const OpCfg& c, int64_t M, int nvec, int T, int max_threads, int arrays,
                int extra, int in_flight, int cluster, int64_t max_teams, RingPlan* out);
 
-// Reads a status word of the current device and clears it.
+// Reads a status word of the current device and clears it. `launched`: whether a kernel
+// that writes it ever was; a word that none did is not read (9 us each).
 template <typename S>
-cudaError_t symbol_read_and_clear(const S& symbol, unsigned int* value) {
+cudaError_t symbol_read_and_clear(const S& symbol, const std::atomic<bool>& launched, unsigned int* value) {
+    *value = 0;
+    if (!launched.load()) return cudaSuccess;
     cudaError_t e = cudaMemcpyFromSymbol(value, symbol, sizeof(*value));
     if (e == cudaSuccess && *value != 0) {
         const unsigned int zero = 0;

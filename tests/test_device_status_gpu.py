@@ -4,6 +4,10 @@ check after it.
 """
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +15,7 @@ from memory_bound_normalization_fwd_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_an_index_is_not_lost_behind_a_wait():
@@ -31,3 +36,30 @@ def test_an_index_is_not_lost_behind_a_wait():
         assert status == -12
         assert B.rmsnorm_check_device_status(0) == 0
     assert both > 0
+
+
+FIRST = """
+import torch
+from memory_bound_normalization_fwd_gb300 import binding as B
+assert B.rmsnorm_check_device_status(0) == 0
+cache = B.Cache(4, 16, 2, 64)
+k = torch.randn(1, 2, 64, device="cuda").bfloat16()
+slot = torch.tensor([3], device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    B.cache_write(cache, k, None, slot)
+assert B.rmsnorm_check_device_status(0) == 0
+slot.fill_(64)
+graph.replay()
+assert B.rmsnorm_check_device_status(0) == -12
+graph.replay()
+slot.fill_(2)
+graph.replay()
+assert B.rmsnorm_check_device_status(0) == -12
+assert B.rmsnorm_check_device_status(0) == 0
+"""
+
+
+def test_an_index_met_by_the_only_launch_of_a_process_a_replayed_graph():
+    p = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, cwd=ROOT)
+    assert p.returncode == 0, p.stderr
