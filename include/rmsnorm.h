@@ -362,7 +362,11 @@ int rmsnorm_bwd_workspace_size(int64_t M, int64_t N, int dtype, const rmsnorm_op
  * work enqueued on `stream`, launched like the forward (programmatic dependent
  * launch, stream order kept); capturable into a CUDA graph. Strides are in
  * elements. Whole 16-byte vectors (row or head size, strides and pointers)
- * take the vector kernels, anything else the element-wise ones. `opts` may be
+ * take the vector kernels: block rows of up to 2048 vectors, its backward's of
+ * up to 32768 columns; heads of up to 64 vectors (halves of an even number of
+ * values); cache heads of whole groups. Anything else takes the element-wise
+ * ones, and so, without an explicit variant, does the block's backward of rows of
+ * at most 128 columns where that is faster. `opts` may be
  * NULL; they read variant (AUTO, CTA: the vector kernels, GENERIC: the
  * element-wise kernels), max_ctas, RMSNORM_FLAG_NO_PDL and, for the block
  * operator's kernels that stage rows, wait_limit_ns.

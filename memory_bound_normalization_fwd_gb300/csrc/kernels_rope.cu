@@ -747,7 +747,7 @@ RopeUnits units_of(RopeP* p, const OpCfg& c, int threads, int ctas_per_sm) {
     // us, at eight units per team and up to 16 heads / one and up to 16 / one and up to
     // 8: 8169 tokens of 25 heads of 128 bf16 with norms 31.6 / 22.8 / 23.6, 7391 of 24 of
     // 80 29.9 / 18.0 / 17.9, 16384 of 40 of 128 59.0 / 59.0 / 56.7, its backward 82.8 /
-    // 84.2 / 82.9).
+    // 84.2 / 82.9, each before the angles' series, which costs up to 2%).
     const int64_t heads = p->seg[0].heads + p->seg[1].heads;
     const int64_t share = std::max<int64_t>(1, std::min<int64_t>(8, tokens * heads / (cap * teams)));
     int64_t work[2] = {0, 0};
