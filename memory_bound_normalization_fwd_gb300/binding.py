@@ -554,7 +554,8 @@ def _workspace(t, size, *key):
 
 
 def _given(workspace, device):
-    """(address, bytes) of a caller's workspace: all of its bytes and no others."""
+    """(address, bytes) of a workspace, which may be a caller's: all of its bytes and no
+    others."""
     if workspace.get_device() != device:
         raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
     if not workspace.is_contiguous():  # a view's bytes are not numel * element size from its start
@@ -689,8 +690,9 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
     zero), the s and rstd that the forward returned and its other arguments.
 
     dgate is in the gate's shape and dtype, dw_post and dw_pre in fp32 (None
-    without gate, w_post, w_pre; zeros where there are no rows). ``workspace`` is a contiguous CUDA tensor of at
-    least rmsnorm_block_bwd_workspace_size() bytes; allocated here when not given.
+    without gate, w_post, w_pre; zeros where there are no rows). ``workspace`` is a
+    contiguous CUDA tensor of at least rmsnorm_block_bwd_workspace_size() bytes;
+    allocated here when not given.
     """
     import torch
     ctx = _elsewhere(h, stream)
