@@ -649,6 +649,154 @@ int rmsnorm_cache_read(const rmsnorm_cache_t* cache, const int32_t* table, int64
                        int64_t rows, const rmsnorm_heads_t* k_out, const rmsnorm_heads_t* v_out,
                        int dtype, const rmsnorm_options_t* opts, void* stream);
 
+/*
+ * Rotary positions with several axes (frames, rows and columns of images and
+ * video): as rmsnorm_rope_fwd and rmsnorm_rope_bwd, but pair i turns by the position
+ * of its axis. args.positions (required) are those of axis 0, axis a's lie axis_stride
+ * elements further each. The pairs are dealt to the axes in sections (the first
+ * pairs[0] pairs to axis 0, the next pairs[1] to axis 1, ...), or in turn: pair i
+ * belongs to axis i % axes while i / axes < pairs[i % axes], and to axis 0 otherwise.
+ * The frequencies (args.steps) are one per pair as before: one table over all
+ * pairs, or, for axes with frequencies of their own, the axes' tables one behind
+ * the other.
+ */
+typedef struct rmsnorm_rope_axes {
+    int32_t struct_size;  /* sizeof(rmsnorm_rope_axes_t) */
+    int32_t axes;         /* 1..4 */
+    int32_t pairs[4];     /* of each axis, >= 0, 0 past the last; together rotary_dim / 2 */
+    int32_t in_turn;      /* 0 or 1; in turn, the pairs named for every axis must lie below
+                             rotary_dim / 2: axes * (pairs[a] - 1) + a for a >= 1 */
+    int32_t reserved;     /* 0 */
+    int64_t axis_stride;  /* >= 0 */
+} rmsnorm_rope_axes_t;
+
+int rmsnorm_rope_axes_fwd(const rmsnorm_rope_args_t* args, const rmsnorm_rope_axes_t* axes,
+                          const rmsnorm_options_t* opts, void* stream);
+int rmsnorm_rope_axes_bwd(const rmsnorm_rope_args_t* args, const rmsnorm_rope_axes_t* axes,
+                          const rmsnorm_rope_grads_t* grads, void* workspace, int64_t workspace_bytes,
+                          const rmsnorm_options_t* opts, void* stream);
+
+/*
+ * Attention of ragged queries over the cache, which is read as it is held:
+ *
+ *   out[i, h] = sum_t p_t v[t, h / G]     p = softmax over t of scale * q[i, h] . k[t, h / G]
+ *   lse[i, h] = log of the sum over t of exp(scale * q[i, h] . k[t, h / G])
+ *
+ * with G = heads_q / cache heads. Rows cu_rows[b] to cu_rows[b + 1] of q and out are
+ * the n newest tokens of sequence b, which holds lengths[b] tokens (the new ones among
+ * them, written before the call): row cu_rows[b] + i is at position
+ * lengths[b] - n + i. It sees the tokens 0 <= t < lengths[b], with causal those up to its
+ * own position, with a window those after its position - window. A row that sees
+ * nothing gets zeros and an lse of -infinity. Token t of sequence b lies in slot
+ * table[b][t / page_size] * page_size + t % page_size; a token whose page lies outside
+ * the cache or the table is left out and reported by rmsnorm_check_device_status.
+ * Tokens that no row sees may hold anything; a group stored with an infinity or a NaN
+ * (scale byte 255) makes NaN of what sees it: of the rows by k, of the group's values by v.
+ * A code that is itself a NaN (E4M3, which rmsnorm_cache_write never stores) may reach
+ * further within its tile of tokens.
+ *
+ * Products are exact (codes and q in 16 bits or split into such), sums and softmax
+ * statistics are held in fp32; probabilities are rounded to 11 bits for 16-bit outputs and
+ * to 22 bits for fp32.
+ *   cu_rows  [sequences + 1] int32, not decreasing, from 0; NULL: one row a sequence
+ *            (rows == sequences)
+ *   rows     rows of q and out; rows from cu_rows[sequences] on are left as they are
+ *   q, out   tokens [rows, heads_q, head_dim] (batch_stride is not read); out may not
+ *            overlap q; the cache must hold v, with head_dim at most 512
+ *   lse      [rows, heads_q] fp32, contiguous, or NULL
+ *   workspace  device scratch of rmsnorm_cache_attention_workspace_size() bytes, 16-byte
+ *            aligned; calls that share one must not overlap on the GPU
+ */
+typedef struct rmsnorm_cache_attention_args {
+    int32_t struct_size;  /* sizeof(rmsnorm_cache_attention_args_t) */
+    int32_t dtype;        /* rmsnorm_dtype_t of q and out */
+    int32_t heads_q;      /* a multiple of the cache's heads */
+    int32_t causal;       /* 0 or 1 */
+    int64_t sequences;
+    int64_t rows;
+    int64_t table_width;
+    int64_t window;       /* tokens a row sees, its own among them; 0: no window (needs causal) */
+    const int32_t* table; /* [sequences, table_width], contiguous */
+    const int32_t* lengths; /* [sequences], >= 0 (below: taken as 0) */
+    const int32_t* cu_rows;
+    float* lse;
+    float scale;          /* finite */
+    float reserved;       /* 0 */
+    rmsnorm_heads_t q;
+    rmsnorm_heads_t out;
+} rmsnorm_cache_attention_args_t;
+
+int rmsnorm_cache_attention(const rmsnorm_cache_t* cache, const rmsnorm_cache_attention_args_t* args,
+                            void* workspace, int64_t workspace_bytes, const rmsnorm_options_t* opts,
+                            void* stream);
+
+/* Bytes of workspace rmsnorm_cache_attention needs on the current device for any
+ * lengths, strides and options. */
+int rmsnorm_cache_attention_workspace_size(int32_t cache_heads, int32_t heads_q, int32_t head_dim,
+                                           int64_t sequences, int64_t rows, int64_t* bytes);
+
+/*
+ * Pages of a cache that sequences share. refs[p] is the number of table entries that name
+ * page p (0: free); an entry below 0 names none; lengths[b] tokens of sequence b lie in
+ * the pages of its row of the table, from the first on.
+ */
+typedef struct rmsnorm_cache_pages {
+    int32_t struct_size;  /* sizeof(rmsnorm_cache_pages_t) */
+    int32_t reserved;     /* 0 */
+    int64_t pages;        /* of the cache: 1..2^25 */
+    int64_t sequences;    /* 0..2^30 */
+    int64_t table_width;  /* 0..2^30 */
+    int32_t* refs;        /* [pages] */
+    int32_t* table;       /* [sequences, table_width], contiguous */
+    int32_t* lengths;     /* [sequences]; rmsnorm_cache_compact takes NULL */
+} rmsnorm_cache_pages_t;
+
+/* Copies page src[i] to page dst[i] for i < n (int32 on the device; either below 0: no
+ * copy). A page past the cache is skipped and reported by rmsnorm_check_device_status.
+ * Pages in dst must be distinct and must not be in src (else they end with bytes of
+ * either). */
+int rmsnorm_cache_copy_pages(const rmsnorm_cache_t* cache, const int32_t* src, const int32_t* dst,
+                             int64_t n, const rmsnorm_options_t* opts, void* stream);
+
+/*
+ * Makes sequence children[i] a copy of parents[i] for i < n (int32 on the device; either
+ * below 0: nothing is done). Full pages are shared (refs + 1); the tokens of a last page that is
+ * not full are copied into a free page, the lowest ones in the order of i; the rest of the
+ * child's row becomes -1. lengths are those before the call. A child must be empty
+ * (length 0; its row is overwritten). Reported by rmsnorm_check_device_status and left as it
+ * is: a child that is not empty, named twice (all but the first), or its own parent; a row
+ * past the table; a parent whose tokens exceed its row; a child for which no free page is
+ * left. Entries of a parent's tokens that name no page of the cache are copied as they are
+ * and reported.
+ *   workspace  rmsnorm_cache_pages_workspace_size() bytes, 16-byte aligned
+ */
+int rmsnorm_cache_fork(const rmsnorm_cache_t* cache, const rmsnorm_cache_pages_t* pages,
+                       const int32_t* parents, const int32_t* children, int64_t n, void* workspace,
+                       int64_t workspace_bytes, const rmsnorm_options_t* opts, void* stream);
+
+/* Frees the sequences rows[i], i < n (int32 on the device; below 0: none): the pages of their
+ * rows lose a reference each, the rows become -1, the lengths 0. A row named twice is freed
+ * once. A row past the table, an entry past the cache and a page without references are
+ * skipped and reported by rmsnorm_check_device_status. */
+int rmsnorm_cache_free(const rmsnorm_cache_pages_t* pages, const int32_t* rows, int64_t n,
+                       const rmsnorm_options_t* opts, void* stream);
+
+/*
+ * Brings the live pages (refs > 0) together: with L of them, those from page L on move, in
+ * their order, into the free pages below L, in theirs. refs_out and table_out (each may be
+ * pages.refs and pages.table themselves) name the pages where they are then; live[0] = L.
+ * Codes and scales of moved pages are copied, and what lies in the pages from L on stays.
+ * Entries past the cache are kept and reported, those that name a free page kept.
+ *   workspace  as in rmsnorm_cache_fork
+ */
+int rmsnorm_cache_compact(const rmsnorm_cache_t* cache, const rmsnorm_cache_pages_t* pages,
+                          int32_t* refs_out, int32_t* table_out, int32_t* live, void* workspace,
+                          int64_t workspace_bytes, const rmsnorm_options_t* opts, void* stream);
+
+/* Bytes of workspace that rmsnorm_cache_fork (of n children, in a table of `sequences` rows)
+ * and rmsnorm_cache_compact (n and sequences 0) need. No CUDA call. */
+int rmsnorm_cache_pages_workspace_size(int64_t pages, int64_t sequences, int64_t n, int64_t* bytes);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * word. Returns RMSNORM_OK, RMSNORM_ERR_DEVICE_TIMEOUT if any kernel since the
  * last check gave up a bounded wait, RMSNORM_ERR_DEVICE_INDEX if one met an

@@ -31,6 +31,9 @@ EXPORTS = ("rmsnorm_fwd", "rmsnorm_fwd_ex", "rmsnorm_fwd_strided", "rmsnorm_fwd_
            "rmsnorm_block_fwd", "rmsnorm_block_bwd", "rmsnorm_block_bwd_workspace_size",
            "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_size",
            "rmsnorm_rope_steps", "rmsnorm_cache_write", "rmsnorm_cache_read",
+           "rmsnorm_rope_axes_fwd", "rmsnorm_rope_axes_bwd", "rmsnorm_cache_attention",
+           "rmsnorm_cache_attention_workspace_size", "rmsnorm_cache_copy_pages", "rmsnorm_cache_fork",
+           "rmsnorm_cache_free", "rmsnorm_cache_compact", "rmsnorm_cache_pages_workspace_size",
            "rmsnorm_check_device_status",
            "rmsnorm_strerror", "rmsnorm_last_error", "rmsnorm_version")
 
@@ -106,6 +109,24 @@ class RopeScaling(ctypes.Structure):
                 + [(n, ctypes.c_double) for n in ("factor", "length", "beta_fast", "beta_slow")])
 
 
+class RopeAxesArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _I), ("axes", _I), ("pairs", _I * 4), ("in_turn", _I), ("reserved", _I),
+                ("axis_stride", _Q)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, _I) for n in ("struct_size", "dtype", "heads_q", "causal")]
+                + [(n, _Q) for n in ("sequences", "rows", "table_width", "window")]
+                + [(n, _P) for n in ("table", "lengths", "cu_rows", "lse")]
+                + [("scale", _F), ("reserved", _F), ("q", Heads), ("out", Heads)])
+
+
+class PagesArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", _I), ("reserved", _I)]
+                + [(n, _Q) for n in ("pages", "sequences", "table_width")]
+                + [(n, _P) for n in ("refs", "table", "lengths")])
+
+
 class CacheArgs(ctypes.Structure):
     _fields_ = ([("struct_size", _I), ("format", _I), ("pages", _Q)]
                 + [(n, _I) for n in ("page_size", "heads", "head_dim", "heads_first")]
@@ -173,6 +194,16 @@ def lib() -> ctypes.CDLL:
             L.rmsnorm_cache_write.argtypes = [vp, vp, vp, vp, i64, i32, ctypes.POINTER(Options), vp]
             L.rmsnorm_cache_read.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, vp, i32,
                                              ctypes.POINTER(Options), vp]
+            opt, size = ctypes.POINTER(Options), ctypes.POINTER(ctypes.c_int64)
+            L.rmsnorm_rope_axes_fwd.argtypes = [vp, vp, opt, vp]
+            L.rmsnorm_rope_axes_bwd.argtypes = [vp, vp, vp, vp, i64, opt, vp]
+            L.rmsnorm_cache_attention.argtypes = [vp, vp, vp, i64, opt, vp]
+            L.rmsnorm_cache_attention_workspace_size.argtypes = [i32, i32, i32, i64, i64, size]
+            L.rmsnorm_cache_copy_pages.argtypes = [vp, vp, vp, i64, opt, vp]
+            L.rmsnorm_cache_fork.argtypes = [vp, vp, vp, vp, i64, vp, i64, opt, vp]
+            L.rmsnorm_cache_free.argtypes = [vp, vp, i64, opt, vp]
+            L.rmsnorm_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, i64, opt, vp]
+            L.rmsnorm_cache_pages_workspace_size.argtypes = [i64, i64, i64, size]
             for name in EXPORTS:
                 if name.startswith(("rmsnorm_block", "rmsnorm_rope", "rmsnorm_cache")):
                     getattr(L, name).restype = i32
@@ -354,6 +385,61 @@ def rmsnorm_cache_read(cache: CacheArgs | bytes, table: int, table_width: int, c
                                     rows, _arg(k_out), _arg(v_out), dtype, _opt(opts), stream)
 
 
+def rmsnorm_rope_axes_fwd(args: RopeArgs | bytes, axes: RopeAxesArgs | bytes, opts: Options | None,
+                          stream: int) -> int:
+    return lib().rmsnorm_rope_axes_fwd(_arg(args), _arg(axes), _opt(opts), stream)
+
+
+def rmsnorm_rope_axes_bwd(args: RopeArgs | bytes, axes: RopeAxesArgs | bytes, grads: RopeGrads | bytes,
+                          workspace: int, workspace_bytes: int, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_rope_axes_bwd(_arg(args), _arg(axes), _arg(grads), workspace, workspace_bytes,
+                                       _opt(opts), stream)
+
+
+def rmsnorm_cache_attention(cache: CacheArgs | bytes, args: AttentionArgs | bytes, workspace: int,
+                            workspace_bytes: int, opts: Options | None, stream: int) -> int:
+    return lib().rmsnorm_cache_attention(_arg(cache), _arg(args), workspace, workspace_bytes, _opt(opts),
+                                         stream)
+
+
+def rmsnorm_cache_attention_workspace_size(cache_heads: int, heads_q: int, head_dim: int, sequences: int,
+                                           rows: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().rmsnorm_cache_attention_workspace_size(cache_heads, heads_q, head_dim, sequences, rows,
+                                                        ctypes.byref(n)))
+    return n.value
+
+
+def rmsnorm_cache_copy_pages(cache: CacheArgs | bytes, src: int, dst: int, n: int, opts: Options | None,
+                             stream: int) -> int:
+    return lib().rmsnorm_cache_copy_pages(_arg(cache), src, dst, n, _opt(opts), stream)
+
+
+def rmsnorm_cache_fork(cache: CacheArgs | bytes, pages: PagesArgs | bytes, parents: int, children: int,
+                       n: int, workspace: int, workspace_bytes: int, opts: Options | None,
+                       stream: int) -> int:
+    return lib().rmsnorm_cache_fork(_arg(cache), _arg(pages), parents, children, n, workspace,
+                                    workspace_bytes, _opt(opts), stream)
+
+
+def rmsnorm_cache_free(pages: PagesArgs | bytes, rows: int, n: int, opts: Options | None,
+                       stream: int) -> int:
+    return lib().rmsnorm_cache_free(_arg(pages), rows, n, _opt(opts), stream)
+
+
+def rmsnorm_cache_compact(cache: CacheArgs | bytes, pages: PagesArgs | bytes, refs_out: int, table_out: int,
+                          live: int, workspace: int, workspace_bytes: int, opts: Options | None,
+                          stream: int) -> int:
+    return lib().rmsnorm_cache_compact(_arg(cache), _arg(pages), refs_out, table_out, live, workspace,
+                                       workspace_bytes, _opt(opts), stream)
+
+
+def rmsnorm_cache_pages_workspace_size(pages: int, sequences: int, n: int) -> int:
+    size = ctypes.c_int64()
+    _check(lib().rmsnorm_cache_pages_workspace_size(pages, sequences, n, ctypes.byref(size)))
+    return size.value
+
+
 def rmsnorm_check_device_status(stream: int = 0) -> int:
     return lib().rmsnorm_check_device_status(stream)
 
@@ -503,6 +589,9 @@ _ROPE = struct.Struct("=2i2q6iQq5Q4f" + "Q3q" * 4)
 _ROPE_GRADS = struct.Struct("=2i" + "Q3q" * 4 + "2Q")
 _CACHE = struct.Struct("=2iq4i4Q")
 _HEADS = struct.Struct("=Q3q")
+_AXES = struct.Struct("=8iq")
+_ATTENTION = struct.Struct("=4i4q4Q2f" + "Q3q" * 2)
+_PAGES = struct.Struct("=2i3q3Q")
 CACHE_FORMATS = {"e4m3": 0, "e2m1": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _CODES: dict = {}
@@ -751,16 +840,49 @@ def block_bwd(h, s, rstd_post, rstd_pre, dy=None, ds=None, w_post=None, w_pre=No
     return dh, dr, dgate, dwa, dwb
 
 
-def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda"):
+class RopeAxes:
+    """The axes (time, height, width; up to four) that the pairs of a head turn by, for
+    rope_fwd and rope_bwd: ``pairs`` of each axis, together rotary_dim / 2. The pairs go to
+    the axes in sections, or with ``in_turn`` one by one: pair i to axis i % axes as long
+    as that one has pairs left, and to the first axis otherwise.
+    """
+
+    def __init__(self, pairs, in_turn: bool = False):
+        self.pairs, self.in_turn = tuple(int(n) for n in pairs), bool(in_turn)
+        if not 1 <= len(self.pairs) <= 4 or min(self.pairs) < 0:
+            raise ValueError(f"pairs must be of one to four axes, each >= 0, got {self.pairs}")
+        self._fields = (40, len(self.pairs), *self.pairs, *(0,) * (4 - len(self.pairs)),
+                        int(self.in_turn), 0)
+        self._packed: dict = {}
+
+    def _args(self, axis_stride: int) -> bytes:
+        args = self._packed.get(axis_stride)
+        if args is None:
+            if len(self._packed) >= 256:  # ragged batches: as many strides as lengths
+                self._packed.clear()
+            args = self._packed[axis_stride] = _AXES.pack(*self._fields, axis_stride)
+        return args
+
+
+def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda",
+               axes: RopeAxes | None = None):
     """steps, magnitude = rope_steps(rotary_dim): the frequencies of rotary positions
     as rope_fwd and rope_bwd take them (int64 [rotary_dim / 2] on the device: turns
     per position times 2^64), and the factor on cos and sin that belongs to them.
+    With ``axes`` (in sections) every axis has frequencies of its own: those of a
+    rotary_dim of twice its pairs, one axis behind the other.
 
     ``scaling``: None or a dict with "kind" ("linear", "ntk", "yarn" or "bands"),
     "factor", and for "yarn" and "bands" the original "length" and optionally
     "beta_fast" (32 for yarn, 4 for bands) and "beta_slow" (1).
     """
     import torch
+    if axes is not None:
+        if axes.in_turn or 2 * sum(axes.pairs) != rotary_dim:
+            raise ValueError(f"frequencies of the axes' own are for sections of {rotary_dim // 2} pairs "
+                             f"together, got {axes.pairs}")
+        own = [rope_steps(2 * n, base, scaling, device) for n in axes.pairs if n]
+        return torch.cat([s for s, _ in own]), own[0][1]
     steps = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
     sc = None
     if scaling:
@@ -802,8 +924,8 @@ def _new_heads(like, shape):
     return t, (t.data_ptr(), S * H * D, H * D, D)
 
 
-def _rope_common(q, k, steps, positions, w_q, w_k, interleaved):
-    """The fields of the rope struct up to the weights."""
+def _rope_common(q, k, steps, positions, w_q, w_k, interleaved, axes):
+    """The fields of the rope struct up to the weights, and the packed axes."""
     import torch
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     if len(shape) == 3:
@@ -821,7 +943,18 @@ def _rope_common(q, k, steps, positions, w_q, w_k, interleaved):
     half = steps.numel()
     sp = _vector(steps, "steps", half, torch.int64, dev)
     pp = ps = 0
-    if positions is not None:
+    packed = None
+    if axes is not None:
+        if positions is None:
+            raise ValueError("positions must be given with axes: [axes, seq] or [axes, batch, seq]")
+        if positions.dtype is not torch.int64 or positions.get_device() != dev:
+            _refuse(positions, "positions", None, torch.int64, dev)
+        ps, n = positions.shape, len(axes.pairs)
+        if (ps != (n, *shape[:-2]) and ps != (n, S)) or (S > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be [{n}, seq] or [{n}, batch, seq], the last contiguous")
+        packed = axes._args(positions.stride(0) if n > 1 else 0)
+        pp, ps = positions.data_ptr(), positions.stride(1) if len(ps) == 3 and B > 1 else 0
+    elif positions is not None:
         if positions.dtype is not torch.int64 or positions.get_device() != dev:
             _refuse(positions, "positions", None, torch.int64, dev)
         ps = positions.shape
@@ -829,12 +962,12 @@ def _rope_common(q, k, steps, positions, w_q, w_k, interleaved):
             raise ValueError("positions must be [seq] or [batch, seq], the last contiguous")
         pp, ps = positions.data_ptr(), positions.stride(0) if len(ps) == 2 and B > 1 else 0
     return (248, _code(dtype), B, S, hq, hk, D, 2 * half, 1 if interleaved else 0, 0, pp, ps, sp,
-            _vector(w_q, "w_q", D, dtype, dev), _vector(w_k, "w_k", D, dtype, dev))
+            _vector(w_q, "w_q", D, dtype, dev), _vector(w_k, "w_k", D, dtype, dev)), packed
 
 
 def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool = False,
              eps: float = 1e-6, offset: float = 0.0, magnitude: float = 1.0, q_out=None, k_out=None,
-             rstd: bool = True, stream=None, **options):
+             rstd: bool = True, stream=None, axes: RopeAxes | None = None, **options):
     """q_out, k_out, rstd_q, rstd_k = rope_fwd(q, k, steps, positions): rotary positions
     on the first 2 * len(steps) values of every head, after the head's RMSNorm where
     w_q or w_k is given.
@@ -846,14 +979,16 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
     (default: the index). Pairs are (i, i + half), or (2i, 2i + 1) when
     ``interleaved``. ``q_out`` and ``k_out`` may be passed (q and k themselves to work in
     place). rstd_q and rstd_k are None without weights or with ``rstd=False``.
+    With ``axes`` (:class:`RopeAxes`) each pair turns by the position of its axis, and
+    ``positions`` is int64 [axes, T], [axes, seq] or [axes, batch, seq].
     """
     import torch
     ctx = _elsewhere(q, stream)
     if ctx is not None:
         with ctx:
             return rope_fwd(q, k, steps, positions, w_q, w_k, interleaved, eps, offset, magnitude,
-                            q_out, k_out, rstd, **options)
-    head = _rope_common(q, k, steps, positions, w_q, w_k, interleaved)
+                            q_out, k_out, rstd, axes=axes, **options)
+    head, axes = _rope_common(q, k, steps, positions, w_q, w_k, interleaved, axes)
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     qh = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
@@ -879,8 +1014,11 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
         a = q.new_empty(shape[:-1], dtype=torch.float32)
         ap = a.data_ptr()
     args = _ROPE.pack(*head, ap, bp, eps, offset, magnitude, 0.0, *qh, *kh, *qo, *ko)
-    rc = (_lib or lib()).rmsnorm_rope_fwd(args, _opt(make_options(**options)) if options else None,
-                                          _stream_ptr(dev))
+    opts = _opt(make_options(**options)) if options else None
+    if axes is None:
+        rc = (_lib or lib()).rmsnorm_rope_fwd(args, opts, _stream_ptr(dev))
+    else:
+        rc = (_lib or lib()).rmsnorm_rope_axes_fwd(args, axes, opts, _stream_ptr(dev))
     if rc:
         _check(rc)
     return q_out, k_out, a, b
@@ -888,21 +1026,23 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
 
 def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None, rstd_k=None,
              w_q=None, w_k=None, interleaved: bool = False, offset: float = 0.0,
-             magnitude: float = 1.0, dq=None, dk=None, workspace=None, stream=None, **options):
+             magnitude: float = 1.0, dq=None, dk=None, workspace=None, stream=None,
+             axes: RopeAxes | None = None, **options):
     """dq, dk, dw_q, dw_k = rope_bwd(dq_out, dk_out, steps, positions, ...): backward of
     :func:`rope_fwd` from the gradients of its outputs. With w_q (w_k) it needs the
     forward's q (k) and the rstd_q (rstd_k) it returned. dw_q and dw_k are fp32
     (None without weights). ``dq`` and ``dk`` may be passed (dq_out and dk_out
     themselves to work in place); ``workspace`` as in :func:`block_bwd`
-    (rmsnorm_rope_bwd_workspace_size() bytes, needed with weights only).
+    (rmsnorm_rope_bwd_workspace_size() bytes, needed with weights only); ``axes`` as in
+    the forward.
     """
     import torch
     ctx = _elsewhere(dq_out, stream)
     if ctx is not None:
         with ctx:
             return rope_bwd(dq_out, dk_out, steps, positions, q, k, rstd_q, rstd_k, w_q, w_k,
-                            interleaved, offset, magnitude, dq, dk, workspace, **options)
-    head = _rope_common(dq_out, dk_out, steps, positions, w_q, w_k, interleaved)
+                            interleaved, offset, magnitude, dq, dk, workspace, axes=axes, **options)
+    head, axes = _rope_common(dq_out, dk_out, steps, positions, w_q, w_k, interleaved, axes)
     shape, dtype, dev, f32 = dq_out.shape, dq_out.dtype, dq_out.get_device(), torch.float32
     D = shape[-1]
     gq = _heads(dq_out, "dq_out", shape, dtype, dev)
@@ -939,9 +1079,12 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
     ws_ptr = ws_bytes = 0
     if workspace is not None:
         ws_ptr, ws_bytes = _given(workspace, dev)
-    rc = (_lib or lib()).rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes,
-                                          _opt(make_options(**options)) if options else None,
-                                          _stream_ptr(dev))
+    opts = _opt(make_options(**options)) if options else None
+    if axes is None:
+        rc = (_lib or lib()).rmsnorm_rope_bwd(args, grads, ws_ptr, ws_bytes, opts, _stream_ptr(dev))
+    else:
+        rc = (_lib or lib()).rmsnorm_rope_axes_bwd(args, axes, grads, ws_ptr, ws_bytes, opts,
+                                                   _stream_ptr(dev))
     if rc:
         _check(rc)
     return dq, dk, dwq, dwk
@@ -1057,3 +1200,172 @@ def cache_read(cache: Cache, table, cu_rows, rows: int, starts=None, dtype=None,
     if rc:
         _check(rc)
     return k_out, v_out
+
+
+def cache_attention(cache: Cache, q, table, lengths, cu_q=None, scale: float | None = None,
+                    causal: bool = True, window: int = 0, out=None, lse: bool = False, workspace=None,
+                    stream=None, **options):
+    """out, lse = cache_attention(cache, q, table, lengths): attention of q ([rows, heads,
+    head_dim], unit stride within a head; heads a multiple of the cache's) over the tokens
+    that ``cache`` holds, read in its 8 or 4 bits.
+
+    Rows cu_q[b] to cu_q[b + 1] (int32 [sequences + 1]; None: one row a sequence) are the
+    newest of the lengths[b] (int32, with the new ones, which are written before) tokens of
+    sequence b, whose pages its row of ``table`` (int32 [sequences, pages per sequence]) names.
+    A row sees the tokens up to its own position, all of its sequence with
+    ``causal=False``, and with ``window`` the last so many of them only; a row that sees nothing
+    gets zeros. ``scale`` is 1 / sqrt(head_dim) by default. ``out`` may be passed; rows behind
+    cu_q[-1] are not written. lse is fp32 [rows, heads] (natural logarithms, for joining with
+    attention over other tokens), None unless asked for. ``workspace`` is a contiguous
+    CUDA tensor of at least rmsnorm_cache_attention_workspace_size() bytes; allocated here when
+    not given.
+    """
+    import torch
+    like = cache.k_codes
+    ctx = _elsewhere(like, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_attention(cache, q, table, lengths, cu_q, scale, causal, window, out, lse,
+                                   workspace, **options)
+    dev, dtype, i32 = like.get_device(), q.dtype, torch.int32
+    code, shape = _code(dtype), q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [rows, heads, {cache.head_dim}], got {tuple(shape)}")
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages per sequence]")
+    rows, heads = shape[0], shape[1]
+    n, width = table.shape
+    qh = _heads(q, "q", shape, dtype, dev)
+    tp = _vector(table, "table", n * width, i32, dev)
+    lp = _vector(lengths, "lengths", n, i32, dev)
+    cp = _vector(cu_q, "cu_q", n + 1, i32, dev)
+    if out is None:
+        out, oh = _new_heads(q, shape)
+    else:
+        oh = _heads(out, "out", shape, dtype, dev)
+    kept, kp = None, 0
+    if lse:
+        kept = q.new_empty(shape[:2], dtype=torch.float32)
+        kp = kept.data_ptr()
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    if workspace is None:
+        workspace = _workspace(q, rmsnorm_cache_attention_workspace_size, cache.heads, heads,
+                               cache.head_dim, n, rows)
+    ws_ptr, ws_bytes = _given(workspace, dev)
+    args = _ATTENTION.pack(152, code, heads, 1 if causal else 0, n, rows, width, window, tp, lp, cp, kp,
+                           scale, 0.0, *qh, *oh)
+    rc = (_lib or lib()).rmsnorm_cache_attention(cache._args, args, ws_ptr, ws_bytes,
+                                                 _opt(make_options(**options)) if options else None,
+                                                 _stream_ptr(dev))
+    if rc:
+        _check(rc)
+    return out, kept
+
+
+def _page_arrays(refs, table, lengths, device):
+    """The packed struct of a cache's shared pages."""
+    import torch
+    i32 = torch.int32
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages per sequence]")
+    n, width = table.shape
+    return _PAGES.pack(56, 0, refs.numel(), n, width, _vector(refs, "refs", refs.numel(), i32, device),
+                       _vector(table, "table", n * width, i32, device),
+                       _vector(lengths, "lengths", n, i32, device))
+
+
+def cache_copy_pages(cache: Cache, src, dst, stream=None, **options) -> None:
+    """Copies page src[i] of ``cache`` to page dst[i] (int32; either below 0: no copy). The
+    pages in dst must be distinct, and none of them in src."""
+    import torch
+    ctx = _elsewhere(cache.k_codes, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_copy_pages(cache, src, dst, **options)
+    dev, n = cache.k_codes.get_device(), src.numel()
+    rc = (_lib or lib()).rmsnorm_cache_copy_pages(
+        cache._args, _vector(src, "src", n, torch.int32, dev), _vector(dst, "dst", n, torch.int32, dev), n,
+        _opt(make_options(**options)) if options else None, _stream_ptr(dev))
+    if rc:
+        _check(rc)
+
+
+def cache_fork(cache: Cache, refs, table, lengths, parents, children, workspace=None, stream=None,
+               **options) -> None:
+    """Makes sequence children[i] a copy of sequence parents[i] (int32; below 0: none).
+
+    refs (int32 [pages]) counts the entries of ``table`` (int32 [sequences, pages per
+    sequence], -1: none) that name a page, lengths (int32 [sequences]) the tokens. Full pages
+    are shared; the tokens of a last page that is not full go into the lowest free pages,
+    in the order of the children. All three are updated. A child must be empty (see
+    :func:`cache_free`); what cannot be forked is left as it is and reported by
+    rmsnorm_check_device_status. ``workspace`` is a contiguous CUDA tensor of at least
+    rmsnorm_cache_pages_workspace_size() bytes; allocated here when not given.
+    """
+    import torch
+    like = cache.k_codes
+    ctx = _elsewhere(like, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_fork(cache, refs, table, lengths, parents, children, workspace, **options)
+    dev, n = like.get_device(), parents.numel()
+    pages = _page_arrays(refs, table, lengths, dev)
+    if workspace is None:
+        workspace = _workspace(like, rmsnorm_cache_pages_workspace_size, refs.numel(), table.shape[0], n)
+    ws_ptr, ws_bytes = _given(workspace, dev)
+    rc = (_lib or lib()).rmsnorm_cache_fork(
+        cache._args, pages, _vector(parents, "parents", n, torch.int32, dev),
+        _vector(children, "children", n, torch.int32, dev), n, ws_ptr, ws_bytes,
+        _opt(make_options(**options)) if options else None, _stream_ptr(dev))
+    if rc:
+        _check(rc)
+
+
+def cache_free(refs, table, lengths, rows, stream=None, **options) -> None:
+    """Frees the sequences ``rows`` (int32; below 0: none): their pages lose a reference each, their
+    rows of ``table`` become -1, their lengths 0. A row named twice is freed once."""
+    import torch
+    ctx = _elsewhere(refs, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_free(refs, table, lengths, rows, **options)
+    dev, n = refs.get_device(), rows.numel()
+    rc = (_lib or lib()).rmsnorm_cache_free(
+        _page_arrays(refs, table, lengths, dev), _vector(rows, "rows", n, torch.int32, dev), n,
+        _opt(make_options(**options)) if options else None, _stream_ptr(dev))
+    if rc:
+        _check(rc)
+
+
+def cache_compact(cache: Cache, refs, table, refs_out=None, table_out=None, workspace=None, stream=None,
+                  **options):
+    """live, refs, table = cache_compact(cache, refs, table): brings the pages in use together in
+    the first live[0] pages (int32 [1] on the device). Live pages behind move into the free
+    ones before, in order; the new counts and table are written to ``refs_out`` and
+    ``table_out`` (which may be refs and table themselves), allocated here when not given.
+    ``workspace`` as in :func:`cache_fork` (sequences and n 0).
+    """
+    import torch
+    like = cache.k_codes
+    ctx = _elsewhere(like, stream)
+    if ctx is not None:
+        with ctx:
+            return cache_compact(cache, refs, table, refs_out, table_out, workspace, **options)
+    dev, i32 = like.get_device(), torch.int32
+    pages = _page_arrays(refs, table, None, dev)
+    if refs_out is None:
+        refs_out = refs.new_empty(refs.shape)
+    if table_out is None:
+        table_out = table.new_empty(table.shape)
+    live = refs.new_empty(1)
+    if workspace is None:
+        workspace = _workspace(like, rmsnorm_cache_pages_workspace_size, refs.numel(), 0, 0)
+    ws_ptr, ws_bytes = _given(workspace, dev)
+    rc = (_lib or lib()).rmsnorm_cache_compact(
+        cache._args, pages, _vector(refs_out, "refs_out", refs.numel(), i32, dev),
+        _vector(table_out, "table_out", table.numel(), i32, dev), live.data_ptr(), ws_ptr, ws_bytes,
+        _opt(make_options(**options)) if options else None, _stream_ptr(dev))
+    if rc:
+        _check(rc)
+    return live, refs_out, table_out

@@ -552,9 +552,12 @@ extern "C" int rmsnorm_check_device_status(void* stream) {
     if (v != 0 || vc != 0 || vb != 0 || vo != 0 || vw != 0)
         return fail(RMSNORM_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait");
     // Read behind the waits' words: an index stays for the next check where one is reported.
+    unsigned int vp = 0, va = 0;
     e = cache_status_read_and_clear(&vi);
+    if (e == cudaSuccess) e = pages_status_read_and_clear(&vp);
+    if (e == cudaSuccess) e = attn_status_read_and_clear(&va);
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
-    if (vi != 0)
+    if (vi != 0 || vp != 0 || va != 0)
         return fail(RMSNORM_ERR_DEVICE_INDEX, "a kernel skipped a slot, page or row index out of range");
     return RMSNORM_OK;
 }

@@ -3,168 +3,10 @@
 // stated in include/rmsnorm.h.
 #include "rmsnorm.h"
 
-#include "ops.h"
-
-#include <algorithm>
-#include <cmath>
+#include "op_checks.h"
 
 namespace rmsn {
 namespace {
-
-constexpr int64_t kSpanLimit = int64_t(1) << 48;  // bytes any array may span
-
-bool dtype_ok(int dtype) {
-    return dtype == RMSNORM_DTYPE_BF16 || dtype == RMSNORM_DTYPE_FP16 || dtype == RMSNORM_DTYPE_FP32;
-}
-
-// A strided array: up to three dimensions of (count, stride in bytes) around
-// `inner` contiguous bytes. For overlap checks.
-struct View {
-    uintptr_t base = 0;
-    int64_t inner = 0;
-    int n = 0;
-    int64_t count[3] = {0, 0, 0}, stride[3] = {0, 0, 0};
-
-    View() {}
-    View(const void* p, int64_t bytes) : base(reinterpret_cast<uintptr_t>(p)), inner(bytes) {}
-    View& dim(int64_t c, int64_t s) {
-        if (c > 1) {
-            count[n] = c;
-            stride[n++] = s;
-        }
-        return *this;
-    }
-    bool empty() const { return base == 0 || inner == 0; }
-    // Bytes from the first to the last, over the dimensions with a stride below `m`.
-    int64_t extent(int64_t m) const {
-        int64_t e = inner;
-        for (int i = 0; i < n; ++i)
-            if (stride[i] < m) e += (count[i] - 1) * stride[i];
-        return e;
-    }
-    int64_t span() const { return extent(INT64_MAX); }
-    // Every stride of `m` bytes and above is a multiple of m.
-    bool periodic(int64_t m) const {
-        for (int i = 0; i < n; ++i)
-            if (stride[i] >= m && stride[i] % m != 0) return false;
-        return extent(m) <= m;
-    }
-    // No element of the array lies on another.
-    bool distinct() const {
-        for (int i = 0; i < n; ++i) {
-            int64_t e = inner;
-            for (int k = 0; k < n; ++k)
-                if (stride[k] < stride[i] || (stride[k] == stride[i] && k < i))
-                    e += (count[k] - 1) * stride[k];
-            if (stride[i] < e) return false;
-        }
-        return true;
-    }
-    bool same(const View& o) const {
-        if (base != o.base || inner != o.inner || n != o.n) return false;
-        for (int i = 0; i < n; ++i)
-            if (count[i] != o.count[i] || stride[i] != o.stride[i]) return false;
-        return true;
-    }
-};
-
-// Whether two arrays may share a byte: their spans meet, and no stride that
-// divides both of them into periods keeps them in different parts of a period
-// (as for q and k as slices of one projection's rows).
-bool meet(const View& a, const View& b) {
-    if (a.empty() || b.empty()) return false;
-    if (a.base >= b.base + static_cast<uintptr_t>(b.span()) ||
-        b.base >= a.base + static_cast<uintptr_t>(a.span()))
-        return false;
-    for (int v = 0; v < 2; ++v) {
-        const View& w = v == 0 ? a : b;
-        for (int i = 0; i < w.n; ++i) {
-            const int64_t m = w.stride[i];
-            if (m <= 0 || !a.periodic(m) || !b.periodic(m)) continue;
-            const int64_t d = static_cast<int64_t>(
-                b.base >= a.base ? (b.base - a.base) % static_cast<uintptr_t>(m)
-                                 : (m - static_cast<int64_t>((a.base - b.base) % static_cast<uintptr_t>(m))) % m);
-            if (d >= a.extent(m) && d + b.extent(m) <= m) return false;
-        }
-    }
-    return true;
-}
-
-int read_op_options(const rmsnorm_options_t* opts, OpCfg* c) {
-    int variant;
-    Knobs k;
-    const int rc = read_knobs(opts, &variant, &k);
-    if (rc != RMSNORM_OK) return rc;
-    if (variant != RMSNORM_VARIANT_AUTO && variant != RMSNORM_VARIANT_CTA &&
-        variant != RMSNORM_VARIANT_GENERIC)
-        return fail(RMSNORM_ERR_UNSUPPORTED, "the operators have the variants AUTO, CTA and GENERIC only");
-    c->variant = variant;
-    c->max_ctas = k.max_ctas;
-    c->pdl = (k.flags & RMSNORM_FLAG_NO_PDL) == 0;
-    c->wait_limit_ns = k.wait_limit_ns < 60000000000LL ? k.wait_limit_ns : 60000000000LL;
-    return RMSNORM_OK;
-}
-
-int finish_cfg(OpCfg* c, void* stream) {
-    c->stream = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = device_info(&c->dev);
-    if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
-    return RMSNORM_OK;
-}
-
-// Plans and launches, and reports. The plans' caches allocate host memory: no
-// exception leaves the C entry points.
-template <typename F>
-int launched(F run) {
-    cudaError_t e;
-    try {
-        e = run();
-    } catch (...) {
-        e = cudaErrorMemoryAllocation;
-    }
-    if (e == cudaErrorNotSupported)
-        return fail(RMSNORM_ERR_UNSUPPORTED, "the vector kernels cannot take these sizes, strides or alignments");
-    if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
-    return RMSNORM_OK;
-}
-
-int clear_floats(float* p, int64_t n, void* stream) {
-    if (!p) return RMSNORM_OK;
-    const cudaError_t e = cudaMemsetAsync(p, 0, static_cast<size_t>(n) * 4, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
-    return RMSNORM_OK;
-}
-
-bool misaligned(const void* p, int64_t to) {
-    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(to - 1)) != 0;
-}
-
-// An argument: its array, its name, and a mark. An output may lie exactly on an
-// input of the same mark (not 0): those that one thread reads before it writes.
-struct Named {
-    View v;
-    const char* name;
-    int mark;
-};
-
-int check_overlaps(const Named* outs, int nout, const Named* ins, int nin) {
-    for (int i = 0; i < nout; ++i) {
-        if (outs[i].v.empty()) continue;
-        if (!outs[i].v.distinct())
-            return fail(RMSNORM_ERR_OVERLAP, "%s overlaps itself (strides)", outs[i].name);
-        for (int k = 0; k < i; ++k)
-            if (meet(outs[i].v, outs[k].v))
-                return fail(RMSNORM_ERR_OVERLAP, "%s overlaps %s", outs[i].name, outs[k].name);
-        for (int k = 0; k < nin; ++k) {
-            if (!meet(outs[i].v, ins[k].v)) continue;
-            const bool pair = outs[i].mark != 0 && outs[i].mark == ins[k].mark;
-            if (pair && outs[i].v.same(ins[k].v)) continue;
-            return fail(RMSNORM_ERR_OVERLAP, "%s overlaps %s%s", outs[i].name, ins[k].name,
-                        pair ? " without being equal to it" : "");
-        }
-    }
-    return RMSNORM_OK;
-}
 
 // ---- block --------------------------------------------------------------------
 
@@ -367,36 +209,6 @@ extern "C" int rmsnorm_block_bwd(const rmsnorm_block_args_t* a, const rmsnorm_bl
 
 namespace {
 
-// Strides of a heads tensor: not negative, and the span within 2^48 bytes.
-int check_heads(const char* name, const rmsnorm_heads_t& h, int64_t batch, int64_t seq, int64_t heads,
-                int64_t D, int64_t eb) {
-    if (h.ptr == nullptr) return fail(RMSNORM_ERR_NULL, "%s is NULL", name);
-    const int64_t count[3] = {batch, seq, heads};
-    const int64_t stride[3] = {h.batch_stride, h.token_stride, h.head_stride};
-    int64_t span = D;
-    for (int i = 0; i < 3; ++i) {
-        if (count[i] <= 1) continue;
-        if (stride[i] < 0) return fail(RMSNORM_ERR_SHAPE, "%s has a negative stride", name);
-        if (stride[i] > kSpanLimit / eb / (count[i] - 1))
-            return fail(RMSNORM_ERR_SHAPE, "%s would span more than 2^48 bytes", name);
-        span += (count[i] - 1) * stride[i];
-    }
-    if (span > kSpanLimit / eb) return fail(RMSNORM_ERR_SHAPE, "%s would span more than 2^48 bytes", name);
-    if (misaligned(h.ptr, eb))
-        return fail(RMSNORM_ERR_ALIGN, "%s must be aligned to the element size (%d bytes)", name,
-                    static_cast<int>(eb));
-    return RMSNORM_OK;
-}
-
-View heads_view(const rmsnorm_heads_t& h, int64_t batch, int64_t seq, int64_t heads, int64_t D, int64_t eb) {
-    return View(h.ptr, D * eb)
-        .dim(batch, h.batch_stride * eb)
-        .dim(seq, h.token_stride * eb)
-        .dim(heads, h.head_stride * eb);
-}
-
-HeadsP heads_p(const rmsnorm_heads_t& h) { return {h.ptr, h.batch_stride, h.token_stride, h.head_stride}; }
-
 int rope_shapes(const rmsnorm_rope_args_t* a, bool fwd) {
     if (a == nullptr) return fail(RMSNORM_ERR_NULL, "args is NULL");
     if (a->struct_size != static_cast<int32_t>(sizeof(*a)) || a->reserved != 0)
@@ -433,7 +245,56 @@ int rope_shapes(const rmsnorm_rope_args_t* a, bool fwd) {
     return RMSNORM_OK;
 }
 
-void rope_fill(const rmsnorm_rope_args_t* a, RopeP* p) {
+// The axes of a call (NULL: one).
+int rope_axes(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* x) {
+    if (x == nullptr) return RMSNORM_OK;
+    if (x->struct_size != static_cast<int32_t>(sizeof(*x)) || x->reserved != 0)
+        return fail(RMSNORM_ERR_OPTIONS, "axes.struct_size is %d, expected %d (reserved 0)", x->struct_size,
+                    static_cast<int>(sizeof(*x)));
+    if (x->in_turn != 0 && x->in_turn != 1) return fail(RMSNORM_ERR_OPTIONS, "in_turn is 0 or 1");
+    if (x->axes < 1 || x->axes > 4) return fail(RMSNORM_ERR_SHAPE, "axes is in 1..4 (got %d)", x->axes);
+    const int half = a->rotary_dim / 2;
+    int64_t sum = 0;
+    for (int k = 0; k < 4; ++k) {
+        if (x->pairs[k] < 0 || (k >= x->axes && x->pairs[k] != 0))
+            return fail(RMSNORM_ERR_SHAPE, "pairs are >= 0, and 0 past the last axis");
+        if (x->in_turn && k > 0 && x->pairs[k] > 0 &&
+            static_cast<int64_t>(x->axes) * (x->pairs[k] - 1) + k >= half)
+            return fail(RMSNORM_ERR_SHAPE, "axis %d takes %d pairs in turn, more than %d pairs hold", k,
+                        x->pairs[k], half);
+        sum += x->pairs[k];
+    }
+    if (sum != half)
+        return fail(RMSNORM_ERR_SHAPE, "the axes take %lld pairs of %d", static_cast<long long>(sum), half);
+    if (a->positions == nullptr && a->batch > 0 && a->seq > 0)
+        return fail(RMSNORM_ERR_NULL, "positions is NULL (needed with axes)");
+    if (x->axis_stride < 0 || (x->axes > 1 && x->axis_stride > kSpanLimit / 8 / (x->axes - 1)))
+        return fail(RMSNORM_ERR_SHAPE, "axis_stride is negative or too large");
+    return RMSNORM_OK;
+}
+
+View positions_view(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* x) {
+    View v(a->positions, a->seq * 8);
+    v.dim(a->batch, a->positions_stride * 8);
+    return x ? v.dim(x->axes, x->axis_stride * 8) : v;
+}
+
+void rope_fill(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* x, RopeP* p) {
+    p->axes = 1;
+    p->in_turn = 0;
+    p->axis_stride = 0;
+    p->cut[0] = p->cut[1] = p->cut[2] = a->rotary_dim / 2;
+    if (x != nullptr) {
+        p->axes = x->axes;
+        p->in_turn = x->in_turn;
+        p->axis_stride = x->axis_stride;
+        int at = 0;
+        for (int k = 0; k < 3; ++k) {
+            at += x->pairs[k];
+            // past the last axis no pair begins one
+            p->cut[k] = x->in_turn ? x->pairs[k + 1] : k + 1 < x->axes ? at : a->rotary_dim / 2;
+        }
+    }
     p->positions = a->positions;
     p->positions_stride = a->positions_stride;
     p->steps = a->steps;
@@ -457,9 +318,12 @@ void rope_fill(const rmsnorm_rope_args_t* a, RopeP* p) {
 
 }  // namespace
 
-extern "C" int rmsnorm_rope_fwd(const rmsnorm_rope_args_t* a, const rmsnorm_options_t* opts, void* stream) {
+namespace {
+
+int rope_forward(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* x, const rmsnorm_options_t* opts,
+                 void* stream) {
     int rc = rope_shapes(a, true);
-    if (rc != RMSNORM_OK) return rc;
+    if (rc != RMSNORM_OK || (rc = rope_axes(a, x)) != RMSNORM_OK) return rc;
     OpCfg c;
     rc = read_op_options(opts, &c);
     if (rc != RMSNORM_OK) return rc;
@@ -479,19 +343,31 @@ extern "C" int rmsnorm_rope_fwd(const rmsnorm_rope_args_t* a, const rmsnorm_opti
                           {View(a->w_k ? a->rstd_k : nullptr, T * Hk * 4), "rstd_k", 0}};
     const Named ins[] = {{qv, "q", 1}, {kv, "k", 2},
                          {View(a->w_q, D * eb), "w_q", 0}, {View(a->w_k, D * eb), "w_k", 0},
-                         {View(a->positions, S * 8).dim(B, a->positions_stride * 8), "positions", 0},
+                         {positions_view(a, x), "positions", 0},
                          {View(a->steps, a->rotary_dim / 2 * 8), "steps", 0}};
     rc = check_overlaps(outs, 4, ins, 6);
     if (rc != RMSNORM_OK) return rc;
     rc = finish_cfg(&c, stream);
     if (rc != RMSNORM_OK) return rc;
     RopeP p;
-    rope_fill(a, &p);
+    rope_fill(a, x, &p);
     p.seg[0].in = heads_p(a->q);
     p.seg[0].out = heads_p(a->out_q);
     p.seg[1].in = heads_p(a->k);
     p.seg[1].out = heads_p(a->out_k);
     return launched([&] { return rope_fwd_run(p, c); });
+}
+
+}  // namespace
+
+extern "C" int rmsnorm_rope_fwd(const rmsnorm_rope_args_t* a, const rmsnorm_options_t* opts, void* stream) {
+    return rope_forward(a, nullptr, opts, stream);
+}
+
+extern "C" int rmsnorm_rope_axes_fwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* axes,
+                                     const rmsnorm_options_t* opts, void* stream) {
+    if (axes == nullptr) return fail(RMSNORM_ERR_NULL, "axes is NULL");
+    return rope_forward(a, axes, opts, stream);
 }
 
 extern "C" int rmsnorm_rope_bwd_workspace_size(int32_t head_dim, int64_t* bytes) {
@@ -505,11 +381,12 @@ extern "C" int rmsnorm_rope_bwd_workspace_size(int32_t head_dim, int64_t* bytes)
     return RMSNORM_OK;
 }
 
-extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope_grads_t* g,
-                                void* workspace, int64_t workspace_bytes,
-                                const rmsnorm_options_t* opts, void* stream) {
+namespace {
+
+int rope_backward(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* x, const rmsnorm_rope_grads_t* g,
+                  void* workspace, int64_t workspace_bytes, const rmsnorm_options_t* opts, void* stream) {
     int rc = rope_shapes(a, false);
-    if (rc != RMSNORM_OK) return rc;
+    if (rc != RMSNORM_OK || (rc = rope_axes(a, x)) != RMSNORM_OK) return rc;
     if (g == nullptr) return fail(RMSNORM_ERR_NULL, "grads is NULL");
     if (g->struct_size != static_cast<int32_t>(sizeof(*g)) || g->reserved != 0)
         return fail(RMSNORM_ERR_OPTIONS, "grads.struct_size is %d, expected %d (reserved 0)",
@@ -551,7 +428,7 @@ extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope
                          {View(a->w_q, D * eb), "w_q", 0}, {View(a->w_k, D * eb), "w_k", 0},
                          {View(a->w_q ? a->rstd_q : nullptr, T * Hq * 4), "rstd_q", 0},
                          {View(a->w_k ? a->rstd_k : nullptr, T * Hk * 4), "rstd_k", 0},
-                         {View(a->positions, S * 8).dim(B, a->positions_stride * 8), "positions", 0},
+                         {positions_view(a, x), "positions", 0},
                          {View(a->steps, a->rotary_dim / 2 * 8), "steps", 0}};
     rc = check_overlaps(outs, 4, ins, 10);
     if (rc != RMSNORM_OK) return rc;
@@ -569,7 +446,7 @@ extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope
             if (meet(ws, i.v)) return fail(RMSNORM_ERR_OVERLAP, "the workspace overlaps %s", i.name);
     }
     RopeP p;
-    rope_fill(a, &p);
+    rope_fill(a, x, &p);
     p.ws = static_cast<float*>(workspace);
     p.seg[0].in = heads_p(g->dout_q);
     p.seg[0].out = heads_p(g->dq);
@@ -580,6 +457,21 @@ extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope
     p.seg[1].x = heads_p(a->k);
     p.seg[1].dw = g->dw_k;
     return launched([&] { return rope_bwd_run(p, c); });
+}
+
+}  // namespace
+
+extern "C" int rmsnorm_rope_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope_grads_t* g,
+                                void* workspace, int64_t workspace_bytes,
+                                const rmsnorm_options_t* opts, void* stream) {
+    return rope_backward(a, nullptr, g, workspace, workspace_bytes, opts, stream);
+}
+
+extern "C" int rmsnorm_rope_axes_bwd(const rmsnorm_rope_args_t* a, const rmsnorm_rope_axes_t* axes,
+                                     const rmsnorm_rope_grads_t* g, void* workspace, int64_t workspace_bytes,
+                                     const rmsnorm_options_t* opts, void* stream) {
+    if (axes == nullptr) return fail(RMSNORM_ERR_NULL, "axes is NULL");
+    return rope_backward(a, axes, g, workspace, workspace_bytes, opts, stream);
 }
 
 extern "C" int rmsnorm_rope_steps(int32_t rotary_dim, double base, const rmsnorm_rope_scaling_t* sc,
@@ -653,46 +545,6 @@ extern "C" int rmsnorm_rope_steps(int32_t rotary_dim, double base, const rmsnorm
 // ---- cache --------------------------------------------------------------------
 
 namespace {
-
-int cache_shapes(const rmsnorm_cache_t* c, int dtype, CacheP* p) {
-    if (c == nullptr) return fail(RMSNORM_ERR_NULL, "cache is NULL");
-    if (c->struct_size != static_cast<int32_t>(sizeof(*c)))
-        return fail(RMSNORM_ERR_OPTIONS, "cache.struct_size is %d, expected %d", c->struct_size,
-                    static_cast<int>(sizeof(*c)));
-    if (c->format != RMSNORM_CACHE_E4M3 && c->format != RMSNORM_CACHE_E2M1)
-        return fail(RMSNORM_ERR_DTYPE, "format %d is not a rmsnorm_cache_format_t", c->format);
-    if (!dtype_ok(dtype)) return fail(RMSNORM_ERR_DTYPE, "dtype %d is not a rmsnorm_dtype_t", dtype);
-    if (c->pages < 1 || c->page_size < 1 || c->heads < 1 || c->heads > (1 << 20) || c->head_dim < 1 ||
-        c->head_dim > 65536 || (c->heads_first != 0 && c->heads_first != 1))
-        return fail(RMSNORM_ERR_SHAPE, "the cache needs pages, page_size and heads >= 1, head_dim in "
-                    "1..65536 and heads_first 0 or 1");
-    *p = CacheP{};
-    p->format = c->format;
-    p->page_size = c->page_size;
-    p->heads = c->heads;
-    p->D = c->head_dim;
-    p->code_bytes = c->format == RMSNORM_CACHE_E4M3 ? c->head_dim : (c->head_dim + 1) / 2;
-    p->groups = (c->head_dim + 31) / 32;
-    p->heads_first = c->heads_first;
-    p->dtype = dtype;
-    const int64_t per_page = static_cast<int64_t>(c->heads) * p->code_bytes;
-    if (c->pages > kSpanLimit / c->page_size / per_page)
-        return fail(RMSNORM_ERR_SHAPE, "the cache would span more than 2^48 bytes");
-    p->slots = c->pages * c->page_size;
-    if (!c->k_codes || !c->k_scales || (c->v_codes != nullptr) != (c->v_scales != nullptr))
-        return fail(RMSNORM_ERR_NULL, "k_codes and k_scales must be given, v_codes and v_scales together");
-    return RMSNORM_OK;
-}
-
-Named cache_array(const rmsnorm_cache_t* c, const CacheP& p, int which) {
-    const int64_t heads = p.slots * p.heads;
-    switch (which) {
-        case 0: return {View(c->k_codes, heads * p.code_bytes), "k_codes", 0};
-        case 1: return {View(c->k_scales, heads * p.groups), "k_scales", 0};
-        case 2: return {View(c->v_codes, heads * p.code_bytes), "v_codes", 0};
-        default: return {View(c->v_scales, heads * p.groups), "v_scales", 0};
-    }
-}
 
 // k and v of a call: tokens of `heads` heads.
 int cache_tensor(const char* name, const rmsnorm_heads_t* h, int64_t T, const CacheP& p, int k, CacheP* out,

@@ -19,7 +19,7 @@
 namespace rmsn {
 namespace {
 
-// cos and sin (times magnitude) of two pairs at a position: the Taylor series of sin and
+// cos and sin (times magnitude) of two pairs at their positions: the Taylor series of sin and
 // cos of y quarter turns, |y| <= 1/2, to y^9 and y^10 (what is left out is below 2^-28),
 // then turned by the quarters. The large term comes last, in one rounding. The same bits
 // for every type and kernel. (The hardware's approximations, whose error does not shrink
@@ -28,8 +28,8 @@ namespace {
 // 83.1 / 84.2, 16384 of 20 heads of 80 with 20 turned 45.4 / 46.3. sincospif of the same
 // rest: 3.05, 58.9, 86.1, 51.2; one angle at a time from a 64-bit conversion: 3.0, 57.9,
 // 84.9, 48.2.)
-__device__ __forceinline__ void turn2(int64_t position, uint64_t step0, uint64_t step1, float magnitude, f2& c,
-                                      f2& s) {
+__device__ __forceinline__ void turn2(int64_t position0, int64_t position1, uint64_t step0, uint64_t step1,
+                                      float magnitude, f2& c, f2& s) {
     constexpr double q = 1.57079632679489661923;  // a quarter turn
     constexpr double q2 = q * q;
     constexpr float s1 = static_cast<float>(q), s1_rest = static_cast<float>(q - s1);
@@ -43,7 +43,7 @@ __device__ __forceinline__ void turn2(int64_t position, uint64_t step0, uint64_t
     float hi[2], lo[2];   // what is left, in quarter turns times 2^32 and 2^64
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const uint64_t phase = static_cast<uint64_t>(position) * (k == 0 ? step0 : step1);
+        const uint64_t phase = static_cast<uint64_t>(k == 0 ? position0 : position1) * (k == 0 ? step0 : step1);
         const uint64_t near = phase + (uint64_t(1) << 29);  // so that lo is signed
         quarter[k] = static_cast<uint32_t>(near >> 32) + 0x20000000u;
         hi[k] = static_cast<float>(static_cast<int32_t>(near >> 30));
@@ -71,12 +71,25 @@ __device__ __forceinline__ void turn2(int64_t position, uint64_t step0, uint64_t
 
 __device__ __forceinline__ float2 turn(int64_t position, uint64_t step, float magnitude) {
     f2 c, s;
-    turn2(position, step, step, magnitude, c, s);
+    turn2(position, position, step, step, magnitude, c, s);
     return make_float2(f2_get(c).x, f2_get(s).x);
 }
 
 __device__ __forceinline__ int64_t position_of(const RopeP& p, int64_t b, int64_t s) {
     return p.positions ? p.positions[b * p.positions_stride + s] : s;
+}
+
+// Several axes: the axis of pair j, whose position turns it. Pairs take the axes by
+// sections (from `cut` to `cut`), or in turn: j % axes while that axis has pairs left,
+// the first axis otherwise. Computed, so that no map can hold an axis that is not there.
+__device__ __forceinline__ int axis_of(const RopeP& p, int j) {
+    if (!p.in_turn) return (j >= p.cut[0]) + (j >= p.cut[1]) + (j >= p.cut[2]);
+    const int i = j / p.axes, a = j - i * p.axes;
+    return a != 0 && i < p.cut[a - 1] ? a : 0;
+}
+__device__ __forceinline__ int64_t position_of(const RopeP& p, int64_t b, int64_t s, int j) {
+    if (p.axes <= 1) return position_of(p, b, s);
+    return __ldg(p.positions + axis_of(p, j) * p.axis_stride + b * p.positions_stride + s);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -160,13 +173,21 @@ struct Lane {
         return LAYOUT == kHalves ? l * E + n : n < N / 2 ? va * (N / 2) + n : vb * (N / 2) + n - N / 2;
     }
     // kExchange: the sines come with the sign that the other value of the pair takes.
-    template <int SIGN>
-    __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t position) {
+    // With several axes a pair's position comes from its axis: a lane's loads are a few
+    // neighbouring ones per unit, from L1.
+    template <int SIGN, bool AXES>
+    __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t b, int64_t s) {
+        angles<SIGN, AXES>(p, g, b, s, AXES ? 0 : position_of(p, b, s));
+    }
+    template <int SIGN, bool AXES>
+    __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t bi, int64_t si,
+                                           int64_t position) {
         if (LAYOUT == kHalves ? l >= g.pairs : va * E >= p.R) return;
         const int half = p.R / 2;
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
             uint64_t step[2];  // 0: an angle that is not used
+            int64_t at[2];
             uint32_t flip[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -174,9 +195,10 @@ struct Lane {
                 const bool second = LAYOUT == kExchange && j >= half;
                 if (second) j -= half;
                 step[k] = LAYOUT == kHalves || j < half ? __ldg(p.steps + j) : 0;
+                at[k] = AXES ? position_of(p, bi, si, j < half ? j : 0) : position;
                 flip[k] = LAYOUT == kExchange && second == (SIGN < 0) ? 0x80000000u : 0u;
             }
-            turn2(position, step[0], step[1], p.magnitude, c[n / 2], s[n / 2]);
+            turn2(at[0], at[1], step[0], step[1], p.magnitude, c[n / 2], s[n / 2]);
             if (LAYOUT == kExchange) {
                 const float2 v = f2_get(s[n / 2]);
                 s[n / 2] = f2_make(__uint_as_float(__float_as_uint(v.x) ^ flip[0]),
@@ -290,7 +312,7 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // Forward.
-template <int DT, int LAYOUT, bool NORM>
+template <int DT, int LAYOUT, bool NORM, bool AXES>
 __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const RopeUnits g) {
     using Ln = Lane<DT, LAYOUT>;
     constexpr int H = Ln::H, S = kAhead;
@@ -335,7 +357,7 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
         };
 #pragma unroll
         for (int k = 0; k < S; ++k) fetch();
-        if (u.n) ln.template angles<1>(p, g, position_of(p, u.b, u.s));
+        if (u.n) ln.template angles<1, AXES>(p, g, u.b, u.s);
         for (int h = 0; h < per; ++h) {
             const bool live = h < u.n;
             copies_wait<S - 1>();
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(const RopeP p, const Rope
 // Backward: turned back, then the norm's backward, with the weights' gradients of
 // a lane's columns summed in registers over all the heads it sees, and over the
 // CTA's teams (in order) into one partial row.
-template <int DT, int LAYOUT, bool NORM>
+template <int DT, int LAYOUT, bool NORM, bool AXES>
 __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const RopeUnits g) {
     using Ln = Lane<DT, LAYOUT>;
     constexpr int E = Ln::E, H = Ln::H, NV = NORM ? 4 : 2, S = kAhead;
@@ -424,7 +446,7 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(const RopeP p, const Rope
 #pragma unroll
         for (int k = 0; k < S; ++k) fetch();
         float r_next = norm && u.n > 0 ? __ldg(rstd) : 0.f;
-        if (u.n) ln.template angles<-1>(p, g, position_of(p, u.b, u.s));
+        if (u.n) ln.template angles<-1, AXES>(p, g, u.b, u.s);
         for (int h = 0; h < per; ++h) {
             const bool live = h < u.n;
             const float r = r_next;
@@ -561,10 +583,9 @@ __global__ void __launch_bounds__(256) rope_fwd_generic_kernel(const RopeP p) {
             const float f = load1<DT>(g.in.p, x0 + j);
             return g.w ? f * r * (p.offset + load1<DT>(g.w, j)) : f;
         };
-        const int64_t pos = position_of(p, u.b, u.s);
         __syncwarp();  // every lane's reads for the sum before the first write
         for (int j = lane; j < half; j += 32) {
-            const float2 cs = turn(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn(position_of(p, u.b, u.s, j), p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float xa = x(a), xb = x(b);
             store1<DT>(g.out.p, y0 + a, fmaf(xa, cs.x, -xb * cs.y));
@@ -594,11 +615,10 @@ __global__ void __launch_bounds__(256) rope_bwd_generic_kernel(const RopeP p) {
         const Place u = unit_of(p, i);
         const RopeSeg& g = p.seg[u.seg];
         const int64_t d0 = at(g.in, u), o0 = at(g.out, u), x0 = at(g.x, u);
-        const int64_t pos = position_of(p, u.b, u.s);
         // The gradient of the normed head at pair j (as its two values) and
         // behind rotary_dim.
         auto back = [&](int j) {
-            const float2 cs = turn(pos, p.steps[j], p.magnitude);
+            const float2 cs = turn(position_of(p, u.b, u.s, j), p.steps[j], p.magnitude);
             const int a = p.interleaved ? 2 * j : j, b = p.interleaved ? 2 * j + 1 : j + half;
             const float da = load1<DT>(g.in.p, d0 + a), db = load1<DT>(g.in.p, d0 + b);
             return make_float2(fmaf(da, cs.x, db * cs.y), fmaf(db, cs.x, -da * cs.y));
@@ -774,9 +794,9 @@ RopeUnits units_of(RopeP* p, const OpCfg& c, int threads, int ctas_per_sm) {
     return g;
 }
 
-template <int DT, int LAYOUT, bool NORM>
+template <int DT, int LAYOUT, bool NORM, bool AXES>
 cudaError_t fwd_units(RopeP p, const OpCfg& c) {
-    auto fn = rope_fwd_kernel<DT, LAYOUT, NORM>;
+    auto fn = rope_fwd_kernel<DT, LAYOUT, NORM, AXES>;
     // Heads to exchange, behind them the copies.
     const int at = LAYOUT == kExchange ? 256 * 2 * VecElems<DT>::value * 4 : 0;
     const int smem = at + 2 * kAhead * 4096;
@@ -796,10 +816,10 @@ cudaError_t launch_dw(const RopeP& p, const OpCfg& c, int64_t rows_q, int64_t ro
     return cudaLaunchKernelEx(&cfg.cfg, rope_dw_kernel, p, RopeRows{{rows_q, rows_k}}, paired);
 }
 
-template <int DT, int LAYOUT, bool NORM>
+template <int DT, int LAYOUT, bool NORM, bool AXES>
 cudaError_t bwd_units(RopeP p, const OpCfg& c) {
     constexpr int E = VecElems<DT>::value;
-    auto fn = rope_bwd_kernel<DT, LAYOUT, NORM>;
+    auto fn = rope_bwd_kernel<DT, LAYOUT, NORM, AXES>;
     // Heads to exchange, then the sums over the warps; behind them the copies.
     const int at = LAYOUT == kExchange || NORM ? 256 * 2 * E * 4 : 0;
     const int smem = at + (NORM ? 4 : 2) * kAhead * 4096;
@@ -811,19 +831,25 @@ cudaError_t bwd_units(RopeP p, const OpCfg& c) {
     return e != cudaSuccess || !NORM ? e : launch_dw(p, c, g.ctas[0], g.ctas[1], 0);
 }
 
-template <int DT, int LAYOUT>
+template <int DT, int LAYOUT, bool AXES>
 cudaError_t run_units(const RopeP& p, const OpCfg& c, bool bwd) {
-    if (p.seg[0].w || p.seg[1].w) return bwd ? bwd_units<DT, LAYOUT, true>(p, c) : fwd_units<DT, LAYOUT, true>(p, c);
-    return bwd ? bwd_units<DT, LAYOUT, false>(p, c) : fwd_units<DT, LAYOUT, false>(p, c);
+    if (p.seg[0].w || p.seg[1].w)
+        return bwd ? bwd_units<DT, LAYOUT, true, AXES>(p, c) : fwd_units<DT, LAYOUT, true, AXES>(p, c);
+    return bwd ? bwd_units<DT, LAYOUT, false, AXES>(p, c) : fwd_units<DT, LAYOUT, false, AXES>(p, c);
+}
+
+template <int DT, int LAYOUT>
+cudaError_t run_axes(const RopeP& p, const OpCfg& c, bool bwd) {
+    return p.axes > 1 ? run_units<DT, LAYOUT, true>(p, c, bwd) : run_units<DT, LAYOUT, false>(p, c, bwd);
 }
 
 template <int DT>
 cudaError_t run(const RopeP& p, const OpCfg& c, bool bwd) {
     if (c.variant != RMSNORM_VARIANT_GENERIC && vectors(p, bwd)) {
         switch (layout_of(p)) {
-            case kHalves: return run_units<DT, kHalves>(p, c, bwd);
-            case kInterleaved: return run_units<DT, kInterleaved>(p, c, bwd);
-            default: return run_units<DT, kExchange>(p, c, bwd);
+            case kHalves: return run_axes<DT, kHalves>(p, c, bwd);
+            case kInterleaved: return run_axes<DT, kInterleaved>(p, c, bwd);
+            default: return run_axes<DT, kExchange>(p, c, bwd);
         }
     }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;

@@ -107,6 +107,11 @@ struct RopeP {
     const int64_t* positions;
     int64_t positions_stride;
     const uint64_t* steps;
+    int axes;             // 1, or 2..4: axis a's positions lie at positions + a * axis_stride
+    int in_turn;
+    int cut[3];           // sections: first pair of the axes 1..3 (past them: R / 2);
+                          // in turn: pairs of the axes 1..3
+    int64_t axis_stride;
     int64_t batch, seq;
     int D, R;
     int interleaved;
@@ -148,6 +153,73 @@ struct CacheP {
 cudaError_t cache_write_run(const CacheP& p, const OpCfg& c);
 cudaError_t cache_read_run(const CacheP& p, const OpCfg& c);
 cudaError_t cache_status_read_and_clear(unsigned int* value);
+
+// ---- pages of the cache ---------------------------------------------------------
+
+// What a page of the four arrays (k and v codes, k and v scales; null: not there) is
+// made of: `runs` runs of `page_size` tokens of `token[a]` bytes (one run of all heads, or with
+// heads first a run a head).
+struct PageBytes {
+    uint8_t* p[4];
+    int64_t page[4];   // bytes of a page
+    int64_t token[4];  // bytes of a token in a run
+    int runs;
+    int page_size;
+    bool vectors;      // every page a multiple of 16 bytes at such an address
+};
+
+constexpr int64_t kMaxPages = int64_t(1) << 25;  // that fork and compact take
+
+struct PagesP {
+    PageBytes bytes;
+    int64_t pages, sequences, width;
+    int32_t* refs;
+    int32_t* table;
+    int32_t* lengths;
+    int64_t n;
+    // copy: src, dst; fork: parents, children; free: rows
+    const int32_t* a;
+    const int32_t* b;
+    // compact
+    int32_t* refs_out;
+    int32_t* table_out;
+    int32_t* live;
+    void* ws;
+};
+
+cudaError_t pages_copy_run(const PagesP& p, const OpCfg& c);
+cudaError_t pages_fork_run(const PagesP& p, const OpCfg& c);
+cudaError_t pages_free_run(const PagesP& p, const OpCfg& c);
+cudaError_t pages_compact_run(const PagesP& p, const OpCfg& c);
+cudaError_t pages_status_read_and_clear(unsigned int* value);
+int64_t pages_ws_bytes(int64_t pages, int64_t sequences, int64_t n);
+
+// ---- attention over the cache -----------------------------------------------------
+
+struct AttnP {
+    int format;
+    int64_t slots;
+    int page_size, heads, D, code_bytes, groups, heads_first;
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    HeadsP q, out;
+    int dtype;
+    int heads_q, G;  // query heads, and those of a cache head
+    int causal;
+    int64_t window;
+    int64_t sequences, rows, width;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* cu;  // null: a row a sequence
+    float* lse;
+    float scale;
+    void* ws;
+    unsigned int* status;  // the device's word for pages that are not there
+};
+
+cudaError_t attn_run(const AttnP& p, const OpCfg& c);
+cudaError_t attn_status_read_and_clear(unsigned int* value);
+int64_t attn_ws_bytes(int64_t heads, int64_t G, int64_t D, int64_t sequences, int64_t rows, int sm_count);
 
 // Front end helpers shared with api.cu.
 cudaError_t device_info(DeviceInfo* out);

@@ -1,0 +1,162 @@
+"""Plain 64-bit implementations of the operators that serve from the cache, written from the
+formulas of include/rmsnorm.h, and the error bounds of their tests.
+
+Bounds of attention. With S = scale * max over t of sum |q k| (the magnitude behind a
+score), a score is off by at most about 32 roundings of fp32 sums, 32 * 2^-23 * S < 4e-6 * S; a
+probability by that, the exponential's 2^-22 and its own rounding (half a step of 11 bits,
+2^-12, for 16-bit outputs; of 22, 2^-23, for fp32); sums by TAU, as for the other
+operators. Numerator and denominator both carry the score's error, so an output is
+within (r + 2 * (4e-6 * S + TAU)) * sum p |v| and half a step of its dtype.
+"""
+from __future__ import annotations
+
+import torch
+
+import ops_util as U
+
+
+def tokens_of(cache, which, pages, have):
+    """The first `have` tokens behind a row of page numbers: [have, heads, D] in 64 bits on
+    the CPU, and whether each token's page is there."""
+    codes = getattr(cache, which + "_codes").cpu()
+    scales = getattr(cache, which + "_scales").cpu()
+    if cache.heads_first:
+        codes, scales = codes.transpose(1, 2), scales.transpose(1, 2)
+    t = torch.arange(have)
+    col = t // cache.page_size
+    there = col < len(pages)
+    page = torch.where(there, torch.as_tensor(pages).long()[col.clamp(max=max(0, len(pages) - 1))], -1) \
+        if len(pages) else torch.full_like(t, -1)
+    there = (page >= 0) & (page < cache.pages)
+    page = page.clamp(0, cache.pages - 1)
+    c, s = codes[page, t % cache.page_size], scales[page, t % cache.page_size]
+    code = U.unpack(c, cache.fmt, cache.head_dim).long()
+    v = U.code_values(cache.fmt)[code]
+    e = s.long()
+    p = torch.pow(torch.tensor(2.0, dtype=torch.float64), (e - 127).double())
+    p = torch.where(e == 255, torch.full_like(p, float("nan")), p)
+    return v * p.repeat_interleave(32, -1)[..., :cache.head_dim], there
+
+
+def attention(cache, q, table, lengths, cu, scale, causal, window):
+    """out, lse and the magnitudes (sum p |v|, S) in 64 bits on the CPU."""
+    q = q.double().cpu()
+    rows, H, D = q.shape
+    G = H // cache.heads
+    out, mag = torch.zeros(rows, H, D, dtype=torch.float64), torch.zeros(rows, H, D, dtype=torch.float64)
+    lse = torch.full((rows, H), -float("inf"), dtype=torch.float64)
+    S = torch.zeros(rows, H, dtype=torch.float64)
+    for b, have in enumerate(lengths):
+        n = cu[b + 1] - cu[b]
+        if n == 0 or have <= 0:
+            continue
+        k, there = tokens_of(cache, "k", table[b], have)
+        v, _ = tokens_of(cache, "v", table[b], have)
+        t = torch.arange(have)
+        for i in range(n):
+            pos = have - n + i
+            see = there.clone()
+            if causal:
+                see &= t <= pos
+            if window:
+                see &= t > pos - window
+            if not bool(see.any()):
+                continue
+            for h in range(H):
+                kk, vv, qq = k[see, h // G], v[see, h // G], q[cu[b] + i, h]
+                s = scale * (kk @ qq)
+                lse[cu[b] + i, h] = torch.logsumexp(s, 0)
+                p = torch.exp(s - lse[cu[b] + i, h])
+                out[cu[b] + i, h] = p @ vv
+                mag[cu[b] + i, h] = p @ vv.abs()
+                S[cu[b] + i, h] = (scale * (kk.abs() @ qq.abs())).abs().max()
+    return out, lse, mag, S
+
+
+def check_attention(got, lse, want, dtype, what):
+    out, ref_lse, mag, S = want
+    got = got.double().cpu()
+    assert got.shape == out.shape, what
+    r = 2.0 ** -23 if dtype is torch.float32 else 2.0 ** -12
+    bad = torch.isnan(out)
+    assert torch.equal(torch.isnan(got), bad), (what, "NaN elsewhere", int(torch.isnan(got).sum()), int(bad.sum()))
+    delta = 4e-6 * S + U.TAU
+    bound = (r + 2 * delta)[..., None] * mag + U.half_step(out, dtype)
+    err = torch.where(bad, 0.0, (got - out).abs())
+    ok = bad | (err <= bound)
+    assert bool(ok.all()), (what, float((err / bound).nan_to_num(0).max()), int((~ok).sum()))
+    if lse is not None:
+        got = lse.double().cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref_lse)), (what, "lse NaN")
+        assert torch.equal(got == -float("inf"), ref_lse == -float("inf")), (what, "lse of empty rows")
+        fine = torch.isfinite(ref_lse)
+        err = (got - ref_lse)[fine].abs()
+        assert bool((err <= (delta + 2.0 ** -22 * ref_lse.abs())[fine]).all()), (what, float(err.max()))
+
+
+# ---- pages ------------------------------------------------------------------------
+
+def arrays(cache):
+    return [t.cpu().clone() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)
+            if t is not None]
+
+
+def fork(cache, refs, table, lengths, parents, children):
+    """The state after a fork (lists, in place), the cache's arrays, and whether anything was
+    reported."""
+    page, S, W = cache.page_size, len(table), len(table[0]) if table else 0
+    old, out = arrays(cache), arrays(cache)
+    before = list(lengths)
+    free = [p for p in range(len(refs)) if refs[p] <= 0]
+    named, reported = set(), False
+    rows0 = [list(r) for r in table]
+    for a, c in zip(parents, children):
+        if a < 0 or c < 0:
+            continue
+        if a >= S or c >= S or a == c or before[c] != 0 or c in named or before[a] < 0 or \
+                -(-before[a] // page) > W:
+            reported = True
+            if c < S:
+                named.add(c)
+            continue
+        named.add(c)
+        full, rest = divmod(before[a], page)
+        row = rows0[a][:full]
+        if rest:
+            if not free:
+                reported = True
+                continue
+            new, src = free.pop(0), rows0[a][full]
+            row = row + [new]
+            if not 0 <= src < cache.pages:
+                reported = True
+            else:
+                for o, t in zip(out, old):
+                    if cache.heads_first:
+                        o[new, :, :rest] = t[src, :, :rest]
+                    else:
+                        o[new, :rest] = t[src, :rest]
+        for p in row:
+            if 0 <= p < cache.pages:
+                refs[p] += 1
+            else:
+                reported = True
+        table[c] = row + [-1] * (W - len(row))
+        lengths[c] = before[a]
+    return out, reported
+
+
+def compact(cache, refs, table):
+    """live, refs, table after compaction, the cache's arrays, whether anything was reported."""
+    P = len(refs)
+    live = sum(r > 0 for r in refs)
+    src = [p for p in range(live, P) if refs[p] > 0]
+    dst = [p for p in range(live) if refs[p] <= 0]
+    out, old = arrays(cache), arrays(cache)
+    new, to = list(refs), {}
+    for s, d in zip(src, dst):
+        to[s] = d
+        new[d], new[s] = refs[s], 0
+        for o, t in zip(out, old):
+            o[d] = t[s]
+    return live, new, [[to.get(p, p) for p in r] for r in table], out, any(p >= P for r in table for p in r)
