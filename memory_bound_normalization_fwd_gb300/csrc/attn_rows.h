@@ -1,0 +1,50 @@
+// How a call of attention over the cache is dealt out to the row kernels (attn_rows.cuh), and
+// their launches by format.
+#pragma once
+
+#include "ops.h"
+
+namespace rmsn {
+
+// The rows of a sequence that share a key head (queries times the query heads of a key
+// head) are taken in blocks of 8 * NT, and the tokens in tiles. A slot is a block of a
+// sequence; the CTAs of a head block take equal runs of all slots' tiles.
+struct RowsPlan {
+    int gd;           // groups of a head that the kernel is made for: 2, 3, 4, 6 or 8, at least the cache's
+    int nt;           // 8 * nt rows a block: 1, 2, or 4 up to 4 groups
+    int hb;           // key heads of a CTA
+    int wph;          // warps a key head, which take turns at the tokens of a tile
+    int head_blocks;  // heads / hb
+    int slots;        // at least the slots of the call: rows * G / (8 nt) + sequences
+    int gx;           // CTAs a head block
+    int split;        // 1: equal runs of tiles; 0: whole slots, one after another
+    int narrow;       // codes are copied by 4 bytes (heads that are not whole groups)
+    int vec_scales;   // a head's scale bytes are read at once
+    int vec_q;        // rows of q are read by vectors
+    int ring;         // bytes of a warp's ring (also room for its results)
+    int at_q, at_factors, at_ring, at_plan;  // offsets in shared memory
+    int smem;
+    // the workspace, of parts of slots that were split: two a CTA of a head block
+    int2* entries;    // [slots]: the first and last CTA of a slot
+    float2* ml;       // [2 gx][heads][rows of a block]: maximum, sum
+    float* o;         // [2 gx][heads][rows of a block][gd * 32]
+};
+
+constexpr int kSplitSlots = 2048;  // most slots (and sequences) of a call that is dealt out evenly
+
+// The row kernels by format and type; attn_join puts the parts of split slots together.
+cudaError_t attn_rows_e2m1(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+cudaError_t attn_rows_e2m1_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+cudaError_t attn_rows_e4m3(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+cudaError_t attn_rows_e4m3_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+cudaError_t attn_join(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+
+// Bytes of a token's codes in a warp's ring: an odd number of the units (32 bytes for 8-bit
+// codes, 16 for 4-bit ones) that four lanes read of it, so that eight tokens lie on different banks.
+__host__ __device__ constexpr int rows_pitch(bool e4m3, int groups) {
+    return e4m3 ? (groups | 1) * 32 : (groups | 1) * 16;
+}
+// Floats a token in the factors' table.
+__host__ __device__ constexpr int rows_factors(int groups) { return groups <= 2 ? 2 : groups <= 4 ? 4 : 8; }
+
+}  // namespace rmsn

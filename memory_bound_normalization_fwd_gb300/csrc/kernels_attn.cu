@@ -3,6 +3,7 @@
 #include "rmsnorm.h"
 
 #include "attn_common.cuh"
+#include "attn_rows.h"
 #include "row_ring_host.h"
 
 #include <algorithm>
@@ -132,6 +133,161 @@ cudaError_t run_generic(const AttnP& p, const OpCfg& c) {
     }
 }
 
+// Joins the parts of slots whose tiles more than one CTA took: a CTA a slot and some of its
+// rows of heads; `wpr` warps (8 or 1) a row, which take turns at the parts.
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnP p, const RowsPlan r, int wpr) {
+    __shared__ __align__(16) float part[8][256 + 4];  // rows of whole vectors
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int R = 8 * r.nt, DP = r.gd * 32;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t slot = blockIdx.x;
+    int64_t lo = 0, hi = p.sequences - 1;
+    auto start = [&](int64_t b) { return first_row(p, b) * p.G / R + b; };
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (start(mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t row0 = first_row(p, lo), r0 = (slot - start(lo)) * R;
+    const int64_t all = (first_row(p, lo + 1) - row0) * p.G;
+    if (slot < start(lo) || r0 >= all) return;  // no such slot
+    const int rows = static_cast<int>(all - r0 < R ? all - r0 : R);
+    const int2 e = r.entries[slot];
+    if (e.x == e.y) return;  // one CTA took all of it
+    const int u = static_cast<int>(blockIdx.y) * (8 / wpr) + (wpr == 8 ? 0 : w);
+    if (u >= p.heads * rows) return;
+    const int hk = u / rows, row = u - hk * rows, n = e.y - e.x + 1;
+    auto at = [&](int k) {  // the k-th part
+        const int64_t id = k == 0 ? 2 * e.x + 1 : 2 * (e.x + k);
+        return (id * p.heads + hk) * R + row;
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, r.ml[at(k)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int first = wpr == 8 ? w : 0;
+    for (int k0 = first; k0 < n; k0 += 4 * wpr) {
+        float2 ml[4];
+        float4 v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + i * wpr;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k >= n) continue;
+            const int64_t a = at(k);
+            ml[i] = r.ml[a];
+            if (lane * 4 < DP) v[i][0] = *reinterpret_cast<const float4*>(r.o + a * DP + lane * 4);
+            if (128 + lane * 4 < DP) v[i][1] = *reinterpret_cast<const float4*>(r.o + a * DP + 128 + lane * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = ml[i].x == -INFINITY ? 1.f : exp2f(ml[i].x - M);  // no token: zeros
+            L += f * ml[i].y;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                o[c].x = fmaf(f, v[i][c].x, o[c].x), o[c].y = fmaf(f, v[i][c].y, o[c].y);
+                o[c].z = fmaf(f, v[i][c].z, o[c].z), o[c].w = fmaf(f, v[i][c].w, o[c].w);
+            }
+        }
+    }
+    const int64_t i = (r0 + row) / p.G, out_row = row0 + i;
+    const int qh = hk * p.G + static_cast<int>(r0 + row - i * p.G);
+    auto put = [&](int d, float v) {
+        if (d >= p.D) return;
+        const int64_t j = out_row * p.out.st + qh * p.out.sh + d;
+        if (p.dtype == kBF16) store1<kBF16>(p.out.p, j, v);
+        else if (p.dtype == kFP16) store1<kFP16>(p.out.p, j, v);
+        else store1<kFP32>(p.out.p, j, v);
+    };
+    if (wpr == 8) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) *reinterpret_cast<float4*>(&part[w][c * 128 + lane * 4]) = o[c];
+        if (lane == 0) part[w][256] = L;
+        __syncthreads();
+        L = 0.f;
+        for (int k = 0; k < 8; ++k) L += part[k][256];
+        float v = 0.f;
+        for (int k = 0; k < 8; ++k) v += part[k][threadIdx.x];
+        put(threadIdx.x, L == 0.f ? 0.f : v / L);
+    } else {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float v[4] = {o[c].x, o[c].y, o[c].z, o[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put(c * 128 + lane * 4 + k, L == 0.f ? 0.f : v[k] * inv);
+        }
+    }
+    if (p.lse && lane == 0 && (wpr == 1 || w == 0))
+        p.lse[out_row * p.heads_q + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// How the row kernels take a call; false where they cannot.
+int divisor_up_to(int n, int most) {
+    int d = n < most ? n : most;
+    while (n % d) --d;
+    return d;
+}
+
+int rows_nt(int64_t G, int64_t gd, int64_t sequences, int64_t rows) {
+    // rows of a key head that a sequence has, on average
+    const int64_t n = (rows + sequences - 1) / sequences * G;
+    return n <= 8 ? 1 : n <= 16 || gd > 4 ? 2 : 4;
+}
+
+int rows_gd(int64_t D) {
+    const int64_t g = (D + 31) / 32;
+    return g <= 2 ? 2 : g <= 4 ? static_cast<int>(g) : g <= 6 ? 6 : 8;
+}
+
+int64_t rows_slots(int64_t G, int nt, int64_t sequences, int64_t rows) { return rows * G / (8 * nt) + sequences; }
+
+// At most this many CTAs for all head blocks together where slots are split.
+int64_t rows_ctas(int nt, int gd, int pieces, int sm_count) {
+    return static_cast<int64_t>(sm_count) * (gd * nt <= 4 && pieces == 1 ? 2 : 1);
+}
+
+bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
+    *r = RowsPlan{};
+    if (p.D > 256) return false;
+    const uintptr_t codes = reinterpret_cast<uintptr_t>(p.codes[0]) | reinterpret_cast<uintptr_t>(p.codes[1]);
+    const uintptr_t scales = reinterpret_cast<uintptr_t>(p.scales[0]) | reinterpret_cast<uintptr_t>(p.scales[1]);
+    r->gd = rows_gd(p.D);
+    r->narrow = p.D != r->gd * 32 || codes % 16 != 0;
+    if (r->narrow && (p.code_bytes % 4 != 0 || codes % 4 != 0)) return false;
+    const int pieces = p.dtype == kFP32 ? 2 : 1;
+    r->nt = rows_nt(p.G, r->gd, p.sequences, p.rows);
+    r->vec_scales = p.groups == r->gd && scales % 8 == 0;
+    const int64_t eb = elem_bytes(p.dtype), e = vec_elems(p.dtype);
+    r->vec_q = aligned16(p.q.p) && (p.rows <= 1 || p.q.st % e == 0) && (p.heads_q <= 1 || p.q.sh % e == 0) && eb > 0;
+    // q's operands of a CTA's heads lie in shared memory where registers do not hold them
+    const int q = r->nt == 1 && pieces == 1 ? 0 : pieces * 2 * r->gd * r->nt * 256;
+    const int room = r->gd > 4 ? 32768 : 65536;
+    r->hb = divisor_up_to(p.heads, q ? std::max(1, std::min(8, room / q)) : 8);
+    r->wph = 8 / r->hb;
+    r->head_blocks = p.heads / r->hb;
+    const int64_t slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
+    if (slots >= (int64_t(1) << 30)) return false;
+    r->slots = static_cast<int>(slots);
+    r->split = slots <= kSplitSlots && p.sequences <= kSplitSlots;
+    int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
+    if (c.max_ctas > 0) ctas = std::min<int64_t>(ctas, c.max_ctas);
+    r->gx = static_cast<int>(std::max<int64_t>(1, r->split ? ctas / r->head_blocks
+                                                          : std::min<int64_t>(slots, (1 << 24) / r->head_blocks)));
+    if (r->split) {
+        const int64_t rows = 2LL * r->gx * p.heads * 8 * r->nt;
+        unsigned char* at = static_cast<unsigned char*>(p.ws);
+        r->o = reinterpret_cast<float*>(at);
+        r->ml = reinterpret_cast<float2*>(at + rows * r->gd * 32 * 4);
+        r->entries = reinterpret_cast<int2*>(at + rows * (r->gd * 32 * 4 + 8));
+    }
+    return true;
+}
+
 // The status word's address on the current device, for kernels of other files.
 cudaError_t status_word(unsigned int** word) {
     constexpr int kDevices = 64;
@@ -150,13 +306,40 @@ cudaError_t status_word(unsigned int** word) {
 
 }  // namespace
 
-int64_t attn_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+cudaError_t attn_join(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
+    // Parts a slot on average; many are joined by eight warps.
+    const int wpr = r.gx / r.slots >= 12 ? 8 : 1;
+    Launch l;
+    l.grid = r.slots;
+    l.threads = 256;
+    LaunchCfg cfg(l, c.stream, c.pdl);
+    cfg.cfg.gridDim.y = static_cast<unsigned>((static_cast<int64_t>(p.heads) * 8 * r.nt * wpr + 7) / 8);
+    return cudaLaunchKernelEx(&cfg.cfg, attn_join_kernel, p, r, wpr);
+}
+
+// For any type, format and alignment of such a call.
+int64_t attn_ws_bytes(int64_t heads, int64_t G, int64_t D, int64_t sequences, int64_t rows, int sm_count) {
+    if (D > 256 || sequences == 0 || rows == 0) return 16;
+    const int gd = rows_gd(D), nt = rows_nt(G, gd, sequences, rows);
+    const int64_t slots = rows_slots(G, nt, sequences, rows);
+    if (slots > kSplitSlots || sequences > kSplitSlots) return 16;
+    // gx * head_blocks CTAs of hb heads: the heads in all CTAs are at most 8 a CTA, or all of them once
+    const int64_t parts = std::max<int64_t>(rows_ctas(nt, gd, 1, sm_count) * std::min<int64_t>(heads, 8), heads);
+    return (2 * parts * 8 * nt * (gd * 32 * 4 + 8) + slots * 8 + 15) / 16 * 16;
+}
 
 cudaError_t attn_run(const AttnP& given, const OpCfg& c) {
     AttnP p = given;
     const cudaError_t e = status_word(&p.status);
     if (e != cudaSuccess) return e;
     g_launched.store(true);
+    RowsPlan r;
+    if (c.variant != RMSNORM_VARIANT_GENERIC && rows_plan(p, c, &r)) {
+        const bool e4 = p.format == RMSNORM_CACHE_E4M3, wide = p.dtype == kFP32;
+        const cudaError_t ran = e4 ? (wide ? attn_rows_e4m3_fp32(p, r, c) : attn_rows_e4m3(p, r, c))
+                                   : (wide ? attn_rows_e2m1_fp32(p, r, c) : attn_rows_e2m1(p, r, c));
+        return ran != cudaSuccess || !r.split || r.gx == 1 ? ran : attn_join(p, r, c);
+    }
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     return p.format == RMSNORM_CACHE_E4M3 ? run_generic<RMSNORM_CACHE_E4M3>(p, c)
                                           : run_generic<RMSNORM_CACHE_E2M1>(p, c);

@@ -1,0 +1,12 @@
+// The row kernels of attention over a cache of 4-bit codes, fp32 queries (attn_rows.cuh).
+#include "rmsnorm.h"
+
+#include "attn_rows.cuh"
+
+namespace rmsn {
+
+cudaError_t attn_rows_e2m1_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
+    return pick_groups<RMSNORM_CACHE_E2M1, 2>(p, r, c);
+}
+
+}  // namespace rmsn

@@ -3,10 +3,19 @@ formulas of include/rmsnorm.h, and the error bounds of their tests.
 
 Bounds of attention. With S = scale * max over t of sum |q k| (the magnitude behind a
 score), a score is off by at most about 32 roundings of fp32 sums, 32 * 2^-23 * S < 4e-6 * S; a
-probability by that, the exponential's 2^-22 and its own rounding (half a step of 11 bits,
-2^-12, for 16-bit outputs; of 22, 2^-23, for fp32); sums by TAU, as for the other
+probability by that, the exponential's 2^-22 and its own rounding: half a step of fp16, which is
+finfo.eps / 2 = 2^-11 (a step is 2^-10 in [1, 2)), for 16-bit outputs; for fp32 the rest of that, at most
+2^-11, is rounded to fp16 again, so 2^-11 * 2^-11 = 2^-22. Sums by TAU, as for the other
 operators. Numerator and denominator both carry the score's error, so an output is
 within (r + 2 * (4e-6 * S + TAU)) * sum p |v| and half a step of its dtype.
+
+Floor. A probability goes into the product in fp16 as p * 2^(b - B + 8), b the scale byte of
+the token's group and B the group's largest so far; below 2^-14 its rounding is no
+longer relative but half of fp16's smallest value, 2^-25. In v's units that is 2^-25 *
+2^(B - 127 - 8) * |code| for a token, and the sum of p, which divides it, is at least 1 (the
+maximum's own p). B is at most the largest byte of the sequence's tokens, so an output may be off by
+2^-33 * 2^(largest byte - 127) * sum |code| over the tokens seen. It shows where the tokens of
+large p have the code 0: (p 2^-23 beside a token of p 1 and code 0 keeps 10 bits).
 """
 from __future__ import annotations
 
@@ -38,20 +47,42 @@ def tokens_of(cache, which, pages, have):
     return v * p.repeat_interleave(32, -1)[..., :cache.head_dim], there
 
 
+def codes_of(cache, pages, have):
+    """|code| and scale of v's tokens behind a row of page numbers (NaN as 0), as tokens_of."""
+    fake = B_like(cache)
+    fake.v_scales = torch.full_like(cache.v_scales, 127)
+    code, _ = tokens_of(fake, "v", pages, have)
+    code = code.abs().nan_to_num(0.0)
+    fake.v_codes = torch.full_like(cache.v_codes, 0x22 if cache.fmt == "e2m1" else 0x38)  # every code 1
+    fake.v_scales = torch.where(cache.v_scales == 255, 0, cache.v_scales)
+    scale, _ = tokens_of(fake, "v", pages, have)
+    return code, scale
+
+
+class B_like:
+    """The fields of a cache that tokens_of reads."""
+
+    def __init__(self, cache):
+        self.__dict__.update({n: getattr(cache, n) for n in (
+            "k_codes", "k_scales", "v_codes", "v_scales", "heads_first", "page_size", "pages", "fmt", "head_dim")})
+
+
 def attention(cache, q, table, lengths, cu, scale, causal, window):
-    """out, lse and the magnitudes (sum p |v|, S) in 64 bits on the CPU."""
+    """out, lse, the magnitudes (sum p |v|, S) and the floor in 64 bits on the CPU."""
     q = q.double().cpu()
     rows, H, D = q.shape
     G = H // cache.heads
     out, mag = torch.zeros(rows, H, D, dtype=torch.float64), torch.zeros(rows, H, D, dtype=torch.float64)
     lse = torch.full((rows, H), -float("inf"), dtype=torch.float64)
-    S = torch.zeros(rows, H, dtype=torch.float64)
+    S, floor = torch.zeros(rows, H, dtype=torch.float64), torch.zeros(rows, H, D, dtype=torch.float64)
     for b, have in enumerate(lengths):
         n = cu[b + 1] - cu[b]
         if n == 0 or have <= 0:
             continue
         k, there = tokens_of(cache, "k", table[b], have)
         v, _ = tokens_of(cache, "v", table[b], have)
+        code, scale_v = codes_of(cache, table[b], have)
+        largest = (scale_v * there[:, None, None]).amax(0)
         t = torch.arange(have)
         for i in range(n):
             pos = have - n + i
@@ -69,19 +100,20 @@ def attention(cache, q, table, lengths, cu, scale, causal, window):
                 p = torch.exp(s - lse[cu[b] + i, h])
                 out[cu[b] + i, h] = p @ vv
                 mag[cu[b] + i, h] = p @ vv.abs()
+                floor[cu[b] + i, h] = 2.0 ** -33 * largest[h // G] * code[see, h // G].sum(0)
                 S[cu[b] + i, h] = (scale * (kk.abs() @ qq.abs())).abs().max()
-    return out, lse, mag, S
+    return out, lse, mag, S, floor
 
 
 def check_attention(got, lse, want, dtype, what):
-    out, ref_lse, mag, S = want
+    out, ref_lse, mag, S, floor = want
     got = got.double().cpu()
     assert got.shape == out.shape, what
-    r = 2.0 ** -23 if dtype is torch.float32 else 2.0 ** -12
+    r = 2.0 ** -22 if dtype is torch.float32 else torch.finfo(torch.float16).eps / 2
     bad = torch.isnan(out)
     assert torch.equal(torch.isnan(got), bad), (what, "NaN elsewhere", int(torch.isnan(got).sum()), int(bad.sum()))
     delta = 4e-6 * S + U.TAU
-    bound = (r + 2 * delta)[..., None] * mag + U.half_step(out, dtype)
+    bound = (r + 2 * delta)[..., None] * mag + U.half_step(out, dtype) + floor
     err = torch.where(bad, 0.0, (got - out).abs())
     ok = bad | (err <= bound)
     assert bool(ok.all()), (what, float((err / bound).nan_to_num(0).max()), int((~ok).sum()))
