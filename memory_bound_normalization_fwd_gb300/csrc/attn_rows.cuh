@@ -16,11 +16,10 @@
 // lane idles for 8 rows. A token's probabilities for the second product come from the first one's
 // sums by an 8x8 transposition in registers.
 // Order of values: the sum over d, the sum over t and the place of d in the result may be permuted
-// at will, as long as both operands agree. A lane takes 8 neighbouring values of K (its k
-// indices 2t, 2t+1, 2t+8, 2t+9 of two instructions) and 4 of V, so that codes are read by words,
-// bytes of two tokens are paired by one permutation for two pairs, and a conversion instruction takes a
-// pair. Row g of the first product is token g ^ (g >> 2 & 1): with that the four tokens of a
-// V read lie on different banks too.
+// at will, as long as both operands agree. So codes come by ldmatrix, which hands a lane the bytes of
+// a token (K) or, transposed, the bytes of two neighbouring tokens at one place (V); the
+// bytes of two tokens are paired by permutations of words, and one conversion instruction
+// makes a pair of fp16 values. Tokens lie an odd number of 16 bytes apart, on different banks.
 //
 // Each warp runs on its own: a ring of two tiles, filled by asynchronous copies of 16 bytes (a token's
 // row of codes at a time), no barrier in the loop; page numbers are looked up two tiles ahead,
@@ -42,15 +41,34 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 __device__ __forceinline__ float2 half2_values(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-__device__ __forceinline__ uint32_t pair_e4m3(uint32_t c) {
-    const __half2 h = static_cast<__half2>(
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3));
-    return *reinterpret_cast<const uint32_t*>(&h);
+// Pairs of fp16 values from the codes of a word, low bytes first.
+__device__ __forceinline__ void pairs_e4m3(uint32_t c, uint32_t& d0, uint32_t& d1) {
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+        : "=r"(d0), "=r"(d1)
+        : "r"(c));
 }
-__device__ __forceinline__ uint32_t pair_e2m1(uint32_t c) {
-    const __half2 h = static_cast<__half2>(
-        __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(c & 0xffu), __NV_E2M1));
-    return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ void pairs_e2m1(uint32_t c, uint32_t& d0, uint32_t& d1, uint32_t& d2, uint32_t& d3) {
+    asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; "
+        "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
+        : "=r"(d0), "=r"(d1), "=r"(d2), "=r"(d3)
+        : "r"(c));
+}
+// 8x8 matrices of 16-bit units; lane l gives row l % 8 of matrix l / 8.
+template <bool TRANS>
+__device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t at) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <bool TRANS>
+__device__ __forceinline__ void load2(uint32_t (&r)[4], uint32_t at) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
 }
 
 // d += a b: a 16x16 (rows lane / 4 and that + 8), b 16x8, fp16 in, fp32 sums.
@@ -59,6 +77,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+// d = a b.
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], const uint2& b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
 }
 // An 8x8 matrix of 16-bit values (row lane / 4, columns 2 (lane % 4) and the next) transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
@@ -80,46 +105,82 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+template <int FP>
+__device__ __forceinline__ void load_factors(float (&f)[FP], const float* from) {
+    if constexpr (FP == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(from);
+        f[0] = v.x, f[1] = v.y;
+    } else {
+#pragma unroll
+        for (int k = 0; k < FP; k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + k);
+            f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+        }
+    }
+}
 // 2^e as fp32, 0 below 2^-126 (e <= 127).
 __device__ __forceinline__ float power(int e) { return __uint_as_float(e < -126 ? 0u : static_cast<uint32_t>(e + 127) << 23); }
 
-// A block of rows of a sequence, and the tiles of tokens that it sees.
+// A block of rows of a sequence, and the tiles of tokens that it sees. (Numbers of rows, tokens
+// and tiles are below 2^31.)
 struct Slot {
-    int64_t b;
-    Sequence s;
-    int64_t r0;        // first row of the block among the sequence's (queries times G)
-    int rows;          // 0: no such slot
-    int64_t low, high; // tokens that any of its rows sees
-    int64_t tile0;     // the first tile
-    int64_t tiles;     // at least one where there are rows
+    int b, row0, n, len;  // the sequence, its first row, its rows and tokens
+    int r0;               // first row of the block among the sequence's (queries times G)
+    int rows;             // 0: no such slot
+    int low, high;        // tokens that any of its rows sees
+    int tile0;            // the first tile
+    int tiles;            // at least one where there are rows
 };
 
-__device__ __forceinline__ int64_t slot_start(const AttnP& p, int64_t b, int R) {
-    return first_row(p, b) * p.G / R + b;
+__device__ __forceinline__ int divide(int a, uint32_t mul, int shift) {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(a)) * mul >> shift);
 }
 
-__device__ __forceinline__ Slot slot_of(const AttnP& p, int64_t slot, int R, int tile) {
-    int64_t lo = 0, hi = p.sequences - 1;
+// First rows and lengths of the sequences: in shared memory where the slots are split.
+struct Sequences {
+    const int* row0;  // null: read from the call's arrays
+    const int* len;
+    __device__ __forceinline__ int row(const AttnP& p, int b) const {
+        return row0 ? row0[b] : static_cast<int>(first_row(p, b));
+    }
+    __device__ __forceinline__ int length(const AttnP& p, int b) const {
+        return row0 ? len[b] : static_cast<int>(sequence(p, b).len);
+    }
+};
+
+// Tokens that query i sees.
+__device__ __forceinline__ void seen32(const AttnP& p, const RowsPlan& r, int n, int len, int i, int& low, int& high) {
+    const int pos = len - n + i;
+    high = p.causal ? max(pos + 1, 0) : len;
+    low = r.window && pos + 1 > r.window ? pos + 1 - r.window : 0;
+}
+
+template <int R>
+__device__ __forceinline__ Slot slot_of(const AttnP& p, const RowsPlan& r, const Sequences& q, int slot) {
+    auto start = [&](int b) { return q.row(p, b) * p.G / R + b; };  // rows * G is below 2^31
+    int lo = 0, hi = static_cast<int>(p.sequences) - 1;
     while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (slot_start(p, mid, R) <= slot) lo = mid;
+        const int mid = (lo + hi + 1) >> 1;
+        if (start(mid) <= slot) lo = mid;
         else hi = mid - 1;
     }
-    Slot r;
-    r.b = lo;
-    r.s = sequence(p, lo);
-    const int64_t start = slot_start(p, lo, R), all = r.s.n * p.G;
-    r.r0 = (slot - start) * R;
-    r.rows = 0;
-    r.low = r.high = r.tile0 = r.tiles = 0;
-    if (slot < start || r.r0 >= all) return r;
-    r.rows = static_cast<int>(all - r.r0 < R ? all - r.r0 : R);
-    r.low = seen(p, r.s, r.r0 / p.G).low;
-    r.high = seen(p, r.s, (r.r0 + r.rows - 1) / p.G).high;
-    if (r.high > r.s.len) r.high = r.s.len;
-    r.tile0 = r.low / tile;
-    r.tiles = r.high > r.low ? (r.high + tile - 1) / tile - r.tile0 : 1;
-    return r;
+    Slot s;
+    s.b = lo;
+    s.row0 = q.row(p, lo);
+    s.n = max(q.row(p, lo + 1) - s.row0, 0);
+    s.len = q.length(p, lo);
+    const int first = s.row0 * p.G / R + lo, all = s.n * p.G;
+    s.r0 = (slot - first) * R;
+    s.rows = s.low = s.high = s.tile0 = s.tiles = 0;
+    if (slot < first || s.r0 >= all) return s;
+    s.rows = min(all - s.r0, R);
+    int unused;
+    seen32(p, r, s.n, s.len, divide(s.r0, r.g_mul, r.g_shift), s.low, unused);
+    seen32(p, r, s.n, s.len, divide(s.r0 + s.rows - 1, r.g_mul, r.g_shift), unused, s.high);
+    s.high = min(s.high, s.len);
+    s.tile0 = s.low >> r.tile_shift;
+    s.tiles = s.high > s.low ? ((s.high - 1) >> r.tile_shift) + 1 - s.tile0 : 1;
+    return s;
 }
 
 // F: format; GD: groups of a head; NT: blocks of 8 NT rows; NP: pieces of q and of the
@@ -165,16 +226,18 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
     constexpr bool E4 = C::E4;
     constexpr int DP = C::DP, RB = C::RB, PITCH = C::PITCH, TM = C::TM, TOK = C::TOK, FP = C::FP, R = C::R, KS = C::KS;
     constexpr float kNegInf = -INFINITY;
+    constexpr uint32_t kNone = 0xffffffffu;  // no token
     extern __shared__ __align__(128) unsigned char sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int head_local = w % r.hb, slice = w / r.hb, threads = blockDim.x;
     const int x = static_cast<int>(blockIdx.x) / r.head_blocks, hblock = static_cast<int>(blockIdx.x) - x * r.head_blocks;
     const int head = hblock * r.hb + head_local;
-    const int tile_tokens = TOK * r.wph;
+    const int tile_tokens = 1 << r.tile_shift;  // TOK * r.wph
     unsigned char* ring = sm + r.at_ring + w * r.ring;
     float* factors = reinterpret_cast<float*>(sm + r.at_factors + w * C::factor_bytes());
     uint2* qs = reinterpret_cast<uint2*>(sm + r.at_q + head_local * C::q_bytes());
-    int64_t* before = reinterpret_cast<int64_t*>(sm + r.at_plan);  // tiles before each slot
+    int* before = reinterpret_cast<int*>(sm + r.at_plan);  // tiles before each slot
+    Sequences seq{nullptr, nullptr};
     if (r.narrow) {  // what lies behind a token's codes stays zero
         for (int i = lane; i < 2 * C::STAGE / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -182,41 +245,50 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
     pdl_launch_dependents();
 
     // Which tiles are this CTA's.
-    int64_t begin = 0, end = 0, share = 1;
-    int64_t slot = x;
+    int begin = 0, end = 0, share = 1, slot = x;
     if (r.split) {
-        __shared__ int64_t warp_tiles[8];
+        __shared__ int warp_tiles[8];
+        int* rows = before + r.slots + 1;
+        int* lens = rows + p.sequences + 1;
+        for (int b = threadIdx.x; b <= p.sequences; b += threads) {
+            rows[b] = static_cast<int>(first_row(p, b));
+            if (b < p.sequences) lens[b] = min(max(__ldg(p.lengths + b), 0), r.most_tokens);
+        }
+        seq = Sequences{rows, lens};
+        __syncthreads();
         const int run = (r.slots + threads - 1) / threads;
-        int64_t own = 0;
-        for (int i = threadIdx.x * run; i < min(r.slots, static_cast<int>(threadIdx.x + 1) * run); ++i) {
-            const int64_t n = slot_of(p, i, R, tile_tokens).tiles;
+        const int run0 = min(static_cast<int>(threadIdx.x) * run, r.slots), run1 = min(run0 + run, r.slots);
+        int own = 0;
+        for (int i = run0; i < run1; ++i) {
+            const int n = slot_of<R>(p, r, seq, i).tiles;
             before[i + 1] = n;
             own += n;
         }
-        int64_t sum = own;
+        int sum = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+            const int o = __shfl_up_sync(0xffffffffu, sum, off);
             if (lane >= off) sum += o;
         }
         if (lane == 31) warp_tiles[w] = sum;
         __syncthreads();
         sum -= own;
-        int64_t total = 0;
+        int total = 0;
         for (int i = 0; i < threads / 32; ++i) {
             if (i < w) sum += warp_tiles[i];
             total += warp_tiles[i];
         }
         if (threadIdx.x == 0) before[0] = 0;
-        for (int i = threadIdx.x * run; i < min(r.slots, static_cast<int>(threadIdx.x + 1) * run); ++i) {
+        for (int i = run0; i < run1; ++i) {
             sum += before[i + 1];
             before[i + 1] = sum;
         }
         __syncthreads();
-        share = (total + r.gx - 1) / r.gx;
-        begin = share * x;
-        end = begin + share < total ? begin + share : total;
-        if (begin >= end) return;
+        share = static_cast<int>((static_cast<uint32_t>(total) + r.gx - 1) / r.gx);
+        const int64_t from = static_cast<int64_t>(share) * x;
+        if (from >= total) return;
+        begin = static_cast<int>(from);
+        end = share < total - begin ? begin + share : total;
         int lo = 0, hi = r.slots - 1;  // the last slot that begins at or before the first tile
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -228,63 +300,126 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
 
     const uint8_t* kcodes = p.codes[0];
     const uint8_t* vcodes = p.codes[1];
-    const int64_t head_off = head * head_step(p);
-    const int gtok = g ^ ((g >> 2) & 1);              // the token of row g of a product
-    const int vt0 = (2 * t4) ^ (t4 >> 1), vt1 = vt0 ^ 1;  // the tokens of its columns 2 t4 and 2 t4 + 1
+    const uint32_t head_off = static_cast<uint32_t>(head * head_step(p));
+    // a lane's row of the matrices that ldmatrix takes from 16 tokens: two of 8 tokens of a 16-byte
+    // piece, two of the next piece
+    const uint32_t mat = (lane & 15) * PITCH + (lane >> 4) * 16;
 
     for (; slot < r.slots; slot += r.split ? 1 : r.gx) {
         if (r.split && before[slot] >= end) break;
-        const Slot sl = slot_of(p, slot, R, tile_tokens);
-        int64_t first = 0, last = sl.tiles;  // tiles of the slot, from its first
-        int64_t slot_begin = 0;
+        const Slot sl = slot_of<R>(p, r, seq, slot);
+        if (sl.rows == 0) continue;
+        int first = 0, last = sl.tiles, slot_begin = 0;
         if (r.split) {
             slot_begin = before[slot];
-            first = begin > slot_begin ? begin - slot_begin : 0;
-            last = before[slot + 1] < end ? sl.tiles : end - slot_begin;
+            first = max(begin - slot_begin, 0);
+            last = min(before[slot + 1], end) - slot_begin;
         }
-        if (sl.rows == 0) continue;
         first += sl.tile0;
         last += sl.tile0;
+        const int32_t* table = p.table + sl.b * p.width;
+
+        // ---- tiles: a token a lane is looked up, copied, and its scale bytes fetched
+        auto lookup = [&](int tile) -> uint32_t {
+            const int t = (tile << r.tile_shift) + slice * TOK + lane;
+            if (tile >= last || lane >= TOK || t < sl.low || t >= sl.high) return kNone;
+            const uint32_t col = divide(t, r.page_mul, r.page_shift), off = t - col * p.page_size;
+            const uint32_t page = static_cast<uint32_t>(__ldg(table + col));
+            if (page >= r.pages) {
+                atomicOr(p.status, 1u);
+                return kNone;
+            }
+            return (p.heads_first ? page * p.heads * p.page_size + off : (page * p.page_size + off) * p.heads) + head_off;
+        };
+        auto copy = [&](int stage, uint32_t at) {
+            const uint32_t to = smem_at(ring + stage * C::STAGE);
+            if (!r.narrow) {
+                constexpr int CH = RB / 16;
+#pragma unroll
+                for (int k = 0; k < TOK * CH / 32; ++k) {
+                    const int i = lane + 32 * k, row = i / CH, c = i - row * CH;
+                    const uint32_t h = __shfl_sync(0xffffffffu, at, row);
+                    const uint64_t off = h == kNone ? 0 : static_cast<uint64_t>(h) * RB + c * 16;
+                    copy_async16(to + row * PITCH + c * 16, kcodes + off, h != kNone);
+                    copy_async16(to + TOK * PITCH + row * PITCH + c * 16, vcodes + off, h != kNone);
+                }
+            } else {
+                const int words = p.code_bytes / 4;
+                for (int row0 = 0; row0 < TOK; row0 += 4) {
+                    const int row = row0 + (lane >> 3);
+                    const uint32_t h = __shfl_sync(0xffffffffu, at, row);
+                    const uint64_t off = h == kNone ? 0 : static_cast<uint64_t>(h) * p.code_bytes;
+                    for (int c = lane & 7; c < words; c += 8) {
+                        copy_async4(to + row * PITCH + c * 4, kcodes + off + c * 4, h != kNone);
+                        copy_async4(to + TOK * PITCH + row * PITCH + c * 4, vcodes + off + c * 4, h != kNone);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // the scale bytes of a token, low byte first
+        auto scales = [&](int which, uint32_t at, uint32_t (&s)[2]) {
+            s[0] = s[1] = 0;
+            if (at == kNone) return;
+            const uint8_t* b = p.scales[which] + static_cast<uint64_t>(at) * p.groups;
+            if (r.vec_scales && GD == 4) {
+                s[0] = __ldg(reinterpret_cast<const uint32_t*>(b));
+            } else if (r.vec_scales && GD == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(b));
+                s[0] = v.x;
+                s[1] = v.y;
+            } else if (r.vec_scales && GD == 2) {
+                s[0] = __ldg(reinterpret_cast<const uint16_t*>(b));
+            } else {
+#pragma unroll
+                for (int k = 0; k < GD; ++k)
+                    if (k < p.groups) s[k >> 2] |= static_cast<uint32_t>(__ldg(b + k)) << (8 * (k & 3));
+            }
+        };
+
+        uint32_t at = lookup(first), at_next = lookup(first + 1);
+        uint32_t sk[2], sv[2];
+        copy(0, at);
+        scales(0, at, sk);
+        scales(1, at, sv);
 
         // ---- q: a row's largest magnitude, its power of two, and its values as fp16 operands
         uint2 qreg[C::QREG ? KS : 1];
         float col_scale[NT][2];
         int lim[NT][2], low[NT][2];  // tokens that a column's row sees, relative to the slot's first tile
-        const int64_t base_token = sl.tile0 * tile_tokens;
+        const int base_token = sl.tile0 << r.tile_shift;
         int min_lim = INT32_MAX, max_low = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int rr = nt * 8 + g;
             const bool live = rr < sl.rows;
-            const int64_t i = live ? (sl.r0 + rr) / p.G : 0;
-            const int64_t row = sl.s.row0 + i;
-            const int qh = head * p.G + (live ? static_cast<int>(sl.r0 + rr - i * p.G) : 0);
-            const int64_t at = row * p.q.st + qh * p.q.sh;
+            const int i = live ? divide(sl.r0 + rr, r.g_mul, r.g_shift) : 0;
+            const int qh = head * p.G + (live ? sl.r0 + rr - i * p.G : 0);
+            const int64_t at = (sl.row0 + i) * p.q.st + qh * p.q.sh;
             float v[GD][8];
             float top = 0.f;
 #pragma unroll
             for (int grp = 0; grp < GD; ++grp) {
-                const int d = grp * 32 + t4 * 8;
-                if (live && r.vec_q && d + 8 <= p.D) {
-                    const unsigned char* src = static_cast<const unsigned char*>(p.q.p) + (at + d) * (NP == 2 ? 4 : 2);
+                // the values of K that the lane gets in two instructions, four each
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + k);
-                        const uint32_t word[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (NP == 2) {
-                                v[grp][(k * 4 + e) & 7] = __uint_as_float(word[e]);
-                            } else {
-                                const float2 f = unpack16(word[e], p.dtype == kBF16);
-                                v[grp][2 * e] = f.x;
-                                v[grp][2 * e + 1] = f.y;
-                            }
+                for (int k = 0; k < 2; ++k) {
+                    const int d = grp * 32 + (E4 ? k * 16 + t4 * 4 : t4 * 8 + k * 4);
+                    float* to = &v[grp][k * 4];
+                    if (live && r.vec_q && d + 4 <= p.D) {
+                        const unsigned char* src = static_cast<const unsigned char*>(p.q.p) + (at + d) * (NP == 2 ? 4 : 2);
+                        if (NP == 2) {
+                            const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+                            to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w;
+                        } else {
+                            const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+                            const float2 a = unpack16(u.x, p.dtype == kBF16), b = unpack16(u.y, p.dtype == kBF16);
+                            to[0] = a.x, to[1] = a.y, to[2] = b.x, to[3] = b.y;
                         }
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[grp][e] = live && d + e < p.D ? load_value<NP>(p.q.p, at + d + e, p.dtype) : 0.f;
+                        for (int e = 0; e < 4; ++e)
+                            to[e] = live && d + e < p.D ? load_value<NP>(p.q.p, at + d + e, p.dtype) : 0.f;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[grp][e]));
@@ -319,10 +454,10 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 lim[nt][e] = INT32_MAX;
                 low[nt][e] = 0;
                 if (cr < sl.rows) {
-                    const Seen see = seen(p, sl.s, (sl.r0 + cr) / p.G);
-                    const int64_t h = (see.high < sl.s.len ? see.high : sl.s.len) - base_token;
-                    lim[nt][e] = static_cast<int>(h < 0 ? 0 : h);
-                    low[nt][e] = static_cast<int>(see.low > base_token ? see.low - base_token : 0);
+                    int from, to;
+                    seen32(p, r, sl.n, sl.len, divide(sl.r0 + cr, r.g_mul, r.g_shift), from, to);
+                    lim[nt][e] = max(min(to, sl.len) - base_token, 0);
+                    low[nt][e] = max(from - base_token, 0);
                     min_lim = min(min_lim, lim[nt][e]);
                     max_low = max(max_low, low[nt][e]);
                 }
@@ -330,7 +465,10 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         }
         min_lim = __reduce_min_sync(0xffffffffu, min_lim);
         max_low = __reduce_max_sync(0xffffffffu, max_low);
-        if (!C::QREG) __syncthreads();
+        if (!C::QREG) {
+            if (r.wph == 1) __syncwarp();
+            else __syncthreads();
+        }
 
         float acc[GD][2][NT][4], m[NT][2], l[NT][2];
         int ref[GD];  // the group's largest scale byte of v so far
@@ -349,85 +487,31 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
 #pragma unroll
             for (int e = 0; e < 2; ++e) m[nt][e] = kNegInf, l[nt][e] = 0.f;
 
-        // ---- tiles: a token a lane is looked up, copied, and its scale bytes fetched
-        auto lookup = [&](int64_t tile) -> int64_t {
-            const int64_t t = tile * tile_tokens + slice * TOK + lane;
-            if (tile >= last || lane >= TOK || t < sl.low || t >= sl.high) return -1;
-            const int64_t at = token_at(p, sl.b, t);
-            if (at < 0) {
-                atomicOr(p.status, 1u);
-                return -1;
-            }
-            return at + head_off;
-        };
-        auto copy = [&](int stage, int64_t at) {
-            const uint32_t to = smem_at(ring + stage * C::STAGE);
-            if (!r.narrow) {
-                constexpr int CH = RB / 16;
-#pragma unroll
-                for (int k = 0; k < TOK * CH / 32; ++k) {
-                    const int i = lane + 32 * k, row = i / CH, c = i - row * CH;
-                    const int64_t h = __shfl_sync(0xffffffffu, at, row);
-                    const int64_t off = (h < 0 ? 0 : h) * RB + c * 16;
-                    copy_async16(to + row * PITCH + c * 16, kcodes + off, h >= 0);
-                    copy_async16(to + TOK * PITCH + row * PITCH + c * 16, vcodes + off, h >= 0);
-                }
-            } else {
-                const int words = p.code_bytes / 4;
-                for (int row0 = 0; row0 < TOK; row0 += 4) {
-                    const int row = row0 + (lane >> 3);
-                    const int64_t h = __shfl_sync(0xffffffffu, at, row);
-                    const int64_t off = (h < 0 ? 0 : h) * p.code_bytes;
-                    for (int c = lane & 7; c < words; c += 8) {
-                        copy_async4(to + row * PITCH + c * 4, kcodes + off + c * 4, h >= 0);
-                        copy_async4(to + TOK * PITCH + row * PITCH + c * 4, vcodes + off + c * 4, h >= 0);
-                    }
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        // the scale bytes of a token, low byte first
-        auto scales = [&](int which, int64_t at, uint32_t (&s)[2]) {
-            s[0] = s[1] = 0;
-            if (at < 0) return;
-            const uint8_t* b = p.scales[which] + at * p.groups;
-            if (r.vec_scales && GD == 4) {
-                s[0] = __ldg(reinterpret_cast<const uint32_t*>(b));
-            } else if (r.vec_scales && GD == 8) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(b));
-                s[0] = v.x;
-                s[1] = v.y;
-            } else if (r.vec_scales && GD == 2) {
-                s[0] = __ldg(reinterpret_cast<const uint16_t*>(b));
-            } else {
-#pragma unroll
-                for (int k = 0; k < GD; ++k)
-                    if (k < p.groups) s[k >> 2] |= static_cast<uint32_t>(__ldg(b + k)) << (8 * (k & 3));
-            }
-        };
-
-        int64_t at = lookup(first), at_next = lookup(first + 1);
-        uint32_t sk[2], sv[2];
-        copy(0, at);
-        scales(0, at, sk);
-        scales(1, at, sv);
         int stage = 0;
-        for (int64_t tile = first; tile < last; ++tile) {
-            const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
+        for (int tile = first; tile < last; ++tile) {
+            const uint32_t there = __ballot_sync(0xffffffffu, at != kNone);
             // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT)
             uint32_t bad = 0;  // groups of this lane's token whose v is not a number
             {
                 float kf[FP], vf[FP];
 #pragma unroll
-                for (int grp = 0; grp < GD; ++grp) {
+                for (int grp = 0; grp < FP; ++grp) {
+                    if (grp >= GD) {
+                        kf[grp] = vf[grp] = 0.f;
+                        continue;
+                    }
                     const uint32_t kb = (sk[grp >> 2] >> (8 * (grp & 3))) & 0xffu;
                     uint32_t vb = (sv[grp >> 2] >> (8 * (grp & 3))) & 0xffu;
-                    if (vb == 255u) {
-                        bad |= 1u << grp;
-                        vb = 0;
+                    // 255: NaN; 0: nothing (below 2^-126)
+                    kf[grp] = __uint_as_float(kb << 23 | ((kb + 1) & 0x100u) << 14);
+                    int most = static_cast<int>(__reduce_max_sync(0xffffffffu, vb));
+                    if (most == 255) {  // not a number: rare
+                        if (vb == 255u) {
+                            bad |= 1u << grp;
+                            vb = 0;
+                        }
+                        most = static_cast<int>(__reduce_max_sync(0xffffffffu, vb));
                     }
-                    kf[grp] = scale_of(kb);
-                    const int most = static_cast<int>(__reduce_max_sync(0xffffffffu, vb));
                     if (most > ref[grp] + 3) {  // the sums move to the new largest scale
                         const float f = power(ref[grp] - most);
                         ref[grp] = most;
@@ -438,10 +522,11 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] *= f;
                     }
-                    vf[grp] = at >= 0 ? power(static_cast<int>(vb) - ref[grp] + C::LIFT) : 0.f;
+                    // 2^(vb - ref + LIFT), 0 where that is below 2^-126; a token that is not
+                    // there has zeros for codes
+                    const int ex = static_cast<int>(vb) - ref[grp] + C::LIFT + 127;
+                    vf[grp] = __uint_as_float(static_cast<uint32_t>(ex > 0 ? ex : 0) << 23);
                 }
-#pragma unroll
-                for (int grp = GD; grp < FP; ++grp) kf[grp] = vf[grp] = 0.f;
                 if (lane < TOK) {
 #pragma unroll
                     for (int k = 0; k < FP; k += 2) {
@@ -461,59 +546,66 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncwarp();  // the tile's codes and factors are there for all lanes
-            const unsigned char* kt = ring + stage * C::STAGE;
-            const unsigned char* vt = kt + TOK * PITCH;
 
             // ---- scores, in powers of two
             float s[TM][NT][4];
+            const uint32_t kt = smem_at(ring + stage * C::STAGE) + mat, vt = kt + TOK * PITCH;
 #pragma unroll
             for (int mt = 0; mt < TM; ++mt) {
+                f2 sum[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-                const unsigned char* row = kt + (mt * 16 + gtok) * PITCH;
-                const float* f0 = factors + (mt * 16 + gtok) * FP;
+                for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0;
+                float fa[FP], fb[FP];
+                load_factors<FP>(fa, factors + (mt * 16 + g) * FP);
+                load_factors<FP>(fb, factors + (mt * 16 + 8 + g) * FP);
+                uint32_t c[4];
 #pragma unroll
                 for (int grp = 0; grp < GD; ++grp) {
                     uint32_t a[2][4];  // two instructions' codes
+                    const uint32_t from = kt + mt * 16 * PITCH + grp * (E4 ? 32 : 16);
                     if (E4) {
-                        const uint2 c0 = *reinterpret_cast<const uint2*>(row + grp * 32 + t4 * 8);
-                        const uint2 c1 = *reinterpret_cast<const uint2*>(row + 8 * PITCH + grp * 32 + t4 * 8);
-                        a[0][0] = pair_e4m3(c0.x), a[0][1] = pair_e4m3(c1.x);
-                        a[0][2] = pair_e4m3(c0.x >> 16), a[0][3] = pair_e4m3(c1.x >> 16);
-                        a[1][0] = pair_e4m3(c0.y), a[1][1] = pair_e4m3(c1.y);
-                        a[1][2] = pair_e4m3(c0.y >> 16), a[1][3] = pair_e4m3(c1.y >> 16);
+                        load4<false>(c, from);
+                        pairs_e4m3(c[0], a[0][0], a[0][2]);
+                        pairs_e4m3(c[1], a[0][1], a[0][3]);
+                        pairs_e4m3(c[2], a[1][0], a[1][2]);
+                        pairs_e4m3(c[3], a[1][1], a[1][3]);
                     } else {
-                        const uint32_t c0 = *reinterpret_cast<const uint32_t*>(row + grp * 16 + t4 * 4);
-                        const uint32_t c1 = *reinterpret_cast<const uint32_t*>(row + 8 * PITCH + grp * 16 + t4 * 4);
-                        a[0][0] = pair_e2m1(c0), a[0][1] = pair_e2m1(c1);
-                        a[0][2] = pair_e2m1(c0 >> 8), a[0][3] = pair_e2m1(c1 >> 8);
-                        a[1][0] = pair_e2m1(c0 >> 16), a[1][1] = pair_e2m1(c1 >> 16);
-                        a[1][2] = pair_e2m1(c0 >> 24), a[1][3] = pair_e2m1(c1 >> 24);
+                        if (grp % 2 == 0 && grp + 1 < GD) load4<false>(c, from);
+                        else if (grp % 2 == 0) load2<false>(c, from);
+                        const int k = grp % 2 * 2;
+                        pairs_e2m1(c[k], a[0][0], a[0][2], a[1][0], a[1][2]);
+                        pairs_e2m1(c[k + 1], a[0][1], a[0][3], a[1][1], a[1][3]);
                     }
-                    const float fa = f0[grp], fb = f0[8 * FP + grp];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        float d[4];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int ks = grp * 2 + k;
-                            mma(d, a[k], C::QREG ? qreg[C::QREG ? ks : 0] : qs[(ks * NT + nt) * 32 + lane]);
+                            const uint2 b = C::QREG ? qreg[C::QREG ? ks : 0] : qs[(ks * NT + nt) * 32 + lane];
+                            if (k == 0) mma_new(d, a[k], b);
+                            else mma(d, a[k], b);
                             if (NP == 2) mma(d, a[k], qs[(KS * NT + ks * NT + nt) * 32 + lane]);
                         }
-                        s[mt][nt][0] = fmaf(d[0], fa, s[mt][nt][0]);
-                        s[mt][nt][1] = fmaf(d[1], fa, s[mt][nt][1]);
-                        s[mt][nt][2] = fmaf(d[2], fb, s[mt][nt][2]);
-                        s[mt][nt][3] = fmaf(d[3], fb, s[mt][nt][3]);
+                        sum[nt][0] = f2_fma(f2_make(d[0], d[1]), f2_dup(fa[grp]), sum[nt][0]);
+                        sum[nt][1] = f2_fma(f2_make(d[2], d[3]), f2_dup(fb[grp]), sum[nt][1]);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float2 v = f2_get(f2_mul(sum[nt][half], f2_make(col_scale[nt][0], col_scale[nt][1])));
+                        s[mt][nt][half * 2] = v.x;
+                        s[mt][nt][half * 2 + 1] = v.y;
                     }
                 }
             }
             // ---- what is seen, and the running maximum
-            const int t0 = static_cast<int>(tile - sl.tile0) * tile_tokens + slice * TOK;
+            const int t0 = ((tile - sl.tile0) << r.tile_shift) + slice * TOK;
             const bool masked = there != (TOK == 32 ? 0xffffffffu : 0xffffu) || t0 + TOK > min_lim || t0 < max_low;
             auto sees = [&](int mt, int half, int nt, int e) {
-                const int tok = mt * 16 + half * 8 + gtok;
+                const int tok = mt * 16 + half * 8 + g;
                 return ((there >> tok) & 1u) && t0 + tok < lim[nt][e] && t0 + tok >= low[nt][e];
             };
             bool grow = false;
@@ -528,7 +620,6 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             float& v = s[mt][nt][half * 2 + e];
-                            v *= col_scale[nt][e];
                             if (masked && !sees(mt, half, nt, e)) v = kNegInf;
                             best = fmaxf(best, v);
                         }
@@ -589,7 +680,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                             for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
                                 for (int half = 0; half < 2; ++half)
-                                    hit |= ((which >> (mt * 16 + half * 8 + gtok)) & 1u) && sees(mt, half, nt, e);
+                                    hit |= ((which >> (mt * 16 + half * 8 + g)) & 1u) && sees(mt, half, nt, e);
                             const uint32_t hits = __ballot_sync(0xffffffffu, hit);
                             if (hits & (0x11111111u << t4)) {
                                 const float nan = __uint_as_float(0x7fc00000u);
@@ -603,51 +694,42 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             // ---- sums of v
 #pragma unroll
             for (int mt = 0; mt < TM; ++mt) {
-                const float* f0 = factors + (TOK + mt * 16 + gtok) * FP;
-                const unsigned char* v0 = vt + (mt * 16 + vt0) * PITCH;
-                const unsigned char* v1 = vt + (mt * 16 + vt1) * PITCH;
+                float fa[FP], fb[FP];
+                load_factors<FP>(fa, factors + (TOK + mt * 16 + g) * FP);
+                load_factors<FP>(fb, factors + (TOK + mt * 16 + 8 + g) * FP);
+                uint32_t c[4];
 #pragma unroll
                 for (int grp = 0; grp < GD; ++grp) {
                     uint32_t a[2][4];
-                    if (E4) {
-                        const int c = grp * 32 + g * 4;
-                        const uint32_t wa = *reinterpret_cast<const uint32_t*>(v0 + c);
-                        const uint32_t wb = *reinterpret_cast<const uint32_t*>(v1 + c);
-                        const uint32_t wc = *reinterpret_cast<const uint32_t*>(v0 + 8 * PITCH + c);
-                        const uint32_t wd = *reinterpret_cast<const uint32_t*>(v1 + 8 * PITCH + c);
-                        const uint32_t p0 = __byte_perm(wa, wb, 0x5140), p1 = __byte_perm(wa, wb, 0x7362);
-                        const uint32_t p2 = __byte_perm(wc, wd, 0x5140), p3 = __byte_perm(wc, wd, 0x7362);
-                        a[0][0] = pair_e4m3(p0), a[0][1] = pair_e4m3(p0 >> 16);
-                        a[0][2] = pair_e4m3(p2), a[0][3] = pair_e4m3(p2 >> 16);
-                        a[1][0] = pair_e4m3(p1), a[1][1] = pair_e4m3(p1 >> 16);
-                        a[1][2] = pair_e4m3(p3), a[1][3] = pair_e4m3(p3 >> 16);
-                    } else {
-                        const int c = grp * 16 + g * 2;
-                        const uint32_t wa = *reinterpret_cast<const uint16_t*>(v0 + c);
-                        const uint32_t wb = *reinterpret_cast<const uint16_t*>(v1 + c);
-                        const uint32_t wc = *reinterpret_cast<const uint16_t*>(v0 + 8 * PITCH + c);
-                        const uint32_t wd = *reinterpret_cast<const uint16_t*>(v1 + 8 * PITCH + c);
-                        const uint32_t y0 = __byte_perm(wa, wc, 0x5410), y1 = __byte_perm(wb, wd, 0x5410);
+                    const uint32_t from = vt + mt * 16 * PITCH + grp * (E4 ? 32 : 16);
+                    if (E4) {  // a word: two values of a token, and of the next
+                        load4<true>(c, from);
+                        pairs_e4m3(__byte_perm(c[0], 0, 0x3120), a[0][0], a[0][1]);
+                        pairs_e4m3(__byte_perm(c[1], 0, 0x3120), a[0][2], a[0][3]);
+                        pairs_e4m3(__byte_perm(c[2], 0, 0x3120), a[1][0], a[1][1]);
+                        pairs_e4m3(__byte_perm(c[3], 0, 0x3120), a[1][2], a[1][3]);
+                    } else {   // a word: four values of a token, and of the next
+                        if (grp % 2 == 0 && grp + 1 < GD) load4<true>(c, from);
+                        else if (grp % 2 == 0) load2<true>(c, from);
+                        const int k = grp % 2 * 2;
+                        const uint32_t y0 = __byte_perm(c[k], c[k + 1], 0x5410), y1 = __byte_perm(c[k], c[k + 1], 0x7632);
                         const uint32_t even = (y0 & 0x0f0f0f0fu) | ((y1 << 4) & 0xf0f0f0f0u);
                         const uint32_t odd = ((y0 >> 4) & 0x0f0f0f0fu) | (y1 & 0xf0f0f0f0u);
-                        a[0][0] = pair_e2m1(even), a[0][1] = pair_e2m1(odd);
-                        a[0][2] = pair_e2m1(even >> 16), a[0][3] = pair_e2m1(odd >> 16);
-                        a[1][0] = pair_e2m1(even >> 8), a[1][1] = pair_e2m1(odd >> 8);
-                        a[1][2] = pair_e2m1(even >> 24), a[1][3] = pair_e2m1(odd >> 24);
+                        pairs_e2m1(even, a[0][0], a[1][0], a[0][2], a[1][2]);
+                        pairs_e2m1(odd, a[0][1], a[1][1], a[0][3], a[1][3]);
                     }
-                    const float fa = f0[grp], fb = f0[8 * FP + grp];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float x0 = s[mt][nt][0] * fa, x1 = s[mt][nt][1] * fa;
-                        const float x2 = s[mt][nt][2] * fb, x3 = s[mt][nt][3] * fb;
-                        const uint32_t h0 = half2_bits(x0, x1), h1 = half2_bits(x2, x3);
+                        const float2 x = f2_get(f2_mul(f2_make(s[mt][nt][0], s[mt][nt][1]), f2_dup(fa[grp])));
+                        const float2 y = f2_get(f2_mul(f2_make(s[mt][nt][2], s[mt][nt][3]), f2_dup(fb[grp])));
+                        const uint32_t h0 = half2_bits(x.x, x.y), h1 = half2_bits(y.x, y.y);
                         const uint2 b = make_uint2(transposed(h0), transposed(h1));
                         mma(acc[grp][0][nt], a[0], b);
                         mma(acc[grp][1][nt], a[1], b);
                         if (NP == 2) {
-                            const float2 y0 = half2_values(h0), y1 = half2_values(h1);
-                            const uint2 b2 = make_uint2(transposed(half2_bits(x0 - y0.x, x1 - y0.y)),
-                                                        transposed(half2_bits(x2 - y1.x, x3 - y1.y)));
+                            const float2 hx = half2_values(h0), hy = half2_values(h1);
+                            const uint2 b2 = make_uint2(transposed(half2_bits(x.x - hx.x, x.y - hx.y)),
+                                                        transposed(half2_bits(y.x - hy.x, y.y - hy.y)));
                             mma(acc[grp][0][nt], a[0], b2);
                             mma(acc[grp][1][nt], a[1], b2);
                         }
@@ -655,7 +737,6 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 }
             }
             __syncwarp();  // the stage and the factors are free again
-            if (tile + 1 >= last) at = -1;
             stage ^= 1;
         }
 
@@ -680,22 +761,29 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                     // 2^(ref - 127 - LIFT) in two factors, which stay normal
                     const int ex = ref[grp] < 0 ? 0 : ref[grp] - 127 - C::LIFT;
                     const float f1 = power(ex / 2), f2_ = power(ex - ex / 2);
-                    *reinterpret_cast<float4*>(mine + row * (DP + 4) + grp * 32 + g * 4) =
-                        make_float4(acc[grp][0][nt][e] * f1 * f2_, acc[grp][0][nt][2 + e] * f1 * f2_,
-                                    acc[grp][1][nt][e] * f1 * f2_, acc[grp][1][nt][2 + e] * f1 * f2_);
+                    float* to = mine + row * (DP + 4) + grp * 32;
+                    const float2 lo = make_float2(acc[grp][0][nt][e] * f1 * f2_, acc[grp][0][nt][2 + e] * f1 * f2_);
+                    const float2 hi = make_float2(acc[grp][1][nt][e] * f1 * f2_, acc[grp][1][nt][2 + e] * f1 * f2_);
+                    if (E4) {
+                        *reinterpret_cast<float2*>(to + g * 2) = lo;
+                        *reinterpret_cast<float2*>(to + 16 + g * 2) = hi;
+                    } else {
+                        *reinterpret_cast<float4*>(to + g * 4) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    }
                 }
             }
         }
-        __syncthreads();
+        if (r.wph == 1) __syncwarp();  // a warp has its head to itself
+        else __syncthreads();
         const bool whole = !r.split || (begin <= slot_begin && before[slot + 1] <= end);
         // begun before this CTA: its part 2x; begun here and unfinished: 2x + 1
         const int part = 2 * x + (r.split && begin <= slot_begin ? 1 : 0);
         if (r.split && begin <= slot_begin && hblock == 0 && threadIdx.x == 0)
             r.entries[slot] = make_int2(x, static_cast<int>((before[slot + 1] - 1) / share));
-        for (int u = w; u < r.hb * sl.rows; u += threads / 32) {
-            const int hl = u % r.hb, row = u / r.hb;
-            const float* from = reinterpret_cast<const float*>(sm + r.at_ring + hl * r.ring);
-            const int stride = r.hb * r.ring / 4;  // to the next slice's warp of the head
+        // a head's warps take its rows in turn
+        const float* from = reinterpret_cast<const float*>(sm + r.at_ring + head_local * r.ring);
+        const int stride = r.hb * r.ring / 4;  // to the next warp of the head
+        for (int row = slice; row < sl.rows; row += r.wph) {
             float M = kNegInf, L = 0.f;
             for (int k = 0; k < r.wph; ++k) M = fmaxf(M, from[k * stride + R * (DP + 4) + row]);
             float4 o[DP <= 128 ? 1 : 2];
@@ -715,9 +803,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                     o[c].z = fmaf(wk, v.z, o[c].z), o[c].w = fmaf(wk, v.w, o[c].w);
                 }
             }
-            const int hk = hblock * r.hb + hl;
             if (!whole) {
-                const int64_t at_part = (static_cast<int64_t>(part) * p.heads + hk) * R + row;
+                const int64_t at_part = (static_cast<int64_t>(part) * p.heads + head) * R + row;
                 if (lane == 0) r.ml[at_part] = make_float2(M, L);
 #pragma unroll
                 for (int c = 0; c < (DP <= 128 ? 1 : 2); ++c) {
@@ -726,9 +813,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 }
                 continue;
             }
-            const int64_t i = (sl.r0 + row) / p.G;
-            const int qh = hk * p.G + static_cast<int>(sl.r0 + row - i * p.G);
-            const int64_t out_row = sl.s.row0 + i;
+            const int i = divide(sl.r0 + row, r.g_mul, r.g_shift), qh = head * p.G + sl.r0 + row - i * p.G;
+            const int64_t out_row = sl.row0 + i;
             const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
             for (int c = 0; c < (DP <= 128 ? 1 : 2); ++c) {
@@ -743,7 +829,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             if (p.lse && lane == 0)
                 p.lse[out_row * p.heads_q + qh] = L == 0.f ? kNegInf : (M + log2f(L)) * 0.6931471805599453f;
         }
-        __syncthreads();  // the rings are free again
+        if (r.wph == 1) __syncwarp();
+        else __syncthreads();  // the rings are free again
         if (r.narrow) {   // and what lies behind a token's codes is zero again
             for (int i = lane; i < 2 * C::STAGE / 16; i += 32)
                 reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -762,7 +849,9 @@ cudaError_t launch_rows(const AttnP& p, RowsPlan r, const OpCfg& c) {
     r.at_factors = r.at_q + r.hb * C::q_bytes();
     r.at_ring = r.at_factors + warps * C::factor_bytes();
     r.at_plan = r.at_ring + warps * r.ring;
-    r.smem = r.at_plan + (r.split ? (r.slots + 1) * 8 : 0);
+    r.tile_shift = C::TOK == 32 ? 5 : 4;
+    while ((C::TOK * r.wph) >> (r.tile_shift + 1)) ++r.tile_shift;  // wph is a power of two
+    r.smem = r.at_plan + (r.split ? (r.slots + 1 + 2 * static_cast<int>(p.sequences) + 1) * 4 : 0);
     if (r.smem + 1024 > c.dev.max_smem_optin) return cudaErrorInvalidConfiguration;
     const cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, c.dev.max_smem_optin - 1024);

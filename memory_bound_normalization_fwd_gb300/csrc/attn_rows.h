@@ -18,6 +18,14 @@ struct RowsPlan {
     int slots;        // at least the slots of the call: rows * G / (8 nt) + sequences
     int gx;           // CTAs a head block
     int split;        // 1: equal runs of tiles; 0: whole slots, one after another
+    int tile_shift;   // tokens of a tile, as a power of two
+    int most_tokens;  // that a row of the table has room for (below 2^31)
+    int window;       // 0: none
+    uint32_t g_mul;   // i / G = i * g_mul >> g_shift for i < 2^31
+    int g_shift;
+    uint32_t pages;
+    uint32_t page_mul;  // t / page_size = t * page_mul >> page_shift for t < 2^31
+    int page_shift;
     int narrow;       // codes are copied by 4 bytes (heads that are not whole groups)
     int vec_scales;   // a head's scale bytes are read at once
     int vec_q;        // rows of q are read by vectors
@@ -30,7 +38,7 @@ struct RowsPlan {
     float* o;         // [2 gx][heads][rows of a block][gd * 32]
 };
 
-constexpr int kSplitSlots = 2048;  // most slots (and sequences) of a call that is dealt out evenly
+constexpr int kSplitSlots = 1024;  // most slots (and sequences) of a call that is dealt out evenly
 
 // The row kernels by format and type; attn_join puts the parts of split slots together.
 cudaError_t attn_rows_e2m1(const AttnP& p, const RowsPlan& r, const OpCfg& c);
@@ -39,10 +47,10 @@ cudaError_t attn_rows_e4m3(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 cudaError_t attn_rows_e4m3_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 cudaError_t attn_join(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 
-// Bytes of a token's codes in a warp's ring: an odd number of the units (32 bytes for 8-bit
-// codes, 16 for 4-bit ones) that four lanes read of it, so that eight tokens lie on different banks.
+// Bytes of a token's codes in a warp's ring: an odd number of 16 bytes, so that eight tokens'
+// pieces of 16 bytes lie on different banks.
 __host__ __device__ constexpr int rows_pitch(bool e4m3, int groups) {
-    return e4m3 ? (groups | 1) * 32 : (groups | 1) * 16;
+    return ((e4m3 ? 2 * groups : groups) | 1) * 16;
 }
 // Floats a token in the factors' table.
 __host__ __device__ constexpr int rows_factors(int groups) { return groups <= 2 ? 2 : groups <= 4 ? 4 : 8; }

@@ -251,9 +251,23 @@ int64_t rows_ctas(int nt, int gd, int pieces, int sm_count) {
     return static_cast<int64_t>(sm_count) * (gd * nt <= 4 && pieces == 1 ? 2 : 1);
 }
 
+// t / d = t * mul >> shift for 0 <= t < 2^31: with 2^l >= d > 2^(l - 1) and mul = floor(2^(31 + l) / d) + 1,
+// t * mul is above t * 2^(31 + l) / d by at most t < 2^31 <= 2^(31 + l) / d.
+void reciprocal(int64_t d, uint32_t* mul, int* shift) {
+    int l = 0;
+    while ((int64_t(1) << l) < d) ++l;
+    *shift = 31 + l;
+    *mul = static_cast<uint32_t>((uint64_t(1) << *shift) / static_cast<uint64_t>(d) + 1);
+}
+
 bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     *r = RowsPlan{};
-    if (p.D > 256) return false;
+    if (p.D > 256 || p.G > (1 << 20) || p.slots * p.heads >= 0xffffffffLL) return false;  // tokens of heads are counted in 32 bits
+    r->pages = static_cast<uint32_t>(p.slots / p.page_size);
+    reciprocal(p.page_size, &r->page_mul, &r->page_shift);
+    reciprocal(p.G, &r->g_mul, &r->g_shift);
+    r->most_tokens = static_cast<int>(std::min<int64_t>(p.width * p.page_size, INT32_MAX - 4096));
+    r->window = static_cast<int>(std::min<int64_t>(p.window, INT32_MAX));
     const uintptr_t codes = reinterpret_cast<uintptr_t>(p.codes[0]) | reinterpret_cast<uintptr_t>(p.codes[1]);
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.scales[0]) | reinterpret_cast<uintptr_t>(p.scales[1]);
     r->gd = rows_gd(p.D);
@@ -271,9 +285,11 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     r->wph = 8 / r->hb;
     r->head_blocks = p.heads / r->hb;
     const int64_t slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
-    if (slots >= (int64_t(1) << 30)) return false;
+    if (p.rows * p.G >= (int64_t(1) << 30) || p.sequences >= (int64_t(1) << 30)) return false;  // counted in 32 bits
     r->slots = static_cast<int>(slots);
-    r->split = slots <= kSplitSlots && p.sequences <= kSplitSlots;
+    // (the sum of all slots' tiles, of 16 tokens at least, is counted in 32 bits too)
+    r->split = slots <= kSplitSlots && p.sequences <= kSplitSlots &&
+               slots * (r->most_tokens / 16 + 2) < (int64_t(1) << 31);
     int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
     if (c.max_ctas > 0) ctas = std::min<int64_t>(ctas, c.max_ctas);
     r->gx = static_cast<int>(std::max<int64_t>(1, r->split ? ctas / r->head_blocks
