@@ -53,6 +53,17 @@ __device__ __forceinline__ void pairs_e2m1(uint32_t c, uint32_t& d0, uint32_t& d
         : "=r"(d0), "=r"(d1), "=r"(d2), "=r"(d3)
         : "r"(c));
 }
+// The low four bits of a's bytes, the high four of b's.
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ const uint8_t* plus(const uint8_t* p, uint32_t n, uint32_t times) {
+    uint64_t r;
+    asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(n), "r"(times), "l"(reinterpret_cast<uint64_t>(p)));
+    return reinterpret_cast<const uint8_t*>(r);
+}
 // 8x8 matrices of 16-bit units; lane l gives row l % 8 of matrix l / 8.
 template <bool TRANS>
 __device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t at) {
@@ -227,6 +238,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
     constexpr int DP = C::DP, RB = C::RB, PITCH = C::PITCH, TM = C::TM, TOK = C::TOK, FP = C::FP, R = C::R, KS = C::KS;
     constexpr float kNegInf = -INFINITY;
     constexpr uint32_t kNone = 0xffffffffu;  // no token
+    constexpr uint32_t kAll = TOK == 32 ? 0xffffffffu : 0xffffu;
+    constexpr int W = (GD + 3) / 4;
     extern __shared__ __align__(128) unsigned char sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int head_local = w % r.hb, slice = w / r.hb, threads = blockDim.x;
@@ -286,6 +299,9 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         __syncthreads();
         share = static_cast<int>((static_cast<uint32_t>(total) + r.gx - 1) / r.gx);
         const int64_t from = static_cast<int64_t>(share) * x;
+        if (x == 0 && hblock == 0)  // slots without rows have no parts to join
+            for (int i = run0; i < run1; ++i)
+                if (before[i + 1] == before[i]) r.entries[i] = make_int4(-1, 0, 0, 0);
         if (from >= total) return;
         begin = static_cast<int>(from);
         end = share < total - begin ? begin + share : total;
@@ -320,28 +336,41 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         const int32_t* table = p.table + sl.b * p.width;
 
         // ---- tiles: a token a lane is looked up, copied, and its scale bytes fetched
-        auto lookup = [&](int tile) -> uint32_t {
-            const int t = (tile << r.tile_shift) + slice * TOK + lane;
+        // (in two steps, a tile apart: the page's number is on its way in between)
+        auto token = [&](int tile) { return (tile << r.tile_shift) + slice * TOK + lane; };
+        auto page_of = [&](int tile) -> uint32_t {
+            const int t = token(tile);
             if (tile >= last || lane >= TOK || t < sl.low || t >= sl.high) return kNone;
-            const uint32_t col = divide(t, r.page_mul, r.page_shift), off = t - col * p.page_size;
-            const uint32_t page = static_cast<uint32_t>(__ldg(table + col));
+            return static_cast<uint32_t>(__ldg(table + divide(t, r.page_mul, r.page_shift)));
+        };
+        auto place = [&](int tile, uint32_t page) -> uint32_t {
             if (page >= r.pages) {
-                atomicOr(p.status, 1u);
+                const int t = token(tile);  // a token that is seen, on a page that is not there
+                if (tile < last && lane < TOK && t >= sl.low && t < sl.high) atomicOr(p.status, 1u);
                 return kNone;
             }
+            const uint32_t t = token(tile), off = t - divide(t, r.page_mul, r.page_shift) * p.page_size;
             return (p.heads_first ? page * p.heads * p.page_size + off : (page * p.page_size + off) * p.heads) + head_off;
         };
-        auto copy = [&](int stage, uint32_t at) {
+        auto copy = [&](int stage, uint32_t at, uint32_t there) {
             const uint32_t to = smem_at(ring + stage * C::STAGE);
             if (!r.narrow) {
                 constexpr int CH = RB / 16;
+                const uint32_t own = at == kNone ? 0 : at;  // nothing is read for a token that is not there
 #pragma unroll
                 for (int k = 0; k < TOK * CH / 32; ++k) {
                     const int i = lane + 32 * k, row = i / CH, c = i - row * CH;
-                    const uint32_t h = __shfl_sync(0xffffffffu, at, row);
-                    const uint64_t off = h == kNone ? 0 : static_cast<uint64_t>(h) * RB + c * 16;
-                    copy_async16(to + row * PITCH + c * 16, kcodes + off, h != kNone);
-                    copy_async16(to + TOK * PITCH + row * PITCH + c * 16, vcodes + off, h != kNone);
+                    const uint32_t h = __shfl_sync(0xffffffffu, own, row);
+                    const uint32_t dst = to + row * PITCH + c * 16;
+                    const uint8_t *kfrom = plus(kcodes + c * 16, h, RB), *vfrom = plus(vcodes + c * 16, h, RB);
+                    if (there == kAll) {
+                        copy_async16(dst, kfrom, true);
+                        copy_async16(dst + TOK * PITCH, vfrom, true);
+                    } else {
+                        const bool some = (there >> row) & 1u;
+                        copy_async16(dst, kfrom, some);
+                        copy_async16(dst + TOK * PITCH, vfrom, some);
+                    }
                 }
             } else {
                 const int words = p.code_bytes / 4;
@@ -377,9 +406,12 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             }
         };
 
-        uint32_t at = lookup(first), at_next = lookup(first + 1);
+        const uint32_t page0 = page_of(first);
+        uint32_t page = page_of(first + 1);
+        const uint32_t at = place(first, page0);
+        uint32_t there_next = __ballot_sync(0xffffffffu, at != kNone);
         uint32_t sk[2], sv[2];
-        copy(0, at);
+        copy(0, at, there_next);
         scales(0, at, sk);
         scales(1, at, sv);
 
@@ -470,62 +502,88 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             else __syncthreads();
         }
 
-        float acc[GD][2][NT][4], m[NT][2], l[NT][2];
-        int ref[GD];  // the group's largest scale byte of v so far
+        // base: what scores are taken relative to (0 before a row has seen a token); limit: where
+        // above it a score moves it (2^4; -infinity before)
+        float acc[GD][2][NT][4], base[NT][2], limit[NT][2], l[NT][2];
+        // scale bytes of v, as the factors take them: the largest so far, and the most that it
+        // serves for
+        uint32_t ref[W][2], most[W][2];
 #pragma unroll
-        for (int grp = 0; grp < GD; ++grp) {
-            ref[grp] = -300;
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ref[i][h] = 0, most[i][h] = 0x00030003u;
+#pragma unroll
+        for (int grp = 0; grp < GD; ++grp)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] = 0.f;
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) m[nt][e] = kNegInf, l[nt][e] = 0.f;
+            for (int e = 0; e < 2; ++e) base[nt][e] = l[nt][e] = 0.f, limit[nt][e] = kNegInf;
 
         int stage = 0;
         for (int tile = first; tile < last; ++tile) {
-            const uint32_t there = __ballot_sync(0xffffffffu, at != kNone);
-            // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT)
+            const uint32_t there = there_next;
+            // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT), 0 where that is
+            // below 2^-126. Two groups at a time, in halves of 16 bits.
             uint32_t bad = 0;  // groups of this lane's token whose v is not a number
             {
                 float kf[FP], vf[FP];
+                uint32_t x[W][2], y[W][2];  // bytes 0 and 2, and 1 and 3, of k's and v's scales
+                uint32_t much = 0;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[i][h] = (sk[i] >> (8 * h)) & 0x00ff00ffu;
+                        y[i][h] = (sv[i] >> (8 * h)) & 0x00ff00ffu;
+                        // more than 2^3 above the largest so far, or not a number
+                        much |= __vmaxu2(y[i][h], most[i][h]) ^ most[i][h];
+                        much |= __vmaxu2(x[i][h], 0x00fe00feu) ^ 0x00fe00feu;
+                    }
+                }
+                uint32_t odd = 0;  // groups whose k is not a number
+                if (__any_sync(0xffffffffu, much != 0)) {
+#pragma unroll
+                    for (int grp = 0; grp < GD; ++grp) {
+                        const int i = grp >> 2, h = grp & 1, sh = (grp & 2) * 8;
+                        if (((x[i][h] >> sh) & 0xffffu) == 255u) odd |= 1u << grp;
+                        if (((y[i][h] >> sh) & 0xffffu) == 255u) {
+                            bad |= 1u << grp;
+                            y[i][h] &= ~(0xffffu << sh);
+                        }
+                        const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, (y[i][h] >> sh) & 0xffffu));
+                        const int have = static_cast<int>((ref[i][h] >> sh) & 0xffffu);
+                        if (top > have + 3) {  // the sums move to the new largest scale
+                            const float f = power(have - top);
+                            ref[i][h] += static_cast<uint32_t>(top - have) << sh;
+                            most[i][h] = (most[i][h] & ~(0xffffu << sh)) | static_cast<uint32_t>(min(top + 3, 254)) << sh;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] *= f;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int grp = 0; grp < FP; ++grp) {
-                    if (grp >= GD) {
+                    const int i = grp >> 2, h = grp & 1;
+                    if (i >= W) {
                         kf[grp] = vf[grp] = 0.f;
                         continue;
                     }
-                    const uint32_t kb = (sk[grp >> 2] >> (8 * (grp & 3))) & 0xffu;
-                    uint32_t vb = (sv[grp >> 2] >> (8 * (grp & 3))) & 0xffu;
-                    // 255: NaN; 0: nothing (below 2^-126)
-                    kf[grp] = __uint_as_float(kb << 23 | ((kb + 1) & 0x100u) << 14);
-                    int most = static_cast<int>(__reduce_max_sync(0xffffffffu, vb));
-                    if (most == 255) {  // not a number: rare
-                        if (vb == 255u) {
-                            bad |= 1u << grp;
-                            vb = 0;
-                        }
-                        most = static_cast<int>(__reduce_max_sync(0xffffffffu, vb));
-                    }
-                    if (most > ref[grp] + 3) {  // the sums move to the new largest scale
-                        const float f = power(ref[grp] - most);
-                        ref[grp] = most;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] *= f;
-                    }
-                    // 2^(vb - ref + LIFT), 0 where that is below 2^-126; a token that is not
-                    // there has zeros for codes
-                    const int ex = static_cast<int>(vb) - ref[grp] + C::LIFT + 127;
-                    vf[grp] = __uint_as_float(static_cast<uint32_t>(ex > 0 ? ex : 0) << 23);
+                    // b - ref + LIFT + 127 as an exponent, at least 0 (a bias of 512, which the shift
+                    // to the exponent's place drops, keeps the halves apart)
+                    const uint32_t e = __vmaxu2(y[i][h] + (0x02000200u + 0x00010001u * (C::LIFT + 127) - ref[i][h]), 0x02000200u);
+                    kf[grp] = __uint_as_float(grp & 2 ? (x[i][h] & 0xffff0000u) << 7 : x[i][h] << 23);
+                    vf[grp] = __uint_as_float(grp & 2 ? (e & 0xffff0000u) << 7 : e << 23);
+                    if (odd >> grp & 1u) kf[grp] = __uint_as_float(0x7fc00000u);
                 }
                 if (lane < TOK) {
 #pragma unroll
@@ -536,25 +594,27 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 }
             }
             if (tile + 1 < last) {
-                copy(stage ^ 1, at_next);
-                scales(0, at_next, sk);
-                scales(1, at_next, sv);
-                at = at_next;
-                at_next = lookup(tile + 2);
+                const uint32_t next = place(tile + 1, page);
+                there_next = __ballot_sync(0xffffffffu, next != kNone);
+                copy(stage ^ 1, next, there_next);
+                scales(0, next, sk);
+                scales(1, next, sv);
+                page = page_of(tile + 2);
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncwarp();  // the tile's codes and factors are there for all lanes
 
-            // ---- scores, in powers of two
+            // ---- scores, in powers of two, relative to the rows' bases
             float s[TM][NT][4];
             const uint32_t kt = smem_at(ring + stage * C::STAGE) + mat, vt = kt + TOK * PITCH;
 #pragma unroll
             for (int mt = 0; mt < TM; ++mt) {
-                f2 sum[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
                 float fa[FP], fb[FP];
                 load_factors<FP>(fa, factors + (mt * 16 + g) * FP);
                 load_factors<FP>(fb, factors + (mt * 16 + 8 + g) * FP);
@@ -587,58 +647,61 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                             else mma(d, a[k], b);
                             if (NP == 2) mma(d, a[k], qs[(KS * NT + ks * NT + nt) * 32 + lane]);
                         }
-                        sum[nt][0] = f2_fma(f2_make(d[0], d[1]), f2_dup(fa[grp]), sum[nt][0]);
-                        sum[nt][1] = f2_fma(f2_make(d[2], d[3]), f2_dup(fb[grp]), sum[nt][1]);
+                        // (not in pairs: a factor for two would have to be copied)
+                        s[mt][nt][0] = fmaf(d[0], fa[grp], s[mt][nt][0]);
+                        s[mt][nt][1] = fmaf(d[1], fa[grp], s[mt][nt][1]);
+                        s[mt][nt][2] = fmaf(d[2], fb[grp], s[mt][nt][2]);
+                        s[mt][nt][3] = fmaf(d[3], fb[grp], s[mt][nt][3]);
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const float2 v = f2_get(f2_mul(sum[nt][half], f2_make(col_scale[nt][0], col_scale[nt][1])));
-                        s[mt][nt][half * 2] = v.x;
-                        s[mt][nt][half * 2 + 1] = v.y;
-                    }
+                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(s[mt][nt][e], col_scale[nt][e & 1], -base[nt][e & 1]);
                 }
             }
             // ---- what is seen, and the running maximum
             const int t0 = ((tile - sl.tile0) << r.tile_shift) + slice * TOK;
-            const bool masked = there != (TOK == 32 ? 0xffffffffu : 0xffffu) || t0 + TOK > min_lim || t0 < max_low;
+            const bool masked = there != kAll || t0 + TOK > min_lim || t0 < max_low;
             auto sees = [&](int mt, int half, int nt, int e) {
                 const int tok = mt * 16 + half * 8 + g;
                 return ((there >> tok) & 1u) && t0 + tok < lim[nt][e] && t0 + tok >= low[nt][e];
             };
+            if (masked) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                if (!sees(mt, half, nt, e)) s[mt][nt][half * 2 + e] = kNegInf;
+            }
             bool grow = false;
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float best = kNegInf;
-#pragma unroll
-                    for (int mt = 0; mt < TM; ++mt) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float& v = s[mt][nt][half * 2 + e];
-                            if (masked && !sees(mt, half, nt, e)) v = kNegInf;
-                            best = fmaxf(best, v);
-                        }
-                    }
-                    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 4));
-                    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 8));
-                    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 16));
-                    top[nt][e] = best;
-                    grow |= best > m[nt][e] + 4.f;
+                    top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+                    if (TM == 2) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[TM - 1][nt][e], s[TM - 1][nt][2 + e]));
+                    grow |= top[nt][e] > limit[nt][e];
                 }
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, grow)) {  // the rows' maxima over all lanes, and all sums to them
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float next = fmaxf(m[nt][e], top[nt][e]);
-                        const float f = m[nt][e] == next ? 1.f : exp2_fast(m[nt][e] - next);
-                        m[nt][e] = next;
+                        float up = top[nt][e];
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+                        if (limit[nt][e] == kNegInf ? up == kNegInf : up <= 0.f) continue;  // nothing seen, or no larger
+                        const float f = limit[nt][e] == kNegInf ? 0.f : exp2_fast(-up);
+                        base[nt][e] += up;
+                        limit[nt][e] = 4.f;
                         l[nt][e] *= f;
 #pragma unroll
                         for (int grp = 0; grp < GD; ++grp)
@@ -647,25 +710,26 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                                 acc[grp][k][nt][e] *= f;
                                 acc[grp][k][nt][2 + e] *= f;
                             }
-                    }
-                }
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float at0 = m[nt][e] == kNegInf ? 0.f : m[nt][e];
-#pragma unroll
-                    for (int mt = 0; mt < TM; ++mt) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float& v = s[mt][nt][half * 2 + e];
-                            v = exp2_fast(v - at0);
-                            l[nt][e] += v;
+                        for (int mt = 0; mt < TM; ++mt) {
+                            s[mt][nt][e] -= up;
+                            s[mt][nt][2 + e] -= up;
                         }
                     }
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float& v = s[mt][nt][half * 2 + e];
+                            v = exp2_fast(v);
+                            l[nt][e] += v;
+                        }
             // ---- groups of v that are not numbers reach the rows that see them (rare)
             if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
@@ -713,15 +777,14 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                         else if (grp % 2 == 0) load2<true>(c, from);
                         const int k = grp % 2 * 2;
                         const uint32_t y0 = __byte_perm(c[k], c[k + 1], 0x5410), y1 = __byte_perm(c[k], c[k + 1], 0x7632);
-                        const uint32_t even = (y0 & 0x0f0f0f0fu) | ((y1 << 4) & 0xf0f0f0f0u);
-                        const uint32_t odd = ((y0 >> 4) & 0x0f0f0f0fu) | (y1 & 0xf0f0f0f0u);
+                        const uint32_t even = low_nibbles(y0, y1 << 4), odd = low_nibbles(y0 >> 4, y1);
                         pairs_e2m1(even, a[0][0], a[1][0], a[0][2], a[1][2]);
                         pairs_e2m1(odd, a[0][1], a[1][1], a[0][3], a[1][3]);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float2 x = f2_get(f2_mul(f2_make(s[mt][nt][0], s[mt][nt][1]), f2_dup(fa[grp])));
-                        const float2 y = f2_get(f2_mul(f2_make(s[mt][nt][2], s[mt][nt][3]), f2_dup(fb[grp])));
+                        const float2 x = make_float2(s[mt][nt][0] * fa[grp], s[mt][nt][1] * fa[grp]);
+                        const float2 y = make_float2(s[mt][nt][2] * fb[grp], s[mt][nt][3] * fb[grp]);
                         const uint32_t h0 = half2_bits(x.x, x.y), h1 = half2_bits(y.x, y.y);
                         const uint2 b = make_uint2(transposed(h0), transposed(h1));
                         mma(acc[grp][0][nt], a[0], b);
@@ -753,13 +816,13 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = nt * 8 + 2 * t4 + e;
                 if (g == 0) {
-                    ml[row] = m[nt][e];
+                    ml[row] = limit[nt][e] == kNegInf ? kNegInf : base[nt][e];
                     ml[R + row] = sum;
                 }
 #pragma unroll
                 for (int grp = 0; grp < GD; ++grp) {
                     // 2^(ref - 127 - LIFT) in two factors, which stay normal
-                    const int ex = ref[grp] < 0 ? 0 : ref[grp] - 127 - C::LIFT;
+                    const int ex = static_cast<int>((ref[grp >> 2][grp & 1] >> (grp & 2) * 8) & 0xffffu) - 127 - C::LIFT;
                     const float f1 = power(ex / 2), f2_ = power(ex - ex / 2);
                     float* to = mine + row * (DP + 4) + grp * 32;
                     const float2 lo = make_float2(acc[grp][0][nt][e] * f1 * f2_, acc[grp][0][nt][2 + e] * f1 * f2_);
@@ -779,7 +842,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         // begun before this CTA: its part 2x; begun here and unfinished: 2x + 1
         const int part = 2 * x + (r.split && begin <= slot_begin ? 1 : 0);
         if (r.split && begin <= slot_begin && hblock == 0 && threadIdx.x == 0)
-            r.entries[slot] = make_int2(x, static_cast<int>((before[slot + 1] - 1) / share));
+            r.entries[slot] = make_int4(whole ? -1 : x | (before[slot + 1] - 1) / share << 16, sl.row0, sl.r0, sl.rows);
         // a head's warps take its rows in turn
         const float* from = reinterpret_cast<const float*>(sm + r.at_ring + head_local * r.ring);
         const int stride = r.hb * r.ring / 4;  // to the next warp of the head

@@ -33,7 +33,8 @@ struct RowsPlan {
     int at_q, at_factors, at_ring, at_plan;  // offsets in shared memory
     int smem;
     // the workspace, of parts of slots that were split: two a CTA of a head block
-    int2* entries;    // [slots]: the first and last CTA of a slot
+    int4* entries;    // [slots]: the first CTA and (from bit 16) the last, -1 where one CTA took all of it;
+                      // the sequence's first row, the block's first row and rows
     float2* ml;       // [2 gx][heads][rows of a block]: maximum, sum
     float* o;         // [2 gx][heads][rows of a block][gd * 32]
 };

@@ -133,33 +133,20 @@ cudaError_t run_generic(const AttnP& p, const OpCfg& c) {
     }
 }
 
-// Joins the parts of slots whose tiles more than one CTA took: a CTA a slot and some of its
-// rows of heads; `wpr` warps (8 or 1) a row, which take turns at the parts.
+// Joins the parts of slots whose tiles more than one CTA took: blockIdx.x is the slot; `wpr` warps (8 or 1) a row of a head, which take turns at the parts.
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnP p, const RowsPlan r, int wpr) {
     __shared__ __align__(16) float part[8][256 + 4];  // rows of whole vectors
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int R = 8 * r.nt, DP = r.gd * 32;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t slot = blockIdx.x;
-    int64_t lo = 0, hi = p.sequences - 1;
-    auto start = [&](int64_t b) { return first_row(p, b) * p.G / R + b; };
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (start(mid) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const int64_t row0 = first_row(p, lo), r0 = (slot - start(lo)) * R;
-    const int64_t all = (first_row(p, lo + 1) - row0) * p.G;
-    if (slot < start(lo) || r0 >= all) return;  // no such slot
-    const int rows = static_cast<int>(all - r0 < R ? all - r0 : R);
-    const int2 e = r.entries[slot];
-    if (e.x == e.y) return;  // one CTA took all of it
+    const int4 slot = r.entries[blockIdx.x];
     const int u = static_cast<int>(blockIdx.y) * (8 / wpr) + (wpr == 8 ? 0 : w);
-    if (u >= p.heads * rows) return;
-    const int hk = u / rows, row = u - hk * rows, n = e.y - e.x + 1;
+    const int hk = u / R, row = u - hk * R;  // R is 8, 16 or 32
+    if (slot.x < 0 || row >= slot.w || hk >= p.heads) return;
+    const int x = slot.x & 0xffff, n = (slot.x >> 16) - x + 1;
     auto at = [&](int k) {  // the k-th part
-        const int64_t id = k == 0 ? 2 * e.x + 1 : 2 * (e.x + k);
+        const int64_t id = k == 0 ? 2 * x + 1 : 2 * (x + k);
         return (id * p.heads + hk) * R + row;
     };
     float M = -INFINITY;
@@ -194,8 +181,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnP p, const Row
             }
         }
     }
-    const int64_t i = (r0 + row) / p.G, out_row = row0 + i;
-    const int qh = hk * p.G + static_cast<int>(r0 + row - i * p.G);
+    const int i = (slot.z + row) / p.G, qh = hk * p.G + slot.z + row - i * p.G;
+    const int64_t out_row = slot.y + i;
     auto put = [&](int d, float v) {
         if (d >= p.D) return;
         const int64_t j = out_row * p.out.st + qh * p.out.sh + d;
@@ -292,6 +279,7 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
                slots * (r->most_tokens / 16 + 2) < (int64_t(1) << 31);
     int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
     if (c.max_ctas > 0) ctas = std::min<int64_t>(ctas, c.max_ctas);
+    ctas = std::min<int64_t>(ctas, 32767);  // a slot's first and last CTA share a word
     r->gx = static_cast<int>(std::max<int64_t>(1, r->split ? ctas / r->head_blocks
                                                           : std::min<int64_t>(slots, (1 << 24) / r->head_blocks)));
     if (r->split) {
@@ -299,7 +287,7 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
         unsigned char* at = static_cast<unsigned char*>(p.ws);
         r->o = reinterpret_cast<float*>(at);
         r->ml = reinterpret_cast<float2*>(at + rows * r->gd * 32 * 4);
-        r->entries = reinterpret_cast<int2*>(at + rows * (r->gd * 32 * 4 + 8));
+        r->entries = reinterpret_cast<int4*>(at + rows * (r->gd * 32 * 4 + 8));
     }
     return true;
 }
@@ -341,7 +329,7 @@ int64_t attn_ws_bytes(int64_t heads, int64_t G, int64_t D, int64_t sequences, in
     if (slots > kSplitSlots || sequences > kSplitSlots) return 16;
     // gx * head_blocks CTAs of hb heads: the heads in all CTAs are at most 8 a CTA, or all of them once
     const int64_t parts = std::max<int64_t>(rows_ctas(nt, gd, 1, sm_count) * std::min<int64_t>(heads, 8), heads);
-    return (2 * parts * 8 * nt * (gd * 32 * 4 + 8) + slots * 8 + 15) / 16 * 16;
+    return 2 * parts * 8 * nt * (gd * 32 * 4 + 8) + slots * 16;
 }
 
 cudaError_t attn_run(const AttnP& given, const OpCfg& c) {
