@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "kernels_warp.cu", "kernels_cta.cu", "kernels_tma.cu", "ker
            "kernels_generic.cu", "kernels_bwd.cu", "host_pipeline.cu", "api_ops.cu", "kernels_block.cu",
            "kernels_block_bwd.cu", "kernels_rope.cu", "kernels_cache.cu", "row_ring.cu", "api_serve.cu",
            "kernels_pages.cu", "kernels_attn.cu", "kernels_attn_e2m1.cu", "kernels_attn_e2m1_fp32.cu",
-           "kernels_attn_e4m3.cu", "kernels_attn_e4m3_fp32.cu"]
+           "kernels_attn_e4m3.cu", "kernels_attn_e4m3_fp32.cu", "kernels_attn_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

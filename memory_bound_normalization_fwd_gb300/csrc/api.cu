@@ -542,14 +542,15 @@ extern "C" int rmsnorm_bwd_plan_info(int64_t M, int64_t N, int dtype, const rmsn
 extern "C" int rmsnorm_check_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "synchronize: %s", cudaGetErrorString(e));
-    unsigned int v = 0, vc = 0, vb = 0, vi = 0, vo = 0, vw = 0;
+    unsigned int v = 0, vc = 0, vb = 0, vi = 0, vo = 0, vw = 0, vl = 0;
     e = status_read_and_clear(&v);
     if (e == cudaSuccess) e = cluster_status_read_and_clear(&vc);
     if (e == cudaSuccess) e = bwd_status_read_and_clear(&vb);
     if (e == cudaSuccess) e = block_status_read_and_clear(&vo);
     if (e == cudaSuccess) e = block_bwd_status_read_and_clear(&vw);
+    if (e == cudaSuccess) e = attn_late_read_and_clear(&vl);
     if (e != cudaSuccess) return fail(RMSNORM_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
-    if (v != 0 || vc != 0 || vb != 0 || vo != 0 || vw != 0)
+    if (v != 0 || vc != 0 || vb != 0 || vo != 0 || vw != 0 || vl != 0)
         return fail(RMSNORM_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait");
     // Read behind the waits' words: an index stays for the next check where one is reported.
     unsigned int vp = 0, va = 0;

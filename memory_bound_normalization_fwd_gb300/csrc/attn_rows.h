@@ -47,6 +47,8 @@ cudaError_t attn_rows_e2m1_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& 
 cudaError_t attn_rows_e4m3(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 cudaError_t attn_rows_e4m3_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 cudaError_t attn_join(const AttnP& p, const RowsPlan& r, const OpCfg& c);
+// Prompts, on the tensor cores: 16-bit types, heads of 64, 96 or 128 values, vectors everywhere.
+cudaError_t attn_tiles(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 
 // Bytes of a token's codes in a warp's ring: an odd number of 16 bytes, so that eight tokens'
 // pieces of 16 bytes lie on different banks.

@@ -12,6 +12,7 @@ namespace rmsn {
 
 // Bit 0: a token's page was not there since the last read. One word per device.
 __device__ unsigned int g_attn_status;
+__device__ unsigned int g_attn_late;  // bit 0: a bounded wait ran out
 static std::atomic<bool> g_launched{false};  // a kernel that writes it
 
 namespace {
@@ -292,20 +293,30 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     return true;
 }
 
-// The status word's address on the current device, for kernels of other files.
-cudaError_t status_word(unsigned int** word) {
+// The status words' addresses on the current device, for kernels of other files.
+cudaError_t status_words(AttnP* p) {
     constexpr int kDevices = 64;
-    static std::atomic<unsigned int*> known[kDevices];
+    static std::atomic<unsigned int*> known[kDevices][2];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < kDevices && (*word = known[dev].load()) != nullptr) return cudaSuccess;
-    void* at = nullptr;
-    e = cudaGetSymbolAddress(&at, g_attn_status);
-    if (e != cudaSuccess) return e;
-    *word = static_cast<unsigned int*>(at);
-    if (dev < kDevices) known[dev].store(*word);
+    if (dev < kDevices && (p->status = known[dev][0].load()) && (p->late = known[dev][1].load())) return cudaSuccess;
+    void *status = nullptr, *late = nullptr;
+    if ((e = cudaGetSymbolAddress(&status, g_attn_status)) != cudaSuccess) return e;
+    if ((e = cudaGetSymbolAddress(&late, g_attn_late)) != cudaSuccess) return e;
+    p->status = static_cast<unsigned int*>(status);
+    p->late = static_cast<unsigned int*>(late);
+    if (dev < kDevices) known[dev][0].store(p->status), known[dev][1].store(p->late);
     return cudaSuccess;
+}
+
+// Whether the tensor cores take a call: enough rows of a key head a sequence to fill most of a
+// block of 256, and blocks for half of the SMs (fewer are split over the tokens by the row kernels).
+bool tiles_ok(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
+    if (p.dtype == kFP32 || p.D % 32 != 0 || p.groups < 2 || p.groups > 4 || r.narrow || !r.vec_q) return false;
+    const int64_t n = (p.rows + p.sequences - 1) / p.sequences * p.G;
+    const int64_t blocks = p.rows * p.G / 256 + p.sequences;
+    return n >= 128 && p.rows * p.G / 256 * p.heads >= c.dev.sm_count / 2 && blocks * p.heads < (int64_t(1) << 31);
 }
 
 }  // namespace
@@ -334,11 +345,12 @@ int64_t attn_ws_bytes(int64_t heads, int64_t G, int64_t D, int64_t sequences, in
 
 cudaError_t attn_run(const AttnP& given, const OpCfg& c) {
     AttnP p = given;
-    const cudaError_t e = status_word(&p.status);
+    const cudaError_t e = status_words(&p);
     if (e != cudaSuccess) return e;
     g_launched.store(true);
     RowsPlan r;
     if (c.variant != RMSNORM_VARIANT_GENERIC && rows_plan(p, c, &r)) {
+        if (tiles_ok(p, r, c)) return attn_tiles(p, r, c);
         const bool e4 = p.format == RMSNORM_CACHE_E4M3, wide = p.dtype == kFP32;
         const cudaError_t ran = e4 ? (wide ? attn_rows_e4m3_fp32(p, r, c) : attn_rows_e4m3(p, r, c))
                                    : (wide ? attn_rows_e2m1_fp32(p, r, c) : attn_rows_e2m1(p, r, c));
@@ -347,6 +359,10 @@ cudaError_t attn_run(const AttnP& given, const OpCfg& c) {
     if (c.variant == RMSNORM_VARIANT_CTA) return cudaErrorNotSupported;
     return p.format == RMSNORM_CACHE_E4M3 ? run_generic<RMSNORM_CACHE_E4M3>(p, c)
                                           : run_generic<RMSNORM_CACHE_E2M1>(p, c);
+}
+
+cudaError_t attn_late_read_and_clear(unsigned int* value) {
+    return symbol_read_and_clear(g_attn_late, g_launched, value);
 }
 
 cudaError_t attn_status_read_and_clear(unsigned int* value) {

@@ -1,0 +1,527 @@
+// Attention over the quantised cache for prompts, on the tensor cores (tcgen05): blocks of 256
+// rows of a key head against tiles of 128 tokens.
+//
+// The mathematics. Each tile's codes become fp16 in shared memory, c * 2^(a - A + C): a the scale
+// byte of a token's group, A the tile's largest, C such that the largest code comes near 2^15. That is
+// exact for groups within 2^-30 of the tile's largest (below, to 2^-40 of it), and A goes into
+// the scores' factor, a number for the tile. q is brought near 2^15 by a power of two per row, as
+// in attn_rows.cuh. So S = Q K^T has exact products and fp32 sums; o += P V has P in fp16 (11
+// bits) and V in the same form as K, with the tile's B relative to a reference R that moves only where
+// B exceeds it by more than 2^6: p * 2^(B - R). Softmax with a running maximum that moves by more
+// than 2^8 at a time, so that the sums in tensor memory are rarely read and scaled.
+//
+// Who does what, in a CTA of 13 warps: two warpgroups of softmax (a thread a row, each with 128
+// rows of its own), one warpgroup that looks up, loads and converts the tiles (into two stages of
+// K and of V), and a thread that issues the matrix instructions. S takes 128 columns of tensor memory for
+// either half, and P goes over it as the second product's first operand; o takes head_dim
+// columns. While one half is in its softmax the other's products run.
+// Bound: the matrix instructions (two products of 128 x 128 x head_dim a half and tile), next to
+// the exponentials and the conversion, each about half of that time.
+//
+// Every wait is bounded; a role whose wait ran out leaves its loop, which makes the others' run out too, and the
+// tensor memory is freed when the matrix instructions are done.
+#include "rmsnorm.h"
+
+#include "async_copy.cuh"
+#include "attn_rows.cuh"
+#include "give_up.h"
+#include "tensor_core.cuh"
+
+namespace rmsn {
+namespace {
+
+constexpr int kTile = 128;      // tokens of a tile
+constexpr int kHalf = 128;      // rows of a half
+constexpr int kThreads = 416;
+constexpr int kInfos = 4;       // tiles whose facts are kept
+
+// What the softmax needs to know of a tile.
+struct TileInfo {
+    int a, b;                  // the largest scale bytes of k and v
+    uint32_t there[4];         // tokens whose page is there and that a row sees
+    uint32_t bad;              // some group of v is not a number
+    uint32_t pad;
+};
+
+template <int GD>
+struct Tiles {
+    static constexpr int D = GD * 32, BLOCKS = (GD + 1) / 2;  // 64 values (128 bytes) of a row
+    static constexpr int MATRIX = BLOCKS * 128 * 128;         // 128 rows
+    static constexpr int Q = 0, K = 2 * MATRIX, V = K + 2 * MATRIX, END = V + 2 * MATRIX;
+    static constexpr int SMEM = END + 1024;  // to a boundary of 1024 bytes
+};
+
+// Byte of piece `c` (16 bytes) of a row in a matrix of 128 rows.
+__device__ __forceinline__ uint32_t piece_at(int row, int c) {
+    return (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void store_piece(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// 2^e as a pair of fp16, 0 below 2^-24 (e <= 15).
+__device__ __forceinline__ uint32_t power_half2(int e) {
+    const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+    return h | h << 16;
+}
+// The lowest n bits (n below 0: none, above 32: all).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// The loading warpgroup's own barrier.
+__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+struct TilesP {
+    int slots;
+    int window;
+    uint32_t g_mul, page_mul, pages;
+    int g_shift, page_shift;
+    long long limit;  // of a wait, in cycles
+};
+
+template <int F, int GD>
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, const TilesP tp) {
+    using C = Tiles<GD>;
+    constexpr bool E4 = F == RMSNORM_CACHE_E4M3;
+    constexpr int CODE = E4 ? 6 : 12;               // C above
+    constexpr int CH = E4 ? 2 * GD : GD;            // 16 code bytes: pieces of a token, and of a thread in a tile
+    constexpr uint32_t kNone = 0xffffffffu;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bars[14];
+    __shared__ TileInfo infos[kInfos];
+    __shared__ uint32_t bads[kInfos][kTile];        // groups of a token's v that are not numbers
+    __shared__ uint32_t tokens[2][kTile];           // where the tile's tokens lie
+    __shared__ int tops[2][2][4];
+    __shared__ uint32_t tmem_at;
+    __shared__ GiveUp late;
+    const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = static_cast<int>(blockIdx.x) % p.heads;
+    const int slot = tp.slots - 1 - static_cast<int>(blockIdx.x) / p.heads;  // the longest first
+    // barriers: K and V ready (loaders), K and V read (products), S ready, P ready, all done
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+    constexpr int kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPFull = 10, kDone = 12;
+    if (w == 0) tmem_alloc(smem_u32(&tmem_at));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kKFull + i), 128);
+            mbar_init(bar(kVFull + i), 128);
+            mbar_init(bar(kKFree + i), 1);
+            mbar_init(bar(kVFree + i), 1);
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPFull + i), 128);
+        }
+        mbar_init(bar(kDone), 1);
+        late.clear();
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    RowsPlan plan;  // what the slots' arithmetic takes of it
+    plan.window = tp.window;
+    plan.g_mul = tp.g_mul;
+    plan.g_shift = tp.g_shift;
+    plan.tile_shift = 7;
+    const Slot sl = slot_of<2 * kHalf>(p, plan, Sequences{nullptr, nullptr}, slot);
+    const int halves = sl.rows > kHalf ? 2 : 1, tiles = sl.tiles;
+
+    // ---- q, by the softmax threads: a row each
+    float row_scale = 0.f;
+    int lim = 0, low = 0;  // tokens that the row sees
+    const int half = w >> 2, rr = threadIdx.x;
+    const bool live = w < 8 && rr < sl.rows;
+    int64_t out_row = 0;
+    int qh = 0;
+    if (w < 8 && half < halves) {
+        uint32_t v[C::D / 2];
+        float top = 0.f;
+        if (live) {
+            const int i = divide(sl.r0 + rr, tp.g_mul, tp.g_shift);
+            out_row = sl.row0 + i;
+            qh = head * p.G + sl.r0 + rr - i * p.G;
+            int to;
+            seen32(p, plan, sl.n, sl.len, i, low, to);
+            lim = min(to, sl.len);
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + out_row * p.q.st + qh * p.q.sh);
+#pragma unroll
+            for (int k = 0; k < C::D / 8; ++k) {
+                const uint4 u = __ldg(q + k);
+                v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < C::D / 2; ++k) v[k] = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < C::D / 2; ++k) {
+            const float2 f = unpack16(v[k], p.dtype == kBF16);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        int ex = static_cast<int>(__float_as_uint(top) >> 23);
+        ex = top == 0.f ? 141 : ex < 15 ? 15 : ex;  // both powers stay normal
+        const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+        row_scale = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23) * (p.scale * 1.4426950408889634f);
+        const uint32_t to = smem + C::Q + half * C::MATRIX;
+#pragma unroll
+        for (int k = 0; k < C::D / 8; ++k) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack16(v[4 * k + e], p.dtype == kBF16);
+                h[e] = half2_bits(f.x * up, f.y * up);
+            }
+            store_piece(to + piece_at(rr & 127, k), h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    if (w < 8) {
+        // ---- softmax
+        if (sl.rows && half < halves) {
+            const uint32_t lanes = tmem + (static_cast<uint32_t>((w & 3) * 32) << 16);
+            const uint32_t s_at = lanes + half * 128, o_at = lanes + 256 + half * 128;
+            float m = 0.f, l = 0.f;
+            bool started = false;
+            int ref = 0;
+            uint32_t nan_groups = 0;
+            bool ok = true;
+            for (int t = 0; t < tiles; ++t) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kSFull + half), t & 1, tp.limit));
+                if (!ok) break;
+                tc_fence_after();
+                const TileInfo& info = infos[t % kInfos];
+                const int a = info.a, b = info.b, t0 = (sl.tile0 + t) * kTile;
+                const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
+                const float factor = row_scale * power(a - 127 - CODE);
+                // Sums of the tiles before, scaled by f (all lanes of the warp).
+                auto scale_sums = [&](float f) {
+#pragma unroll
+                    for (int c = 0; c < GD; ++c) {
+                        uint32_t v[32];
+                        tmem_load(v, o_at + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        tmem_store32(o_at + c * 32, v);
+                    }
+                    tmem_stored();
+                };
+                if (t == 0) ref = b;
+                if (b > ref + 6) {  // the same for all threads
+                    scale_sums(power(ref - b));
+                    ref = b;
+                }
+                const float shift = static_cast<float>(b - ref);
+                const bool whole = (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
+                const bool masked = __any_sync(0xffffffffu, !whole || t0 + kTile > lim || t0 < low);
+                if (info.bad) {  // rare: which groups of v are not numbers for this row
+                    for (int k = 0; k < kTile; ++k)
+                        if (t0 + k < lim && t0 + k >= low) nan_groups |= bads[t % kInfos][k];
+                }
+                float sum, most;
+                uint32_t h[4][16];  // P stays here until S, which it will lie over, is not needed again
+                for (int pass = 0;; ++pass) {
+                    sum = 0.f;
+                    most = -INFINITY;
+                    const float less = shift - m;
+                    const bool first = t == 0 && pass == 0;  // only the maximum is wanted
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_load(v, s_at + c * 32);
+                        // in powers of two, above the row's maximum so far; -infinity where the row
+                        // does not see the token
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), factor, less));
+                        if (masked) {
+                            const uint32_t sees = there[c] & bits_below(lim - t0 - c * 32) & ~bits_below(low - t0 - c * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((sees >> e) & 1u)) v[e] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) most = fmaxf(most, __uint_as_float(v[e]));
+                        if (first) continue;
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float px = exp2_fast(__uint_as_float(v[e])), py = exp2_fast(__uint_as_float(v[e + 1]));
+                            s0 += px;
+                            s1 += py;
+                            h[c][e / 2] = half2_bits(px, py);
+                        }
+                        sum += s0 + s1;
+                    }
+                    const float above = most - shift;  // over the row's maximum so far
+                    const bool grow = started ? above > 8.f : most > -INFINITY;
+                    if (!first && !__any_sync(0xffffffffu, grow)) break;
+                    const float f = grow && started ? exp2_fast(-above) : grow ? 0.f : 1.f;
+                    if (grow) {
+                        m += above;
+                        started = true;
+                        l *= f;
+                    }
+                    if (t > 0) scale_sums(f);
+                    if (pass == 2) break;  // (a maximum that is not finite)
+                }
+                l += sum * power(ref - b);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_store16(s_at + c * 16, h[c]);
+                tmem_stored();
+                tc_fence_before();
+                mbar_arrive(bar(kPFull + half));
+            }
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDone), 0, tp.limit));
+            if (!ok) {
+                if (lane == 0) atomicOr(p.late, 1u);
+            } else {
+                tc_fence_after();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                // 2^(ref - 127 - CODE) in two factors, which stay normal
+                const int e = ref - 127 - CODE;
+                const float f1 = power(e / 2) * inv, f2_ = power(e - e / 2);
+                uint16_t* out = static_cast<uint16_t*>(p.out.p) + out_row * p.out.st + qh * p.out.sh;
+                const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+#pragma unroll
+                for (int c = 0; c < GD; ++c) {
+                    uint32_t v[32], h[16];
+                    tmem_load(v, o_at + c * 32);
+                    const bool nan = (nan_groups >> c) & 1u;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float x = __uint_as_float(v[2 * k]) * f1 * f2_, y = __uint_as_float(v[2 * k + 1]) * f1 * f2_;
+                        if (l == 0.f) x = y = 0.f;
+                        if (nan) x = y = __uint_as_float(0x7fc00000u);
+                        h[k] = p.dtype == kBF16 ? Codec<kBF16>::pack2(x, y) : Codec<kFP16>::pack2(x, y);
+                    }
+                    if (!live) continue;
+                    if (vec) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            out[c * 32 + 2 * k] = static_cast<uint16_t>(h[k]);
+                            out[c * 32 + 2 * k + 1] = static_cast<uint16_t>(h[k] >> 16);
+                        }
+                    }
+                }
+                if (p.lse && live)
+                    p.lse[out_row * p.heads_q + qh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+        }
+    } else if (w < 12) {
+        // ---- tiles: thread i looks up token i; pieces of 16 code bytes go round the threads
+        if (sl.rows) {
+            const int tid = threadIdx.x - 256, lw = w - 8;
+            const int32_t* table = p.table + static_cast<int64_t>(sl.b) * p.width;
+            const uint32_t head_off = static_cast<uint32_t>(head * head_step(p));
+            auto lookup = [&](int t) {
+                const int tok = (sl.tile0 + t) * kTile + tid;
+                uint32_t at = kNone;
+                if (t < tiles && tok >= sl.low && tok < sl.high) {
+                    const uint32_t col = divide(tok, tp.page_mul, tp.page_shift), off = tok - col * p.page_size;
+                    const uint32_t page = static_cast<uint32_t>(__ldg(table + col));
+                    if (page < tp.pages)
+                        at = (p.heads_first ? page * p.heads * p.page_size + off : (page * p.page_size + off) * p.heads) + head_off;
+                    else
+                        atomicOr(p.status, 1u);
+                }
+                tokens[t & 1][tid] = at;
+                bads[t % kInfos][tid] = 0;
+                const uint32_t some = __ballot_sync(0xffffffffu, at != kNone);
+                if (lane == 0) infos[t % kInfos].there[lw] = some;
+                if (tid == 0) infos[t % kInfos].bad = 0;
+            };
+            uint4 kc[CH], vc[CH];
+            uint32_t ks[CH], vs[CH];
+            auto load_codes = [&](int t, int which, uint4 (&c)[CH]) {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int i = tid + 128 * k, tok = i / CH, part = i - tok * CH;
+                    const uint32_t at = tokens[t & 1][tok];
+                    c[k] = at == kNone ? make_uint4(0u, 0u, 0u, 0u)
+                                       : __ldg(reinterpret_cast<const uint4*>(plus(p.codes[which] + part * 16, at, CH * 16)));
+                }
+            };
+            auto load_scales = [&](int t, int which, uint32_t (&s)[CH]) {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int i = tid + 128 * k, tok = i / CH, part = i - tok * CH;
+                    const uint32_t at = tokens[t & 1][tok];
+                    s[k] = at == kNone ? 0u : __ldg(plus(p.scales[which] + (E4 ? part >> 1 : part), at, GD));
+                }
+            };
+            // A piece of codes as fp16 into the matrix at `to`.
+            auto convert = [&](uint32_t to, int k, const uint4& c, uint32_t f) {
+                const int i = tid + 128 * k, tok = i / CH, part = i - tok * CH;
+                const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+                if (E4) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t h[4];
+                        pairs_e4m3(word[2 * j], h[0], h[1]);
+                        pairs_e4m3(word[2 * j + 1], h[2], h[3]);
+                        store_piece(to + piece_at(tok, part * 2 + j), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
+                    }
+                } else {
+#pragma unroll
+                    for (int j0 = 0; j0 < 4; ++j0) {
+                        const int j = j0;
+                        uint32_t h[4];
+                        pairs_e2m1(word[j], h[0], h[1], h[2], h[3]);
+                        store_piece(to + piece_at(tok, part * 4 + j), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
+                    }
+                }
+            };
+            lookup(0);
+            loaders_sync();
+            load_codes(0, 0, kc);
+            load_scales(0, 0, ks);
+            load_scales(0, 1, vs);
+            for (int t = 0; t < tiles; ++t) {
+                const int stage = t & 1;
+                load_codes(t, 1, vc);
+                // the largest scale bytes that are numbers
+                int a = 0, b = 0;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    a = max(a, static_cast<int>(ks[k] == 255u ? 0u : ks[k]));
+                    b = max(b, static_cast<int>(vs[k] == 255u ? 0u : vs[k]));
+                }
+                a = __reduce_max_sync(0xffffffffu, a);
+                b = __reduce_max_sync(0xffffffffu, b);
+                if (lane == 0) tops[stage][0][lw] = a, tops[stage][1][lw] = b;
+                if (t >= 2 && !mbar_wait_bounded(bar(kKFree + stage), ((t >> 1) + 1) & 1, tp.limit)) late.mark(2 * t);
+                loaders_sync();
+                if (late.at(2 * t)) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a = max(a, tops[stage][0][k]), b = max(b, tops[stage][1][k]);
+                if (tid == 0) infos[t % kInfos].a = a, infos[t % kInfos].b = b;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    if (vs[k] == 255u) {
+                        const int i = tid + 128 * k, tok = i / CH, part = i - tok * CH;
+                        atomicOr(&bads[t % kInfos][tok], 1u << (E4 ? part >> 1 : part));
+                        infos[t % kInfos].bad = 1;
+                    }
+                    const uint32_t f = ks[k] == 255u ? 0x7e007e00u : power_half2(static_cast<int>(ks[k]) - a + CODE);
+                    convert(smem + C::K + stage * C::MATRIX, k, kc[k], f);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kKFull + stage));
+                lookup(t + 1);
+                uint32_t vf[CH];
+#pragma unroll
+                for (int k = 0; k < CH; ++k) vf[k] = vs[k] == 255u ? 0u : power_half2(static_cast<int>(vs[k]) - b + CODE);
+                if (t >= 2 && !mbar_wait_bounded(bar(kVFree + stage), ((t >> 1) + 1) & 1, tp.limit)) late.mark(2 * t + 1);
+                loaders_sync();
+                if (late.at(2 * t + 1)) break;
+                if (t + 1 < tiles) {
+                    load_codes(t + 1, 0, kc);
+                    load_scales(t + 1, 0, ks);
+                    load_scales(t + 1, 1, vs);
+                }
+#pragma unroll
+                for (int k = 0; k < CH; ++k) convert(smem + C::V + stage * C::MATRIX, k, vc[k], vf[k]);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kVFull + stage));
+            }
+        }
+    } else if (lane == 0 && sl.rows) {
+        // ---- matrix instructions
+        constexpr uint32_t s_shape = mma_shape(128, 128, false), o_shape = mma_shape(128, C::D, true);
+        bool ok = true;
+        auto scores = [&](int q, int stage) {
+            const uint32_t a = smem + C::Q + q * C::MATRIX, b = smem + C::K + stage * C::MATRIX;
+#pragma unroll
+            for (int k = 0; k < C::D / 16; ++k) {
+                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                tc_mma(tmem + q * 128, smem_matrix(a + off, 16, 1024), smem_matrix(b + off, 16, 1024), s_shape, k > 0);
+            }
+            tc_commit(bar(kSFull + q));
+        };
+        ok = mbar_wait_bounded(bar(kKFull), 0, tp.limit);
+        if (ok) {
+            tc_fence_after();
+            for (int q = 0; q < halves; ++q) scores(q, 0);
+            tc_commit(bar(kKFree));
+        }
+        for (int t = 0; ok && t < tiles; ++t) {
+            const int stage = t & 1;
+            ok = mbar_wait_bounded(bar(kVFull + stage), (t >> 1) & 1, tp.limit);
+            for (int q = 0; ok && q < halves; ++q) {
+                ok = mbar_wait_bounded(bar(kPFull + q), t & 1, tp.limit);
+                if (!ok) break;
+                tc_fence_after();
+                // V: 64 values of head_dim a row of 128 bytes; 16 tokens are 2048 bytes on
+                const uint32_t v = smem + C::V + stage * C::MATRIX;
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    tc_mma_tmem(tmem + 256 + q * 128, tmem + q * 128 + k * 8, smem_matrix(v + k * 2048, 16384, 1024), o_shape,
+                                t > 0 || k > 0);
+                if (q == halves - 1) tc_commit(bar(kVFree + stage));
+                if (t + 1 < tiles) {
+                    if (q == 0) ok = mbar_wait_bounded(bar(kKFull + (stage ^ 1)), ((t + 1) >> 1) & 1, tp.limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(q, stage ^ 1);
+                    if (q == halves - 1) tc_commit(bar(kKFree + (stage ^ 1)));
+                }
+            }
+        }
+        if (!ok) atomicOr(p.late, 1u);
+        tc_commit(bar(kDone));
+        mbar_wait_bounded(bar(kDone), 0, tp.limit);  // nothing of it is on its way when the memory is freed
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (w == 0) {
+        tc_fence_after();
+        tmem_free(tmem);
+    }
+}
+
+template <int F, int GD>
+cudaError_t launch_tiles(const AttnP& p, const TilesP& tp, const OpCfg& c) {
+    auto fn = attn_tiles_kernel<F, GD>;
+    const int smem = Tiles<GD>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return op_launch(c, fn, static_cast<int64_t>(tp.slots) * p.heads, kThreads, smem, p, tp);
+}
+
+template <int F>
+cudaError_t pick_tiles(const AttnP& p, const TilesP& tp, const OpCfg& c) {
+    switch (p.groups) {
+        case 2: return launch_tiles<F, 2>(p, tp, c);
+        case 3: return launch_tiles<F, 3>(p, tp, c);
+        default: return launch_tiles<F, 4>(p, tp, c);
+    }
+}
+
+}  // namespace
+
+cudaError_t attn_tiles(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
+    TilesP tp;
+    tp.slots = static_cast<int>(p.rows * p.G / (2 * kHalf) + p.sequences);
+    tp.window = r.window;
+    tp.g_mul = r.g_mul;
+    tp.g_shift = r.g_shift;
+    tp.page_mul = r.page_mul;
+    tp.page_shift = r.page_shift;
+    tp.pages = r.pages;
+    // SM cycles, at about two a nanosecond
+    tp.limit = 2 * (c.wait_limit_ns > 0 ? c.wait_limit_ns : 1000000000LL);
+    return p.format == RMSNORM_CACHE_E4M3 ? pick_tiles<RMSNORM_CACHE_E4M3>(p, tp, c) : pick_tiles<RMSNORM_CACHE_E2M1>(p, tp, c);
+}
+
+}  // namespace rmsn

@@ -215,10 +215,12 @@ struct AttnP {
     float scale;
     void* ws;
     unsigned int* status;  // the device's word for pages that are not there
+    unsigned int* late;    // and for waits that ran out
 };
 
 cudaError_t attn_run(const AttnP& p, const OpCfg& c);
 cudaError_t attn_status_read_and_clear(unsigned int* value);
+cudaError_t attn_late_read_and_clear(unsigned int* value);
 int64_t attn_ws_bytes(int64_t heads, int64_t G, int64_t D, int64_t sequences, int64_t rows, int sm_count);
 
 // Front end helpers shared with api.cu.

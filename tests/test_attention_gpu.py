@@ -123,6 +123,68 @@ def test_a_prompt(G):
             _run(cache, table, lens, counts, 2 * G, dtype, 9, variants=("auto",))
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 150)])
+def test_long_prompts(fmt, D, dtype, causal, window):
+    """Enough rows for the tensor cores: blocks of 256 rows that end inside, sequences that hold more
+    than their queries, and fewer, a group that is not a power of two."""
+    heads, G = 6, 5
+    lens, counts = [700, 300, 129, 40, 513], [300, 300, 129, 260, 1]
+    cache, table = _filled(lens, 24, heads, D, fmt, D + window, first=bool(window))
+    _run(cache, table, lens, counts, heads * G, U.DT[dtype], window, causal=causal, window=window, variants=("auto",))
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_long_prompts_with_what_is_not_finite_or_not_there(fmt):
+    heads, G = 8, 8
+    lens, counts = [500, 260, 300], [200, 250, 260]
+    cache, table = _filled(lens, 16, heads, 128, fmt, 2)
+    g = torch.Generator().manual_seed(3)
+    # scales far apart, from token to token and from tile to tile
+    cache.v_scales[torch.tensor(table[0][:31]).long()] += torch.randint(
+        -9, 20, cache.v_scales[torch.tensor(table[0][:31]).long()].shape, generator=g).to(torch.uint8).to(DEV)
+    cache.v_scales[table[0][28]] += 12
+    for page, head, grp, which in ((table[0][20], 3, 2, "k"), (table[1][8], 0, 0, "v"), (table[1][15], 7, 3, "v")):
+        getattr(cache, which + "_scales")[page, 5, head, grp] = 255
+    table[2][3], table[2][9] = -1, cache.pages
+    for dtype in (torch.bfloat16, torch.float16):
+        _run(cache, table, lens, counts, heads * G, dtype, 1, status=-12, variants=("auto",))
+
+
+def test_long_prompts_on_odd_strides_and_twice():
+    heads, G, D = 8, 4, 128
+    lens, counts = [600, 500], [600, 500]
+    cache, table = _filled(lens, 16, heads, D, "e2m1", 2)
+    cu, q = [0, 600, 1100], _q(1100, heads * G, D, torch.bfloat16, 3)
+    want = S.attention(cache, q, table, lens, cu, D ** -0.5, True, 0)
+    ref, lse = B.cache_attention(cache, q, _i32(table), _i32(lens), cu_q=_i32(cu), lse=True)
+    S.check_attention(ref, lse, want, torch.bfloat16, "prompt")
+    odd = torch.zeros(1100, heads * G + 1, D + 3, dtype=torch.bfloat16, device=DEV)
+    for _ in range(3):  # rows of the output on no vector's border; the same bits
+        B.cache_attention(cache, q, _i32(table), _i32(lens), cu_q=_i32(cu), out=odd[:, 1:, 1:D + 1])
+        assert torch.equal(odd[:, 1:, 1:D + 1], ref)
+    assert bool((odd[:, 0] == 0).all()) and bool((odd[..., 0] == 0).all()) and bool((odd[..., D + 1:] == 0).all())
+    # rows behind the last sequence stay
+    out = torch.full((1130, heads * G, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    more = torch.cat([q, q[:30]])
+    B.cache_attention(cache, more, _i32(table), _i32(lens), cu_q=_i32(cu), out=out)
+    assert torch.equal(out[:1100], ref) and bool((out[1100:] == 3).all())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    t, ln, c = _i32(table), _i32(lens), _i32(cu)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got, _ = B.cache_attention(cache, q, t, ln, cu_q=c)
+    graph.replay()
+    assert torch.equal(ref, got)
+    both = [B.cache_attention(cache, q, _i32(table), _i32(lens), cu_q=_i32(cu), stream=s)[0] for s in (side, None, side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref, b) for b in both)
+
+
 def test_no_cu_is_one_row_each_and_out_and_strides():
     lens = [20, 33]
     cache, table = _filled(lens, 16, 2, 64, "e2m1", 8)
