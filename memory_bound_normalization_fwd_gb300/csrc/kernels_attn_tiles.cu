@@ -10,11 +10,12 @@
 // B exceeds it by more than 2^6: p * 2^(B - R). Softmax with a running maximum that moves by more
 // than 2^8 at a time, so that the sums in tensor memory are rarely read and scaled.
 //
-// Who does what, in a CTA of 13 warps: two warpgroups of softmax (a thread a row, each with 128
+// Who does what, in a CTA of 16 warps: two warpgroups of softmax (a thread a row, each with 128
 // rows of its own), one warpgroup that looks up, loads and converts the tiles (into two stages of
-// K and of V), and a thread that issues the matrix instructions. S takes 128 columns of tensor memory for
-// either half, and P goes over it as the second product's first operand; o takes head_dim
-// columns. While one half is in its softmax the other's products run.
+// K and of V), and a thread that issues the matrix instructions. A tile is taken in two steps of
+// 64 tokens. S takes 64 columns of tensor memory for either half and step, and P goes over it as the
+// second product's first operand; o takes head_dim columns. While a half's softmax is in one
+// step, the products of the other step run: P V of the last tile, then S of the next.
 // Bound: the matrix instructions (two products of 128 x 128 x head_dim a half and tile), next to
 // the exponentials and the conversion, each about half of that time.
 //
@@ -32,7 +33,8 @@ namespace {
 
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kHalf = 128;      // rows of a half
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
+constexpr int kStep = 64;       // tokens of a step
 constexpr int kInfos = 4;       // tiles whose facts are kept
 
 // What the softmax needs to know of a tile.
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     constexpr int CH = E4 ? 2 * GD : GD;            // 16 code bytes: pieces of a token, and of a thread in a tile
     constexpr uint32_t kNone = 0xffffffffu;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t bars[14];
+    __shared__ __align__(8) uint64_t bars[19];
     __shared__ TileInfo infos[kInfos];
     __shared__ uint32_t bads[kInfos][kTile];        // groups of a token's v that are not numbers
     __shared__ uint32_t tokens[2][kTile];           // where the tile's tokens lie
@@ -100,9 +102,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = static_cast<int>(blockIdx.x) % p.heads;
     const int slot = tp.slots - 1 - static_cast<int>(blockIdx.x) / p.heads;  // the longest first
-    // barriers: K and V ready (loaders), K and V read (products), S ready, P ready, all done
+    // barriers: K and V ready (loaders), K and V read (products), S ready, P ready, o summed, all done
     auto bar = [&](int i) { return smem_u32(bars + i); };
-    constexpr int kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPFull = 10, kDone = 12;
+    constexpr int kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPFull = 12, kOFree = 16, kDone = 18;
     if (w == 0) tmem_alloc(smem_u32(&tmem_at));
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -110,6 +112,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             mbar_init(bar(kVFull + i), 128);
             mbar_init(bar(kKFree + i), 1);
             mbar_init(bar(kVFree + i), 1);
+            mbar_init(bar(kOFree + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {  // half * 2 + step
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), 128);
         }
@@ -182,100 +187,103 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     tc_fence_after();
     const uint32_t tmem = tmem_at;
 
+    // Registers go from the others to the softmax: 2 * 168 + 120 + 56 = 4 * 128 of each warpgroup.
     if (w < 8) {
         // ---- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         if (sl.rows && half < halves) {
             const uint32_t lanes = tmem + (static_cast<uint32_t>((w & 3) * 32) << 16);
-            const uint32_t s_at = lanes + half * 128, o_at = lanes + 256 + half * 128;
+            const uint32_t o_at = lanes + 256 + half * 128;
             float m = 0.f, l = 0.f;
             bool started = false;
             int ref = 0;
             uint32_t nan_groups = 0;
             bool ok = true;
-            for (int t = 0; t < tiles; ++t) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kSFull + half), t & 1, tp.limit));
+            for (int u = 0; u < 2 * tiles; ++u) {
+                const int t = u >> 1, step = u & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kSFull + half * 2 + step), t & 1, tp.limit));
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t s_at = lanes + half * 128 + step * 64;
+                uint32_t v[64];
+                tmem_load_async(v, s_at);
+                tmem_load_async(v + 32, s_at + 32);
                 const TileInfo& info = infos[t % kInfos];
-                const int a = info.a, b = info.b, t0 = (sl.tile0 + t) * kTile;
-                const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
+                const int a = info.a, b = info.b, t0 = (sl.tile0 + t) * kTile + step * kStep;
+                const uint32_t there0 = info.there[2 * step], there1 = info.there[2 * step + 1];
                 const float factor = row_scale * power(a - 127 - CODE);
                 // Sums of the tiles before, scaled by f (all lanes of the warp).
                 auto scale_sums = [&](float f) {
+#pragma unroll 1
+                    for (int c = 0; c < GD * 32; c += 16) {
+                        uint32_t o[16];
+                        tmem_load16(o, o_at + c);
 #pragma unroll
-                    for (int c = 0; c < GD; ++c) {
-                        uint32_t v[32];
-                        tmem_load(v, o_at + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        tmem_store32(o_at + c * 32, v);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_store16(o_at + c, o);
                     }
                     tmem_stored();
                 };
-                if (t == 0) ref = b;
-                if (b > ref + 6) {  // the same for all threads
-                    scale_sums(power(ref - b));
-                    ref = b;
-                }
-                const float shift = static_cast<float>(b - ref);
-                const bool whole = (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
-                const bool masked = __any_sync(0xffffffffu, !whole || t0 + kTile > lim || t0 < low);
+                if (u == 0) ref = b;
+                const int far = b - ref;  // the same for all threads
+                const float shift = far > 6 ? 0.f : static_cast<float>(far);
+                const bool masked = __any_sync(0xffffffffu, (there0 & there1) != 0xffffffffu || t0 + kStep > lim || t0 < low);
                 if (info.bad) {  // rare: which groups of v are not numbers for this row
-                    for (int k = 0; k < kTile; ++k)
-                        if (t0 + k < lim && t0 + k >= low) nan_groups |= bads[t % kInfos][k];
+                    for (int k = 0; k < kStep; ++k)
+                        if (t0 + k < lim && t0 + k >= low) nan_groups |= bads[t % kInfos][step * kStep + k];
                 }
-                float sum, most;
-                uint32_t h[4][16];  // P stays here until S, which it will lie over, is not needed again
-                for (int pass = 0;; ++pass) {
-                    sum = 0.f;
-                    most = -INFINITY;
-                    const float less = shift - m;
-                    const bool first = t == 0 && pass == 0;  // only the maximum is wanted
+                // in powers of two, above the row's maximum so far; -infinity where the row does
+                // not see the token
+                const float less = shift - m;
+                float most = -INFINITY;
+                tmem_loaded(v);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_load(v, s_at + c * 32);
-                        // in powers of two, above the row's maximum so far; -infinity where the row
-                        // does not see the token
+                for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), factor, less));
+                if (masked) {
+                    const uint32_t s0 = there0 & bits_below(lim - t0) & ~bits_below(low - t0);
+                    const uint32_t s1 = there1 & bits_below(lim - t0 - 32) & ~bits_below(low - t0 - 32);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), factor, less));
-                        if (masked) {
-                            const uint32_t sees = there[c] & bits_below(lim - t0 - c * 32) & ~bits_below(low - t0 - c * 32);
+                    for (int e = 0; e < 64; ++e)
+                        if (!(((e < 32 ? s0 : s1) >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+                }
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((sees >> e) & 1u)) v[e] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) most = fmaxf(most, __uint_as_float(v[e]));
-                        if (first) continue;
-                        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float px = exp2_fast(__uint_as_float(v[e])), py = exp2_fast(__uint_as_float(v[e + 1]));
-                            s0 += px;
-                            s1 += py;
-                            h[c][e / 2] = half2_bits(px, py);
-                        }
-                        sum += s0 + s1;
-                    }
-                    const float above = most - shift;  // over the row's maximum so far
-                    const bool grow = started ? above > 8.f : most > -INFINITY;
-                    if (!first && !__any_sync(0xffffffffu, grow)) break;
-                    const float f = grow && started ? exp2_fast(-above) : grow ? 0.f : 1.f;
+                for (int e = 0; e < 64; ++e) most = fmaxf(most, __uint_as_float(v[e]));
+                const float above = most - shift;
+                const bool grow = started ? above > 8.f : most > -INFINITY;
+                if (__any_sync(0xffffffffu, grow || far > 6)) {
+                    // the sums so far are complete: the products that this S waited behind
+                    float f = far > 6 ? power(-far) : 1.f;
+                    if (far > 6) ref = b;
                     if (grow) {
+                        const float g = started ? exp2_fast(-above) : 0.f;
                         m += above;
                         started = true;
-                        l *= f;
-                    }
-                    if (t > 0) scale_sums(f);
-                    if (pass == 2) break;  // (a maximum that is not finite)
-                }
-                l += sum * power(ref - b);
+                        l *= g;
+                        f *= g;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_store16(s_at + c * 16, h[c]);
+                        for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - above);
+                    }
+                    if (u > 0) {
+                        // (with two steps the product before the last may still be on its way)
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kOFree + half), (u - 1) & 1, tp.limit));
+                        if (!ok) break;
+                        tc_fence_after();
+                        scale_sums(f);
+                    }
+                }
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const float px = exp2_fast(__uint_as_float(v[e])), py = exp2_fast(__uint_as_float(v[e + 1]));
+                    s0 += px;
+                    s1 += py;
+                    v[e / 2] = half2_bits(px, py);
+                }
+                tmem_store32(s_at, v);
+                l = fmaf(s0 + s1, power(ref - b), l);
                 tmem_stored();
                 tc_fence_before();
-                mbar_arrive(bar(kPFull + half));
+                mbar_arrive(bar(kPFull + half * 2 + step));
             }
             ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDone), 0, tp.limit));
             if (!ok) {
@@ -291,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
 #pragma unroll
                 for (int c = 0; c < GD; ++c) {
                     uint32_t v[32], h[16];
-                    tmem_load(v, o_at + c * 32);
+                    tmem_load_async(v, o_at + c * 32);
+                    tmem_loaded(v);
                     const bool nan = (nan_groups >> c) & 1u;
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -319,16 +328,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
         }
     } else if (w < 12) {
         // ---- tiles: thread i looks up token i; pieces of 16 code bytes go round the threads
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         if (sl.rows) {
             const int tid = threadIdx.x - 256, lw = w - 8;
             const int32_t* table = p.table + static_cast<int64_t>(sl.b) * p.width;
             const uint32_t head_off = static_cast<uint32_t>(head * head_step(p));
-            auto lookup = [&](int t) {
+            // (in two steps, a tile apart: the page's number is on its way in between)
+            auto page_of = [&](int t) -> uint32_t {
+                const int tok = (sl.tile0 + t) * kTile + tid;
+                if (t >= tiles || tok < sl.low || tok >= sl.high) return kNone;
+                return static_cast<uint32_t>(__ldg(table + divide(tok, tp.page_mul, tp.page_shift)));
+            };
+            auto lookup = [&](int t, uint32_t page) {
                 const int tok = (sl.tile0 + t) * kTile + tid;
                 uint32_t at = kNone;
                 if (t < tiles && tok >= sl.low && tok < sl.high) {
-                    const uint32_t col = divide(tok, tp.page_mul, tp.page_shift), off = tok - col * p.page_size;
-                    const uint32_t page = static_cast<uint32_t>(__ldg(table + col));
+                    const uint32_t off = tok - divide(tok, tp.page_mul, tp.page_shift) * p.page_size;
                     if (page < tp.pages)
                         at = (p.heads_first ? page * p.heads * p.page_size + off : (page * p.page_size + off) * p.heads) + head_off;
                     else
@@ -381,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                     }
                 }
             };
-            lookup(0);
+            lookup(0, page_of(0));
+            uint32_t page = page_of(1);
             loaders_sync();
             load_codes(0, 0, kc);
             load_scales(0, 0, ks);
@@ -417,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(kKFull + stage));
-                lookup(t + 1);
+                lookup(t + 1, page);
+                page = page_of(t + 2);
                 uint32_t vf[CH];
 #pragma unroll
                 for (int k = 0; k < CH; ++k) vf[k] = vs[k] == 255u ? 0u : power_half2(static_cast<int>(vs[k]) - b + CODE);
@@ -435,51 +452,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 mbar_arrive(bar(kVFull + stage));
             }
         }
-    } else if (lane == 0 && sl.rows) {
+    } else {
         // ---- matrix instructions
-        constexpr uint32_t s_shape = mma_shape(128, 128, false), o_shape = mma_shape(128, C::D, true);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (w == 12 && lane == 0 && sl.rows) {
+        constexpr uint32_t s_shape = mma_shape(128, kStep, false), o_shape = mma_shape(128, C::D, true);
         bool ok = true;
-        auto scores = [&](int q, int stage) {
-            const uint32_t a = smem + C::Q + q * C::MATRIX, b = smem + C::K + stage * C::MATRIX;
+        auto scores = [&](int q, int step, int stage) {
+            const uint32_t a = smem + C::Q + q * C::MATRIX, b = smem + C::K + stage * C::MATRIX + step * kStep * 128;
 #pragma unroll
             for (int k = 0; k < C::D / 16; ++k) {
                 const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                tc_mma(tmem + q * 128, smem_matrix(a + off, 16, 1024), smem_matrix(b + off, 16, 1024), s_shape, k > 0);
+                tc_mma(tmem + q * 128 + step * 64, smem_matrix(a + off, 16, 1024), smem_matrix(b + off, 16, 1024), s_shape, k > 0);
             }
-            tc_commit(bar(kSFull + q));
+            tc_commit(bar(kSFull + q * 2 + step));
         };
         ok = mbar_wait_bounded(bar(kKFull), 0, tp.limit);
         if (ok) {
             tc_fence_after();
-            for (int q = 0; q < halves; ++q) scores(q, 0);
+            for (int step = 0; step < 2; ++step)
+                for (int q = 0; q < halves; ++q) scores(q, step, 0);
             tc_commit(bar(kKFree));
         }
-        for (int t = 0; ok && t < tiles; ++t) {
-            const int stage = t & 1;
-            ok = mbar_wait_bounded(bar(kVFull + stage), (t >> 1) & 1, tp.limit);
+        for (int u = 0; ok && u < 2 * tiles; ++u) {
+            const int t = u >> 1, step = u & 1, stage = t & 1;
+            if (step == 0) ok = mbar_wait_bounded(bar(kVFull + stage), (t >> 1) & 1, tp.limit);
             for (int q = 0; ok && q < halves; ++q) {
-                ok = mbar_wait_bounded(bar(kPFull + q), t & 1, tp.limit);
+                ok = mbar_wait_bounded(bar(kPFull + q * 2 + step), t & 1, tp.limit);
                 if (!ok) break;
                 tc_fence_after();
                 // V: 64 values of head_dim a row of 128 bytes; 16 tokens are 2048 bytes on
-                const uint32_t v = smem + C::V + stage * C::MATRIX;
+                const uint32_t v = smem + C::V + stage * C::MATRIX + step * kStep * 128;
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc_mma_tmem(tmem + 256 + q * 128, tmem + q * 128 + k * 8, smem_matrix(v + k * 2048, 16384, 1024), o_shape,
-                                t > 0 || k > 0);
-                if (q == halves - 1) tc_commit(bar(kVFree + stage));
+                for (int k = 0; k < kStep / 16; ++k)
+                    tc_mma_tmem(tmem + 256 + q * 128, tmem + q * 128 + step * 64 + k * 8, smem_matrix(v + k * 2048, 16384, 1024),
+                                o_shape, u > 0 || k > 0);
+                tc_commit(bar(kOFree + q));
+                if (step == 1 && q == halves - 1) tc_commit(bar(kVFree + stage));
                 if (t + 1 < tiles) {
-                    if (q == 0) ok = mbar_wait_bounded(bar(kKFull + (stage ^ 1)), ((t + 1) >> 1) & 1, tp.limit);
+                    if (step == 0 && q == 0) ok = mbar_wait_bounded(bar(kKFull + (stage ^ 1)), ((t + 1) >> 1) & 1, tp.limit);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(q, stage ^ 1);
-                    if (q == halves - 1) tc_commit(bar(kKFree + (stage ^ 1)));
+                    scores(q, step, stage ^ 1);
+                    if (step == 1 && q == halves - 1) tc_commit(bar(kKFree + (stage ^ 1)));
                 }
             }
         }
         if (!ok) atomicOr(p.late, 1u);
         tc_commit(bar(kDone));
         mbar_wait_bounded(bar(kDone), 0, tp.limit);  // nothing of it is on its way when the memory is freed
+        }
     }
     __syncwarp();
     tc_fence_before();

@@ -44,8 +44,9 @@ static __device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint6
 static __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// A thread's lane (row) of 32 columns, and 32 or 16 columns back.
-static __device__ __forceinline__ void tmem_load(uint32_t (&v)[32], uint32_t at) {
+// A thread's lane (row) of 32 or 16 columns, and back.
+// (v holds the values behind tmem_loaded, whose operands keep them from being read before)
+static __device__ __forceinline__ void tmem_load_async(uint32_t* v, uint32_t at) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -55,7 +56,21 @@ static __device__ __forceinline__ void tmem_load(uint32_t (&v)[32], uint32_t at)
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(at)
         : "memory");
+}
+template <int N>
+static __device__ __forceinline__ void tmem_loaded(uint32_t (&v)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+static __device__ __forceinline__ void tmem_load16(uint32_t (&v)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at)
+        : "memory");
+    tmem_loaded(v);
 }
 static __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile(
@@ -64,7 +79,7 @@ static __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t 
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-static __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
+static __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
         "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
