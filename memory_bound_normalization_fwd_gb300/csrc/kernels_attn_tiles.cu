@@ -72,6 +72,12 @@ __device__ __forceinline__ uint32_t power_half2(int e) {
 }
 // The lowest n bits (n below 0: none, above 32: all).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// True for one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
 // The loading warpgroup's own barrier.
 __device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -455,51 +461,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     } else {
         // ---- matrix instructions
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (w == 12 && lane == 0 && sl.rows) {
+        if (w == 12 && sl.rows) {  // all lanes go through it together, one issues
         constexpr uint32_t s_shape = mma_shape(128, kStep, false), o_shape = mma_shape(128, C::D, true);
+        const bool leader = elect_one();
         bool ok = true;
-        auto scores = [&](int q, int step, int stage) {
-            const uint32_t a = smem + C::Q + q * C::MATRIX, b = smem + C::K + stage * C::MATRIX + step * kStep * 128;
-#pragma unroll
-            for (int k = 0; k < C::D / 16; ++k) {
-                const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                tc_mma(tmem + q * 128 + step * 64, smem_matrix(a + off, 16, 1024), smem_matrix(b + off, 16, 1024), s_shape, k > 0);
-            }
-            tc_commit(bar(kSFull + q * 2 + step));
+        // Matrices by their first piece; others are a number of 16 bytes on.
+        const uint64_t q_at = smem_matrix(smem + C::Q, 16, 1024), k_at = smem_matrix(smem + C::K, 16, 1024);
+        const uint64_t v_at = smem_matrix(smem + C::V, 16384, 1024);
+        auto commit = [&](int i) {
+            if (leader) tc_commit(bar(i));
         };
-        ok = mbar_wait_bounded(bar(kKFull), 0, tp.limit);
+        auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity, tp.limit)); };
+        auto scores = [&](int q, int step, int stage) {
+            const uint64_t a = q_at + q * (C::MATRIX / 16), b = k_at + stage * (C::MATRIX / 16) + step * (kStep * 128 / 16);
+            const uint32_t d = tmem + q * 128 + step * 64;
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < C::D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+                    tc_mma(d, a + off, b + off, s_shape, k > 0);
+                }
+                tc_commit(bar(kSFull + q * 2 + step));
+            }
+        };
+        ok = wait(kKFull, 0);
         if (ok) {
             tc_fence_after();
             for (int step = 0; step < 2; ++step)
                 for (int q = 0; q < halves; ++q) scores(q, step, 0);
-            tc_commit(bar(kKFree));
+            commit(kKFree);
         }
         for (int u = 0; ok && u < 2 * tiles; ++u) {
             const int t = u >> 1, step = u & 1, stage = t & 1;
-            if (step == 0) ok = mbar_wait_bounded(bar(kVFull + stage), (t >> 1) & 1, tp.limit);
+            if (step == 0) ok = wait(kVFull + stage, (t >> 1) & 1);
             for (int q = 0; ok && q < halves; ++q) {
-                ok = mbar_wait_bounded(bar(kPFull + q * 2 + step), t & 1, tp.limit);
+                ok = wait(kPFull + q * 2 + step, t & 1);
                 if (!ok) break;
                 tc_fence_after();
                 // V: 64 values of head_dim a row of 128 bytes; 16 tokens are 2048 bytes on
-                const uint32_t v = smem + C::V + stage * C::MATRIX + step * kStep * 128;
+                const uint64_t v = v_at + stage * (C::MATRIX / 16) + step * (kStep * 128 / 16);
+                const uint32_t from = tmem + q * 128 + step * 64, d = tmem + 256 + q * 128;
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kStep / 16; ++k)
-                    tc_mma_tmem(tmem + 256 + q * 128, tmem + q * 128 + step * 64 + k * 8, smem_matrix(v + k * 2048, 16384, 1024),
-                                o_shape, u > 0 || k > 0);
-                tc_commit(bar(kOFree + q));
-                if (step == 1 && q == halves - 1) tc_commit(bar(kVFree + stage));
+                    for (int k = 0; k < kStep / 16; ++k) tc_mma_tmem(d, from + k * 8, v + k * 128, o_shape, u > 0 || k > 0);
+                    tc_commit(bar(kOFree + q));
+                }
+                if (step == 1 && q == halves - 1) commit(kVFree + stage);
                 if (t + 1 < tiles) {
-                    if (step == 0 && q == 0) ok = mbar_wait_bounded(bar(kKFull + (stage ^ 1)), ((t + 1) >> 1) & 1, tp.limit);
+                    if (step == 0 && q == 0) ok = wait(kKFull + (stage ^ 1), ((t + 1) >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     scores(q, step, stage ^ 1);
-                    if (step == 1 && q == halves - 1) tc_commit(bar(kKFree + (stage ^ 1)));
+                    if (step == 1 && q == halves - 1) commit(kKFree + (stage ^ 1));
                 }
             }
         }
-        if (!ok) atomicOr(p.late, 1u);
-        tc_commit(bar(kDone));
+        if (!ok && leader) atomicOr(p.late, 1u);
+        commit(kDone);
         mbar_wait_bounded(bar(kDone), 0, tp.limit);  // nothing of it is on its way when the memory is freed
         }
     }
