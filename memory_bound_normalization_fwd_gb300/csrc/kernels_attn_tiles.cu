@@ -12,10 +12,11 @@
 //
 // Who does what, in a CTA of 16 warps: two warpgroups of softmax (a thread a row, each with 128
 // rows of its own), one warpgroup that looks up, loads and converts the tiles (into two stages of
-// K and of V), and a thread that issues the matrix instructions. A tile is taken in two steps of
-// 64 tokens. S takes 64 columns of tensor memory for either half and step, and P goes over it as the
-// second product's first operand; o takes head_dim columns. While a half's softmax is in one
-// step, the products of the other step run: P V of the last tile, then S of the next.
+// K and of V), and two warps that issue the matrix instructions, one for either half (one for both
+// took longer over them than they run: prompts' chunks 361 us). The softmax takes a tile in two
+// steps of 64 tokens. S takes 128 columns of tensor memory for either half, and P goes over it as the
+// second product's first operand; o takes head_dim columns. While one half is in its softmax the
+// other half's products run.
 // Bound: the matrix instructions (two products of 128 x 128 x head_dim a half and tile), next to
 // the exponentials and the conversion, each about half of that time.
 //
@@ -112,22 +113,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     auto bar = [&](int i) { return smem_u32(bars + i); };
     constexpr int kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPFull = 12, kOFree = 16, kDone = 18;
     if (w == 0) tmem_alloc(smem_u32(&tmem_at));
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kKFull + i), 128);
-            mbar_init(bar(kVFull + i), 128);
-            mbar_init(bar(kKFree + i), 1);
-            mbar_init(bar(kVFree + i), 1);
-            mbar_init(bar(kOFree + i), 1);
-        }
-        for (int i = 0; i < 4; ++i) {  // half * 2 + step
-            mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPFull + i), 128);
-        }
-        mbar_init(bar(kDone), 1);
-        late.clear();
-        fence_mbar_init();
-    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -138,6 +123,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     plan.tile_shift = 7;
     const Slot sl = slot_of<2 * kHalf>(p, plan, Sequences{nullptr, nullptr}, slot);
     const int halves = sl.rows > kHalf ? 2 : 1, tiles = sl.tiles;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kKFull + i), 128);
+            mbar_init(bar(kVFull + i), 128);
+            mbar_init(bar(kKFree + i), halves);
+            mbar_init(bar(kVFree + i), halves);
+            mbar_init(bar(kOFree + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(bar(kSFull + i), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(kPFull + i), 128);  // half * 2 + step
+        mbar_init(bar(kDone), halves);
+        late.clear();
+        fence_mbar_init();
+    }
 
     // ---- q, by the softmax threads: a row each
     float row_scale = 0.f;
@@ -207,8 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             bool ok = true;
             for (int u = 0; u < 2 * tiles; ++u) {
                 const int t = u >> 1, step = u & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kSFull + half * 2 + step), t & 1, tp.limit));
-                if (!ok) break;
+                if (step == 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kSFull + half), t & 1, tp.limit));
+                    if (!ok) break;
+                }
                 tc_fence_after();
                 const uint32_t s_at = lanes + half * 128 + step * 64;
                 uint32_t v[64];
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                         for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - above);
                     }
                     if (u > 0) {
-                        // (with two steps the product before the last may still be on its way)
+                        // (S came behind the last tile's products; step 0's may be on its way)
                         ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kOFree + half), (u - 1) & 1, tp.limit));
                         if (!ok) break;
                         tc_fence_after();
@@ -383,22 +384,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             // A piece of codes as fp16 into the matrix at `to`.
             auto convert = [&](uint32_t to, int k, const uint4& c, uint32_t f) {
                 const int i = tid + 128 * k, tok = i / CH, part = i - tok * CH;
-                const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+                // Lanes of the upper half of a row's pieces write theirs in another order: eight lanes
+                // write to eight different columns of 16 bytes.
+                const bool upper = part >= CH / 2 && C::BLOCKS == 2 && GD == 4;
+                const uint32_t word[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z, upper ? c.y : c.w};
                 if (E4) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t h[4];
                         pairs_e4m3(word[2 * j], h[0], h[1]);
                         pairs_e4m3(word[2 * j + 1], h[2], h[3]);
-                        store_piece(to + piece_at(tok, part * 2 + j), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
+                        store_piece(to + piece_at(tok, part * 2 + (j ^ (upper ? 1 : 0))), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
                     }
                 } else {
 #pragma unroll
-                    for (int j0 = 0; j0 < 4; ++j0) {
-                        const int j = j0;
+                    for (int j = 0; j < 4; ++j) {
                         uint32_t h[4];
                         pairs_e2m1(word[j], h[0], h[1], h[2], h[3]);
-                        store_piece(to + piece_at(tok, part * 4 + j), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
+                        store_piece(to + piece_at(tok, part * 4 + (j ^ (upper ? 2 : 0))), mul2(h[0], f), mul2(h[1], f), mul2(h[2], f), mul2(h[3], f));
                     }
                 }
             };
@@ -461,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     } else {
         // ---- matrix instructions
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (w == 12 && sl.rows) {  // all lanes go through it together, one issues
-        constexpr uint32_t s_shape = mma_shape(128, kStep, false), o_shape = mma_shape(128, C::D, true);
+        const int q = w - 12;  // the half
+        if (q < halves && sl.rows) {  // all lanes go through it together, one issues
+        constexpr uint32_t s_shape = mma_shape(128, kTile, false), o_shape = mma_shape(128, C::D, true);
         const bool leader = elect_one();
         bool ok = true;
         // Matrices by their first piece; others are a number of 16 bytes on.
@@ -472,48 +476,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             if (leader) tc_commit(bar(i));
         };
         auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity, tp.limit)); };
-        auto scores = [&](int q, int step, int stage) {
-            const uint64_t a = q_at + q * (C::MATRIX / 16), b = k_at + stage * (C::MATRIX / 16) + step * (kStep * 128 / 16);
-            const uint32_t d = tmem + q * 128 + step * 64;
+        auto scores = [&](int stage) {
+            const uint64_t a = q_at + q * (C::MATRIX / 16), b = k_at + stage * (C::MATRIX / 16);
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < C::D / 16; ++k) {
                     const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
-                    tc_mma(d, a + off, b + off, s_shape, k > 0);
+                    tc_mma(tmem + q * 128, a + off, b + off, s_shape, k > 0);
                 }
-                tc_commit(bar(kSFull + q * 2 + step));
+                tc_commit(bar(kSFull + q));
+                tc_commit(bar(kKFree + stage));
             }
         };
         ok = wait(kKFull, 0);
         if (ok) {
             tc_fence_after();
-            for (int step = 0; step < 2; ++step)
-                for (int q = 0; q < halves; ++q) scores(q, step, 0);
-            commit(kKFree);
+            scores(0);
         }
         for (int u = 0; ok && u < 2 * tiles; ++u) {
             const int t = u >> 1, step = u & 1, stage = t & 1;
             if (step == 0) ok = wait(kVFull + stage, (t >> 1) & 1);
-            for (int q = 0; ok && q < halves; ++q) {
-                ok = wait(kPFull + q * 2 + step, t & 1);
+            ok = ok && wait(kPFull + q * 2 + step, t & 1);
+            if (!ok) break;
+            tc_fence_after();
+            // V: 64 values of head_dim a row of 128 bytes; 16 tokens are 2048 bytes on
+            const uint64_t v = v_at + stage * (C::MATRIX / 16) + step * (kStep * 128 / 16);
+            const uint32_t from = tmem + q * 128 + step * 64, d = tmem + 256 + q * 128;
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < kStep / 16; ++k) tc_mma_tmem(d, from + k * 8, v + k * 128, o_shape, u > 0 || k > 0);
+                tc_commit(bar(kOFree + q));
+            }
+            if (step == 1) commit(kVFree + stage);
+            if (step == 1 && t + 1 < tiles) {
+                ok = wait(kKFull + (stage ^ 1), ((t + 1) >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                // V: 64 values of head_dim a row of 128 bytes; 16 tokens are 2048 bytes on
-                const uint64_t v = v_at + stage * (C::MATRIX / 16) + step * (kStep * 128 / 16);
-                const uint32_t from = tmem + q * 128 + step * 64, d = tmem + 256 + q * 128;
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k) tc_mma_tmem(d, from + k * 8, v + k * 128, o_shape, u > 0 || k > 0);
-                    tc_commit(bar(kOFree + q));
-                }
-                if (step == 1 && q == halves - 1) commit(kVFree + stage);
-                if (t + 1 < tiles) {
-                    if (step == 0 && q == 0) ok = wait(kKFull + (stage ^ 1), ((t + 1) >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(q, step, stage ^ 1);
-                    if (step == 1 && q == halves - 1) commit(kKFree + (stage ^ 1));
-                }
+                scores(stage ^ 1);
             }
         }
         if (!ok && leader) atomicOr(p.late, 1u);
