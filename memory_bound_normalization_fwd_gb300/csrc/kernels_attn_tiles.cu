@@ -71,6 +71,11 @@ __device__ __forceinline__ uint32_t power_half2(int e) {
     const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
     return h | h << 16;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // The lowest n bits (n below 0: none, above 32: all).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 // True for one lane of the warp.
@@ -244,8 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 const float less = shift - m;
                 float most = -INFINITY;
                 tmem_loaded(v);
+                const f2 factor2 = f2_dup(factor), less2 = f2_dup(less);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), factor, less));
+                for (int e = 0; e < 64; e += 2) {
+                    const float2 x = f2_get(f2_fma(f2_make(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), factor2, less2));
+                    v[e] = __float_as_uint(x.x);
+                    v[e + 1] = __float_as_uint(x.y);
+                }
                 if (masked) {
                     const uint32_t s0 = there0 & bits_below(lim - t0) & ~bits_below(low - t0);
                     const uint32_t s1 = there1 & bits_below(lim - t0 - 32) & ~bits_below(low - t0 - 32);
@@ -253,8 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                     for (int e = 0; e < 64; ++e)
                         if (!(((e < 32 ? s0 : s1) >> (e & 31)) & 1u)) v[e] = 0xff800000u;
                 }
+                float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 64; ++e) most = fmaxf(most, __uint_as_float(v[e]));
+                for (int e = 0; e < 64; e += 4) {
+                    m0 = max3(m0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    m1 = max3(m1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                }
+                most = fmaxf(m0, m1);
                 const float above = most - shift;
                 const bool grow = started ? above > 8.f : most > -INFINITY;
                 if (__any_sync(0xffffffffu, grow || far > 6)) {
@@ -278,16 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                         scale_sums(f);
                     }
                 }
-                float s0 = 0.f, s1 = 0.f;
+                f2 s0 = 0, s1 = 0;
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
                     const float px = exp2_fast(__uint_as_float(v[e])), py = exp2_fast(__uint_as_float(v[e + 1]));
-                    s0 += px;
-                    s1 += py;
+                    if (e & 2) s1 = f2_add(s1, f2_make(px, py));
+                    else s0 = f2_add(s0, f2_make(px, py));
                     v[e / 2] = half2_bits(px, py);
                 }
                 tmem_store32(s_at, v);
-                l = fmaf(s0 + s1, power(ref - b), l);
+                l = fmaf(f2_sum(f2_add(s0, s1)), power(ref - b), l);
                 tmem_stored();
                 tc_fence_before();
                 mbar_arrive(bar(kPFull + half * 2 + step));
