@@ -224,11 +224,23 @@ __device__ __forceinline__ float load_value(const void* p, int64_t i, int dtype)
     if (NP == 2) return load1<kFP32>(p, i);
     return dtype == kBF16 ? load1<kBF16>(p, i) : load1<kFP16>(p, i);
 }
+// Values d and d + 1 of a row at `at` (of D; `vec`: rows start on vectors' borders).
 template <int NP>
-__device__ __forceinline__ void store_value(void* p, int64_t i, float v, int dtype) {
-    if (NP == 2) store1<kFP32>(p, i, v);
-    else if (dtype == kBF16) store1<kBF16>(p, i, v);
-    else store1<kFP16>(p, i, v);
+__device__ __forceinline__ void store_two(void* p, int64_t at, int d, float a, float b, int D, bool vec, int dtype) {
+    if (d >= D) return;
+    if (vec && d + 2 <= D) {
+        if (NP == 2) *reinterpret_cast<float2*>(static_cast<float*>(p) + at + d) = make_float2(a, b);
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at + d) =
+            dtype == kBF16 ? Codec<kBF16>::pack2(a, b) : Codec<kFP16>::pack2(a, b);
+        return;
+    }
+    for (int k = 0; k < 2; ++k) {
+        if (d + k >= D) return;
+        const float v = k ? b : a;
+        if (NP == 2) store1<kFP32>(p, at + d + k, v);
+        else if (dtype == kBF16) store1<kBF16>(p, at + d + k, v);
+        else store1<kFP16>(p, at + d + k, v);
+    }
 }
 
 template <int F, int GD, int NT, int NP>
@@ -428,39 +440,61 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             const int i = live ? divide(sl.r0 + rr, r.g_mul, r.g_shift) : 0;
             const int qh = head * p.G + (live ? sl.r0 + rr - i * p.G : 0);
             const int64_t at = (sl.row0 + i) * p.q.st + qh * p.q.sh;
+            // the values of K that the lane gets in two instructions of a group, four each
             float v[GD][8];
             float top = 0.f;
+            if (r.vec_q && p.D == DP) {  // no branch: a row past the block's takes the first one's values, times 0
+                const unsigned char* src = static_cast<const unsigned char*>(p.q.p) + at * (NP == 2 ? 4 : 2);
+                if (NP == 2) {
 #pragma unroll
-            for (int grp = 0; grp < GD; ++grp) {
-                // the values of K that the lane gets in two instructions, four each
+                    for (int k = 0; k < KS; ++k) {
+                        const int d = (k >> 1) * 32 + (E4 ? (k & 1) * 16 + t4 * 4 : t4 * 8 + (k & 1) * 4);
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(src + d * 4));
+                        float* to = &v[k >> 1][(k & 1) * 4];
+                        to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w;
+                    }
+                } else {
+                    uint2 u[KS];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int d = grp * 32 + (E4 ? k * 16 + t4 * 4 : t4 * 8 + k * 4);
-                    float* to = &v[grp][k * 4];
-                    if (live && r.vec_q && d + 4 <= p.D) {
-                        const unsigned char* src = static_cast<const unsigned char*>(p.q.p) + (at + d) * (NP == 2 ? 4 : 2);
-                        if (NP == 2) {
-                            const float4 f = __ldg(reinterpret_cast<const float4*>(src));
-                            to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w;
-                        } else {
-                            const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-                            const float2 a = unpack16(u.x, p.dtype == kBF16), b = unpack16(u.y, p.dtype == kBF16);
+                    for (int k = 0; k < KS; ++k) {
+                        const int d = (k >> 1) * 32 + (E4 ? (k & 1) * 16 + t4 * 4 : t4 * 8 + (k & 1) * 4);
+                        u[k] = __ldg(reinterpret_cast<const uint2*>(src + d * 2));
+                    }
+                    const bool bf16 = p.dtype == kBF16;
+                    if (bf16) {
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            const float2 a = unpack16(u[k].x, true), b = unpack16(u[k].y, true);
+                            float* to = &v[k >> 1][(k & 1) * 4];
                             to[0] = a.x, to[1] = a.y, to[2] = b.x, to[3] = b.y;
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            to[e] = live && d + e < p.D ? load_value<NP>(p.q.p, at + d + e, p.dtype) : 0.f;
+                        for (int k = 0; k < KS; ++k) {
+                            const float2 a = unpack16(u[k].x, false), b = unpack16(u[k].y, false);
+                            float* to = &v[k >> 1][(k & 1) * 4];
+                            to[0] = a.x, to[1] = a.y, to[2] = b.x, to[3] = b.y;
+                        }
                     }
                 }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const int d = (k >> 1) * 32 + (E4 ? (k & 1) * 16 + t4 * 4 : t4 * 8 + (k & 1) * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[k >> 1][(k & 1) * 4 + e] = live && d + e < p.D ? load_value<NP>(p.q.p, at + d + e, p.dtype) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int grp = 0; grp < GD; ++grp)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[grp][e]));
-            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             int ex = static_cast<int>(__float_as_uint(top) >> 23);
             ex = top == 0.f ? 141 : ex < 15 ? 15 : ex;  // both powers stay normal
-            const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+            const float up = live ? __uint_as_float(static_cast<uint32_t>(268 - ex) << 23) : 0.f;
             const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23) * (p.scale * 1.4426950408889634f);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -803,6 +837,75 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             stage ^= 1;
         }
 
+        const bool whole = !r.split || (begin <= slot_begin && before[slot + 1] <= end);
+        // begun before this CTA: its part 2x; begun here and unfinished: 2x + 1
+        const int part = 2 * x + (r.split && begin <= slot_begin ? 1 : 0);
+        if (r.split && begin <= slot_begin && hblock == 0 && threadIdx.x == 0)
+            r.entries[slot] = make_int4(whole ? -1 : x | (before[slot + 1] - 1) / share << 16, sl.row0, sl.r0, sl.rows);
+        // the sums in v's own scale: times 2^(ref - 127 - LIFT), in two factors, which stay normal
+#pragma unroll
+        for (int grp = 0; grp < GD; ++grp) {
+            const int ex = static_cast<int>((ref[grp >> 2][grp & 1] >> (grp & 2) * 8) & 0xffffu) - 127 - C::LIFT;
+            const float f1 = power(ex >> 1), f2_ = power(ex - (ex >> 1));
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] = acc[grp][k][nt][e] * f1 * f2_;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+            }
+        }
+        // ---- a warp that has its head to itself writes from its registers: lanes of a row lie side
+        // by side, four values each (two and two with 8-bit codes)
+        if (r.wph == 1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = nt * 8 + 2 * t4 + e;
+                    if (row >= sl.rows) continue;
+                    const float L = l[nt][e], M = limit[nt][e] == kNegInf ? kNegInf : base[nt][e];
+                    if (!whole) {
+                        const int64_t at_part = (static_cast<int64_t>(part) * p.heads + head) * R + row;
+                        if (g == 0) r.ml[at_part] = make_float2(M, L);
+                        float* to = r.o + at_part * DP + (E4 ? 2 : 4) * g;
+#pragma unroll
+                        for (int grp = 0; grp < GD; ++grp) {
+                            const float(&a)[4] = acc[grp][0][nt], (&b)[4] = acc[grp][1][nt];
+                            if (E4) {
+                                *reinterpret_cast<float2*>(to + grp * 32) = make_float2(a[e], a[2 + e]);
+                                *reinterpret_cast<float2*>(to + grp * 32 + 16) = make_float2(b[e], b[2 + e]);
+                            } else {
+                                *reinterpret_cast<float4*>(to + grp * 32) = make_float4(a[e], a[2 + e], b[e], b[2 + e]);
+                            }
+                        }
+                        continue;
+                    }
+                    const int i = divide(sl.r0 + row, r.g_mul, r.g_shift), qh = head * p.G + sl.r0 + row - i * p.G;
+                    const int64_t out_row = sl.row0 + i, at = out_row * p.out.st + qh * p.out.sh;
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                    for (int grp = 0; grp < GD; ++grp) {
+                        const float v0 = acc[grp][0][nt][e] * inv, v1 = acc[grp][0][nt][2 + e] * inv;
+                        const float v2 = acc[grp][1][nt][e] * inv, v3 = acc[grp][1][nt][2 + e] * inv;
+                        const int d = grp * 32 + (E4 ? 2 : 4) * g;
+                        store_two<NP>(p.out.p, at, d, v0, v1, p.D, r.vec_out, p.dtype);
+                        store_two<NP>(p.out.p, at, d + (E4 ? 16 : 2), v2, v3, p.D, r.vec_out, p.dtype);
+                    }
+                    if (p.lse && g == 0)
+                        p.lse[out_row * p.heads_q + qh] = L == 0.f ? kNegInf : (M + log2f(L)) * 0.6931471805599453f;
+                }
+            }
+            continue;
+        }
         // ---- the warps of a head are joined, and the result or the part of it is written
         float* mine = reinterpret_cast<float*>(ring);  // [R][DP + 4], then maxima and sums
         float* ml = mine + R * (DP + 4);
@@ -810,23 +913,16 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[nt][e];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = nt * 8 + 2 * t4 + e;
                 if (g == 0) {
                     ml[row] = limit[nt][e] == kNegInf ? kNegInf : base[nt][e];
-                    ml[R + row] = sum;
+                    ml[R + row] = l[nt][e];
                 }
 #pragma unroll
                 for (int grp = 0; grp < GD; ++grp) {
-                    // 2^(ref - 127 - LIFT) in two factors, which stay normal
-                    const int ex = static_cast<int>((ref[grp >> 2][grp & 1] >> (grp & 2) * 8) & 0xffffu) - 127 - C::LIFT;
-                    const float f1 = power(ex / 2), f2_ = power(ex - ex / 2);
                     float* to = mine + row * (DP + 4) + grp * 32;
-                    const float2 lo = make_float2(acc[grp][0][nt][e] * f1 * f2_, acc[grp][0][nt][2 + e] * f1 * f2_);
-                    const float2 hi = make_float2(acc[grp][1][nt][e] * f1 * f2_, acc[grp][1][nt][2 + e] * f1 * f2_);
+                    const float2 lo = make_float2(acc[grp][0][nt][e], acc[grp][0][nt][2 + e]);
+                    const float2 hi = make_float2(acc[grp][1][nt][e], acc[grp][1][nt][2 + e]);
                     if (E4) {
                         *reinterpret_cast<float2*>(to + g * 2) = lo;
                         *reinterpret_cast<float2*>(to + 16 + g * 2) = hi;
@@ -836,13 +932,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 }
             }
         }
-        if (r.wph == 1) __syncwarp();  // a warp has its head to itself
-        else __syncthreads();
-        const bool whole = !r.split || (begin <= slot_begin && before[slot + 1] <= end);
-        // begun before this CTA: its part 2x; begun here and unfinished: 2x + 1
-        const int part = 2 * x + (r.split && begin <= slot_begin ? 1 : 0);
-        if (r.split && begin <= slot_begin && hblock == 0 && threadIdx.x == 0)
-            r.entries[slot] = make_int4(whole ? -1 : x | (before[slot + 1] - 1) / share << 16, sl.row0, sl.r0, sl.rows);
+        __syncthreads();
         // a head's warps take its rows in turn
         const float* from = reinterpret_cast<const float*>(sm + r.at_ring + head_local * r.ring);
         const int stride = r.hb * r.ring / 4;  // to the next warp of the head
@@ -882,18 +972,14 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
 #pragma unroll
             for (int c = 0; c < (DP <= 128 ? 1 : 2); ++c) {
                 const int d = lane * 4 + c * 128;
-                const float v[4] = {o[c].x, o[c].y, o[c].z, o[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (d + e < p.D)
-                        store_value<NP>(p.out.p, out_row * p.out.st + qh * p.out.sh + d + e, L == 0.f ? 0.f : v[e] * inv,
-                                        p.dtype);
+                const int64_t at = out_row * p.out.st + qh * p.out.sh;
+                store_two<NP>(p.out.p, at, d, o[c].x * inv, o[c].y * inv, p.D, r.vec_out, p.dtype);
+                store_two<NP>(p.out.p, at, d + 2, o[c].z * inv, o[c].w * inv, p.D, r.vec_out, p.dtype);
             }
             if (p.lse && lane == 0)
                 p.lse[out_row * p.heads_q + qh] = L == 0.f ? kNegInf : (M + log2f(L)) * 0.6931471805599453f;
         }
-        if (r.wph == 1) __syncwarp();
-        else __syncthreads();  // the rings are free again
+        __syncthreads();  // the rings are free again
         if (r.narrow) {   // and what lies behind a token's codes is zero again
             for (int i = lane; i < 2 * C::STAGE / 16; i += 32)
                 reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);

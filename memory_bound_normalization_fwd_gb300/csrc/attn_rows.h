@@ -29,6 +29,7 @@ struct RowsPlan {
     int narrow;       // codes are copied by 4 bytes (heads that are not whole groups)
     int vec_scales;   // a head's scale bytes are read at once
     int vec_q;        // rows of q are read by vectors
+    int vec_out;      // rows of out are written in pairs
     int ring;         // bytes of a warp's ring (also room for its results)
     int at_q, at_factors, at_ring, at_plan;  // offsets in shared memory
     int smem;

@@ -266,6 +266,7 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     r->vec_scales = p.groups == r->gd && scales % 8 == 0;
     const int64_t eb = elem_bytes(p.dtype), e = vec_elems(p.dtype);
     r->vec_q = aligned16(p.q.p) && (p.rows <= 1 || p.q.st % e == 0) && (p.heads_q <= 1 || p.q.sh % e == 0) && eb > 0;
+    r->vec_out = aligned16(p.out.p) && (p.rows <= 1 || p.out.st % 2 == 0) && (p.heads_q <= 1 || p.out.sh % 2 == 0);
     // q's operands of a CTA's heads lie in shared memory where registers do not hold them
     const int q = r->nt == 1 && pieces == 1 ? 0 : pieces * 2 * r->gd * r->nt * 256;
     const int room = r->gd > 4 ? 32768 : 65536;
