@@ -1002,8 +1002,7 @@ cudaError_t launch_rows(const AttnP& p, RowsPlan r, const OpCfg& c) {
     while ((C::TOK * r.wph) >> (r.tile_shift + 1)) ++r.tile_shift;  // wph is a power of two
     r.smem = r.at_plan + (r.split ? (r.slots + 1 + 2 * static_cast<int>(p.sequences) + 1) * 4 : 0);
     if (r.smem + 1024 > c.dev.max_smem_optin) return cudaErrorInvalidConfiguration;
-    const cudaError_t e =
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, c.dev.max_smem_optin - 1024);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), c.dev.max_smem_optin - 1024);
     if (e != cudaSuccess) return e;
     return op_launch(c, fn, static_cast<int64_t>(r.gx) * r.head_blocks, warps * 32, r.smem, p, r);
 }

@@ -42,6 +42,9 @@ struct RowsPlan {
 
 constexpr int kSplitSlots = 1024;  // most slots (and sequences) of a call that is dealt out evenly
 
+// Allows a kernel `smem` bytes of shared memory on the current device, once.
+cudaError_t allow_smem(const void* kernel, int smem);
+
 // The row kernels by format and type; attn_join puts the parts of split slots together.
 cudaError_t attn_rows_e2m1(const AttnP& p, const RowsPlan& r, const OpCfg& c);
 cudaError_t attn_rows_e2m1_fp32(const AttnP& p, const RowsPlan& r, const OpCfg& c);

@@ -7,6 +7,9 @@
 #include "row_ring_host.h"
 
 #include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
 
 namespace rmsn {
 
@@ -270,15 +273,29 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     // q's operands of a CTA's heads lie in shared memory where registers do not hold them
     const int q = r->nt == 1 && pieces == 1 ? 0 : pieces * 2 * r->gd * r->nt * 256;
     const int room = r->gd > 4 ? 32768 : 65536;
-    r->hb = divisor_up_to(p.heads, q ? std::max(1, std::min(8, room / q)) : 8);
-    r->wph = 8 / r->hb;
-    r->head_blocks = p.heads / r->hb;
+    const int most_heads = q ? std::max(1, std::min(8, room / q)) : 8;
+    r->hb = divisor_up_to(p.heads, most_heads);
     const int64_t slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
     if (p.rows * p.G >= (int64_t(1) << 30) || p.sequences >= (int64_t(1) << 30)) return false;  // counted in 32 bits
     r->slots = static_cast<int>(slots);
     // (the sum of all slots' tiles, of 16 tokens at least, is counted in 32 bits too)
     r->split = slots <= kSplitSlots && p.sequences <= kSplitSlots &&
                slots * (r->most_tokens / 16 + 2) < (int64_t(1) << 31);
+    // Where a slot has few tokens whatever the lengths (by the table's width, or the window), a CTA
+    // takes all of them, with its warps side by side, and nothing is left to join; fewer heads a
+    // CTA where there would be fewer CTAs than two an SM. (GB300, us, 4 sequences of up to 509
+    // tokens, 8 heads: 10.7, so 7.5; 17 of five queries in a window of 1000, 5 heads: 29.7, so 21.2.)
+    const int64_t tile = (p.format == RMSNORM_CACHE_E2M1 && r->gd <= 4 ? 32 : 16) * 8;
+    const int64_t rows_seen = r->window ? static_cast<int64_t>(r->window) + 8 * r->nt : INT32_MAX;
+    if (std::min<int64_t>(r->most_tokens, rows_seen) <= 4 * tile + 64) {
+        r->split = 0;
+        int hb = r->hb;
+        while (hb > 1 && slots * (p.heads / hb) < 2 * c.dev.sm_count) hb = divisor_up_to(p.heads, hb - 1);
+        r->hb = hb;
+    }
+    r->wph = 8 / r->hb;
+    while (r->wph & (r->wph - 1)) --r->wph;  // a power of two
+    r->head_blocks = p.heads / r->hb;
     int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
     if (c.max_ctas > 0) ctas = std::min<int64_t>(ctas, c.max_ctas);
     ctas = std::min<int64_t>(ctas, 32767);  // a slot's first and last CTA share a word
@@ -321,6 +338,19 @@ bool tiles_ok(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel, int smem) {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> guard(mu);
+    if (done.count({dev, kernel})) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.insert({dev, kernel});
+    return e;
+}
 
 cudaError_t attn_join(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
     // Parts a slot on average; many are joined by eight warps.

@@ -548,7 +548,7 @@ template <int F, int GD>
 cudaError_t launch_tiles(const AttnP& p, const TilesP& tp, const OpCfg& c) {
     auto fn = attn_tiles_kernel<F, GD>;
     const int smem = Tiles<GD>::SMEM;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     return op_launch(c, fn, static_cast<int64_t>(tp.slots) * p.heads, kThreads, smem, p, tp);
 }
