@@ -697,7 +697,7 @@ int rmsnorm_rope_axes_bwd(const rmsnorm_rope_args_t* args, const rmsnorm_rope_ax
  *
  * Products are exact (codes and q in 16 bits or split into such), sums and softmax
  * statistics are held in fp32; probabilities are rounded to 11 bits for 16-bit outputs and
- * to 22 bits for fp32, with a floor: p * (scale of the token's group of v) is kept to
+ * to 22 bits for fp32, with a floor: p * (largest scale of the token's v) is kept to
  * 2^-33 of the sequence's largest such scale.
  *   cu_rows  [sequences + 1] int32, not decreasing, from 0; NULL: one row a sequence
  *            (rows == sequences)

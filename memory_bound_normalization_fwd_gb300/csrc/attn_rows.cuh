@@ -8,9 +8,14 @@
 // brought near 2^15 by a power of two, so that fp16 holds bf16 and fp16 values exactly but for those
 // 2^-28 below the row's largest; fp32 in two pieces of 11 bits), and the scale is a factor on
 // fp32 sums: 16 tokens x 8 rows of a group in four instructions per lane instead of one per
-// value. For V the scale goes to the probabilities, o[d, r] += c[t, d] * (2^b[t, g] p[t, r]), per
-// group, relative to the group's largest scale so far and times 2^8: 22 powers of two below the
-// largest are full fp16 values, 32 are kept in part.
+// value. For V the token's largest scale goes to the probabilities,
+//   o[d, r] += (c[t, d] 2^(b[t, g] - b[t] + C)) * (2^(b[t] - B + 8) p[t, r])
+// relative to the largest scale B so far, where 22 powers of two below the largest are full fp16
+// values and 32 are kept in part; what the groups of a token differ by goes to the codes, by
+// packed fp16 products (exact down to 2^-(C + 15) of the token's largest scale, kept in part
+// to 2^-(C + 24); C is 6 for 8-bit codes, 12 for 4-bit ones). (A scale per group on the
+// probabilities took a conversion and a transposition for every group and block of 8 rows: one
+// key head of 256 values in 8 bits, 16 rows, 52.6 us.)
 // Both products take the codes as the first operand (16 tokens x 16 values of K; 16 values
 // x 16 tokens of V) and 8 rows as the second, so a row costs an eighth of an instruction and no
 // lane idles for 8 rows. A token's probabilities for the second product come from the first one's
@@ -129,6 +134,12 @@ __device__ __forceinline__ void load_factors(float (&f)[FP], const float* from) 
         }
     }
 }
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ bool at_there(uint32_t there, int lane) { return (there >> lane) & 1u; }
 // 2^e as fp32, 0 below 2^-126 (e <= 127).
 __device__ __forceinline__ float power(int e) { return __uint_as_float(e < -126 ? 0u : static_cast<uint32_t>(e + 127) << 23); }
 
@@ -212,7 +223,8 @@ struct Rows {
         return 2 * STAGE > results ? 2 * STAGE : results;
     }
     static __host__ __device__ constexpr int q_bytes() { return QREG ? 0 : NP * KS * NT * 32 * 8; }
-    static __host__ __device__ constexpr int factor_bytes() { return 2 * TOK * FP * 4; }
+    static constexpr int CODE = E4 ? 6 : 12;  // C above
+    static __host__ __device__ constexpr int factor_bytes() { return TOK * FP * 4 + TOK * 4 + (GD + 1) / 2 * 2 * TOK * 2; }
 };
 
 // A 16-bit pair of the call's type.
@@ -539,13 +551,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         // base: what scores are taken relative to (0 before a row has seen a token); limit: where
         // above it a score moves it (2^4; -infinity before)
         float acc[GD][2][NT][4], base[NT][2], limit[NT][2], l[NT][2];
-        // scale bytes of v, as the factors take them: the largest so far, and the most that it
-        // serves for
-        uint32_t ref[W][2], most[W][2];
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) ref[i][h] = 0, most[i][h] = 0x00030003u;
+        uint32_t ref = 0, most = 3;  // v's largest scale byte so far, and the most that it serves for
 #pragma unroll
         for (int grp = 0; grp < GD; ++grp)
 #pragma unroll
@@ -562,26 +568,46 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         int stage = 0;
         for (int tile = first; tile < last; ++tile) {
             const uint32_t there = there_next;
-            // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT), 0 where that is
-            // below 2^-126. Two groups at a time, in halves of 16 bits.
+            // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT), b the token's largest
+            // byte, and 2^(the group's byte - b + CODE) in fp16. Two groups at a time, in halves of 16 bits.
             uint32_t bad = 0;  // groups of this lane's token whose v is not a number
             {
-                float kf[FP], vf[FP];
-                uint32_t x[W][2], y[W][2];  // bytes 0 and 2, and 1 and 3, of k's and v's scales
-                uint32_t much = 0;
+                constexpr uint32_t kBoth = 0x00010001u;
+                uint32_t x[W][2], y[W][2], e[W][2];  // bytes 0 and 2, and 1 and 3, of k's and v's scales
+                uint32_t kmax = 0, vmax = 0;
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         x[i][h] = (sk[i] >> (8 * h)) & 0x00ff00ffu;
                         y[i][h] = (sv[i] >> (8 * h)) & 0x00ff00ffu;
-                        // more than 2^3 above the largest so far, or not a number
-                        much |= __vmaxu2(y[i][h], most[i][h]) ^ most[i][h];
-                        much |= __vmaxu2(x[i][h], 0x00fe00feu) ^ 0x00fe00feu;
+                        kmax = __vmaxu2(kmax, x[i][h]);
+                        vmax = __vmaxu2(vmax, y[i][h]);
                     }
                 }
+                uint32_t b = max(vmax & 0xffffu, vmax >> 16);
+                // a byte - b + CODE + 15 as fp16's exponent, at least 0 (a bias of 256 keeps the
+                // halves apart)
+                uint32_t least = 0xffffffffu;
+                auto exponents = [&]() {
+                    least = 0xffffffffu;
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            e[i][h] = __vmaxu2(y[i][h] + kBoth * (256 + C::CODE + 15) - kBoth * b, kBoth * 256) - kBoth * 256;
+                            // (groups that are not there do not count)
+                            const int g0 = i * 4 + h;
+                            least = __vminu2(least, e[i][h] | (g0 < GD ? 0u : 0xffffu) | (g0 + 2 < GD ? 0u : 0xffff0000u));
+                        }
+                };
+                exponents();
                 uint32_t odd = 0;  // groups whose k is not a number
-                if (__any_sync(0xffffffffu, much != 0)) {
+                const bool rare = b > most || (least & 0xffffu) == 0 || least < 0x10000u || (kmax & 0xffffu) == 255u ||
+                                  kmax >= 0xff0000u;
+                const bool slow = __any_sync(0xffffffffu, rare && at_there(there, lane));
+                if (slow) {
+                    b = 0;
 #pragma unroll
                     for (int grp = 0; grp < GD; ++grp) {
                         const int i = grp >> 2, h = grp & 1, sh = (grp & 2) * 8;
@@ -590,41 +616,47 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                             bad |= 1u << grp;
                             y[i][h] &= ~(0xffffu << sh);
                         }
-                        const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, (y[i][h] >> sh) & 0xffffu));
-                        const int have = static_cast<int>((ref[i][h] >> sh) & 0xffffu);
-                        if (top > have + 3) {  // the sums move to the new largest scale
-                            const float f = power(have - top);
-                            ref[i][h] += static_cast<uint32_t>(top - have) << sh;
-                            most[i][h] = (most[i][h] & ~(0xffffu << sh)) | static_cast<uint32_t>(min(top + 3, 254)) << sh;
+                        b = max(b, (y[i][h] >> sh) & 0xffffu);
+                    }
+                    exponents();
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, b);
+                    if (top > ref + 3) {  // the sums move to the new largest scale
+                        const float f = power(static_cast<int>(ref) - static_cast<int>(top));
+                        ref = top;
+                        most = min(top + 3, 254u);
+#pragma unroll
+                        for (int grp = 0; grp < GD; ++grp)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] *= f;
-                        }
+                                    for (int q = 0; q < 4; ++q) acc[grp][k][nt][q] *= f;
                     }
-                }
-#pragma unroll
-                for (int grp = 0; grp < FP; ++grp) {
-                    const int i = grp >> 2, h = grp & 1;
-                    if (i >= W) {
-                        kf[grp] = vf[grp] = 0.f;
-                        continue;
-                    }
-                    // b - ref + LIFT + 127 as an exponent, at least 0 (a bias of 512, which the shift
-                    // to the exponent's place drops, keeps the halves apart)
-                    const uint32_t e = __vmaxu2(y[i][h] + (0x02000200u + 0x00010001u * (C::LIFT + 127) - ref[i][h]), 0x02000200u);
-                    kf[grp] = __uint_as_float(grp & 2 ? (x[i][h] & 0xffff0000u) << 7 : x[i][h] << 23);
-                    vf[grp] = __uint_as_float(grp & 2 ? (e & 0xffff0000u) << 7 : e << 23);
-                    if (odd >> grp & 1u) kf[grp] = __uint_as_float(0x7fc00000u);
                 }
                 if (lane < TOK) {
+                    float kf[FP];
+                    uint16_t* hf = reinterpret_cast<uint16_t*>(factors + TOK * FP + TOK) + lane;
 #pragma unroll
-                    for (int k = 0; k < FP; k += 2) {
-                        *reinterpret_cast<float2*>(factors + lane * FP + k) = make_float2(kf[k], kf[k + 1]);
-                        *reinterpret_cast<float2*>(factors + (TOK + lane) * FP + k) = make_float2(vf[k], vf[k + 1]);
+                    for (int grp = 0; grp < FP; ++grp) {
+                        const int i = grp >> 2, h = grp & 1;
+                        kf[grp] = 0.f;
+                        if (i >= W || grp >= GD) continue;
+                        kf[grp] = __uint_as_float(grp & 2 ? (x[i][h] & 0xffff0000u) << 7 : x[i][h] << 23);
+                        uint32_t half = (grp & 2 ? e[i][h] >> 16 : e[i][h] & 0xffffu) << 10;
+                        if (slow) {
+                            if (odd >> grp & 1u) kf[grp] = __uint_as_float(0x7fc00000u);
+                            // below fp16's normal values
+                            const int low = static_cast<int>(y[i][h] >> (grp & 2) * 8 & 0xffffu) - static_cast<int>(b) + C::CODE;
+                            if (low < -14) half = low >= -24 ? 1u << (low + 24) : 0u;
+                        }
+                        hf[grp * TOK] = static_cast<uint16_t>(half);
                     }
+#pragma unroll
+                    for (int k = 0; k < FP; k += 2)
+                        *reinterpret_cast<float2*>(factors + lane * FP + k) = make_float2(kf[k], kf[k + 1]);
+                    const int ex = static_cast<int>(b) - static_cast<int>(ref) + C::LIFT + 127;
+                    factors[TOK * FP + lane] = __uint_as_float(static_cast<uint32_t>(max(ex, 0)) << 23);
                 }
             }
             if (tile + 1 < last) {
@@ -792,9 +824,21 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             // ---- sums of v
 #pragma unroll
             for (int mt = 0; mt < TM; ++mt) {
-                float fa[FP], fb[FP];
-                load_factors<FP>(fa, factors + (TOK + mt * 16 + g) * FP);
-                load_factors<FP>(fb, factors + (TOK + mt * 16 + 8 + g) * FP);
+                const float fa = factors[TOK * FP + mt * 16 + g], fb = factors[TOK * FP + mt * 16 + 8 + g];
+                uint2 b[NT], b2[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 x = make_float2(s[mt][nt][0] * fa, s[mt][nt][1] * fa);
+                    const float2 y = make_float2(s[mt][nt][2] * fb, s[mt][nt][3] * fb);
+                    const uint32_t h0 = half2_bits(x.x, x.y), h1 = half2_bits(y.x, y.y);
+                    b[nt] = make_uint2(transposed(h0), transposed(h1));
+                    if (NP == 2) {
+                        const float2 hx = half2_values(h0), hy = half2_values(h1);
+                        b2[nt] = make_uint2(transposed(half2_bits(x.x - hx.x, x.y - hx.y)),
+                                            transposed(half2_bits(y.x - hy.x, y.y - hy.y)));
+                    }
+                }
+                const uint16_t* hf = reinterpret_cast<const uint16_t*>(factors + TOK * FP + TOK) + mt * 16 + 2 * t4;
                 uint32_t c[4];
 #pragma unroll
                 for (int grp = 0; grp < GD; ++grp) {
@@ -815,20 +859,21 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                         pairs_e2m1(even, a[0][0], a[1][0], a[0][2], a[1][2]);
                         pairs_e2m1(odd, a[0][1], a[1][1], a[0][3], a[1][3]);
                     }
+                    // the group's scale beside the token's, of tokens 2 t4 and the next, and 8 on
+                    const uint32_t f0 = *reinterpret_cast<const uint32_t*>(hf + grp * TOK);
+                    const uint32_t f1 = *reinterpret_cast<const uint32_t*>(hf + grp * TOK + 8);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        a[k][0] = mul2(a[k][0], f0), a[k][1] = mul2(a[k][1], f0);
+                        a[k][2] = mul2(a[k][2], f1), a[k][3] = mul2(a[k][3], f1);
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float2 x = make_float2(s[mt][nt][0] * fa[grp], s[mt][nt][1] * fa[grp]);
-                        const float2 y = make_float2(s[mt][nt][2] * fb[grp], s[mt][nt][3] * fb[grp]);
-                        const uint32_t h0 = half2_bits(x.x, x.y), h1 = half2_bits(y.x, y.y);
-                        const uint2 b = make_uint2(transposed(h0), transposed(h1));
-                        mma(acc[grp][0][nt], a[0], b);
-                        mma(acc[grp][1][nt], a[1], b);
+                        mma(acc[grp][0][nt], a[0], b[nt]);
+                        mma(acc[grp][1][nt], a[1], b[nt]);
                         if (NP == 2) {
-                            const float2 hx = half2_values(h0), hy = half2_values(h1);
-                            const uint2 b2 = make_uint2(transposed(half2_bits(x.x - hx.x, x.y - hx.y)),
-                                                        transposed(half2_bits(y.x - hy.x, y.y - hy.y)));
-                            mma(acc[grp][0][nt], a[0], b2);
-                            mma(acc[grp][1][nt], a[1], b2);
+                            mma(acc[grp][0][nt], a[0], b2[nt]);
+                            mma(acc[grp][1][nt], a[1], b2[nt]);
                         }
                     }
                 }
@@ -842,18 +887,17 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         const int part = 2 * x + (r.split && begin <= slot_begin ? 1 : 0);
         if (r.split && begin <= slot_begin && hblock == 0 && threadIdx.x == 0)
             r.entries[slot] = make_int4(whole ? -1 : x | (before[slot + 1] - 1) / share << 16, sl.row0, sl.r0, sl.rows);
-        // the sums in v's own scale: times 2^(ref - 127 - LIFT), in two factors, which stay normal
+        // the sums in v's own scale: times 2^(ref - 127 - LIFT - CODE), in two factors, which stay normal
+        const int ex = static_cast<int>(ref) - 127 - C::LIFT - C::CODE;
+        const float f1 = power(ex >> 1), f2_ = power(ex - (ex >> 1));
 #pragma unroll
-        for (int grp = 0; grp < GD; ++grp) {
-            const int ex = static_cast<int>((ref[grp >> 2][grp & 1] >> (grp & 2) * 8) & 0xffffu) - 127 - C::LIFT;
-            const float f1 = power(ex >> 1), f2_ = power(ex - (ex >> 1));
+        for (int grp = 0; grp < GD; ++grp)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[grp][k][nt][e] = acc[grp][k][nt][e] * f1 * f2_;
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

@@ -61,11 +61,6 @@ __device__ __forceinline__ uint32_t piece_at(int row, int c) {
 __device__ __forceinline__ void store_piece(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // 2^e as a pair of fp16, 0 below 2^-24 (e <= 15).
 __device__ __forceinline__ uint32_t power_half2(int e) {
     const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;

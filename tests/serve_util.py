@@ -9,13 +9,17 @@ finfo.eps / 2 = 2^-11 (a step is 2^-10 in [1, 2)), for 16-bit outputs; for fp32 
 operators. Numerator and denominator both carry the score's error, so an output is
 within (r + 2 * (4e-6 * S + TAU)) * sum p |v| and half a step of its dtype.
 
-Floor. A probability goes into the product in fp16 as p * 2^(b - B + 8), b the scale byte of
-the token's group and B the group's largest so far; below 2^-14 its rounding is no
+Floor. A probability goes into the product in fp16 as p * 2^(b - B + 8), b the token's largest
+scale byte (of a head) and B the largest so far; below 2^-14 its rounding is no
 longer relative but half of fp16's smallest value, 2^-25. In v's units that is 2^-25 *
 2^(B - 127 - 8) * |code| for a token, and the sum of p, which divides it, is at least 1 (the
 maximum's own p). B is at most the largest byte of the sequence's tokens, so an output may be off by
 2^-33 * 2^(largest byte - 127) * sum |code| over the tokens seen. It shows where the tokens of
 large p have the code 0: (p 2^-23 beside a token of p 1 and code 0 keeps 10 bits).
+v goes into it as code * 2^(group's byte - b + C), C = 6 for 8-bit codes (whose last bit is at least
+2^-9) and 12 for 4-bit ones (2^-1): exact while the last bit is at least 2^-24, that is for groups within
+2^21 (2^35) of the token's largest; below it is off by 2^-25, and groups beyond 2^-(C + 24) are
+left out, which is at most 448 * 2^-31 < 2^-22 (6 * 2^-37 < 2^-34) of 2^(b - 127) for a token.
 """
 from __future__ import annotations
 
@@ -104,7 +108,10 @@ def attention(cache, q, table, lengths, cu, scale, causal, window):
             o[lost], z[lost] = torch.nan, torch.nan
             out[rows_b, h], lse[rows_b, h] = torch.where(some[:, None], o, 0.0), z
             mag[rows_b, h] = p @ vv.nan_to_num(0.0).abs()
-            floor[rows_b, h] = 2.0 ** -33 * largest[h // G] * (seen @ cc)
+            top = scale_v[:, h // G].amax(-1, keepdim=True)
+            far = top * (scale_v[:, h // G] * 2.0 ** (21 if cache.fmt == "e4m3" else 35) < top)
+            floor[rows_b, h] = 2.0 ** -33 * largest[h // G].amax() * (seen @ cc) + \
+                2.0 ** (-22 if cache.fmt == "e4m3" else -34) * (p @ far)
             big = (scale * (qq.abs() @ kk.nan_to_num(0.0).abs().T)).abs()
             S[rows_b, h] = torch.where(see, big, 0.0).amax(-1)
     return out, lse, mag, S, floor
