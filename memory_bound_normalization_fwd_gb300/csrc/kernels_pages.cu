@@ -39,9 +39,8 @@ __device__ __forceinline__ void copy_bytes(uint8_t* to, const uint8_t* from, int
     }
 }
 
-// A whole page. Vectors of the four arrays are numbered through, four of a thread in
-// flight.
-constexpr int kInFlight = 4;
+// A page. Vectors of the four arrays are numbered through, `FLY` of a thread in flight.
+template <int FLY>
 __device__ __forceinline__ void copy_page(const PageBytes& b, int64_t from, int64_t to, int lane, int lanes) {
     if (!b.vectors) {
 #pragma unroll
@@ -51,13 +50,13 @@ __device__ __forceinline__ void copy_page(const PageBytes& b, int64_t from, int6
     }
     const int e0 = static_cast<int>(b.page[0] / 16), e1 = e0 + static_cast<int>(b.page[1] / 16);
     const int e2 = e1 + static_cast<int>(b.page[2] / 16), e3 = e2 + static_cast<int>(b.page[3] / 16);
-    for (int i0 = lane; i0 < e3; i0 += lanes * kInFlight) {
-        uint4 v[kInFlight];
-        uint8_t* base[kInFlight];
-        int64_t size[kInFlight];
-        int at[kInFlight];
+    for (int i0 = lane; i0 < e3; i0 += lanes * FLY) {
+        uint4 v[FLY];
+        uint8_t* base[FLY];
+        int64_t size[FLY];
+        int at[FLY];
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
+        for (int k = 0; k < FLY; ++k) {
             const int i = i0 + k * lanes;
             const int a = (i >= e0) + (i >= e1) + (i >= e2);
             base[k] = i < e3 ? (a == 0 ? b.p[0] : a == 1 ? b.p[1] : a == 2 ? b.p[2] : b.p[3]) : nullptr;
@@ -66,14 +65,15 @@ __device__ __forceinline__ void copy_page(const PageBytes& b, int64_t from, int6
             if (base[k]) v[k] = ld_stream(reinterpret_cast<const uint4*>(base[k] + from * size[k]) + at[k]);
         }
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k)
+        for (int k = 0; k < FLY; ++k)
             if (base[k]) st_stream(reinterpret_cast<uint4*>(base[k] + to * size[k]) + at[k], v[k]);
     }
 }
 
 // ---- copy ------------------------------------------------------------------------
 
-// A team of `team` threads (a warp or the CTA) takes a page at a time.
+// A team of `team` threads (a warp or the CTA) takes a page. One page a team: CTAs that come
+// free take the next ones (6000 pages of 17 KB, us: 1216 CTAs of as many pages each 36.4, so 33.8).
 __global__ void __launch_bounds__(256) copy_pages_kernel(const PagesP p, int team) {
     pdl_wait();
     pdl_launch_dependents();
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PagesP p, int tea
             if (lane == 0) report();
             continue;
         }
-        copy_page(p.bytes, from, to, lane, team);
+        copy_page<5>(p.bytes, from, to, lane, team);
     }
 }
 
@@ -336,11 +336,11 @@ __device__ __forceinline__ int bit_at(uint32_t mask, int k) {
 // Ranks and selections among the live pages. before[b]: live pages before the b-th 1024
 // (in shared memory).
 struct Ranks {
-    const uint2* words;
+    const uint2* words;  // in shared memory where they fit
     const int32_t* before;
     int blocks;
     __device__ __forceinline__ int64_t live_before(int64_t page) const {
-        const uint2 w = __ldg(words + (page >> 5));
+        const uint2 w = words[page >> 5];
         return before[page >> 10] + static_cast<int>(w.y) + __popc(w.x & ((1u << (page & 31)) - 1u));
     }
     // The k-th live (or free) page; there are more than k.
@@ -356,22 +356,22 @@ struct Ranks {
         const int r = static_cast<int>(k - at_block(lo));
         const uint2* w = words + lo * int64_t(32);
         auto at_word = [&](int i) {
-            const int v = static_cast<int>(__ldg(&w[i].y));
+            const int v = static_cast<int>(w[i].y);
             return LIVE ? v : i * 32 - v;
         };
         int a = 0;
 #pragma unroll
         for (int half = 16; half > 0; half >>= 1)
             if (at_word(a + half) <= r) a += half;
-        const uint32_t mask = __ldg(&w[a].x);
+        const uint32_t mask = w[a].x;
         return lo * int64_t(1024) + a * 32 + bit_at(LIVE ? mask : ~mask, r - at_word(a));
     }
 };
 
 // Moves, the counts and the table. With L live pages, `stay` of them below L: the i-th
 // move takes the (stay + i)-th live page to the i-th free one.
-__global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, int move_ctas) {
-    extern __shared__ int32_t before[];  // [blocks + 1]
+__global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, int move_ctas, int staged) {
+    extern __shared__ __align__(16) int32_t before[];  // [blocks + 1], behind it the words
     __shared__ int warp_sums[8];
     const LiveMap m = live_map(p.ws, p.pages);
     const int blocks = static_cast<int>((p.pages + 1023) / 1024), tid = threadIdx.x;
@@ -397,16 +397,28 @@ __global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, 
     }
     int all = 0;
     for (int w = 0; w < 8; ++w) all += warp_sums[w];
+    uint2* words = reinterpret_cast<uint2*>(before + (blocks + 4) / 4 * 4);
+    if (staged)
+        for (int i = tid; i < blocks * 32; i += 256) words[i] = m.words[i];
     __syncthreads();
     const int64_t L = all;
-    const Ranks r{m.words, before, blocks};
+    const Ranks r{staged ? words : m.words, before, blocks};
     const int64_t stay = L < p.pages ? r.live_before(L) : L, moves = L - stay;
     if (static_cast<int>(blockIdx.x) < move_ctas) {
+        // The CTA's next 256 moves are found by a thread each (by all threads for each one,
+        // the searches took longer than the copies).
+        __shared__ int64_t from[256], to[256];
         const int per = 256 / team, lane = tid & (team - 1);
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * per + tid / team; i < moves;
-             i += static_cast<int64_t>(move_ctas) * per) {
-            const int64_t from = r.select<true>(stay + i), to = r.select<false>(i);
-            copy_page(p.bytes, from, to, lane, team);
+        for (int64_t i0 = blockIdx.x; i0 < moves; i0 += static_cast<int64_t>(move_ctas) * 256) {
+            const int64_t i = i0 + static_cast<int64_t>(tid) * move_ctas;
+            __syncthreads();
+            if (i < moves) {
+                from[tid] = r.select<true>(stay + i);
+                to[tid] = r.select<false>(i);
+            }
+            __syncthreads();
+            for (int k = tid / team; k < 256 && i0 + static_cast<int64_t>(k) * move_ctas < moves; k += per)
+                copy_page<4>(p.bytes, from[k], to[k], lane, team);
         }
         return;
     }
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, 
     }
     if (p.refs_out != p.refs) {
         for (int64_t q = first; q < p.pages; q += step) {
-            const bool is_live = (__ldg(&m.words[q >> 5].x) >> (q & 31)) & 1u;
+            const bool is_live = (r.words[q >> 5].x >> (q & 31)) & 1u;
             if (is_live ? q < L : q >= L) p.refs_out[q] = p.refs[q];
         }
     }
@@ -431,7 +443,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, 
         int32_t page = p.table[e];
         if (page >= p.pages) {
             report();
-        } else if (page >= L && ((__ldg(&m.words[page >> 5].x) >> (page & 31)) & 1u)) {
+        } else if (page >= L && ((r.words[page >> 5].x >> (page & 31)) & 1u)) {
             page = static_cast<int32_t>(r.select<false>(r.live_before(page) - stay));
         }
         p.table_out[e] = page;
@@ -454,7 +466,8 @@ int64_t pages_ws_bytes(int64_t pages, int64_t sequences, int64_t n) {
 cudaError_t pages_copy_run(const PagesP& p, const OpCfg& c) {
     g_launched.store(true);
     const int team = team_of(p.bytes);
-    const int64_t G = persistent_grid(p.n, 256 / team, c.dev.sm_count, 8, c.max_ctas);
+    int64_t G = std::min<int64_t>((p.n + 256 / team - 1) / (256 / team), 1 << 24);
+    if (c.max_ctas > 0) G = std::min<int64_t>(G, c.max_ctas);
     return op_launch(c, copy_pages_kernel, G, 256, 0, p, team);
 }
 
@@ -476,7 +489,10 @@ cudaError_t pages_compact_run(const PagesP& p, const OpCfg& c) {
     cudaError_t e = op_launch(c, live_kernel, persistent_grid(blocks, 1, c.dev.sm_count, 2, c.max_ctas), 1024, 0, p);
     if (e != cudaSuccess) return e;
     const int team = team_of(p.bytes);
-    const int smem = static_cast<int>(blocks + 1) * 4;
+    // Up to 128 thousand pages: the words are searched in shared memory.
+    const int staged = blocks <= 128 ? 1 : 0;
+    const int smem = staged ? static_cast<int>((blocks + 4) / 4 * 4) * 4 + static_cast<int>(blocks) * 32 * 8
+                            : static_cast<int>(blocks + 1) * 4;
     if (smem > 48 * 1024) {  // always to the most, so that no call lowers it for another
         e = cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kMaxPages / 1024 + 1) * 4);
@@ -486,7 +502,7 @@ cudaError_t pages_compact_run(const PagesP& p, const OpCfg& c) {
     const int64_t move = persistent_grid((p.pages + 1) / 2, 256 / team, c.dev.sm_count, 7, c.max_ctas);
     const int64_t small = std::max(p.pages, p.sequences * p.width);
     const int64_t rest = persistent_grid(small, 256, c.dev.sm_count, 1, c.max_ctas);
-    return op_launch(c, compact_kernel, move + rest, 256, smem, p, team, static_cast<int>(move));
+    return op_launch(c, compact_kernel, move + rest, 256, smem, p, team, static_cast<int>(move), staged);
 }
 
 cudaError_t pages_status_read_and_clear(unsigned int* value) {
