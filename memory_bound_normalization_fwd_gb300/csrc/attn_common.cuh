@@ -18,6 +18,7 @@ constexpr int kGroup = 32;  // values that share a scale
 struct Sequence {
     int64_t row0;
     int64_t n, len;  // queries, tokens
+    int64_t held;    // tokens that the row of the table has room for
 };
 
 __device__ __forceinline__ int64_t first_row(const AttnP& p, int64_t b) {
@@ -32,7 +33,8 @@ __device__ __forceinline__ Sequence sequence(const AttnP& p, int64_t b) {
     const int64_t end = first_row(p, b + 1);
     s.n = end > s.row0 ? end - s.row0 : 0;
     const int64_t len = __ldg(p.lengths + b), most = p.width * p.page_size;
-    s.len = len < 0 ? 0 : len > most ? most : len;
+    s.len = len < 0 ? 0 : len;
+    s.held = s.len < most ? s.len : most;
     return s;
 }
 
@@ -44,7 +46,7 @@ struct Seen {
 __device__ __forceinline__ Seen seen(const AttnP& p, const Sequence& s, int64_t i) {
     const int64_t pos = s.len - s.n + i;
     Seen r;
-    r.high = p.causal ? pos + 1 : s.len;
+    r.high = p.causal && pos + 1 < s.held ? pos + 1 : s.held;
     r.low = p.window && pos + 1 > p.window ? pos + 1 - p.window : 0;
     if (r.high < 0) r.high = 0;
     return r;

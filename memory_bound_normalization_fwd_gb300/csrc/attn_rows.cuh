@@ -147,6 +147,7 @@ __device__ __forceinline__ float power(int e) { return __uint_as_float(e < -126 
 // and tiles are below 2^31.)
 struct Slot {
     int b, row0, n, len;  // the sequence, its first row, its rows and tokens
+    int held;             // tokens that the row of the table has room for
     int r0;               // first row of the block among the sequence's (queries times G)
     int rows;             // 0: no such slot
     int low, high;        // tokens that any of its rows sees
@@ -191,6 +192,7 @@ __device__ __forceinline__ Slot slot_of(const AttnP& p, const RowsPlan& r, const
     s.row0 = q.row(p, lo);
     s.n = max(q.row(p, lo + 1) - s.row0, 0);
     s.len = q.length(p, lo);
+    s.held = min(s.len, r.most_tokens);
     const int first = s.row0 * p.G / R + lo, all = s.n * p.G;
     s.r0 = (slot - first) * R;
     s.rows = s.low = s.high = s.tile0 = s.tiles = 0;
@@ -199,7 +201,7 @@ __device__ __forceinline__ Slot slot_of(const AttnP& p, const RowsPlan& r, const
     int unused;
     seen32(p, r, s.n, s.len, divide(s.r0, r.g_mul, r.g_shift), s.low, unused);
     seen32(p, r, s.n, s.len, divide(s.r0 + s.rows - 1, r.g_mul, r.g_shift), unused, s.high);
-    s.high = min(s.high, s.len);
+    s.high = min(s.high, s.held);
     s.tile0 = s.low >> r.tile_shift;
     s.tiles = s.high > s.low ? ((s.high - 1) >> r.tile_shift) + 1 - s.tile0 : 1;
     return s;
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         int* lens = rows + p.sequences + 1;
         for (int b = threadIdx.x; b <= p.sequences; b += threads) {
             rows[b] = static_cast<int>(first_row(p, b));
-            if (b < p.sequences) lens[b] = min(max(__ldg(p.lengths + b), 0), r.most_tokens);
+            if (b < p.sequences) lens[b] = max(__ldg(p.lengths + b), 0);
         }
         seq = Sequences{rows, lens};
         __syncthreads();
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         if (r.split && before[slot] >= end) break;
         const Slot sl = slot_of<R>(p, r, seq, slot);
         if (sl.rows == 0) continue;
+        if (sl.len > sl.held && threadIdx.x == 0) atomicOr(p.status, 1u);  // tokens past the table's row
         int first = 0, last = sl.tiles, slot_begin = 0;
         if (r.split) {
             slot_begin = before[slot];
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 if (cr < sl.rows) {
                     int from, to;
                     seen32(p, r, sl.n, sl.len, divide(sl.r0 + cr, r.g_mul, r.g_shift), from, to);
-                    lim[nt][e] = max(min(to, sl.len) - base_token, 0);
+                    lim[nt][e] = max(min(to, sl.held) - base_token, 0);
                     low[nt][e] = max(from - base_token, 0);
                     min_lim = min(min_lim, lim[nt][e]);
                     max_low = max(max_low, low[nt][e]);

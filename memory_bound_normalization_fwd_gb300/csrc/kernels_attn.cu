@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(128) attn_generic_kernel(const AttnP p) {
             }
             return __half2float(__ushort_as_half(static_cast<unsigned short>(pair))) * f;
         };
-        for (int64_t t = see.low + w; t < see.high && t < s.len; t += 4) {
+        if (s.len > s.held && threadIdx.x == 0) atomicOr(p.status, 1u);
+        for (int64_t t = see.low + w; t < see.high; t += 4) {
             int64_t head = token_at(p, b, t);
             if (head < 0) {
                 if (lane == 0) atomicOr(p.status, 1u);

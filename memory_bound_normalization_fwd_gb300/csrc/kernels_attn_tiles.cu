@@ -84,7 +84,7 @@ __device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;"
 
 struct TilesP {
     int slots;
-    int window;
+    int window, most_tokens;
     uint32_t g_mul, page_mul, pages;
     int g_shift, page_shift;
     long long limit;  // of a wait, in cycles
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
     plan.g_mul = tp.g_mul;
     plan.g_shift = tp.g_shift;
     plan.tile_shift = 7;
+    plan.most_tokens = tp.most_tokens;
     const Slot sl = slot_of<2 * kHalf>(p, plan, Sequences{nullptr, nullptr}, slot);
     const int halves = sl.rows > kHalf ? 2 : 1, tiles = sl.tiles;
     if (threadIdx.x == 0) {
@@ -138,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
         fence_mbar_init();
     }
 
+    if (sl.rows && sl.len > sl.held && threadIdx.x == 0) atomicOr(p.status, 1u);  // tokens past the table's row
+
     // ---- q, by the softmax threads: a row each
     float row_scale = 0.f;
     int lim = 0, low = 0;  // tokens that the row sees
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             qh = head * p.G + sl.r0 + rr - i * p.G;
             int to;
             seen32(p, plan, sl.n, sl.len, i, low, to);
-            lim = min(to, sl.len);
+            lim = min(to, sl.held);
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + out_row * p.q.st + qh * p.q.sh);
 #pragma unroll
             for (int k = 0; k < C::D / 8; ++k) {
@@ -527,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
         }
         if (!ok && leader) atomicOr(p.late, 1u);
         commit(kDone);
-        mbar_wait_bounded(bar(kDone), 0, tp.limit);  // nothing of it is on its way when the memory is freed
+        // nothing of it is on its way when the memory is freed (two seconds, whatever the call's limit)
+        mbar_wait_bounded(bar(kDone), 0, 4000000000LL);
         }
     }
     __syncwarp();
@@ -563,6 +567,7 @@ cudaError_t attn_tiles(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
     TilesP tp;
     tp.slots = static_cast<int>(p.rows * p.G / (2 * kHalf) + p.sequences);
     tp.window = r.window;
+    tp.most_tokens = r.most_tokens;
     tp.g_mul = r.g_mul;
     tp.g_shift = r.g_shift;
     tp.page_mul = r.page_mul;

@@ -1,6 +1,10 @@
 """Attention over the quantised cache against the plain 64-bit implementation."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +15,7 @@ from memory_bound_normalization_fwd_gb300 import binding as B
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 VARIANTS = ("generic", "auto")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _cu(counts):
@@ -283,10 +288,63 @@ def test_pages_that_are_not_there():
     cache, table = _filled([64, 64, 64], 16, 2, 64, "e2m1", 13)
     table[0][1], table[1][0] = -1, cache.pages
     _run(cache, table, [64, 64, 64], [1, 2, 1], 4, torch.bfloat16, status=-12)
-    # tokens behind the row of the table are left out; the call reports nothing past it
+    # lengths of nothing, and below
     out, _ = B.cache_attention(cache, _q(3, 4, 64, torch.bfloat16, 0), _i32(table), _i32([0, 0, -5]))
     assert bool((out == 0).all())
     assert B.rmsnorm_check_device_status(0) == 0
+
+
+@pytest.mark.parametrize("D,heads,G,counts", [(64, 2, 2, [3, 1]), (512, 2, 2, [3, 1]), (128, 8, 8, [310, 200])])
+def test_tokens_past_the_row_of_the_table(D, heads, G, counts):
+    """A length that the row has no room for: the positions are the true ones, the tokens past the
+    row are left out and reported."""
+    held = [400, 200]
+    cache, table = _filled(held, 16, heads, D, "e2m1", 5, width=25)
+    _run(cache, table, [440, 200], counts, heads * G, torch.bfloat16, 1, status=-12, variants=("auto",))
+    _run(cache, table, [440, 200], counts, heads * G, torch.bfloat16, 1, status=-12, variants=("auto",), window=60)
+    _run(cache, table, [400, 200], counts, heads * G, torch.bfloat16, 1, variants=("auto",))
+
+
+def test_a_wait_that_runs_out():
+    """Waits of the tensor cores' roles on one another, with no time to wait: the status says so, and the
+    next call is whole."""
+    heads, G, lens = 8, 8, [600, 500]
+    cache, table = _filled(lens, 16, heads, 128, "e4m3", 2)
+    q = _q(1100, heads * G, 128, torch.bfloat16, 3)
+    args = (cache, q, _i32(table), _i32(lens))
+    cu = _i32([0, 600, 1100])
+    ref, _ = B.cache_attention(*args, cu_q=cu)
+    B.cache_attention(*args, cu_q=cu, wait_limit_ns=1)
+    assert B.lib().rmsnorm_check_device_status(0) == -7
+    assert B.lib().rmsnorm_check_device_status(0) == 0
+    again, _ = B.cache_attention(*args, cu_q=cu)
+    assert torch.equal(ref, again) and B.lib().rmsnorm_check_device_status(0) == 0
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+from memory_bound_normalization_fwd_gb300 import binding as B
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+for rows, heads in ((2, 4), (2400, 32)):
+    c = B.Cache(200, 16, 4, 64, "e2m1")
+    c.k_scales.fill_(127), c.v_scales.fill_(127), c.v_codes.fill_(0x22)
+    n = rows // 2
+    q = torch.randn(rows, heads, 64, device="cuda").to(torch.bfloat16)
+    t, ln, cu = i32([list(range(100)), list(range(100, 200))]), i32([1500, 1400]), i32([0, n, rows])
+    ws = torch.empty(1 << 27, dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        B.cache_attention(c, q, t, ln, cu_q=cu, out=out, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert bool((out == 1).all()), out
+""" % ROOT
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr[-2000:]
 
 
 def test_slots_past_32_bits():
