@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         const int run0 = min(static_cast<int>(threadIdx.x) * run, r.slots), run1 = min(run0 + run, r.slots);
         int own = 0;
         for (int i = run0; i < run1; ++i) {
-            const int n = slot_of<R>(p, r, seq, i).tiles;
+            // a slot's start counts as some tiles: what a CTA spends on another slot beside its tiles
+            const int tiles = slot_of<R>(p, r, seq, i).tiles, n = tiles ? tiles + r.start_tiles : 0;
             before[i + 1] = n;
             own += n;
         }
@@ -354,9 +355,10 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         if (sl.len > sl.held && threadIdx.x == 0) atomicOr(p.status, 1u);  // tokens past the table's row
         int first = 0, last = sl.tiles, slot_begin = 0;
         if (r.split) {
-            slot_begin = before[slot];
+            slot_begin = before[slot] + r.start_tiles;
             first = max(begin - slot_begin, 0);
             last = min(before[slot + 1], end) - slot_begin;
+            if (first >= last) continue;  // only a part of its start
         }
         first += sl.tile0;
         last += sl.tile0;

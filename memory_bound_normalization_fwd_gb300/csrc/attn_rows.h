@@ -17,6 +17,7 @@ struct RowsPlan {
     int head_blocks;  // heads / hb
     int slots;        // at least the slots of the call: rows * G / (8 nt) + sequences
     int gx;           // CTAs a head block
+    int start_tiles;  // tiles that a slot's start counts as in the runs
     int split;        // 1: equal runs of tiles; 0: whole slots, one after another
     int tile_shift;   // tokens of a tile, as a power of two
     int most_tokens;  // that a row of the table has room for (below 2^31)

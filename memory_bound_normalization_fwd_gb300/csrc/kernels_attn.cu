@@ -281,7 +281,7 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     r->slots = static_cast<int>(slots);
     // (the sum of all slots' tiles, of 16 tokens at least, is counted in 32 bits too)
     r->split = slots <= kSplitSlots && p.sequences <= kSplitSlots &&
-               slots * (r->most_tokens / 16 + 2) < (int64_t(1) << 31);
+               slots * (r->most_tokens / 16 + 8) < (int64_t(1) << 31);
     // Where a slot has few tokens whatever the lengths (by the table's width, or the window), a CTA
     // takes all of them, with its warps side by side, and nothing is left to join; fewer heads a
     // CTA where there would be fewer CTAs than two an SM. (GB300, us, 4 sequences of up to 509
@@ -295,6 +295,9 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
         r->hb = hb;
     }
     r->wph = 8 / r->hb;
+    // (GB300, us, at 0 / 3 / 5: 32 sequences of up to 8192 tokens, 8 heads 49.2 / 45.9 / 48.0, two of
+    // up to 131072, one head 53.1 / 46.6 / 45.3)
+    r->start_tiles = r->wph == 1 ? 3 : 5;
     while (r->wph & (r->wph - 1)) --r->wph;  // a power of two
     r->head_blocks = p.heads / r->hb;
     int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
@@ -329,13 +332,18 @@ cudaError_t status_words(AttnP* p) {
     return cudaSuccess;
 }
 
-// Whether the tensor cores take a call: enough rows of a key head a sequence to fill most of a
-// block of 256, and blocks for half of the SMs (fewer are split over the tokens by the row kernels).
+// Whether the tensor cores take a call. A wave of their blocks (one an SM, of up to 256 rows) costs
+// about as much as 6500 rows in the row kernels, which also split the tokens of few blocks.
+// (GB300, us, tensor cores / row kernels, 8 heads of 128 values in 4 bits, bf16, contexts of 4096:
+// 16 sequences of 64 rows 80 / 127, 64 of 32 rows 323 / 235, one of 512 rows 90 / 68, of 2048 90 / 195)
+constexpr int64_t kRowsOfAWave = 6500;
 bool tiles_ok(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
     if (p.dtype == kFP32 || p.D % 32 != 0 || p.groups < 2 || p.groups > 4 || r.narrow || !r.vec_q) return false;
-    const int64_t n = (p.rows + p.sequences - 1) / p.sequences * p.G;
-    const int64_t blocks = p.rows * p.G / 256 + p.sequences;
-    return n >= 128 && p.rows * p.G / 256 * p.heads >= c.dev.sm_count / 2 && blocks * p.heads < (int64_t(1) << 31);
+    const int64_t n = (p.rows + p.sequences - 1) / p.sequences * p.G;  // rows of a sequence, on average
+    const int64_t blocks = ((n + 255) / 256 * p.sequences) * p.heads;
+    const int64_t waves = (blocks + c.dev.sm_count - 1) / c.dev.sm_count;
+    return p.rows * p.G * p.heads >= kRowsOfAWave * waves &&
+           (p.rows * p.G / 256 + p.sequences) * p.heads < (int64_t(1) << 31);
 }
 
 }  // namespace
