@@ -1059,7 +1059,7 @@ cudaError_t launch_rows(const AttnP& p, RowsPlan r, const OpCfg& c) {
 template <int F, int NP, int GD>
 cudaError_t pick_rows(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
     if (r.nt == 1) return launch_rows<F, GD, 1, NP>(p, r, c);
-    if constexpr (GD <= 4) {
+    if constexpr (GD <= 3) {
         if (r.nt == 4) return launch_rows<F, GD, 4, NP>(p, r, c);
     }
     return launch_rows<F, GD, 2, NP>(p, r, c);

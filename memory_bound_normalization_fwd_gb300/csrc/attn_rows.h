@@ -11,7 +11,7 @@ namespace rmsn {
 // sequence; the CTAs of a head block take equal runs of all slots' tiles.
 struct RowsPlan {
     int gd;           // groups of a head that the kernel is made for: 2, 3, 4, 6 or 8, at least the cache's
-    int nt;           // 8 * nt rows a block: 1, 2, or 4 up to 4 groups
+    int nt;           // 8 * nt rows a block: 1, 2, or 4 up to 3 groups
     int hb;           // key heads of a CTA
     int wph;          // warps a key head, which take turns at the tokens of a tile
     int head_blocks;  // heads / hb

@@ -225,10 +225,15 @@ int divisor_up_to(int n, int most) {
     return d;
 }
 
+// Rows of a key head in a CTA, eights of them. 32 rows take about 1.7 times 16 rows' time, so they are
+// taken together where that leaves enough fewer CTAs; with more than 96 values a head they spill.
+// (GB300, us, 32 / 16 rows a CTA, 32 sequences, contexts of 8192, 8 heads, bf16: 32 rows of a head of
+// 64 values in 4 bits 111 / 125, of 128 values 224 / 196, in 8 bits 265 / 304; 40 rows 415 / 284, in
+// 8 bits 455 / 444, fp32 604 / 361; 17 sequences of 40 rows of 64 values, a window of 400, 21.5 / 11.5)
 int rows_nt(int64_t G, int64_t gd, int64_t sequences, int64_t rows) {
     // rows of a key head that a sequence has, on average
     const int64_t n = (rows + sequences - 1) / sequences * G;
-    return n <= 8 ? 1 : n <= 16 || gd > 4 ? 2 : 4;
+    return n <= 8 ? 1 : gd <= 3 && (n + 31) / 32 * 7 <= (n + 15) / 16 * 4 ? 4 : 2;
 }
 
 int rows_gd(int64_t D) {
@@ -272,11 +277,13 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     r->vec_q = aligned16(p.q.p) && (p.rows <= 1 || p.q.st % e == 0) && (p.heads_q <= 1 || p.q.sh % e == 0) && eb > 0;
     r->vec_out = aligned16(p.out.p) && (p.rows <= 1 || p.out.st % 2 == 0) && (p.heads_q <= 1 || p.out.sh % 2 == 0);
     // q's operands of a CTA's heads lie in shared memory where registers do not hold them
-    const int q = r->nt == 1 && pieces == 1 ? 0 : pieces * 2 * r->gd * r->nt * 256;
-    const int room = r->gd > 4 ? 32768 : 65536;
-    const int most_heads = q ? std::max(1, std::min(8, room / q)) : 8;
-    r->hb = divisor_up_to(p.heads, most_heads);
-    const int64_t slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
+    const auto most_heads = [&] {
+        const int q = r->nt == 1 && pieces == 1 ? 0 : pieces * 2 * r->gd * r->nt * 256;
+        const int room = r->gd > 4 ? 32768 : 65536;
+        return q ? std::max(1, std::min(8, room / q)) : 8;
+    };
+    r->hb = divisor_up_to(p.heads, most_heads());
+    int64_t slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
     if (p.rows * p.G >= (int64_t(1) << 30) || p.sequences >= (int64_t(1) << 30)) return false;  // counted in 32 bits
     r->slots = static_cast<int>(slots);
     // (the sum of all slots' tiles, of 16 tokens at least, is counted in 32 bits too)
@@ -284,12 +291,20 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
                slots * (r->most_tokens / 16 + 8) < (int64_t(1) << 31);
     // Where a slot has few tokens whatever the lengths (by the table's width, or the window), a CTA
     // takes all of them, with its warps side by side, and nothing is left to join; fewer heads a
-    // CTA where there would be fewer CTAs than two an SM. (GB300, us, 4 sequences of up to 509
-    // tokens, 8 heads: 10.7, so 7.5; 17 of five queries in a window of 1000, 5 heads: 29.7, so 21.2.)
+    // CTA where there would be fewer CTAs than two an SM. (GB300, us, split and
+    // joined / so: 4 sequences of up to 509 tokens, 8 heads 10.7 / 7.8; 17 of five queries in a window
+    // of 1000, 5 heads of 96 values, 32 rows a CTA 29.7 / 21.2)
     const int64_t tile = (p.format == RMSNORM_CACHE_E2M1 && r->gd <= 4 ? 32 : 16) * 8;
     const int64_t rows_seen = r->window ? static_cast<int64_t>(r->window) + 8 * r->nt : INT32_MAX;
     if (std::min<int64_t>(r->most_tokens, rows_seen) <= 4 * tile + 64) {
         r->split = 0;
+        // (8 rows a CTA where 16 would leave one CTA an SM: GB300, us, 8 / 16, sequences of five queries
+        // in a window of 1000, 5 heads: 17 of 20 rows of 96 values 15.4 / 26.6; 17 of 40 rows of 128
+        // values 27.8 / 29.4, 136 of them 139 / 173; 17 of 10 rows 17.2 / 15.1)
+        if (pieces == 1 && (r->gd == 3 || r->gd == 4)) r->nt = 1;
+        slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
+        r->slots = static_cast<int>(slots);
+        r->hb = divisor_up_to(p.heads, most_heads());
         int hb = r->hb;
         while (hb > 1 && slots * (p.heads / hb) < 2 * c.dev.sm_count) hb = divisor_up_to(p.heads, hb - 1);
         r->hb = hb;
@@ -335,7 +350,7 @@ cudaError_t status_words(AttnP* p) {
 // Whether the tensor cores take a call. A wave of their blocks (one an SM, of up to 256 rows) costs
 // about as much as 6500 rows in the row kernels, which also split the tokens of few blocks.
 // (GB300, us, tensor cores / row kernels, 8 heads of 128 values in 4 bits, bf16, contexts of 4096:
-// 16 sequences of 64 rows 80 / 127, 64 of 32 rows 323 / 235, one of 512 rows 90 / 68, of 2048 90 / 195)
+// 16 sequences of 64 rows 82 / 112, 64 of 32 rows 323 / 207, one of 512 rows 90 / 63, of 2048 90 / 190)
 constexpr int64_t kRowsOfAWave = 6500;
 bool tiles_ok(const AttnP& p, const RowsPlan& r, const OpCfg& c) {
     if (p.dtype == kFP32 || p.D % 32 != 0 || p.groups < 2 || p.groups > 4 || r.narrow || !r.vec_q) return false;
