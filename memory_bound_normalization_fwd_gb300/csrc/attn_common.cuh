@@ -11,8 +11,6 @@
 
 namespace rmsn {
 
-constexpr int kGroup = 32;  // values that share a scale
-
 // Sequence b of a call: its rows and tokens, kept within the call's arrays whatever the
 // device arrays hold.
 struct Sequence {

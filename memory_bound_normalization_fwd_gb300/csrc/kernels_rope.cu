@@ -174,7 +174,9 @@ struct Lane {
     }
     // kExchange: the sines come with the sign that the other value of the pair takes.
     // With several axes a pair's position comes from its axis: a lane's loads are a few
-    // neighbouring ones per unit, from L1.
+    // neighbouring ones per unit, from L1. (GB300, us, three axes / one: 16384 tokens of 40 heads of
+    // 128 bf16 without norms 60 / 58, 84% of the rate of a copy; backward of 16381 of 48 heads with norms
+    // 107 / 101, 84%; 64 tokens of 40 heads 3.4 / 2.9.)
     template <int SIGN, bool AXES>
     __device__ __forceinline__ void angles(const RopeP& p, const RopeUnits& g, int64_t b, int64_t s) {
         angles<SIGN, AXES>(p, g, b, s, AXES ? 0 : position_of(p, b, s));
