@@ -639,7 +639,8 @@ def _workspace(t, size, *key):
         if len(_sizes) >= 4096:  # ragged batches: as many sizes as lengths
             _sizes.clear()
         n = _sizes[(size, t.get_device(), key)] = size(*key)
-    return t.new_empty(n, dtype=torch.uint8)
+    # (torch.empty on a named device: 1.5 us on the host against 3.1 for new_empty)
+    return torch.empty(n, dtype=torch.uint8, device=t.device)
 
 
 def _given(workspace, device):
@@ -878,7 +879,7 @@ def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: dict | None = No
     """
     import torch
     if axes is not None:
-        if axes.in_turn or 2 * sum(axes.pairs) != rotary_dim:
+        if axes.in_turn or rotary_dim < 2 or 2 * sum(axes.pairs) != rotary_dim:
             raise ValueError(f"frequencies of the axes' own are for sections of {rotary_dim // 2} pairs "
                              f"together, got {axes.pairs}")
         own = [rope_steps(2 * n, base, scaling, device) for n in axes.pairs if n]
@@ -916,7 +917,8 @@ _NO_HEADS = (0, 0, 0, 0)
 
 def _new_heads(like, shape):
     """A new contiguous heads tensor and its struct values."""
-    t = like.new_empty(shape)
+    import torch
+    t = torch.empty(shape, dtype=like.dtype, device=like.device)
     if len(shape) == 3:
         H, D = shape[1], shape[2]
         return t, (t.data_ptr(), 0, H * D, D)
@@ -1006,12 +1008,12 @@ def rope_fwd(q, k, steps, positions=None, w_q=None, w_k=None, interleaved: bool 
         else:
             ko = _heads(k_out, "k_out", kshape, dtype, dev)
         if rstd and w_k is not None:
-            b = k.new_empty(kshape[:-1], dtype=torch.float32)
+            b = torch.empty(kshape[:-1], dtype=torch.float32, device=k.device)
             bp = b.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     if rstd and w_q is not None:
-        a = q.new_empty(shape[:-1], dtype=torch.float32)
+        a = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
         ap = a.data_ptr()
     args = _ROPE.pack(*head, ap, bp, eps, offset, magnitude, 0.0, *qh, *kh, *qo, *ko)
     opts = _opt(make_options(**options)) if options else None
@@ -1056,7 +1058,7 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
     if w_q is not None:
         ap = _vector(rstd_q, "rstd_q", shape[:-1].numel(), f32, dev)
         qh = _heads(q, "q", shape, dtype, dev)
-        dwq = dq_out.new_empty(D, dtype=f32)
+        dwq = torch.empty(D, dtype=f32, device=dq_out.device)
         wqp = dwq.data_ptr()
     if dk_out is not None:
         kshape = dk_out.shape
@@ -1068,7 +1070,7 @@ def rope_bwd(dq_out, dk_out, steps, positions=None, q=None, k=None, rstd_q=None,
         if w_k is not None:
             bp = _vector(rstd_k, "rstd_k", kshape[:-1].numel(), f32, dev)
             kh = _heads(k, "k", kshape, dtype, dev)
-            dwk = dq_out.new_empty(D, dtype=f32)
+            dwk = torch.empty(D, dtype=f32, device=dq_out.device)
             wkp = dwk.data_ptr()
     elif dk is not None:
         raise ValueError("dk without dk_out")
@@ -1245,7 +1247,7 @@ def cache_attention(cache: Cache, q, table, lengths, cu_q=None, scale: float | N
         oh = _heads(out, "out", shape, dtype, dev)
     kept, kp = None, 0
     if lse:
-        kept = q.new_empty(shape[:2], dtype=torch.float32)
+        kept = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
         kp = kept.data_ptr()
     if scale is None:
         scale = cache.head_dim ** -0.5
@@ -1355,10 +1357,10 @@ def cache_compact(cache: Cache, refs, table, refs_out=None, table_out=None, work
     dev, i32 = like.get_device(), torch.int32
     pages = _page_arrays(refs, table, None, dev)
     if refs_out is None:
-        refs_out = refs.new_empty(refs.shape)
+        refs_out = torch.empty(refs.shape, dtype=i32, device=like.device)
     if table_out is None:
-        table_out = table.new_empty(table.shape)
-    live = refs.new_empty(1)
+        table_out = torch.empty(table.shape, dtype=i32, device=like.device)
+    live = torch.empty(1, dtype=i32, device=like.device)
     if workspace is None:
         workspace = _workspace(like, rmsnorm_cache_pages_workspace_size, refs.numel(), 0, 0)
     ws_ptr, ws_bytes = _given(workspace, dev)
