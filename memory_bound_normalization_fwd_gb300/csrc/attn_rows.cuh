@@ -406,18 +406,32 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                     }
                 }
             } else {
-                const int words = p.code_bytes / 4;
                 for (int row0 = 0; row0 < TOK; row0 += 4) {
                     const int row = row0 + (lane >> 3);
                     const uint32_t h = __shfl_sync(0xffffffffu, at, row);
-                    const uint64_t off = h == kNone ? 0 : static_cast<uint64_t>(h) * p.code_bytes;
-                    for (int c = lane & 7; c < words; c += 8) {
-                        copy_async4(to + row * PITCH + c * 4, kcodes + off + c * 4, h != kNone);
-                        copy_async4(to + TOK * PITCH + row * PITCH + c * 4, vcodes + off + c * 4, h != kNone);
+                    const bool some = h != kNone;
+                    const uint64_t off = some ? static_cast<uint64_t>(h) * p.code_bytes : 0;
+                    const uint8_t *kfrom = kcodes + off, *vfrom = vcodes + off;
+                    const uint32_t dst = to + row * PITCH;
+                    for (int c = (lane & 7) * r.narrow; c < p.code_bytes; c += 8 * r.narrow) {
+                        if (r.narrow == 16) {
+                            copy_async16(dst + c, kfrom + c, some);
+                            copy_async16(dst + TOK * PITCH + c, vfrom + c, some);
+                        } else {
+                            copy_async4(dst + c, kfrom + c, some);
+                            copy_async4(dst + TOK * PITCH + c, vfrom + c, some);
+                        }
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // Bits before a token's scale bytes in the words that are read for them.
+        auto scale_place = [&](uint32_t at) -> uint32_t { return at * static_cast<uint32_t>(p.groups) % 4 * 8; };
+        auto shifted = [&](uint32_t (&s)[2], uint32_t shift) {
+            s[0] = __funnelshift_r(s[0], s[1], shift);
+            if (GD == 3) s[0] &= 0xffffffu, s[1] = 0;
+            else s[1] = s[1] >> shift & 0xffffu;
         };
         // the scale bytes of a token, low byte first
         auto scales = [&](int which, uint32_t at, uint32_t (&s)[2]) {
@@ -432,6 +446,13 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 s[1] = v.y;
             } else if (r.vec_scales && GD == 2) {
                 s[0] = __ldg(reinterpret_cast<const uint16_t*>(b));
+            } else if (r.vec_scales && (GD == 3 || GD == 6)) {
+                // the words that hold them (the array is whole words), shifted where they are used: there
+                // the loads have arrived (GB300, us, 32 sequences of 8192 tokens, 8 heads in 4 bits, shifted
+                // here / there: 96 values 97 / 72, 192 values 281 / 163)
+                const uint32_t* words = reinterpret_cast<const uint32_t*>(b - scale_place(at) / 8);
+                s[0] = __ldg(words);
+                if (GD == 6 || scale_place(at) > 8) s[1] = __ldg(words + 1);
             } else {
 #pragma unroll
                 for (int k = 0; k < GD; ++k)
@@ -447,6 +468,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
         copy(0, at, there_next);
         scales(0, at, sk);
         scales(1, at, sv);
+        uint32_t shift = scale_place(at);
 
         // ---- q: a row's largest magnitude, its power of two, and its values as fp16 operands
         uint2 qreg[C::QREG ? KS : 1];
@@ -580,6 +602,10 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
             // factors of the tile's tokens: 2^a for k; for v 2^(b - ref + LIFT), b the token's largest
             // byte, and 2^(the group's byte - b + CODE) in fp16. Two groups at a time, in halves of 16 bits.
             uint32_t bad = 0;  // groups of this lane's token whose v is not a number
+            if ((GD == 3 || GD == 6) && r.vec_scales) {
+                shifted(sk, shift);
+                shifted(sv, shift);
+            }
             {
                 constexpr uint32_t kBoth = 0x00010001u;
                 uint32_t x[W][2], y[W][2], e[W][2];  // bytes 0 and 2, and 1 and 3, of k's and v's scales
@@ -674,6 +700,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                 copy(stage ^ 1, next, there_next);
                 scales(0, next, sk);
                 scales(1, next, sv);
+                shift = scale_place(next);
                 page = page_of(tile + 2);
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {

@@ -27,7 +27,7 @@ struct RowsPlan {
     uint32_t pages;
     uint32_t page_mul;  // t / page_size = t * page_mul >> page_shift for t < 2^31
     int page_shift;
-    int narrow;       // codes are copied by 4 bytes (heads that are not whole groups)
+    int narrow;       // 0, or the bytes that codes are copied by: 4 or 16 (heads that are not whole groups)
     int vec_scales;   // a head's scale bytes are read at once
     int vec_q;        // rows of q are read by vectors
     int vec_out;      // rows of out are written in pairs

@@ -268,11 +268,14 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     const uintptr_t codes = reinterpret_cast<uintptr_t>(p.codes[0]) | reinterpret_cast<uintptr_t>(p.codes[1]);
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.scales[0]) | reinterpret_cast<uintptr_t>(p.scales[1]);
     r->gd = rows_gd(p.D);
-    r->narrow = p.D != r->gd * 32 || codes % 16 != 0;
-    if (r->narrow && (p.code_bytes % 4 != 0 || codes % 4 != 0)) return false;
+    // (GB300, us, 32 sequences of 8192 tokens, 8 heads of 80 values in 8 bits, by 4 / 16 bytes 135 / 111;
+    // 4 bits, 40 bytes a token: by 4 / 8 97 / 95, two chunks of 512 queries 345 / 374)
+    const uintptr_t run = codes | static_cast<uintptr_t>(p.code_bytes);
+    r->narrow = p.D == r->gd * 32 && codes % 16 == 0 ? 0 : run % 16 == 0 ? 16 : 4;
+    if (r->narrow == 4 && run % 4 != 0) return false;
     const int pieces = p.dtype == kFP32 ? 2 : 1;
     r->nt = rows_nt(p.G, r->gd, p.sequences, p.rows);
-    r->vec_scales = p.groups == r->gd && scales % 8 == 0;
+    r->vec_scales = p.groups == r->gd && scales % 8 == 0 && p.slots * p.heads * p.groups % 4 == 0;
     const int64_t eb = elem_bytes(p.dtype), e = vec_elems(p.dtype);
     r->vec_q = aligned16(p.q.p) && (p.rows <= 1 || p.q.st % e == 0) && (p.heads_q <= 1 || p.q.sh % e == 0) && eb > 0;
     r->vec_out = aligned16(p.out.p) && (p.rows <= 1 || p.out.st % 2 == 0) && (p.heads_q <= 1 || p.out.sh % 2 == 0);

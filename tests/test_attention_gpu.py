@@ -109,6 +109,27 @@ def test_long_sequences_are_split_and_joined(D, fmt):
         _run(cache, table, lens, [1, 1, 1], G, torch.float16, G)
 
 
+@pytest.mark.parametrize("D", [72, 80, 96, 176, 192, 224])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("page,heads,first", [(1, 1, False), (3, 1, True), (3, 3, False), (8, 2, True)])
+def test_scale_bytes_anywhere_in_a_word(D, fmt, page, heads, first):
+    # a head's 3, 5, 6 or 7 bytes begin at every place of a word; arrays that are not whole words
+    lens = [67, 2, 41]
+    cache, table = _filled(lens, page, heads, D, fmt, D + page, first)
+    for dtype in (torch.bfloat16, torch.float32):
+        _run(cache, table, lens, [1, 2, 1], 4 * heads, dtype, 1)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 192])
+@pytest.mark.parametrize("window", [0, 30])
+def test_rows_around_a_block(D, window):
+    # rows of a key head around the 8, 16 and 32 of a block, long sequences and a short table
+    for lens in ([900, 400], [130, 33]):
+        cache, table = _filled(lens, 16, 2, D, "e2m1", D)
+        for G, n in ((8, 1), (3, 3), (4, 4), (17, 1), (8, 3), (8, 4), (3, 11), (8, 5), (16, 3)):
+            _run(cache, table, lens, [n, n], 2 * G, torch.bfloat16, n, window=window, variants=("auto",))
+
+
 def test_many_sequences():
     lens = [(7 * i) % 61 for i in range(700)]
     cache, table = _filled(lens, 8, 2, 64, "e2m1", 1)
