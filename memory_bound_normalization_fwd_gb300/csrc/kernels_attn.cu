@@ -295,14 +295,14 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     // Where a slot has few tokens whatever the lengths (by the table's width, or the window), a CTA
     // takes all of them, with its warps side by side, and nothing is left to join; fewer heads a
     // CTA where there would be fewer CTAs than two an SM. (GB300, us, split and
-    // joined / so: 4 sequences of up to 509 tokens, 8 heads 10.7 / 7.8; 17 of five queries in a window
-    // of 1000, 5 heads of 96 values, 32 rows a CTA 29.7 / 21.2)
+    // joined / so: 4 sequences of up to 509 tokens, 8 heads 11.4 / 7.9; 17 of five queries in a window
+    // of 1000, 5 heads of 96 values 23.6 / 14.8)
     const int64_t tile = (p.format == RMSNORM_CACHE_E2M1 && r->gd <= 4 ? 32 : 16) * 8;
     const int64_t rows_seen = r->window ? static_cast<int64_t>(r->window) + 8 * r->nt : INT32_MAX;
     if (std::min<int64_t>(r->most_tokens, rows_seen) <= 4 * tile + 64) {
         r->split = 0;
         // (8 rows a CTA where 16 would leave one CTA an SM: GB300, us, 8 / 16, sequences of five queries
-        // in a window of 1000, 5 heads: 17 of 20 rows of 96 values 15.4 / 26.6; 17 of 40 rows of 128
+        // in a window of 1000, 5 heads: 17 of 20 rows of 96 values 14.8 / 21.0; 17 of 40 rows of 128
         // values 27.8 / 29.4, 136 of them 139 / 173; 17 of 10 rows 17.2 / 15.1)
         if (pieces == 1 && (r->gd == 3 || r->gd == 4)) r->nt = 1;
         slots = rows_slots(p.G, r->nt, p.sequences, p.rows);
