@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
     Sequences seq{nullptr, nullptr};
     if (r.narrow) {  // what lies behind a token's codes stays zero
         for (int i = lane; i < 2 * C::STAGE / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();  // before other lanes' copies go there
     }
     pdl_wait();
     pdl_launch_dependents();
