@@ -239,8 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                     tmem_stored();
                 };
                 if (u == 0) ref = b;
-                const int far = b - ref;  // the same for all threads
-                const float shift = far > 6 ? 0.f : static_cast<float>(far);
+                // The same for all threads. Where v lies far below the reference (a tile of zeros: byte 0),
+                // no lower than -40: P is at most 2^(8 - 40) there, nothing in fp16, and l, which is
+                // summed from the shifted values, keeps the tile's weight.
+                const int far = max(b - ref, -40), moved = far > 6 ? 0 : far;
+                const float shift = static_cast<float>(moved);
                 const bool masked = __any_sync(0xffffffffu, (there0 & there1) != 0xffffffffu || t0 + kStep > lim || t0 < low);
                 if (info.bad) {  // rare: which groups of v are not numbers for this row
                     for (int k = 0; k < kStep; ++k)
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                     v[e / 2] = half2_bits(px, py);
                 }
                 tmem_store32(s_at, v);
-                l = fmaf(f2_sum(f2_add(s0, s1)), power(ref - b), l);
+                l = fmaf(f2_sum(f2_add(s0, s1)), power(-moved), l);
                 tmem_stored();
                 tc_fence_before();
                 mbar_arrive(bar(kPFull + half * 2 + step));
