@@ -2,13 +2,16 @@
 // rows of a key head against tiles of 128 tokens.
 //
 // The mathematics. Each tile's codes become fp16 in shared memory, c * 2^(a - A + C): a the scale
-// byte of a token's group, A the tile's largest, C such that the largest code comes near 2^15. That is
-// exact for groups within 2^-30 of the tile's largest (below, to 2^-40 of it), and A goes into
-// the scores' factor, a number for the tile. q is brought near 2^15 by a power of two per row, as
+// byte of a token's group, A the tile's largest, C such that the largest code comes near 2^15 (6 for
+// 8-bit codes, 12 for 4-bit ones). That is exact while the codes' last bit (2^-9; 2^-1) stays at
+// 2^-24 or above: for groups within 2^21 (2^35) of the tile's largest. Below, values are off by less
+// than 2^-22 (2^-34) of 2^(A - 127), and groups beyond 2^30 (2^36) are left out. A goes into the
+// scores' factor, a number for the tile. q is brought near 2^15 by a power of two per row, as
 // in attn_rows.cuh. So S = Q K^T has exact products and fp32 sums; o += P V has P in fp16 (11
 // bits) and V in the same form as K, with the tile's B relative to a reference R that moves only where
-// B exceeds it by more than 2^6: p * 2^(B - R). Softmax with a running maximum that moves by more
-// than 2^8 at a time, so that the sums in tensor memory are rarely read and scaled.
+// B exceeds it by more than 2^3: p * 2^(B - R + 8), which keeps p to 2^-33 of R. Softmax with a running
+// maximum that moves by more than 2^4 at a time, so that the sums in tensor memory are rarely read
+// and scaled.
 //
 // Who does what, in a CTA of 16 warps: two warpgroups of softmax (a thread a row, each with 128
 // rows of its own), one warpgroup that looks up, loads and converts the tiles (into two stages of
@@ -41,6 +44,9 @@ constexpr int kHalf = 128;      // rows of a half
 constexpr int kThreads = 512;
 constexpr int kStep = 64;       // tokens of a step
 constexpr int kInfos = 4;       // tiles whose facts are kept
+// P = p * 2^(B - R + kLift) in fp16: below 2^-14 of it rounding is no longer relative, so that p * 2^(B - R)
+// is kept to 2^-33. The maximum may lag by 2^kGrow, R by 2^kFar: together at most 2^15.
+constexpr int kLift = 8, kGrow = 4, kFar = 3;
 
 // What the softmax needs to know of a tile.
 struct TileInfo {
@@ -240,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 };
                 if (u == 0) ref = b;
                 // The same for all threads. Where v lies far below the reference (a tile of zeros: byte 0),
-                // no lower than -40: P is at most 2^(8 - 40) there, nothing in fp16, and l, which is
+                // no lower than -40: P is at most 2^(12 - 40) there, nothing in fp16, and l, which is
                 // summed from the shifted values, keeps the tile's weight.
-                const int far = max(b - ref, -40), moved = far > 6 ? 0 : far;
+                const int far = max(b - ref, -40), moved = far > kFar ? kLift : far + kLift;
                 const float shift = static_cast<float>(moved);
                 const bool masked = __any_sync(0xffffffffu, (there0 & there1) != 0xffffffffu || t0 + kStep > lim || t0 < low);
                 if (info.bad) {  // rare: which groups of v are not numbers for this row
@@ -276,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 }
                 most = fmaxf(m0, m1);
                 const float above = most - shift;
-                const bool grow = started ? above > 8.f : most > -INFINITY;
-                if (__any_sync(0xffffffffu, grow || far > 6)) {
+                const bool grow = started ? above > static_cast<float>(kGrow) : most > -INFINITY;
+                if (__any_sync(0xffffffffu, grow || far > kFar)) {
                     // the sums so far are complete: the products that this S waited behind
-                    float f = far > 6 ? power(-far) : 1.f;
-                    if (far > 6) ref = b;
+                    float f = far > kFar ? power(-far) : 1.f;
+                    if (far > kFar) ref = b;
                     if (grow) {
                         const float g = started ? exp2_fast(-above) : 0.f;
                         m += above;
@@ -318,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
             } else {
                 tc_fence_after();
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                // 2^(ref - 127 - CODE) in two factors, which stay normal
-                const int e = ref - 127 - CODE;
+                // 2^(ref - 127 - CODE - kLift) in two factors, which stay normal
+                const int e = ref - 127 - CODE - kLift;
                 const float f1 = power(e / 2) * inv, f2_ = power(e - e / 2);
                 uint16_t* out = static_cast<uint16_t*>(p.out.p) + out_row * p.out.st + qh * p.out.sh;
                 const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;

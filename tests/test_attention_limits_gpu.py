@@ -6,7 +6,7 @@ import torch
 
 import serve_util as S
 from memory_bound_normalization_fwd_gb300 import binding as B
-from test_attention_gpu import DEV, _filled, _i32, _q, _run
+from test_attention_gpu import DEV, _cu, _filled, _i32, _q, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -72,7 +72,7 @@ def _put(cache, name, row, from_, to, value, group=None):
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 @pytest.mark.parametrize("byte", [8, 121, 127, 128, 129, 200])
-@pytest.mark.parametrize("tiles", [(1,), (0,), (2, 3), (4,)])
+@pytest.mark.parametrize("tiles", [(1,), (0,), (2, 3), (4,), (0, 1, 2, 3)])
 def test_prompts_over_tiles_of_zero_v(fmt, byte, tiles):
     """Tokens whose v is zero (scale byte 0, as cache_write stores zeros) keep their weight: whole
     tiles of 128, in any place, and a short last one."""
@@ -110,3 +110,89 @@ def test_prompts_over_a_tile_whose_pages_are_not_there(byte):
     for j in range(8, 16):
         table[0][j] = -1
     _run(cache, table, lens, [NEW], HEADS * G, torch.bfloat16, byte, status=-12)
+
+
+def _apart(cache, q, row, from_, to, gap):
+    """Puts tokens' scores `gap` (natural) above the others' (below, where it is negative): value 0 of
+    k and q is theirs."""
+    D = cache.head_dim
+    q[..., 0] = 8.0
+    code = cache.k_codes  # value 0 of everyone: 0
+    if cache.fmt == "e2m1":
+        code[..., 0] &= 0xf0
+    else:
+        code[..., 0] = 0
+    # the code 1.0, times the group's scale: a power of two next to the gap
+    _put(cache, "k_scales", row, from_, to, 0, 0)
+    at = _tokens(cache, row, from_, to)
+    one = (2 if gap > 0 else 10) if cache.fmt == "e2m1" else (0x38 if gap > 0 else 0xb8)
+    t = code.transpose(1, 2) if cache.heads_first else code
+    t[at[0], at[1], :, :cache.k_codes.shape[-1] // (D // 32)] = 0
+    t[at[0], at[1], :, 0] = one
+    e = int(torch.log2(torch.tensor(abs(gap) * D ** 0.5 / 8.0)).round())
+    _put(cache, "k_scales", row, from_, to, 127 + e, 0)
+
+
+def _check_prompt(cache, table, lens, counts, q, dtype, rounded=0.0):
+    """As check_attention, plus `rounded`: what each value of v may be off by."""
+    cu = _cu(counts)
+    out, lse, mag, s, floor = S.attention(cache, q, table, lens, cu, cache.head_dim ** -0.5, True, 0)
+    want = (out, lse, mag, s, floor + rounded)
+    got, got_lse = B.cache_attention(cache, q, _i32(table), _i32(lens), cu_q=_i32(cu), lse=True)
+    assert B.lib().rmsnorm_check_device_status(0) == 0
+    S.check_attention(got, got_lse, want, dtype, (cache.fmt, cache.head_dim))
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gap", [11.0, 15.0])
+def test_prompts_with_a_sink_token(fmt, D, gap):
+    """A token that takes nearly all of the weight and whose v is zero: what the others' small
+    probabilities add up to has the bits that the interface states."""
+    lens = [400]
+    cache, table = _prompt(lens, D, fmt, D)
+    q = _q(NEW, HEADS * G, D, torch.bfloat16, 5).contiguous()
+    _apart(cache, q, table[0], 0, 1, gap)
+    _put(cache, "v_codes", table[0], 0, 1, 0)
+    _put(cache, "v_scales", table[0], 0, 1, 0)
+    _check_prompt(cache, table, lens, [NEW], q, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("apart", [12, 20, 25, 33])
+@pytest.mark.parametrize("where", [0, 1, 2])
+def test_prompts_with_tiles_of_v_far_apart(fmt, apart, where):
+    """A tile whose v lies powers of two above the others', and which hardly anything weighs."""
+    lens = [400]
+    cache, table = _prompt(lens, 64, fmt, apart)
+    q = _q(NEW, HEADS * G, 64, torch.bfloat16, 5).contiguous()
+    _apart(cache, q, table[0], where * 128, where * 128 + 128, -60.0)
+    _put(cache, "v_scales", table[0], where * 128, where * 128 + 128, 127 + apart)
+    _check_prompt(cache, table, lens, [NEW], q, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt,apart", [("e4m3", 21), ("e4m3", 25), ("e4m3", 33), ("e2m1", 35), ("e2m1", 40)])
+def test_prompts_with_groups_of_v_far_apart_in_a_tile(fmt, apart):
+    """In a tile of 128 tokens v is exact within 2^21 of the largest scale (8 bits; 4 bits: 2^35), and off
+    by at most 2^-22 (2^-34) of it below."""
+    lens = [300]
+    cache, table = _prompt(lens, 64, fmt, apart)
+    _put(cache, "v_scales", table[0], 37, 38, 127 + apart, 0)
+    q = _q(NEW, HEADS * G, 64, torch.bfloat16, 5).contiguous()
+    _apart(cache, q, table[0], 37, 38, -60.0)
+    exact = 21 if fmt == "e4m3" else 35
+    _check_prompt(cache, table, lens, [NEW], q, torch.bfloat16,
+                  0.0 if apart <= exact else 2.0 ** (apart - (22 if fmt == "e4m3" else 34)))
+
+
+@pytest.mark.parametrize("fmt,apart", [("e4m3", 10), ("e4m3", 21), ("e2m1", 21), ("e2m1", 35)])
+def test_prompts_with_groups_of_k_far_apart_in_a_tile(fmt, apart):
+    """k is exact there too: a group that lies above the others, where q is zero, takes nothing from them."""
+    lens = [300]
+    cache, table = _prompt(lens, 64, fmt, apart)
+    _put(cache, "k_scales", table[0], 37, 38, 127 + apart, 1)
+    cache.k_scales.clamp_(min=127, max=127 + apart)
+    q = _q(NEW, HEADS * G, 64, torch.bfloat16, 5).contiguous()
+    q[..., 32:] = 0
+    q *= 0.1
+    _check_prompt(cache, table, lens, [NEW], q, torch.bfloat16)
