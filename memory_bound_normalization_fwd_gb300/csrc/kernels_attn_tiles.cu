@@ -9,8 +9,8 @@
 // scores' factor, a number for the tile. q is brought near 2^15 by a power of two per row, as
 // in attn_rows.cuh. So S = Q K^T has exact products and fp32 sums; o += P V has P in fp16 (11
 // bits) and V in the same form as K, with the tile's B relative to a reference R that moves only where
-// B exceeds it by more than 2^3: p * 2^(B - R + 8), which keeps p to 2^-33 of R. Softmax with a running
-// maximum that moves by more than 2^4 at a time, so that the sums in tensor memory are rarely read
+// B exceeds it by more than 2^1: p * 2^(B - R + 8), which keeps p to 2^-33 of R. Softmax with a running
+// maximum that moves by more than 2^6 at a time, so that the sums in tensor memory are rarely read
 // and scaled.
 //
 // Who does what, in a CTA of 16 warps: two warpgroups of softmax (a thread a row, each with 128
@@ -45,8 +45,9 @@ constexpr int kThreads = 512;
 constexpr int kStep = 64;       // tokens of a step
 constexpr int kInfos = 4;       // tiles whose facts are kept
 // P = p * 2^(B - R + kLift) in fp16: below 2^-14 of it rounding is no longer relative, so that p * 2^(B - R)
-// is kept to 2^-33. The maximum may lag by 2^kGrow, R by 2^kFar: together at most 2^15.
-constexpr int kLift = 8, kGrow = 4, kFar = 3;
+// is kept to 2^-33. The maximum may lag by 2^kGrow, R by 2^kFar: together at most 2^15. (GB300, prompts' chunks
+// as above, us, grow / far: 4 / 3 372, 5 / 2 358, 6 / 1 351, 7 / 0 352; without the lift, 8 / 6, 355.)
+constexpr int kLift = 8, kGrow = 6, kFar = 1;
 
 // What the softmax needs to know of a tile.
 struct TileInfo {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 };
                 if (u == 0) ref = b;
                 // The same for all threads. Where v lies far below the reference (a tile of zeros: byte 0),
-                // no lower than -40: P is at most 2^(12 - 40) there, nothing in fp16, and l, which is
+                // no lower than -40: P is at most 2^(14 - 40) there, nothing in fp16, and l, which is
                 // summed from the shifted values, keeps the tile's weight.
                 const int far = max(b - ref, -40), moved = far > kFar ? kLift : far + kLift;
                 const float shift = static_cast<float>(moved);
