@@ -496,7 +496,7 @@ cudaError_t pages_compact_run(const PagesP& p, const OpCfg& c) {
     const int staged = blocks <= 128 ? 1 : 0;
     const int smem = staged ? static_cast<int>((blocks + 4) / 4 * 4) * 4 + static_cast<int>(blocks) * 32 * 8
                             : static_cast<int>(blocks + 1) * 4;
-    if (smem > 48 * 1024) {  // always to the most, so that no call lowers it for another
+    if (!staged) {  // always to the most, so that no call lowers it for another
         e = cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kMaxPages / 1024 + 1) * 4);
         if (e != cudaSuccess) return e;
