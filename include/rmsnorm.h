@@ -767,8 +767,9 @@ int rmsnorm_cache_copy_pages(const rmsnorm_cache_t* cache, const int32_t* src, c
  * (length 0; its row is overwritten). Reported by rmsnorm_check_device_status and left as it
  * is: a child that is not empty, named twice (all but the first), or its own parent; a row
  * past the table; a parent whose tokens exceed its row; a child for which no free page is
- * left. Entries of a parent's tokens that name no page of the cache are copied as they are
- * and reported.
+ * left. Entries of a parent's tokens that name no page of the cache, the last one's among
+ * them, are copied as they are and reported (the free page that a last one would have taken
+ * stays free).
  *   workspace  rmsnorm_cache_pages_workspace_size() bytes, 16-byte aligned
  */
 int rmsnorm_cache_fork(const rmsnorm_cache_t* cache, const rmsnorm_cache_pages_t* pages,

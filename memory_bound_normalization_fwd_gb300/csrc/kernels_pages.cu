@@ -257,18 +257,20 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagesP p) {
                 if (page >= 0 && page < p.pages) atomicAdd(p.refs + page, 1);
                 else report();
             } else if (j == full && rest) {
-                page = fresh;
-                p.refs[page] = 1;
+                page = from[j];
+                if (page >= 0 && page < p.pages) {
+                    page = fresh;
+                    p.refs[page] = 1;
+                } else {  // stays what it is; the page set aside for it stays free
+                    report();
+                }
             }
             to[j] = page;
         }
         if (threadIdx.x == 0) p.lengths[p.b[i]] = have;
         if (!rest) continue;
         const int32_t old = from[full];
-        if (old < 0 || old >= p.pages) {
-            if (threadIdx.x == 0) report();
-            continue;
-        }
+        if (old < 0 || old >= p.pages) continue;
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             if (!b.p[a]) continue;

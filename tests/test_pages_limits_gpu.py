@@ -4,8 +4,9 @@ from __future__ import annotations
 import pytest
 import torch
 
+import serve_util as S
 from memory_bound_normalization_fwd_gb300 import binding as B
-from test_pages_gpu import DEV, _i32
+from test_pages_gpu import DEV, _cache, _i32, _same, _status
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,35 @@ def test_compact_of_millions_of_pages(pages):
         t[dst] = t[src]
         assert torch.equal(t, got)
     assert live.tolist() == [L] and bool((rf[:L] == 1).all()) and not bool(rf[L:].any())
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_fork_of_a_last_page_that_is_not_there(first, fmt):
+    """An entry of a parent's tokens that names no page is copied as it is, the last one's too: the child
+    gets no page of other tokens for it."""
+    page, pages = 4, 9
+    c = _cache(pages, page, 2, 32, fmt, first)
+    table = [[0, -1, -1], [1, pages, -1], [2, 3, -1], [-5, -1, -1]] + [[-1] * 3 for _ in range(5)]
+    lengths = [6, 7, 5, 2, 0, 0, 0, 0, 0]
+    refs = [1, 1, 1, 1, 0, 0, 0, 0, 1]
+    t, ln, rf = _i32(table), _i32(lengths), _i32(refs)
+    before = S.arrays(c)
+    B.cache_fork(c, rf, t, ln, _i32([0, 1, 3]), _i32([4, 5, 6]))
+    assert _status() == -12
+    assert t.tolist()[4:7] == [[0, -1, -1], [1, pages, -1], [-5, -1, -1]] and ln.tolist()[4:7] == [6, 7, 2]
+    assert rf.tolist() == [2, 2, 1, 1, 0, 0, 0, 0, 1]
+    _same(c, before)
+    # those beside it are forked as ever
+    B.cache_fork(c, rf, t, ln, _i32([0, 2]), _i32([7, 8]))
+    assert _status() == -12
+    assert t.tolist()[7] == [0, -1, -1] and t.tolist()[8][0] == 2 and t.tolist()[8][2] == -1
+    new = t.tolist()[8][1]
+    assert 4 <= new < 8 and rf.tolist() == [3, 2, 2, 1] + [int(p == new) for p in range(4, 8)] + [1]
+    for got, old in zip(S.arrays(c), before):
+        if first:
+            assert torch.equal(got[new, :, :1], old[3, :, :1])
+        else:
+            assert torch.equal(got[new, :1], old[3, :1])
+        got[new] = old[new]
+        assert torch.equal(got, old)
