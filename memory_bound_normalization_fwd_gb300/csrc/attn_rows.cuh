@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
     const int head_local = w % r.hb, slice = w / r.hb, threads = blockDim.x;
     const int x = static_cast<int>(blockIdx.x) / r.head_blocks, hblock = static_cast<int>(blockIdx.x) - x * r.head_blocks;
     const int head = hblock * r.hb + head_local;
-    const int tile_tokens = 1 << r.tile_shift;  // TOK * r.wph
     unsigned char* ring = sm + r.at_ring + w * r.ring;
     float* factors = reinterpret_cast<float*>(sm + r.at_factors + w * C::factor_bytes());
     uint2* qs = reinterpret_cast<uint2*>(sm + r.at_q + head_local * C::q_bytes());
@@ -678,7 +677,8 @@ __global__ void __launch_bounds__(256, Rows<F, GD, NT, NP>::CTAS) attn_rows_kern
                         const int i = grp >> 2, h = grp & 1;
                         kf[grp] = 0.f;
                         if (i >= W || grp >= GD) continue;
-                        kf[grp] = __uint_as_float(grp & 2 ? (x[i][h] & 0xffff0000u) << 7 : x[i][h] << 23);
+                        // (byte 0: 2^-127, below the normal values)
+                        kf[grp] = __uint_as_float(max(grp & 2 ? (x[i][h] & 0xffff0000u) << 7 : x[i][h] << 23, 0x400000u));
                         uint32_t half = (grp & 2 ? e[i][h] >> 16 : e[i][h] & 0xffffu) << 10;
                         if (slow) {
                             if (odd >> grp & 1u) kf[grp] = __uint_as_float(0x7fc00000u);

@@ -4,6 +4,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+import ops_util as U
 import serve_util as S
 from memory_bound_normalization_fwd_gb300 import binding as B
 from test_attention_gpu import DEV, _cu, _filled, _i32, _q, _run
@@ -196,3 +197,22 @@ def test_prompts_with_groups_of_k_far_apart_in_a_tile(fmt, apart):
     q[..., 32:] = 0
     q *= 0.1
     _check_prompt(cache, table, lens, [NEW], q, torch.bfloat16)
+
+
+# ---- k of scale byte 0 ---------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+def test_k_of_the_lowest_scale(fmt, dtype, D):
+    """A scale byte 0 is 2^-127, beside q near the type's largest values: scores of ordinary size."""
+    lens = [90, 33, 400]
+    cache, table = _filled(lens, 16, 2, D, fmt, D)
+    cache.k_codes &= 0x77
+    cache.k_scales.fill_(0)
+    g = torch.Generator().manual_seed(2)
+    more = torch.randint(0, 2, cache.k_scales.shape, generator=g, dtype=torch.uint8).to(DEV)
+    q = (_q(3, 8, D, torch.float32, 3).clamp(-3, 3) * 2.0 ** (118 if fmt == "e4m3" else 122)).to(U.DT[dtype])
+    for add in (0, 1):
+        cache.k_scales += add * more  # bytes 0 and 1
+        _run(cache, table, lens, [1, 1, 1], 8, U.DT[dtype], q=q, scale=0.5)
