@@ -51,7 +51,8 @@ constexpr int kLift = 8, kGrow = 6, kFar = 1;
 
 // What the softmax needs to know of a tile.
 struct TileInfo {
-    int a, b;                  // the largest scale bytes of k and v
+    float k;                   // 2^(a - 127 - C), a k's largest scale byte
+    int b;                     // v's largest scale byte
     uint32_t there[4];         // tokens whose page is there and that a row sees
     uint32_t bad;              // some group of v is not a number
     uint32_t pad;
@@ -76,6 +77,10 @@ __device__ __forceinline__ void store_piece(uint32_t at, uint32_t a, uint32_t b,
 __device__ __forceinline__ uint32_t power_half2(int e) {
     const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
     return h | h << 16;
+}
+// 2^e as fp32, also below 2^-126 (-149 <= e <= 127).
+__device__ __forceinline__ float tiny_power(int e) {
+    return __uint_as_float(e < -126 ? 1u << (e + 149) : static_cast<uint32_t>(e + 127) << 23);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -230,9 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 tmem_load_async(v, s_at);
                 tmem_load_async(v + 32, s_at + 32);
                 const TileInfo& info = infos[t % kInfos];
-                const int a = info.a, b = info.b, t0 = (sl.tile0 + t) * kTile + step * kStep;
+                const int b = info.b, t0 = (sl.tile0 + t) * kTile + step * kStep;
                 const uint32_t there0 = info.there[2 * step], there1 = info.there[2 * step + 1];
-                const float factor = row_scale * power(a - 127 - CODE);
+                const float factor = row_scale * info.k;
                 // Sums of the tiles before, scaled by f (all lanes of the warp).
                 auto scale_sums = [&](float f) {
 #pragma unroll 1
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnP p, 
                 if (late.at(2 * t)) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) a = max(a, tops[stage][0][k]), b = max(b, tops[stage][1][k]);
-                if (tid == 0) infos[t % kInfos].a = a, infos[t % kInfos].b = b;
+                if (tid == 0) infos[t % kInfos].k = tiny_power(a - 127 - CODE), infos[t % kInfos].b = b;
 #pragma unroll
                 for (int k = 0; k < CH; ++k) {
                     if (vs[k] == 255u) {

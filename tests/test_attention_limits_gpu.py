@@ -216,3 +216,15 @@ def test_k_of_the_lowest_scale(fmt, dtype, D):
     for add in (0, 1):
         cache.k_scales += add * more  # bytes 0 and 1
         _run(cache, table, lens, [1, 1, 1], 8, U.DT[dtype], q=q, scale=0.5)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("byte", [0, 3, 9])
+def test_prompts_over_k_of_the_lowest_scales(fmt, byte):
+    lens = [300]
+    cache, table = _prompt(lens, 64, fmt, 3)
+    cache.k_codes &= 0x77
+    cache.k_scales.fill_(byte)
+    size = 2.0 ** ((118 if fmt == "e4m3" else 122) - byte)
+    q = (_q(NEW, HEADS * G, 64, torch.float32, 3).clamp(-3, 3) * size).to(torch.bfloat16)
+    _run(cache, table, lens, [NEW], HEADS * G, torch.bfloat16, q=q, scale=0.5)
