@@ -368,8 +368,10 @@ int rmsnorm_bwd_workspace_size(int64_t M, int64_t N, int dtype, const rmsnorm_op
  * ones, and so, without an explicit variant, does the block's backward of rows of
  * at most 128 columns where that is faster. `opts` may be
  * NULL; they read variant (AUTO, CTA: the vector kernels, GENERIC: the
- * element-wise kernels), max_ctas, RMSNORM_FLAG_NO_PDL and, for the block
- * operator's kernels that stage rows, wait_limit_ns.
+ * element-wise kernels), max_ctas (a cap on persistent grids: not on the kernels of
+ * rmsnorm_cache_attention that take prompts and that join parts, and of at least one CTA
+ * a block of up to 8 key heads there), RMSNORM_FLAG_NO_PDL and wait_limit_ns (the block
+ * operator's kernels that stage rows, attention's for prompts).
  * ------------------------------------------------------------------------- */
 
 /*

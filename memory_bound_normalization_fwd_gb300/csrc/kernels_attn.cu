@@ -294,7 +294,7 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
                slots * (r->most_tokens / 16 + 8) < (int64_t(1) << 31);
     // Where a slot has few tokens whatever the lengths (by the table's width, or the window), a CTA
     // takes all of them, with its warps side by side, and nothing is left to join; fewer heads a
-    // CTA where there would be fewer CTAs than two an SM. (GB300, us, split and
+    // CTA where there would be fewer CTAs than two an SM (or than the call allows). (GB300, us, split and
     // joined / so: 4 sequences of up to 509 tokens, 8 heads 11.4 / 7.9; 17 of five queries in a window
     // of 1000, 5 heads of 96 values 23.6 / 14.8)
     const int64_t tile = (p.format == RMSNORM_CACHE_E2M1 && r->gd <= 4 ? 32 : 16) * 8;
@@ -309,8 +309,12 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
         r->slots = static_cast<int>(slots);
         r->hb = divisor_up_to(p.heads, most_heads());
         int hb = r->hb;
-        while (hb > 1 && slots * (p.heads / hb) < 2 * c.dev.sm_count) hb = divisor_up_to(p.heads, hb - 1);
-        r->hb = hb;
+        const int64_t most = c.max_ctas > 0 ? c.max_ctas : INT32_MAX;
+        while (hb > 1 && slots * (p.heads / hb) < std::min<int64_t>(2 * c.dev.sm_count, most)) {
+            hb = divisor_up_to(p.heads, hb - 1);
+            if (p.heads / hb > most) break;
+            r->hb = hb;
+        }
     }
     r->wph = 8 / r->hb;
     // (GB300, us, at 0 / 3 / 5: 32 sequences of up to 8192 tokens, 8 heads 49.2 / 45.9 / 48.0, two of
@@ -321,8 +325,9 @@ bool rows_plan(const AttnP& p, const OpCfg& c, RowsPlan* r) {
     int64_t ctas = rows_ctas(r->nt, r->gd, pieces, c.dev.sm_count);
     if (c.max_ctas > 0) ctas = std::min<int64_t>(ctas, c.max_ctas);
     ctas = std::min<int64_t>(ctas, 32767);  // a slot's first and last CTA share a word
+    const int64_t whole = c.max_ctas > 0 ? c.max_ctas : 1 << 24;  // CTAs that take slots whole
     r->gx = static_cast<int>(std::max<int64_t>(1, r->split ? ctas / r->head_blocks
-                                                          : std::min<int64_t>(slots, (1 << 24) / r->head_blocks)));
+                                                          : std::min<int64_t>(slots, whole / r->head_blocks)));
     if (r->split) {
         const int64_t rows = 2LL * r->gx * p.heads * 8 * r->nt;
         unsigned char* at = static_cast<unsigned char*>(p.ws);

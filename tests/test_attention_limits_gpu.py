@@ -7,6 +7,7 @@ import torch
 import ops_util as U
 import serve_util as S
 from memory_bound_normalization_fwd_gb300 import binding as B
+from graph_nodes import captured_grids
 from test_attention_gpu import DEV, _cu, _filled, _i32, _q, _run
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +229,25 @@ def test_prompts_over_k_of_the_lowest_scales(fmt, byte):
     size = 2.0 ** ((118 if fmt == "e4m3" else 122) - byte)
     q = (_q(NEW, HEADS * G, 64, torch.float32, 3).clamp(-3, 3) * size).to(torch.bfloat16)
     _run(cache, table, lens, [NEW], HEADS * G, torch.bfloat16, q=q, scale=0.5)
+
+
+# ---- a cap on the CTAs ------------------------------------------------------------------
+
+@pytest.mark.parametrize("most", [1, 3, 8, 40])
+@pytest.mark.parametrize("D,heads", [(64, 2), (96, 5), (128, 8), (192, 8)])
+def test_whole_slots_in_few_ctas(most, D, heads):
+    """A short table: CTAs take slots whole, no more of them than the call allows (one a block of key heads
+    at least)."""
+    lens = [(29 * i) % 150 for i in range(60)]
+    cache, table = _filled(lens, 16, heads, D, "e2m1", D)
+    _run(cache, table, lens, [1] * 60, 4 * heads, torch.bfloat16, variants=("auto",))
+    q, t, ln = _q(60, 4 * heads, D, torch.bfloat16, 0), _i32(table), _i32(lens)
+    out, lse = B.cache_attention(cache, q, t, ln, lse=True, max_ctas=most)
+    S.check_attention(out, lse, S.attention(cache, q, table, lens, list(range(61)), D ** -0.5, True, 0),
+                      torch.bfloat16, (most, D))
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    res = torch.empty_like(q)
+    grids = captured_grids(lambda: B.cache_attention(cache, q, t, ln, out=res, workspace=ws, max_ctas=most))
+    assert len(grids) == 1 and grids[0] <= max(most, -(-heads // 8)), grids
+    grids = captured_grids(lambda: B.cache_attention(cache, q, t, ln, out=res, workspace=ws))
+    assert grids[0] > 40
