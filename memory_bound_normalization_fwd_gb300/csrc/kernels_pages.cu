@@ -425,10 +425,12 @@ __global__ void __launch_bounds__(256) compact_kernel(const PagesP p, int team, 
             for (int k = tid / team; k < 256 && i0 + static_cast<int64_t>(k) * move_ctas < moves; k += per)
                 copy_page<4>(p.bytes, from[k], to[k], lane, team);
         }
-        return;
+        if (static_cast<int>(gridDim.x) > move_ctas) return;
     }
-    const int64_t first = static_cast<int64_t>(blockIdx.x - move_ctas) * 256 + tid;
-    const int64_t step = static_cast<int64_t>(gridDim.x - move_ctas) * 256;
+    // counts and table: by the CTAs behind, or by a single one too
+    const int before_rest = static_cast<int>(gridDim.x) > move_ctas ? move_ctas : 0;
+    const int64_t first = static_cast<int64_t>(blockIdx.x - before_rest) * 256 + tid;
+    const int64_t step = static_cast<int64_t>(gridDim.x - before_rest) * 256;
     if (first == 0) *p.live = static_cast<int32_t>(L);
     // a move's two counts, by one thread; the others stay as they are
     for (int64_t i = first; i < moves; i += step) {
@@ -504,9 +506,13 @@ cudaError_t pages_compact_run(const PagesP& p, const OpCfg& c) {
         if (e != cudaSuccess) return e;
     }
     // At most half of the pages can move; some CTAs beside take counts and table.
-    const int64_t move = persistent_grid((p.pages + 1) / 2, 256 / team, c.dev.sm_count, 7, c.max_ctas);
+    int64_t move = persistent_grid((p.pages + 1) / 2, 256 / team, c.dev.sm_count, 7, c.max_ctas);
     const int64_t small = std::max(p.pages, p.sequences * p.width);
-    const int64_t rest = persistent_grid(small, 256, c.dev.sm_count, 1, c.max_ctas);
+    int64_t rest = persistent_grid(small, 256, c.dev.sm_count, 1, 0);
+    if (c.max_ctas > 0) {  // both together
+        rest = std::min<int64_t>(rest, c.max_ctas == 1 ? 0 : std::max(1, c.max_ctas / 8));
+        move = std::min<int64_t>(move, c.max_ctas - rest);
+    }
     return op_launch(c, compact_kernel, move + rest, 256, smem, p, team, static_cast<int>(move), staged);
 }
 

@@ -1,10 +1,13 @@
 """Pages of the cache at the edges of what their operators take."""
 from __future__ import annotations
 
+import random
+
 import pytest
 import torch
 
 import serve_util as S
+from graph_nodes import captured_grids
 from memory_bound_normalization_fwd_gb300 import binding as B
 from test_pages_gpu import DEV, _cache, _i32, _same, _status
 
@@ -28,6 +31,33 @@ def test_compact_of_millions_of_pages(pages):
         t[dst] = t[src]
         assert torch.equal(t, got)
     assert live.tolist() == [L] and bool((rf[:L] == 1).all()) and not bool(rf[L:].any())
+
+
+@pytest.mark.parametrize("most", [1, 2, 7, 100])
+@pytest.mark.parametrize("shape", [(16, 8, 128), (1, 1, 7)])
+def test_compact_in_few_ctas(most, shape):
+    rng = random.Random(most)
+    pages = 3000 if shape[0] == 1 else 700
+    refs = [rng.randint(0, 2) for _ in range(pages)]
+    live = [p for p in range(pages) if refs[p]]
+    rng.shuffle(live)
+    table = [live[:50], live[20:70]]
+    c = _cache(pages, *shape)
+    want = S.compact(c, refs, table)
+    first = [t.clone() for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales)]
+    rf, t = _i32(refs), _i32(table)
+    got = B.cache_compact(c, rf, t, max_ctas=most)
+    assert [g.tolist() for g in got] == [[want[0]], want[1], want[2]]
+    _same(c, want[3])
+    for a, b in zip((c.k_codes, c.k_scales, c.v_codes, c.v_scales), first):
+        a.copy_(b)
+    got = B.cache_compact(c, rf, t, refs_out=rf, table_out=t, max_ctas=most)  # in place
+    assert [g.tolist() for g in got] == [[want[0]], want[1], want[2]]
+    _same(c, want[3])
+    assert _status() == 0
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    grids = captured_grids(lambda: B.cache_compact(c, rf, t, refs_out=rf, table_out=t, workspace=ws, max_ctas=most))
+    assert len(grids) == 2 and max(grids) <= most, grids
 
 
 @pytest.mark.parametrize("first", [False, True])
