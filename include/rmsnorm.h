@@ -697,10 +697,14 @@ int rmsnorm_rope_axes_bwd(const rmsnorm_rope_args_t* args, const rmsnorm_rope_ax
  * A code that is itself a NaN (E4M3, which rmsnorm_cache_write never stores) may reach
  * further within its tile of tokens.
  *
- * Products are exact (codes and q in 16 bits or split into such), sums and softmax
- * statistics are held in fp32; probabilities are rounded to 11 bits for 16-bit outputs and
- * to 22 bits for fp32, with a floor: p * (largest scale of the token's v) is kept to
- * 2^-33 of the sequence's largest such scale.
+ * Sums and softmax statistics are held in fp32. The matrix instructions take fp16: q is exact
+ * within 2^28 of its row's largest value (fp32: 22 bits of it), codes within 2^21 (8 bits; 4
+ * bits: 2^35) of the largest scale beside theirs, and what lies below is off by less than
+ * 2^-22 (2^-34) of that scale. Beside it are, for v, the groups of its token and head; in calls
+ * of enough rows for the tensor cores, for k and v, those of the head in a run of 128 tokens.
+ * Probabilities are rounded to 11 bits for 16-bit outputs and to 22 bits for fp32, with a
+ * floor: p * (largest scale beside the token's v) is kept to 2^-33 of the sequence's largest
+ * scale. The element-wise kernel computes all of it in fp32.
  *   cu_rows  [sequences + 1] int32, not decreasing, from 0; NULL: one row a sequence
  *            (rows == sequences)
  *   rows     rows of q and out; rows from cu_rows[sequences] on are left as they are

@@ -30,10 +30,10 @@
 // row of codes at a time), no barrier in the loop; page numbers are looked up two tiles ahead,
 // scale bytes travel through registers one tile ahead. Softmax with a running maximum, which moves
 // only where a score exceeds it by more than 2^4 (the sums then carry factors up to 2^4).
-// Bound (GB300): instructions. 32 sequences of up to 8192 tokens, 32 query heads on 8 of 128 values in 4
-// bits, 144 MB, 46 us, 46% of the rate of a copy: issue slots 57%, integer and conversion units 47%
-// (each of their instructions takes two cycles), matrix units 18%; about 650 instructions a tile of
-// 32 tokens and 1800 a slot. Two sequences of up to 131072 tokens, 16 query heads on one of 256 values
+// Bound (GB300): the latency of a warp's instructions; no unit is full. 32 sequences of up to 8192 tokens, 32
+// query heads on 8 of 128 values in 4 bits, 144 MB, 48 us, 45% of the rate of a copy: issue slots 57%,
+// integer and conversion units 47% (each of their instructions takes two cycles), matrix units 18%, four
+// warps a scheduler; about 650 instructions a tile of 32 tokens and 1800 a slot. In fp32 55 us. Two sequences of up to 131072 tokens, 16 query heads on one of 256 values
 // in 8 bits, 131 MB, 46 us: 2 warps a scheduler, which the sums in registers allow, issue 33% of the time.
 #pragma once
 

@@ -21,7 +21,7 @@
 // second product's first operand; o takes head_dim columns. While one half is in its softmax the
 // other half's products run.
 // Bound (GB300): the chain of softmax and products within a half. Three chunks of 2048 queries of 32
-// heads of 128 values behind up to 8192 tokens of 8 heads in 4 bits, bf16, 352 us, 46% of the rate of
+// heads of 128 values behind up to 8192 tokens of 8 heads in 4 bits, bf16, 351 us, 46% of the rate of
 // a large product: matrix units active 39%, issue slots 45%, exponentials 20%; a half waits for S about as
 // long as its softmax takes, as both halves' products go through the same matrix unit, which reads
 // their operands at the rate of shared memory. (S in steps of 64 tokens, so that softmax starts
